@@ -58,8 +58,15 @@ typedef enum {
   XP_EBADTOKEN = 5,     /* device flag: a token id outside [0, V) was clamped          */
   XP_ETIMEOUT = 6,      /* device flag: a bounded wait inside a kernel gave up         */
   XP_EUNSUPPORTED = 7,  /* shape not supported by this build                           */
-  XP_ERANGE = 8         /* device flag: a latent-stage value left the fp16 range of the
+  XP_ERANGE = 8,        /* device flag: a latent-stage value left the fp16 range of the
                            tensor-core latent's exchanges (saturated; results unreliable) */
+  XP_EBADPAGE = 9,      /* device flag: a page id outside the pool (clamped when read, ignored
+                           when freed) or a page freed more often than it was held        */
+  XP_ENOPAGES = 10,     /* device flag: the pool ran out of free pages; rows were cut short */
+  XP_ESHARED = 11,      /* device flag: a resize would have ended inside a shared page; the
+                           row was left as it was                                          */
+  XP_ELENGTH = 12,      /* device flag: a length or a row number outside its range was clamped */
+  XP_EEMPTY = 13        /* device flag: a target row left no token to draw (token -1)      */
 } xp_status;
 
 typedef enum { XP_BF16 = 0, XP_F32 = 1 } xp_dtype;
@@ -277,8 +284,8 @@ int xp_readout_pairs(const xp_head* head, int N);
 int xp_passes_persistent(const xp_head* head, const void* base, int64_t stride_n,
                          int64_t stride_b, int N);
 
-/* Synchronise `stream`, read and clear the head's device error word:
- * XP_OK, XP_EBADTOKEN, XP_ERANGE or XP_ETIMEOUT (precedence in reverse order). */
+/* Synchronise `stream`, read and clear the head's device error word: XP_OK, XP_EBADTOKEN,
+ * XP_ELENGTH, XP_EEMPTY, XP_ERANGE or XP_ETIMEOUT (precedence in reverse order). */
 xp_status xp_get_error(const xp_head* head, cudaStream_t stream);
 
 /* Failure-path self-test (no counterpart on the pages): launches one kernel whose
@@ -306,6 +313,169 @@ xp_status xp_profile_timeline(xp_head* head, void* buf, size_t bytes, int K, siz
 
 /* Name of the readout kernel the head uses for its shape (for profiling). */
 const char* xp_readout_kernel_name(const xp_head* head);
+
+/* ---------------------------------------------------------------------------------------
+ * After the refinement: the drafted blocks are scored by the target model over a paged
+ * cache, verified, and the cache is cut back to what was accepted.  None of these calls has
+ * a counterpart on the pages; they are the target's side of the same draft step.
+ * ------------------------------------------------------------------------------------- */
+
+/* Verification of drafted blocks against the target's probabilities, from given random
+ * numbers.  With D = n_draft[n] drafted tokens x_b = blk[n, 1+b] (b = 0..D-1) per block:
+ *   p_b = softmax(target[n, b] / t[n])      b = 0..D (row b is the target after slot b)
+ *   q_b = softmax(draft[n, b] / t[n]), or one-hot at x_b when draft == NULL (the refinement's
+ *         own greedy drafts)
+ *   slot b is accepted while u[n, b] * q_b(x_b) < p_b(x_b); the first slot a that is not ends
+ *   the block with one token drawn from the normalised residual max(p_a - q_a, 0); when all D
+ *   are accepted, a = D and the token is drawn from p_D.
+ * The draw is a race: argmax_v w(v) / noise[n, v], which draws from w when the noise is
+ * exponential; equal ratios go to the lowest id.  (Where rounding leaves no positive
+ * residual, p_a itself is drawn from.)  t[n] = 0 makes block n greedy: p_b is one-hot at the
+ * lowest argmax, a draft is accepted when it is that id, and no noise is read.
+ * The emitted tokens then follow the target's own distribution, whatever the draft's.
+ *
+ * target: device [N, B, V] head dtype, row (n, b) at target + n*stride_n + b*stride_b, unit
+ * stride over v.  draft: device fp32, row n*(B-1) + b at draft + (n*(B-1) + b)*ld_draft (the
+ * layout xp_refine_logits writes), or NULL.  blk: device [N, B] int64.  n_draft: device [N]
+ * int32 (clamped to [0, B-1], XP_ELENGTH), or NULL for B-1.  temperature: device [N] fp32, or
+ * NULL for 1; a negative or NaN one counts as 0.  u: device [N, B-1] fp32 in [0, 1).  noise:
+ * device fp32 > 0, row n at noise + n*ld_noise.
+ * tokens (out): device [N, B] int64: the accepted drafts, then the drawn token, then -1.
+ * counts (out): device [N] int32, tokens emitted (accepted + 1).  prob (out): device
+ * [N, B-1] fp32 = min(1, p_b(x_b) / q_b(x_b)) for the slots tested, 0 behind them, or NULL.
+ * Logits are read as: NaN like -inf (never drawn), +inf like the largest finite value.  A
+ * target row with nothing above -inf accepts nothing, and a block that ends there gets
+ * token -1 (XP_EEMPTY).  A drafted id outside [0, V) is rejected (XP_EBADTOKEN).
+ * Rows behind a block's first rejection cannot change the result and are mostly not read.
+ * B, V, dtype: what the buffers were made for; XP_EINVAL unless they are the head's.
+ * ws: xp_verify_workspace_bytes, zeroed once with xp_workspace_init; calls that overlap on
+ * the GPU need a workspace each. */
+size_t xp_verify_workspace_bytes(const xp_head* head, int N);
+xp_status xp_verify_drafts(const xp_head* head, const void* target, int64_t stride_n,
+                           int64_t stride_b, const float* draft, int64_t ld_draft,
+                           const int64_t* blk, const int32_t* n_draft, int N, int B, int V,
+                           xp_dtype dtype, const float* temperature, const float* u, const float* noise,
+                           int64_t ld_noise, int64_t* tokens, int32_t* counts, float* prob,
+                           void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* A paged key/value cache.  K and V are pools of `pages` pages of `page_size` tokens in each
+ * of `layers` layers; a sequence is a row of page ids (its table) and a length, and a page
+ * that several rows hold is counted in `refs`.  The pools belong to the caller; element
+ * (layer, page, token, head, i) of either is at
+ *   layer*stride_layer + page*stride_page + token*stride_token + head*stride_head + i
+ * (elements).  A page is one dense block in either order: tokens outside
+ * (stride_token = kv_heads*head_dim, stride_head = head_dim) or heads outside
+ * (stride_head = page_size*head_dim, stride_token = head_dim). */
+typedef struct {
+  int pages, page_size, layers, kv_heads, head_dim;
+  int max_seqs;    /* most rows any table call will pass */
+  xp_dtype dtype;
+  int64_t stride_layer, stride_page, stride_token, stride_head;
+  void* k;
+  void* v;
+} xp_cache_desc;
+
+typedef struct xp_cache xp_cache; /* opaque, host-side */
+
+/* Device bytes of the cache's error word and of the table calls' scratch. */
+size_t xp_cache_prep_bytes(const xp_cache_desc* d);
+
+/* Host handle of a cache.  prep_dev: device, 256-byte aligned, cleared by the call.  The
+ * pools stay the caller's and must outlive the handle.  head_dim <= 256. */
+xp_status xp_cache_create(const xp_cache_desc* d, void* prep_dev, size_t prep_bytes,
+                          cudaStream_t stream, xp_cache** out);
+void xp_cache_destroy(xp_cache* cache);
+
+/* Synchronise `stream`, read and clear the cache's device error word: XP_OK or one of
+ * XP_EBADPAGE, XP_ENOPAGES, XP_ESHARED, XP_ELENGTH, XP_ETIMEOUT (the last named first). */
+xp_status xp_cache_get_error(const xp_cache* cache, cudaStream_t stream);
+
+/* Write the keys and values of the T newest tokens of N sequences: token t of row n goes to
+ * position lens[n] - T + t (lens counts them already; positions below 0 are skipped).
+ * k, v: device, element (n, t, head, i) at n*stride_n + t*stride_t + head*stride_h + i.
+ * heads, head_dim, dtype: theirs; XP_EINVAL unless they are the cache's.  table: device
+ * int32, row n at table + n*ld_table (ld_table >= its columns); lens: device [N] int32. */
+xp_status xp_cache_append(const xp_cache* cache, int layer, const void* k, const void* v,
+                          int64_t stride_n, int64_t stride_t, int64_t stride_h,
+                          int heads, int head_dim, xp_dtype dtype, const int32_t* table,
+                          int64_t ld_table, const int32_t* lens, int N, int T,
+                          cudaStream_t stream);
+
+/* The table calls below change page tables, lengths and reference counts (and, where they
+ * say so, move pages of K and V in every layer).  Each output may be the matching input
+ * itself.  Page ids of a table behind ceil(length / page_size) are not read and are written
+ * as -1.  `width`: columns of the tables; `pages`: entries of refs, refs_out and map, XP_EINVAL
+ * unless the pool's.  They share the handle's scratch: calls on one
+ * cache must not overlap on the GPU. */
+
+/* Copy whole pages src[i] -> dst[i] (device int32, `count` of them), K and V, every layer.
+ * A negative id skips the pair; no page may be the target of one pair and in another. */
+xp_status xp_cache_copy(const xp_cache* cache, const int32_t* src, const int32_t* dst, int count,
+                        cudaStream_t stream);
+
+/* Lengths old -> new: pages behind the new length are let go (refs - 1), missing ones taken
+ * (refs = 1): the lowest free ids, after all releases, in row and then in column order.
+ * new_lens is clamped to [0, width*page_size] (XP_ELENGTH).  Where the pool runs out, rows
+ * end at the last page they got (XP_ENOPAGES).  A row whose old or new length, the smaller
+ * of the two, ends inside a page that is held more than once stays as it was (XP_ESHARED):
+ * fork it instead. */
+xp_status xp_cache_resize(const xp_cache* cache, const int32_t* table, int64_t ld_table,
+                          const int32_t* lens, const int32_t* new_lens, const int32_t* refs,
+                          int pages, int N, int width, int32_t* table_out, int64_t ld_out, int32_t* lens_out,
+                          int32_t* refs_out, cudaStream_t stream);
+
+/* M children: child i continues row parent[i] of a table of `rows` rows at length
+ * min(lens[parent[i]], cut[i]) (cut may be NULL).  Its full pages are shared (refs + 1); of a
+ * partly filled last page it gets a copy of its own, the tokens it holds only: the lowest
+ * free id, in child order.  Without one it ends at its last full page (XP_ENOPAGES).  A
+ * parent outside [0, rows) gives an empty child (XP_ELENGTH).  child_table may be other rows
+ * of the same table. */
+xp_status xp_cache_fork(const xp_cache* cache, const int32_t* table, int64_t ld_table,
+                        const int32_t* lens, int rows, const int32_t* parent, const int32_t* cut,
+                        int M, int width, const int32_t* refs, int pages, int32_t* child_table,
+                        int64_t ld_child, int32_t* child_lens, int32_t* refs_out,
+                        cudaStream_t stream);
+
+/* Pack the pages in use (refs > 0) to ids 0..live-1: the i-th of those with an id >= live
+ * moves to the i-th free id < live.  Every table row, refs and the pools follow; map (device
+ * [pages] int32, may be NULL) receives each page's new id, -1 for a free one, for tables
+ * kept elsewhere; live (device [1] int32, may be NULL) their number. */
+xp_status xp_cache_compact(const xp_cache* cache, const int32_t* table, int64_t ld_table,
+                           const int32_t* lens, int N, int width, const int32_t* refs, int pages,
+                           int32_t* table_out, int64_t ld_out, int32_t* refs_out, int32_t* map,
+                           int32_t* live, cudaStream_t stream);
+
+/* Attention of N sequences of T new tokens (T = 1: plain decoding; T = B: a drafted block)
+ * that share a prefix of prefix_len tokens and each have a tail of their own.  Query (n, t)
+ * of head h sees the whole prefix and the tail's positions below lens[n] - T + t + 1 (the
+ * new tokens' keys and values are in the tail already), through kv head
+ * h / (heads / kv_heads):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j).
+ * The prefix is read once for the whole batch, not once a sequence.  A query that sees
+ * nothing gets out = 0 and lse = -inf.  Tokens behind the lengths may hold anything, NaN
+ * included; what is visible is assumed finite.
+ * q, out: cache dtype, element (n, t, h, i) at n*stride_n + t*stride_t + h*stride_h + i.
+ * prefix_table: device int32, prefix_pages >= ceil(prefix_len / page_size) entries.  table:
+ * device int32, row n at table + n*ld_table, width >= ceil(max_len / page_size) columns.  lens: device [N] int32;
+ * lengths above max_len are clamped (XP_ELENGTH).  lse: device fp32 [N, T, heads] or NULL.
+ * Scores, softmax and sums are fp32 (bf16: each weight is rounded to bf16 before it
+ * multiplies v, as the tensor cores take it). */
+typedef struct {
+  int layer, N, T, heads;
+  int head_dim;      /* head_dim and dtype: those of q and out, which must be the cache's */
+  xp_dtype dtype;
+  int prefix_len, max_len;
+  float scale;
+  int64_t q_stride_n, q_stride_t, q_stride_h;
+  int64_t o_stride_n, o_stride_t, o_stride_h;
+} xp_attn;
+
+/* Device bytes of the attention's workspace (need not be cleared). */
+size_t xp_attention_workspace_bytes(const xp_cache* cache, const xp_attn* a);
+xp_status xp_prefix_attention(const xp_cache* cache, const xp_attn* a, const void* q,
+                              const int32_t* prefix_table, int prefix_pages, const int32_t* table,
+                              int64_t ld_table, int width, const int32_t* lens, void* out, float* lse,
+                              void* ws, size_t ws_bytes, cudaStream_t stream);
 
 const char* xp_status_str(xp_status s);
 

@@ -1,0 +1,325 @@
+// Shared-prefix attention on plain CUDA cores (fp32 caches, and shapes the tensor-core
+// kernel does not tile), and the kernel that joins partial results.
+#include <float.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "xp_device.cuh"
+
+using namespace xpd;
+typedef __nv_bfloat16 bf16;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeys = 64;    // keys of one step
+
+// query row r of a tile -> its (sequence, token, head within the group); false behind the end
+struct Row {
+  int n, t, j;
+};
+__device__ __forceinline__ bool row_of(const xp_attn_args& g, bool prefix, int tile, int r, int n,
+                                       int rows_tile, Row* out) {
+  const int i = tile * rows_tile + r;
+  const int per_seq = g.a.T * g.group;
+  if (i >= (prefix ? g.a.N * per_seq : per_seq)) return false;
+  out->n = prefix ? i / per_seq : n;
+  out->t = i % per_seq / g.group;
+  out->j = i % g.group;
+  return true;
+}
+
+template <typename T, int RM, int NC>
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args g) {
+  constexpr int BM = 16 * RM;
+  extern __shared__ __align__(16) float smem[];
+  const int D = g.dim, DP = (D + 3) / 4 * 4, LD = DP + 4;
+  float* sq = smem;                      // [BM][LD]
+  float* sk = sq + BM * LD;              // [kKeys][LD]
+  float* sv = sk + kKeys * LD;           // [kKeys][NC * 64]
+  float* sp = sv + kKeys * NC * 64;      // [BM][kKeys + 4]
+  constexpr int LP = kKeys + 4;
+  __shared__ int s_limit[BM];            // keys each row sees
+  __shared__ int s_page[kKeys];
+
+  const xp_attn_plan& pl = g.plan;
+  const int hk = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  int unit = blockIdx.x;
+  const bool prefix = unit < pl.prefix_tiles * pl.prefix_splits;
+  int tile, split, n = 0, part, keys;
+  const int32_t* table = g.prefix_table;
+  if (prefix) {
+    tile = unit / pl.prefix_splits;
+    split = unit % pl.prefix_splits;
+    part = split;
+    keys = g.a.prefix_len;
+  } else {
+    unit -= pl.prefix_tiles * pl.prefix_splits;
+    split = unit % pl.tail_splits;
+    tile = unit / pl.tail_splits % pl.tail_tiles;
+    n = unit / pl.tail_splits / pl.tail_tiles;
+    part = pl.prefix_splits + split;
+    table = g.table + n * g.ld_table;
+    keys = g.lens[n];
+    if (keys < 0 || keys > g.a.max_len) {
+      if (tid == 0) atomicOr(g.err, XP_ERR_LENGTH);
+      keys = keys < 0 ? 0 : g.a.max_len;
+    }
+  }
+  const int step = prefix ? pl.prefix_keys : pl.tail_keys;
+  const int k0 = split * step, k1 = min(keys, k0 + step);
+
+  for (int i = tid; i < BM; i += kThreads) {
+    Row r;
+    int lim = 0;
+    if (row_of(g, prefix, tile, i, n, BM, &r)) lim = prefix ? keys : keys - g.a.T + r.t + 1;
+    s_limit[i] = min(lim, k1);
+  }
+  // queries, scaled so that the softmax runs in base 2
+  const float scale = g.a.scale * 1.44269504088896f;
+  for (int i = tid; i < BM * LD; i += kThreads) {
+    const int r = i / LD, d = i % LD;
+    Row w;
+    float x = 0.0f;
+    if (d < D && row_of(g, prefix, tile, r, n, BM, &w))
+      x = to_f(((const T*)g.q)[w.n * g.a.q_stride_n + w.t * g.a.q_stride_t +
+                               (int64_t)(hk * g.group + w.j) * g.a.q_stride_h + d]) * scale;
+    sq[i] = x;
+  }
+  float o[RM][NC * 4], m[RM], l[RM];
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC * 4; ++c) o[i][c] = 0.0f;
+  }
+
+  for (int kb = k0; kb < k1; kb += kKeys) {
+    __syncthreads();
+    if (tid < kKeys) {
+      int p = -1;
+      if (kb + tid < k1) {
+        p = table[(kb + tid) / g.page_size];
+        if (p < 0 || p >= g.pages) {
+          atomicOr(g.err, XP_ERR_BADPAGE);
+          p = p < 0 ? 0 : g.pages - 1;
+        }
+      }
+      s_page[tid] = p;
+    }
+    __syncthreads();
+    for (int i = tid; i < kKeys * DP; i += kThreads) {
+      const int j = i / DP, d = i % DP;
+      float kx = 0.0f, vx = 0.0f;
+      if (s_page[j] >= 0 && d < D) {   // tokens behind the length are not read
+        const int64_t at = s_page[j] * g.kv_page + (kb + j) % g.page_size * g.kv_token +
+                           hk * g.kv_head + d;
+        kx = to_f(((const T*)g.k)[at]);
+        vx = to_f(((const T*)g.v)[at]);
+      }
+      sk[j * LD + d] = kx;
+      sv[j * NC * 64 + d] = vx;
+    }
+    if (DP < NC * 64)
+      for (int i = tid; i < kKeys * (NC * 64 - DP); i += kThreads)
+        sv[i / (NC * 64 - DP) * NC * 64 + DP + i % (NC * 64 - DP)] = 0.0f;
+    __syncthreads();
+    // scores: rows ty*RM.., keys tx + 16 j
+    float s[RM][4];
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+    for (int d = 0; d < DP; d += 4) {
+      float4 qa[RM], ka[4];
+#pragma unroll
+      for (int i = 0; i < RM; ++i) qa[i] = *(const float4*)&sq[(ty * RM + i) * LD + d];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ka[j] = *(const float4*)&sk[(tx + 16 * j) * LD + d];
+#pragma unroll
+      for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(qa[i].x, ka[j].x, s[i][j]);
+          s[i][j] = fmaf(qa[i].y, ka[j].y, s[i][j]);
+          s[i][j] = fmaf(qa[i].z, ka[j].z, s[i][j]);
+          s[i][j] = fmaf(qa[i].w, ka[j].w, s[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      const int lim = s_limit[ty * RM + i];
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (kb + tx + 16 * j >= lim) s[i][j] = -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+      const float now = fmaxf(m[i], top);
+      const float base = now == -INFINITY ? 0.0f : now;   // a row that sees none of these keys
+      const float keep = exp2f(m[i] - base);
+      m[i] = now;
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = exp2f(s[i][j] - base);
+        sp[(ty * RM + i) * LP + tx + 16 * j] = e;
+        sum += e;
+      }
+      l[i] = l[i] * keep + sum;   // this thread's keys only
+#pragma unroll
+      for (int c = 0; c < NC * 4; ++c) o[i][c] *= keep;
+    }
+    __syncwarp();   // a row's 16 threads are in one warp
+    // weights times values: dims 4 tx + 64 c
+    for (int j = 0; j < kKeys; j += 4) {
+      float pa[RM][4];
+#pragma unroll
+      for (int i = 0; i < RM; ++i) {
+        const float4 x = *(const float4*)&sp[(ty * RM + i) * LP + j];
+        pa[i][0] = x.x; pa[i][1] = x.y; pa[i][2] = x.z; pa[i][3] = x.w;
+      }
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float4 x = *(const float4*)&sv[(j + jj) * NC * 64 + c * 64 + tx * 4];
+#pragma unroll
+          for (int i = 0; i < RM; ++i) {
+            o[i][c * 4 + 0] = fmaf(pa[i][jj], x.x, o[i][c * 4 + 0]);
+            o[i][c * 4 + 1] = fmaf(pa[i][jj], x.y, o[i][c * 4 + 1]);
+            o[i][c * 4 + 2] = fmaf(pa[i][jj], x.z, o[i][c * 4 + 2]);
+            o[i][c * 4 + 3] = fmaf(pa[i][jj], x.w, o[i][c * 4 + 3]);
+          }
+        }
+    }
+  }
+  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], x);
+    Row w;
+    if (!row_of(g, prefix, tile, ty * RM + i, n, BM, &w)) continue;
+    const int64_t row = ((int64_t)w.n * g.a.T + w.t) * g.a.heads + hk * g.group + w.j;
+    if (tx == 0) {
+      g.stat[(part * rows + row) * 2] = m[i];
+      g.stat[(part * rows + row) * 2 + 1] = l[i];
+    }
+    float* acc = g.acc + (part * rows + row) * D;
+    if (l[i] > 0.0f) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c * 64 + tx * 4 + e < D) acc[c * 64 + tx * 4 + e] = o[i][c * 4 + e];
+    }
+  }
+}
+
+// One warp a query row: partial results (maximum, sum, weighted values) of all its key
+// ranges, brought to a common maximum.  out = sum_p a_p O_p / sum_p a_p l_p, a_p = 2^(m_p - m).
+template <typename T>
+__global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g) {
+  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31, parts = g.plan.parts, D = g.dim;
+  if (row >= rows) return;
+  float m = -INFINITY;
+  for (int p = lane; p < parts; p += 32) {
+    const float2 st = *(const float2*)&g.stat[(p * rows + row) * 2];
+    if (st.y > 0.0f) m = fmaxf(m, st.x);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+  float o[8], l = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) o[c] = 0.0f;
+  for (int p = 0; p < parts; ++p) {
+    const float2 st = *(const float2*)&g.stat[(p * rows + row) * 2];
+    if (!(st.y > 0.0f)) continue;   // no key of this range
+    const float w = exp2f(st.x - m);
+    l += w * st.y;
+    const float* acc = g.acc + (p * rows + row) * D;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c * 32 + lane < D) o[c] = fmaf(w, acc[c * 32 + lane], o[c]);
+  }
+  const int h = (int)(row % g.a.heads), t = (int)(row / g.a.heads % g.a.T);
+  const int n = (int)(row / g.a.heads / g.a.T);
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  T* out = (T*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (c * 32 + lane < D) out[c * 32 + lane] = from_f<T>(o[c] * inv);
+  if (lane == 0 && g.lse) g.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+}
+
+size_t simt_smem(int rm, int nc, int D) {
+  const int LD = (D + 3) / 4 * 4 + 4, BM = 16 * rm;
+  return sizeof(float) * ((size_t)BM * LD + kKeys * LD + kKeys * nc * 64 + BM * (kKeys + 4));
+}
+
+template <typename T, int RM, int NC>
+cudaError_t launch(const xp_attn_args& g, cudaStream_t s) {
+  const size_t smem = simt_smem(RM, NC, g.dim);
+  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, RM, NC>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const xp_attn_plan& p = g.plan;
+  const dim3 grid(p.prefix_tiles * p.prefix_splits + g.a.N * p.tail_tiles * p.tail_splits,
+                  g.kv_heads);
+  attn_simt_kernel<T, RM, NC><<<grid, kThreads, smem, s>>>(g);
+  return cudaGetLastError();
+}
+template <typename T, int RM>
+cudaError_t launch_nc(const xp_attn_args& g, cudaStream_t s) {
+  switch ((g.dim + 63) / 64) {
+    case 1: return launch<T, RM, 1>(g, s);
+    case 2: return launch<T, RM, 2>(g, s);
+    case 3: return launch<T, RM, 3>(g, s);
+    default: return launch<T, RM, 4>(g, s);
+  }
+}
+
+}  // namespace
+
+// Row tiles of 16 or 64 query rows; key ranges so that about four CTAs an SM have work.
+xp_attn_plan xp_attn_simt_plan(const xp_cache* c, const xp_attn* a) {
+  xp_attn_plan p = {};
+  const int group = a->heads / c->d.kv_heads, per_seq = a->T * group;
+  p.rows_tile = per_seq > 16 ? 64 : 16;
+  const int64_t want = (int64_t)c->num_sms * 4;
+  auto splits = [&](int64_t tiles, int keys, int* range) {
+    int64_t s = std::max<int64_t>(1, want / std::max<int64_t>(1, tiles * c->d.kv_heads));
+    s = std::min<int64_t>(s, std::max(1, (keys + 4 * kKeys - 1) / (4 * kKeys)));
+    const int64_t r = (keys + s - 1) / s;
+    *range = (int)std::max<int64_t>(kKeys, (r + kKeys - 1) / kKeys * kKeys);
+    return keys > 0 ? (keys + *range - 1) / *range : 0;
+  };
+  p.prefix_tiles = (int)(((int64_t)a->N * per_seq + p.rows_tile - 1) / p.rows_tile);
+  p.tail_tiles = (per_seq + p.rows_tile - 1) / p.rows_tile;
+  p.prefix_splits = (int)splits(p.prefix_tiles, a->prefix_len, &p.prefix_keys);
+  p.tail_splits = (int)splits((int64_t)a->N * p.tail_tiles, a->max_len, &p.tail_keys);
+  p.parts = p.prefix_splits + p.tail_splits;
+  return p;
+}
+
+cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
+  if (g.plan.parts == 0) return cudaSuccess;
+  const bool small = g.plan.rows_tile == 16;
+  if (c->d.dtype == XP_BF16) return small ? launch_nc<bf16, 1>(g, s) : launch_nc<bf16, 4>(g, s);
+  return small ? launch_nc<float, 1>(g, s) : launch_nc<float, 4>(g, s);
+}
+
+cudaError_t xp_launch_attn_combine(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
+  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
+  const unsigned grid = (unsigned)((rows + 7) / 8);
+  if (c->d.dtype == XP_BF16) attn_combine_kernel<bf16><<<grid, 256, 0, s>>>(g);
+  else attn_combine_kernel<float><<<grid, 256, 0, s>>>(g);
+  return cudaGetLastError();
+}

@@ -155,6 +155,11 @@ const char* xp_status_str(xp_status s) {
     case XP_ETIMEOUT: return "bounded wait in a kernel timed out";
     case XP_EUNSUPPORTED: return "unsupported shape";
     case XP_ERANGE: return "latent value outside the fp16 exchange range (saturated)";
+    case XP_EBADPAGE: return "page id out of range, or a page freed too often";
+    case XP_ENOPAGES: return "no free page left in the pool";
+    case XP_ESHARED: return "length would end inside a shared page";
+    case XP_ELENGTH: return "length or row number out of range (clamped)";
+    case XP_EEMPTY: return "target row left no token to draw";
   }
   return "unknown status";
 }
@@ -446,6 +451,8 @@ xp_status xp_get_error(const xp_head* h, cudaStream_t stream) {
   if (cudaMemset(h->err, 0, sizeof(word)) != cudaSuccess) return XP_ECUDA;
   if (word & XP_ERR_TIMEOUT) return XP_ETIMEOUT;
   if (word & XP_ERR_RANGE) return XP_ERANGE;
+  if (word & XP_ERR_EMPTY) return XP_EEMPTY;
+  if (word & XP_ERR_LENGTH) return XP_ELENGTH;
   if (word & XP_ERR_BADTOKEN) return XP_EBADTOKEN;
   return XP_OK;
 }

@@ -36,7 +36,10 @@ struct xp_head {
 };
 
 // device error word bits
-enum : uint32_t { XP_ERR_BADTOKEN = 1u, XP_ERR_TIMEOUT = 2u, XP_ERR_RANGE = 4u };
+enum : uint32_t {
+  XP_ERR_BADTOKEN = 1u, XP_ERR_TIMEOUT = 2u, XP_ERR_RANGE = 4u, XP_ERR_BADPAGE = 8u,
+  XP_ERR_NOPAGES = 16u, XP_ERR_SHARED = 32u, XP_ERR_LENGTH = 64u, XP_ERR_EMPTY = 128u
+};
 
 // Workspace layout.  Regions that must stay zero between calls come first and
 // are sized by the head's max_N so that the layout never moves with N.
@@ -144,6 +147,102 @@ cudaError_t xp_launch_topc_gather(const xp_head* h, const void* base, int64_t sn
 cudaError_t xp_launch_topc_readout(const xp_head* h, const void* lat, const void* base_c,
                                    const int64_t* cand, const void* w2c, int N, int C,
                                    int64_t* blk, float* win, cudaStream_t s);
+
+// Verification of drafted blocks.  packed, marks and tickets must be zero between calls.
+struct xp_verify_ws {
+  size_t marks, tickets, packed, draw_ticket;   // zero between calls
+  size_t part, row;                             // softmax statistics: per chunk, per row
+  size_t total;
+};
+xp_verify_ws xp_verify_layout(const xp_head* h, int N);
+struct xp_verify_args {
+  const void* target;
+  int64_t sn, sb;
+  const float* draft;
+  int64_t ld_draft;
+  const int64_t* blk;
+  const int32_t* n_draft;
+  const float* temperature;
+  const float* u;
+  const float* noise;
+  int64_t ld_noise;
+  int64_t* tokens;
+  int32_t* counts;
+  float* prob;
+  int N, B, V;
+  uint32_t* err;
+  // workspace
+  unsigned* marks;
+  unsigned* tickets;
+  unsigned long long* packed;
+  unsigned* draw_ticket;
+  float* part;
+  float* row;
+};
+cudaError_t xp_launch_verify(const xp_head* h, const xp_verify_args& a, cudaStream_t s);
+
+// Host-side cache: the caller's pools, the prepared scratch, device facts.
+struct xp_cache {
+  xp_cache_desc d;
+  int device, num_sms;
+  bool heads_outside;      // page order: [head][token][dim] instead of [token][head][dim]
+  uint32_t* err;           // device error word (XP_ERR_* bits)
+  int32_t *src, *dst, *cnt;  // page moves: source, target, tokens (scratch, `pages` each)
+  int32_t* n_moves;        // their number
+  int32_t* map;            // compaction: new id of every page (scratch)
+  int32_t *row_a, *row_b, *row_c;  // per-row scratch of the table calls (max_seqs each)
+  int attn_tc;             // tensor-core attention usable for this cache's shapes
+  CUtensorMap tm_k, tm_v;  // the pools as (dim, token, head, page, layer)
+};
+
+cudaError_t xp_launch_append(const xp_cache* c, int layer, const void* k, const void* v, int64_t sn,
+                             int64_t st, int64_t sh, const int32_t* table, int64_t ld,
+                             const int32_t* lens, int N, int T, cudaStream_t s);
+// moves given by the caller (n on the host) or left by a table kernel (n_moves on the device);
+// tokens == nullptr copies whole pages
+cudaError_t xp_launch_copy_pages(const xp_cache* c, const int32_t* src, const int32_t* dst,
+                                 const int32_t* tokens, int n, const int32_t* n_dev,
+                                 cudaStream_t s);
+cudaError_t xp_launch_resize(const xp_cache* c, const int32_t* table, int64_t ld,
+                             const int32_t* lens, const int32_t* new_lens, const int32_t* refs,
+                             int N, int width, int32_t* table_out, int64_t ld_out,
+                             int32_t* lens_out, int32_t* refs_out, cudaStream_t s);
+cudaError_t xp_launch_fork(const xp_cache* c, const int32_t* table, int64_t ld,
+                           const int32_t* lens, int rows, const int32_t* parent,
+                           const int32_t* cut, int M, int width, const int32_t* refs,
+                           int32_t* child, int64_t ld_child, int32_t* child_lens,
+                           int32_t* refs_out, cudaStream_t s);
+cudaError_t xp_launch_compact(const xp_cache* c, const int32_t* table, int64_t ld,
+                              const int32_t* lens, int N, int width, const int32_t* refs,
+                              int32_t* table_out, int64_t ld_out, int32_t* refs_out, int32_t* map,
+                              int32_t* live, cudaStream_t s);
+
+// How one attention call is split: `prefix_splits` ranges of prefix_keys keys, then
+// `tail_splits` ranges of tail_keys keys; every range leaves one partial result a row.
+struct xp_attn_plan {
+  int rows_tile;                 // query rows of one work item
+  int prefix_tiles, tail_tiles;  // row tiles: over the batch, of one sequence
+  int prefix_splits, prefix_keys, tail_splits, tail_keys;
+  int parts;
+  size_t stat_off, acc_off, total;   // workspace: (max, sum) pairs, accumulators
+};
+struct xp_attn_args {
+  xp_attn a;
+  int group, kv_heads, dim, page_size, pages;
+  const void *q, *k, *v;         // k, v: this layer's pools
+  int64_t kv_page, kv_token, kv_head;
+  const int32_t *prefix_table, *table, *lens;
+  int64_t ld_table;
+  void* out;
+  float* lse;
+  float* stat;                   // [parts][N*T*heads][2]
+  float* acc;                    // [parts][N*T*heads][dim]
+  uint32_t* err;
+  xp_attn_plan plan;
+};
+xp_attn_plan xp_attn_simt_plan(const xp_cache* c, const xp_attn* a);
+cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
+cudaError_t xp_launch_attn_combine(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 
 // Launch with a programmatic dependency on the previous kernel in the stream:
 // the kernel's prologue may overlap that kernel's tail; the kernel itself must

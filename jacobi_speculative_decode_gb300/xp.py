@@ -18,9 +18,11 @@ LIB_PATH = os.path.join(_HERE, "libxp.so")
 XP_BF16, XP_F32 = 0, 1
 XP_PASSES_AUTO, XP_PASSES_PERSISTENT, XP_PASSES_PER_STAGE = 0, 1, 2
 STATUS = {0: "XP_OK", 1: "XP_EINVAL", 2: "XP_ECAPACITY", 3: "XP_ENOTPREPARED", 4: "XP_ECUDA",
-          5: "XP_EBADTOKEN", 6: "XP_ETIMEOUT", 7: "XP_EUNSUPPORTED", 8: "XP_ERANGE"}
+          5: "XP_EBADTOKEN", 6: "XP_ETIMEOUT", 7: "XP_EUNSUPPORTED", 8: "XP_ERANGE",
+          9: "XP_EBADPAGE", 10: "XP_ENOPAGES", 11: "XP_ESHARED", 12: "XP_ELENGTH", 13: "XP_EEMPTY"}
 XP_OK, XP_EINVAL, XP_ECAPACITY, XP_ENOTPREPARED, XP_ECUDA, XP_EBADTOKEN, XP_ETIMEOUT, \
-    XP_EUNSUPPORTED, XP_ERANGE = range(9)
+    XP_EUNSUPPORTED, XP_ERANGE, XP_EBADPAGE, XP_ENOPAGES, XP_ESHARED, XP_ELENGTH, \
+    XP_EEMPTY = range(14)
 
 
 class XPError(RuntimeError):
@@ -37,6 +39,25 @@ class xp_weights(ctypes.Structure):
                 ("in_proj", ctypes.c_void_p), ("mix_L", ctypes.c_void_p),
                 ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
                 ("w_down", ctypes.c_void_p), ("w2", ctypes.c_void_p)]
+
+
+class xp_cache_desc(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("layers", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("max_seqs", ctypes.c_int),
+                ("dtype", ctypes.c_int),
+                ("stride_layer", ctypes.c_int64), ("stride_page", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class xp_attn(ctypes.Structure):
+    _fields_ = [("layer", ctypes.c_int), ("N", ctypes.c_int), ("T", ctypes.c_int),
+                ("heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("prefix_len", ctypes.c_int), ("max_len", ctypes.c_int),
+                ("scale", ctypes.c_float),
+                ("q_stride_n", ctypes.c_int64), ("q_stride_t", ctypes.c_int64),
+                ("q_stride_h", ctypes.c_int64), ("o_stride_n", ctypes.c_int64),
+                ("o_stride_t", ctypes.c_int64), ("o_stride_h", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -70,6 +91,21 @@ _SIGS = {
     "xp_readout_kernel_name": (ctypes.c_char_p, [_P]),
     "xp_profile_timeline": (_I, [_P, _P, _S, _I, ctypes.POINTER(_S)]),
     "xp_status_str": (ctypes.c_char_p, [_I]),
+    "xp_verify_workspace_bytes": (_S, [_P, _I]),
+    "xp_verify_drafts": (_I, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I64, _P, _P,
+                              _P, _P, _S, _P]),
+    "xp_cache_prep_bytes": (_S, [ctypes.POINTER(xp_cache_desc)]),
+    "xp_cache_create": (_I, [ctypes.POINTER(xp_cache_desc), _P, _S, _P, ctypes.POINTER(_P)]),
+    "xp_cache_destroy": (None, [_P]),
+    "xp_cache_get_error": (_I, [_P, _P]),
+    "xp_cache_append": (_I, [_P, _I, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P, _I64, _P, _I, _I, _P]),
+    "xp_cache_copy": (_I, [_P, _P, _P, _I, _P]),
+    "xp_cache_resize": (_I, [_P, _P, _I64, _P, _P, _P, _I, _I, _I, _P, _I64, _P, _P, _P]),
+    "xp_cache_fork": (_I, [_P, _P, _I64, _P, _I, _P, _P, _I, _I, _P, _I, _P, _I64, _P, _P, _P]),
+    "xp_cache_compact": (_I, [_P, _P, _I64, _P, _I, _I, _P, _I, _P, _I64, _P, _P, _P, _P]),
+    "xp_attention_workspace_bytes": (_S, [_P, ctypes.POINTER(xp_attn)]),
+    "xp_prefix_attention": (_I, [_P, ctypes.POINTER(xp_attn), _P, _P, _I, _P, _I64, _I, _P, _P, _P,
+                                 _P, _S, _P]),
 }
 
 _lib = None
@@ -274,6 +310,205 @@ def xp_readout_kernel_name(head) -> str:
     return lib().xp_readout_kernel_name(head).decode()
 
 
+# ------------------------------------- verification, cache and attention calls ---
+#
+# These calls take their sizes and strides from the tensors; a tensor that the C call could
+# not read as it is (another type, a strided last dimension, too few elements) is refused
+# with ValueError.
+
+def _want(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _code(name, t):
+    """The library's type code of a tensor's dtype."""
+    import torch
+    _want(t.dtype in (torch.bfloat16, torch.float32), f"{name}: bf16 or fp32")
+    return XP_BF16 if t.dtype == torch.bfloat16 else XP_F32
+
+
+def _ints(name, t, n):
+    """A contiguous int32 vector of at least n elements on the GPU (None passes)."""
+    import torch
+    if t is not None:
+        _want(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() >= n,
+              f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
+
+
+def _table(name, t, rows=None):
+    """An int32 page table [rows, width] on the GPU, unit stride over the columns."""
+    import torch
+    _want(t.dtype == torch.int32 and t.is_cuda and t.dim() == 2 and t.shape[1] > 0
+          and (t.stride(1) == 1 or t.shape[1] == 1) and (rows is None or t.shape[0] >= rows),
+          f"{name}: an int32 CUDA tensor [rows, width], unit stride over the columns")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def xp_verify_workspace_bytes(head, N: int) -> int:
+    return lib().xp_verify_workspace_bytes(head, N)
+
+
+def xp_verify_drafts(head, target, draft, blk, n_draft, temperature, u, noise, tokens, counts, prob,
+                     ws, stream=None):
+    """Accept drafted slots and draw one token a block.  target [N, B, V]; draft
+    [N*(B-1), >= V] fp32 logits, or None for greedy (one-hot) drafts; blk [N, B]; u [N, B-1];
+    noise [N, >= V]; out: tokens [N, B], counts [N], prob [N, B-1] (or None)."""
+    import torch
+    N, B, V = target.shape
+    f32, i64, i32 = torch.float32, torch.int64, torch.int32
+    _want(target.stride(2) == 1 and target.is_cuda, "target: [N, B, V] with unit stride over V")
+    _want(draft is None or (draft.dtype == f32 and draft.dim() == 2 and draft.stride(1) == 1
+                            and draft.shape[0] >= N * (B - 1) and draft.shape[1] >= V),
+          "draft: fp32 [N*(B-1), >= V] with unit stride over V")
+    _want(noise.dtype == f32 and noise.dim() == 2 and noise.stride(1) == 1 and noise.shape[0] >= N
+          and noise.shape[1] >= V, "noise: fp32 [N, >= V] with unit stride over V")
+    for name, t, dt, count in (("blk", blk, i64, N * B), ("n_draft", n_draft, i32, N),
+                               ("temperature", temperature, f32, N), ("u", u, f32, N * (B - 1)),
+                               ("tokens", tokens, i64, N * B), ("counts", counts, i32, N),
+                               ("prob", prob, f32, N * (B - 1))):
+        _want(t is None or (t.dtype == dt and t.is_contiguous() and t.numel() >= count),
+              f"{name}: contiguous {dt} of at least {count} elements")
+    _check("xp_verify_drafts", lib().xp_verify_drafts(
+        head, _ptr(target), target.stride(0), target.stride(1), _ptr(draft),
+        draft.stride(0) if draft is not None else 0, _ptr(blk), _ptr(n_draft), N, B, V,
+        _code("target", target), _ptr(temperature), _ptr(u), _ptr(noise), noise.stride(0) if N > 1 else noise.shape[1], _ptr(tokens),
+        _ptr(counts), _ptr(prob), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def make_cache_desc(k, v, max_seqs: int = 4096) -> xp_cache_desc:
+    """Descriptor of K and V pools seen as [layers, pages, page_size, kv_heads, head_dim] (views
+    with the heads outside the tokens too)."""
+    _want(k.dim() == 5 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
+          and k.stride(4) == 1 and k.is_cuda and v.is_cuda,
+          "k, v: bf16 or fp32 CUDA tensors [layers, pages, page_size, kv_heads, head_dim] of the "
+          "same strides, unit stride over head_dim")
+    layers, pages, ps, heads, dim = k.shape
+    return xp_cache_desc(pages, ps, layers, heads, dim, max_seqs, _code("k", k), k.stride(0),
+                         k.stride(1), k.stride(2), k.stride(3), _ptr(k), _ptr(v))
+
+
+def xp_cache_prep_bytes(d: xp_cache_desc) -> int:
+    return lib().xp_cache_prep_bytes(ctypes.byref(d))
+
+
+def xp_cache_create(d: xp_cache_desc, prep, stream=None):
+    out = ctypes.c_void_p()
+    _check("xp_cache_create", lib().xp_cache_create(ctypes.byref(d), _ptr(prep), _nbytes(prep),
+                                                    _stream(stream), ctypes.byref(out)))
+    return out.value
+
+
+def xp_cache_destroy(cache):
+    lib().xp_cache_destroy(cache)
+
+
+def xp_cache_get_error(cache, stream=None) -> int:
+    """Synchronise the stream, read and clear the cache's error word; returns the status code."""
+    return lib().xp_cache_get_error(cache, _stream(stream))
+
+
+def xp_cache_append(cache, layer, k, v, table, lens, stream=None):
+    """Write the K and V rows [N, T, kv_heads, head_dim] of the newest tokens (lens counts them)."""
+    N, T = k.shape[:2]
+    _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
+          and k.stride(3) == 1, "k, v: [N, T, kv_heads, head_dim] of the same strides")
+    ld = _table("table", table, N)
+    _ints("lens", lens, N)
+    _check("xp_cache_append", lib().xp_cache_append(
+        cache, layer, _ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), k.shape[2],
+        k.shape[3], _code("k", k), _ptr(table), ld, _ptr(lens), N, T, _stream(stream)))
+
+
+def xp_cache_copy(cache, src, dst, stream=None):
+    """Copy whole pages src[i] -> dst[i] in every layer."""
+    _ints("src", src, 0)
+    _ints("dst", dst, src.numel())
+    _check("xp_cache_copy", lib().xp_cache_copy(cache, _ptr(src), _ptr(dst), src.numel(),
+                                                _stream(stream)))
+
+
+def xp_cache_resize(cache, table, lens, new_lens, refs, table_out, lens_out, refs_out, stream=None):
+    """Lengths lens -> new_lens: give back or take pages (outputs may be the inputs)."""
+    N, width = table.shape
+    ld, ld_out = _table("table", table), _table("table_out", table_out, N)
+    _want(table_out.shape[1] >= width, "table_out: as wide as table")
+    for name, t in (("lens", lens), ("new_lens", new_lens), ("lens_out", lens_out)):
+        _ints(name, t, N)
+    _ints("refs", refs, 1)
+    _ints("refs_out", refs_out, refs.numel())
+    _check("xp_cache_resize", lib().xp_cache_resize(
+        cache, _ptr(table), ld, _ptr(lens), _ptr(new_lens), _ptr(refs), refs.numel(), N, width,
+        _ptr(table_out), ld_out, _ptr(lens_out), _ptr(refs_out), _stream(stream)))
+
+
+def xp_cache_fork(cache, table, lens, parent, cut, refs, child_table, child_lens, refs_out,
+                  stream=None):
+    """Children parent[i] continued at min(lens[parent[i]], cut[i]) (cut may be None)."""
+    rows, width = table.shape
+    M = parent.numel()
+    ld, ld_child = _table("table", table), _table("child_table", child_table, M)
+    _want(child_table.shape[1] >= width, "child_table: as wide as table")
+    for name, t, n in (("lens", lens, rows), ("parent", parent, M), ("cut", cut, M),
+                       ("child_lens", child_lens, M), ("refs", refs, 1)):
+        _ints(name, t, n)
+    _ints("refs_out", refs_out, refs.numel())
+    _check("xp_cache_fork", lib().xp_cache_fork(
+        cache, _ptr(table), ld, _ptr(lens), rows, _ptr(parent), _ptr(cut), M, width, _ptr(refs),
+        refs.numel(), _ptr(child_table), ld_child, _ptr(child_lens), _ptr(refs_out), _stream(stream)))
+
+
+def xp_cache_compact(cache, table, lens, refs, table_out, refs_out, map=None, live=None,
+                     stream=None):
+    """Pack the pages in use to the pool's front; map[page] is each page's new id."""
+    N, width = table.shape
+    ld, ld_out = _table("table", table), _table("table_out", table_out, N)
+    _want(table_out.shape[1] >= width, "table_out: as wide as table")
+    _ints("lens", lens, N)
+    _ints("refs", refs, 1)
+    _ints("refs_out", refs_out, refs.numel())
+    _ints("map", map, refs.numel())
+    _ints("live", live, 1)
+    _check("xp_cache_compact", lib().xp_cache_compact(
+        cache, _ptr(table), ld, _ptr(lens), N, width, _ptr(refs), refs.numel(), _ptr(table_out),
+        ld_out, _ptr(refs_out), _ptr(map), _ptr(live), _stream(stream)))
+
+
+def make_attn(q, out, layer: int, prefix_len: int, max_len: int, scale: float) -> xp_attn:
+    """Sizes and strides of one attention call: q, out [N, T, heads, head_dim]."""
+    _want(q.dim() == 4 and q.shape == out.shape and q.dtype == out.dtype and q.stride(3) == 1
+          and out.stride(3) == 1, "q, out: [N, T, heads, head_dim] of one type, unit stride last")
+    N, T, heads, dim = q.shape
+    a = xp_attn(layer, N, T, heads, dim, _code("q", q), prefix_len, max_len, scale, *q.stride()[:3], *out.stride()[:3])
+    a.q_like = (q.shape, q.stride(), q.dtype)
+    a.out_like = (out.shape, out.stride(), out.dtype)
+    return a
+
+
+def xp_attention_workspace_bytes(cache, attn: xp_attn) -> int:
+    return lib().xp_attention_workspace_bytes(cache, ctypes.byref(attn))
+
+
+def xp_prefix_attention(cache, attn, q, prefix_table, table, lens, out, lse, ws, stream=None):
+    """Attention of attn.N sequences of attn.T new tokens over a shared prefix and their tails
+    (attn from make_attn for tensors of these shapes and strides)."""
+    _want((q.shape, q.stride(), q.dtype) == attn.q_like
+          and (out.shape, out.stride(), out.dtype) == attn.out_like,
+          "q, out: the shapes, strides and type that make_attn was given")
+    ld = width = 0
+    if table is not None:
+        ld, width = _table("table", table, attn.N), table.shape[1]
+    _ints("lens", lens, attn.N)
+    _ints("prefix_table", prefix_table, 0)
+    _want(lse is None or (lse.is_contiguous() and lse.element_size() == 4
+                          and lse.numel() >= attn.N * attn.T * attn.heads),
+          "lse: contiguous fp32 [N, T, heads]")
+    _check("xp_prefix_attention", lib().xp_prefix_attention(
+        cache, ctypes.byref(attn), _ptr(q), _ptr(prefix_table),
+        0 if prefix_table is None else prefix_table.numel(), _ptr(table), ld, width, _ptr(lens),
+        _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
 # ------------------------------------------------------ torch conveniences ---
 
 def torch_dtype(dtype: str):
@@ -323,9 +558,44 @@ class Head:
         w = self.weights_struct()
         return torch.zeros(xp_workspace_bytes(w, N, topc), dtype=torch.uint8, device="cuda")
 
+    def verify_workspace(self, N: int):
+        import torch
+        return torch.zeros(xp_verify_workspace_bytes(self.handle, N), dtype=torch.uint8,
+                           device="cuda")
+
     def close(self):
         if self.handle:
             xp_head_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Cache:
+    """A paged cache over the caller's K and V pools, seen as [layers, pages, page_size, kv_heads,
+    head_dim] (kept alive here), with its prepared scratch and handle."""
+
+    def __init__(self, k, v, max_seqs: int = 4096, stream=None):
+        import torch
+        self.handle = None
+        self.k, self.v = k, v
+        desc = make_cache_desc(k, v, max_seqs)
+        self.prep = torch.empty(max(256, xp_cache_prep_bytes(desc)), dtype=torch.uint8,
+                                device=k.device)
+        self.handle = xp_cache_create(desc, self.prep, stream)
+
+    def attention_workspace(self, attn: xp_attn):
+        import torch
+        return torch.empty(xp_attention_workspace_bytes(self.handle, attn), dtype=torch.uint8,
+                           device=self.k.device)
+
+    def close(self):
+        if self.handle:
+            xp_cache_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
