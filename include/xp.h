@@ -458,7 +458,7 @@ xp_status xp_cache_compact(const xp_cache* cache, const int32_t* table, int64_t 
  * prefix_table: device int32, prefix_pages >= ceil(prefix_len / page_size) entries.  table:
  * device int32, row n at table + n*ld_table, width >= ceil(max_len / page_size) columns.  lens: device [N] int32;
  * lengths above max_len are clamped (XP_ELENGTH).  lse: device fp32 [N, T, heads] or NULL.
- * Scores, softmax and sums are fp32 (bf16: each weight is rounded to bf16 before it
+ * scale: positive and finite.  Scores, softmax and sums are fp32 (bf16: each weight is rounded to bf16 before it
  * multiplies v, as the tensor cores take it). */
 typedef struct {
   int layer, N, T, heads;

@@ -1,5 +1,6 @@
 // Host side of the calls around a drafted block: the paged cache, the shared-prefix
 // attention over it and the verification.  Validation and launch order only.
+#include <float.h>
 #include <limits.h>
 
 #include <algorithm>
@@ -68,13 +69,13 @@ xp_status check_table(const xp_cache* c, const int32_t* table, int64_t ld, const
 bool valid_attn(const xp_cache* c, const xp_attn* a) {
   return a && a->layer >= 0 && a->layer < c->d.layers && a->N >= 0 && a->T > 0 && a->heads > 0 &&
          a->head_dim == c->d.head_dim && a->dtype == c->d.dtype &&
-         a->heads % c->d.kv_heads == 0 && a->prefix_len >= 0 && a->max_len >= 0 &&
+         a->scale > 0.0f && a->scale <= FLT_MAX && a->heads % c->d.kv_heads == 0 && a->prefix_len >= 0 && a->max_len >= 0 &&
          (int64_t)a->N * a->T * a->heads <= INT_MAX &&
          (int64_t)a->prefix_len + a->max_len <= INT_MAX - 1024;
 }
 
 xp_attn_plan attn_plan(const xp_cache* c, const xp_attn* a) {
-  xp_attn_plan p = xp_attn_simt_plan(c, a);
+  xp_attn_plan p = c->attn_tc ? xp_attn_tc_plan(c, a) : xp_attn_simt_plan(c, a);
   const size_t rows = (size_t)a->N * a->T * a->heads;
   p.stat_off = 0;
   p.acc_off = align_up(rows * p.parts * 8);
@@ -117,6 +118,7 @@ xp_status xp_cache_create(const xp_cache_desc* d, void* prep_dev, size_t prep_by
   c->row_a = (int32_t*)(p + L.row_a);
   c->row_b = (int32_t*)(p + L.row_b);
   c->row_c = (int32_t*)(p + L.row_c);
+  c->attn_tc = xp_attn_tc_maps(c);
   if (cudaMemsetAsync(prep_dev, 0, L.total, stream) != cudaSuccess) {
     delete c;
     return XP_ECUDA;
@@ -250,7 +252,7 @@ xp_status xp_prefix_attention(const xp_cache* c, const xp_attn* a, const void* q
   g.acc = (float*)((char*)ws + plan.acc_off);
   g.err = c->err;
   g.plan = plan;
-  cudaError_t e = xp_launch_attn_simt(c, g, stream);
+  cudaError_t e = c->attn_tc ? xp_launch_attn_tc(c, g, stream) : xp_launch_attn_simt(c, g, stream);
   if (e == cudaSuccess) e = xp_launch_attn_combine(c, g, stream);
   return cuda_status(e);
 }

@@ -191,7 +191,7 @@ struct xp_cache {
   int32_t* n_moves;        // their number
   int32_t* map;            // compaction: new id of every page (scratch)
   int32_t *row_a, *row_b, *row_c;  // per-row scratch of the table calls (max_seqs each)
-  int attn_tc;             // tensor-core attention usable for this cache's shapes
+  int attn_tc;             // tokens of a TMA box of the tensor-core attention, 0: not usable
   CUtensorMap tm_k, tm_v;  // the pools as (dim, token, head, page, layer)
 };
 
@@ -241,6 +241,9 @@ struct xp_attn_args {
   xp_attn_plan plan;
 };
 xp_attn_plan xp_attn_simt_plan(const xp_cache* c, const xp_attn* a);
+int xp_attn_tc_maps(xp_cache* c);   // tokens of a TMA box, 0 where the kernel cannot run
+xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a);
+cudaError_t xp_launch_attn_tc(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 cudaError_t xp_launch_attn_combine(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 
