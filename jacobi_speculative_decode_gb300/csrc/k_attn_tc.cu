@@ -10,8 +10,8 @@
 // else they are the even and the odd key tiles of one row tile and are joined at the end.
 // O is rescaled only when a row's maximum grew by more than 2^8 since the last time.
 //
-// Warps: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread is a query row), 8 issues the
-// products, 9 loads K and V by TMA, a box of tokens of one page at a time.
+// Warps: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread is a query row), 8 and 9 issue
+// their products, 10 loads K and V by TMA, a box of tokens of one page at a time.
 #include <math.h>
 
 #include <algorithm>
@@ -25,9 +25,12 @@ namespace {
 
 constexpr int kRows = 128;      // query rows of a tile (tensor memory lanes)
 constexpr int kTile = 128;      // keys of a tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// registers a thread: 384 x 168 at launch, moved from the issuing warpgroup to the softmax ones
+constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
 constexpr int kChunkBytes = kTile * 128;   // 64 elements of 128 rows, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;
+constexpr int kApart = 4;       // items of a stream from which the streams are set apart
 constexpr float kLazy = 8.0f;   // growth of the maximum (base 2) that P may carry
 
 template <int D>
@@ -40,7 +43,7 @@ struct Cfg {
 
 struct Bars {
   uint64_t full[10], empty[10];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2];
+  uint64_t q_full, s_full[2], p_half[2], p_full[2], o_full[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -57,6 +60,25 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// two fp32 operations an instruction
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
@@ -143,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars* bars = reinterpret_cast<Bars*>(smem + C::SMEM);
   volatile int* abort = &bars->abort;
   const uint32_t sq = ptx::smem_u32(smem), ring = sq + 2 * C::TILE_BYTES;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
   Unit w;
   const bool work = decode_unit(g, blockIdx.x, &w);
@@ -168,11 +190,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bars->full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bars->empty[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->empty[s]), w.shared ? 2 : 1);
     }
     ptx::mbar_init(ptx::smem_u32(&bars->q_full), 8);
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(ptx::smem_u32(&bars->s_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars->p_half[t]), t ? active1 : active0);
       ptx::mbar_init(ptx::smem_u32(&bars->p_full[t]), t ? active1 : active0);
       ptx::mbar_init(ptx::smem_u32(&bars->o_full[t]), 1);
     }
@@ -188,93 +211,129 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp == 9) {
-    // ---- K and V tiles: lane (chunk, box) loads `box` tokens of one page ----
-    const uint64_t pol = w.prefix ? ptx::policy_evict_last() : ptx::policy_evict_first();
-    uint32_t issued = 0;   // tiles loaded
-    bool ok = true;
-    for (int pos = 0; pos < 2 * T && ok; ++pos) {
-      // pos -> K0 K1 V0 K2 V1 ...
-      const bool is_v = pos == 2 * T - 1 || (pos > 0 && pos % 2 == 0);
-      const int j = pos == 0 ? 0 : pos == 2 * T - 1 ? T - 1 : is_v ? pos / 2 - 1 : (pos + 1) / 2;
-      const int s = pos % C::STAGES;
-      ok = ptx::mbar_wait(ptx::smem_u32(&bars->empty[s]), ((pos / C::STAGES) & 1) ^ 1, abort, g.err);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      const int key = w.k0 + j * kTile;
-      const int boxes = (min(kTile, w.k1 - key) + box - 1) / box;
-      const uint32_t full = ptx::smem_u32(&bars->full[s]);
-      if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * box * 128 * C::CH);
-      __syncwarp();
-      if (lane < boxes * C::CH) {
-        const int c = lane / boxes, b = lane % boxes, at = key + b * box;
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 10) {
+      // ---- K and V tiles: lane (chunk, box) loads `box` tokens of one page ----
+      const uint64_t pol = w.prefix ? ptx::policy_evict_last() : ptx::policy_evict_first();
+      const int per = kTile / box, chunk = lane / per, in_tile = lane % per * box;
+      int issued = 0;   // tiles loaded
+      // this lane's page of tile j (its box may lie behind the range: then none is loaded)
+      auto page_of = [&](int j) {
+        const int at = w.k0 + j * kTile + in_tile;
+        if (chunk >= C::CH || at >= w.k1) return -1;
         int page = w.table[at / g.page_size];
         if (page < 0 || page >= g.pages) {
           atomicOr(g.err, XP_ERR_BADPAGE);
           page = page < 0 ? 0 : g.pages - 1;
         }
-        const uint32_t dst = ring + s * C::TILE_BYTES + c * kChunkBytes + b * box * 128;
-        ptx::tma_load_5d(dst, is_v ? &tm_v : &tm_k, full, c * 64, at % g.page_size, w.hk, page,
-                         g.a.layer, pol);
-      }
-      ++issued;
-    }
-    // nothing may land in shared memory after the CTA is gone
-    volatile int no_abort = 0;
-    for (int s = 0; s < C::STAGES; ++s) {
-      const int n = ((int)issued + C::STAGES - 1 - s) / C::STAGES;   // loads of this stage
-      if (n > 0) ptx::mbar_wait(ptx::smem_u32(&bars->full[s]), (n - 1) & 1, &no_abort, g.err);
-    }
-  } else if (warp == 8) {
-    // ---- products: S(i) = Q K^T for item i, O += P(i) V two items later ----
-    if (lane == 0) {
-      constexpr uint32_t kS = ptx::idesc_bf16_f32(kRows, kTile);
-      constexpr uint32_t kO = ptx::idesc_bf16_f32(kRows, D) | (1u << 16);   // V: head dims contiguous
-      auto wait = [&](uint64_t* bar, int phase) {
-        return ptx::mbar_wait(ptx::smem_u32(bar), phase & 1, abort, g.err);
+        return page;
       };
-      auto kv = [&](int i) { return w.shared ? i >> 1 : i; };
-      // the stage of load `pos` is free again, where another load waits for it (a commit that
-      // nobody waits for could land behind the CTA's end)
-      auto release = [&](int i, int pos) {
-        if ((!w.shared || (i & 1)) && pos + C::STAGES < 2 * T)
-          ptx::mma_commit(ptx::smem_u32(&bars->empty[pos % C::STAGES]));
-      };
-      auto scores = [&](int i) {
-        const int t = i & 1, pos = pos_k(kv(i)), s = pos % C::STAGES;
-        if (!wait(&bars->full[s], pos / C::STAGES)) return false;
-        ptx::tc_fence_after();
-        const uint32_t q = sq + (w.shared ? t * C::TILE_BYTES : 0), k = ring + s * C::TILE_BYTES;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * kChunkBytes + (ks % 4) * 32;
-          ptx::mma_bf16(tmem + t * kTile, ptx::sw128_desc(q + off), ptx::sw128_desc(k + off), kS,
-                        ks > 0);
-        }
-        ptx::mma_commit(ptx::smem_u32(&bars->s_full[t]));
-        release(i, pos);
+      auto load = [&](int j, int page, const CUtensorMap* map) {
+        const int s = issued % C::STAGES;
+        bool ok = ptx::mbar_wait(ptx::smem_u32(&bars->empty[s]), ((issued / C::STAGES) & 1) ^ 1, abort,
+                                 g.err);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return false;
+        const int key = w.k0 + j * kTile;
+        const int boxes = (min(kTile, w.k1 - key) + box - 1) / box;
+        const uint32_t full = ptx::smem_u32(&bars->full[s]);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * box * 128 * C::CH);
+        __syncwarp();
+        if (page >= 0)
+          ptx::tma_load_5d(ring + s * C::TILE_BYTES + chunk * kChunkBytes + in_tile * 128, map, full,
+                           chunk * 64, (key + in_tile) % g.page_size, w.hk, page, g.a.layer, pol);
+        ++issued;
         return true;
       };
-      bool ok = wait(&bars->q_full, 0);
-      ok = ok && scores(0);
-      if (items > 1) ok = ok && scores(1);
-      for (int i = 0; i < items && ok; ++i) {
-        const int t = i & 1, pos = pos_v(kv(i), T), s = pos % C::STAGES;
-        ok = wait(&bars->p_full[t], i >> 1) && wait(&bars->full[s], pos / C::STAGES);
+      int now = page_of(0), next = page_of(1);   // the page ids are read ahead of the loads
+      bool ok = load(0, now, &tm_k);
+      for (int j = 0; j < T && ok; ++j) {
+        const int after = page_of(j + 2);
+        if (j + 1 < T) ok = load(j + 1, next, &tm_k);
+        ok = ok && load(j, now, &tm_v);
+        now = next;
+        next = after;
+      }
+      // nothing may land in shared memory after the CTA is gone
+      volatile int no_abort = 0;
+      for (int s = 0; s < C::STAGES; ++s) {
+        const int n = (issued + C::STAGES - 1 - s) / C::STAGES;   // loads of this stage
+        if (n > 0) ptx::mbar_wait(ptx::smem_u32(&bars->full[s]), (n - 1) & 1, &no_abort, g.err);
+      }
+    } else if (warp < 10) {
+      // ---- the products of stream t: O += P V of its item j, then S = Q K^T of item j + 1 in
+      // its place.  The warp runs the loop converged, so that descriptors stay in uniform
+      // registers, and a warp a stream, so that one's waits run under the other's products ----
+      constexpr uint32_t kS = ptx::idesc_bf16_f32(kRows, kTile);
+      constexpr uint32_t kO = ptx::idesc_bf16_f32(kRows, D) | (1u << 16);   // V: head dims contiguous
+      const int t = warp - 8, mine = (items + 1 - t) / 2;
+      const uint32_t q = sq + (w.shared ? t * C::TILE_BYTES : 0);
+      const uint32_t s_col = tmem + t * kTile, o_col = tmem + 2 * kTile + t * D;
+      const bool leader = ptx::elect_one();
+      auto wait = [&](uint64_t* bar, int phase) {
+        const bool ok = ptx::mbar_wait(ptx::smem_u32(bar), phase & 1, abort, g.err);
+        return __all_sync(0xFFFFFFFFu, ok) != 0;
+      };
+      auto loaded = [&](int pos) { return wait(&bars->full[pos % C::STAGES], pos / C::STAGES); };
+      auto kv = [&](int j) { return w.shared ? j : 2 * j + t; };
+      // the stage of load `pos` is free again, where another load waits for it (a commit that
+      // nobody waits for could land behind the CTA's end)
+      auto release = [&](int pos) {
+        if (pos + C::STAGES < 2 * T) ptx::mma_commit(ptx::smem_u32(&bars->empty[pos % C::STAGES]));
+      };
+      auto scores = [&](int pos) {
+        const uint32_t k = ring + pos % C::STAGES * C::TILE_BYTES;
+        if (leader) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks / 4) * kChunkBytes + (ks % 4) * 32;
+            ptx::mma_bf16(s_col, ptx::sw128_desc(q + off), ptx::sw128_desc(k + off), kS, ks > 0);
+          }
+          ptx::mma_commit(ptx::smem_u32(&bars->s_full[t]));
+          release(pos);
+        }
+        __syncwarp();
+      };
+      bool ok = mine > 0 && wait(&bars->q_full, 0) && loaded(pos_k(kv(0)));
+      // the streams run half a period apart (started together they would stay together, and
+      // neither's products would run under the other's exponentials)
+      if (ok && t == 1 && mine >= kApart) ok = wait(&bars->p_half[0], 0);
+      if (ok) {
+        ptx::tc_fence_after();
+        scores(pos_k(kv(0)));
+      }
+      for (int j = 0; j < mine && ok; ++j) {
+        const int pv = pos_v(kv(j), T), pk = pos_k(kv(j + 1));
+        const uint32_t v = ring + pv % C::STAGES * C::TILE_BYTES;
+        // the tiles are there before the weights are
+        ok = loaded(pv) && (j + 1 >= mine || loaded(pk));
+        ok = ok && wait(&bars->p_half[t], j);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t v = ring + s * C::TILE_BYTES;
+        if (leader) {
 #pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
-          ptx::mma_bf16_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + ks * 8, v_desc(v + ks * 2048),
-                           kO, i > 1 || ks > 0);
-        ptx::mma_commit(ptx::smem_u32(&bars->o_full[t]));
-        release(i, pos);
-        if (i + 2 < items) ok = scores(i + 2);
+          for (int ks = 0; ks < kTile / 32; ++ks)
+            ptx::mma_bf16_ts(o_col, s_col + ks * 8, v_desc(v + ks * 2048), kO, j > 0 || ks > 0);
+        }
+        __syncwarp();
+        ok = wait(&bars->p_full[t], j);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int ks = kTile / 32; ks < kTile / 16; ++ks)
+            ptx::mma_bf16_ts(o_col, s_col + ks * 8, v_desc(v + ks * 2048), kO, 1);
+          ptx::mma_commit(ptx::smem_u32(&bars->o_full[t]));
+          release(pv);
+        }
+        __syncwarp();
+        if (j + 1 < mine) scores(pk);
       }
     }
   } else {
     // ---- softmax ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp / 4, r = threadIdx.x - t * 128;
     const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
     const int tile = w.shared ? w.tile + t : w.tile;
@@ -310,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool active = warp % 4 < (t ? active1 : active0);
     int n, tt, h, limit;
     const int64_t row = row_of(g, w, tile, r, &n, &tt, &h, &limit);
+    if (row < 0) limit = w.k1;   // rows behind the end ask for no mask of their own
     const float c = g.a.scale * 1.44269504088896f;
     const int mine = active ? (items + 1 - t) / 2 : 0;   // items of this stream
     float m = -INFINITY, l = 0.0f;
@@ -333,12 +393,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 32; ++x)
             if (key + q * 32 + x >= limit) s[q][x] = 0xFF800000u;   // -inf
       }
-      float top = -INFINITY;
+      float top[4];   // four chains, three operands an instruction
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q) {
+        top[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
 #pragma unroll
-        for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(s[q][x]));
-      const float now = fmaxf(m, top);
+        for (int x = 2; x < 32; x += 2)
+          top[q] = fmaxf(fmaxf(top[q], __uint_as_float(s[q][x])), __uint_as_float(s[q][x + 1]));
+      }
+      const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
       if (j == 0) {
         m = now;
       } else {
@@ -351,38 +414,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = grown ? ex2((m - now) * c) : 1.0f;
           const uint32_t ocol = tmem + lanes + 2 * kTile + t * D;
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            ptx::tmem_ld32(ocol + q * 32, o);
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            ptx::tmem_ld16(ocol + q * 16, o);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            ptx::tmem_st32(ocol + q * 32, o);
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            ptx::tmem_st16(ocol + q * 16, o);
           }
           ptx::tmem_wait_st();
           l *= f;
           if (grown) m = now;
         }
       }
-      const float base = m == -INFINITY ? 0.0f : m * c;
-      float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float a = ex2(fmaf(__uint_as_float(s[2 * q + x / 16][2 * (x % 16)]), c, -base));
-          const float b = ex2(fmaf(__uint_as_float(s[2 * q + x / 16][2 * (x % 16) + 1]), c, -base));
-          sum0 += a;
-          sum1 += b;
-          pk[x] = pack_bf16(a, b);
-        }
-        ptx::tmem_st32(scol + q * 32, pk);
-      }
-      l += sum0 + sum1;
-      // V rows behind the range may hold anything: cleared before the product reads them
+      // V rows behind the range may hold anything: cleared before this stream's product reads
+      // them (streams that share the tile both write the zeros)
       const int valid = w.k1 - key;
-      if (valid < kTile && (!w.shared || t == 0)) {
+      if (valid < kTile) {
         const int pos = pos_v(kt, T), st = pos % C::STAGES;
         ok = ptx::mbar_wait(ptx::smem_u32(&bars->full[st]), (pos / C::STAGES) & 1, abort, g.err);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -395,6 +443,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
+      const float base = m == -INFINITY ? 0.0f : m * c;
+      const uint64_t c2 = pair(c, c), nb2 = pair(-base, -base);
+      uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2, nb2);
+          const float a = ex2(low(z)), b = ex2(high(z));
+          sum[x % 4] = add2(sum[x % 4], pair(a, b));
+          pk[x] = pack_bf16(a, b);
+        }
+        ptx::tmem_st16(scol + q * 16, pk);
+        if (q == 1) {   // the product may start on the first half of the keys
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[t]));
+        }
+      }
+      sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+      l += low(sum[0]) + high(sum[0]);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
