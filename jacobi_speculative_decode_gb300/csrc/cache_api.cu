@@ -300,6 +300,7 @@ xp_status xp_verify_drafts(const xp_head* h, const void* target, int64_t stride_
   a.tickets = (unsigned*)(w + L.tickets);
   a.packed = (unsigned long long*)(w + L.packed);
   a.draw_ticket = (unsigned*)(w + L.draw_ticket);
+  a.next = (unsigned*)(w + L.next);
   a.part = (float*)(w + L.part);
   a.row = (float*)(w + L.row);
   return cuda_status(xp_launch_verify(h, a, stream));

@@ -267,8 +267,10 @@ size_t simt_smem(int rm, int nc, int D) {
 template <typename T, int RM, int NC>
 cudaError_t launch(const xp_attn_args& g, cudaStream_t s) {
   const size_t smem = simt_smem(RM, NC, g.dim);
-  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, RM, NC>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the widest head of this instantiation, so that one call covers them all
+  static unsigned long long allowed = 0;
+  const cudaError_t e = xp_allow_smem((const void*)attn_simt_kernel<T, RM, NC>,
+                                      simt_smem(RM, NC, NC * 64), &allowed);
   if (e != cudaSuccess) return e;
   const xp_attn_plan& p = g.plan;
   const dim3 grid(p.prefix_tiles * p.prefix_splits + g.a.N * p.tail_tiles * p.tail_splits,

@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 cudaError_t launch(const xp_cache* c, const xp_attn_args& g, unsigned grid, cudaStream_t s) {
   const size_t smem = Cfg<D>::SMEM + sizeof(Bars) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static unsigned long long allowed = 0;
+  const cudaError_t e = xp_allow_smem((const void*)attn_tc_kernel<D>, smem, &allowed);
   if (e != cudaSuccess) return e;
   const bool wide = ((uintptr_t)g.q | (uint64_t)g.a.q_stride_n * 2 | (uint64_t)g.a.q_stride_t * 2 |
                      (uint64_t)g.a.q_stride_h * 2) % 16 == 0;

@@ -3,9 +3,11 @@
 //                       and each slot's test u q(x) < p(x);
 //  verify_draw_kernel   the one token each block draws, at the slot where it ended.
 #include <float.h>
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sm100_ptx.cuh"
 #include "xp_device.cuh"
@@ -17,8 +19,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kLoads = 4;           // 16-byte loads a thread has in flight
-constexpr int kResident = 3;        // CTAs an SM: 48 KB of loads in flight
+constexpr int kLoads = 4;               // 16-byte vectors of a stage a thread reads
+constexpr int kStageBytes = kThreads * kLoads * 16;   // 16 KB
+constexpr int kStages = 4;              // 64 KB in flight a CTA
+constexpr int kResident = 2;            // CTAs an SM
 constexpr float kLog2e = 1.44269504088896f;
 
 // a logit as the softmax reads it: scaled, NaN as -inf, +inf as the largest finite value
@@ -29,6 +33,23 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// two fp32 operations an instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // Softmax statistics of part of a row: its maximum (a raw logit) and the sum of
@@ -67,21 +88,44 @@ __device__ __forceinline__ int drafts_of(const xp_verify_args& a, int n, bool te
   return d;
 }
 
-// 16 bytes of logits as floats
+// 16 bytes of logits
 template <typename T> struct Vec;
 template <> struct Vec<bf16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    const uint32_t w = i / 2 == 0 ? v.x : i / 2 == 1 ? v.y : i / 2 == 2 ? v.z : v.w;
+  static constexpr uint32_t kNone = 0xFF80FF80u;   // -inf, twice
+  static __device__ __forceinline__ float get(uint32_t w, int i) {
     return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+  static __device__ __forceinline__ float top(const uint4 (&x)[kLoads]) {   // NaN left out
+    __nv_bfloat162 m = __float2bfloat162_rn(-INFINITY);
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    }
+    return fmaxf(__low2float(m), __high2float(m));
   }
 };
 template <> struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  static constexpr uint32_t kNone = 0xFF800000u;
+  static __device__ __forceinline__ float get(uint32_t w, int) { return __uint_as_float(w); }
+  static __device__ __forceinline__ float top(const uint4 (&x)[kLoads]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(x[u].x), __uint_as_float(x[u].y)),
+                         fmaxf(__uint_as_float(x[u].z), __uint_as_float(x[u].w))));
+    return m;
   }
 };
+template <typename T>
+__device__ __forceinline__ float element(const uint4& x, int i) {
+  constexpr int P = Vec<T>::N / 4;   // logits a word
+  const uint32_t w = i / P == 0 ? x.x : i / P == 1 ? x.y : i / P == 2 ? x.z : x.w;
+  return Vec<T>::get(w, i % P);
+}
 
 // elements before the first 16-byte boundary of a row
 template <typename T>
@@ -89,255 +133,456 @@ __device__ __forceinline__ int head_of(const T* row, int V) {
   return min(V, (int)(((16 - ((uintptr_t)row & 15)) & 15) / sizeof(T)));
 }
 
-// Chunk c of a row (its 16-byte aligned vectors [c*chunk, (c+1)*chunk) elements behind the head;
-// the first chunk also takes the head, the last one what is left of the row), a thread's share:
-// statistics, and with TOP the lowest id of the maximum.
-template <typename T, bool TOP>
-__device__ __forceinline__ Stat thread_stat(const T* row, int V, int chunk, int c, bool last, float k,
-                                            int* top) {
-  constexpr int VN = Vec<T>::N;
-  const int head = head_of(row, V), vecs = (V - head) / VN;
-  const int v0 = c * (chunk / VN), v1 = last ? vecs : min(vecs, v0 + chunk / VN);
-  const uint4* at = (const uint4*)(row + head);
-  Stat st = {-INFINITY, 0.0f};
-  int id = 0x7FFFFFFF;
-  // at most one single element a thread: of the head, or behind the last vector
-  const int rest = V - head - vecs * VN;
-  int one = -1;
-  if (c == 0 && (int)threadIdx.x < head) one = threadIdx.x;
-  if (last && threadIdx.x >= 32 && (int)threadIdx.x < 32 + rest)
-    one = head + vecs * VN + threadIdx.x - 32;
-  if (one >= 0) {
-    st.m = read_logit(to_f(row[one]), 1.0f);
-    st.s = st.m > -INFINITY ? 1.0f : 0.0f;
-    id = one;
-  }
-  for (int i0 = v0 + (int)threadIdx.x; i0 < v1; i0 += kThreads * kLoads) {
-    uint4 x[kLoads];
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      if (i0 + u * kThreads < v1) x[u] = __ldcs(at + i0 + u * kThreads);
-    float m = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      if (i0 + u * kThreads < v1)
-#pragma unroll
-        for (int e = 0; e < VN; ++e) m = fmaxf(m, Vec<T>::get(x[u], e));
-    m = fminf(m, FLT_MAX);
-    if (TOP && m >= st.m) {
-#pragma unroll
-      for (int u = kLoads - 1; u >= 0; --u)
-        if (i0 + u * kThreads < v1)
-#pragma unroll
-          for (int e = VN - 1; e >= 0; --e) {
-            const int v = head + (i0 + u * kThreads) * VN + e;
-            // an equal maximum of a later vector does not count, one of the row's end does
-            if (read_logit(Vec<T>::get(x[u], e), 1.0f) == m && (m > st.m || v < id)) id = v;
-          }
-    }
-    const float now = fmaxf(st.m, m), base = base_of(now);
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      if (i0 + u * kThreads < v1)
-#pragma unroll
-        for (int e = 0; e < VN; e += 2) {
-          s0 += weight(Vec<T>::get(x[u], e), k, base);
-          s1 += weight(Vec<T>::get(x[u], e + 1), k, base);
-        }
-    st.s = st.s * weight(st.m, k, base) + s0 + s1;
-    st.m = now;
-  }
-  if (TOP) *top = id;
-  return st;
-}
-
-// the row's chunk over the CTA; warp 0's result counts
-template <typename T, bool TOP>
-__device__ Stat chunk_stat(const T* row, int V, int chunk, int c, bool last, float k, int* top,
-                           Stat* s_warp, int* s_top) {
-  Stat st = thread_stat<T, TOP>(row, V, chunk, c, last, k, top);
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  if (TOP) {
-    float m = st.m;
-    warp_argmax(m, *top);
-    if (lane == 0) s_top[w] = *top;
-  }
-  st = warp_join(st, k);
-  if (lane == 0) s_warp[w] = st;
-  __syncthreads();
-  if (w == 0) {
-    st = lane < kWarps ? s_warp[lane] : Stat{-INFINITY, 0.0f};
-    if (TOP) {
-      float m = st.m;
-      *top = lane < kWarps ? s_top[lane] : 0x7FFFFFFF;
-      warp_argmax(m, *top);
-    }
-    st = warp_join(st, k);
-  }
-  __syncthreads();
-  return st;
-}
-
-// Work items (slot, block, chunk), slots outermost, dealt out over a resident grid: the rows of
-// early slots are done first, and a row behind a slot that was rejected by then is skipped.
-// Nothing waits for that: a row read in vain changes no result.
+// One batch of a row, kLoads vectors a thread (those behind the row hold -inf), into running
+// statistics.  Returns the batch's maximum.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kResident) verify_stats_kernel(const xp_verify_args a, int chunk,
-                                                                int chunks) {
-  __shared__ Stat s_warp[kWarps];
-  __shared__ int s_top[kWarps];
-  __shared__ unsigned s_next;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t items = (int64_t)a.B * a.N * chunks;
-  int64_t it = blockIdx.x;
-  while (it < items) {
-    // a thread an item: the next one of this CTA's that is still wanted
-    if (threadIdx.x == 0) s_next = kThreads;
-    __syncthreads();
-    {
-      const int64_t mine = it + (int64_t)threadIdx.x * gridDim.x;
-      bool wanted = false;
-      if (mine < items) {
-        const int n = (int)(mine / chunks % a.N), b = (int)(mine / chunks / a.N);
-        // marks[n] = B - (first rejected slot known so far), 0 when none is
-        const int done = a.B - (int)__ldcg(&a.marks[n]);
-        wanted = b <= drafts_of(a, n, b == 0) && b <= done;
-      }
-      const unsigned any = __ballot_sync(0xFFFFFFFFu, wanted);
-      if (lane == 0 && any) atomicMin(&s_next, w * 32 + __ffs(any) - 1);
+__device__ __forceinline__ float batch_stat(const uint4 (&x)[kLoads], float k, Stat& st) {
+  constexpr int VN = Vec<T>::N;
+  const float m = fminf(Vec<T>::top(x), FLT_MAX), now = fmaxf(st.m, m), base = base_of(now);
+  // two logits an instruction: 2^(l k - base k)
+  uint64_t sum[2] = {0, 0};
+  const uint64_t k2 = pair(k, k), b2 = pair(-base * k, -base * k);
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+    for (int e = 0; e < VN; e += 2) {
+      const uint64_t z = fma2(pair(element<T>(x[u], e), element<T>(x[u], e + 1)), k2, b2);
+      sum[e / 2 % 2] = add2(sum[e / 2 % 2], pair(ex2(low(z)), ex2(high(z))));
     }
-    __syncthreads();
-    const unsigned skip = s_next;
-    it += (int64_t)skip * gridDim.x;
-    if (skip == kThreads) continue;
+  sum[0] = add2(sum[0], sum[1]);
+  float s = low(sum[0]) + high(sum[0]);
+  // NaN or +inf among them, or a base whose rounding would show: logit by logit
+  if (!(s <= (float)(kLoads * VN + 1)) || fabsf(base * k) > 16384.0f) {
+    s = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+#pragma unroll 1
+      for (int e = 0; e < VN; ++e) s += weight(element<T>(x[u], e), k, base);
+  }
+  st.s = st.s * weight(st.m, k, base) + s;
+  st.m = now;
+  return m;
+}
 
-    const int c = (int)(it % chunks);
-    const int n = (int)(it / chunks % a.N), b = (int)(it / chunks / a.N);
-    it += gridDim.x;
-    const int drafts = drafts_of(a, n, false);
-    const float heat = heat_of(a, n);
-    const float inv_t = heat > 0.0f ? 1.0f / heat : 1.0f, k = inv_t * kLog2e;
-    const bool last = c == chunks - 1, two = a.draft && heat > 0.0f && b < drafts;
-    const int64_t row = (int64_t)n * a.B + b;
-    const T* t_row = (const T*)a.target + n * a.sn + b * a.sb;
-    const float* d_row = two ? a.draft + ((int64_t)n * (a.B - 1) + b) * a.ld_draft : nullptr;
-    Stat d = {0.0f, 1.0f}, t;
-    int top = -1;
-    if (heat > 0.0f)
-      t = chunk_stat<T, false>(t_row, a.V, chunk, c, last, k, nullptr, s_warp, s_top);
-    else
-      t = chunk_stat<T, true>(t_row, a.V, chunk, c, last, k, &top, s_warp, s_top);
-    if (two) d = chunk_stat<float, false>(d_row, a.V, chunk, c, last, k, nullptr, s_warp, s_top);
-    if (w != 0) continue;
-    // the rest is warp 0's: the row's last chunk joins them all and tests the slot
-    float* out = a.part + (row * chunks + c) * 5;
-    unsigned ticket = 0;
-    if (lane == 0) {
-      __stcg(out, t.m);
-      __stcg(out + 1, t.s);
-      __stcg(out + 2, d.m);
-      __stcg(out + 3, d.s);
-      __stcg(out + 4, __int_as_float(top));
-      asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;"
-                   : "=r"(ticket)
-                   : "l"(&a.tickets[row])
-                   : "memory");
+// The maximum of a greedy row as it is met: its value, the first vector of the batch that held
+// it (-1: none), and a logit that no vector holds.  The id is looked up at the item's end, by
+// the few lanes that hold the item's maximum.
+struct Top {
+  float m;
+  int batch;
+  float single;
+  int single_id;
+};
+template <typename T>
+__device__ __forceinline__ int id_of(const T* row, int V, int v1, const Top& t, float m) {
+  constexpr int VN = Vec<T>::N;
+  const int head = head_of(row, V);
+  int id = t.single == m ? t.single_id : 0x7FFFFFFF;
+  if (t.m == m && t.batch >= 0)
+    for (int u = kLoads - 1; u >= 0; --u) {
+      const int at = t.batch + (int)threadIdx.x + u * kThreads;
+      if (at < v1)
+        for (int e = VN - 1; e >= 0; --e) {
+          const int v = head + at * VN + e;
+          if (read_logit(to_f(row[v]), 1.0f) == m) id = min(id, v);
+        }
     }
-    ticket = __shfl_sync(0xFFFFFFFFu, ticket, 0);
-    if (ticket != (unsigned)chunks - 1) continue;
-    __threadfence();
-    t = d = {-INFINITY, 0.0f};
-    float m = -INFINITY;
-    top = 0x7FFFFFFF;
-    for (int i = lane; i < chunks; i += 32) {
-      const float* in = a.part + (row * chunks + i) * 5;
-      const Stat x = {__ldcg(in), __ldcg(in + 1)};
-      const int id = __float_as_int(__ldcg(in + 4));
-      if (better(x.m, id, m, top)) { m = x.m; top = id; }
-      t = join(t, x, k);
-      if (two) d = join(d, {__ldcg(in + 2), __ldcg(in + 3)}, k);
+  return id;
+}
+// vectors [*v0, *v1) of chunk c of a row
+template <typename T>
+__device__ __forceinline__ void vectors_of(const T* row, int V, int chunk, int chunks, int c, int* v0,
+                                           int* v1) {
+  constexpr int VN = Vec<T>::N;
+  const int vecs = (V - head_of(row, V)) / VN;
+  *v0 = min(vecs, c * (chunk / VN));
+  *v1 = c == chunks - 1 ? vecs : min(vecs, *v0 + chunk / VN);
+}
+
+// What a stage of the ring holds: `bytes` of the item's target or draft row, behind `first` vectors
+struct Stage {
+  int item, kind;     // kind: bit 0 draft, bit 1 first of its row's chunk, bit 2 last of the item
+  int first, bytes;   // first vector of the stage in the row
+};
+constexpr int kDraft = 1, kOpens = 2, kEnds = 4, kStop = 8;
+
+constexpr int kItems = 4;
+struct Ring {
+  uint64_t full[kStages], empty[kStages];
+  Stage stage[kStages];
+  // finished items on their way to the joining warp: statistics (target, draft) of every warp
+  uint64_t written[kItems], read[kItems];
+  Stat stat[kItems][kWarps][2];
+  int top[kItems][kWarps];
+  int item[kItems];          // -1: there are no more
+  int abort;
+};
+
+// The statistics of every wanted row, in items (slot, block, chunk) with the slots outermost: the
+// rows of early slots are done first, and a row behind a slot that was rejected by then is
+// skipped.  Nothing waits for that: a row read in vain changes no result.
+// Warp 8 claims the items from a counter and streams the rows into a ring by bulk copies, ahead
+// over the items' ends; warps 0-7 sum what it holds; warp 9 writes the items' results, and
+// where an item is its row's last joins them and tests the slot (its round trips to memory
+// hold nobody up).
+template <typename T>
+__global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
+    const xp_verify_args a, int chunk, int chunks) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ Ring sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per_slot = a.N * chunks;
+  volatile int* abort = &sh.abort;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&sh.full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&sh.empty[s]), kWarps);
     }
-    warp_argmax(m, top);
-    t = warp_join(t, k);
-    if (two) d = warp_join(d, k);
-    if (lane != 0) continue;
-    float* out_row = a.row + row * 5;
-    out_row[0] = t.m;
-    out_row[1] = t.s;
-    out_row[2] = d.m;
-    out_row[3] = d.s;
-    out_row[4] = __int_as_float(t.m > -INFINITY ? top : -1);
-    if (b >= drafts) continue;
-    const int64_t x = a.blk[(int64_t)n * a.B + 1 + b];
-    float px = 0.0f, qx = 1.0f;
-    if (x < 0 || x >= a.V) {
-      atomicOr(a.err, XP_ERR_BADTOKEN);
-    } else if (t.m > -INFINITY) {
-      if (heat == 0.0f) {
-        px = x == top ? 1.0f : 0.0f;
+    for (int h = 0; h < kItems; ++h) {
+      ptx::mbar_init(ptx::smem_u32(&sh.written[h]), kWarps);
+      ptx::mbar_init(ptx::smem_u32(&sh.read[h]), 1);
+    }
+    sh.abort = 0;
+    ptx::fence_barrier_init();
+  }
+  __syncthreads();
+
+  if (warp == kWarps) {
+    const int items = a.B * per_slot;
+    int issued = 0;
+    bool ok = true;
+    // room for the next stage
+    auto room = [&]() {
+      const int s = issued % kStages;
+      ok = ptx::mbar_wait(ptx::smem_u32(&sh.empty[s]), ((issued / kStages) & 1) ^ 1, abort, a.err);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      return s;
+    };
+    auto post = [&](int s, const Stage& st, const void* from) {
+      if (lane == 0) {
+        sh.stage[s] = st;
+        const uint32_t full = ptx::smem_u32(&sh.full[s]);
+        if (st.bytes > 0) {
+          ptx::mbar_arrive_expect_tx(full, st.bytes);
+          ptx::bulk_load(ptx::smem_u32(ring + s * kStageBytes), from, st.bytes, full);
+        } else {
+          ptx::mbar_arrive(full);
+        }
+      }
+      __syncwarp();
+      ++issued;
+    };
+    // the stages of one row's chunk
+    auto stream = [&](auto* row, int item, int c, int kind, int ends) {
+      using E = typename std::remove_const<typename std::remove_pointer<decltype(row)>::type>::type;
+      constexpr int VN = Vec<E>::N, kPer = kStageBytes / 16;
+      const int head = head_of(row, a.V);
+      int v, v1, opens = kOpens;
+      vectors_of(row, a.V, chunk, chunks, c, &v, &v1);
+      do {
+        const int n = min(kPer, v1 - v), s = room();
+        if (!ok) return;
+        post(s, {item, kind | opens | (v + n == v1 ? ends : 0), v, n * 16}, row + head + (int64_t)v * VN);
+        v += n;
+        opens = 0;
+      } while (v < v1);
+    };
+    // A CTA's first item is its own number, the others come from the counter.  The counter and
+    // the next item's mark are read while this one streams.
+    // marks[n] = B - (first rejected slot known so far), 0 when none is
+    auto mark_of = [&](int i) { return i < items ? (int)__ldcg(&a.marks[i / chunks % a.N]) : a.B; };
+    auto claim = [&]() {
+      unsigned i = 0;
+      if (lane == 0) i = min(gridDim.x + atomicAdd(a.next, 1u), (unsigned)items);
+      return (int)i;
+    };
+    int next = blockIdx.x, mark = mark_of(next), claimed = claim();
+    while (ok && next < items) {
+      const int i = next, c = i % chunks, n = i / chunks % a.N, b = i / per_slot;
+      const int drafts = drafts_of(a, n, c == 0 && b == 0 && lane == 0);
+      const bool wanted = b <= a.B - mark && b <= drafts;
+      next = __shfl_sync(0xFFFFFFFFu, claimed, 0);
+      mark = mark_of(next);
+      claimed = claim();
+      if (!wanted) continue;
+      const bool two = a.draft && heat_of(a, n) > 0.0f && b < drafts;
+      stream((const T*)a.target + n * a.sn + b * a.sb, i, c, 0, two ? 0 : kEnds);
+      if (two && ok)
+        stream(a.draft + ((int64_t)n * (a.B - 1) + b) * a.ld_draft, i, c, kDraft, kEnds);
+    }
+    if (ok) {
+      const int s = room();
+      if (ok) post(s, {0, kStop, 0, 0}, nullptr);
+    }
+    // nothing may land in shared memory after the CTA is gone
+    volatile int no_abort = 0;
+    for (int s = 0; s < kStages; ++s) {
+      const int n = (issued + kStages - 1 - s) / kStages;
+      if (n > 0) ptx::mbar_wait(ptx::smem_u32(&sh.full[s]), (n - 1) & 1, &no_abort, a.err);
+    }
+    return;
+  }
+
+  if (warp == kWarps + 1) {
+    for (int done = 0;; ++done) {
+      const int h = done % kItems;
+      const bool ok = ptx::mbar_wait(ptx::smem_u32(&sh.written[h]), (done / kItems) & 1, abort, a.err);
+      if (!__all_sync(0xFFFFFFFFu, ok)) return;
+      const int item = sh.item[h];
+      if (item < 0) return;
+      const int c = item % chunks, n = item / chunks % a.N, b = item / per_slot, row = n * a.B + b;
+      const int drafts = drafts_of(a, n, false);
+      const float heat = heat_of(a, n);
+      const float inv_t = heat > 0.0f ? 1.0f / heat : 1.0f, k = inv_t * kLog2e;
+      const bool draft = a.draft && heat > 0.0f && b < drafts;
+      Stat t = {-INFINITY, 0.0f}, d = t;
+      int top = 0x7FFFFFFF;
+      if (lane < kWarps) {
+        t = sh.stat[h][lane][0];
+        d = sh.stat[h][lane][1];
+        top = sh.top[h][lane];
+      }
+      float m = t.m;
+      warp_argmax(m, top);
+      t = warp_join(t, k);
+      d = draft ? warp_join(d, k) : Stat{0.0f, 1.0f};
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.read[h]));
+      float* out = a.part + ((int64_t)row * chunks + c) * 5;
+      unsigned ticket = 0;
+      if (lane == 0) {
+        __stcg(out, t.m);
+        __stcg(out + 1, t.s);
+        __stcg(out + 2, d.m);
+        __stcg(out + 3, d.s);
+        __stcg(out + 4, __int_as_float(top));
+        asm volatile("atom.add.acq_rel.gpu.u32 %0, [%1], 1;"
+                     : "=r"(ticket)
+                     : "l"(&a.tickets[row])
+                     : "memory");
+      }
+      ticket = __shfl_sync(0xFFFFFFFFu, ticket, 0);
+      if (ticket != (unsigned)chunks - 1) continue;
+      // the row's last item
+      __threadfence();
+      t = d = {-INFINITY, 0.0f};
+      m = -INFINITY;
+      top = 0x7FFFFFFF;
+      for (int i = lane; i < chunks; i += 32) {
+        const float* in = a.part + ((int64_t)row * chunks + i) * 5;
+        const Stat x = {__ldcg(in), __ldcg(in + 1)};
+        const int id = __float_as_int(__ldcg(in + 4));
+        if (better(x.m, id, m, top)) { m = x.m; top = id; }
+        t = join(t, x, k);
+        if (draft) d = join(d, {__ldcg(in + 2), __ldcg(in + 3)}, k);
+      }
+      warp_argmax(m, top);
+      t = warp_join(t, k);
+      if (draft) d = warp_join(d, k);
+      if (lane != 0) continue;
+      float* out_row = a.row + (int64_t)row * 5;
+      out_row[0] = t.m;
+      out_row[1] = t.s;
+      out_row[2] = d.m;
+      out_row[3] = d.s;
+      out_row[4] = __int_as_float(t.m > -INFINITY ? top : -1);
+      if (b >= drafts) continue;
+      const int64_t x = a.blk[(int64_t)n * a.B + 1 + b];
+      float px = 0.0f, qx = 1.0f;
+      if (x < 0 || x >= a.V) {
+        atomicOr(a.err, XP_ERR_BADTOKEN);
+      } else if (t.m > -INFINITY) {
+        if (heat == 0.0f) {
+          px = x == top ? 1.0f : 0.0f;
+        } else {
+          const T* t_row = (const T*)a.target + n * a.sn + b * a.sb;
+          px = expf(read_logit(to_f(t_row[x]), inv_t) - read_logit(t.m, inv_t)) / t.s;
+          if (draft) {
+            const float* d_row = a.draft + ((int64_t)n * (a.B - 1) + b) * a.ld_draft;
+            qx = d.m > -INFINITY
+                     ? expf(read_logit(d_row[x], inv_t) - read_logit(d.m, inv_t)) / d.s
+                     : 0.0f;
+          }
+        }
+      }
+      const float u = a.u[(int64_t)n * (a.B - 1) + b];
+      if (a.prob) a.prob[(int64_t)n * (a.B - 1) + b] = px > 0.0f ? fminf(px / qx, 1.0f) : 0.0f;
+      if (!(u * qx < px)) atomicMax(&a.marks[n], (unsigned)(a.B - b));
+    }
+  }
+
+  Stat st = {-INFINITY, 0.0f}, kept = {-INFINITY, 0.0f};   // of the row in progress; of the target
+  Top tp = {-INFINITY, -1, -INFINITY, 0x7FFFFFFF};
+  int n = 0, b = 0, c = 0, done = 0;   // done: items finished
+  float heat = 1.0f, k = kLog2e;
+  for (int pos = 0;; ++pos) {
+    const int s = pos % kStages;
+    bool ok = ptx::mbar_wait(ptx::smem_u32(&sh.full[s]), (pos / kStages) & 1, abort, a.err);
+    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+    const Stage sg = sh.stage[s];
+    if (sg.kind & kStop) {
+      const int h = done % kItems;
+      ok = ptx::mbar_wait(ptx::smem_u32(&sh.read[h]), ((done / kItems) & 1) ^ 1, abort, a.err);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (lane == 0) {
+        if (warp == 0) sh.item[h] = -1;
+        ptx::mbar_arrive(ptx::smem_u32(&sh.written[h]));
+      }
+      break;
+    }
+    const bool draft = sg.kind & kDraft;
+    if (sg.kind & kOpens) {
+      if (!draft) {
+        c = sg.item % chunks;
+        n = sg.item / chunks % a.N;
+        b = sg.item / per_slot;
+        heat = heat_of(a, n);
+        k = (heat > 0.0f ? 1.0f / heat : 1.0f) * kLog2e;
+        tp = {-INFINITY, -1, -INFINITY, 0x7FFFFFFF};
       } else {
-        px = expf(read_logit(to_f(t_row[x]), inv_t) - read_logit(t.m, inv_t)) / t.s;
-        if (two)
-          qx = d.m > -INFINITY
-                   ? expf(read_logit(d_row[x], inv_t) - read_logit(d.m, inv_t)) / d.s
-                   : 0.0f;
+        kept = st;
+      }
+      st = {-INFINITY, 0.0f};
+    }
+    uint4 x[kLoads];
+    const uint32_t none = draft ? Vec<float>::kNone : Vec<T>::kNone;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int at = (threadIdx.x + u * kThreads) * 16;
+      x[u] = at < sg.bytes ? *(const uint4*)(ring + s * kStageBytes + at)
+                           : make_uint4(none, none, none, none);
+    }
+    float m;
+    if (draft) {
+      m = batch_stat<float>(x, k, st);
+    } else if (heat > 0.0f) {
+      m = batch_stat<T>(x, k, st);
+    } else {
+      m = fminf(Vec<T>::top(x), FLT_MAX);
+      if (m > tp.m) {
+        tp.m = m;
+        tp.batch = sg.first;
       }
     }
-    const float u = a.u[(int64_t)n * (a.B - 1) + b];
-    if (a.prob) a.prob[(int64_t)n * (a.B - 1) + b] = px > 0.0f ? fminf(px / qx, 1.0f) : 0.0f;
-    if (!(u * qx < px)) atomicMax(&a.marks[n], (unsigned)(a.B - b));
+    // given back only when every lane's loads have returned: the arrival hangs on a value (always
+    // true) that is made from all of them
+    if (__any_sync(0xFFFFFFFFu, m >= -INFINITY) && lane == 0)
+      ptx::mbar_arrive(ptx::smem_u32(&sh.empty[s]));
+    if (sg.kind & kOpens) {   // what no 16-byte vector holds: the row's head and end
+      auto single = [&](auto* row) {
+        using E = typename std::remove_const<typename std::remove_pointer<decltype(row)>::type>::type;
+        const int head = head_of(row, a.V), rest = (a.V - head) % Vec<E>::N, i = threadIdx.x;
+        const int v = c == 0 && i < head                                      ? i
+                      : c == chunks - 1 && i >= 32 && i < 32 + rest ? a.V - rest + i - 32
+                                                                    : -1;
+        if (v < 0) return;
+        const float l = read_logit(to_f(row[v]), 1.0f);
+        if (heat == 0.0f) {
+          tp.single = l;
+          tp.single_id = v;
+        } else {
+          st = join(st, {l, l > -INFINITY ? 1.0f : 0.0f}, k);
+        }
+      };
+      if (draft) single(a.draft + ((int64_t)n * (a.B - 1) + b) * a.ld_draft);
+      else single((const T*)a.target + n * a.sn + b * a.sb);
+    }
+    if (!(sg.kind & kEnds)) continue;
+
+    // the item's end: this warp's results go to the joining warp
+    Stat t = draft ? kept : st, d = {0.0f, 1.0f};
+    int top = 0x7FFFFFFF;
+    if (heat > 0.0f) {
+      t = warp_join(t, k);
+      if (draft) d = warp_join(st, k);
+    } else {
+      m = fmaxf(tp.m, tp.single);
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const T* row = (const T*)a.target + n * a.sn + b * a.sb;
+      int v0, v1;
+      vectors_of(row, a.V, chunk, chunks, c, &v0, &v1);
+      if (tp.m == m || tp.single == m) top = id_of(row, a.V, v1, tp, m);
+      for (int o = 16; o > 0; o >>= 1) top = min(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      t = {m, m > -INFINITY ? 1.0f : 0.0f};
+    }
+    const int h = done % kItems;
+    ok = ptx::mbar_wait(ptx::smem_u32(&sh.read[h]), ((done / kItems) & 1) ^ 1, abort, a.err);
+    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+    ++done;
+    if (lane == 0) {
+      sh.stat[h][warp][0] = t;
+      sh.stat[h][warp][1] = d;
+      sh.top[h][warp] = top;
+      if (warp == 0) sh.item[h] = sg.item;
+      ptx::mbar_arrive(ptx::smem_u32(&sh.written[h]));
+    }
+    __syncwarp();
   }
 }
 
-// The race of one id: w / e with w = max(p - q, 0).  Most ids are far behind the best, so a
-// quick form (approximate exponential and reciprocal: relative error below 2^-15 of p and q,
-// the exponent's rounding at most 150 * 2^-23) decides first whether the exact one, which
-// alone counts, is worth computing.
+// The race of one id is w / e with w = max(p - q, 0).  One pass takes an upper bound of it
+// from quick exponentials and logarithms, and keeps each thread's highest bound and the one
+// after it; the exact form, which alone counts, is computed for the highest, and for the
+// others only where their bound reaches the best exact value of the CTA.
+//  one row (TWO false): log2(p / e) = l k - shift - log2 e, as l k - log2 e
+//  two rows: (p (1 + d) - q (1 - d)) / e
+// `slack` and d = 2^-14 cover the rounding of l k at most 200 below the maximum, of ex2, lg2
+// and of the exact form's own exponent.
 struct Race {
   float inv_t, inv_s, tz, inv_d, dz;   // dz, inv_d: the draft's, where it has a row
+  float k, slack, shift;
   int64_t x;                           // a one-hot draft's id, -1
-  unsigned long long best;
-  float best_f;
 
-  __device__ __forceinline__ float exact(float l, bool two, float d, float e, int v) const {
-    const float p = expf(read_logit(l, inv_t) - tz) * inv_s;
-    const float q = two ? expf(read_logit(d, inv_t) - dz) * inv_d : v == x ? 1.0f : 0.0f;
-    return p > q ? (p - q) / e : 0.0f;
+  __device__ __forceinline__ void start(float heat, float tm, float ts) {
+    inv_t = 1.0f / heat;
+    inv_s = 1.0f / ts;
+    tz = read_logit(tm, inv_t);
+    k = inv_t * kLog2e;
+    shift = tz * kLog2e + log2f(ts);
+    slack = 1e-4f + fabsf(tz) * 1e-6f;
   }
   template <bool TWO>
-  __device__ __forceinline__ void take(float l, float d, float e, int v) {
-    constexpr float kMore = 1.0f + 1.0f / 16384, kLess = 1.0f - 1.0f / 16384;
-    float w = __saturatef(ex2((l * inv_t - tz) * kLog2e)) * inv_s * kMore;
-    if (TWO) w -= __saturatef(ex2((d * inv_t - dz) * kLog2e)) * inv_d * kLess;
-    if (w > 0.0f && __fdividef(w, e) * kMore >= best_f) {
-      const float r = exact(l, TWO, d, e, v);
-      if (r > 0.0f) {
-        best = max(best, pack_best(r, (uint32_t)v));
-        best_f = packed_val(best);
-      }
+  __device__ __forceinline__ float bound(float l, float d, float e) const {
+    if (TWO) {
+      constexpr float kMore = 1.0f + 1.0f / 16384, kLess = 1.0f - 1.0f / 16384;
+      const float p = __saturatef(ex2((l * inv_t - tz) * kLog2e)) * inv_s;
+      const float q = __saturatef(ex2((d * inv_t - dz) * kLog2e)) * inv_d;
+      return __fdividef(p * kMore - q * kLess, e) * kMore;
     }
+    float lg;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(e));
+    return fmaf(l, k, -lg);
+  }
+  // the bound that an exact value of `best` asks for
+  template <bool TWO>
+  __device__ __forceinline__ float asks(unsigned long long best) const {
+    if (!best) return TWO ? 0.0f : -FLT_MAX;
+    const float r = packed_val(best);
+    return TWO ? r : log2f(r) + shift - slack;
+  }
+  template <bool TWO>
+  __device__ __forceinline__ unsigned long long exact(float l, float d, float e, int v) const {
+    const float p = expf(read_logit(l, inv_t) - tz) * inv_s;
+    const float q = TWO ? expf(read_logit(d, inv_t) - dz) * inv_d : v == x ? 1.0f : 0.0f;
+    return p > q && (p - q) / e > 0.0f ? pack_best((p - q) / e, (uint32_t)v) : 0ull;
   }
 };
 
-// Chunk c of a block's race: rows of target, draft and noise need not share an alignment, so
-// ids are taken in vectors of the noise row (fp32); the others come with plain loads where
-// theirs differs.
-template <typename T, bool TWO>
-__device__ void race_chunk(Race& r, const T* t_row, const float* d_row, const float* e_row, int V,
-                           int lo, int hi) {
-  // common case: all three rows on 16-byte boundaries from the same id on
+// f(l, d, e, v) for this thread's ids of [lo, hi)
+template <typename T, bool TWO, typename F>
+__device__ __forceinline__ void each_id(const T* t_row, const float* d_row, const float* e_row, int lo,
+                                        int hi, F&& f) {
+  // vectors where all rows are on 16-byte boundaries from the same id on
   const bool wide = (((uintptr_t)(t_row + lo) | (uintptr_t)(e_row + lo) |
                       (TWO ? (uintptr_t)(d_row + lo) : 0)) & 15) == 0;
   int v = lo;
   if (wide) {
-    constexpr int W = 8;
+    constexpr int W = 8, TV = (int)sizeof(T) / 2;
     const int vecs = (hi - lo) / W;
+#pragma unroll 2
     for (int i = threadIdx.x; i < vecs; i += kThreads) {
       const int at = lo + i * W;
-      uint4 tx[sizeof(T) / 2], ex[2], dx[2];
+      uint4 tx[TV], ex[2], dx[2];
 #pragma unroll
-      for (int u = 0; u < (int)sizeof(T) / 2; ++u) tx[u] = __ldcs((const uint4*)(t_row + at) + u);
+      for (int u = 0; u < TV; ++u) tx[u] = __ldcs((const uint4*)(t_row + at) + u);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         ex[u] = __ldcs((const uint4*)(e_row + at) + u);
@@ -345,24 +590,60 @@ __device__ void race_chunk(Race& r, const T* t_row, const float* d_row, const fl
       }
 #pragma unroll
       for (int e = 0; e < W; ++e)
-        r.take<TWO>(Vec<T>::get(tx[e / Vec<T>::N], e % Vec<T>::N),
-                    TWO ? Vec<float>::get(dx[e / 4], e % 4) : 0.0f, Vec<float>::get(ex[e / 4], e % 4),
-                    at + e);
+        f(element<T>(tx[e / Vec<T>::N], e % Vec<T>::N), TWO ? element<float>(dx[e / 4], e % 4) : 0.0f,
+          element<float>(ex[e / 4], e % 4), at + e);
     }
     v = lo + vecs * W;
   }
   for (v += (int)threadIdx.x; v < hi; v += kThreads)
-    r.take<TWO>(to_f(t_row[v]), TWO ? d_row[v] : 0.0f, e_row[v], v);
+    f(to_f(t_row[v]), TWO ? d_row[v] : 0.0f, e_row[v], v);
+}
+
+// the race of ids [lo, hi) over the CTA: every thread gets the best, 0 when no weight is positive
+template <typename T, bool TWO>
+__device__ unsigned long long race(const Race& r, const T* t_row, const float* d_row,
+                                   const float* e_row, int lo, int hi, unsigned long long* s_best) {
+  float top = -INFINITY, second = -INFINITY;
+  int at = -1;
+  each_id<T, TWO>(t_row, d_row, e_row, lo, hi, [&](float l, float d, float e, int v) {
+    const float u = r.bound<TWO>(l, d, e);   // NaN: no
+    const bool more = u > top;
+    second = fmaxf(second, more ? top : u);
+    top = more ? u : top;
+    at = more ? v : at;
+  });
+  if (threadIdx.x == 0) *s_best = 0;
+  __syncthreads();
+  unsigned long long best = 0;
+  if (at >= 0) best = r.exact<TWO>(to_f(t_row[at]), TWO ? d_row[at] : 0.0f, e_row[at], at);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+  if ((threadIdx.x & 31) == 0 && best) atomicMax(s_best, best);
+  __syncthreads();
+  best = *s_best;
+  const float asked = r.asks<TWO>(best);
+  __syncthreads();
+  if (second >= asked) {   // rare: another of this thread's ids may be the one
+    each_id<T, TWO>(t_row, d_row, e_row, lo, hi, [&](float l, float d, float e, int v) {
+      if (r.bound<TWO>(l, d, e) >= asked) best = max(best, r.exact<TWO>(l, d, e, v));
+    });
+    if (best) atomicMax(s_best, best);
+  }
+  __syncthreads();
+  best = *s_best;
+  __syncthreads();
+  return best;
 }
 
 // Work items (block, chunk): the race of every id of the chunk, merged into the block's best;
 // the block's last chunk writes its tokens and clears its counters for the next call.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const xp_verify_args a, int chunk) {
-  __shared__ unsigned long long s_best[kWarps];
+  __shared__ unsigned long long s_best;
   __shared__ int s_last;
   ptx::pdl_wait();
-  const int n = blockIdx.y, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int n = blockIdx.y;
+  if (blockIdx.x == 0 && n == 0 && threadIdx.x == 0) *a.next = 0;
   const int drafts = drafts_of(a, n, false);
   const unsigned mark = a.marks[n];
   const bool rejected = mark != 0;
@@ -375,30 +656,21 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const xp_verify_a
   const float* e_row = a.noise + n * a.ld_noise;
   Race r = {};
   if (heat > 0.0f && !empty) {
-    r.inv_t = 1.0f / heat;
-    r.inv_s = 1.0f / a.row[row * 5 + 1];
-    r.tz = read_logit(tm, r.inv_t);
+    r.start(heat, tm, a.row[row * 5 + 1]);
     r.x = rejected && !a.draft ? a.blk[(int64_t)n * a.B + 1 + end] : -1;
     const float dm = a.row[row * 5 + 2];
     const bool two = a.draft && rejected && dm > -INFINITY;
     const float* d_row = two ? a.draft + ((int64_t)n * (a.B - 1) + end) * a.ld_draft : nullptr;
     const int lo = blockIdx.x * chunk, hi = min(a.V, lo + chunk);
+    unsigned long long best;
     if (two) {
       r.inv_d = 1.0f / a.row[row * 5 + 3];
       r.dz = read_logit(dm, r.inv_t);
-      race_chunk<T, true>(r, t_row, d_row, e_row, a.V, lo, hi);
+      best = race<T, true>(r, t_row, d_row, e_row, lo, hi, &s_best);
     } else {
-      race_chunk<T, false>(r, t_row, nullptr, e_row, a.V, lo, hi);
+      best = race<T, false>(r, t_row, nullptr, e_row, lo, hi, &s_best);
     }
-    unsigned long long best = r.best;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-    if (lane == 0) s_best[w] = best;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int i = 1; i < kWarps; ++i) best = max(best, s_best[i]);
-      if (best) atomicMax(&a.packed[n], best);
-    }
+    if (threadIdx.x == 0 && best) atomicMax(&a.packed[n], best);
   }
   if (!arrive_last(&a.draw_ticket[n], gridDim.x, &s_last)) return;
   int64_t last = -1;
@@ -410,15 +682,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const xp_verify_a
     unsigned long long best = __ldcg(&a.packed[n]);
     if (!best) {   // rounding left no positive residual: p itself is raced, by this CTA alone
       r.x = -1;
-      r.best = 0;
-      r.best_f = 0.0f;
-      race_chunk<T, false>(r, t_row, nullptr, e_row, a.V, 0, a.V);
-      best = r.best;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-      if (lane == 0) s_best[w] = best;
-      __syncthreads();
-      for (int i = 0; i < kWarps; ++i) best = max(best, s_best[i]);
+      best = race<T, false>(r, t_row, nullptr, e_row, 0, a.V, &s_best);
     }
     last = packed_idx(best);
   }
@@ -438,13 +702,15 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const xp_verify_a
   }
 }
 
-// Vocabulary ids of one work item: 16384 where that leaves every SM several items, less
-// (down to 2048) for few rows, whose latency counts.
-int chunk_of(int64_t rows, int V, int sms) {
-  int chunk = 16384;
-  while (chunk > 2048 && rows * ((V + chunk - 1) / chunk) < (int64_t)sms * 4) chunk /= 2;
+// Vocabulary ids of one work item of `workers` that share `rows` rows: from `most` down to
+// `least` where few rows would leave workers idle.
+int chunk_of(int64_t rows, int V, int64_t workers, int most, int least) {
+  int chunk = most;
+  while (chunk > least && rows * ((V + chunk - 1) / chunk) < workers) chunk /= 2;
   return chunk;
 }
+constexpr int kMostIds = 65536, kLeastIds = 8192;
+constexpr int kMostRace = 16384, kLeastRace = 2048;
 
 }  // namespace
 
@@ -458,7 +724,8 @@ xp_verify_ws xp_verify_layout(const xp_head* h, int N) {
   L.tickets = take(rows * 4);
   L.packed = take(n * 8);
   L.draw_ticket = take(n * 4);
-  L.part = take(rows * (((size_t)h->V + 2047) / 2048) * 20);
+  L.next = take(4);
+  L.part = take(rows * (((size_t)h->V + kLeastIds - 1) / kLeastIds) * 20);
   L.row = take(rows * 20);
   L.total = o;
   return L;
@@ -466,15 +733,23 @@ xp_verify_ws xp_verify_layout(const xp_head* h, int N) {
 
 template <typename T>
 static cudaError_t launch_verify(const xp_head* h, const xp_verify_args& a, cudaStream_t s) {
-  const int64_t rows = (int64_t)a.N * a.B;
-  const int chunk = chunk_of(rows, a.V, h->num_sms), chunks = (a.V + chunk - 1) / chunk;
-  const unsigned grid = (unsigned)std::min<int64_t>(rows * chunks, (int64_t)h->num_sms * kResident);
-  verify_stats_kernel<T><<<grid, kThreads, 0, s>>>(a, chunk, chunks);
+  const int64_t rows = (int64_t)a.N * a.B, ctas = (int64_t)h->num_sms * kResident;
+  // a batch of requests rarely needs the rows of more than a few slots
+  const int chunk =
+      chunk_of(std::min<int64_t>(rows, (int64_t)a.N * 4), a.V, ctas * 3 / 2, kMostIds, kLeastIds);
+  const int chunks = (a.V + chunk - 1) / chunk;
+  if (rows * chunks > INT_MAX / 2) return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)std::min(rows * chunks, ctas);
+  const int smem = kStages * kStageBytes;
+  static unsigned long long allowed = 0;
+  const cudaError_t f = xp_allow_smem((const void*)verify_stats_kernel<T>, smem, &allowed);
+  if (f != cudaSuccess) return f;
+  verify_stats_kernel<T><<<grid, kThreads + 64, smem, s>>>(a, chunk, chunks);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int draw = chunk_of(a.N, a.V, h->num_sms);
-  return xp_launch_pdl(verify_draw_kernel<T>, dim3((a.V + draw - 1) / draw, a.N), dim3(kThreads), 0, s,
-                       a, draw);
+  const int race = chunk_of(a.N, a.V, (int64_t)h->num_sms * 4, kMostRace, kLeastRace);
+  return xp_launch_pdl(verify_draw_kernel<T>, dim3((a.V + race - 1) / race, a.N), dim3(kThreads), 0, s,
+                       a, race);
 }
 
 cudaError_t xp_launch_verify(const xp_head* h, const xp_verify_args& a, cudaStream_t s) {

@@ -150,7 +150,7 @@ cudaError_t xp_launch_topc_readout(const xp_head* h, const void* lat, const void
 
 // Verification of drafted blocks.  packed, marks and tickets must be zero between calls.
 struct xp_verify_ws {
-  size_t marks, tickets, packed, draw_ticket;   // zero between calls
+  size_t marks, tickets, packed, draw_ticket, next;   // zero between calls
   size_t part, row;                             // softmax statistics: per chunk, per row
   size_t total;
 };
@@ -176,6 +176,7 @@ struct xp_verify_args {
   unsigned* tickets;
   unsigned long long* packed;
   unsigned* draw_ticket;
+  unsigned* next;
   float* part;
   float* row;
 };
@@ -246,6 +247,18 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a);
 cudaError_t xp_launch_attn_tc(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 cudaError_t xp_launch_attn_combine(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
+
+// Let a kernel use `bytes` of dynamic shared memory: asked of the runtime once a device.
+inline cudaError_t xp_allow_smem(const void* kernel, size_t bytes, unsigned long long* devices) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (__atomic_load_n(devices, __ATOMIC_RELAXED) >> dev & 1)) return cudaSuccess;
+  const cudaError_t f =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (f == cudaSuccess && dev < 64) __atomic_fetch_or(devices, 1ull << dev, __ATOMIC_RELAXED);
+  return f;
+}
 
 // Launch with a programmatic dependency on the previous kernel in the stream:
 // the kernel's prologue may overlap that kernel's tail; the kernel itself must

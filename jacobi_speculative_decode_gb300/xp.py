@@ -142,9 +142,10 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
-        if not torch.cuda.is_available():
+        if not torch.cuda.is_initialized() and not torch.cuda.is_available():
             raise RuntimeError("no CUDA device: libxp has no CPU path")
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
