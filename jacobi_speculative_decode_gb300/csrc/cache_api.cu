@@ -75,7 +75,8 @@ bool valid_attn(const xp_cache* c, const xp_attn* a) {
 }
 
 xp_attn_plan attn_plan(const xp_cache* c, const xp_attn* a) {
-  xp_attn_plan p = c->attn_tc ? xp_attn_tc_plan(c, a) : xp_attn_simt_plan(c, a);
+  if (c->attn_tc) return xp_attn_tc_plan(c, a);
+  xp_attn_plan p = xp_attn_simt_plan(c, a);
   const size_t rows = (size_t)a->N * a->T * a->heads;
   p.stat_off = 0;
   p.acc_off = align_up(rows * p.parts * 8);
@@ -250,9 +251,11 @@ xp_status xp_prefix_attention(const xp_cache* c, const xp_attn* a, const void* q
   g.lse = lse;
   g.stat = (float*)((char*)ws + plan.stat_off);
   g.acc = (float*)((char*)ws + plan.acc_off);
+  g.line = (long long*)((char*)ws + plan.line_off);
   g.err = c->err;
   g.plan = plan;
-  cudaError_t e = c->attn_tc ? xp_launch_attn_tc(c, g, stream) : xp_launch_attn_simt(c, g, stream);
+  if (c->attn_tc) return cuda_status(xp_launch_attn_tc(c, g, stream));
+  cudaError_t e = xp_launch_attn_simt(c, g, stream);
   if (e == cudaSuccess) e = xp_launch_attn_combine(c, g, stream);
   return cuda_status(e);
 }

@@ -30,7 +30,6 @@ constexpr int kThreads = 384;
 constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
 constexpr int kChunkBytes = kTile * 128;   // 64 elements of 128 rows, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;
-constexpr int kApart = 4;       // items of a stream from which the streams are set apart
 constexpr float kLazy = 8.0f;   // growth of the maximum (base 2) that P may carry
 
 template <int D>
@@ -41,20 +40,58 @@ struct Cfg {
   static constexpr int SMEM = (2 + STAGES) * TILE_BYTES;
 };
 
-struct Bars {
-  uint64_t full[10], empty[10];
-  uint64_t q_full, s_full[2], p_half[2], p_full[2], o_full[2];
-  uint32_t tmem_base;
-  int abort;
+constexpr int kFrags = 4;       // fragments announced ahead
+constexpr int kUnitCost = 3;    // what a unit costs besides its tiles, in tiles of one stream
+constexpr int kMinChunk = 5;    // least cost a CTA is given
+
+struct Frag {
+  int kind;              // 0 prefix, 1 tail, -1 no more
+  int shared;            // two row tiles over the same keys
+  int n, hk, tile;       // sequence (tail), kv head, first row tile
+  int len;               // keys of the source
+  int t0, t1;            // key tiles
+  int slot;              // where its partial result goes: -1 the unit's own place, else a CTA's
 };
 
-struct Unit {
-  bool prefix, shared;   // shared: two row tiles over the same keys
-  int n, hk, tile;       // first row tile (of the batch, or of the sequence)
-  int part, k0, k1;      // key range
-  int len;               // keys of the source
-  const int32_t* table;
+struct Bars {
+  uint64_t full[10], empty[10];
+  uint64_t frag_full[kFrags], frag_empty[kFrags];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
+  uint64_t x_full, x_done;       // both softmax groups: statistics exchanged, sums read
+  Frag frag[kFrags];
+  float2 stat[2][kRows];
+  long long total[kThreads / 32], start_base;   // start: where this CTA's share begins
+  int start_n;
+  uint32_t tmem_base;
+  int abort;
+  int issued[2];                 // items of each stream whose products are issued
 };
+
+// The work is one line of cost: prefix units (kv head, pair of row tiles), then the units of
+// each sequence's tail, a unit costing kUnitCost and 2 (two streams on each tile) or 1 a key
+// tile.  CTA i does [i*chunk, (i+1)*chunk) of it, so that a unit may be cut anywhere between
+// two of its tiles and every CTA gets the same.  A piece that begins its unit leaves its
+// result in the unit's place, one that does not in the place of its CTA, of which there is
+// at most one.
+struct Line {
+  int pairs, odd, T;       // row tiles as pairs and one over; key tiles
+  __host__ __device__ Line(int row_tiles, int keys)
+      : pairs(row_tiles / 2), odd(row_tiles % 2), T((keys + kTile - 1) / kTile) {}
+  __host__ __device__ long long unit(int p) const { return (p < pairs ? 2 : 1) * (long long)T + kUnitCost; }
+  // all row tiles of one kv head
+  __host__ __device__ long long head() const {
+    return T ? pairs * unit(0) + odd * unit(pairs) : 0;
+  }
+  // first tile of unit p that lies behind a cost of x from the unit's beginning
+  __host__ __device__ int tile_at(int p, long long x) const {
+    const int w = p < pairs ? 2 : 1;
+    const long long t = (x - kUnitCost + w - 1) / w;
+    return x <= kUnitCost ? 0 : t > T ? T : (int)t;
+  }
+};
+
+// the same value in every lane, known to be: descriptors made from it need no per-lane registers
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -102,56 +139,78 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t saddr) {
 __device__ __forceinline__ int pos_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int pos_v(int j, int T) { return j < T - 1 ? 2 * j + 2 : 2 * T - 1; }
 
-__device__ __forceinline__ bool decode_unit(const xp_attn_args& g, int u, Unit* w) {
-  const xp_attn_plan& p = g.plan;
-  const int pairs = (p.prefix_tiles + 1) / 2, n_prefix = p.prefix_splits * pairs * g.kv_heads;
-  int tiles, split, step;
-  w->prefix = u < n_prefix;
-  if (w->prefix) {
-    w->tile = u % pairs * 2;
-    w->hk = u / pairs % g.kv_heads;
-    split = u / pairs / g.kv_heads;
-    w->n = 0;
-    w->part = split;
-    w->len = g.a.prefix_len;
-    w->table = g.prefix_table;
-    tiles = p.prefix_tiles;
-    step = p.prefix_keys;
-  } else {
-    u -= n_prefix;
-    const int tp = (p.tail_tiles + 1) / 2;
-    w->hk = u % g.kv_heads;
-    w->tile = u / g.kv_heads % tp * 2;
-    split = u / g.kv_heads / tp % p.tail_splits;
-    w->n = u / g.kv_heads / tp / p.tail_splits;
-    w->part = p.prefix_splits + split;
-    w->table = g.table + w->n * g.ld_table;
-    w->len = g.lens[w->n];
-    if (w->len < 0 || w->len > g.a.max_len) {
-      if (threadIdx.x == 0) atomicOr(g.err, XP_ERR_LENGTH);
-      w->len = w->len < 0 ? 0 : g.a.max_len;
-    }
-    tiles = p.tail_tiles;
-    step = p.tail_keys;
-  }
-  w->shared = w->tile + 1 < tiles;
-  w->k0 = split * step;
-  w->k1 = min(w->len, w->k0 + step);
-  return w->k0 < w->k1;
-}
-
-// query row r of a row tile: its place among the N*T*heads rows, -1 behind the end, and the
+// query row r of row tile `tile`: its place among the N*T*heads rows, -1 behind the end, and the
 // number of keys it sees
-__device__ __forceinline__ int64_t row_of(const xp_attn_args& g, const Unit& w, int tile, int r,
-                                          int* n, int* t, int* h, int* limit) {
+__device__ __forceinline__ int64_t row_of(const xp_attn_args& g, const Frag& w, int tile, int r, int* n,
+                                          int* t, int* h, int* limit) {
   const int per_seq = g.a.T * g.group, i = tile * kRows + r;
   *limit = 0;
-  if (i >= (w.prefix ? g.a.N * per_seq : per_seq)) return -1;
-  *n = w.prefix ? i / per_seq : w.n;
+  if (i >= (w.kind == 0 ? g.a.N * per_seq : per_seq)) return -1;
+  *n = w.kind == 0 ? i / per_seq : w.n;
   *t = i % per_seq / g.group;
   *h = w.hk * g.group + i % g.group;
-  *limit = min(w.k1, w.prefix ? w.len : w.len - g.a.T + *t + 1);
+  *limit = w.kind == 0 ? w.len : w.len - g.a.T + *t + 1;
   return ((int64_t)*n * g.a.T + *t) * g.a.heads + *h;
+}
+
+// Partial results lie in blocks of 32 query rows, [D/4][32 rows][4], so that a warp writes and
+// reads them 512 bytes at a time: the prefix's by kv head, then each sequence's by kv head,
+// then 8 blocks for every CTA's piece that does not begin its unit.
+__device__ __forceinline__ int64_t block_of(const xp_attn_args& g, int kind, int n, int hk) {
+  const int64_t per_seq = g.a.T * g.group, all = (g.a.N * per_seq + 31) / 32;
+  return kind == 0 ? hk * all : g.kv_heads * all + ((int64_t)n * g.kv_heads + hk) * ((per_seq + 31) / 32);
+}
+__device__ __forceinline__ int64_t blocks_of(const xp_attn_args& g) { return block_of(g, 1, g.a.N, 0); }
+
+__device__ __forceinline__ int tail_len(const xp_attn_args& g, int n, bool tell) {
+  int len = g.lens[n];
+  if (len < 0 || len > g.a.max_len) {
+    if (tell) atomicOr(g.err, XP_ERR_LENGTH);
+    len = len < 0 ? 0 : g.a.max_len;
+  }
+  return len;
+}
+
+// Sums the tails' costs over the CTA: the chunk, and the sequence in which this CTA's share
+// begins (with the cost before it).  CTA 0 leaves the chunk and every sequence's beginning for
+// the kernel that joins the results.
+__device__ long long plan_line(const xp_attn_args& g, Bars* bars) {
+  const Line pre(g.plan.prefix_tiles, g.a.prefix_len);
+  const long long before = pre.head() * g.kv_heads;
+  const int N = g.a.max_len > 0 ? g.a.N : 0;
+  const int per = (N + kThreads - 1) / kThreads, n0 = min(N, (int)threadIdx.x * per), n1 = min(N, n0 + per);
+  auto cost = [&](int n) { return Line(g.plan.tail_tiles, tail_len(g, n, blockIdx.x == 0)).head() * g.kv_heads; };
+  long long mine = 0;
+  for (int n = n0; n < n1; ++n) mine += cost(n);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) bars->total[warp] = inc;
+  __syncthreads();
+  long long base = before + inc - mine, all = before;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    base += w < warp ? bars->total[w] : 0;
+    all += bars->total[w];
+  }
+  long long chunk = (all + gridDim.x - 1) / gridDim.x;
+  chunk = chunk < kMinChunk ? kMinChunk : chunk;
+  const long long x = (long long)blockIdx.x * chunk;
+  for (int n = n0; n < n1; ++n) {
+    const long long c = cost(n);
+    if (blockIdx.x == 0) g.line[1 + n] = base;
+    if (c > 0 && x >= base && x < base + c) {
+      bars->start_n = n;
+      bars->start_base = base;
+    }
+    base += c;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) g.line[0] = chunk;
+  __syncthreads();
+  return x < all ? chunk : 0;
 }
 
 template <int D>
@@ -159,47 +218,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const xp_attn_args g, int box, bool q_wide) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = ptx::smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + C::SMEM);
   volatile int* abort = &bars->abort;
   const uint32_t sq = ptx::smem_u32(smem), ring = sq + 2 * C::TILE_BYTES;
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
-  Unit w;
-  const bool work = decode_unit(g, blockIdx.x, &w);
-  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
-  const int per_tile_rows =
-      min(kRows * (w.shared ? 2 : 1),
-          (w.prefix ? g.a.N * g.a.T * g.group : g.a.T * g.group) - w.tile * kRows);
-  if (!work) {   // no key in this range: its parts are empty
-    for (int r = threadIdx.x; r < per_tile_rows; r += kThreads) {
-      int n, t, h, lim;
-      const int64_t row = row_of(g, w, w.tile, r, &n, &t, &h, &lim);
-      *(float2*)&g.stat[(w.part * rows + row) * 2] = make_float2(-INFINITY, 0.0f);
-    }
+  const long long chunk = plan_line(g, bars);
+  if (chunk == 0) return;   // the line ends before this CTA's share
+  if (sq & 1023u) {         // the swizzled tiles need it; the declared alignment gives it
+    if (threadIdx.x == 0) atomicOr(g.err, XP_ERR_TIMEOUT);
     return;
   }
-  const int T = (w.k1 - w.k0 + kTile - 1) / kTile;
-  const int items = w.shared ? 2 * T : T;
-  // softmax warps that hold rows; the others stay out of the streams
-  const int active0 = min(4, (per_tile_rows + 31) / 32);
-  const int active1 = w.shared ? min(4, (per_tile_rows - kRows + 31) / 32) : active0;
 
   if (threadIdx.x == 0) {
+    auto init = [](uint64_t* bar, int count) { ptx::mbar_init(ptx::smem_u32(bar), count); };
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&bars->full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bars->empty[s]), w.shared ? 2 : 1);
+      init(&bars->full[s], 1);
+      init(&bars->empty[s], 2);
     }
-    ptx::mbar_init(ptx::smem_u32(&bars->q_full), 8);
+    for (int s = 0; s < kFrags; ++s) {
+      init(&bars->frag_full[s], 1);
+      init(&bars->frag_empty[s], 11);   // 8 softmax warps, 2 issuing the products, 1 loading
+    }
     for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(ptx::smem_u32(&bars->s_full[t]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bars->p_half[t]), t ? active1 : active0);
-      ptx::mbar_init(ptx::smem_u32(&bars->p_full[t]), t ? active1 : active0);
-      ptx::mbar_init(ptx::smem_u32(&bars->o_full[t]), 1);
+      init(&bars->q_full[t], 1);
+      init(&bars->q_empty[t], 2);
+      init(&bars->s_full[t], 1);
+      init(&bars->p_half[t], 4);
+      init(&bars->p_full[t], 4);
+      init(&bars->o_full[t], 1);
     }
+    init(&bars->x_full, 8);
+    init(&bars->x_done, 8);
     bars->abort = 0;
+    bars->issued[0] = bars->issued[1] = 0;
     ptx::fence_barrier_init();
   }
   if (warp == 8) {
@@ -211,313 +264,451 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
+  auto wait = [&](uint64_t* bar, int phase) {
+    const bool ok = ptx::mbar_wait(ptx::smem_u32(bar), phase & 1, abort, g.err);
+    return __all_sync(0xFFFFFFFFu, ok) != 0;
+  };
+  // fragment f as announced; its place is free again at once
+  auto next_frag = [&](int f, Frag* w) {
+    if (!wait(&bars->frag_full[f % kFrags], f / kFrags)) return false;
+    *w = bars->frag[f % kFrags];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->frag_empty[f % kFrags]));
+    return w->kind >= 0;
+  };
+
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 10) {
-      // ---- K and V tiles: lane (chunk, box) loads `box` tokens of one page ----
-      const uint64_t pol = w.prefix ? ptx::policy_evict_last() : ptx::policy_evict_first();
-      const int per = kTile / box, chunk = lane / per, in_tile = lane % per * box;
-      int issued = 0;   // tiles loaded
-      // this lane's page of tile j (its box may lie behind the range: then none is loaded)
-      auto page_of = [&](int j) {
-        const int at = w.k0 + j * kTile + in_tile;
-        if (chunk >= C::CH || at >= w.k1) return -1;
-        int page = w.table[at / g.page_size];
-        if (page < 0 || page >= g.pages) {
-          atomicOr(g.err, XP_ERR_BADPAGE);
-          page = page < 0 ? 0 : g.pages - 1;
+    if (warp == 11) {
+      // ---- announces the fragments and loads their query tiles.  Two query tiles a shared
+      // fragment, one of the two places in turn for the others, so that the next one's queries
+      // are there before the present one is done ----
+      const long long x0 = (long long)blockIdx.x * chunk, x1 = x0 + chunk;
+      const Line pre(g.plan.prefix_tiles, g.a.prefix_len);
+      const long long before = pre.head() * g.kv_heads;
+      const int N = g.a.max_len > 0 ? g.a.N : 0;
+      int f = 0, splits = 0, used[2] = {0, 0};
+      bool ok = true;
+      auto load_q = [&](const Frag& w, int tile, int place) {
+        if (!wait(&bars->q_empty[place], (used[place] & 1) ^ 1)) return false;
+        ++used[place];
+        uint8_t* dst = smem + place * C::TILE_BYTES;
+        for (int r = lane; r < kRows; r += 32) {
+          int n, t, h, lim;
+          if (row_of(g, w, tile, r, &n, &t, &h, &lim) < 0) break;   // rows behind the end: anything
+          const bf16* src = (const bf16*)g.q + n * g.a.q_stride_n + t * g.a.q_stride_t +
+                            h * g.a.q_stride_h;
+          for (int seg = 0; seg < D / 8; ++seg) {
+            uint8_t* to = dst + (seg / 8) * kChunkBytes + r * 128 + (((seg % 8) ^ (r & 7)) << 4);
+            if (q_wide) {
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(to)),
+                           "l"(__cvta_generic_to_global(src + seg * 8))
+                           : "memory");
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) ((uint16_t*)to)[e] = ((const uint16_t*)src)[seg * 8 + e];
+            }
+          }
         }
-        return page;
-      };
-      auto load = [&](int j, int page, const CUtensorMap* map) {
-        const int s = issued % C::STAGES;
-        bool ok = ptx::mbar_wait(ptx::smem_u32(&bars->empty[s]), ((issued / C::STAGES) & 1) ^ 1, abort,
-                                 g.err);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) return false;
-        const int key = w.k0 + j * kTile;
-        const int boxes = (min(kTile, w.k1 - key) + box - 1) / box;
-        const uint32_t full = ptx::smem_u32(&bars->full[s]);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * box * 128 * C::CH);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (page >= 0)
-          ptx::tma_load_5d(ring + s * C::TILE_BYTES + chunk * kChunkBytes + in_tile * 128, map, full,
-                           chunk * 64, (key + in_tile) % g.page_size, w.hk, page, g.a.layer, pol);
-        ++issued;
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->q_full[place]));
         return true;
       };
-      int now = page_of(0), next = page_of(1);   // the page ids are read ahead of the loads
-      bool ok = load(0, now, &tm_k);
-      for (int j = 0; j < T && ok; ++j) {
-        const int after = page_of(j + 2);
-        if (j + 1 < T) ok = load(j + 1, next, &tm_k);
-        ok = ok && load(j, now, &tm_v);
-        now = next;
-        next = after;
+      auto announce = [&](const Frag& w) {
+        if (!wait(&bars->frag_empty[f % kFrags], ((f / kFrags) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          bars->frag[f % kFrags] = w;
+          ptx::mbar_arrive(ptx::smem_u32(&bars->frag_full[f % kFrags]));
+        }
+        __syncwarp();
+        ++f;
+        if (w.kind < 0) return true;
+        if (w.shared) return load_q(w, w.tile, 0) && load_q(w, w.tile + 1, 1);
+        return load_q(w, w.tile, splits++ & 1);
+      };
+      // the units of one source that lie in [x0, x1), from cost `at` on
+      auto source = [&](const Line& l, int kind, int n, int len, long long at) {
+        if (l.T == 0) return true;
+        const int per = l.pairs + l.odd;
+        int hk = 0, p = 0;
+        if (x0 > at) {   // skip what lies before
+          const long long off = x0 - at;
+          hk = (int)(off / l.head());
+          at += hk * l.head();
+          p = (int)min((long long)l.pairs, (x0 - at) / l.unit(0));
+          at += p * l.unit(0);
+          if (hk >= g.kv_heads) return true;
+        }
+        for (; hk < g.kv_heads && at < x1; ++hk, p = 0)
+          for (; p < per && at < x1; ++p) {
+            const long long cost = l.unit(p);
+            const int t0 = l.tile_at(p, x0 - at), t1 = l.tile_at(p, min(x1 - at, cost));
+            if (t0 < t1) {
+              const Frag w = {kind, p < l.pairs, n, hk, 2 * p, len, t0, t1, t0 > 0 ? (int)blockIdx.x : -1};
+              if (!announce(w)) return false;
+            }
+            at += cost;
+          }
+        return true;
+      };
+      if (x0 < before) ok = source(pre, 0, 0, g.a.prefix_len, 0);
+      if (x1 > before) {
+        int n = x0 < before ? 0 : bars->start_n;
+        long long at = x0 < before ? before : bars->start_base;
+        int len = n < N ? tail_len(g, n, false) : 0;
+        for (; ok && n < N && at < x1; ++n) {
+          const int after = n + 1 < N ? tail_len(g, n + 1, false) : 0;   // read ahead
+          const Line l(g.plan.tail_tiles, len);
+          ok = source(l, 1, n, len, at);
+          at += l.head() * g.kv_heads;
+          len = after;
+        }
       }
-      // nothing may land in shared memory after the CTA is gone
+      if (ok) announce({-1, 0, 0, 0, 0, 0, 0, 0, 0});
+    } else if (warp == 10) {
+      // ---- K and V tiles: lane (chunk, box) loads `box` tokens of one page ----
+      const uint64_t keep = ptx::policy_evict_last(), stream = ptx::policy_evict_first();
+      const int per = kTile / box, chunk_of = lane / per, in_tile = lane % per * box;
+      int issued = 0;   // tiles loaded
+      Frag w;
+      bool ok = true;
+      for (int f = 0; ok && next_frag(f, &w); ++f) {
+        const int32_t* table = w.kind == 0 ? g.prefix_table : g.table + w.n * g.ld_table;
+        const int end = min(w.len, w.t1 * kTile);
+        // this lane's page of key tile j (its box may lie behind the end: then none is loaded)
+        auto page_of = [&](int j) {
+          const int at = j * kTile + in_tile;
+          if (chunk_of >= C::CH || at >= end) return -1;
+          int page = table[at / g.page_size];
+          if (page < 0 || page >= g.pages) {
+            atomicOr(g.err, XP_ERR_BADPAGE);
+            page = page < 0 ? 0 : g.pages - 1;
+          }
+          return page;
+        };
+        auto load = [&](int j, int page, const CUtensorMap* map) {
+          const int s = issued % C::STAGES;
+          if (!wait(&bars->empty[s], ((issued / C::STAGES) & 1) ^ 1)) return false;
+          const int key = j * kTile, boxes = (min(kTile, end - key) + box - 1) / box;
+          const uint32_t full = ptx::smem_u32(&bars->full[s]);
+          if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * box * 128 * C::CH);
+          __syncwarp();
+          if (page >= 0)
+            ptx::tma_load_5d(ring + s * C::TILE_BYTES + chunk_of * kChunkBytes + in_tile * 128, map,
+                             full, chunk_of * 64, (key + in_tile) % g.page_size, w.hk, page, g.a.layer,
+                             w.kind == 0 ? keep : stream);
+          ++issued;
+          return true;
+        };
+        int now = page_of(w.t0), next = page_of(w.t0 + 1);   // the page ids are read ahead
+        ok = load(w.t0, now, &tm_k);
+        for (int j = w.t0; j < w.t1 && ok; ++j) {
+          const int after = page_of(j + 2);
+          if (j + 1 < w.t1) ok = load(j + 1, next, &tm_k);
+          ok = ok && load(j, now, &tm_v);
+          now = next;
+          next = after;
+        }
+      }
+      // nothing may land in shared memory after the CTA is gone: neither the loads nor the
+      // products' arrivals
       volatile int no_abort = 0;
       for (int s = 0; s < C::STAGES; ++s) {
         const int n = (issued + C::STAGES - 1 - s) / C::STAGES;   // loads of this stage
-        if (n > 0) ptx::mbar_wait(ptx::smem_u32(&bars->full[s]), (n - 1) & 1, &no_abort, g.err);
+        if (n > 0) {
+          ptx::mbar_wait(ptx::smem_u32(&bars->full[s]), (n - 1) & 1, &no_abort, g.err);
+          if (!*abort) ptx::mbar_wait(ptx::smem_u32(&bars->empty[s]), (n - 1) & 1, abort, g.err);
+        }
       }
-    } else if (warp < 10) {
+    } else {
       // ---- the products of stream t: O += P V of its item j, then S = Q K^T of item j + 1 in
       // its place.  The warp runs the loop converged, so that descriptors stay in uniform
       // registers, and a warp a stream, so that one's waits run under the other's products ----
       constexpr uint32_t kS = ptx::idesc_bf16_f32(kRows, kTile);
       constexpr uint32_t kO = ptx::idesc_bf16_f32(kRows, D) | (1u << 16);   // V: head dims contiguous
-      const int t = warp - 8, mine = (items + 1 - t) / 2;
-      const uint32_t q = sq + (w.shared ? t * C::TILE_BYTES : 0);
-      const uint32_t s_col = tmem + t * kTile, o_col = tmem + 2 * kTile + t * D;
+      const int t = warp - 8;
+      const uint32_t s_col = uniform(tmem + t * kTile), o_col = uniform(tmem + 2 * kTile + t * D);
       const bool leader = ptx::elect_one();
-      auto wait = [&](uint64_t* bar, int phase) {
-        const bool ok = ptx::mbar_wait(ptx::smem_u32(bar), phase & 1, abort, g.err);
-        return __all_sync(0xFFFFFFFFu, ok) != 0;
+      int done = 0, other = 0, pos0 = 0, splits = 0, used[2] = {0, 0};   // items of both streams
+      // The streams take turns: were both to issue together, their products would end together,
+      // and neither's would run under the other's exponentials.  A pause, nothing more: it
+      // ends by itself, and no result depends on it.
+      auto turn = [&](int j, int theirs) {
+        const int want = other + min(t ? j + 1 : j, theirs);
+        for (int spin = 0; spin < 100 && *(volatile int*)&bars->issued[1 - t] < want; ++spin) {}
+        __syncwarp();
       };
       auto loaded = [&](int pos) { return wait(&bars->full[pos % C::STAGES], pos / C::STAGES); };
-      auto kv = [&](int j) { return w.shared ? j : 2 * j + t; };
-      // the stage of load `pos` is free again, where another load waits for it (a commit that
-      // nobody waits for could land behind the CTA's end)
-      auto release = [&](int pos) {
-        if (pos + C::STAGES < 2 * T) ptx::mma_commit(ptx::smem_u32(&bars->empty[pos % C::STAGES]));
-      };
-      auto scores = [&](int pos) {
-        const uint32_t k = ring + pos % C::STAGES * C::TILE_BYTES;
-        if (leader) {
+      Frag w;
+      bool ok = true;
+      for (int f = 0; ok && next_frag(f, &w); ++f) {
+        const int T = w.t1 - w.t0, items = w.shared ? 2 * T : T, mine = (items + 1 - t) / 2;
+        const int place = w.shared ? t : splits & 1;
+        const uint32_t q = uniform(sq + place * C::TILE_BYTES);
+        if (w.shared) {
+          ++used[0];
+          ++used[1];
+        } else {
+          ++used[place];
+          ++splits;
+        }
+        auto kv = [&](int j) { return w.shared ? j : 2 * j + t; };
+        // a tile that both streams read is free when both are done; one's own counts twice
+        auto release = [&](int pos) {
+          const uint32_t bar = ptx::smem_u32(&bars->empty[pos % C::STAGES]);
+          ptx::mma_commit(bar);
+          if (!w.shared) ptx::mma_commit(bar);
+        };
+        auto scores = [&](int j) {
+          const int pos = pos0 + pos_k(kv(j));
+          const uint32_t k = uniform(ring + pos % C::STAGES * C::TILE_BYTES);
+          if (leader) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks / 4) * kChunkBytes + (ks % 4) * 32;
-            ptx::mma_bf16(s_col, ptx::sw128_desc(q + off), ptx::sw128_desc(k + off), kS, ks > 0);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks / 4) * kChunkBytes + (ks % 4) * 32;
+              ptx::mma_bf16(s_col, ptx::sw128_desc(q + off), ptx::sw128_desc(k + off), kS, ks > 0);
+            }
+            ptx::mma_commit(ptx::smem_u32(&bars->s_full[t]));
+            release(pos);
+            if (j == mine - 1) {   // the queries are read
+              ptx::mma_commit(ptx::smem_u32(&bars->q_empty[place]));
+              if (w.shared) ptx::mma_commit(ptx::smem_u32(&bars->q_empty[place]));
+            }
           }
-          ptx::mma_commit(ptx::smem_u32(&bars->s_full[t]));
-          release(pos);
-        }
-        __syncwarp();
-      };
-      bool ok = mine > 0 && wait(&bars->q_full, 0) && loaded(pos_k(kv(0)));
-      // the streams run half a period apart (started together they would stay together, and
-      // neither's products would run under the other's exponentials)
-      if (ok && t == 1 && mine >= kApart) ok = wait(&bars->p_half[0], 0);
-      if (ok) {
-        ptx::tc_fence_after();
-        scores(pos_k(kv(0)));
-      }
-      for (int j = 0; j < mine && ok; ++j) {
-        const int pv = pos_v(kv(j), T), pk = pos_k(kv(j + 1));
-        const uint32_t v = ring + pv % C::STAGES * C::TILE_BYTES;
-        // the tiles are there before the weights are
-        ok = loaded(pv) && (j + 1 >= mine || loaded(pk));
-        ok = ok && wait(&bars->p_half[t], j);
+          __syncwarp();
+        };
+        // waited for also where this stream has no item: its arrival must not count for the
+        // queries that were there before
+        ok = wait(&bars->q_full[place], used[place] - 1);
         if (!ok) break;
-        ptx::tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int ks = 0; ks < kTile / 32; ++ks)
-            ptx::mma_bf16_ts(o_col, s_col + ks * 8, v_desc(v + ks * 2048), kO, j > 0 || ks > 0);
+        if (mine == 0) {
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->q_empty[place]));
+        } else {
+          ok = loaded(pos0 + pos_k(kv(0)));
+          if (ok) {
+            ptx::tc_fence_after();
+            scores(0);
+          }
         }
-        __syncwarp();
-        ok = wait(&bars->p_full[t], j);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (leader) {
+        for (int j = 0; j < mine && ok; ++j) {
+          const int pv = pos0 + pos_v(kv(j), T);
+          const uint32_t v = uniform(ring + pv % C::STAGES * C::TILE_BYTES);
+          // the tiles are there before the weights are
+          ok = loaded(pv) && (j + 1 >= mine || loaded(pos0 + pos_k(kv(j + 1))));
+          ok = ok && wait(&bars->p_half[t], done + j);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (leader) {
 #pragma unroll
-          for (int ks = kTile / 32; ks < kTile / 16; ++ks)
-            ptx::mma_bf16_ts(o_col, s_col + ks * 8, v_desc(v + ks * 2048), kO, 1);
-          ptx::mma_commit(ptx::smem_u32(&bars->o_full[t]));
-          release(pv);
+            for (int ks = 0; ks < kTile / 32; ++ks)
+              ptx::mma_bf16_ts(o_col, s_col + ks * 8, v_desc(v + ks * 2048), kO, j > 0 || ks > 0);
+          }
+          __syncwarp();
+          ok = wait(&bars->p_full[t], done + j);
+          if (!ok) break;
+          turn(j, items - mine);
+          ptx::tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int ks = kTile / 32; ks < kTile / 16; ++ks)
+              ptx::mma_bf16_ts(o_col, s_col + ks * 8, v_desc(v + ks * 2048), kO, 1);
+            ptx::mma_commit(ptx::smem_u32(&bars->o_full[t]));
+            release(pv);
+          }
+          __syncwarp();
+          if (j + 1 < mine) scores(j + 1);
+          if (leader) *(volatile int*)&bars->issued[t] = done + j + 1;
         }
-        __syncwarp();
-        if (j + 1 < mine) scores(pk);
+        done += mine;
+        other += items - mine;
+        pos0 += 2 * T;
       }
     }
   } else {
-    // ---- softmax ----
+    // ---- softmax: warps 0-3 of stream 0, 4-7 of stream 1; a thread is a query row ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp / 4, r = threadIdx.x - t * 128;
     const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
-    const int tile = w.shared ? w.tile + t : w.tile;
-    // the query tile, 16 bytes at a time, in the swizzled layout of the A operand
-    if (t == 0 || w.shared) {
-      constexpr int SEG = D / 8;
-      for (int i = r; i < kRows * SEG; i += 128) {
-        const int rr = i / SEG, seg = i % SEG;
-        int n, tt, h, lim;
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (row_of(g, w, tile, rr, &n, &tt, &h, &lim) >= 0) {
-          const bf16* src = (const bf16*)g.q + n * g.a.q_stride_n + tt * g.a.q_stride_t +
-                            h * g.a.q_stride_h + seg * 8;
-          if (q_wide) {
-            val = *(const uint4*)src;
-          } else {
-            uint16_t e[8];
+    const float c = g.a.scale * 1.44269504088896f;
+    int done = 0, pos0 = 0, joins = 0;
+    bool unread = false;   // the other group may still read this one's sums
+    Frag w;
+    bool ok = true;
+    for (int f = 0; ok && next_frag(f, &w); ++f) {
+      const int T = w.t1 - w.t0, items = w.shared ? 2 * T : T, mine = (items + 1 - t) / 2;
+      const int tile = w.shared ? w.tile + t : w.tile;
+      int n, tt, h, limit;
+      const int64_t row = row_of(g, w, tile, r, &n, &tt, &h, &limit);
+      const int end = min(w.len, w.t1 * kTile);
+      limit = row < 0 ? end : min(limit, end);   // rows behind the end ask for no mask of their own
+      const bool active = __any_sync(0xFFFFFFFFu, row >= 0);
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < mine; ++j) {
+        ok = wait(&bars->s_full[t], done + j);
+        if (!ok) break;
+        const int kt = w.shared ? j : 2 * j + t, key = (w.t0 + kt) * kTile;
+        // V rows behind the range may hold anything: cleared before this stream's product reads
+        // them (streams that share the tile both write the zeros)
+        const int valid = end - key;
+        if (valid < kTile) {
+          const int pos = pos0 + pos_v(kt, T), st = pos % C::STAGES;
+          ok = wait(&bars->full[st], pos / C::STAGES);
+          if (!ok) break;
+          uint8_t* v = smem + (2 + st) * C::TILE_BYTES;
+          for (int i = r; i < (kTile - valid) * C::CH * 8; i += 128) {
+            const int rr = valid + i / (C::CH * 8), seg = i % (C::CH * 8);
+            *(uint4*)(v + (seg / 8) * kChunkBytes + rr * 128 + (seg % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (j == 0 && unread) {
+          ok = wait(&bars->x_done, joins - 1);
+          if (!ok) break;
+          unread = false;
+        }
+        if (!active) {   // no rows here: only the hand-over
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[t]));
+            ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[t]));
+          }
+          continue;
+        }
+        ptx::tc_fence_after();
+        const uint32_t scol = tmem + lanes + t * kTile;
+        uint32_t s[4][32];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) e[x] = ((const uint16_t*)src)[x];
-            val = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16,
-                             e[4] | (uint32_t)e[5] << 16, e[6] | (uint32_t)e[7] << 16);
+        for (int q = 0; q < 4; ++q) ptx::tmem_ld32(scol + q * 32, s[q]);
+        ptx::tmem_wait_ld();
+        if (__any_sync(0xFFFFFFFFu, key + kTile > limit)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (key + q * 32 + x >= limit) s[q][x] = 0xFF800000u;   // -inf
+        }
+        float top[4];   // four chains, three operands an instruction
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          top[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+#pragma unroll
+          for (int x = 2; x < 32; x += 2)
+            top[q] = fmaxf(fmaxf(top[q], __uint_as_float(s[q][x])), __uint_as_float(s[q][x + 1]));
+        }
+        const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+        if (j == 0) {
+          m = now;
+        } else {
+          const bool grown = (now - m) * c > kLazy;   // from -inf too
+          if (__any_sync(0xFFFFFFFFu, grown)) {
+            ok = wait(&bars->o_full[t], done + j - 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const float f = grown ? ex2((m - now) * c) : 1.0f;
+            const uint32_t ocol = tmem + lanes + 2 * kTile + t * D;
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              ptx::tmem_ld16(ocol + q * 16, o);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              ptx::tmem_st16(ocol + q * 16, o);
+            }
+            ptx::tmem_wait_st();
+            l *= f;
+            if (grown) m = now;
           }
         }
-        const int c = seg / 8;
-        *(uint4*)(smem + t * C::TILE_BYTES + c * kChunkBytes + rr * 128 +
-                  (((seg % 8) ^ (rr & 7)) << 4)) = val;
+        const float base = m == -INFINITY ? 0.0f : m * c;
+        const uint64_t c2 = pair(c, c), nb2 = pair(-base, -base);
+        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2, nb2);
+            const float a = ex2(low(z)), b = ex2(high(z));
+            sum[x % 4] = add2(sum[x % 4], pair(a, b));
+            pk[x] = pack_bf16(a, b);
+          }
+          ptx::tmem_st16(scol + q * 16, pk);
+          if (q & 1) {   // the product may start on the first half of the keys
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::mbar_arrive(ptx::smem_u32(q == 1 ? &bars->p_half[t] : &bars->p_full[t]));
+            }
+          }
+        }
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += low(sum[0]) + high(sum[0]);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->q_full));
-
-    const bool active = warp % 4 < (t ? active1 : active0);
-    int n, tt, h, limit;
-    const int64_t row = row_of(g, w, tile, r, &n, &tt, &h, &limit);
-    if (row < 0) limit = w.k1;   // rows behind the end ask for no mask of their own
-    const float c = g.a.scale * 1.44269504088896f;
-    const int mine = active ? (items + 1 - t) / 2 : 0;   // items of this stream
-    float m = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int j = 0; j < mine; ++j) {
-      ok = ptx::mbar_wait(ptx::smem_u32(&bars->s_full[t]), j & 1, abort, g.err);
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      done += mine;
+      pos0 += 2 * T;
+      if (mine > 0 && ok) ok = wait(&bars->o_full[t], done - 1);
       if (!ok) break;
       ptx::tc_fence_after();
-      const uint32_t scol = tmem + lanes + t * kTile;
-      uint32_t s[4][32];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) ptx::tmem_ld32(scol + q * 32, s[q]);
-      ptx::tmem_wait_ld();
-      const int kt = w.shared ? j : 2 * j + t;
-      const int key = w.k0 + kt * kTile;
-      if (__any_sync(0xFFFFFFFFu, key + kTile > limit)) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (key + q * 32 + x >= limit) s[q][x] = 0xFF800000u;   // -inf
-      }
-      float top[4];   // four chains, three operands an instruction
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        top[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
-#pragma unroll
-        for (int x = 2; x < 32; x += 2)
-          top[q] = fmaxf(fmaxf(top[q], __uint_as_float(s[q][x])), __uint_as_float(s[q][x + 1]));
-      }
-      const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
-      if (j == 0) {
-        m = now;
-      } else {
-        const bool grown = (now - m) * c > kLazy;   // from -inf too
-        if (__any_sync(0xFFFFFFFFu, grown)) {
-          ok = ptx::mbar_wait(ptx::smem_u32(&bars->o_full[t]), (j - 1) & 1, abort, g.err);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+      // a row's keys are the whole range (shared) or every second tile: join the two streams
+      float f0 = 1.0f, f1 = 0.0f, mm = m, ll = l;
+      if (!w.shared) {
+        if (unread) {   // no item of this stream: the other group may still read the statistics
+          ok = wait(&bars->x_done, joins - 1);
           if (!ok) break;
-          ptx::tc_fence_after();
-          const float f = grown ? ex2((m - now) * c) : 1.0f;
-          const uint32_t ocol = tmem + lanes + 2 * kTile + t * D;
-#pragma unroll
-          for (int q = 0; q < D / 16; ++q) {
-            uint32_t o[16];
-            ptx::tmem_ld16(ocol + q * 16, o);
+          unread = false;
+        }
+        bars->stat[t][r] = make_float2(m, mine > 0 ? l : 0.0f);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->x_full));
+        ok = wait(&bars->x_full, joins);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const float2 a = bars->stat[0][r], b = bars->stat[1][r];
+        mm = fmaxf(a.y > 0.0f ? a.x : -INFINITY, b.y > 0.0f ? b.x : -INFINITY);
+        f0 = a.y > 0.0f ? ex2((a.x - mm) * c) : 0.0f;
+        f1 = b.y > 0.0f ? ex2((b.x - mm) * c) : 0.0f;
+        ll = f0 * a.y + f1 * b.y;
+      }
+      // each stream writes its rows, or (joined) its half of the head dims
+      if (active) {
+        const int q0 = w.shared ? 0 : t * (D / 64), q1 = w.shared ? D / 32 : q0 + D / 64;
+        const int64_t block = (w.slot < 0 ? block_of(g, w.kind, w.n, w.hk) + tile * 4
+                                          : blocks_of(g) + w.slot * 8 + (w.shared ? t * 4 : 0)) +
+                              warp % 4;
+        if (w.shared || t == 0)
+          ((float2*)g.stat)[block * 32 + lane] = make_float2(ll > 0.0f ? mm * c : -INFINITY, ll);
+        float4* acc = (float4*)g.acc + block * (D / 4) * 32 + lane;
+        for (int q = q0; q < q1; ++q) {
+          uint32_t o[32];
+          ptx::tmem_ld32(tmem + lanes + 2 * kTile + (w.shared ? t * D : 0) + q * 32, o);
+          if (w.shared || items == 1) {
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            ptx::tmem_st16(ocol + q * 16, o);
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f0);
+          } else {
+            uint32_t b[32];
+            ptx::tmem_ld32(tmem + lanes + 2 * kTile + D + q * 32, b);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              o[x] = __float_as_uint(__uint_as_float(o[x]) * f0 + __uint_as_float(b[x]) * f1);
           }
-          ptx::tmem_wait_st();
-          l *= f;
-          if (grown) m = now;
+#pragma unroll
+          for (int x = 0; x < 32; x += 4)   // a row's 16 bytes beside the next row's
+            *(uint4*)&acc[(q * 8 + x / 4) * 32] = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
         }
       }
-      // V rows behind the range may hold anything: cleared before this stream's product reads
-      // them (streams that share the tile both write the zeros)
-      const int valid = w.k1 - key;
-      if (valid < kTile) {
-        const int pos = pos_v(kt, T), st = pos % C::STAGES;
-        ok = ptx::mbar_wait(ptx::smem_u32(&bars->full[st]), (pos / C::STAGES) & 1, abort, g.err);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        const int aw = t ? active1 : active0;
-        uint8_t* v = smem + (2 + st) * C::TILE_BYTES;
-        for (int i = (warp % 4) * 32 + lane; i < (kTile - valid) * C::CH * 8; i += aw * 32) {
-          const int rr = valid + i / (C::CH * 8), seg = i % (C::CH * 8);
-          *(uint4*)(v + (seg / 8) * kChunkBytes + rr * 128 + (seg % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
-      const float base = m == -INFINITY ? 0.0f : m * c;
-      const uint64_t c2 = pair(c, c), nb2 = pair(-base, -base);
-      uint64_t sum[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2, nb2);
-          const float a = ex2(low(z)), b = ex2(high(z));
-          sum[x % 4] = add2(sum[x % 4], pair(a, b));
-          pk[x] = pack_bf16(a, b);
-        }
-        ptx::tmem_st16(scol + q * 16, pk);
-        if (q == 1) {   // the product may start on the first half of the keys
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->p_half[t]));
-        }
-      }
-      sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-      l += low(sum[0]) + high(sum[0]);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->p_full[t]));
-    }
-    if (mine > 0 && ok) {
-      ok = ptx::mbar_wait(ptx::smem_u32(&bars->o_full[t]), (mine - 1) & 1, abort, g.err);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-    }
-    ptx::tc_fence_after();
-    // a row's keys are the whole range (shared) or every second tile: join the two streams
-    float f0 = 1.0f, f1 = 0.0f, mm = m, ll = l;
-    if (!w.shared) {
-      float2* stat = (float2*)(smem + C::TILE_BYTES);   // the second query tile's room is free
-      stat[t * kRows + r] = make_float2(m, mine > 0 ? l : 0.0f);
-      ptx::tc_fence_before();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      ptx::tc_fence_after();
-      const float m0 = stat[r].x, l0 = stat[r].y;
-      const float m1 = stat[kRows + r].x, l1 = stat[kRows + r].y;
-      mm = fmaxf(l0 > 0.0f ? m0 : -INFINITY, l1 > 0.0f ? m1 : -INFINITY);
-      f0 = l0 > 0.0f ? ex2((m0 - mm) * c) : 0.0f;
-      f1 = l1 > 0.0f ? ex2((m1 - mm) * c) : 0.0f;
-      ll = f0 * l0 + f1 * l1;
-    }
-    // each stream writes its rows, or (joined) its half of the head dims
-    if (active && ok && !*abort) {
-      const int q0 = w.shared ? 0 : t * (D / 64), q1 = w.shared ? D / 32 : q0 + D / 64;
-      float* acc = g.acc + (w.part * rows + (row < 0 ? 0 : row)) * D;
-      if (row >= 0 && (w.shared || t == 0))
-        *(float2*)&g.stat[(w.part * rows + row) * 2] =
-            make_float2(ll > 0.0f ? mm * c : -INFINITY, ll);
-      for (int q = q0; q < q1; ++q) {
-        uint32_t o[32];
-        ptx::tmem_ld32(tmem + lanes + 2 * kTile + (w.shared ? t * D : 0) + q * 32, o);
-        if (w.shared || items == 1) {
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f0);
-        } else {
-          uint32_t b[32];
-          ptx::tmem_ld32(tmem + lanes + 2 * kTile + D + q * 32, b);
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            o[x] = __float_as_uint(__uint_as_float(o[x]) * f0 + __uint_as_float(b[x]) * f1);
-        }
-        if (row >= 0 && ll > 0.0f) {
-#pragma unroll
-          for (int x = 0; x < 32; x += 4)
-            *(uint4*)(acc + q * 32 + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-        }
+      if (!w.shared) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->x_done));
+        ++joins;
+        unread = true;
       }
     }
   }
@@ -530,16 +721,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// A query row's partial results: of the prefix and of its tail, each the unit's own and those of
+// the CTAs at whose beginning it was cut, brought to a common maximum:
+//   out = sum a_p O_p / sum a_p l_p,  a_p = 2^(m_p - m).
+// A CTA joins 32 rows of (sequence, kv head, token, head) order: a thread is a row, a warp every
+// eighth of its 16-byte pieces; the rows leave through shared memory.
 template <int D>
-cudaError_t launch(const xp_cache* c, const xp_attn_args& g, unsigned grid, cudaStream_t s) {
-  const size_t smem = Cfg<D>::SMEM + sizeof(Bars) + 1024;
+__global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args g, int ctas) {
+  constexpr int kPer = D / 32;   // 16-byte pieces a thread
+  __shared__ __align__(16) uint2 s_out[32][D / 4 + 2];   // rows 16 bytes apart in the banks
+  __shared__ bf16* s_to[32];
+  ptx::pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per_seq = g.a.T * g.group;
+  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads, e = (int64_t)blockIdx.x * 32 + lane;
+  bf16* to = nullptr;
+  if (e < rows) {
+    const int i = (int)(e % per_seq), hk = (int)(e / per_seq % g.kv_heads);
+    const int n = (int)(e / per_seq / g.kv_heads), t = i / g.group, h = hk * g.group + i % g.group;
+    const long long chunk = g.line[0];
+    float m = -INFINITY, l = 0.0f;
+    float4 o[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto take = [&](int64_t block, int r) {
+      const float2 st = __ldcg((const float2*)g.stat + block * 32 + r);
+      if (!(st.y > 0.0f)) return;   // no visible key in this piece
+      float4 x[kPer];
+#pragma unroll
+      for (int c = 0; c < kPer; ++c)
+        x[c] = __ldcs((const float4*)g.acc + (block * (D / 4) + warp + 8 * c) * 32 + r);
+      const float now = fmaxf(m, st.x), a = exp2f(m - now), b = exp2f(st.x - now);
+      m = now;
+      l = l * a + st.y * b;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c)
+        o[c] = make_float4(o[c].x * a + x[c].x * b, o[c].y * a + x[c].y * b, o[c].z * a + x[c].z * b,
+                           o[c].w * a + x[c].w * b);
+    };
+    for (int kind = 0; kind < 2; ++kind) {
+      if (kind == 1 && g.a.max_len <= 0) break;
+      const Line ln(kind ? g.plan.tail_tiles : g.plan.prefix_tiles,
+                    kind ? tail_len(g, n, false) : g.a.prefix_len);
+      if (ln.T == 0) continue;
+      const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / kRows, p = tile / 2;
+      const long long at = (kind ? g.line[1 + n] : 0) + hk * ln.head() + p * ln.unit(0), cost = ln.unit(p);
+      take(block_of(g, kind, n, hk) + at_row / 32, at_row % 32);
+      for (long long c = at / chunk + 1; c < ctas && c * chunk < at + cost; ++c) {
+        const int t0 = ln.tile_at(p, c * chunk - at), t1 = ln.tile_at(p, min((c + 1) * chunk - at, cost));
+        if (t0 == 0 || t0 >= t1) continue;
+        take(blocks_of(g) + c * 8 + (p < ln.pairs ? tile % 2 * 4 : 0) + at_row % kRows / 32, at_row % 32);
+      }
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+      s_out[lane][warp + 8 * c] = make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv),
+                                             pack_bf16(o[c].z * inv, o[c].w * inv));
+    to = (bf16*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h;
+    if (warp == 0 && g.lse)
+      g.lse[((int64_t)n * g.a.T + t) * g.a.heads + h] =
+          l > 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+  }
+  if (warp == 0) s_to[lane] = to;
+  __syncthreads();
+  for (int x = threadIdx.x; x < 32 * (D / 8); x += 256) {
+    const int r = x / (D / 8), c = x % (D / 8);
+    bf16* p = s_to[r];
+    if (!p) continue;
+    const uint4 v = *(const uint4*)&s_out[r][2 * c];
+    if (((uintptr_t)p & 15) == 0) {
+      *(uint4*)(p + c * 8) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ((uint16_t*)p)[c * 8 + k] = (uint16_t)(w[k / 2] >> (k % 2 * 16));
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
+  const size_t smem = Cfg<D>::SMEM + sizeof(Bars);
   static unsigned long long allowed = 0;
-  const cudaError_t e = xp_allow_smem((const void*)attn_tc_kernel<D>, smem, &allowed);
+  cudaError_t e = xp_allow_smem((const void*)attn_tc_kernel<D>, smem, &allowed);
   if (e != cudaSuccess) return e;
   const bool wide = ((uintptr_t)g.q | (uint64_t)g.a.q_stride_n * 2 | (uint64_t)g.a.q_stride_t * 2 |
                      (uint64_t)g.a.q_stride_h * 2) % 16 == 0;
-  attn_tc_kernel<D><<<grid, kThreads, smem, s>>>(c->tm_k, c->tm_v, g, c->attn_tc, wide);
-  return cudaGetLastError();
+  attn_tc_kernel<D><<<c->num_sms, kThreads, smem, s>>>(c->tm_k, c->tm_v, g, c->attn_tc, wide);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
+  return xp_launch_pdl(attn_tc_combine_kernel<D>, dim3((unsigned)((rows + 31) / 32)), dim3(256), 0, s, g,
+                       c->num_sms);
 }
 
 }  // namespace
@@ -577,34 +850,25 @@ int xp_attn_tc_maps(xp_cache* c) {
   return box;
 }
 
+// Row tiles only: where the work is cut is found on the device, from the lengths.
 xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
   xp_attn_plan p = {};
-  const int group = a->heads / c->d.kv_heads, per_seq = a->T * group;
+  const int per_seq = a->T * (a->heads / c->d.kv_heads);
   p.rows_tile = kRows;
   p.prefix_tiles = (int)(((int64_t)a->N * per_seq + kRows - 1) / kRows);
   p.tail_tiles = (per_seq + kRows - 1) / kRows;
-  // ranges of whole key tiles, so that about one CTA an SM has work, of at least two tiles
-  auto splits = [&](int64_t units, int keys, int* range) {
-    if (keys <= 0) return 0;
-    const int tiles = (keys + kTile - 1) / kTile;
-    int64_t s = std::max<int64_t>(1, c->num_sms / std::max<int64_t>(1, units));
-    s = std::min<int64_t>(s, std::max(1, tiles / 2));
-    *range = (int)((tiles + s - 1) / s) * kTile;
-    return (keys + *range - 1) / *range;
-  };
-  p.prefix_splits = splits((int64_t)(p.prefix_tiles + 1) / 2 * c->d.kv_heads, a->prefix_len,
-                           &p.prefix_keys);
-  p.tail_splits = splits((int64_t)a->N * ((p.tail_tiles + 1) / 2) * c->d.kv_heads, a->max_len,
-                         &p.tail_keys);
-  p.parts = p.prefix_splits + p.tail_splits;
+  const size_t H = c->d.kv_heads, D = c->d.head_dim;
+  const size_t blocks = H * (((size_t)a->N * per_seq + 31) / 32) + a->N * H * ((per_seq + 31) / 32) +
+                        (size_t)c->num_sms * 8;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
+  p.line_off = take(((size_t)a->N + 1) * 8);
+  p.stat_off = take(blocks * 32 * 8);
+  p.acc_off = take(blocks * 32 * D * 4);
+  p.total = o;
   return p;
 }
 
 cudaError_t xp_launch_attn_tc(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
-  const xp_attn_plan& p = g.plan;
-  const unsigned grid = (unsigned)(((int64_t)p.prefix_splits * ((p.prefix_tiles + 1) / 2) +
-                                    (int64_t)g.a.N * ((p.tail_tiles + 1) / 2) * p.tail_splits) *
-                                   g.kv_heads);
-  if (grid == 0) return cudaSuccess;
-  return g.dim == 128 ? launch<128>(c, g, grid, s) : launch<64>(c, g, grid, s);
+  return g.dim == 128 ? launch<128>(c, g, s) : launch<64>(c, g, s);
 }

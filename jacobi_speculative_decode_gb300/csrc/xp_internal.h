@@ -225,7 +225,8 @@ struct xp_attn_plan {
   int prefix_tiles, tail_tiles;  // row tiles: over the batch, of one sequence
   int prefix_splits, prefix_keys, tail_splits, tail_keys;
   int parts;
-  size_t stat_off, acc_off, total;   // workspace: (max, sum) pairs, accumulators
+  // workspace: (max, sum) pairs, accumulators; tensor-core form: where each sequence's work begins
+  size_t stat_off, acc_off, line_off, total;
 };
 struct xp_attn_args {
   xp_attn a;
@@ -236,8 +237,9 @@ struct xp_attn_args {
   int64_t ld_table;
   void* out;
   float* lse;
-  float* stat;                   // [parts][N*T*heads][2]
-  float* acc;                    // [parts][N*T*heads][dim]
+  float* stat;                   // CUDA-core form: [parts][N*T*heads][2]
+  float* acc;                    //                 [parts][N*T*heads][dim]
+  long long* line;
   uint32_t* err;
   xp_attn_plan plan;
 };
