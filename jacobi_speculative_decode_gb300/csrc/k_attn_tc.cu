@@ -10,8 +10,9 @@
 // else they are the even and the odd key tiles of one row tile and are joined at the end.
 // O is rescaled only when a row's maximum grew by more than 2^8 since the last time.
 //
-// Warps: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread is a query row), 8 and 9 issue
-// their products, 10 loads K and V by TMA, a box of tokens of one page at a time.
+// Warps: 0-7 and 8-15 the softmax of stream 0 and 1 (a warp is 16 query rows, four lanes a row),
+// 16 and 17 issue their products, 18 loads K and V by TMA, a box of tokens of one page at a
+// time, 19 cuts the work and loads the queries.
 #include <math.h>
 
 #include <algorithm>
@@ -25,9 +26,9 @@ namespace {
 
 constexpr int kRows = 128;      // query rows of a tile (tensor memory lanes)
 constexpr int kTile = 128;      // keys of a tile
-constexpr int kThreads = 384;
-// registers a thread: 384 x 168 at launch, moved from the issuing warpgroup to the softmax ones
-constexpr int kRegsIssue = 56, kRegsSoftmax = 224;
+constexpr int kThreads = 640;
+// registers a thread: 640 x 96 at launch, moved from the issuing warpgroup to the softmax ones
+constexpr int kRegsIssue = 64, kRegsSoftmax = 104;
 constexpr int kChunkBytes = kTile * 128;   // 64 elements of 128 rows, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;   // growth of the maximum (base 2) that P may carry
@@ -239,23 +240,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kFrags; ++s) {
       init(&bars->frag_full[s], 1);
-      init(&bars->frag_empty[s], 11);   // 8 softmax warps, 2 issuing the products, 1 loading
+      init(&bars->frag_empty[s], 19);   // 16 softmax warps, 2 issuing the products, 1 loading
     }
     for (int t = 0; t < 2; ++t) {
       init(&bars->q_full[t], 1);
       init(&bars->q_empty[t], 2);
       init(&bars->s_full[t], 1);
-      init(&bars->p_half[t], 4);
-      init(&bars->p_full[t], 4);
+      init(&bars->p_half[t], 8);
+      init(&bars->p_full[t], 8);
       init(&bars->o_full[t], 1);
     }
-    init(&bars->x_full, 8);
-    init(&bars->x_done, 8);
+    init(&bars->x_full, 16);
+    init(&bars->x_done, 16);
     bars->abort = 0;
     bars->issued[0] = bars->issued[1] = 0;
     ptx::fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == 16) {
     ptx::tmem_alloc(ptx::smem_u32(&bars->tmem_base), kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -277,9 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return w->kind >= 0;
   };
 
-  if (warp >= 8) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 11) {
+    if (warp == 19) {
       // ---- announces the fragments and loads their query tiles.  Two query tiles a shared
       // fragment, one of the two places in turn for the others, so that the next one's queries
       // are there before the present one is done ----
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (ok) announce({-1, 0, 0, 0, 0, 0, 0, 0, 0});
-    } else if (warp == 10) {
+    } else if (warp == 18) {
       // ---- K and V tiles: lane (chunk, box) loads `box` tokens of one page ----
       const uint64_t keep = ptx::policy_evict_last(), stream = ptx::policy_evict_first();
       const int per = kTile / box, chunk_of = lane / per, in_tile = lane % per * box;
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // registers, and a warp a stream, so that one's waits run under the other's products ----
       constexpr uint32_t kS = ptx::idesc_bf16_f32(kRows, kTile);
       constexpr uint32_t kO = ptx::idesc_bf16_f32(kRows, D) | (1u << 16);   // V: head dims contiguous
-      const int t = warp - 8;
+      const int t = warp - 16;
       const uint32_t s_col = uniform(tmem + t * kTile), o_col = uniform(tmem + 2 * kTile + t * D);
       const bool leader = ptx::elect_one();
       int done = 0, other = 0, pos0 = 0, splits = 0, used[2] = {0, 0};   // items of both streams
@@ -527,24 +528,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- softmax: warps 0-3 of stream 0, 4-7 of stream 1; a thread is a query row ----
+    // ---- softmax: a warp is 16 query rows; a thread holds, of two rows 8 apart, every fourth
+    // pair of columns, so that a row's maximum is two shuffles away and its sum needs none ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = warp / 4, r = threadIdx.x - t * 128;
-    const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
+    const int t = warp / 8, quad = lane % 4;
+    const int r0 = warp % 4 * 32 + warp / 4 % 2 * 16 + lane / 4;      // and r0 + 8
+    const uint32_t lanes = (uint32_t)(r0 - lane / 4) << 16;
     const float c = g.a.scale * 1.44269504088896f;
     int done = 0, pos0 = 0, joins = 0;
-    bool unread = false;   // the other group may still read this one's sums
+    bool unread = false;   // the other stream's warps may still read this one's sums
     Frag w;
     bool ok = true;
     for (int f = 0; ok && next_frag(f, &w); ++f) {
       const int T = w.t1 - w.t0, items = w.shared ? 2 * T : T, mine = (items + 1 - t) / 2;
       const int tile = w.shared ? w.tile + t : w.tile;
-      int n, tt, h, limit;
-      const int64_t row = row_of(g, w, tile, r, &n, &tt, &h, &limit);
       const int end = min(w.len, w.t1 * kTile);
-      limit = row < 0 ? end : min(limit, end);   // rows behind the end ask for no mask of their own
-      const bool active = __any_sync(0xFFFFFFFFu, row >= 0);
-      float m = -INFINITY, l = 0.0f;
+      int limit[2];
+      bool any_row = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int n, tt, h;
+        const bool is_row = row_of(g, w, tile, r0 + 8 * i, &n, &tt, &h, &limit[i]) >= 0;
+        limit[i] = is_row ? min(limit[i], end) : end;   // rows behind the end ask for no mask
+        any_row |= is_row;
+      }
+      const bool active = __any_sync(0xFFFFFFFFu, any_row);
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // l: of this thread's columns
       for (int j = 0; j < mine; ++j) {
         ok = wait(&bars->s_full[t], done + j);
         if (!ok) break;
@@ -557,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(&bars->full[st], pos / C::STAGES);
           if (!ok) break;
           uint8_t* v = smem + (2 + st) * C::TILE_BYTES;
-          for (int i = r; i < (kTile - valid) * C::CH * 8; i += 128) {
+          for (int i = threadIdx.x % 256; i < (kTile - valid) * C::CH * 8; i += 256) {
             const int rr = valid + i / (C::CH * 8), seg = i % (C::CH * 8);
             *(uint4*)(v + (seg / 8) * kChunkBytes + rr * 128 + (seg % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -578,101 +587,126 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tc_fence_after();
         const uint32_t scol = tmem + lanes + t * kTile;
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ptx::tmem_ld32(scol + q * 32, s[q]);
+        uint32_t s[2][32];   // [half of the columns][4 x 8 columns: row 0 pair, row 1 pair]
+        ptx::tmem_ld_16x64(scol, s[0]);
+        ptx::tmem_ld_16x64(scol + 64, s[1]);
         ptx::tmem_wait_ld();
-        if (__any_sync(0xFFFFFFFFu, key + kTile > limit)) {
+        if (__any_sync(0xFFFFFFFFu, key + kTile > min(limit[0], limit[1]))) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              if (key + q * 32 + x >= limit) s[q][x] = 0xFF800000u;   // -inf
+              if (key + q * 64 + x / 4 * 8 + quad * 2 + x % 2 >= limit[x / 2 % 2])
+                s[q][x] = 0xFF800000u;   // -inf
         }
-        float top[4];   // four chains, three operands an instruction
+        float now[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          top[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
+        for (int i = 0; i < 2; ++i) {
+          float top[2];   // two chains, three operands an instruction
 #pragma unroll
-          for (int x = 2; x < 32; x += 2)
-            top[q] = fmaxf(fmaxf(top[q], __uint_as_float(s[q][x])), __uint_as_float(s[q][x + 1]));
+          for (int q = 0; q < 2; ++q) {
+            top[q] = fmaxf(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1]));
+#pragma unroll
+            for (int x = 4; x < 32; x += 4)
+              top[q] = fmaxf(fmaxf(top[q], __uint_as_float(s[q][x + 2 * i])),
+                             __uint_as_float(s[q][x + 2 * i + 1]));
+          }
+          now[i] = fmaxf(top[0], top[1]);
         }
-        const float now = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            now[i] = fmaxf(now[i], __shfl_xor_sync(0xFFFFFFFFu, now[i], o));
+        now[0] = fmaxf(now[0], m[0]);
+        now[1] = fmaxf(now[1], m[1]);
         if (j == 0) {
-          m = now;
+          m[0] = now[0];
+          m[1] = now[1];
         } else {
-          const bool grown = (now - m) * c > kLazy;   // from -inf too
-          if (__any_sync(0xFFFFFFFFu, grown)) {
+          const bool grown0 = (now[0] - m[0]) * c > kLazy, grown1 = (now[1] - m[1]) * c > kLazy;
+          if (__any_sync(0xFFFFFFFFu, grown0 || grown1)) {   // from -inf too
             ok = wait(&bars->o_full[t], done + j - 1);
             if (!ok) break;
             ptx::tc_fence_after();
-            const float f = grown ? ex2((m - now) * c) : 1.0f;
+            const float f0 = grown0 ? ex2((m[0] - now[0]) * c) : 1.0f;
+            const float f1 = grown1 ? ex2((m[1] - now[1]) * c) : 1.0f;
             const uint32_t ocol = tmem + lanes + 2 * kTile + t * D;
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
               uint32_t o[16];
-              ptx::tmem_ld16(ocol + q * 16, o);
+              ptx::tmem_ld_16x32(ocol + q * 32, o);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              ptx::tmem_st16(ocol + q * 16, o);
+              for (int x = 0; x < 16; ++x)
+                o[x] = __float_as_uint(__uint_as_float(o[x]) * (x & 2 ? f1 : f0));
+              ptx::tmem_st_16x32(ocol + q * 32, o);
             }
             ptx::tmem_wait_st();
-            l *= f;
-            if (grown) m = now;
+            l[0] *= f0;
+            l[1] *= f1;
+            if (grown0) m[0] = now[0];
+            if (grown1) m[1] = now[1];
           }
         }
-        const float base = m == -INFINITY ? 0.0f : m * c;
-        const uint64_t c2 = pair(c, c), nb2 = pair(-base, -base);
-        uint64_t sum[4] = {0, 0, 0, 0};
+        const float b0 = m[0] == -INFINITY ? 0.0f : m[0] * c, b1 = m[1] == -INFINITY ? 0.0f : m[1] * c;
+        const uint64_t c2 = pair(c, c), nb[2] = {pair(-b0, -b0), pair(-b1, -b1)};
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t pk[16];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2, nb2);
+          for (int x = 0; x < 16; ++x) {   // row x % 2, columns 8 (x / 2) + 2 quad
+            const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2, nb[x % 2]);
             const float a = ex2(low(z)), b = ex2(high(z));
-            sum[x % 4] = add2(sum[x % 4], pair(a, b));
+            sum[x % 2] = add2(sum[x % 2], pair(a, b));
             pk[x] = pack_bf16(a, b);
           }
-          ptx::tmem_st16(scol + q * 16, pk);
-          if (q & 1) {   // the product may start on the first half of the keys
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              ptx::mbar_arrive(ptx::smem_u32(q == 1 ? &bars->p_half[t] : &bars->p_full[t]));
-            }
-          }
+          ptx::tmem_st_16x32_narrow(scol + q * 32, pk);
+          // the product may start on the first half of the keys
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(q == 0 ? &bars->p_half[t] : &bars->p_full[t]));
         }
-        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l += low(sum[0]) + high(sum[0]);
+        l[0] += low(sum[0]) + high(sum[0]);
+        l[1] += low(sum[1]) + high(sum[1]);
       }
       done += mine;
       pos0 += 2 * T;
       if (mine > 0 && ok) ok = wait(&bars->o_full[t], done - 1);
       if (!ok) break;
       ptx::tc_fence_after();
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
       // a row's keys are the whole range (shared) or every second tile: join the two streams
-      float f0 = 1.0f, f1 = 0.0f, mm = m, ll = l;
+      float f0[2] = {1.0f, 1.0f}, f1[2] = {0.0f, 0.0f};
       if (!w.shared) {
-        if (unread) {   // no item of this stream: the other group may still read the statistics
+        if (unread) {   // no item of this stream: the other's warps may still read the statistics
           ok = wait(&bars->x_done, joins - 1);
           if (!ok) break;
           unread = false;
         }
-        bars->stat[t][r] = make_float2(m, mine > 0 ? l : 0.0f);
+        if (quad == 0)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            bars->stat[t][r0 + 8 * i] = make_float2(m[i], mine > 0 ? l[i] : 0.0f);
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->x_full));
         ok = wait(&bars->x_full, joins);
         if (!ok) break;
         ptx::tc_fence_after();
-        const float2 a = bars->stat[0][r], b = bars->stat[1][r];
-        mm = fmaxf(a.y > 0.0f ? a.x : -INFINITY, b.y > 0.0f ? b.x : -INFINITY);
-        f0 = a.y > 0.0f ? ex2((a.x - mm) * c) : 0.0f;
-        f1 = b.y > 0.0f ? ex2((b.x - mm) * c) : 0.0f;
-        ll = f0 * a.y + f1 * b.y;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 a = bars->stat[0][r0 + 8 * i], b = bars->stat[1][r0 + 8 * i];
+          m[i] = fmaxf(a.y > 0.0f ? a.x : -INFINITY, b.y > 0.0f ? b.x : -INFINITY);
+          f0[i] = a.y > 0.0f ? ex2((a.x - m[i]) * c) : 0.0f;
+          f1[i] = b.y > 0.0f ? ex2((b.x - m[i]) * c) : 0.0f;
+          l[i] = f0[i] * a.y + f1[i] * b.y;
+        }
       }
       // each stream writes its rows, or (joined) its half of the head dims
       if (active) {
@@ -680,27 +714,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t block = (w.slot < 0 ? block_of(g, w.kind, w.n, w.hk) + tile * 4
                                           : blocks_of(g) + w.slot * 8 + (w.shared ? t * 4 : 0)) +
                               warp % 4;
-        if (w.shared || t == 0)
-          ((float2*)g.stat)[block * 32 + lane] = make_float2(ll > 0.0f ? mm * c : -INFINITY, ll);
-        float4* acc = (float4*)g.acc + block * (D / 4) * 32 + lane;
+        const int rb = r0 % 32;   // in the block, and rb + 8
+        if (quad == 0 && (w.shared || t == 0))
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            ((float2*)g.stat)[block * 32 + rb + 8 * i] =
+                make_float2(l[i] > 0.0f ? m[i] * c : -INFINITY, l[i]);
+        float* acc = g.acc + block * D * 32 + (quad / 2 * 32 + rb) * 4 + quad % 2 * 2;
         for (int q = q0; q < q1; ++q) {
-          uint32_t o[32];
-          ptx::tmem_ld32(tmem + lanes + 2 * kTile + (w.shared ? t * D : 0) + q * 32, o);
+          uint32_t o[16];
+          ptx::tmem_ld_16x32(tmem + lanes + 2 * kTile + (w.shared ? t * D : 0) + q * 32, o);
           if (w.shared || items == 1) {
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f0);
+            for (int x = 0; x < 16; ++x)
+              o[x] = __float_as_uint(__uint_as_float(o[x]) * f0[x / 2 % 2]);
           } else {
-            uint32_t b[32];
-            ptx::tmem_ld32(tmem + lanes + 2 * kTile + D + q * 32, b);
+            uint32_t b[16];
+            ptx::tmem_ld_16x32(tmem + lanes + 2 * kTile + D + q * 32, b);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              o[x] = __float_as_uint(__uint_as_float(o[x]) * f0 + __uint_as_float(b[x]) * f1);
+            for (int x = 0; x < 16; ++x)
+              o[x] = __float_as_uint(__uint_as_float(o[x]) * f0[x / 2 % 2] +
+                                     __uint_as_float(b[x]) * f1[x / 2 % 2]);
           }
 #pragma unroll
-          for (int x = 0; x < 32; x += 4)   // a row's 16 bytes beside the next row's
-            *(uint4*)&acc[(q * 8 + x / 4) * 32] = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+          for (int k = 0; k < 4; ++k)   // 8 columns: two pieces of 16 bytes a row
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              *(uint2*)&acc[((q * 4 + k) * 2 * 32 + 8 * i) * 4] =
+                  make_uint2(o[4 * k + 2 * i], o[4 * k + 2 * i + 1]);
         }
       }
       if (!w.shared) {
@@ -714,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
