@@ -59,6 +59,7 @@ struct Bars {
   uint64_t frag_full[kFrags], frag_empty[kFrags];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
   uint64_t x_full, x_done;       // both softmax groups: statistics exchanged, sums read
+  uint64_t drained;              // both streams' products have all run
   Frag frag[kFrags];
   float2 stat[2][kRows];
   long long total[kThreads / 32], start_base;   // start: where this CTA's share begins
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       init(&bars->o_full[t], 1);
     }
     init(&bars->x_full, 16);
+    init(&bars->drained, 2);
     init(&bars->x_done, 16);
     bars->abort = 0;
     bars->issued[0] = bars->issued[1] = 0;
@@ -433,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t s_col = uniform(tmem + t * kTile), o_col = uniform(tmem + 2 * kTile + t * D);
       const bool leader = ptx::elect_one();
       int done = 0, other = 0, pos0 = 0, splits = 0, used[2] = {0, 0};   // items of both streams
+      int seen = 0;   // loads this warp has seen land
       // The streams take turns: were both to issue together, their products would end together,
       // and neither's would run under the other's exponentials.  A pause, nothing more: it
       // ends by itself, and no result depends on it.
@@ -441,27 +444,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int spin = 0; spin < 100 && *(volatile int*)&bars->issued[1 - t] < want; ++spin) {}
         __syncwarp();
       };
-      auto loaded = [&](int pos) { return wait(&bars->full[pos % C::STAGES], pos / C::STAGES); };
       Frag w;
       bool ok = true;
       for (int f = 0; ok && next_frag(f, &w); ++f) {
         const int T = w.t1 - w.t0, items = w.shared ? 2 * T : T, mine = (items + 1 - t) / 2;
-        const int place = w.shared ? t : splits & 1;
+        const int place = w.shared ? t : splits & 1, end = min(w.len, w.t1 * kTile);
         const uint32_t q = uniform(sq + place * C::TILE_BYTES);
-        if (w.shared) {
-          ++used[0];
-          ++used[1];
-        } else {
-          ++used[place];
-          ++splits;
-        }
         auto kv = [&](int j) { return w.shared ? j : 2 * j + t; };
-        // a tile that both streams read is free when both are done; one's own counts twice
-        auto release = [&](int pos) {
-          const uint32_t bar = ptx::smem_u32(&bars->empty[pos % C::STAGES]);
-          ptx::mma_commit(bar);
-          if (!w.shared) ptx::mma_commit(bar);
+        // An mbarrier tells a phase from the one before it only.  So both warps see every load of
+        // the ring land, in order, their own or not, and a stage is free again when both are
+        // done with it: behind the products that read it, or at once where it is the other
+        // stream's tile.  (The same holds for the places of the queries.)
+        auto see = [&](int off) {
+          for (; seen <= pos0 + off; ++seen) {
+            const int s = seen % C::STAGES, o = seen - pos0;
+            if (!wait(&bars->full[s], seen / C::STAGES)) return false;
+            const int tile = o == 0 ? 0 : o == 2 * T - 1 ? T - 1 : o & 1 ? (o + 1) / 2 : o / 2 - 1;
+            if (!w.shared && (tile & 1) != t && lane == 0)
+              ptx::mbar_arrive(ptx::smem_u32(&bars->empty[s]));
+          }
+          return true;
         };
+        auto release = [&](int pos) { ptx::mma_commit(ptx::smem_u32(&bars->empty[pos % C::STAGES])); };
         auto scores = [&](int j) {
           const int pos = pos0 + pos_k(kv(j));
           const uint32_t k = uniform(ring + pos % C::STAGES * C::TILE_BYTES);
@@ -473,34 +477,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ptx::mma_commit(ptx::smem_u32(&bars->s_full[t]));
             release(pos);
-            if (j == mine - 1) {   // the queries are read
-              ptx::mma_commit(ptx::smem_u32(&bars->q_empty[place]));
-              if (w.shared) ptx::mma_commit(ptx::smem_u32(&bars->q_empty[place]));
-            }
+            if (j == mine - 1) ptx::mma_commit(ptx::smem_u32(&bars->q_empty[place]));   // all read
           }
           __syncwarp();
         };
-        // waited for also where this stream has no item: its arrival must not count for the
-        // queries that were there before
-        ok = wait(&bars->q_full[place], used[place] - 1);
-        if (!ok) break;
-        if (mine == 0) {
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->q_empty[place]));
-        } else {
-          ok = loaded(pos0 + pos_k(kv(0)));
-          if (ok) {
-            ptx::tc_fence_after();
-            scores(0);
-          }
+        for (int p = 0; p < 2 && ok; ++p) {
+          if (!w.shared && p != place) continue;
+          ok = wait(&bars->q_full[p], used[p]++);
+          if (ok && (p != place || mine == 0) && lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->q_empty[p]));
         }
-        for (int j = 0; j < mine && ok; ++j) {
-          const int pv = pos0 + pos_v(kv(j), T);
-          const uint32_t v = uniform(ring + pv % C::STAGES * C::TILE_BYTES);
-          // the tiles are there before the weights are
-          ok = loaded(pv) && (j + 1 >= mine || loaded(pos0 + pos_k(kv(j + 1))));
-          ok = ok && wait(&bars->p_half[t], done + j);
+        splits += !w.shared;
+        if (ok && mine > 0) {
+          ok = see(pos_k(kv(0)));
           if (!ok) break;
           ptx::tc_fence_after();
+          scores(0);
+        }
+        for (int j = 0; j < mine && ok; ++j) {
+          const int pv = pos0 + pos_v(kv(j), T), valid = end - (w.t0 + kv(j)) * kTile;
+          // the tiles are there before the weights are
+          ok = see(pv - pos0) && (j + 1 >= mine || see(pos_k(kv(j + 1))));
+          if (!ok) break;
+          // V rows behind the range may hold anything: cleared before the product reads them
+          // (streams that share the tile both write the zeros)
+          if (valid < kTile) {
+            uint8_t* rows = smem + (2 + pv % C::STAGES) * C::TILE_BYTES;
+            for (int i = lane; i < (kTile - valid) * C::CH * 8; i += 32) {
+              const int rr = valid + i / (C::CH * 8), seg = i % (C::CH * 8);
+              *(uint4*)(rows + (seg / 8) * kChunkBytes + rr * 128 + (seg % 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          ok = wait(&bars->p_half[t], done + j);
+          if (!ok) break;
+          turn(j, items - mine);
+          ptx::tc_fence_after();
+          const uint32_t v = uniform(ring + pv % C::STAGES * C::TILE_BYTES);
           if (leader) {
 #pragma unroll
             for (int ks = 0; ks < kTile / 32; ++ks)
@@ -509,7 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           ok = wait(&bars->p_full[t], done + j);
           if (!ok) break;
-          turn(j, items - mine);
           ptx::tc_fence_after();
           if (leader) {
 #pragma unroll
@@ -522,10 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 < mine) scores(j + 1);
           if (leader) *(volatile int*)&bars->issued[t] = done + j + 1;
         }
+        ok = ok && see(2 * T - 1);
         done += mine;
         other += items - mine;
         pos0 += 2 * T;
       }
+      // whatever ended the loop, tensor memory is freed behind the last product only
+      if (leader) ptx::mma_commit(ptx::smem_u32(&bars->drained));
     }
   } else {
     // ---- softmax: a warp is 16 query rows; a thread holds, of two rows 8 apart, every fourth
@@ -535,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = warp % 4 * 32 + warp / 4 % 2 * 16 + lane / 4;      // and r0 + 8
     const uint32_t lanes = (uint32_t)(r0 - lane / 4) << 16;
     const float c = g.a.scale * 1.44269504088896f;
-    int done = 0, pos0 = 0, joins = 0;
+    int done = 0, joins = 0;
     bool unread = false;   // the other stream's warps may still read this one's sums
     Frag w;
     bool ok = true;
@@ -558,20 +574,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(&bars->s_full[t], done + j);
         if (!ok) break;
         const int kt = w.shared ? j : 2 * j + t, key = (w.t0 + kt) * kTile;
-        // V rows behind the range may hold anything: cleared before this stream's product reads
-        // them (streams that share the tile both write the zeros)
-        const int valid = end - key;
-        if (valid < kTile) {
-          const int pos = pos0 + pos_v(kt, T), st = pos % C::STAGES;
-          ok = wait(&bars->full[st], pos / C::STAGES);
-          if (!ok) break;
-          uint8_t* v = smem + (2 + st) * C::TILE_BYTES;
-          for (int i = threadIdx.x % 256; i < (kTile - valid) * C::CH * 8; i += 256) {
-            const int rr = valid + i / (C::CH * 8), seg = i % (C::CH * 8);
-            *(uint4*)(v + (seg / 8) * kChunkBytes + rr * 128 + (seg % 8) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         if (j == 0 && unread) {
           ok = wait(&bars->x_done, joins - 1);
           if (!ok) break;
@@ -668,12 +670,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(q == 0 ? &bars->p_half[t] : &bars->p_full[t]));
+          __syncwarp();
         }
         l[0] += low(sum[0]) + high(sum[0]);
         l[1] += low(sum[1]) + high(sum[1]);
       }
       done += mine;
-      pos0 += 2 * T;
       if (mine > 0 && ok) ok = wait(&bars->o_full[t], done - 1);
       if (!ok) break;
       ptx::tc_fence_after();
@@ -720,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 2; ++i)
             ((float2*)g.stat)[block * 32 + rb + 8 * i] =
                 make_float2(l[i] > 0.0f ? m[i] * c : -INFINITY, l[i]);
+        __syncwarp();
         float* acc = g.acc + block * D * 32 + (quad / 2 * 32 + rb) * 4 + quad % 2 * 2;
         for (int q = q0; q < q1; ++q) {
           uint32_t o[16];
@@ -758,6 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 16) {
+    volatile int no_abort = 0;
+    ptx::mbar_wait(ptx::smem_u32(&bars->drained), 0, &no_abort, g.err);
     __syncwarp();
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
