@@ -7,7 +7,7 @@
 // The streams alternate on the tensor core, so one stream's products run under the other's
 // exponentials.  Where a row tile has a neighbour with the same keys (the prefix, and blocks
 // of more than 128 rows) the two streams are two row tiles and share every K and V tile;
-// else they are the even and the odd key tiles of one row tile and are joined at the end.
+// else they are the even and the odd key tiles of one row tile, each with a result of its own.
 // O is rescaled only when a row's maximum grew by more than 2^8 since the last time.
 //
 // Warps: 0-7 and 8-15 the softmax of stream 0 and 1 (a warp is 16 query rows, four lanes a row),
@@ -42,8 +42,9 @@ struct Cfg {
 };
 
 constexpr int kFrags = 4;       // fragments announced ahead
-constexpr int kUnitCost = 3;    // what a unit costs besides its tiles, in tiles of one stream
-constexpr int kMinChunk = 5;    // least cost a CTA is given
+// cost of a key tile for two row tiles, for one, and of a unit besides its tiles (ns / 180)
+constexpr int kPairCost = 8, kTileCost = 5, kUnitCost = 8;
+constexpr int kMinChunk = 18;   // least cost a CTA is given
 
 struct Frag {
   int kind;              // 0 prefix, 1 tail, -1 no more
@@ -58,10 +59,8 @@ struct Bars {
   uint64_t full[10], empty[10];
   uint64_t frag_full[kFrags], frag_empty[kFrags];
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
-  uint64_t x_full, x_done;       // both softmax groups: statistics exchanged, sums read
   uint64_t drained;              // both streams' products have all run
   Frag frag[kFrags];
-  float2 stat[2][kRows];
   long long total[kThreads / 32], start_base;   // start: where this CTA's share begins
   int start_n;
   uint32_t tmem_base;
@@ -70,8 +69,7 @@ struct Bars {
 };
 
 // The work is one line of cost: prefix units (kv head, pair of row tiles), then the units of
-// each sequence's tail, a unit costing kUnitCost and 2 (two streams on each tile) or 1 a key
-// tile.  CTA i does [i*chunk, (i+1)*chunk) of it, so that a unit may be cut anywhere between
+// each sequence's tail, a unit costing kUnitCost and kPairCost or kTileCost a key tile.  CTA i does [i*chunk, (i+1)*chunk) of it, so that a unit may be cut anywhere between
 // two of its tiles and every CTA gets the same.  A piece that begins its unit leaves its
 // result in the unit's place, one that does not in the place of its CTA, of which there is
 // at most one.
@@ -79,14 +77,15 @@ struct Line {
   int pairs, odd, T;       // row tiles as pairs and one over; key tiles
   __host__ __device__ Line(int row_tiles, int keys)
       : pairs(row_tiles / 2), odd(row_tiles % 2), T((keys + kTile - 1) / kTile) {}
-  __host__ __device__ long long unit(int p) const { return (p < pairs ? 2 : 1) * (long long)T + kUnitCost; }
+  __host__ __device__ int tile_cost(int p) const { return p < pairs ? kPairCost : kTileCost; }
+  __host__ __device__ long long unit(int p) const { return tile_cost(p) * (long long)T + kUnitCost; }
   // all row tiles of one kv head
   __host__ __device__ long long head() const {
     return T ? pairs * unit(0) + odd * unit(pairs) : 0;
   }
   // first tile of unit p that lies behind a cost of x from the unit's beginning
   __host__ __device__ int tile_at(int p, long long x) const {
-    const int w = p < pairs ? 2 : 1;
+    const int w = tile_cost(p);
     const long long t = (x - kUnitCost + w - 1) / w;
     return x <= kUnitCost ? 0 : t > T ? T : (int)t;
   }
@@ -156,13 +155,21 @@ __device__ __forceinline__ int64_t row_of(const xp_attn_args& g, const Frag& w, 
 }
 
 // Partial results lie in blocks of 32 query rows, [D/4][32 rows][4], so that a warp writes and
-// reads them 512 bytes at a time: the prefix's by kv head, then each sequence's by kv head,
-// then 8 blocks for every CTA's piece that does not begin its unit.
+// reads them 512 bytes at a time: the prefix's by kv head, each sequence's by kv head, the same
+// again for stream 1 of the one row tile of each that both streams work on, then 8 blocks for
+// every CTA's piece that does not begin its unit.
+__device__ __forceinline__ int64_t per_seq_of(const xp_attn_args& g) { return g.a.T * g.group; }
 __device__ __forceinline__ int64_t block_of(const xp_attn_args& g, int kind, int n, int hk) {
-  const int64_t per_seq = g.a.T * g.group, all = (g.a.N * per_seq + 31) / 32;
-  return kind == 0 ? hk * all : g.kv_heads * all + ((int64_t)n * g.kv_heads + hk) * ((per_seq + 31) / 32);
+  const int64_t all = (g.a.N * per_seq_of(g) + 31) / 32, one = (per_seq_of(g) + 31) / 32;
+  return kind == 0 ? hk * all : g.kv_heads * all + ((int64_t)n * g.kv_heads + hk) * one;
 }
-__device__ __forceinline__ int64_t blocks_of(const xp_attn_args& g) { return block_of(g, 1, g.a.N, 0); }
+__device__ __forceinline__ int64_t second_block_of(const xp_attn_args& g, int kind, int n, int hk) {
+  const int64_t one = min((per_seq_of(g) + 31) / 32, (int64_t)4);
+  return block_of(g, 1, g.a.N, 0) + (kind == 0 ? hk * 4 : g.kv_heads * 4 + ((int64_t)n * g.kv_heads + hk) * one);
+}
+__device__ __forceinline__ int64_t cut_block(const xp_attn_args& g, long long cta, int half) {
+  return second_block_of(g, 1, g.a.N, 0) + cta * 8 + half * 4;
+}
 
 __device__ __forceinline__ int tail_len(const xp_attn_args& g, int n, bool tell) {
   int len = g.lens[n];
@@ -218,7 +225,7 @@ __device__ long long plan_line(const xp_attn_args& g, Bars* bars) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const xp_attn_args g, int box, bool q_wide) {
+                   const __grid_constant__ CUtensorMap tm_q, const xp_attn_args g, int box, bool q_tma) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + C::SMEM);
@@ -251,9 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       init(&bars->p_full[t], 8);
       init(&bars->o_full[t], 1);
     }
-    init(&bars->x_full, 16);
     init(&bars->drained, 2);
-    init(&bars->x_done, 16);
     bars->abort = 0;
     bars->issued[0] = bars->issued[1] = 0;
     ptx::fence_barrier_init();
@@ -290,30 +295,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Line pre(g.plan.prefix_tiles, g.a.prefix_len);
       const long long before = pre.head() * g.kv_heads;
       const int N = g.a.max_len > 0 ? g.a.N : 0;
+      const uint64_t once = ptx::policy_evict_first();
       int f = 0, splits = 0, used[2] = {0, 0};
       bool ok = true;
       auto load_q = [&](const Frag& w, int tile, int place) {
         if (!wait(&bars->q_empty[place], (used[place] & 1) ^ 1)) return false;
         ++used[place];
         uint8_t* dst = smem + place * C::TILE_BYTES;
+        if (q_tma) {   // 128 / group tokens of all the group's heads
+          if (lane == 0) {
+            const uint32_t bar = ptx::smem_u32(&bars->q_full[place]);
+            const int token = (w.kind == 0 ? 0 : w.n * g.a.T) + tile * (kRows / g.group);
+            ptx::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+            for (int ch = 0; ch < C::CH; ++ch)
+              ptx::tma_load_4d(ptx::smem_u32(dst + ch * kChunkBytes), &tm_q, bar, ch * 64, 0, w.hk, token,
+                               once);
+          }
+          __syncwarp();
+          return true;
+        }
         for (int r = lane; r < kRows; r += 32) {
           int n, t, h, lim;
           if (row_of(g, w, tile, r, &n, &t, &h, &lim) < 0) break;   // rows behind the end: anything
-          const bf16* src = (const bf16*)g.q + n * g.a.q_stride_n + t * g.a.q_stride_t +
-                            h * g.a.q_stride_h;
+          const uint16_t* src = (const uint16_t*)g.q + n * g.a.q_stride_n + t * g.a.q_stride_t +
+                                h * g.a.q_stride_h;
           for (int seg = 0; seg < D / 8; ++seg) {
-            uint8_t* to = dst + (seg / 8) * kChunkBytes + r * 128 + (((seg % 8) ^ (r & 7)) << 4);
-            if (q_wide) {
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(to)),
-                           "l"(__cvta_generic_to_global(src + seg * 8))
-                           : "memory");
-            } else {
+            uint16_t* to = (uint16_t*)(dst + (seg / 8) * kChunkBytes + r * 128 + (((seg % 8) ^ (r & 7)) << 4));
 #pragma unroll
-              for (int e = 0; e < 8; ++e) ((uint16_t*)to)[e] = ((const uint16_t*)src)[seg * 8 + e];
-            }
+            for (int e = 0; e < 8; ++e) to[e] = src[seg * 8 + e];
           }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->q_full[place]));
@@ -370,6 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (ok) announce({-1, 0, 0, 0, 0, 0, 0, 0, 0});
+      volatile int no_abort = 0;   // as with K and V below
+      for (int p = 0; p < 2; ++p)
+        if (used[p]) ptx::mbar_wait(ptx::smem_u32(&bars->q_full[p]), (used[p] - 1) & 1, &no_abort, g.err);
     } else if (warp == 18) {
       // ---- K and V tiles: lane (chunk, box) loads `box` tokens of one page ----
       const uint64_t keep = ptx::policy_evict_last(), stream = ptx::policy_evict_first();
@@ -551,8 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = warp % 4 * 32 + warp / 4 % 2 * 16 + lane / 4;      // and r0 + 8
     const uint32_t lanes = (uint32_t)(r0 - lane / 4) << 16;
     const float c = g.a.scale * 1.44269504088896f;
-    int done = 0, joins = 0;
-    bool unread = false;   // the other stream's warps may still read this one's sums
+    int done = 0;
     Frag w;
     bool ok = true;
     for (int f = 0; ok && next_frag(f, &w); ++f) {
@@ -574,11 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(&bars->s_full[t], done + j);
         if (!ok) break;
         const int kt = w.shared ? j : 2 * j + t, key = (w.t0 + kt) * kTile;
-        if (j == 0 && unread) {
-          ok = wait(&bars->x_done, joins - 1);
-          if (!ok) break;
-          unread = false;
-        }
         if (!active) {   // no rows here: only the hand-over
           __syncwarp();
           if (lane == 0) {
@@ -676,86 +684,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[1] += low(sum[1]) + high(sum[1]);
       }
       done += mine;
-      if (mine > 0 && ok) ok = wait(&bars->o_full[t], done - 1);
+      if (!ok) break;
+      if (mine == 0 || !active) continue;
+      ok = wait(&bars->o_full[t], done - 1);
       if (!ok) break;
       ptx::tc_fence_after();
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
-      // a row's keys are the whole range (shared) or every second tile: join the two streams
-      float f0[2] = {1.0f, 1.0f}, f1[2] = {0.0f, 0.0f};
-      if (!w.shared) {
-        if (unread) {   // no item of this stream: the other's warps may still read the statistics
-          ok = wait(&bars->x_done, joins - 1);
-          if (!ok) break;
-          unread = false;
-        }
-        if (quad == 0)
+      const int64_t block =
+          (w.slot >= 0            ? cut_block(g, w.slot, t)
+           : !w.shared && t == 1 ? second_block_of(g, w.kind, w.n, w.hk)
+                                 : block_of(g, w.kind, w.n, w.hk) + tile * 4) +
+          warp % 4;
+      const int rb = r0 % 32;   // in the block, and rb + 8
+      if (quad == 0)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          ((float2*)g.stat)[block * 32 + rb + 8 * i] =
+              make_float2(l[i] > 0.0f ? m[i] * c : -INFINITY, l[i]);
+      __syncwarp();
+      float* acc = g.acc + block * D * 32 + (quad / 2 * 32 + rb) * 4 + quad % 2 * 2;
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {
+        uint32_t o[32];
+        ptx::tmem_ld_16x64(tmem + lanes + 2 * kTile + t * D + q * 64, o);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)   // 8 columns: two pieces of 16 bytes a row
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            bars->stat[t][r0 + 8 * i] = make_float2(m[i], mine > 0 ? l[i] : 0.0f);
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->x_full));
-        ok = wait(&bars->x_full, joins);
-        if (!ok) break;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 a = bars->stat[0][r0 + 8 * i], b = bars->stat[1][r0 + 8 * i];
-          m[i] = fmaxf(a.y > 0.0f ? a.x : -INFINITY, b.y > 0.0f ? b.x : -INFINITY);
-          f0[i] = a.y > 0.0f ? ex2((a.x - m[i]) * c) : 0.0f;
-          f1[i] = b.y > 0.0f ? ex2((b.x - m[i]) * c) : 0.0f;
-          l[i] = f0[i] * a.y + f1[i] * b.y;
-        }
+            *(uint2*)&acc[((q * 8 + k) * 2 * 32 + 8 * i) * 4] =
+                make_uint2(o[4 * k + 2 * i], o[4 * k + 2 * i + 1]);
       }
-      // each stream writes its rows, or (joined) its half of the head dims
-      if (active) {
-        const int q0 = w.shared ? 0 : t * (D / 64), q1 = w.shared ? D / 32 : q0 + D / 64;
-        const int64_t block = (w.slot < 0 ? block_of(g, w.kind, w.n, w.hk) + tile * 4
-                                          : blocks_of(g) + w.slot * 8 + (w.shared ? t * 4 : 0)) +
-                              warp % 4;
-        const int rb = r0 % 32;   // in the block, and rb + 8
-        if (quad == 0 && (w.shared || t == 0))
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            ((float2*)g.stat)[block * 32 + rb + 8 * i] =
-                make_float2(l[i] > 0.0f ? m[i] * c : -INFINITY, l[i]);
-        __syncwarp();
-        float* acc = g.acc + block * D * 32 + (quad / 2 * 32 + rb) * 4 + quad % 2 * 2;
-        for (int q = q0; q < q1; ++q) {
-          uint32_t o[16];
-          ptx::tmem_ld_16x32(tmem + lanes + 2 * kTile + (w.shared ? t * D : 0) + q * 32, o);
-          if (w.shared || items == 1) {
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-              o[x] = __float_as_uint(__uint_as_float(o[x]) * f0[x / 2 % 2]);
-          } else {
-            uint32_t b[16];
-            ptx::tmem_ld_16x32(tmem + lanes + 2 * kTile + D + q * 32, b);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-              o[x] = __float_as_uint(__uint_as_float(o[x]) * f0[x / 2 % 2] +
-                                     __uint_as_float(b[x]) * f1[x / 2 % 2]);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)   // 8 columns: two pieces of 16 bytes a row
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              *(uint2*)&acc[((q * 4 + k) * 2 * 32 + 8 * i) * 4] =
-                  make_uint2(o[4 * k + 2 * i], o[4 * k + 2 * i + 1]);
-        }
-      }
-      if (!w.shared) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->x_done));
-        ++joins;
-        unread = true;
-      }
+      ptx::tc_fence_before();
     }
   }
   ptx::tc_fence_before();
@@ -813,11 +776,20 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args
       if (ln.T == 0) continue;
       const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / kRows, p = tile / 2;
       const long long at = (kind ? g.line[1 + n] : 0) + hk * ln.head() + p * ln.unit(0), cost = ln.unit(p);
-      take(block_of(g, kind, n, hk) + at_row / 32, at_row % 32);
+      // a piece of two row tiles has a half of each, one of a single row tile a half of each
+      // stream (the second from two key tiles on)
+      const bool shared = p < ln.pairs;
+      const int in_tile = at_row % kRows / 32, r = at_row % 32;
+      long long cut = (at / chunk + 1) * chunk - at;   // where the unit is first cut,
+      if (ln.tile_at(p, cut) == 0) cut += chunk;       // behind its first tile
+      const int first = ln.tile_at(p, min(cut, cost));
+      if (first > 0) take(block_of(g, kind, n, hk) + at_row / 32, r);
+      if (first > 1 && !shared) take(second_block_of(g, kind, n, hk) + in_tile, r);
       for (long long c = at / chunk + 1; c < ctas && c * chunk < at + cost; ++c) {
         const int t0 = ln.tile_at(p, c * chunk - at), t1 = ln.tile_at(p, min((c + 1) * chunk - at, cost));
         if (t0 == 0 || t0 >= t1) continue;
-        take(blocks_of(g) + c * 8 + (p < ln.pairs ? tile % 2 * 4 : 0) + at_row % kRows / 32, at_row % 32);
+        take(cut_block(g, c, shared ? tile % 2 : 0) + in_tile, r);
+        if (t1 - t0 > 1 && !shared) take(cut_block(g, c, 1) + in_tile, r);
       }
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -853,9 +825,25 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   static unsigned long long allowed = 0;
   cudaError_t e = xp_allow_smem((const void*)attn_tc_kernel<D>, smem, &allowed);
   if (e != cudaSuccess) return e;
-  const bool wide = ((uintptr_t)g.q | (uint64_t)g.a.q_stride_n * 2 | (uint64_t)g.a.q_stride_t * 2 |
-                     (uint64_t)g.a.q_stride_h * 2) % 16 == 0;
-  attn_tc_kernel<D><<<c->num_sms, kThreads, smem, s>>>(c->tm_k, c->tm_v, g, c->attn_tc, wide);
+  // Queries by TMA where a tile is a whole number of tokens, one stride apart; else by loads.
+  CUtensorMap tm_q = {};
+  const int64_t token = g.a.T > 1 ? g.a.q_stride_t : g.a.q_stride_n;
+  bool q_tma = kRows % g.group == 0 && (g.a.T == 1 || g.a.N == 1 || g.a.q_stride_n == g.a.T * token) &&
+               (uintptr_t)g.q % 16 == 0 && token % 8 == 0 && g.a.q_stride_h % 8 == 0 && token > 0 &&
+               g.a.q_stride_h > 0;
+  if (q_tma) {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)g.group, (cuuint64_t)g.kv_heads,
+                                (cuuint64_t)g.a.N * g.a.T};
+    const cuuint64_t strides[3] = {(cuuint64_t)g.a.q_stride_h * 2,
+                                   (cuuint64_t)g.a.q_stride_h * 2 * g.group, (cuuint64_t)token * 2};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)g.group, 1, (cuuint32_t)(kRows / g.group)};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    q_tma = xp_get_encode_tiled()(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void*)g.q, dims, strides,
+                                  boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  attn_tc_kernel<D><<<c->num_sms, kThreads, smem, s>>>(c->tm_k, c->tm_v, tm_q, g, c->attn_tc, q_tma);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
@@ -906,8 +894,9 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
   p.prefix_tiles = (int)(((int64_t)a->N * per_seq + kRows - 1) / kRows);
   p.tail_tiles = (per_seq + kRows - 1) / kRows;
   const size_t H = c->d.kv_heads, D = c->d.head_dim;
-  const size_t blocks = H * (((size_t)a->N * per_seq + 31) / 32) + a->N * H * ((per_seq + 31) / 32) +
-                        (size_t)c->num_sms * 8;
+  const size_t one = (per_seq + 31) / 32;
+  const size_t blocks = H * (((size_t)a->N * per_seq + 31) / 32) + a->N * H * one + H * 4 +
+                        a->N * H * std::min<size_t>(one, 4) + (size_t)c->num_sms * 8;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
   p.line_off = take(((size_t)a->N + 1) * 8);
