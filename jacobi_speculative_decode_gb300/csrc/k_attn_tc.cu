@@ -43,8 +43,8 @@ struct Cfg {
 
 constexpr int kFrags = 4;       // fragments announced ahead
 // cost of a key tile for two row tiles, for one, and of a unit besides its tiles (ns / 180)
-constexpr int kPairCost = 8, kTileCost = 5, kUnitCost = 8;
-constexpr int kMinChunk = 18;   // least cost a CTA is given
+constexpr int kPairCost = 8, kTileCost = 5, kUnitCost = 12;
+constexpr int kMinChunk = 22;   // least cost a CTA is given
 
 struct Frag {
   int kind;              // 0 prefix, 1 tail, -1 no more
@@ -565,21 +565,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = warp % 4 * 32 + warp / 4 % 2 * 16 + lane / 4;      // and r0 + 8
     const uint32_t lanes = (uint32_t)(r0 - lane / 4) << 16;
     const float c = g.a.scale * 1.44269504088896f;
-    int done = 0;
+    const int all_rows = g.a.N * g.a.T * g.group;
+    int done = 0, known = -1, token[2] = {0, 0};   // the rows' tokens in a tail's row tile `known`
     Frag w;
     bool ok = true;
     for (int f = 0; ok && next_frag(f, &w); ++f) {
       const int T = w.t1 - w.t0, items = w.shared ? 2 * T : T, mine = (items + 1 - t) / 2;
       const int tile = w.shared ? w.tile + t : w.tile;
       const int end = min(w.len, w.t1 * kTile);
+      // keys its rows see: all of a prefix, a tail's by the row's token
       int limit[2];
       bool any_row = false;
+      if (w.kind == 1 && tile != known) {
+        known = tile;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) token[i] = (tile * kRows + r0 + 8 * i) / g.group;
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        int n, tt, h;
-        const bool is_row = row_of(g, w, tile, r0 + 8 * i, &n, &tt, &h, &limit[i]) >= 0;
-        limit[i] = is_row ? min(limit[i], end) : end;   // rows behind the end ask for no mask
-        any_row |= is_row;
+        const bool is_row = w.kind == 0 ? tile * kRows + r0 + 8 * i < all_rows : token[i] < g.a.T;
+        limit[i] = is_row && w.kind == 1 ? min(w.len - g.a.T + token[i] + 1, end) : end;
+        any_row |= is_row;   // rows behind the end ask for no mask
       }
       const bool active = __any_sync(0xFFFFFFFFu, any_row);
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // l: of this thread's columns
@@ -609,6 +615,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (key + q * 64 + x / 4 * 8 + quad * 2 + x % 2 >= limit[x / 2 % 2])
                 s[q][x] = 0xFF800000u;   // -inf
         }
+        // The first half's weights are computed with the maximum as it was: it rarely grows by
+        // more than P may carry, and neither has to wait for the other.
+        const uint64_t c2 = pair(c, c);
+        uint64_t sum[2];
+        uint32_t pk[16];
+        auto weights = [&](int q) {   // row x % 2, columns 8 (x / 2) + 2 quad
+          const float b0 = m[0] == -INFINITY ? 0.0f : m[0] * c, b1 = m[1] == -INFINITY ? 0.0f : m[1] * c;
+          const uint64_t nb[2] = {pair(-b0, -b0), pair(-b1, -b1)};
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2, nb[x % 2]);
+            const float a = ex2(low(z)), b = ex2(high(z));
+            sum[x % 2] = add2(sum[x % 2], pair(a, b));
+            pk[x] = pack_bf16(a, b);
+          }
+        };
+        sum[0] = sum[1] = 0;
+        if (j > 0) weights(0);
         float now[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -630,12 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             now[i] = fmaxf(now[i], __shfl_xor_sync(0xFFFFFFFFu, now[i], o));
         now[0] = fmaxf(now[0], m[0]);
         now[1] = fmaxf(now[1], m[1]);
-        if (j == 0) {
-          m[0] = now[0];
-          m[1] = now[1];
-        } else {
-          const bool grown0 = (now[0] - m[0]) * c > kLazy, grown1 = (now[1] - m[1]) * c > kLazy;
-          if (__any_sync(0xFFFFFFFFu, grown0 || grown1)) {   // from -inf too
+        const bool grown0 = j == 0 || (now[0] - m[0]) * c > kLazy;   // from -inf too
+        const bool grown1 = j == 0 || (now[1] - m[1]) * c > kLazy;
+        if (__any_sync(0xFFFFFFFFu, grown0 || grown1)) {
+          if (j > 0) {
             ok = wait(&bars->o_full[t], done + j - 1);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -655,23 +677,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tmem_wait_st();
             l[0] *= f0;
             l[1] *= f1;
-            if (grown0) m[0] = now[0];
-            if (grown1) m[1] = now[1];
           }
+          if (grown0) m[0] = now[0];
+          if (grown1) m[1] = now[1];
+          sum[0] = sum[1] = 0;
+          weights(0);
         }
-        const float b0 = m[0] == -INFINITY ? 0.0f : m[0] * c, b1 = m[1] == -INFINITY ? 0.0f : m[1] * c;
-        const uint64_t c2 = pair(c, c), nb[2] = {pair(-b0, -b0), pair(-b1, -b1)};
-        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {   // row x % 2, columns 8 (x / 2) + 2 quad
-            const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2, nb[x % 2]);
-            const float a = ex2(low(z)), b = ex2(high(z));
-            sum[x % 2] = add2(sum[x % 2], pair(a, b));
-            pk[x] = pack_bf16(a, b);
-          }
+          if (q == 1) weights(1);
           ptx::tmem_st_16x32_narrow(scol + q * 32, pk);
           // the product may start on the first half of the keys
           ptx::tmem_wait_st();
