@@ -75,7 +75,10 @@ bool valid_attn(const xp_cache* c, const xp_attn* a) {
 }
 
 xp_attn_plan attn_plan(const xp_cache* c, const xp_attn* a) {
-  if (c->attn_tc) return xp_attn_tc_plan(c, a);
+  if (c->attn_tc) {
+    const xp_attn_plan tc = xp_attn_tc_plan(c, a);
+    if (tc.total) return tc;   // 0: more work than its line can count
+  }
   xp_attn_plan p = xp_attn_simt_plan(c, a);
   const size_t rows = (size_t)a->N * a->T * a->heads;
   p.stat_off = 0;
@@ -251,10 +254,10 @@ xp_status xp_prefix_attention(const xp_cache* c, const xp_attn* a, const void* q
   g.lse = lse;
   g.stat = (float*)((char*)ws + plan.stat_off);
   g.acc = (float*)((char*)ws + plan.acc_off);
-  g.line = (long long*)((char*)ws + plan.line_off);
+  g.line = (int*)((char*)ws + plan.line_off);
   g.err = c->err;
   g.plan = plan;
-  if (c->attn_tc) return cuda_status(xp_launch_attn_tc(c, g, stream));
+  if (plan.tc) return cuda_status(xp_launch_attn_tc(c, g, stream));
   cudaError_t e = xp_launch_attn_simt(c, g, stream);
   if (e == cudaSuccess) e = xp_launch_attn_combine(c, g, stream);
   return cuda_status(e);

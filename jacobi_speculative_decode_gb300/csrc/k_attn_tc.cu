@@ -44,7 +44,7 @@ struct Cfg {
 constexpr int kFrags = 4;       // fragments announced ahead
 // cost of a key tile for two row tiles, for one, and of a unit besides its tiles (ns / 180)
 constexpr int kPairCost = 8, kTileCost = 5, kUnitCost = 12;
-constexpr int kMinChunk = 22;   // least cost a CTA is given
+constexpr int kMinChunk = kUnitCost + kTileCost;   // least cost a CTA is given
 
 struct Frag {
   int kind;              // 0 prefix, 1 tail, -1 no more
@@ -61,7 +61,7 @@ struct Bars {
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
   uint64_t drained;              // both streams' products have all run
   Frag frag[kFrags];
-  long long total[kThreads / 32], start_base;   // start: where this CTA's share begins
+  int total[kThreads / 32], start_base;   // start: where this CTA's share begins
   int start_n;
   uint32_t tmem_base;
   int abort;
@@ -78,16 +78,13 @@ struct Line {
   __host__ __device__ Line(int row_tiles, int keys)
       : pairs(row_tiles / 2), odd(row_tiles % 2), T((keys + kTile - 1) / kTile) {}
   __host__ __device__ int tile_cost(int p) const { return p < pairs ? kPairCost : kTileCost; }
-  __host__ __device__ long long unit(int p) const { return tile_cost(p) * (long long)T + kUnitCost; }
+  __host__ __device__ int unit(int p) const { return tile_cost(p) * T + kUnitCost; }
   // all row tiles of one kv head
-  __host__ __device__ long long head() const {
-    return T ? pairs * unit(0) + odd * unit(pairs) : 0;
-  }
+  __host__ __device__ int head() const { return T ? pairs * unit(0) + odd * unit(pairs) : 0; }
   // first tile of unit p that lies behind a cost of x from the unit's beginning
-  __host__ __device__ int tile_at(int p, long long x) const {
-    const int w = tile_cost(p);
-    const long long t = (x - kUnitCost + w - 1) / w;
-    return x <= kUnitCost ? 0 : t > T ? T : (int)t;
+  __host__ __device__ int tile_at(int p, int x) const {
+    const int w = tile_cost(p), t = (x - kUnitCost + w - 1) / w;
+    return x <= kUnitCost ? 0 : t > T ? T : t;
   }
 };
 
@@ -167,7 +164,7 @@ __device__ __forceinline__ int64_t second_block_of(const xp_attn_args& g, int ki
   const int64_t one = min((per_seq_of(g) + 31) / 32, (int64_t)4);
   return block_of(g, 1, g.a.N, 0) + (kind == 0 ? hk * 4 : g.kv_heads * 4 + ((int64_t)n * g.kv_heads + hk) * one);
 }
-__device__ __forceinline__ int64_t cut_block(const xp_attn_args& g, long long cta, int half) {
+__device__ __forceinline__ int64_t cut_block(const xp_attn_args& g, int64_t cta, int half) {
   return second_block_of(g, 1, g.a.N, 0) + cta * 8 + half * 4;
 }
 
@@ -183,33 +180,34 @@ __device__ __forceinline__ int tail_len(const xp_attn_args& g, int n, bool tell)
 // Sums the tails' costs over the CTA: the chunk, and the sequence in which this CTA's share
 // begins (with the cost before it).  CTA 0 leaves the chunk and every sequence's beginning for
 // the kernel that joins the results.
-__device__ long long plan_line(const xp_attn_args& g, Bars* bars) {
+__device__ int plan_line(const xp_attn_args& g, Bars* bars) {
   const Line pre(g.plan.prefix_tiles, g.a.prefix_len);
-  const long long before = pre.head() * g.kv_heads;
+  const int before = pre.head() * g.kv_heads;
   const int N = g.a.max_len > 0 ? g.a.N : 0;
   const int per = (N + kThreads - 1) / kThreads, n0 = min(N, (int)threadIdx.x * per), n1 = min(N, n0 + per);
   auto cost = [&](int n) { return Line(g.plan.tail_tiles, tail_len(g, n, blockIdx.x == 0)).head() * g.kv_heads; };
-  long long mine = 0;
+  int mine = 0;
   for (int n = n0; n < n1; ++n) mine += cost(n);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    const int t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += t;
   }
   if (lane == 31) bars->total[warp] = inc;
   __syncthreads();
-  long long base = before + inc - mine, all = before;
+  int base = before + inc - mine, all = before;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    base += w < warp ? bars->total[w] : 0;
-    all += bars->total[w];
+    const int t = bars->total[w];
+    base += w < warp ? t : 0;
+    all += t;
   }
-  long long chunk = (all + gridDim.x - 1) / gridDim.x;
-  chunk = chunk < kMinChunk ? kMinChunk : chunk;
-  const long long x = (long long)blockIdx.x * chunk;
+  const int chunk = max(kMinChunk, (int)((all + gridDim.x - 1) / gridDim.x));
+  const int x = blockIdx.x * chunk;
   for (int n = n0; n < n1; ++n) {
-    const long long c = cost(n);
+    const int c = per == 1 ? mine : cost(n);
     if (blockIdx.x == 0) g.line[1 + n] = base;
     if (c > 0 && x >= base && x < base + c) {
       bars->start_n = n;
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sq = ptx::smem_u32(smem), ring = sq + 2 * C::TILE_BYTES;
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
-  const long long chunk = plan_line(g, bars);
+  const int chunk = plan_line(g, bars);
   if (chunk == 0) return;   // the line ends before this CTA's share
   if (sq & 1023u) {         // the swizzled tiles need it; the declared alignment gives it
     if (threadIdx.x == 0) atomicOr(g.err, XP_ERR_TIMEOUT);
@@ -291,9 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- announces the fragments and loads their query tiles.  Two query tiles a shared
       // fragment, one of the two places in turn for the others, so that the next one's queries
       // are there before the present one is done ----
-      const long long x0 = (long long)blockIdx.x * chunk, x1 = x0 + chunk;
+      const int x0 = blockIdx.x * chunk, x1 = x0 + chunk;
       const Line pre(g.plan.prefix_tiles, g.a.prefix_len);
-      const long long before = pre.head() * g.kv_heads;
+      const int before = pre.head() * g.kv_heads;
       const int N = g.a.max_len > 0 ? g.a.N : 0;
       const uint64_t once = ptx::policy_evict_first();
       int f = 0, splits = 0, used[2] = {0, 0};
@@ -343,21 +341,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         return load_q(w, w.tile, splits++ & 1);
       };
       // the units of one source that lie in [x0, x1), from cost `at` on
-      auto source = [&](const Line& l, int kind, int n, int len, long long at) {
+      auto source = [&](const Line& l, int kind, int n, int len, int at) {
         if (l.T == 0) return true;
         const int per = l.pairs + l.odd;
         int hk = 0, p = 0;
         if (x0 > at) {   // skip what lies before
-          const long long off = x0 - at;
-          hk = (int)(off / l.head());
+          hk = (x0 - at) / l.head();
           at += hk * l.head();
-          p = (int)min((long long)l.pairs, (x0 - at) / l.unit(0));
+          p = min(l.pairs, (x0 - at) / l.unit(0));
           at += p * l.unit(0);
           if (hk >= g.kv_heads) return true;
         }
         for (; hk < g.kv_heads && at < x1; ++hk, p = 0)
           for (; p < per && at < x1; ++p) {
-            const long long cost = l.unit(p);
+            const int cost = l.unit(p);
             const int t0 = l.tile_at(p, x0 - at), t1 = l.tile_at(p, min(x1 - at, cost));
             if (t0 < t1) {
               const Frag w = {kind, p < l.pairs, n, hk, 2 * p, len, t0, t1, t0 > 0 ? (int)blockIdx.x : -1};
@@ -370,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x0 < before) ok = source(pre, 0, 0, g.a.prefix_len, 0);
       if (x1 > before) {
         int n = x0 < before ? 0 : bars->start_n;
-        long long at = x0 < before ? before : bars->start_base;
+        int at = x0 < before ? before : bars->start_base;
         int len = n < N ? tail_len(g, n, false) : 0;
         for (; ok && n < N && at < x1; ++n) {
           const int after = n + 1 < N ? tail_len(g, n + 1, false) : 0;   // read ahead
@@ -763,7 +760,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args
   if (e < rows) {
     const int i = (int)(e % per_seq), hk = (int)(e / per_seq % g.kv_heads);
     const int n = (int)(e / per_seq / g.kv_heads), t = i / g.group, h = hk * g.group + i % g.group;
-    const long long chunk = g.line[0];
+    const int chunk = g.line[0];
     float m = -INFINITY, l = 0.0f;
     float4 o[kPer];
 #pragma unroll
@@ -789,17 +786,17 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args
                     kind ? tail_len(g, n, false) : g.a.prefix_len);
       if (ln.T == 0) continue;
       const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / kRows, p = tile / 2;
-      const long long at = (kind ? g.line[1 + n] : 0) + hk * ln.head() + p * ln.unit(0), cost = ln.unit(p);
+      const int at = (kind ? g.line[1 + n] : 0) + hk * ln.head() + p * ln.unit(0), cost = ln.unit(p);
       // a piece of two row tiles has a half of each, one of a single row tile a half of each
       // stream (the second from two key tiles on)
       const bool shared = p < ln.pairs;
       const int in_tile = at_row % kRows / 32, r = at_row % 32;
-      long long cut = (at / chunk + 1) * chunk - at;   // where the unit is first cut,
+      int cut = (at / chunk + 1) * chunk - at;   // where the unit is first cut,
       if (ln.tile_at(p, cut) == 0) cut += chunk;       // behind its first tile
       const int first = ln.tile_at(p, min(cut, cost));
       if (first > 0) take(block_of(g, kind, n, hk) + at_row / 32, r);
       if (first > 1 && !shared) take(second_block_of(g, kind, n, hk) + in_tile, r);
-      for (long long c = at / chunk + 1; c < ctas && c * chunk < at + cost; ++c) {
+      for (int c = at / chunk + 1; c < ctas && c * chunk < at + cost; ++c) {
         const int t0 = ln.tile_at(p, c * chunk - at), t1 = ln.tile_at(p, min((c + 1) * chunk - at, cost));
         if (t0 == 0 || t0 >= t1) continue;
         take(cut_block(g, c, shared ? tile % 2 : 0) + in_tile, r);
@@ -903,6 +900,7 @@ int xp_attn_tc_maps(xp_cache* c) {
 // Row tiles only: where the work is cut is found on the device, from the lengths.
 xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
   xp_attn_plan p = {};
+  p.tc = true;
   const int per_seq = a->T * (a->heads / c->d.kv_heads);
   p.rows_tile = kRows;
   p.prefix_tiles = (int)(((int64_t)a->N * per_seq + kRows - 1) / kRows);
@@ -913,10 +911,15 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
                         a->N * H * std::min<size_t>(one, 4) + (size_t)c->num_sms * 8;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
-  p.line_off = take(((size_t)a->N + 1) * 8);
+  p.line_off = take(((size_t)a->N + 1) * 4);
   p.stat_off = take(blocks * 32 * 8);
   p.acc_off = take(blocks * 32 * D * 4);
-  p.total = o;
+  // the line's length, at the greatest lengths, has to be an int (with room for one share more)
+  const Line pre(p.prefix_tiles, a->prefix_len), tail(p.tail_tiles, a->max_len);
+  const double work = ((double)pre.pairs * kPairCost + pre.odd * kTileCost) * pre.T * H +
+                      ((double)tail.pairs * kPairCost + tail.odd * kTileCost) * tail.T * H * a->N +
+                      (double)kUnitCost * H * (pre.pairs + pre.odd + (double)a->N * (tail.pairs + tail.odd));
+  p.total = work < 1e9 ? o : 0;
   return p;
 }
 

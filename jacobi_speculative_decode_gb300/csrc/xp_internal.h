@@ -221,6 +221,7 @@ cudaError_t xp_launch_compact(const xp_cache* c, const int32_t* table, int64_t l
 // How one attention call is split: `prefix_splits` ranges of prefix_keys keys, then
 // `tail_splits` ranges of tail_keys keys; every range leaves one partial result a row.
 struct xp_attn_plan {
+  bool tc;                       // the tensor-core form
   int rows_tile;                 // query rows of one work item
   int prefix_tiles, tail_tiles;  // row tiles: over the batch, of one sequence
   int prefix_splits, prefix_keys, tail_splits, tail_keys;
@@ -239,7 +240,7 @@ struct xp_attn_args {
   float* lse;
   float* stat;                   // CUDA-core form: [parts][N*T*heads][2]
   float* acc;                    //                 [parts][N*T*heads][dim]
-  long long* line;
+  int* line;
   uint32_t* err;
   xp_attn_plan plan;
 };
