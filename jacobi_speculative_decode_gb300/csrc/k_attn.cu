@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "sm100_ptx.cuh"
 #include "xp_device.cuh"
 
 using namespace xpd;
@@ -30,8 +31,27 @@ __device__ __forceinline__ bool row_of(const xp_attn_args& g, bool prefix, int t
   return true;
 }
 
+// four consecutive elements as floats; wide: 16 (fp32) or 8 (bf16) bytes at once
+__device__ __forceinline__ float4 load4(const float* p, bool wide, int n) {
+  if (wide) return *(const float4*)p;
+  return make_float4(p[0], n > 1 ? p[1] : 0.0f, n > 2 ? p[2] : 0.0f, n > 3 ? p[3] : 0.0f);
+}
+__device__ __forceinline__ float4 load4(const bf16* p, bool wide, int n) {
+  if (wide) {
+    const uint2 v = *(const uint2*)p;
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+  }
+  return make_float4(to_f(p[0]), n > 1 ? to_f(p[1]) : 0.0f, n > 2 ? to_f(p[2]) : 0.0f,
+                     n > 3 ? to_f(p[3]) : 0.0f);
+}
+
+// A CTA holds BM query rows and walks over its keys 64 at a time: scores from shared memory (RM
+// x 4 a thread), one pass of the softmax in base 2 with a running maximum and sum, weights times
+// values.  A warp loads eight keys and values at once, a lane four dims.
 template <typename T, int RM, int NC>
-__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args g) {
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args g,
+                                                             bool wide) {
   constexpr int BM = 16 * RM;
   extern __shared__ __align__(16) float smem[];
   const int D = g.dim, DP = (D + 3) / 4 * 4, LD = DP + 4;
@@ -41,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
   float* sp = sv + kKeys * NC * 64;      // [BM][kKeys + 4]
   constexpr int LP = kKeys + 4;
   __shared__ int s_limit[BM];            // keys each row sees
-  __shared__ int s_page[kKeys];
+  __shared__ int64_t s_at[kKeys];        // where each key begins in the pools, -1 behind the range
 
   const xp_attn_plan& pl = g.plan;
   const int hk = blockIdx.y, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -78,14 +98,13 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
   }
   // queries, scaled so that the softmax runs in base 2
   const float scale = g.a.scale * 1.44269504088896f;
-  for (int i = tid; i < BM * LD; i += kThreads) {
-    const int r = i / LD, d = i % LD;
+  for (int r = tid >> 5; r < BM; r += kThreads / 32) {
     Row w;
-    float x = 0.0f;
-    if (d < D && row_of(g, prefix, tile, r, n, BM, &w))
-      x = to_f(((const T*)g.q)[w.n * g.a.q_stride_n + w.t * g.a.q_stride_t +
-                               (int64_t)(hk * g.group + w.j) * g.a.q_stride_h + d]) * scale;
-    sq[i] = x;
+    const bool is_row = row_of(g, prefix, tile, r, n, BM, &w);
+    const T* src = is_row ? (const T*)g.q + w.n * g.a.q_stride_n + w.t * g.a.q_stride_t +
+                                (int64_t)(hk * g.group + w.j) * g.a.q_stride_h
+                          : nullptr;
+    for (int d = tid & 31; d < LD; d += 32) sq[r * LD + d] = is_row && d < D ? to_f(src[d]) * scale : 0.0f;
   }
   float o[RM][NC * 4], m[RM], l[RM];
 #pragma unroll
@@ -99,32 +118,37 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
   for (int kb = k0; kb < k1; kb += kKeys) {
     __syncthreads();
     if (tid < kKeys) {
-      int p = -1;
+      int64_t at = -1;
       if (kb + tid < k1) {
-        p = table[(kb + tid) / g.page_size];
+        const int key = kb + tid, page = key / g.page_size;
+        int p = table[page];
         if (p < 0 || p >= g.pages) {
           atomicOr(g.err, XP_ERR_BADPAGE);
           p = p < 0 ? 0 : g.pages - 1;
         }
+        at = p * g.kv_page + (key - page * g.page_size) * g.kv_token + hk * g.kv_head;
       }
-      s_page[tid] = p;
+      s_at[tid] = at;
     }
     __syncthreads();
-    for (int i = tid; i < kKeys * DP; i += kThreads) {
-      const int j = i / DP, d = i % DP;
-      float kx = 0.0f, vx = 0.0f;
-      if (s_page[j] >= 0 && d < D) {   // tokens behind the length are not read
-        const int64_t at = s_page[j] * g.kv_page + (kb + j) % g.page_size * g.kv_token +
-                           hk * g.kv_head + d;
-        kx = to_f(((const T*)g.k)[at]);
-        vx = to_f(((const T*)g.v)[at]);
+    for (int d = (tid & 31) * 4; d < NC * 64; d += 128) {
+      float4 kx[kKeys / 8], vx[kKeys / 8];
+#pragma unroll
+      for (int i = 0; i < kKeys / 8; ++i) {
+        const int64_t at = s_at[(tid >> 5) + 8 * i];
+        kx[i] = vx[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (at >= 0 && d < D) {   // tokens behind the length are not read
+          kx[i] = load4((const T*)g.k + at + d, wide, D - d);
+          vx[i] = load4((const T*)g.v + at + d, wide, D - d);
+        }
       }
-      sk[j * LD + d] = kx;
-      sv[j * NC * 64 + d] = vx;
+#pragma unroll
+      for (int i = 0; i < kKeys / 8; ++i) {
+        const int j = (tid >> 5) + 8 * i;
+        if (d < DP) *(float4*)&sk[j * LD + d] = kx[i];
+        *(float4*)&sv[j * NC * 64 + d] = vx[i];
+      }
     }
-    if (DP < NC * 64)
-      for (int i = tid; i < kKeys * (NC * 64 - DP); i += kThreads)
-        sv[i / (NC * 64 - DP) * NC * 64 + DP + i % (NC * 64 - DP)] = 0.0f;
     __syncthreads();
     // scores: rows ty*RM.., keys tx + 16 j
     float s[RM][4];
@@ -225,6 +249,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
 // ranges, brought to a common maximum.  out = sum_p a_p O_p / sum_p a_p l_p, a_p = 2^(m_p - m).
 template <typename T>
 __global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g) {
+  ptx::pdl_wait();
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
   const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31, parts = g.plan.parts, D = g.dim;
@@ -239,6 +264,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g)
   float o[8], l = 0.0f;
 #pragma unroll
   for (int c = 0; c < 8; ++c) o[c] = 0.0f;
+#pragma unroll 4
   for (int p = 0; p < parts; ++p) {
     const float2 st = *(const float2*)&g.stat[(p * rows + row) * 2];
     if (!(st.y > 0.0f)) continue;   // no key of this range
@@ -275,7 +301,11 @@ cudaError_t launch(const xp_attn_args& g, cudaStream_t s) {
   const xp_attn_plan& p = g.plan;
   const dim3 grid(p.prefix_tiles * p.prefix_splits + g.a.N * p.tail_tiles * p.tail_splits,
                   g.kv_heads);
-  attn_simt_kernel<T, RM, NC><<<grid, kThreads, smem, s>>>(g);
+  const uint64_t unit = 4 * sizeof(T);
+  const bool wide = g.dim % 4 == 0 && ((uintptr_t)g.k | (uintptr_t)g.v | (uint64_t)g.kv_page * sizeof(T) |
+                                       (uint64_t)g.kv_token * sizeof(T) |
+                                       (uint64_t)g.kv_head * sizeof(T)) % unit == 0;
+  attn_simt_kernel<T, RM, NC><<<grid, kThreads, smem, s>>>(g, wide);
   return cudaGetLastError();
 }
 template <typename T, int RM>
@@ -290,38 +320,42 @@ cudaError_t launch_nc(const xp_attn_args& g, cudaStream_t s) {
 
 }  // namespace
 
-// Row tiles of 16 or 64 query rows; key ranges so that about four CTAs an SM have work.
+// Row tiles of 16, 32 or 64 query rows; key ranges so that about two CTAs an SM have work.
 xp_attn_plan xp_attn_simt_plan(const xp_cache* c, const xp_attn* a) {
   xp_attn_plan p = {};
   const int group = a->heads / c->d.kv_heads, per_seq = a->T * group;
-  p.rows_tile = per_seq > 16 ? 64 : 16;
-  const int64_t want = (int64_t)c->num_sms * 4;
-  auto splits = [&](int64_t tiles, int keys, int* range) {
-    int64_t s = std::max<int64_t>(1, want / std::max<int64_t>(1, tiles * c->d.kv_heads));
-    s = std::min<int64_t>(s, std::max(1, (keys + 4 * kKeys - 1) / (4 * kKeys)));
-    const int64_t r = (keys + s - 1) / s;
-    *range = (int)std::max<int64_t>(kKeys, (r + kKeys - 1) / kKeys * kKeys);
+  p.rows_tile = per_seq > 32 ? 64 : per_seq > 16 ? 32 : 16;
+  const int64_t want = (int64_t)c->num_sms * 2;
+  // both sources share the CTAs by their keys; a range is a whole number of steps
+  const int64_t all_steps =
+      (((int64_t)a->N * per_seq + p.rows_tile - 1) / p.rows_tile * ((a->prefix_len + kKeys - 1) / kKeys) +
+       (int64_t)a->N * ((per_seq + p.rows_tile - 1) / p.rows_tile) * ((a->max_len + kKeys - 1) / kKeys)) *
+      c->d.kv_heads;
+  const int64_t steps = std::max<int64_t>(1, (all_steps + want - 1) / want);
+  auto splits = [&](int keys, int* range) {
+    const int64_t r = std::min<int64_t>(steps * kKeys, ((int64_t)keys + kKeys - 1) / kKeys * kKeys);
+    *range = (int)std::max<int64_t>(kKeys, r);
     return keys > 0 ? (keys + *range - 1) / *range : 0;
   };
   p.prefix_tiles = (int)(((int64_t)a->N * per_seq + p.rows_tile - 1) / p.rows_tile);
   p.tail_tiles = (per_seq + p.rows_tile - 1) / p.rows_tile;
-  p.prefix_splits = (int)splits(p.prefix_tiles, a->prefix_len, &p.prefix_keys);
-  p.tail_splits = (int)splits((int64_t)a->N * p.tail_tiles, a->max_len, &p.tail_keys);
+  p.prefix_splits = splits(a->prefix_len, &p.prefix_keys);
+  p.tail_splits = splits(a->max_len, &p.tail_keys);
   p.parts = p.prefix_splits + p.tail_splits;
   return p;
 }
 
 cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   if (g.plan.parts == 0) return cudaSuccess;
-  const bool small = g.plan.rows_tile == 16;
-  if (c->d.dtype == XP_BF16) return small ? launch_nc<bf16, 1>(g, s) : launch_nc<bf16, 4>(g, s);
-  return small ? launch_nc<float, 1>(g, s) : launch_nc<float, 4>(g, s);
+  const int rm = g.plan.rows_tile / 16;
+  if (c->d.dtype == XP_BF16)
+    return rm == 1 ? launch_nc<bf16, 1>(g, s) : rm == 2 ? launch_nc<bf16, 2>(g, s) : launch_nc<bf16, 4>(g, s);
+  return rm == 1 ? launch_nc<float, 1>(g, s) : rm == 2 ? launch_nc<float, 2>(g, s) : launch_nc<float, 4>(g, s);
 }
 
 cudaError_t xp_launch_attn_combine(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
-  const unsigned grid = (unsigned)((rows + 7) / 8);
-  if (c->d.dtype == XP_BF16) attn_combine_kernel<bf16><<<grid, 256, 0, s>>>(g);
-  else attn_combine_kernel<float><<<grid, 256, 0, s>>>(g);
-  return cudaGetLastError();
+  const dim3 grid((unsigned)((rows + 7) / 8)), block(256);
+  return c->d.dtype == XP_BF16 ? xp_launch_pdl(attn_combine_kernel<bf16>, grid, block, 0, s, g)
+                               : xp_launch_pdl(attn_combine_kernel<float>, grid, block, 0, s, g);
 }

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 
+#include "sm100_ptx.cuh"
 #include "xp_device.cuh"
 
 namespace cg = cooperative_groups;
@@ -375,7 +376,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 // Page copies: (move, plane, chunk) items, a plane being K or V of one layer.
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
-constexpr int kPerThread = 4;
+constexpr int kPerThread = 8;   // vectors of a thread in flight: 32 KB a CTA
 
 struct CopyArgs {
   char *k, *v;
@@ -391,6 +392,7 @@ struct CopyArgs {
 
 template <typename U>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyArgs a) {
+  ptx::pdl_wait();
   constexpr int kChunk = kCopyThreads * kPerThread * (int)sizeof(U);
   const int n = a.n_dev ? *a.n_dev : a.n;
   const int chunks = (int)((a.block_bytes + kChunk - 1) / kChunk);
@@ -406,6 +408,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyArgs
       continue;
     }
     const int64_t keep = a.tokens ? a.tokens[i] * a.token_bytes : a.seg_bytes;
+    // a page of one segment has nothing to copy behind its tokens
+    if (a.seg_bytes == a.block_bytes && (int64_t)c * kChunk >= keep) continue;
     char* pool = plane & 1 ? a.v : a.k;
     pool += (plane >> 1) * a.layer_bytes;
     const char* from = pool + sp * a.page_bytes;
@@ -507,10 +511,10 @@ cudaError_t xp_launch_copy_pages(const xp_cache* c, const int32_t* src, const in
   const bool wide = ((uintptr_t)d.k | (uintptr_t)d.v | (uint64_t)a.layer_bytes |
                      (uint64_t)a.page_bytes | (uint64_t)a.token_bytes) % 16 == 0;
   const unsigned grid = (unsigned)c->num_sms * 8;
-  if (wide) copy_pages_kernel<uint4><<<grid, kCopyThreads, 0, s>>>(a);
-  else if (es == 4) copy_pages_kernel<uint32_t><<<grid, kCopyThreads, 0, s>>>(a);
-  else copy_pages_kernel<uint16_t><<<grid, kCopyThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const dim3 g(grid), b(kCopyThreads);
+  return wide      ? xp_launch_pdl(copy_pages_kernel<uint4>, g, b, 0, s, a)
+         : es == 4 ? xp_launch_pdl(copy_pages_kernel<uint32_t>, g, b, 0, s, a)
+                   : xp_launch_pdl(copy_pages_kernel<uint16_t>, g, b, 0, s, a);
 }
 
 cudaError_t xp_launch_resize(const xp_cache* c, const int32_t* table, int64_t ld,
