@@ -18,7 +18,7 @@ constexpr int kThreads = 1024;
 
 struct Scan {
   int warp[32];
-  int total[kCtas];
+  int total[3][kCtas];   // every CTA's sums, one row a use of cluster_base
 };
 
 __device__ __forceinline__ void flag(uint32_t* err, uint32_t bit) { atomicOr(err, bit); }
@@ -48,22 +48,22 @@ __device__ __forceinline__ int block_scan(int v, Scan& s, int* sum) {
   return (w == 0 ? 0 : before) + inc - v;
 }
 
-// Sum of v over the CTA's threads, then the CTA's exclusive prefix among the cluster's.
-// Orders the cluster: whatever any CTA wrote before is visible behind it.
-__device__ __forceinline__ int cluster_base(cg::cluster_group& cl, int v, Scan& s, int* total) {
+// Sum of v over the CTA's threads, then the CTA's exclusive prefix among the cluster's (use:
+// the sum's own row).  Orders the cluster: whatever any CTA wrote before is visible behind it.
+__device__ __forceinline__ int cluster_base(cg::cluster_group& cl, int use, int v, Scan& s,
+                                            int* total) {
   int sum;
   block_scan(v, s, &sum);
   const int rank = (int)cl.block_rank();
-  if (threadIdx.x < kCtas) *cl.map_shared_rank(&s.total[rank], threadIdx.x) = sum;
+  if (threadIdx.x < kCtas) *cl.map_shared_rank(&s.total[use][rank], threadIdx.x) = sum;
   cl.sync();
   int base = 0, all = 0;
   for (int r = 0; r < kCtas; ++r) {
-    const int t = s.total[r];
+    const int t = s.total[use][r];
     base += r < rank ? t : 0;
     all += t;
   }
   *total = all;
-  cl.sync();   // s.total may be written again
   return base;
 }
 
@@ -89,7 +89,7 @@ __device__ int take_free(cg::cluster_group& cl, int32_t* refs, int lo, int hi, i
     mine += r <= 0;
   }
   int total;
-  int base = cluster_base(cl, mine, s, &total);
+  int base = cluster_base(cl, 1, mine, s, &total);
   for (int p0 = lo; p0 < hi && base < want; p0 += kThreads) {
     const int p = p0 + (int)threadIdx.x;
     const int is_free = p < hi && refs[p] <= 0;
@@ -127,6 +127,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   const int p1 = (int)((int64_t)a.pages * (rank + 1) / kCtas);
 
   // each row's lengths, on the counts as they were
+  if (a.refs_out != a.refs)
+    for (int p = p0 + tid; p < p1; p += kThreads) a.refs_out[p] = a.refs[p];
   int need = 0;
   for (int n = r0 + tid; n < r1; n += kThreads) {
     const int len = checked_len(a.lens[n], a.width * a.ps, a.err);
@@ -144,10 +146,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     need += max(0, ceil_div(now, a.ps) - ceil_div(len, a.ps));
   }
   int all_need;
-  int base = cluster_base(cl, need, s, &all_need);
-  // the counts move over only now: refs_out may be refs
-  if (a.refs_out != a.refs)
-    for (int p = p0 + tid; p < p1; p += kThreads) a.refs_out[p] = a.refs[p];
+  int base = cluster_base(cl, 0, need, s, &all_need);   // from here on refs_out may change
   for (int n0 = r0; n0 < r1; n0 += kThreads) {
     const int n = n0 + tid;
     const int v = n < r1 ? max(0, ceil_div(a.row_new[n], a.ps) - ceil_div(a.row_old[n], a.ps)) : 0;
@@ -156,28 +155,28 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     if (n < r1) a.row_off[n] = off;
     base += sum;
   }
-  cl.sync();
 
   // kept entries, and the pages let go
-  for (int64_t i = tid; i < (int64_t)(r1 - r0) * a.width; i += kThreads) {
-    const int n = r0 + (int)(i / a.width), j = (int)(i % a.width);
+  const int lane = tid & 31;
+  for (int n = r0 + (tid >> 5); n < r1; n += kThreads / 32) {
     const int have = ceil_div(a.row_old[n], a.ps), want = ceil_div(a.row_new[n], a.ps);
-    int out = -1;
-    if (j < have) {
-      const int p = a.table[n * a.ld + j];
-      const bool ok = p >= 0 && p < a.pages;
-      if (!ok) flag(a.err, XP_ERR_BADPAGE);
-      if (j < want) out = p;
-      else if (ok) atomicSub(&a.refs_out[p], 1);
+    for (int j = lane; j < a.width; j += 32) {
+      int out = -1;
+      if (j < have) {
+        const int p = a.table[n * a.ld + j];
+        const bool ok = p >= 0 && p < a.pages;
+        if (!ok) flag(a.err, XP_ERR_BADPAGE);
+        if (j < want) out = p;
+        else if (ok) atomicSub(&a.refs_out[p], 1);
+      }
+      if (j < have || j >= want) a.table_out[n * a.ld_out + j] = out;
     }
-    if (j < have || j >= want) a.table_out[n * a.ld_out + j] = out;
   }
   cl.sync();
 
   const int n_free = take_free(cl, a.refs_out, p0, p1, all_need, a.free_list, s, a.err);
 
   // the free pages go to the rows in order
-  const int lane = tid & 31;
   for (int n = r0 + (tid >> 5); n < r1; n += kThreads / 32) {
     const int old_len = a.row_old[n], now = a.row_new[n], off = a.row_off[n];
     const int have = ceil_div(old_len, a.ps), want = ceil_div(now, a.ps);
@@ -221,6 +220,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   const int p0 = (int)((int64_t)a.pages * rank / kCtas);
   const int p1 = (int)((int64_t)a.pages * (rank + 1) / kCtas);
 
+  if (a.refs_out != a.refs)
+    for (int p = p0 + tid; p < p1; p += kThreads) a.refs_out[p] = a.refs[p];
   int need = 0;
   for (int i = r0 + tid; i < r1; i += kThreads) {
     int p = a.parent[i], len = 0;
@@ -244,9 +245,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     need += len % a.ps != 0;
   }
   int all_need;
-  int base = cluster_base(cl, need, s, &all_need);
-  if (a.refs_out != a.refs)
-    for (int p = p0 + tid; p < p1; p += kThreads) a.refs_out[p] = a.refs[p];
+  int base = cluster_base(cl, 0, need, s, &all_need);   // from here on refs_out may change
   for (int i0 = r0; i0 < r1; i0 += kThreads) {
     const int i = i0 + tid;
     int sum;
@@ -254,19 +253,20 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     if (i < r1) a.row_off[i] = off;
     base += sum;
   }
-  cl.sync();
 
   // full pages are shared
-  for (int64_t e = tid; e < (int64_t)(r1 - r0) * a.width; e += kThreads) {
-    const int i = r0 + (int)(e / a.width), j = (int)(e % a.width);
-    const int len = a.row_len[i];
-    int out = -1;
-    if (j < len / a.ps) {
-      out = a.table[a.row_parent[i] * a.ld + j];
-      if (out >= 0 && out < a.pages) atomicAdd(&a.refs_out[out], 1);
-      else flag(a.err, XP_ERR_BADPAGE);
+  for (int i = r0 + (tid >> 5); i < r1; i += kThreads / 32) {
+    const int full = a.row_len[i] / a.ps;
+    const int32_t* row = a.table + a.row_parent[i] * a.ld;
+    for (int j = tid & 31; j < a.width; j += 32) {
+      int out = -1;
+      if (j < full) {
+        out = row[j];
+        if (out >= 0 && out < a.pages) atomicAdd(&a.refs_out[out], 1);
+        else flag(a.err, XP_ERR_BADPAGE);
+      }
+      a.child[i * a.ld_child + j] = out;
     }
-    a.child[i * a.ld_child + j] = out;
   }
   cl.sync();
 
@@ -315,7 +315,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   int used = 0;
   for (int p = p0 + tid; p < p1; p += kThreads) used += a.refs[p] > 0;
   int live;
-  cluster_base(cl, used, s, &live);
+  cluster_base(cl, 0, used, s, &live);
 
   // pages in use behind the line, and holes before it: equally many
   int high = 0, holes = 0;
@@ -325,8 +325,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     holes += !u && p < live;
   }
   int moves, same;
-  int base_h = cluster_base(cl, high, s, &moves);
-  int base_o = cluster_base(cl, holes, s, &same);
+  int base_h = cluster_base(cl, 1, high, s, &moves);
+  int base_o = cluster_base(cl, 2, holes, s, &same);
   for (int q0 = p0; q0 < p1; q0 += kThreads) {
     const int p = q0 + tid;
     const bool u = p < p1 && a.refs[p] > 0;
@@ -355,16 +355,17 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   cl.sync();
   if (a.refs_out == a.refs)
     for (int p = max(p0, live) + tid; p < p1; p += kThreads) a.refs_out[p] = 0;
-  for (int64_t i = tid; i < (int64_t)(r1 - r0) * a.width; i += kThreads) {
-    const int n = r0 + (int)(i / a.width), j = (int)(i % a.width);
-    const int len = checked_len(a.lens[n], a.width * a.ps, a.err);
-    int out = -1;
-    if (j < ceil_div(len, a.ps)) {
-      const int p = a.table[n * a.ld + j];
-      if (p >= 0 && p < a.pages) out = a.map[p];
-      else flag(a.err, XP_ERR_BADPAGE);
+  for (int n = r0 + (tid >> 5); n < r1; n += kThreads / 32) {
+    const int held = ceil_div(checked_len(a.lens[n], a.width * a.ps, a.err), a.ps);
+    for (int j = tid & 31; j < a.width; j += 32) {
+      int out = -1;
+      if (j < held) {
+        const int p = a.table[n * a.ld + j];
+        if (p >= 0 && p < a.pages) out = a.map[p];
+        else flag(a.err, XP_ERR_BADPAGE);
+      }
+      a.table_out[n * a.ld_out + j] = out;
     }
-    a.table_out[n * a.ld_out + j] = out;
   }
   if (rank == 0 && tid == 0) {
     *a.n_moves = moves;
