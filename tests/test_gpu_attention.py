@@ -262,3 +262,72 @@ def test_refusals():
     with pytest.raises(ValueError):
         code(lens=c.lens_t[:1])
     assert xp.xp_cache_get_error(c.cache.handle) == xp.XP_OK
+
+
+def reference64(c, q):
+    """The fp64 definition on the GPU, one sequence at a time (for sizes the CPU statement is slow at)."""
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).double().cuda()     # noqa: E731
+    kp, vp = dev(c.kp), dev(c.vp)
+    outs, lses = [], []
+    for n, length in enumerate(c.lens):
+        T, heads, D = q.shape[1:]
+        g = heads // kp.shape[1]
+        k = torch.cat([kp, dev(c.tails[n][0])]).repeat_interleave(g, 1)
+        v = torch.cat([vp, dev(c.tails[n][1])]).repeat_interleave(g, 1)
+        score = torch.einsum("thd,jhd->htj", q[n].double(), k) * c.scale
+        sees = c.P + (length - T + 1 + torch.arange(T, device="cuda")).clamp(min=0)
+        score = score.masked_fill(torch.arange(len(k), device="cuda") >= sees[None, :, None], -math.inf)
+        lse = torch.logsumexp(score, -1)
+        p = torch.exp(score - torch.where(lse == -math.inf, 0.0, lse)[..., None])
+        outs.append(torch.einsum("htj,jhd->thd", p, v))
+        lses.append(lse.t())
+    return torch.stack(outs), torch.stack(lses)
+
+
+BATCHES = {
+    # shapes whose units are cut between CTAs in different ways: odd row tiles, one tile of a
+    # prefix, tails of every length, a row tile pair of one sequence, a long tail alone
+    "odd tiles": dict(lens=[(37 * i) % 1500 for i in range(33)], T=5, H=2, G=4, D=128, P=1000, ps=64),
+    "single tokens": dict(lens=[(91 * i) % 900 for i in range(150)], T=1, H=4, G=8, D=64, P=3000, ps=32),
+    "one row": dict(lens=[(53 * i) % 700 for i in range(90)], T=1, H=8, G=1, D=128, P=129, ps=16),
+    "no prefix": dict(lens=[(211 * i) % 2000 for i in range(60)], T=2, H=3, G=3, D=64, P=0, ps=128),
+    "wide blocks": dict(lens=[(331 * i) % 600 for i in range(20)], T=16, H=1, G=20, D=128, P=640, ps=64),
+    "blocks of 130 rows": dict(lens=[5, 500, 129, 257, 0, 64, 1000], T=13, H=2, G=10, D=64, P=77, ps=24),
+    "one long": dict(lens=[0, 20000, 3, 0], T=4, H=2, G=2, D=128, P=20, ps=256),
+    "prefix only": dict(lens=[0] * 70, T=3, H=5, G=2, D=128, P=4100, ps=8),
+    "tiny tails": dict(lens=[i % 3 for i in range(400)], T=1, H=8, G=4, D=128, P=300, ps=16),
+}
+
+
+@pytest.mark.parametrize("name", list(BATCHES))
+def test_batches_match_the_definition(name):
+    c = Case(dtype="bf16", seed=len(name), **BATCHES[name])
+    out, lse = c.run()
+    assert xp.xp_cache_get_error(c.cache.handle) == xp.XP_OK
+    want, want_lse = reference64(c, c.q)
+    empty = want_lse == -math.inf
+    assert torch.equal(lse == -math.inf, empty) and not out[empty].any()
+    # a weight's and the output's rounding to bf16, 2^-9 each: their root mean square over rows of
+    # weights that are spread, three times that for the worst element of |v|max
+    err = out.double() - want
+    scale = want.square().mean().sqrt() + 1e-3
+    assert err.square().mean().sqrt() <= 2.0 ** -8 * 2 * scale
+    assert err.abs().max() <= 2.0 ** -8 * (want.abs().max() + 4.5)
+    assert (lse.double() - want_lse)[~empty].abs().max() <= 2.0 ** -16
+    again = c.run()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_calls_on_two_streams():
+    cases = [Case([700, 30, 5], T=4, D=128, P=900, seed=s) for s in (11, 12)]
+    want = [c.run() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(c.run())
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
