@@ -382,48 +382,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int p = 0; p < 2; ++p)
         if (used[p]) ptx::mbar_wait(ptx::smem_u32(&bars->q_full[p]), (used[p] - 1) & 1, &no_abort, g.err);
     } else if (warp == 18) {
-      // ---- K and V tiles: lane (chunk, box) loads `box` tokens of one page ----
+      // ---- K and V tiles: lane (chunk, box) loads `box` tokens of one page.  The tails' rate is set
+      // by how soon this warp comes to the next load: a copy takes it about 100 cycles to issue
+      // (fewer where its operands are known to be one for the warp), nothing is divided from
+      // tile to tile, and page ids are read two tiles ahead ----
       const uint64_t keep = ptx::policy_evict_last(), stream = ptx::policy_evict_first();
-      const int per = kTile / box, chunk_of = lane / per, in_tile = lane % per * box;
-      int issued = 0;   // tiles loaded
+      const int per = kTile / box, in_tile = lane % per * box, chunk_of = lane / per;
+      const int more = kTile / g.page_size, rest = kTile % g.page_size;   // a tile further
+      const uint32_t place = ring + chunk_of * kChunkBytes + in_tile * 128;
+      int issued = 0, s = 0;   // tiles loaded, the next one's stage
       Frag w;
       bool ok = true;
       for (int f = 0; ok && next_frag(f, &w); ++f) {
         const int32_t* table = w.kind == 0 ? g.prefix_table : g.table + w.n * g.ld_table;
-        const int end = min(w.len, w.t1 * kTile);
-        // this lane's page of key tile j (its box may lie behind the end: then none is loaded)
-        auto page_of = [&](int j) {
-          const int at = j * kTile + in_tile;
-          if (chunk_of >= C::CH || at >= end) return -1;
-          int page = table[at / g.page_size];
-          if (page < 0 || page >= g.pages) {
+        const int end = min(w.len, w.t1 * kTile), hk = (int)uniform(w.hk);
+        const uint64_t policy = uniform(w.kind) == 0 ? keep : stream;
+        // this lane's box of the next key tile to look up: where it is in the table
+        int at = chunk_of < C::CH ? w.t0 * kTile + in_tile : end;
+        int index = at / g.page_size, row = at - index * g.page_size;
+        auto look_up = [&](int* from) {   // the page, -1 behind the end; *from: its row there
+          const int page = at < end ? table[index] : -1;
+          *from = at < end ? row : -1;
+          at += chunk_of < C::CH ? kTile : 0;
+          index += more;
+          row += rest;
+          if (row >= g.page_size) {
+            row -= g.page_size;
+            ++index;
+          }
+          return page;
+        };
+        auto check = [&](int page, int from) {   // at its first use, not when it is asked for
+          if (from >= 0 && (page < 0 || page >= g.pages)) {
             atomicOr(g.err, XP_ERR_BADPAGE);
             page = page < 0 ? 0 : g.pages - 1;
           }
           return page;
         };
-        auto load = [&](int j, int page, const CUtensorMap* map) {
-          const int s = issued % C::STAGES;
+        auto load = [&](int j, int page, int from, const CUtensorMap* map) {
           if (!wait(&bars->empty[s], ((issued / C::STAGES) & 1) ^ 1)) return false;
-          const int key = j * kTile, boxes = (min(kTile, end - key) + box - 1) / box;
-          const uint32_t full = ptx::smem_u32(&bars->full[s]);
-          if (lane == 0) ptx::mbar_arrive_expect_tx(full, boxes * box * 128 * C::CH);
+          const uint32_t full = uniform(ptx::smem_u32(&bars->full[s]));
+          const int rows = (min(kTile, end - j * kTile) + box - 1) & -box;   // a power of two
+          if (lane == 0) ptx::mbar_arrive_expect_tx(full, rows * 128 * C::CH);
           __syncwarp();
-          if (page >= 0)
-            ptx::tma_load_5d(ring + s * C::TILE_BYTES + chunk_of * kChunkBytes + in_tile * 128, map,
-                             full, chunk_of * 64, (key + in_tile) % g.page_size, w.hk, page, g.a.layer,
-                             w.kind == 0 ? keep : stream);
+          if (from >= 0)
+            ptx::tma_load_5d(place + s * C::TILE_BYTES, map, full, C::CH == 1 ? 0 : chunk_of * 64, from,
+                             hk, page, g.a.layer, policy);
           ++issued;
+          s = s + 1 == C::STAGES ? 0 : s + 1;
           return true;
         };
-        int now = page_of(w.t0), next = page_of(w.t0 + 1);   // the page ids are read ahead
-        ok = load(w.t0, now, &tm_k);
+        int row0, row1, row2;
+        int now = look_up(&row0), next = look_up(&row1);
+        now = check(now, row0);
+        ok = load(w.t0, now, row0, &tm_k);
         for (int j = w.t0; j < w.t1 && ok; ++j) {
-          const int after = page_of(j + 2);
-          if (j + 1 < w.t1) ok = load(j + 1, next, &tm_k);
-          ok = ok && load(j, now, &tm_v);
-          now = next;
-          next = after;
+          const int after = look_up(&row2);
+          if (j + 1 < w.t1) {
+            next = check(next, row1);
+            ok = load(j + 1, next, row1, &tm_k);
+          }
+          ok = ok && load(j, now, row0, &tm_v);
+          now = next, row0 = row1;
+          next = after, row1 = row2;
         }
       }
       // nothing may land in shared memory after the CTA is gone: neither the loads nor the
