@@ -452,8 +452,8 @@ xp_status xp_cache_compact(const xp_cache* cache, const int32_t* table, int64_t 
  * h / (heads / kv_heads):
  *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j).
  * The prefix is read once for the whole batch, not once a sequence.  A query that sees
- * nothing gets out = 0 and lse = -inf.  Tokens behind the lengths may hold anything, NaN
- * included; what is visible is assumed finite.
+ * nothing gets out = 0 and lse = -inf.  Tokens behind the lengths may hold anything, and an
+ * infinite or NaN key or value reaches the queries that see it and no others.
  * q, out: cache dtype, element (n, t, h, i) at n*stride_n + t*stride_t + h*stride_h + i.
  * prefix_table: device int32, prefix_pages >= ceil(prefix_len / page_size) entries.  table:
  * device int32, row n at table + n*ld_table, width >= ceil(max_len / page_size) columns.  lens: device [N] int32;

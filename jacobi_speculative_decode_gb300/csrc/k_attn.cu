@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sm100_ptx.cuh"
 #include "xp_device.cuh"
@@ -199,28 +200,36 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
       for (int c = 0; c < NC * 4; ++c) o[i][c] *= keep;
     }
     __syncwarp();   // a row's 16 threads are in one warp
-    // weights times values: dims 4 tx + 64 c
-    for (int j = 0; j < kKeys; j += 4) {
-      float pa[RM][4];
+    // weights times values: dims 4 tx + 64 c.  Where the mask hides keys of this step from some
+    // rows, a hidden key's value is left out, not multiplied by zero: it may be infinite or NaN.
+    auto add = [&](auto some_hidden) {
+      for (int j = 0; j < kKeys; j += 4) {
+        float pa[RM][4];
 #pragma unroll
-      for (int i = 0; i < RM; ++i) {
-        const float4 x = *(const float4*)&sp[(ty * RM + i) * LP + j];
-        pa[i][0] = x.x; pa[i][1] = x.y; pa[i][2] = x.z; pa[i][3] = x.w;
-      }
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float4 x = *(const float4*)&sv[(j + jj) * NC * 64 + c * 64 + tx * 4];
-#pragma unroll
-          for (int i = 0; i < RM; ++i) {
-            o[i][c * 4 + 0] = fmaf(pa[i][jj], x.x, o[i][c * 4 + 0]);
-            o[i][c * 4 + 1] = fmaf(pa[i][jj], x.y, o[i][c * 4 + 1]);
-            o[i][c * 4 + 2] = fmaf(pa[i][jj], x.z, o[i][c * 4 + 2]);
-            o[i][c * 4 + 3] = fmaf(pa[i][jj], x.w, o[i][c * 4 + 3]);
-          }
+        for (int i = 0; i < RM; ++i) {
+          const float4 x = *(const float4*)&sp[(ty * RM + i) * LP + j];
+          pa[i][0] = x.x; pa[i][1] = x.y; pa[i][2] = x.z; pa[i][3] = x.w;
         }
-    }
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float4 x = *(const float4*)&sv[(j + jj) * NC * 64 + c * 64 + tx * 4];
+#pragma unroll
+            for (int i = 0; i < RM; ++i) {
+              if (decltype(some_hidden)::value && kb + j + jj >= s_limit[ty * RM + i]) continue;
+              o[i][c * 4 + 0] = fmaf(pa[i][jj], x.x, o[i][c * 4 + 0]);
+              o[i][c * 4 + 1] = fmaf(pa[i][jj], x.y, o[i][c * 4 + 1]);
+              o[i][c * 4 + 2] = fmaf(pa[i][jj], x.z, o[i][c * 4 + 2]);
+              o[i][c * 4 + 3] = fmaf(pa[i][jj], x.w, o[i][c * 4 + 3]);
+            }
+          }
+      }
+    };
+    if (prefix || kb + kKeys <= keys - g.a.T + 1)
+      add(std::false_type());
+    else
+      add(std::true_type());
   }
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
 #pragma unroll
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
       g.stat[(part * rows + row) * 2 + 1] = l[i];
     }
     float* acc = g.acc + (part * rows + row) * D;
-    if (l[i] > 0.0f) {
+    if (l[i] != 0.0f) {   // NaN where a visible score is
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -257,7 +266,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g)
   float m = -INFINITY;
   for (int p = lane; p < parts; p += 32) {
     const float2 st = *(const float2*)&g.stat[(p * rows + row) * 2];
-    if (st.y > 0.0f) m = fmaxf(m, st.x);
+    if (st.y != 0.0f) m = fmaxf(m, st.x);
   }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g)
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) {
     const float2 st = *(const float2*)&g.stat[(p * rows + row) * 2];
-    if (!(st.y > 0.0f)) continue;   // no key of this range
+    if (st.y == 0.0f) continue;   // no key of this range
     const float w = exp2f(st.x - m);
     l += w * st.y;
     const float* acc = g.acc + (p * rows + row) * D;
@@ -277,12 +286,12 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g)
   }
   const int h = (int)(row % g.a.heads), t = (int)(row / g.a.heads % g.a.T);
   const int n = (int)(row / g.a.heads / g.a.T);
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
   T* out = (T*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h;
 #pragma unroll
   for (int c = 0; c < 8; ++c)
     if (c * 32 + lane < D) out[c * 32 + lane] = from_f<T>(o[c] * inv);
-  if (lane == 0 && g.lse) g.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+  if (lane == 0 && g.lse) g.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
 }
 
 size_t simt_smem(int rm, int nc, int D) {

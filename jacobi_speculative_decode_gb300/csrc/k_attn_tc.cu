@@ -764,13 +764,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// A row's tail from the definition, joined to what its prefix left (maximum *m in base 2, sum *l,
+// weighted values o of this thread's dims).  Hidden keys weigh nothing on the tensor cores, but nothing
+// times an infinite or NaN value is NaN; a row with a NaN in its result comes here, where
+// hidden values are not read.  A thread a row: slow, and for such inputs only.
+template <int D>
+__device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, int t, int h, int warp,
+                                        float* m, float* l, float4* o) {
+  const int end = tail_len(g, n, false) - g.a.T + t + 1;
+  const float c = g.a.scale * 1.44269504088896f;
+  const bf16* q = (const bf16*)g.q + n * g.a.q_stride_n + t * g.a.q_stride_t + h * g.a.q_stride_h;
+  for (int j = 0; j < end; ++j) {
+    const int page = min(max(g.table[n * g.ld_table + j / g.page_size], 0), g.pages - 1);
+    const int64_t at = page * g.kv_page + j % g.page_size * g.kv_token + hk * g.kv_head;
+    const bf16 *k = (const bf16*)g.k + at, *v = (const bf16*)g.v + at;
+    float z = 0.0f;
+#pragma unroll 8
+    for (int d = 0; d < D; ++d) z = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), z);
+    z *= c;
+    const float now = fmaxf(*m, z);
+    if (now == -INFINITY) continue;
+    const float a = exp2f(*m - now), p = exp2f(z - now);
+    *m = now;
+    *l = *l * a + p;
+    for (int i = 0; i < D / 32; ++i) {
+      const bf16* x = v + (warp + 8 * i) * 4;
+      o[i] = make_float4(o[i].x * a + p * __bfloat162float(x[0]), o[i].y * a + p * __bfloat162float(x[1]),
+                         o[i].z * a + p * __bfloat162float(x[2]), o[i].w * a + p * __bfloat162float(x[3]));
+    }
+  }
+}
+
 // A query row's partial results: of the prefix and of its tail, each the unit's own and those of
 // the CTAs at whose beginning it was cut, brought to a common maximum:
 //   out = sum a_p O_p / sum a_p l_p,  a_p = 2^(m_p - m).
 // A CTA joins 32 rows of (sequence, kv head, token, head) order: a thread is a row, a warp every
 // eighth of its 16-byte pieces; the rows leave through shared memory.
 template <int D>
-__global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args g, int ctas) {
+__global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_constant__ xp_attn_args g,
+                                                              int ctas) {
   constexpr int kPer = D / 32;   // 16-byte pieces a thread
   __shared__ __align__(16) uint2 s_out[32][D / 4 + 2];   // rows 16 bytes apart in the banks
   __shared__ bf16* s_to[32];
@@ -788,7 +820,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args
     for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto take = [&](int64_t block, int r) {
       const float2 st = __ldcg((const float2*)g.stat + block * 32 + r);
-      if (!(st.y > 0.0f)) return;   // no visible key in this piece
+      if (st.y == 0.0f) return;   // no visible key in this piece
       float4 x[kPer];
 #pragma unroll
       for (int c = 0; c < kPer; ++c)
@@ -801,11 +833,10 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args
         o[c] = make_float4(o[c].x * a + x[c].x * b, o[c].y * a + x[c].y * b, o[c].z * a + x[c].z * b,
                            o[c].w * a + x[c].w * b);
     };
-    for (int kind = 0; kind < 2; ++kind) {
-      if (kind == 1 && g.a.max_len <= 0) break;
+    auto join = [&](int kind) {
       const Line ln(kind ? g.plan.tail_tiles : g.plan.prefix_tiles,
                     kind ? tail_len(g, n, false) : g.a.prefix_len);
-      if (ln.T == 0) continue;
+      if (ln.T == 0) return;
       const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / kRows, p = tile / 2;
       const int at = (kind ? g.line[1 + n] : 0) + hk * ln.head() + p * ln.unit(0), cost = ln.unit(p);
       // a piece of two row tiles has a half of each, one of a single row tile a half of each
@@ -823,8 +854,29 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args
         take(cut_block(g, c, shared ? tile % 2 : 0) + in_tile, r);
         if (t1 - t0 > 1 && !shared) take(cut_block(g, c, 1) + in_tile, r);
       }
+    };
+    join(0);
+    if (g.a.max_len > 0) {
+      join(1);
+      float all = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) all += o[c].x + o[c].y + o[c].z + o[c].w;
+      if (all != all && l == l && g.a.T > 1) {
+        m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        join(0);
+        float m2 = m, l2 = l;
+        float4 o2[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) o2[c] = o[c];
+        tail_again<D>(g, n, hk, t, h, warp, &m2, &l2, o2);
+        m = m2, l = l2;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) o[c] = o2[c];
+      }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // NaN where a visible score is
 #pragma unroll
     for (int c = 0; c < kPer; ++c)
       s_out[lane][warp + 8 * c] = make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv),
@@ -832,7 +884,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const xp_attn_args
     to = (bf16*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h;
     if (warp == 0 && g.lse)
       g.lse[((int64_t)n * g.a.T + t) * g.a.heads + h] =
-          l > 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+          l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
   }
   if (warp == 0) s_to[lane] = to;
   __syncthreads();

@@ -331,3 +331,53 @@ def test_calls_on_two_streams():
     torch.cuda.synchronize()
     for i, (o, l) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+HIDDEN = {
+    "blocks": dict(lens=[1, 2, 7, 129, 300, 131, 0, 16], T=16, H=2, G=4, D=128, P=70, ps=16),
+    "cut between ranges": dict(lens=[2900, 40], T=16, H=1, G=2, D=64, P=0, ps=32),
+    "row tile pairs": dict(lens=[5, 260, 131, 19], T=20, H=1, G=16, D=128, P=20, ps=64),
+    "row tile pairs narrow": dict(lens=[128, 129, 2000], T=13, H=2, G=20, D=64, P=0, ps=24),
+    "odd width": dict(lens=[70, 5, 64], P=30, T=6, D=40, H=2, G=3, ps=20),
+    "single tokens": dict(lens=[70, 5, 64], P=30, T=1, D=64, H=2, G=3),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(HIDDEN))
+def test_what_is_not_finite_reaches_only_the_rows_that_see_it(name, dtype):
+    c = Case(dtype=dtype, seed=len(name), **HIDDEN[name])
+    out, lse = c.run()
+    T, D, ps = c.T, c.q.shape[3], c.k.shape[2]
+    heads = c.k.shape[3]
+    group = c.q.shape[2] // heads
+    odd = [math.inf, math.nan, -math.inf]
+    place = lambda n, j: (0, int(c.table[n, j // ps]), j % ps)     # noqa: E731
+    sees = lambda n, j: max(0, min(T, j - c.lens[n] + T))          # first row that sees token j  # noqa: E731
+    want = out.clone()
+    for n, length in enumerate(c.lens):          # values of the last, third last and first tokens
+        for i, j in enumerate(sorted({length - 1, length - 3, 0})):
+            if 0 <= j < length:
+                h, d = (n + i) % heads, (7 * n + 11 * i) % D
+                c.v[place(n, j)][h, d] = odd[(n + i) % 3]
+                want[n, sees(n, j):, h * group:(h + 1) * group, d] += odd[(n + i) % 3]
+    def same(got):
+        # a row whose own block held such a value may have been summed in another order, with its
+        # weights unrounded: as far off as two roundings of a weight and of the output to bf16
+        eps = 2.0 ** -16 if dtype == "f32" else 2.0 ** -7
+        for x, y, bound in zip(got, (want, lse), (eps * 5, 2.0 ** -16)):
+            assert torch.equal(x.isnan(), y.isnan()) and torch.equal(x.isinf(), y.isinf())
+            assert torch.equal(x[x.isinf()], y[y.isinf()])
+            fine = x.isfinite()
+            assert ((x - y)[fine].abs() <= bound).all()
+
+    same(c.run())
+    lse = lse.clone()
+    for n, length in enumerate(c.lens):          # a key of the last token, of one head
+        if length:
+            c.k[place(n, length - 1)][n % heads, 3] = math.nan
+            rows = (n, slice(sees(n, length - 1), None), slice(n % heads * group, (n % heads + 1) * group))
+            want[rows] = math.nan
+            lse[rows] = math.nan
+    same(c.run())
+    assert xp.xp_cache_get_error(c.cache.handle) == xp.XP_OK
