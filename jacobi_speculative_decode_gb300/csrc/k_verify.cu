@@ -638,7 +638,7 @@ __device__ unsigned long long race(const Race& r, const T* t_row, const float* d
 // Work items (block, chunk): the race of every id of the chunk, merged into the block's best;
 // the block's last chunk writes its tokens and clears its counters for the next call.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const xp_verify_args a, int chunk) {
+__global__ void __launch_bounds__(kThreads, 5) verify_draw_kernel(const xp_verify_args a, int chunk) {
   __shared__ unsigned long long s_best;
   __shared__ int s_last;
   ptx::pdl_wait();
@@ -710,7 +710,7 @@ int chunk_of(int64_t rows, int V, int64_t workers, int most, int least) {
   return chunk;
 }
 constexpr int kMostIds = 65536, kLeastIds = 8192;
-constexpr int kMostRace = 16384, kLeastRace = 2048;
+constexpr int kMostRace = 32768, kLeastRace = 2048;
 
 }  // namespace
 
