@@ -13,6 +13,19 @@
 // Warps: 0-7 and 8-15 the softmax of stream 0 and 1 (a warp is 16 query rows, four lanes a row),
 // 16 and 17 issue their products, 18 loads K and V by TMA, a box of tokens of one page at a
 // time, 19 cuts the work and loads the queries.
+//
+// What bounds it.  Two row tiles against 128 keys of 128 dims are 16.8 MFLOP, and 256 KB of
+// shared memory read by the products: 2,048 cycles either way.  A pair of tiles takes 2,700 to
+// 2,800, as each stream's chain is as long: S 512, softmax to the first half of P 990 and to the
+// second 550, the second half of P V 256, and about 100 for each of four hand-overs.  128
+// blocks of 16 tokens, 32 heads of 128 over 8, behind a shared prefix of 8192 and tails up to
+// 2048 (309 GFLOP, 608 MB): 265 to 285 us, 1.1 to 1.2 PFLOP/s, 58-62% of measured.
+// A tail of few rows is bound by one tile's chain, 1,080 cycles a tile of 128 keys with two
+// streams, and by what a unit costs at its ends (about 5,000 cycles: a masked tile, the last
+// product, the result's way out, code and constants that must be fetched anew).  256 single tokens,
+// 64 heads of 64 over 8, a prefix of 16384 and tails up to 2000 (588 MB): 198 us, 2.97 TB/s.
+// Tiles of 128 rows: 64 would halve the operand A's reuse of every K and V read from shared
+// memory; two streams of 128 columns of scores and D of results fill tensor memory at D = 128.
 #include <math.h>
 
 #include <algorithm>
@@ -69,10 +82,12 @@ struct Bars {
 };
 
 // The work is one line of cost: prefix units (kv head, pair of row tiles), then the units of
-// each sequence's tail, a unit costing kUnitCost and kPairCost or kTileCost a key tile.  CTA i does [i*chunk, (i+1)*chunk) of it, so that a unit may be cut anywhere between
-// two of its tiles and every CTA gets the same.  A piece that begins its unit leaves its
-// result in the unit's place, one that does not in the place of its CTA, of which there is
-// at most one.
+// each sequence's tail, a unit costing kUnitCost and kPairCost or kTileCost a key tile.  CTA i
+// does [i*chunk, (i+1)*chunk) of it, so that a unit may be cut anywhere between two of its
+// tiles and every CTA gets the same.  A piece that begins its unit leaves its result in the
+// unit's place, one that does not in the place of its CTA, of which there is at most one.
+// (A fixed grid of units and key ranges took 380 us where this takes 285: its last wave was half
+// empty.  Costs from 8/3/8 to 8/7/24 were timed; 8/5/12 is best or within 3% of it everywhere.)
 struct Line {
   int pairs, odd, T;       // row tiles as pairs and one over; key tiles
   __host__ __device__ Line(int row_tiles, int keys)
@@ -799,7 +814,9 @@ __device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, in
 // the CTAs at whose beginning it was cut, brought to a common maximum:
 //   out = sum a_p O_p / sum a_p l_p,  a_p = 2^(m_p - m).
 // A CTA joins 32 rows of (sequence, kv head, token, head) order: a thread is a row, a warp every
-// eighth of its 16-byte pieces; the rows leave through shared memory.
+// eighth of its 16-byte pieces; the rows leave through shared memory.  Bound by the partial
+// results' bytes, mostly from L2: 65,536 rows of 128 with three or four each, about 110 MB, in
+// 24 us.
 template <int D>
 __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_constant__ xp_attn_args g,
                                                               int ctas) {

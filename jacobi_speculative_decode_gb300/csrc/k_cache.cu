@@ -411,6 +411,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyArgs
     const int64_t keep = a.tokens ? a.tokens[i] * a.token_bytes : a.seg_bytes;
     // a page of one segment has nothing to copy behind its tokens
     if (a.seg_bytes == a.block_bytes && (int64_t)c * kChunk >= keep) continue;
+    // which bytes move: no division where a page is one segment, or moves whole
+    const bool plain = a.seg_bytes == a.block_bytes || keep == a.seg_bytes;
+    const int64_t end = keep == a.seg_bytes ? a.block_bytes : plain ? keep : a.block_bytes;
+    auto moves = [&](int64_t o) { return o < end && (plain || o % a.seg_bytes < keep); };
     char* pool = plane & 1 ? a.v : a.k;
     pool += (plane >> 1) * a.layer_bytes;
     const char* from = pool + sp * a.page_bytes;
@@ -420,12 +424,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyArgs
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
       const int64_t o = at + (int64_t)k * kCopyThreads * sizeof(U);
-      if (o < a.block_bytes && o % a.seg_bytes < keep) val[k] = *(const U*)(from + o);
+      if (moves(o)) val[k] = *(const U*)(from + o);
     }
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
       const int64_t o = at + (int64_t)k * kCopyThreads * sizeof(U);
-      if (o < a.block_bytes && o % a.seg_bytes < keep) *(U*)(to + o) = val[k];
+      if (moves(o)) *(U*)(to + o) = val[k];
     }
   }
 }
@@ -445,7 +449,10 @@ struct AppendArgs {
   uint32_t* err;
 };
 
-template <typename T>
+// U: the unit that all rows, strides and bases are whole numbers of (16 bytes, or one element).
+// Half a warp moves K and half V, so that the 256 bytes of a row of 128 bf16 leave in one
+// instruction of each.
+template <typename U>
 __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   const int64_t w = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
@@ -464,10 +471,9 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   }
   const int64_t from = n * a.sn + t * a.st + h * a.sh;
   const int64_t to = p * a.page + pos % a.ps * a.token + h * a.head;
-  for (int i = lane; i < a.D; i += 32) {
-    ((T*)a.kp)[to + i] = ((const T*)a.k)[from + i];
-    ((T*)a.vp)[to + i] = ((const T*)a.v)[from + i];
-  }
+  const U* src = (const U*)(lane < 16 ? a.k : a.v) + from;
+  U* dst = (U*)(lane < 16 ? a.kp : a.vp) + to;
+  for (int i = lane % 16; i < a.D; i += 16) dst[i] = src[i];
 }
 
 }  // namespace
@@ -477,14 +483,19 @@ cudaError_t xp_launch_append(const xp_cache* c, int layer, const void* k, const 
                              const int32_t* lens, int N, int T, cudaStream_t s) {
   const xp_cache_desc& d = c->d;
   const size_t es = xp_elem(d.dtype);
-  AppendArgs a = {k, v, sn, st, sh,
-                  (char*)d.k + layer * d.stride_layer * es, (char*)d.v + layer * d.stride_layer * es,
-                  d.stride_page, d.stride_token, d.stride_head, table, ld, lens, N, T, d.kv_heads,
-                  d.head_dim, d.page_size, d.pages, c->err};
+  char *kp = (char*)d.k + layer * d.stride_layer * es, *vp = (char*)d.v + layer * d.stride_layer * es;
+  const int64_t strides = sn | st | sh | d.stride_page | d.stride_token | d.stride_head | d.head_dim;
+  const bool wide = (((uintptr_t)k | (uintptr_t)v | (uintptr_t)kp | (uintptr_t)vp) & 15) == 0 &&
+                    strides * (int64_t)es % 16 == 0;
+  const int64_t unit = wide ? 16 / (int64_t)es : 1;   // elements
+  AppendArgs a = {k, v, sn / unit, st / unit, sh / unit, kp, vp, d.stride_page / unit,
+                  d.stride_token / unit, d.stride_head / unit, table, ld, lens, N, T, d.kv_heads,
+                  d.head_dim / (int)unit, d.page_size, d.pages, c->err};
   const int64_t warps = (int64_t)N * T * d.kv_heads;
   const unsigned grid = (unsigned)((warps + 7) / 8);
-  if (d.dtype == XP_BF16) append_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  else append_kernel<float><<<grid, 256, 0, s>>>(a);
+  if (wide) append_kernel<uint4><<<grid, 256, 0, s>>>(a);
+  else if (d.dtype == XP_BF16) append_kernel<uint16_t><<<grid, 256, 0, s>>>(a);
+  else append_kernel<uint32_t><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
