@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
   const int D = g.dim, DP = (D + 3) / 4 * 4, LD = DP + 4;
   float* sq = smem;                      // [BM][LD]
   float* sk = sq + BM * LD;              // [kKeys][LD]
-  float* sv = sk + kKeys * LD;           // [kKeys][NC * 64]
-  float* sp = sv + kKeys * NC * 64;      // [BM][kKeys + 4]
+  float* sv = sk + kKeys * LD;           // [kKeys][DP]; dims behind a row's end: the next row's, or sp
+  float* sp = sv + kKeys * DP;           // [BM][kKeys + 4]
   constexpr int LP = kKeys + 4;
   __shared__ int s_limit[BM];            // keys each row sees
   __shared__ int64_t s_at[kKeys];        // where each key begins in the pools, -1 behind the range
@@ -136,13 +136,13 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
       s_at[tid] = at;
     }
     __syncthreads();
-    for (int d = (tid & 31) * 4; d < NC * 64; d += 128) {
+    for (int d = (tid & 31) * 4; d < DP; d += 128) {
       float4 kx[kKeys / 8], vx[kKeys / 8];
 #pragma unroll
       for (int i = 0; i < kKeys / 8; ++i) {
         const int64_t at = s_at[(tid >> 5) + 8 * i];
         kx[i] = vx[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (at >= 0 && d < D) {   // tokens behind the length are not read
+        if (at >= 0) {   // tokens behind the length are not read
           kx[i] = load4((const T*)g.k + at + d, wide, D - d);
           vx[i] = load4((const T*)g.v + at + d, wide, D - d);
         }
@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
 #pragma unroll
       for (int i = 0; i < kKeys / 8; ++i) {
         const int j = (tid >> 5) + 8 * i;
-        if (d < DP) *(float4*)&sk[j * LD + d] = kx[i];
-        *(float4*)&sv[j * NC * 64 + d] = vx[i];
+        *(float4*)&sk[j * LD + d] = kx[i];
+        *(float4*)&sv[j * DP + d] = vx[i];
       }
     }
     __syncthreads();
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args 
         for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const float4 x = *(const float4*)&sv[(j + jj) * NC * 64 + c * 64 + tx * 4];
+            const float4 x = *(const float4*)&sv[(j + jj) * DP + c * 64 + tx * 4];
 #pragma unroll
             for (int i = 0; i < RM; ++i) {
               if (decltype(some_hidden)::value && kb + j + jj >= s_limit[ty * RM + i]) continue;
@@ -299,18 +299,18 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g)
   if (lane == 0 && g.lse) g.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
 }
 
-size_t simt_smem(int rm, int nc, int D) {
-  const int LD = (D + 3) / 4 * 4 + 4, BM = 16 * rm;
-  return sizeof(float) * ((size_t)BM * LD + kKeys * LD + kKeys * nc * 64 + BM * (kKeys + 4));
+size_t simt_smem(int rm, int D) {
+  const int DP = (D + 3) / 4 * 4, LD = DP + 4, BM = 16 * rm;
+  return sizeof(float) * ((size_t)BM * LD + kKeys * LD + kKeys * DP + BM * (kKeys + 4));
 }
 
 template <typename T, int RM, int NC>
 cudaError_t launch(const xp_attn_args& g, cudaStream_t s) {
-  const size_t smem = simt_smem(RM, NC, g.dim);
+  const size_t smem = simt_smem(RM, g.dim);
   // the widest head of this instantiation, so that one call covers them all
   static unsigned long long allowed = 0;
   const cudaError_t e = xp_allow_smem((const void*)attn_simt_kernel<T, RM, NC>,
-                                      simt_smem(RM, NC, NC * 64), &allowed);
+                                      simt_smem(RM, NC * 64), &allowed);
   if (e != cudaSuccess) return e;
   const xp_attn_plan& p = g.plan;
   const dim3 grid(p.prefix_tiles * p.prefix_splits + g.a.N * p.tail_tiles * p.tail_splits,
