@@ -55,7 +55,7 @@ __device__ __forceinline__ float4 load4(const bf16* p, bool wide, int n) {
 // CTAs an SM have work: 7 sequences of 5 tokens, 12 heads of 96 over 3, prefix 1001, tails up to
 // 333: 34.5 us both kernels (46 with ranges of at least four steps).
 template <typename T, int RM, int NC>
-__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const xp_attn_args g,
+__global__ void __launch_bounds__(kThreads, RM <= 2 ? 2 : 1) attn_simt_kernel(const xp_attn_args g,
                                                              bool wide) {
   constexpr int BM = 16 * RM;
   extern __shared__ __align__(16) float smem[];
@@ -278,17 +278,23 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g)
   float o[8], l = 0.0f;
 #pragma unroll
   for (int c = 0; c < 8; ++c) o[c] = 0.0f;
+  for (int p0 = 0; p0 < parts; p0 += 32) {   // a lane a range's weight, then all ranges' results
+    float2 st = make_float2(0.0f, 0.0f);
+    if (p0 + lane < parts) st = *(const float2*)&g.stat[((p0 + lane) * rows + row) * 2];
+    const float mine = st.y != 0.0f ? exp2f(st.x - m) : 0.0f;   // 0: no key of this range
+    l += mine * st.y;
+    const int n = min(32, parts - p0);
 #pragma unroll 4
-  for (int p = 0; p < parts; ++p) {
-    const float2 st = *(const float2*)&g.stat[(p * rows + row) * 2];
-    if (st.y == 0.0f) continue;   // no key of this range
-    const float w = exp2f(st.x - m);
-    l += w * st.y;
-    const float* acc = g.acc + (p * rows + row) * D;
+    for (int p = 0; p < n; ++p) {
+      const float w = __shfl_sync(0xFFFFFFFFu, mine, p);
+      const float* acc = g.acc + ((p0 + p) * rows + row) * D;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (c * 32 + lane < D) o[c] = fmaf(w, acc[c * 32 + lane], o[c]);
+      for (int c = 0; c < 8; ++c)
+        if (w != 0.0f && c * 32 + lane < D) o[c] = fmaf(w, acc[c * 32 + lane], o[c]);
+    }
   }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
   const int h = (int)(row % g.a.heads), t = (int)(row / g.a.heads % g.a.T);
   const int n = (int)(row / g.a.heads / g.a.T);
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;
