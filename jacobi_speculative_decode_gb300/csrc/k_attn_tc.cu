@@ -98,8 +98,9 @@ struct Line {
   __host__ __device__ int head() const { return T ? pairs * unit(0) + odd * unit(pairs) : 0; }
   // first tile of unit p that lies behind a cost of x from the unit's beginning
   __host__ __device__ int tile_at(int p, int x) const {
-    const int w = tile_cost(p), t = (x - kUnitCost + w - 1) / w;
-    return x <= kUnitCost ? 0 : t > T ? T : t;
+    const int y = x - kUnitCost;   // both divisors known: no division at run time
+    const int t = p < pairs ? (y + kPairCost - 1) / kPairCost : (y + kTileCost - 1) / kTileCost;
+    return y <= 0 ? 0 : t > T ? T : t;
   }
 };
 
@@ -817,7 +818,11 @@ __device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, in
 // eighth of its 16-byte pieces; the rows leave through shared memory.  Bound by the partial
 // results' bytes, mostly from L2: 65,536 rows of 128 with three or four each, about 110 MB, in
 // 24 us.
-template <int D>
+// TOGETHER: partial results asked for at once.  Few rows have many (a long prefix is cut by every
+// CTA) and nobody else's work to wait under: four at once take 16.4 us where one takes 17.3 (both
+// kernels, one request of 4 tokens).  Many rows have three or four, and one at a time leaves
+// room for more CTAs: 266 us and 274 (128 blocks of 16 tokens).
+template <int D, int TOGETHER>
 __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_constant__ xp_attn_args g,
                                                               int ctas) {
   constexpr int kPer = D / 32;   // 16-byte pieces a thread
@@ -835,21 +840,6 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
     float4 o[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto take = [&](int64_t block, int r) {
-      const float2 st = __ldcg((const float2*)g.stat + block * 32 + r);
-      if (st.y == 0.0f) return;   // no visible key in this piece
-      float4 x[kPer];
-#pragma unroll
-      for (int c = 0; c < kPer; ++c)
-        x[c] = __ldcs((const float4*)g.acc + (block * (D / 4) + warp + 8 * c) * 32 + r);
-      const float now = fmaxf(m, st.x), a = exp2f(m - now), b = exp2f(st.x - now);
-      m = now;
-      l = l * a + st.y * b;
-#pragma unroll
-      for (int c = 0; c < kPer; ++c)
-        o[c] = make_float4(o[c].x * a + x[c].x * b, o[c].y * a + x[c].y * b, o[c].z * a + x[c].z * b,
-                           o[c].w * a + x[c].w * b);
-    };
     auto join = [&](int kind) {
       const Line ln(kind ? g.plan.tail_tiles : g.plan.prefix_tiles,
                     kind ? tail_len(g, n, false) : g.a.prefix_len);
@@ -862,14 +852,44 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
       const int in_tile = at_row % kRows / 32, r = at_row % 32;
       int cut = (at / chunk + 1) * chunk - at;   // where the unit is first cut,
       if (ln.tile_at(p, cut) == 0) cut += chunk;       // behind its first tile
-      const int first = ln.tile_at(p, min(cut, cost));
-      if (first > 0) take(block_of(g, kind, n, hk) + at_row / 32, r);
-      if (first > 1 && !shared) take(second_block_of(g, kind, n, hk) + in_tile, r);
-      for (int c = at / chunk + 1; c < ctas && c * chunk < at + cost; ++c) {
-        const int t0 = ln.tile_at(p, c * chunk - at), t1 = ln.tile_at(p, min((c + 1) * chunk - at, cost));
-        if (t0 == 0 || t0 >= t1) continue;
-        take(cut_block(g, c, shared ? tile % 2 : 0) + in_tile, r);
-        if (t1 - t0 > 1 && !shared) take(cut_block(g, c, 1) + in_tile, r);
+      const int first = ln.tile_at(p, min(cut, cost)), cta0 = at / chunk + 1;
+      const int cuts = max(0, min(ctas - 1, (at + cost - 1) / chunk) - cta0 + 1);
+      const int64_t own = block_of(g, kind, n, hk) + at_row / 32;
+      const int64_t second = second_block_of(g, kind, n, hk) + in_tile;
+      const int64_t cut0 = cut_block(g, cta0, 0) + in_tile;
+      // the block of piece q: the unit's own (and its second), then those of the CTAs; -1: none
+      auto block = [&](int q) -> int64_t {
+        if (q == 0) return first > 0 ? own : -1;
+        if (q == 1 && !shared) return first > 1 ? second : -1;
+        const int c = shared ? q - 1 : (q - 2) / 2, half = shared ? tile % 2 : q % 2;
+        const int x = (cta0 + c) * chunk - at, t0 = ln.tile_at(p, x), t1 = ln.tile_at(p, min(x + chunk, cost));
+        return t0 == 0 || t0 >= t1 || (!shared && half && t1 - t0 < 2) ? -1 : cut0 + c * 8 + half * 4;
+      };
+      const int pieces = shared ? 1 + cuts : 2 + 2 * cuts;
+      for (int q = 0; q < pieces; q += TOGETHER) {
+        float2 st[TOGETHER];
+        float4 x[TOGETHER][kPer];
+#pragma unroll
+        for (int u = 0; u < TOGETHER; ++u) {
+          const int64_t b = q + u < pieces ? block(q + u) : -1;
+          st[u] = make_float2(0.0f, 0.0f);
+          if (b < 0) continue;
+          st[u] = __ldcg((const float2*)g.stat + b * 32 + r);
+#pragma unroll
+          for (int c = 0; c < kPer; ++c)
+            x[u][c] = __ldcs((const float4*)g.acc + (b * (D / 4) + warp + 8 * c) * 32 + r);
+        }
+#pragma unroll
+        for (int u = 0; u < TOGETHER; ++u) {
+          if (st[u].y == 0.0f) continue;   // no visible key in this piece: x may be anything
+          const float now = fmaxf(m, st[u].x), a = exp2f(m - now), b = exp2f(st[u].x - now);
+          m = now;
+          l = l * a + st[u].y * b;
+#pragma unroll
+          for (int c = 0; c < kPer; ++c)
+            o[c] = make_float4(o[c].x * a + x[u][c].x * b, o[c].y * a + x[u][c].y * b,
+                               o[c].z * a + x[u][c].z * b, o[c].w * a + x[u][c].w * b);
+        }
       }
     };
     join(0);
@@ -948,8 +968,9 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
-  return xp_launch_pdl(attn_tc_combine_kernel<D>, dim3((unsigned)((rows + 31) / 32)), dim3(256), 0, s, g,
-                       c->num_sms);
+  const unsigned grid = (unsigned)((rows + 31) / 32);
+  return xp_launch_pdl(grid <= (unsigned)c->num_sms ? attn_tc_combine_kernel<D, 4> : attn_tc_combine_kernel<D, 1>,
+                       dim3(grid), dim3(256), 0, s, g, c->num_sms);
 }
 
 }  // namespace
