@@ -157,7 +157,7 @@ __device__ __forceinline__ int pos_v(int j, int T) { return j < T - 1 ? 2 * j + 
 // number of keys it sees
 __device__ __forceinline__ int64_t row_of(const xp_attn_args& g, const Frag& w, int tile, int r, int* n,
                                           int* t, int* h, int* limit) {
-  const int per_seq = g.a.T * g.group, i = tile * kRows + r;
+  const int per_seq = g.a.T * g.group, i = tile * g.plan.rows_tile + r;
   *limit = 0;
   if (i >= (w.kind == 0 ? g.a.N * per_seq : per_seq)) return -1;
   *n = w.kind == 0 ? i / per_seq : w.n;
@@ -171,13 +171,12 @@ __device__ __forceinline__ int64_t row_of(const xp_attn_args& g, const Frag& w, 
 // reads them 512 bytes at a time: the prefix's by kv head, each sequence's by kv head, the same
 // again for stream 1 of the one row tile of each that both streams work on, then 8 blocks for
 // every CTA's piece that does not begin its unit.
-__device__ __forceinline__ int64_t per_seq_of(const xp_attn_args& g) { return g.a.T * g.group; }
 __device__ __forceinline__ int64_t block_of(const xp_attn_args& g, int kind, int n, int hk) {
-  const int64_t all = (g.a.N * per_seq_of(g) + 31) / 32, one = (per_seq_of(g) + 31) / 32;
-  return kind == 0 ? hk * all : g.kv_heads * all + ((int64_t)n * g.kv_heads + hk) * one;
+  const int64_t all = g.plan.prefix_blocks;
+  return kind == 0 ? hk * all : g.kv_heads * all + ((int64_t)n * g.kv_heads + hk) * g.plan.tail_blocks;
 }
 __device__ __forceinline__ int64_t second_block_of(const xp_attn_args& g, int kind, int n, int hk) {
-  const int64_t one = min((per_seq_of(g) + 31) / 32, (int64_t)4);
+  const int64_t one = min(g.plan.tail_blocks, 4);
   return block_of(g, 1, g.a.N, 0) + (kind == 0 ? hk * 4 : g.kv_heads * 4 + ((int64_t)n * g.kv_heads + hk) * one);
 }
 __device__ __forceinline__ int64_t cut_block(const xp_attn_args& g, int64_t cta, int half) {
@@ -316,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&bars->q_empty[place], (used[place] & 1) ^ 1)) return false;
         ++used[place];
         uint8_t* dst = smem + place * C::TILE_BYTES;
-        if (q_tma) {   // 128 / group tokens of all the group's heads
+        if (q_tma) {   // whole tokens, all the group's heads of each
           if (lane == 0) {
             const uint32_t bar = ptx::smem_u32(&bars->q_full[place]);
-            const int token = (w.kind == 0 ? 0 : w.n * g.a.T) + tile * (kRows / g.group);
-            ptx::mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+            const int token = (w.kind == 0 ? 0 : w.n * g.a.T) + tile * (g.plan.rows_tile / g.group);
+            ptx::mbar_arrive_expect_tx(bar, g.plan.rows_tile * 128 * C::CH);
             for (int ch = 0; ch < C::CH; ++ch)
               ptx::tma_load_4d(ptx::smem_u32(dst + ch * kChunkBytes), &tm_q, bar, ch * 64, 0, w.hk, token,
                                once);
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           return true;
         }
-        for (int r = lane; r < kRows; r += 32) {
+        for (int r = lane; r < g.plan.rows_tile; r += 32) {
           int n, t, h, lim;
           if (row_of(g, w, tile, r, &n, &t, &h, &lim) < 0) break;   // rows behind the end: anything
           const uint16_t* src = (const uint16_t*)g.q + n * g.a.q_stride_n + t * g.a.q_stride_t +
@@ -599,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = warp % 4 * 32 + warp / 4 % 2 * 16 + lane / 4;      // and r0 + 8
     const uint32_t lanes = (uint32_t)(r0 - lane / 4) << 16;
     const float c = g.a.scale * 1.44269504088896f;
-    const int all_rows = g.a.N * g.a.T * g.group;
+    const int all_rows = g.a.N * g.a.T * g.group, RT = g.plan.rows_tile;
     int done = 0, known = -1, token[2] = {0, 0};   // the rows' tokens in a tail's row tile `known`
     Frag w;
     bool ok = true;
@@ -613,11 +612,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w.kind == 1 && tile != known) {
         known = tile;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) token[i] = (tile * kRows + r0 + 8 * i) / g.group;
+        for (int i = 0; i < 2; ++i) token[i] = (tile * RT + r0 + 8 * i) / g.group;
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const bool is_row = w.kind == 0 ? tile * kRows + r0 + 8 * i < all_rows : token[i] < g.a.T;
+        const bool is_row = r0 + 8 * i < RT && (w.kind == 0 ? tile * RT + r0 + 8 * i < all_rows : token[i] < g.a.T);
         limit[i] = is_row && w.kind == 1 ? min(w.len - g.a.T + token[i] + 1, end) : end;
         any_row |= is_row;   // rows behind the end ask for no mask
       }
@@ -835,7 +834,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
   if (e < rows) {
     const int i = (int)(e % per_seq), hk = (int)(e / per_seq % g.kv_heads);
     const int n = (int)(e / per_seq / g.kv_heads), t = i / g.group, h = hk * g.group + i % g.group;
-    const int chunk = g.line[0];
+    const int chunk = g.line[0], RT = g.plan.rows_tile;
     float m = -INFINITY, l = 0.0f;
     float4 o[kPer];
 #pragma unroll
@@ -844,17 +843,17 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
       const Line ln(kind ? g.plan.tail_tiles : g.plan.prefix_tiles,
                     kind ? tail_len(g, n, false) : g.a.prefix_len);
       if (ln.T == 0) return;
-      const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / kRows, p = tile / 2;
+      const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / RT, p = tile / 2;
       const int at = (kind ? g.line[1 + n] : 0) + hk * ln.head() + p * ln.unit(0), cost = ln.unit(p);
       // a piece of two row tiles has a half of each, one of a single row tile a half of each
       // stream (the second from two key tiles on)
       const bool shared = p < ln.pairs;
-      const int in_tile = at_row % kRows / 32, r = at_row % 32;
+      const int in_tile = at_row % RT / 32, r = at_row % RT % 32;
       int cut = (at / chunk + 1) * chunk - at;   // where the unit is first cut,
       if (ln.tile_at(p, cut) == 0) cut += chunk;       // behind its first tile
       const int first = ln.tile_at(p, min(cut, cost)), cta0 = at / chunk + 1;
       const int cuts = max(0, min(ctas - 1, (at + cost - 1) / chunk) - cta0 + 1);
-      const int64_t own = block_of(g, kind, n, hk) + at_row / 32;
+      const int64_t own = block_of(g, kind, n, hk) + tile * 4 + in_tile;
       const int64_t second = second_block_of(g, kind, n, hk) + in_tile;
       const int64_t cut0 = cut_block(g, cta0, 0) + in_tile;
       // the block of piece q: the unit's own (and its second), then those of the CTAs; -1: none
@@ -949,7 +948,7 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   // Queries by TMA where a tile is a whole number of tokens, one stride apart; else by loads.
   CUtensorMap tm_q = {};
   const int64_t token = g.a.T > 1 ? g.a.q_stride_t : g.a.q_stride_n;
-  bool q_tma = kRows % g.group == 0 && (g.a.T == 1 || g.a.N == 1 || g.a.q_stride_n == g.a.T * token) &&
+  bool q_tma = g.group <= kRows && (g.a.T == 1 || g.a.N == 1 || g.a.q_stride_n == g.a.T * token) &&
                (uintptr_t)g.q % 16 == 0 && token % 8 == 0 && g.a.q_stride_h % 8 == 0 && token > 0 &&
                g.a.q_stride_h > 0;
   if (q_tma) {
@@ -957,7 +956,7 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
                                 (cuuint64_t)g.a.N * g.a.T};
     const cuuint64_t strides[3] = {(cuuint64_t)g.a.q_stride_h * 2,
                                    (cuuint64_t)g.a.q_stride_h * 2 * g.group, (cuuint64_t)token * 2};
-    const cuuint32_t boxes[4] = {64, (cuuint32_t)g.group, 1, (cuuint32_t)(kRows / g.group)};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)g.group, 1, (cuuint32_t)(g.plan.rows_tile / g.group)};
     const cuuint32_t es[4] = {1, 1, 1, 1};
     q_tma = xp_get_encode_tiled()(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void*)g.q, dims, strides,
                                   boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1013,12 +1012,18 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
   xp_attn_plan p = {};
   p.tc = true;
   const int per_seq = a->T * (a->heads / c->d.kv_heads);
-  p.rows_tile = kRows;
-  p.prefix_tiles = (int)(((int64_t)a->N * per_seq + kRows - 1) / kRows);
-  p.tail_tiles = (per_seq + kRows - 1) / kRows;
+  // Whole tokens, so that a tile's queries are one box: loaded by plain loads instead (tiles of 128
+  // rows for every group), a tile took one warp 20 us, and 80 single tokens of groups of 7 111 us.
+  const int group = a->heads / c->d.kv_heads, RT = group <= kRows ? kRows / group * group : kRows;
+  p.rows_tile = RT;
+  p.prefix_tiles = (int)(((int64_t)a->N * per_seq + RT - 1) / RT);
+  p.tail_tiles = (per_seq + RT - 1) / RT;
+  auto row_blocks = [&](int64_t rows) { return (int)(rows / RT * 4 + (rows % RT + 31) / 32); };
+  p.prefix_blocks = row_blocks((int64_t)a->N * per_seq);
+  p.tail_blocks = row_blocks(per_seq);
   const size_t H = c->d.kv_heads, D = c->d.head_dim;
-  const size_t one = (per_seq + 31) / 32;
-  const size_t blocks = H * (((size_t)a->N * per_seq + 31) / 32) + a->N * H * one + H * 4 +
+  const size_t one = p.tail_blocks;
+  const size_t blocks = H * p.prefix_blocks + a->N * H * one + H * 4 +
                         a->N * H * std::min<size_t>(one, 4) + (size_t)c->num_sms * 8;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
