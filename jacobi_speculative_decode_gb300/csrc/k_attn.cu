@@ -53,7 +53,7 @@ __device__ __forceinline__ float4 load4(const bf16* p, bool wide, int n) {
 // For large calls the fp32 multiply-adds bound it; for small ones the latency of a step's loads
 // (page ids, then keys and values), so key ranges are as short as one step of 64 keys until two
 // CTAs an SM have work: 7 sequences of 5 tokens, 12 heads of 96 over 3, prefix 1001, tails up to
-// 333: 34.5 us both kernels (46 with ranges of at least four steps).
+// 333: 33.3 us both kernels (84 with loads of single elements and longer ranges).
 template <typename T, int RM, int NC>
 __global__ void __launch_bounds__(kThreads, RM <= 2 ? 2 : 1) attn_simt_kernel(const xp_attn_args g,
                                                              bool wide) {

