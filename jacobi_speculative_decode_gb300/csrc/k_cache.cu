@@ -217,6 +217,7 @@ struct ForkArgs {
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     fork_kernel(const ForkArgs a) {
   __shared__ Scan s;
+  ptx::pdl_trigger();   // the next kernel's CTAs come up as this one's leave, and wait there
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tid = (int)threadIdx.x;
   const int r0 = (int)((int64_t)a.M * rank / kCtas), r1 = (int)((int64_t)a.M * (rank + 1) / kCtas);
@@ -309,6 +310,7 @@ struct CompactArgs {
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     compact_kernel(const CompactArgs a) {
   __shared__ Scan s;
+  ptx::pdl_trigger();   // the next kernel's CTAs come up as this one's leave, and wait there
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tid = (int)threadIdx.x;
   const int r0 = (int)((int64_t)a.N * rank / kCtas), r1 = (int)((int64_t)a.N * (rank + 1) / kCtas);
