@@ -56,14 +56,17 @@ struct Cfg {
 };
 
 constexpr int kFrags = 4;       // fragments announced ahead
-// cost of a key tile for two row tiles, for one, and of a unit besides its tiles (ns / 180)
-constexpr int kPairCost = 8, kTileCost = 5, kUnitCost = 12;
+// What a unit of work is: two row tiles of one kv head, one row tile of each of two kv heads, one
+// row tile of one
+enum { kRowPair, kHeadPair, kSingle, kUnitKinds };
+// cost of a key tile for each, and of a unit besides its tiles (ns / 180)
+constexpr int kPairCost = 8, kHeadsCost = 9, kTileCost = 5, kUnitCost = 12;
 constexpr int kMinChunk = kUnitCost + kTileCost;   // least cost a CTA is given
 
 struct Frag {
   int kind;              // 0 prefix, 1 tail, -1 no more
-  int shared;            // two row tiles over the same keys
-  int n, hk, tile;       // sequence (tail), kv head, first row tile
+  int unit;              // kRowPair, kHeadPair, kSingle
+  int n, hk, tile;       // sequence (tail), first kv head, first row tile
   int len;               // keys of the source
   int t0, t1;            // key tiles
   int slot;              // where its partial result goes: -1 the unit's own place, else a CTA's
@@ -91,17 +94,29 @@ struct Bars {
 // all: many blocks 270 us, and 298 at 8/4/12, 276 at 8/6/12, 273 at 8/5/16; single tokens 198, 208,
 // 217 and 208.
 struct Line {
-  int pairs, odd, T;       // row tiles as pairs and one over; key tiles
-  __host__ __device__ Line(int row_tiles, int keys)
-      : pairs(row_tiles / 2), odd(row_tiles % 2), T((keys + kTile - 1) / kTile) {}
-  __host__ __device__ int tile_cost(int p) const { return p < pairs ? kPairCost : kTileCost; }
-  __host__ __device__ int unit(int p) const { return tile_cost(p) * T + kUnitCost; }
-  // all row tiles of one kv head
-  __host__ __device__ int head() const { return T ? pairs * unit(0) + odd * unit(pairs) : 0; }
-  // first tile of unit p that lies behind a cost of x from the unit's beginning
-  __host__ __device__ int tile_at(int p, int x) const {
-    const int y = x - kUnitCost;   // both divisors known: no division at run time
-    const int t = p < pairs ? (y + kPairCost - 1) / kPairCost : (y + kTileCost - 1) / kTileCost;
+  int H, pairs, odd, T;    // kv heads; row tiles as pairs and one over; key tiles
+  __host__ __device__ Line(int heads, int row_tiles, int keys)
+      : H(heads), pairs(row_tiles / 2), odd(row_tiles % 2), T((keys + kTile - 1) / kTile) {}
+  __host__ __device__ int count(int kind) const {
+    return kind == kRowPair ? H * pairs : !odd ? 0 : kind == kHeadPair ? H / 2 : H % 2;
+  }
+  __host__ __device__ static int tile_cost(int kind) {
+    return kind == kRowPair ? kPairCost : kind == kHeadPair ? kHeadsCost : kTileCost;
+  }
+  __host__ __device__ int unit(int kind) const { return tile_cost(kind) * T + kUnitCost; }
+  // cost of the units of all kinds before this one; of everything (kind = kUnitKinds)
+  __host__ __device__ int before(int kind) const {
+    int sum = 0;
+    for (int k = 0; k < kUnitKinds; ++k) sum += k < kind ? count(k) * unit(k) : 0;
+    return T ? sum : 0;
+  }
+  __host__ __device__ int total() const { return before(kUnitKinds); }
+  // first tile of such a unit that lies behind a cost of x from its beginning
+  __host__ __device__ int tile_at(int kind, int x) const {
+    const int y = x - kUnitCost;   // divisors known: no division at run time
+    const int t = kind == kRowPair    ? (y + kPairCost - 1) / kPairCost
+                  : kind == kHeadPair ? (y + kHeadsCost - 1) / kHeadsCost
+                                      : (y + kTileCost - 1) / kTileCost;
     return y <= 0 ? 0 : t > T ? T : t;
   }
 };
@@ -157,32 +172,32 @@ __device__ __forceinline__ int pos_v(int j, int T) { return j < T - 1 ? 2 * j + 
 
 // query row r of row tile `tile`: its place among the N*T*heads rows, -1 behind the end, and the
 // number of keys it sees
-__device__ __forceinline__ int64_t row_of(const xp_attn_args& g, const Frag& w, int tile, int r, int* n,
-                                          int* t, int* h, int* limit) {
+__device__ __forceinline__ int64_t row_of(const xp_attn_args& g, const Frag& w, int hk, int tile, int r,
+                                          int* n, int* t, int* h, int* limit) {
   const int per_seq = g.a.T * g.group, i = tile * g.plan.rows_tile + r;
   *limit = 0;
   if (i >= (w.kind == 0 ? g.a.N * per_seq : per_seq)) return -1;
   *n = w.kind == 0 ? i / per_seq : w.n;
   *t = i % per_seq / g.group;
-  *h = w.hk * g.group + i % g.group;
+  *h = hk * g.group + i % g.group;
   *limit = w.kind == 0 ? w.len : w.len - g.a.T + *t + 1;
   return ((int64_t)*n * g.a.T + *t) * g.a.heads + *h;
 }
 
 // Partial results lie in blocks of 32 query rows, [D/4][32 rows][4], so that a warp writes and
-// reads them 512 bytes at a time: the prefix's by kv head, each sequence's by kv head, the same
-// again for stream 1 of the one row tile of each that both streams work on, then 8 blocks for
-// every CTA's piece that does not begin its unit.
+// reads them 512 bytes at a time: the prefix's by kv head, each sequence's by kv head, then stream
+// 1's of the single units (the last row tile of the last kv head, where both are odd), then 8 blocks
+// for every CTA's piece that does not begin its unit.
 __device__ __forceinline__ int64_t block_of(const xp_attn_args& g, int kind, int n, int hk) {
   const int64_t all = g.plan.prefix_blocks;
   return kind == 0 ? hk * all : g.kv_heads * all + ((int64_t)n * g.kv_heads + hk) * g.plan.tail_blocks;
 }
-__device__ __forceinline__ int64_t second_block_of(const xp_attn_args& g, int kind, int n, int hk) {
+__device__ __forceinline__ int64_t second_block_of(const xp_attn_args& g, int kind, int n) {
   const int64_t one = min(g.plan.tail_blocks, 4);
-  return block_of(g, 1, g.a.N, 0) + (kind == 0 ? hk * 4 : g.kv_heads * 4 + ((int64_t)n * g.kv_heads + hk) * one);
+  return block_of(g, 1, g.a.N, 0) + (kind == 0 ? 0 : 4 + n * one);
 }
 __device__ __forceinline__ int64_t cut_block(const xp_attn_args& g, int64_t cta, int half) {
-  return second_block_of(g, 1, g.a.N, 0) + cta * 8 + half * 4;
+  return block_of(g, 1, g.a.N, 0) + g.plan.second_blocks + cta * 8 + half * 4;
 }
 
 __device__ __forceinline__ int tail_len(const xp_attn_args& g, int n, bool tell) {
@@ -198,11 +213,12 @@ __device__ __forceinline__ int tail_len(const xp_attn_args& g, int n, bool tell)
 // begins (with the cost before it).  CTA 0 leaves the chunk and every sequence's beginning for
 // the kernel that joins the results.
 __device__ int plan_line(const xp_attn_args& g, Bars* bars) {
-  const Line pre(g.plan.prefix_tiles, g.a.prefix_len);
-  const int before = pre.head() * g.kv_heads;
+  const int before = Line(g.kv_heads, g.plan.prefix_tiles, g.a.prefix_len).total();
   const int N = g.a.max_len > 0 ? g.a.N : 0;
   const int per = (N + kThreads - 1) / kThreads, n0 = min(N, (int)threadIdx.x * per), n1 = min(N, n0 + per);
-  auto cost = [&](int n) { return Line(g.plan.tail_tiles, tail_len(g, n, blockIdx.x == 0)).head() * g.kv_heads; };
+  auto cost = [&](int n) {
+    return Line(g.kv_heads, g.plan.tail_tiles, tail_len(g, n, blockIdx.x == 0)).total();
+  };
   int mine = 0;
   for (int n = n0; n < n1; ++n) mine += cost(n);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -303,17 +319,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 19) {
-      // ---- announces the fragments and loads their query tiles.  Two query tiles a shared
-      // fragment, one of the two places in turn for the others, so that the next one's queries
-      // are there before the present one is done ----
+      // ---- announces the fragments and loads their query tiles: two for a pair, one of the two
+      // places in turn for a single unit, so that the next one's queries are there before the
+      // present one is done ----
       const int x0 = blockIdx.x * chunk, x1 = x0 + chunk;
-      const Line pre(g.plan.prefix_tiles, g.a.prefix_len);
-      const int before = pre.head() * g.kv_heads;
+      const Line pre(g.kv_heads, g.plan.prefix_tiles, g.a.prefix_len);
+      const int before = pre.total();
       const int N = g.a.max_len > 0 ? g.a.N : 0;
       const uint64_t once = ptx::policy_evict_first();
       int f = 0, splits = 0, used[2] = {0, 0};
       bool ok = true;
-      auto load_q = [&](const Frag& w, int tile, int place) {
+      auto load_q = [&](const Frag& w, int hk, int tile, int place) {
         if (!wait(&bars->q_empty[place], (used[place] & 1) ^ 1)) return false;
         ++used[place];
         uint8_t* dst = smem + place * C::TILE_BYTES;
@@ -323,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int token = (w.kind == 0 ? 0 : w.n * g.a.T) + tile * (g.plan.rows_tile / g.group);
             ptx::mbar_arrive_expect_tx(bar, g.plan.rows_tile * 128 * C::CH);
             for (int ch = 0; ch < C::CH; ++ch)
-              ptx::tma_load_4d(ptx::smem_u32(dst + ch * kChunkBytes), &tm_q, bar, ch * 64, 0, w.hk, token,
+              ptx::tma_load_4d(ptx::smem_u32(dst + ch * kChunkBytes), &tm_q, bar, ch * 64, 0, hk, token,
                                once);
           }
           __syncwarp();
@@ -331,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int r = lane; r < g.plan.rows_tile; r += 32) {
           int n, t, h, lim;
-          if (row_of(g, w, tile, r, &n, &t, &h, &lim) < 0) break;   // rows behind the end: anything
+          if (row_of(g, w, hk, tile, r, &n, &t, &h, &lim) < 0) break;   // rows behind the end: anything
           const uint16_t* src = (const uint16_t*)g.q + n * g.a.q_stride_n + t * g.a.q_stride_t +
                                 h * g.a.q_stride_h;
           for (int seg = 0; seg < D / 8; ++seg) {
@@ -354,31 +370,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++f;
         if (w.kind < 0) return true;
-        if (w.shared) return load_q(w, w.tile, 0) && load_q(w, w.tile + 1, 1);
-        return load_q(w, w.tile, splits++ & 1);
+        if (w.unit == kRowPair) return load_q(w, w.hk, w.tile, 0) && load_q(w, w.hk, w.tile + 1, 1);
+        if (w.unit == kHeadPair) return load_q(w, w.hk, w.tile, 0) && load_q(w, w.hk + 1, w.tile, 1);
+        return load_q(w, w.hk, w.tile, splits++ & 1);
       };
       // the units of one source that lie in [x0, x1), from cost `at` on
       auto source = [&](const Line& l, int kind, int n, int len, int at) {
         if (l.T == 0) return true;
-        const int per = l.pairs + l.odd;
-        int hk = 0, p = 0;
-        if (x0 > at) {   // skip what lies before
-          hk = (x0 - at) / l.head();
-          at += hk * l.head();
-          p = min(l.pairs, (x0 - at) / l.unit(0));
-          at += p * l.unit(0);
-          if (hk >= g.kv_heads) return true;
-        }
-        for (; hk < g.kv_heads && at < x1; ++hk, p = 0)
-          for (; p < per && at < x1; ++p) {
-            const int cost = l.unit(p);
-            const int t0 = l.tile_at(p, x0 - at), t1 = l.tile_at(p, min(x1 - at, cost));
-            if (t0 < t1) {
-              const Frag w = {kind, p < l.pairs, n, hk, 2 * p, len, t0, t1, t0 > 0 ? (int)blockIdx.x : -1};
-              if (!announce(w)) return false;
-            }
-            at += cost;
+        for (int unit = 0; unit < kUnitKinds; ++unit) {
+          const int count = l.count(unit), cost = l.unit(unit);
+          int u = x0 > at ? min(count, (x0 - at) / cost) : 0;   // skip what lies before
+          for (int from = at + u * cost; u < count && from < x1; ++u, from += cost) {
+            const int t0 = l.tile_at(unit, x0 - from), t1 = l.tile_at(unit, min(x1 - from, cost));
+            if (t0 >= t1) continue;
+            const int hk = unit == kRowPair ? u / l.pairs : unit == kHeadPair ? 2 * u : l.H - 1;
+            const int tile = unit == kRowPair ? 2 * (u % l.pairs) : 2 * l.pairs;
+            const Frag w = {kind, unit, n, hk, tile, len, t0, t1, t0 > 0 ? (int)blockIdx.x : -1};
+            if (!announce(w)) return false;
           }
+          at += count * cost;
+        }
         return true;
       };
       if (x0 < before) ok = source(pre, 0, 0, g.a.prefix_len, 0);
@@ -388,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int len = n < N ? tail_len(g, n, false) : 0;
         for (; ok && n < N && at < x1; ++n) {
           const int after = n + 1 < N ? tail_len(g, n + 1, false) : 0;   // read ahead
-          const Line l(g.plan.tail_tiles, len);
+          const Line l(g.kv_heads, g.plan.tail_tiles, len);
           ok = source(l, 1, n, len, at);
-          at += l.head() * g.kv_heads;
+          at += l.total();
           len = after;
         }
       }
@@ -436,26 +447,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return page;
         };
+        // tile j of the ring: key tile j, or, of two heads in turn, key tile j / 2
+        const int heads = uniform(w.unit) == kHeadPair, T = (w.t1 - w.t0) << heads;
         auto load = [&](int j, int page, int from, const CUtensorMap* map) {
           if (!wait(&bars->empty[s], ((issued / C::STAGES) & 1) ^ 1)) return false;
           const uint32_t full = uniform(ptx::smem_u32(&bars->full[s]));
-          const int rows = (min(kTile, end - j * kTile) + box - 1) & -box;   // a power of two
+          // a whole number of boxes, which are powers of two
+          const int rows = (min(kTile, end - (w.t0 + (j >> heads)) * kTile) + box - 1) & -box;
           if (lane == 0) ptx::mbar_arrive_expect_tx(full, rows * 128 * C::CH);
           __syncwarp();
           if (from >= 0)
             ptx::tma_load_5d(place + s * C::TILE_BYTES, map, full, C::CH == 1 ? 0 : chunk_of * 64, from,
-                             hk, page, g.a.layer, policy);
+                             hk + (j & heads), page, g.a.layer, policy);
           ++issued;
           s = s + 1 == C::STAGES ? 0 : s + 1;
           return true;
         };
         int row0, row1, row2;
-        int now = look_up(&row0), next = look_up(&row1);
+        int now = look_up(&row0), next = now, after;
+        row1 = row0;
+        if (!heads) next = look_up(&row1);
         now = check(now, row0);
-        ok = load(w.t0, now, row0, &tm_k);
-        for (int j = w.t0; j < w.t1 && ok; ++j) {
-          const int after = look_up(&row2);
-          if (j + 1 < w.t1) {
+        ok = load(0, now, row0, &tm_k);
+        for (int j = 0; j < T && ok; ++j) {
+          after = next, row2 = row1;
+          if (!(heads && (j & 1))) after = look_up(&row2);
+          if (j + 1 < T) {
             next = check(next, row1);
             ok = load(j + 1, next, row1, &tm_k);
           }
@@ -496,10 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       Frag w;
       bool ok = true;
       for (int f = 0; ok && next_frag(f, &w); ++f) {
-        const int T = w.t1 - w.t0, items = w.shared ? 2 * T : T, mine = (items + 1 - t) / 2;
-        const int place = w.shared ? t : splits & 1, end = min(w.len, w.t1 * kTile);
+        const bool one = w.unit == kSingle, same = w.unit == kRowPair;   // same: one ring of tiles for both
+        const int keys = w.t1 - w.t0, T = w.unit == kHeadPair ? 2 * keys : keys;   // T: tiles of the ring
+        const int items = one ? keys : 2 * keys, mine = (items + 1 - t) / 2;
+        const int place = one ? splits & 1 : t, end = min(w.len, w.t1 * kTile);
         const uint32_t q = uniform(sq + place * C::TILE_BYTES);
-        auto kv = [&](int j) { return w.shared ? j : 2 * j + t; };
+        auto kv = [&](int j) { return same ? j : 2 * j + t; };
         // An mbarrier tells a phase from the one before it only.  So both warps see every load of
         // the ring land, in order, their own or not, and a stage is free again when both are
         // done with it: behind the products that read it, or at once where it is the other
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = seen % C::STAGES, o = seen - pos0;
             if (!wait(&bars->full[s], seen / C::STAGES)) return false;
             const int tile = o == 0 ? 0 : o == 2 * T - 1 ? T - 1 : o & 1 ? (o + 1) / 2 : o / 2 - 1;
-            if (!w.shared && (tile & 1) != t && lane == 0)
+            if (!same && (tile & 1) != t && lane == 0)
               ptx::mbar_arrive(ptx::smem_u32(&bars->empty[s]));
           }
           return true;
@@ -531,11 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         };
         for (int p = 0; p < 2 && ok; ++p) {
-          if (!w.shared && p != place) continue;
+          if (one && p != place) continue;
           ok = wait(&bars->q_full[p], used[p]++);
           if (ok && (p != place || mine == 0) && lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->q_empty[p]));
         }
-        splits += !w.shared;
+        splits += one;
         if (ok && mine > 0) {
           ok = see(pos_k(kv(0)));
           if (!ok) break;
@@ -543,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           scores(0);
         }
         for (int j = 0; j < mine && ok; ++j) {
-          const int pv = pos0 + pos_v(kv(j), T), valid = end - (w.t0 + kv(j)) * kTile;
+          const int pv = pos0 + pos_v(kv(j), T), valid = end - (w.t0 + (one ? kv(j) : j)) * kTile;
           // the tiles are there before the weights are
           ok = see(pv - pos0) && (j + 1 >= mine || see(pos_k(kv(j + 1))));
           if (!ok) break;
@@ -605,8 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Frag w;
     bool ok = true;
     for (int f = 0; ok && next_frag(f, &w); ++f) {
-      const int T = w.t1 - w.t0, items = w.shared ? 2 * T : T, mine = (items + 1 - t) / 2;
-      const int tile = w.shared ? w.tile + t : w.tile;
+      const bool one = w.unit == kSingle;
+      const int T = w.t1 - w.t0, mine = one ? (T + 1 - t) / 2 : T;
+      const int tile = w.unit == kRowPair ? w.tile + t : w.tile;
+      const int hk = w.unit == kHeadPair ? w.hk + t : w.hk;
       const int end = min(w.len, w.t1 * kTile);
       // keys its rows see: all of a prefix, a tail's by the row's token
       int limit[2];
@@ -627,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < mine; ++j) {
         ok = wait(&bars->s_full[t], done + j);
         if (!ok) break;
-        const int kt = w.shared ? j : 2 * j + t, key = (w.t0 + kt) * kTile;
+        const int kt = one ? 2 * j + t : j, key = (w.t0 + kt) * kTile;
         if (!active) {   // no rows here: only the hand-over
           __syncwarp();
           if (lane == 0) {
@@ -743,9 +764,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], o);
       const int64_t block =
-          (w.slot >= 0            ? cut_block(g, w.slot, t)
-           : !w.shared && t == 1 ? second_block_of(g, w.kind, w.n, w.hk)
-                                 : block_of(g, w.kind, w.n, w.hk) + tile * 4) +
+          (w.slot >= 0      ? cut_block(g, w.slot, t)
+           : one && t == 1 ? second_block_of(g, w.kind, w.n)
+                           : block_of(g, w.kind, w.n, hk) + tile * 4) +
           warp % 4;
       const int rb = r0 % 32;   // in the block, and rb + 8
       if (quad == 0)
@@ -842,31 +863,35 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
 #pragma unroll
     for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto join = [&](int kind) {
-      const Line ln(kind ? g.plan.tail_tiles : g.plan.prefix_tiles,
+      const Line ln(g.kv_heads, kind ? g.plan.tail_tiles : g.plan.prefix_tiles,
                     kind ? tail_len(g, n, false) : g.a.prefix_len);
       if (ln.T == 0) return;
-      const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / RT, p = tile / 2;
-      const int at = (kind ? g.line[1 + n] : 0) + hk * ln.head() + p * ln.unit(0), cost = ln.unit(p);
-      // a piece of two row tiles has a half of each, one of a single row tile a half of each
-      // stream (the second from two key tiles on)
-      const bool shared = p < ln.pairs;
+      const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / RT;
+      const int unit = tile < 2 * ln.pairs ? kRowPair : hk < ln.H / 2 * 2 ? kHeadPair : kSingle;
+      const int u = unit == kRowPair ? hk * ln.pairs + tile / 2 : unit == kHeadPair ? hk / 2 : 0;
+      const int cost = ln.unit(unit), at = (kind ? g.line[1 + n] : 0) + ln.before(unit) + u * cost;
+      // a piece of a pair has a half of each, one of a single row tile a half of each stream (the
+      // second from two key tiles on)
+      const bool one = unit == kSingle;
+      const int mine = unit == kRowPair ? tile % 2 : hk % 2;
       const int in_tile = at_row % RT / 32, r = at_row % RT % 32;
       int cut = (at / chunk + 1) * chunk - at;   // where the unit is first cut,
-      if (ln.tile_at(p, cut) == 0) cut += chunk;       // behind its first tile
-      const int first = ln.tile_at(p, min(cut, cost)), cta0 = at / chunk + 1;
+      if (ln.tile_at(unit, cut) == 0) cut += chunk;       // behind its first tile
+      const int first = ln.tile_at(unit, min(cut, cost)), cta0 = at / chunk + 1;
       const int cuts = max(0, min(ctas - 1, (at + cost - 1) / chunk) - cta0 + 1);
       const int64_t own = block_of(g, kind, n, hk) + tile * 4 + in_tile;
-      const int64_t second = second_block_of(g, kind, n, hk) + in_tile;
+      const int64_t second = second_block_of(g, kind, n) + in_tile;
       const int64_t cut0 = cut_block(g, cta0, 0) + in_tile;
       // the block of piece q: the unit's own (and its second), then those of the CTAs; -1: none
       auto block = [&](int q) -> int64_t {
         if (q == 0) return first > 0 ? own : -1;
-        if (q == 1 && !shared) return first > 1 ? second : -1;
-        const int c = shared ? q - 1 : (q - 2) / 2, half = shared ? tile % 2 : q % 2;
-        const int x = (cta0 + c) * chunk - at, t0 = ln.tile_at(p, x), t1 = ln.tile_at(p, min(x + chunk, cost));
-        return t0 == 0 || t0 >= t1 || (!shared && half && t1 - t0 < 2) ? -1 : cut0 + c * 8 + half * 4;
+        if (q == 1 && one) return first > 1 ? second : -1;
+        const int c = one ? (q - 2) / 2 : q - 1, half = one ? q % 2 : mine;
+        const int x = (cta0 + c) * chunk - at;
+        const int t0 = ln.tile_at(unit, x), t1 = ln.tile_at(unit, min(x + chunk, cost));
+        return t0 == 0 || t0 >= t1 || (one && half && t1 - t0 < 2) ? -1 : cut0 + c * 8 + half * 4;
       };
-      const int pieces = shared ? 1 + cuts : 2 + 2 * cuts;
+      const int pieces = one ? 2 + 2 * cuts : 1 + cuts;
       for (int q = 0; q < pieces; q += TOGETHER) {
         float2 st[TOGETHER];
         float4 x[TOGETHER][kPer];
@@ -1024,19 +1049,23 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
   p.prefix_blocks = row_blocks((int64_t)a->N * per_seq);
   p.tail_blocks = row_blocks(per_seq);
   const size_t H = c->d.kv_heads, D = c->d.head_dim;
-  const size_t one = p.tail_blocks;
-  const size_t blocks = H * p.prefix_blocks + a->N * H * one + H * 4 +
-                        a->N * H * std::min<size_t>(one, 4) + (size_t)c->num_sms * 8;
+  p.second_blocks = H % 2 ? 4 + (int64_t)a->N * std::min(p.tail_blocks, 4) : 0;
+  const size_t blocks = H * p.prefix_blocks + (size_t)a->N * H * p.tail_blocks + p.second_blocks +
+                        (size_t)c->num_sms * 8;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
   p.line_off = take(((size_t)a->N + 1) * 4);
   p.stat_off = take(blocks * 32 * 8);
   p.acc_off = take(blocks * 32 * D * 4);
   // the line's length, at the greatest lengths, has to be an int (with room for one share more)
-  const Line pre(p.prefix_tiles, a->prefix_len), tail(p.tail_tiles, a->max_len);
-  const double work = ((double)pre.pairs * kPairCost + pre.odd * kTileCost) * pre.T * H +
-                      ((double)tail.pairs * kPairCost + tail.odd * kTileCost) * tail.T * H * a->N +
-                      (double)kUnitCost * H * (pre.pairs + pre.odd + (double)a->N * (tail.pairs + tail.odd));
+  auto work_of = [](const Line& l) {
+    double sum = 0;
+    for (int k = 0; k < kUnitKinds; ++k)
+      sum += (double)l.count(k) * ((double)Line::tile_cost(k) * l.T + kUnitCost);
+    return sum;
+  };
+  const double work = work_of(Line(c->d.kv_heads, p.prefix_tiles, a->prefix_len)) +
+                      work_of(Line(c->d.kv_heads, p.tail_tiles, a->max_len)) * a->N;
   p.total = work < 1e9 ? o : 0;
   return p;
 }

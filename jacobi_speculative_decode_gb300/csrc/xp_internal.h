@@ -225,6 +225,7 @@ struct xp_attn_plan {
   int rows_tile;                 // query rows of one work item
   int prefix_tiles, tail_tiles;  // row tiles: over the batch, of one sequence
   int prefix_blocks, tail_blocks;   // tensor-core form: the same in blocks of 32 rows
+  int64_t second_blocks;            // and those of the second stream's own results
   int prefix_splits, prefix_keys, tail_splits, tail_keys;
   int parts;
   // workspace: (max, sum) pairs, accumulators; tensor-core form: where each sequence's work begins
