@@ -5,9 +5,9 @@
 //   S = Q K^T (tcgen05, fp32 in tensor memory), P = 2^(c S - m) rounded to bf16 over S,
 //   O += P V (tcgen05, P read from tensor memory), running maximum m and sum per row.
 // The streams alternate on the tensor core, so one stream's products run under the other's
-// exponentials.  Where a row tile has a neighbour with the same keys (the prefix, and blocks
-// of more than 128 rows) the two streams are two row tiles and share every K and V tile;
-// else they are the even and the odd key tiles of one row tile, each with a result of its own.
+// exponentials.  They are two row tiles of one kv head that share every K and V tile (the prefix,
+// and blocks of more than 128 rows); one row tile of each of two kv heads; or, for the last
+// head of an odd number, the even and the odd key tiles of one row tile, with a result each.
 // O is rescaled only when a row's maximum grew by more than 2^8 since the last time.
 //
 // Warps: 0-7 and 8-15 the softmax of stream 0 and 1 (a warp is 16 query rows, four lanes a row),
@@ -61,6 +61,7 @@ constexpr int kFrags = 4;       // fragments announced ahead
 enum { kRowPair, kHeadPair, kSingle, kUnitKinds };
 // cost of a key tile for each, and of a unit besides its tiles (ns / 180)
 constexpr int kPairCost = 8, kHeadsCost = 9, kTileCost = 5, kUnitCost = 12;
+constexpr int kHeadsFewCost = 8, kFewRows = 16;   // a head pair's tiles of few rows (one warp's)
 constexpr int kMinChunk = kUnitCost + kTileCost;   // least cost a CTA is given
 
 struct Frag {
@@ -85,23 +86,26 @@ struct Bars {
   int issued[2];                 // items of each stream whose products are issued
 };
 
-// The work is one line of cost: prefix units (kv head, pair of row tiles), then the units of
-// each sequence's tail, a unit costing kUnitCost and kPairCost or kTileCost a key tile.  CTA i
-// does [i*chunk, (i+1)*chunk) of it, so that a unit may be cut anywhere between two of its
-// tiles and every CTA gets the same.  A piece that begins its unit leaves its result in the
-// unit's place, one that does not in the place of its CTA, of which there is at most one.
-// The costs are what was timed (a unit 2.2 us); of ten others from 8/3/8 to 8/7/24 none is better for
-// all: many blocks 270 us, and 298 at 8/4/12, 276 at 8/6/12, 273 at 8/5/16; single tokens 198, 208,
-// 217 and 208.
+// The work is one line of cost: the prefix's units, then those of each sequence's tail, by kind
+// (every head's row tile pairs, then the tile over of two heads each, then of the last head alone);
+// a unit costs kUnitCost and its kind's cost a key tile.  CTA i does [i*chunk, (i+1)*chunk) of the
+// line, so that a unit may be cut anywhere between two of its tiles and every CTA gets the
+// same.  A piece that begins its unit leaves its result in the unit's place, one that does not in
+// the place of its CTA, of which there is at most one.
+// The costs are timed (a unit 2.2 us, two row tiles 1.4 a key tile, two heads 1.6, or 1.4 with one
+// warp's rows).  Many blocks of 16 tokens take 253 us; with 8 or 10 for two heads 259 and 258,
+// with units of 20 254.  256 single tokens take 162; with 9 or 7 for few rows 171 and 163, and 128
+// blocks of 4 tokens (32 rows, not few) 195 to 198 with 9 to 10 and 217 with 7.
 struct Line {
   int H, pairs, odd, T;    // kv heads; row tiles as pairs and one over; key tiles
-  __host__ __device__ Line(int heads, int row_tiles, int keys)
-      : H(heads), pairs(row_tiles / 2), odd(row_tiles % 2), T((keys + kTile - 1) / kTile) {}
+  bool few;                // rows of the one over
+  __host__ __device__ Line(int heads, int row_tiles, bool few_over, int keys)
+      : H(heads), pairs(row_tiles / 2), odd(row_tiles % 2), T((keys + kTile - 1) / kTile), few(few_over) {}
   __host__ __device__ int count(int kind) const {
     return kind == kRowPair ? H * pairs : !odd ? 0 : kind == kHeadPair ? H / 2 : H % 2;
   }
-  __host__ __device__ static int tile_cost(int kind) {
-    return kind == kRowPair ? kPairCost : kind == kHeadPair ? kHeadsCost : kTileCost;
+  __host__ __device__ int tile_cost(int kind) const {
+    return kind == kRowPair ? kPairCost : kind == kSingle ? kTileCost : few ? kHeadsFewCost : kHeadsCost;
   }
   __host__ __device__ int unit(int kind) const { return tile_cost(kind) * T + kUnitCost; }
   // cost of the units of all kinds before this one; of everything (kind = kUnitKinds)
@@ -114,9 +118,10 @@ struct Line {
   // first tile of such a unit that lies behind a cost of x from its beginning
   __host__ __device__ int tile_at(int kind, int x) const {
     const int y = x - kUnitCost;   // divisors known: no division at run time
-    const int t = kind == kRowPair    ? (y + kPairCost - 1) / kPairCost
-                  : kind == kHeadPair ? (y + kHeadsCost - 1) / kHeadsCost
-                                      : (y + kTileCost - 1) / kTileCost;
+    const int t = kind == kRowPair  ? (y + kPairCost - 1) / kPairCost
+                  : kind == kSingle ? (y + kTileCost - 1) / kTileCost
+                  : few             ? (y + kHeadsFewCost - 1) / kHeadsFewCost
+                                    : (y + kHeadsCost - 1) / kHeadsCost;
     return y <= 0 ? 0 : t > T ? T : t;
   }
 };
@@ -213,11 +218,11 @@ __device__ __forceinline__ int tail_len(const xp_attn_args& g, int n, bool tell)
 // begins (with the cost before it).  CTA 0 leaves the chunk and every sequence's beginning for
 // the kernel that joins the results.
 __device__ int plan_line(const xp_attn_args& g, Bars* bars) {
-  const int before = Line(g.kv_heads, g.plan.prefix_tiles, g.a.prefix_len).total();
+  const int before = Line(g.kv_heads, g.plan.prefix_tiles, g.plan.prefix_few, g.a.prefix_len).total();
   const int N = g.a.max_len > 0 ? g.a.N : 0;
   const int per = (N + kThreads - 1) / kThreads, n0 = min(N, (int)threadIdx.x * per), n1 = min(N, n0 + per);
   auto cost = [&](int n) {
-    return Line(g.kv_heads, g.plan.tail_tiles, tail_len(g, n, blockIdx.x == 0)).total();
+    return Line(g.kv_heads, g.plan.tail_tiles, g.plan.tail_few, tail_len(g, n, blockIdx.x == 0)).total();
   };
   int mine = 0;
   for (int n = n0; n < n1; ++n) mine += cost(n);
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // places in turn for a single unit, so that the next one's queries are there before the
       // present one is done ----
       const int x0 = blockIdx.x * chunk, x1 = x0 + chunk;
-      const Line pre(g.kv_heads, g.plan.prefix_tiles, g.a.prefix_len);
+      const Line pre(g.kv_heads, g.plan.prefix_tiles, g.plan.prefix_few, g.a.prefix_len);
       const int before = pre.total();
       const int N = g.a.max_len > 0 ? g.a.N : 0;
       const uint64_t once = ptx::policy_evict_first();
@@ -399,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int len = n < N ? tail_len(g, n, false) : 0;
         for (; ok && n < N && at < x1; ++n) {
           const int after = n + 1 < N ? tail_len(g, n + 1, false) : 0;   // read ahead
-          const Line l(g.kv_heads, g.plan.tail_tiles, len);
+          const Line l(g.kv_heads, g.plan.tail_tiles, g.plan.tail_few, len);
           ok = source(l, 1, n, len, at);
           at += l.total();
           len = after;
@@ -864,6 +869,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
     for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto join = [&](int kind) {
       const Line ln(g.kv_heads, kind ? g.plan.tail_tiles : g.plan.prefix_tiles,
+                    kind ? g.plan.tail_few : g.plan.prefix_few,
                     kind ? tail_len(g, n, false) : g.a.prefix_len);
       if (ln.T == 0) return;
       const int at_row = (kind ? 0 : n * per_seq) + i, tile = at_row / RT;
@@ -1045,6 +1051,9 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
   p.rows_tile = RT;
   p.prefix_tiles = (int)(((int64_t)a->N * per_seq + RT - 1) / RT);
   p.tail_tiles = (per_seq + RT - 1) / RT;
+  auto few = [&](int64_t rows) { return (rows - 1) % RT < kFewRows; };
+  p.prefix_few = few((int64_t)a->N * per_seq);
+  p.tail_few = few(per_seq);
   auto row_blocks = [&](int64_t rows) { return (int)(rows / RT * 4 + (rows % RT + 31) / 32); };
   p.prefix_blocks = row_blocks((int64_t)a->N * per_seq);
   p.tail_blocks = row_blocks(per_seq);
@@ -1061,11 +1070,11 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
   auto work_of = [](const Line& l) {
     double sum = 0;
     for (int k = 0; k < kUnitKinds; ++k)
-      sum += (double)l.count(k) * ((double)Line::tile_cost(k) * l.T + kUnitCost);
+      sum += (double)l.count(k) * ((double)l.tile_cost(k) * l.T + kUnitCost);
     return sum;
   };
-  const double work = work_of(Line(c->d.kv_heads, p.prefix_tiles, a->prefix_len)) +
-                      work_of(Line(c->d.kv_heads, p.tail_tiles, a->max_len)) * a->N;
+  const double work = work_of(Line(c->d.kv_heads, p.prefix_tiles, p.prefix_few, a->prefix_len)) +
+                      work_of(Line(c->d.kv_heads, p.tail_tiles, p.tail_few, a->max_len)) * a->N;
   p.total = work < 1e9 ? o : 0;
   return p;
 }

@@ -224,6 +224,7 @@ struct xp_attn_plan {
   bool tc;                       // the tensor-core form
   int rows_tile;                 // query rows of one work item
   int prefix_tiles, tail_tiles;  // row tiles: over the batch, of one sequence
+  bool prefix_few, tail_few;     // tensor-core form: few rows in the last of them
   int prefix_blocks, tail_blocks;   // tensor-core form: the same in blocks of 32 rows
   int64_t second_blocks;            // and those of the second stream's own results
   int prefix_splits, prefix_keys, tail_splits, tail_keys;

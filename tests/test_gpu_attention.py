@@ -296,6 +296,11 @@ BATCHES = {
     "one long": dict(lens=[0, 20000, 3, 0], T=4, H=2, G=2, D=128, P=20, ps=256),
     "prefix only": dict(lens=[0] * 70, T=3, H=5, G=2, D=128, P=4100, ps=8),
     "tiny tails": dict(lens=[i % 3 for i in range(400)], T=1, H=8, G=4, D=128, P=300, ps=16),
+    "pairs of tiles, of heads, and one": dict(lens=[(331 * i) % 900 for i in range(14)], T=16, H=3, G=17,
+                                              D=128, P=1000, ps=32),
+    "the same narrow": dict(lens=[(57 * i) % 700 for i in range(21)], T=15, H=5, G=18, D=64, P=60, ps=64),
+    "odd heads": dict(lens=[(91 * i) % 1300 for i in range(40)], T=2, H=7, G=1, D=128, P=700, ps=16),
+    "groups of seven": dict(lens=[(91 * i) % 500 for i in range(50)], T=5, H=4, G=7, D=128, P=333, ps=64),
 }
 
 
