@@ -315,7 +315,7 @@ def xp_readout_kernel_name(head) -> str:
 #
 # These calls take their sizes and strides from the tensors; a tensor that the C call could
 # not read as it is (another type, a strided last dimension, too few elements) is refused
-# with ValueError.
+# with ValueError (whose text is made only then: a call's checks are part of its latency).
 
 def _want(ok: bool, what: str):
     if not ok:
@@ -325,24 +325,27 @@ def _want(ok: bool, what: str):
 def _code(name, t):
     """The library's type code of a tensor's dtype."""
     import torch
-    _want(t.dtype in (torch.bfloat16, torch.float32), f"{name}: bf16 or fp32")
-    return XP_BF16 if t.dtype == torch.bfloat16 else XP_F32
+    if t.dtype == torch.bfloat16:
+        return XP_BF16
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name}: bf16 or fp32")
+    return XP_F32
 
 
 def _ints(name, t, n):
     """A contiguous int32 vector of at least n elements on the GPU (None passes)."""
     import torch
-    if t is not None:
-        _want(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() >= n,
-              f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
+    if t is not None and not (t.dtype == torch.int32 and t.is_cuda and t.is_contiguous()
+                              and t.numel() >= n):
+        raise ValueError(f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
 
 
 def _table(name, t, rows=None):
     """An int32 page table [rows, width] on the GPU, unit stride over the columns."""
     import torch
-    _want(t.dtype == torch.int32 and t.is_cuda and t.dim() == 2 and t.shape[1] > 0
-          and (t.stride(1) == 1 or t.shape[1] == 1) and (rows is None or t.shape[0] >= rows),
-          f"{name}: an int32 CUDA tensor [rows, width], unit stride over the columns")
+    if not (t.dtype == torch.int32 and t.is_cuda and t.dim() == 2 and t.shape[1] > 0
+            and (t.stride(1) == 1 or t.shape[1] == 1) and (rows is None or t.shape[0] >= rows)):
+        raise ValueError(f"{name}: an int32 CUDA tensor [rows, width], unit stride over the columns")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
@@ -368,8 +371,8 @@ def xp_verify_drafts(head, target, draft, blk, n_draft, temperature, u, noise, t
                                ("temperature", temperature, f32, N), ("u", u, f32, N * (B - 1)),
                                ("tokens", tokens, i64, N * B), ("counts", counts, i32, N),
                                ("prob", prob, f32, N * (B - 1))):
-        _want(t is None or (t.dtype == dt and t.is_contiguous() and t.numel() >= count),
-              f"{name}: contiguous {dt} of at least {count} elements")
+        if t is not None and not (t.dtype == dt and t.is_contiguous() and t.numel() >= count):
+            raise ValueError(f"{name}: contiguous {dt} of at least {count} elements")
     _check("xp_verify_drafts", lib().xp_verify_drafts(
         head, _ptr(target), target.stride(0), target.stride(1), _ptr(draft),
         draft.stride(0) if draft is not None else 0, _ptr(blk), _ptr(n_draft), N, B, V,
