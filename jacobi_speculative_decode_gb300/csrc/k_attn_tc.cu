@@ -19,11 +19,12 @@
 // 2,800, as each stream's chain is as long: S 512, softmax to the first half of P 990 and to the
 // second 550, the second half of P V 256, and about 100 for each of four hand-overs.  128
 // blocks of 16 tokens, 32 heads of 128 over 8, behind a shared prefix of 8192 and tails up to
-// 2048 (309 GFLOP, 608 MB): 261 us back to back, 1.19 PFLOP/s, 63% of measured.
-// A tail of few rows is bound by one tile's chain, 1,080 cycles a tile of 128 keys with two
-// streams, and by what a unit costs at its ends (about 5,000 cycles: a masked tile, the last
+// 2048 (309 GFLOP, 608 MB): 248 us back to back, 1.25 PFLOP/s, 66% of measured.
+// A tail of few rows is bound by one tile's chain, 2,160 cycles for a tile of 128 keys of two
+// heads, and by what a unit costs at its ends (about 5,000 cycles: a masked tile, the last
 // product, the result's way out, code and constants that must be fetched anew).  256 single tokens,
-// 64 heads of 64 over 8, a prefix of 16384 and tails up to 2000 (588 MB): 197 us, 2.99 TB/s.
+// 64 heads of 64 over 8, a prefix of 16384 and tails up to 2000 (588 MB): 165 us, 3.6 TB/s.
+// (Two streams on one head's even and odd tiles took 197: two results and two ends a unit.)
 // Tiles of 128 x 128: a product reads 8 KB of shared memory for 64 cycles of work, which is all
 // that can be read; half a tile of rows or keys would be bound by it.  Two streams: 128 columns of
 // scores and D of results each fill tensor memory at D = 128.
@@ -843,8 +844,8 @@ __device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, in
 //   out = sum a_p O_p / sum a_p l_p,  a_p = 2^(m_p - m).
 // A CTA joins 32 rows of (sequence, kv head, token, head) order: a thread is a row, a warp every
 // eighth of its 16-byte pieces; the rows leave through shared memory.  Bound by the partial
-// results' bytes, mostly from L2: 65,536 rows of 128 with three or four each, about 110 MB, in
-// 24 us; with few rows by the latency of what it asks for.
+// results' bytes, mostly from L2: 65,536 rows of 128 with two or three each, about 80 MB, in
+// 20 to 25 us; with few rows by the latency of what it asks for.
 // TOGETHER: partial results asked for at once.  Few rows have many (a long prefix is cut by every
 // CTA) and nobody else's work to wait under: four at once take 16.4 us where one takes 17.3 (both
 // kernels, one request of 4 tokens).  Many rows have three or four, and one at a time leaves
