@@ -262,7 +262,8 @@ __device__ int plan_line(const xp_attn_args& g, Bars* bars) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ CUtensorMap tm_q, const xp_attn_args g, int box, bool q_tma) {
+                   const __grid_constant__ CUtensorMap tm_q, const xp_attn_args g, int box, bool q_tma,
+                   bool q_wide) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + C::SMEM);
@@ -356,10 +357,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row_of(g, w, hk, tile, r, &n, &t, &h, &lim) < 0) break;   // rows behind the end: anything
           const uint16_t* src = (const uint16_t*)g.q + n * g.a.q_stride_n + t * g.a.q_stride_t +
                                 h * g.a.q_stride_h;
-          for (int seg = 0; seg < D / 8; ++seg) {
-            uint16_t* to = (uint16_t*)(dst + (seg / 8) * kChunkBytes + r * 128 + (((seg % 8) ^ (r & 7)) << 4));
+          auto to = [&](int seg) {
+            return dst + (seg / 8) * kChunkBytes + r * 128 + (((seg % 8) ^ (r & 7)) << 4);
+          };
+          if (q_wide) {
+#pragma unroll 4
+            for (int seg = 0; seg < D / 8; ++seg) *(uint4*)to(seg) = *(const uint4*)(src + seg * 8);
+          } else {
+#pragma unroll 1
+            for (int seg = 0; seg < D / 8; ++seg)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) to[e] = src[seg * 8 + e];
+              for (int e = 0; e < 8; ++e) ((uint16_t*)to(seg))[e] = src[seg * 8 + e];
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -376,9 +384,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++f;
         if (w.kind < 0) return true;
-        if (w.unit == kRowPair) return load_q(w, w.hk, w.tile, 0) && load_q(w, w.hk, w.tile + 1, 1);
-        if (w.unit == kHeadPair) return load_q(w, w.hk, w.tile, 0) && load_q(w, w.hk + 1, w.tile, 1);
-        return load_q(w, w.hk, w.tile, splits++ & 1);
+        const bool one = w.unit == kSingle;
+#pragma unroll 1
+        for (int k = 0; k < (one ? 1 : 2); ++k)
+          if (!load_q(w, w.hk + (w.unit == kHeadPair ? k : 0), w.tile + (w.unit == kRowPair ? k : 0),
+                      one ? splits & 1 : k))
+            return false;
+        splits += one;
+        return true;
       };
       // the units of one source that lie in [x0, x1), from cost `at` on
       auto source = [&](const Line& l, int kind, int n, int len, int at) {
@@ -982,8 +995,10 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   // Queries by TMA where a tile is a whole number of tokens, one stride apart; else by loads.
   CUtensorMap tm_q = {};
   const int64_t token = g.a.T > 1 ? g.a.q_stride_t : g.a.q_stride_n;
-  bool q_tma = g.group <= kRows && (g.a.T == 1 || g.a.N == 1 || g.a.q_stride_n == g.a.T * token) &&
-               (uintptr_t)g.q % 16 == 0 && token % 8 == 0 && g.a.q_stride_h % 8 == 0 && token > 0 &&
+  const bool q_wide = (uintptr_t)g.q % 16 == 0 &&
+                      (g.a.q_stride_n | g.a.q_stride_t | g.a.q_stride_h) % 8 == 0;
+  bool q_tma = q_wide && g.group <= kRows &&
+               (g.a.T == 1 || g.a.N == 1 || g.a.q_stride_n == g.a.T * token) && token > 0 &&
                g.a.q_stride_h > 0;
   if (q_tma) {
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)g.group, (cuuint64_t)g.kv_heads,
@@ -997,7 +1012,7 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   }
-  attn_tc_kernel<D><<<c->num_sms, kThreads, smem, s>>>(c->tm_k, c->tm_v, tm_q, g, c->attn_tc, q_tma);
+  attn_tc_kernel<D><<<c->num_sms, kThreads, smem, s>>>(c->tm_k, c->tm_v, tm_q, g, c->attn_tc, q_tma, q_wide);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
