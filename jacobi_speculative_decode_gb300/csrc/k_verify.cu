@@ -201,10 +201,10 @@ __device__ __forceinline__ void vectors_of(const T* row, int V, int chunk, int c
 
 // What a stage of the ring holds: `bytes` of the item's target or draft row, behind `first` vectors
 struct Stage {
-  int item, kind;     // kind: bit 0 draft, bit 1 first of its row's chunk, bit 2 last of the item
+  int item, kind;     // kind: of the draft's row, first of its row's chunk, last of the item, ...
   int first, bytes;   // first vector of the stage in the row
 };
-constexpr int kDraft = 1, kOpens = 2, kEnds = 4, kStop = 8;
+constexpr int kDraft = 1, kOpens = 2, kEnds = 4, kStop = 8, kDropped = 16;
 
 constexpr int kItems = 4;
 struct Ring {
@@ -279,20 +279,27 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
       __syncwarp();
       ++issued;
     };
-    // the stages of one row's chunk
+    // The stages of one row's chunk; false where the row was found to lie behind a rejection on the
+    // way (it can never be wanted, and its item leaves no result).
     auto stream = [&](auto* row, int item, int c, int kind, int ends) {
       using E = typename std::remove_const<typename std::remove_pointer<decltype(row)>::type>::type;
       constexpr int VN = Vec<E>::N, kPer = kStageBytes / 16;
       const int head = head_of(row, a.V);
-      int v, v1, opens = kOpens;
+      int v, v1, opens = kOpens, seen = 0;
       vectors_of(row, a.V, chunk, chunks, c, &v, &v1);
       do {
         const int n = min(kPer, v1 - v), s = room();
-        if (!ok) return;
+        if (!ok) return false;
+        if (item / per_slot > a.B - seen) {
+          post(s, {item, kDropped, 0, 0}, nullptr);
+          return false;
+        }
         post(s, {item, kind | opens | (v + n == v1 ? ends : 0), v, n * 16}, row + head + (int64_t)v * VN);
+        seen = (int)__ldcg(&a.marks[item / chunks % a.N]);   // there by the time of the next stage
         v += n;
         opens = 0;
       } while (v < v1);
+      return true;
     };
     // A CTA's first item is its own number, the others come from the counter.  The counter and
     // the next item's mark are read while this one streams.
@@ -313,8 +320,7 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
       claimed = claim();
       if (!wanted) continue;
       const bool two = a.draft && heat_of(a, n) > 0.0f && b < drafts;
-      stream((const T*)a.target + n * a.sn + b * a.sb, i, c, 0, two ? 0 : kEnds);
-      if (two && ok)
+      if (stream((const T*)a.target + n * a.sn + b * a.sb, i, c, 0, two ? 0 : kEnds) && two)
         stream(a.draft + ((int64_t)n * (a.B - 1) + b) * a.ld_draft, i, c, kDraft, kEnds);
     }
     if (ok) {
@@ -435,6 +441,10 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
         ptx::mbar_arrive(ptx::smem_u32(&sh.written[h]));
       }
       break;
+    }
+    if (sg.kind & kDropped) {
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[s]));
+      continue;
     }
     const bool draft = sg.kind & kDraft;
     if (sg.kind & kOpens) {
