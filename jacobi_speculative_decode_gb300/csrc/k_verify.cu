@@ -225,14 +225,18 @@ struct Ring {
 // over the items' ends; warps 0-7 sum what it holds; warp 9 writes the items' results, and
 // where an item is its row's last joins them and tests the slot (its round trips to memory
 // hold nobody up).
-// Bound by HBM, and by rows read in vain (about a third): two items a CTA are claimed and under way,
-// close to a slot of a large batch, and a rejection is known only when its row is done.
-// 256 blocks of 16 slots, 151,936 ids, bf16, one-hot drafts of which 0.7 are accepted: 110 us, about
-// 5 TB/s of what it reads; the wanted rows alone would take 55.  Two CTAs of 64 KB in flight an
-// SM.  Items of 65536 ids where there are enough: 164 us for both kernels, and 186, 234 and 321 at
-// 32768, 16384 and 8192 (an item's end costs about 3 us of latency).  Claims of several items at
-// once, for the slots where most are not wanted, leave some CTAs with several rows at the end: 170
-// to 350 us.
+// Bound by HBM, and by rows read in vain: two items a CTA are claimed and under way, close to a
+// slot of a large batch, and a rejection is known only when its row is done.  So the streaming
+// warp looks at the block's mark again with every stage and leaves a row in the middle (draft
+// logits below: 75 us without).
+// 256 blocks of 16 slots, 151,936 ids, bf16, one-hot drafts of which 0.7 are accepted: 105 us, 4.6
+// TB/s of what it reads (490 MB, a quarter of it in vain); the wanted rows alone would take 55.  Both kernels take 150 there, 68 for
+// 32 blocks with the drafter's logits.
+// Two CTAs of 64 KB in flight an SM: one of 512 threads and 96 to 192 KB takes 10 to 30 us more.
+// Items of 65536 ids where there are enough of them: 32768, 16384 and 8192 took 23, 70 and 157 us
+// more for the large batch (an item's end costs about 3 us of latency).  Claims of several
+// items at once, for the slots where most are not wanted, leave some CTAs with several rows at the
+// end: 10 to 190 us more.
 template <typename T>
 __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
     const xp_verify_args a, int chunk, int chunks) {
