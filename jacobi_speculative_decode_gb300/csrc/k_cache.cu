@@ -51,13 +51,24 @@ __device__ __forceinline__ int block_scan(int v, Scan& s, int* sum) {
   return (w == 0 ? 0 : before) + inc - v;
 }
 
+// Every CTA says at its start that it runs, and waits for the others' word just before the first
+// store into their shared memory (which may not be reached before): the reads between hide it.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Sum of v over the CTA's threads, then the CTA's exclusive prefix among the cluster's (use:
-// the sum's own row).  Orders the cluster: whatever any CTA wrote before is visible behind it.
+// the sum's own row; 0 comes first).  Orders the cluster: whatever any CTA wrote before is visible
+// behind it.
 __device__ __forceinline__ int cluster_base(cg::cluster_group& cl, int use, int v, Scan& s,
                                             int* total) {
   int sum;
   block_scan(v, s, &sum);
   const int rank = (int)cl.block_rank();
+  if (use == 0) cluster_wait();
   if (threadIdx.x < kCtas) *cl.map_shared_rank(&s.total[use][rank], threadIdx.x) = sum;
   cl.sync();
   int base = 0, all = 0;
@@ -123,6 +134,7 @@ struct ResizeArgs {
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     resize_kernel(const ResizeArgs a) {
   __shared__ Scan s;
+  cluster_arrive();
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tid = (int)threadIdx.x;
   const int r0 = (int)((int64_t)a.N * rank / kCtas), r1 = (int)((int64_t)a.N * (rank + 1) / kCtas);
@@ -217,6 +229,7 @@ struct ForkArgs {
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     fork_kernel(const ForkArgs a) {
   __shared__ Scan s;
+  cluster_arrive();
   ptx::pdl_trigger();   // the next kernel's CTAs come up as this one's leave, and wait there
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tid = (int)threadIdx.x;
@@ -310,6 +323,7 @@ struct CompactArgs {
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     compact_kernel(const CompactArgs a) {
   __shared__ Scan s;
+  cluster_arrive();
   ptx::pdl_trigger();   // the next kernel's CTAs come up as this one's leave, and wait there
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), tid = (int)threadIdx.x;

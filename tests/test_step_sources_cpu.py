@@ -1,0 +1,42 @@
+"""Rules of the memory model that no run of a kernel can show to be broken, held to the sources."""
+import os
+import re
+
+from conftest import ROOT
+
+CSRC = os.path.join(ROOT, "jacobi_speculative_decode_gb300", "csrc")
+
+
+def source(name):
+    """A source without its comments."""
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", text, flags=re.S))
+
+
+def body(text, name):
+    """What stands between the braces of the function `name`."""
+    at = text.index("{", re.search(r"\b%s\s*\([^;{]*\)\s*\{" % name, text).start())
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at + 1:i]
+    raise ValueError(name)
+
+
+def test_peers_have_started_before_their_shared_memory_is_written():
+    # a CTA's shared memory may be reached by its cluster only once that CTA is known to run: every
+    # table kernel arrives on the cluster's barrier before all else, and the first remote store
+    # waits for it
+    text = source("k_cache.cu")
+    kernels = re.findall(r"__cluster_dims__\([^)]*\)[^{;]*?(\w+_kernel)\s*\(", text)
+    assert sorted(kernels) == ["compact_kernel", "fork_kernel", "resize_kernel"]
+    for k in kernels:
+        b = body(text, k)
+        first = b.index("cluster_base(")
+        assert -1 < b.find("cluster_arrive()") < first, k
+        assert re.match(r"cluster_base\(cl, 0,", b[first:]), k          # the use that waits
+        assert "map_shared_rank" not in b, k
+    base = body(text, "cluster_base")
+    assert -1 < base.find("if (use == 0) cluster_wait()") < base.index("map_shared_rank")
+    assert text.count("map_shared_rank") == 1
