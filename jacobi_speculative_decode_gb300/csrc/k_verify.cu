@@ -262,6 +262,11 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
     const int items = a.B * per_slot;
     int issued = 0;
     bool ok = true;
+    // marks[n] = B - (first rejected slot known so far), 0 when none is.  Other CTAs raise it
+    // meanwhile: lane 0 reads it and the warp takes its value, where it is used.
+    auto mark_of = [&](int i) {
+      return lane == 0 && i < items ? (int)__ldcg(&a.marks[i / chunks % a.N]) : a.B;
+    };
     // room for the next stage
     auto room = [&]() {
       const int s = issued % kStages;
@@ -294,12 +299,12 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
       do {
         const int n = min(kPer, v1 - v), s = room();
         if (!ok) return false;
-        if (item / per_slot > a.B - seen) {
+        if (item / per_slot > a.B - __shfl_sync(0xFFFFFFFFu, seen, 0)) {
           post(s, {item, kDropped, 0, 0}, nullptr);
           return false;
         }
         post(s, {item, kind | opens | (v + n == v1 ? ends : 0), v, n * 16}, row + head + (int64_t)v * VN);
-        seen = (int)__ldcg(&a.marks[item / chunks % a.N]);   // there by the time of the next stage
+        seen = mark_of(item);   // there by the time of the next stage
         v += n;
         opens = 0;
       } while (v < v1);
@@ -307,18 +312,17 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
     };
     // A CTA's first item is its own number, the others come from the counter.  The counter and
     // the next item's mark are read while this one streams.
-    // marks[n] = B - (first rejected slot known so far), 0 when none is
-    auto mark_of = [&](int i) { return i < items ? (int)__ldcg(&a.marks[i / chunks % a.N]) : a.B; };
     auto claim = [&]() {
       unsigned i = 0;
       if (lane == 0) i = min(gridDim.x + atomicAdd(a.next, 1u), (unsigned)items);
       return (int)i;
     };
-    int next = blockIdx.x, mark = mark_of(next), claimed = claim();
+    int next = blockIdx.x, mark = mark_of(next);
+    int claimed = claim();
     while (ok && next < items) {
       const int i = next, c = i % chunks, n = i / chunks % a.N, b = i / per_slot;
       const int drafts = drafts_of(a, n, c == 0 && b == 0 && lane == 0);
-      const bool wanted = b <= a.B - mark && b <= drafts;
+      const bool wanted = b <= a.B - __shfl_sync(0xFFFFFFFFu, mark, 0) && b <= drafts;
       next = __shfl_sync(0xFFFFFFFFu, claimed, 0);
       mark = mark_of(next);
       claimed = claim();

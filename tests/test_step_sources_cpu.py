@@ -40,3 +40,16 @@ def test_peers_have_started_before_their_shared_memory_is_written():
     base = body(text, "cluster_base")
     assert -1 < base.find("if (use == 0) cluster_wait()") < base.index("map_shared_rank")
     assert text.count("map_shared_rank") == 1
+
+
+def test_one_lane_reads_what_a_whole_warp_decides_by():
+    # marks change while the streaming warp reads them: lanes that read for themselves could decide
+    # differently before full-mask shuffles, so one lane reads and all take its value
+    b = body(source("k_verify.cu"), "verify_stats_kernel")
+    reads = [m.start() for m in re.finditer(r"__ldcg\(&a\.marks", b)]
+    assert len(reads) == 1
+    assert re.search(r"lane == 0[^;?]*\? \(int\)$", b[:reads[0]])
+    for name in ("mark", "seen"):       # every use but its assignments goes through lane 0's value
+        uses = [m for m in re.finditer(r"\b%s\b(?!\s*=[^=])" % name, b)]
+        shuffled = re.findall(r"__shfl_sync\(0xFFFFFFFFu, %s, 0\)" % name, b)
+        assert len(uses) == len(shuffled) == 1, name
