@@ -394,12 +394,19 @@ xp_status xp_cache_get_error(const xp_cache* cache, cudaStream_t stream);
  * position lens[n] - T + t (lens counts them already; positions below 0 are skipped).
  * k, v: device, element (n, t, head, i) at n*stride_n + t*stride_t + head*stride_h + i.
  * heads, head_dim, dtype: theirs; XP_EINVAL unless they are the cache's.  table: device
- * int32, row n at table + n*ld_table (ld_table >= its columns); lens: device [N] int32. */
+ * int32, row n at table + n*ld_table; lens: device [N] int32.  Positions behind a row's columns are
+ * skipped (XP_ELENGTH): xp_cache_append takes ld_table as their number, xp_cache_append_columns
+ * has `width` of them (a table that is some columns of a wider one). */
 xp_status xp_cache_append(const xp_cache* cache, int layer, const void* k, const void* v,
                           int64_t stride_n, int64_t stride_t, int64_t stride_h,
                           int heads, int head_dim, xp_dtype dtype, const int32_t* table,
                           int64_t ld_table, const int32_t* lens, int N, int T,
                           cudaStream_t stream);
+xp_status xp_cache_append_columns(const xp_cache* cache, int layer, const void* k, const void* v,
+                                  int64_t stride_n, int64_t stride_t, int64_t stride_h,
+                                  int heads, int head_dim, xp_dtype dtype, const int32_t* table,
+                                  int64_t ld_table, int width, const int32_t* lens, int N, int T,
+                                  cudaStream_t stream);
 
 /* The table calls below change page tables, lengths and reference counts (and, where they
  * say so, move pages of K and V in every layer).  Each output may be the matching input

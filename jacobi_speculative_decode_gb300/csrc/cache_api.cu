@@ -87,6 +87,19 @@ xp_attn_plan attn_plan(const xp_cache* c, const xp_attn* a) {
   return p;
 }
 
+xp_status append(const xp_cache* c, int layer, const void* k, const void* v, int64_t stride_n,
+                 int64_t stride_t, int64_t stride_h, int heads, int head_dim, xp_dtype dtype,
+                 const int32_t* table, int64_t ld_table, int64_t width, const int32_t* lens, int N,
+                 int T, cudaStream_t stream) {
+  if (!c) return XP_ENOTPREPARED;
+  if (heads != c->d.kv_heads || head_dim != c->d.head_dim || dtype != c->d.dtype || !k || !v || !table || !lens || layer < 0 || layer >= c->d.layers || N < 0 || T <= 0 ||
+      width <= 0 || ld_table < width || (int64_t)N * T * c->d.kv_heads > INT_MAX || !on_device(c))
+    return XP_EINVAL;
+  if (N == 0) return XP_OK;
+  return cuda_status(xp_launch_append(c, layer, k, v, stride_n, stride_t, stride_h, table, ld_table,
+                                      width, lens, N, T, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -154,13 +167,17 @@ xp_status xp_cache_append(const xp_cache* c, int layer, const void* k, const voi
                           int heads, int head_dim, xp_dtype dtype, const int32_t* table,
                           int64_t ld_table, const int32_t* lens, int N, int T,
                           cudaStream_t stream) {
-  if (!c) return XP_ENOTPREPARED;
-  if (heads != c->d.kv_heads || head_dim != c->d.head_dim || dtype != c->d.dtype || !k || !v || !table || !lens || layer < 0 || layer >= c->d.layers || N < 0 || T <= 0 ||
-      ld_table <= 0 || (int64_t)N * T * c->d.kv_heads > INT_MAX || !on_device(c))
-    return XP_EINVAL;
-  if (N == 0) return XP_OK;
-  return cuda_status(xp_launch_append(c, layer, k, v, stride_n, stride_t, stride_h, table, ld_table,
-                                      lens, N, T, stream));
+  return append(c, layer, k, v, stride_n, stride_t, stride_h, heads, head_dim, dtype, table,
+                ld_table, ld_table, lens, N, T, stream);
+}
+
+xp_status xp_cache_append_columns(const xp_cache* c, int layer, const void* k, const void* v,
+                                  int64_t stride_n, int64_t stride_t, int64_t stride_h,
+                                  int heads, int head_dim, xp_dtype dtype, const int32_t* table,
+                                  int64_t ld_table, int width, const int32_t* lens, int N, int T,
+                                  cudaStream_t stream) {
+  return append(c, layer, k, v, stride_n, stride_t, stride_h, heads, head_dim, dtype, table,
+                ld_table, width, lens, N, T, stream);
 }
 
 xp_status xp_cache_copy(const xp_cache* c, const int32_t* src, const int32_t* dst, int count,

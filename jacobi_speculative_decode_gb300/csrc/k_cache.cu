@@ -466,7 +466,7 @@ struct AppendArgs {
   void *kp, *vp;   // this layer's pools
   int64_t page, token, head;
   const int32_t* table;
-  int64_t ld;
+  int64_t ld, width;   // its columns: width
   const int32_t* lens;
   int N, T, H, D, ps, pages;
   uint32_t* err;
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   const int h = (int)(w % a.H), t = (int)(w / a.H % a.T), n = (int)(w / a.H / a.T);
   const int64_t pos = (int64_t)a.lens[n] - a.T + t;
   if (pos < 0) return;
-  if (pos / a.ps >= a.ld) {   // behind the row's columns
+  if (pos / a.ps >= a.width) {   // behind the row's columns
     if (lane == 0) flag(a.err, XP_ERR_LENGTH);
     return;
   }
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
 
 cudaError_t xp_launch_append(const xp_cache* c, int layer, const void* k, const void* v, int64_t sn,
                              int64_t st, int64_t sh, const int32_t* table, int64_t ld,
-                             const int32_t* lens, int N, int T, cudaStream_t s) {
+                             int64_t width, const int32_t* lens, int N, int T, cudaStream_t s) {
   const xp_cache_desc& d = c->d;
   const size_t es = xp_elem(d.dtype);
   char *kp = (char*)d.k + layer * d.stride_layer * es, *vp = (char*)d.v + layer * d.stride_layer * es;
@@ -512,7 +512,7 @@ cudaError_t xp_launch_append(const xp_cache* c, int layer, const void* k, const 
                     strides * (int64_t)es % 16 == 0;
   const int64_t unit = wide ? 16 / (int64_t)es : 1;   // elements
   AppendArgs a = {k, v, sn / unit, st / unit, sh / unit, kp, vp, d.stride_page / unit,
-                  d.stride_token / unit, d.stride_head / unit, table, ld, lens, N, T, d.kv_heads,
+                  d.stride_token / unit, d.stride_head / unit, table, ld, width, lens, N, T, d.kv_heads,
                   d.head_dim / (int)unit, d.page_size, d.pages, c->err};
   const int64_t warps = (int64_t)N * T * d.kv_heads;
   const unsigned grid = (unsigned)((warps + 7) / 8);

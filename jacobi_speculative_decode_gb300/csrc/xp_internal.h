@@ -198,7 +198,7 @@ struct xp_cache {
 
 cudaError_t xp_launch_append(const xp_cache* c, int layer, const void* k, const void* v, int64_t sn,
                              int64_t st, int64_t sh, const int32_t* table, int64_t ld,
-                             const int32_t* lens, int N, int T, cudaStream_t s);
+                             int64_t width, const int32_t* lens, int N, int T, cudaStream_t s);
 // moves given by the caller (n on the host) or left by a table kernel (n_moves on the device);
 // tokens == nullptr copies whole pages
 cudaError_t xp_launch_copy_pages(const xp_cache* c, const int32_t* src, const int32_t* dst,

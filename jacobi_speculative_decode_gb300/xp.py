@@ -99,6 +99,8 @@ _SIGS = {
     "xp_cache_destroy": (None, [_P]),
     "xp_cache_get_error": (_I, [_P, _P]),
     "xp_cache_append": (_I, [_P, _I, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P, _I64, _P, _I, _I, _P]),
+    "xp_cache_append_columns": (_I, [_P, _I, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P, _I64, _I, _P, _I, _I,
+                                     _P]),
     "xp_cache_copy": (_I, [_P, _P, _P, _I, _P]),
     "xp_cache_resize": (_I, [_P, _P, _I64, _P, _P, _P, _I, _I, _I, _P, _I64, _P, _P, _P]),
     "xp_cache_fork": (_I, [_P, _P, _I64, _P, _I, _P, _P, _I, _I, _P, _I, _P, _I64, _P, _P, _P]),
@@ -413,15 +415,17 @@ def xp_cache_get_error(cache, stream=None) -> int:
 
 
 def xp_cache_append(cache, layer, k, v, table, lens, stream=None):
-    """Write the K and V rows [N, T, kv_heads, head_dim] of the newest tokens (lens counts them)."""
+    """Write the K and V rows [N, T, kv_heads, head_dim] of the newest tokens (lens counts them).
+    Only the table's own columns are read, those of a wider tensor that it is a part of are not."""
     N, T = k.shape[:2]
     _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
           and k.stride(3) == 1, "k, v: [N, T, kv_heads, head_dim] of the same strides")
     ld = _table("table", table, N)
     _ints("lens", lens, N)
-    _check("xp_cache_append", lib().xp_cache_append(
+    _check("xp_cache_append", lib().xp_cache_append_columns(
         cache, layer, _ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), k.shape[2],
-        k.shape[3], _code("k", k), _ptr(table), ld, _ptr(lens), N, T, _stream(stream)))
+        k.shape[3], _code("k", k), _ptr(table), ld, table.shape[1], _ptr(lens), N, T,
+        _stream(stream)))
 
 
 def xp_cache_copy(cache, src, dst, stream=None):
