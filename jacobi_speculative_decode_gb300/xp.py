@@ -316,12 +316,22 @@ def xp_readout_kernel_name(head) -> str:
 # ------------------------------------- verification, cache and attention calls ---
 #
 # These calls take their sizes and strides from the tensors; a tensor that the C call could
-# not read as it is (another type, a strided last dimension, too few elements) is refused
-# with ValueError (whose text is made only then: a call's checks are part of its latency).
+# not read as it is (not on the current device, another type, a strided last dimension, too few
+# elements) is refused with ValueError (whose text is made only then: a call's checks are part of
+# its latency).
 
 def _want(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
+
+
+def _here(**tensors):
+    """All of them on the current device (None passes)."""
+    import torch
+    device = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name}: not on the current CUDA device")
 
 
 def _code(name, t):
@@ -343,11 +353,11 @@ def _ints(name, t, n):
 
 
 def _table(name, t, rows=None):
-    """An int32 page table [rows, width] on the GPU, unit stride over the columns."""
+    """An int32 page table [rows, width], unit stride over the columns."""
     import torch
-    if not (t.dtype == torch.int32 and t.is_cuda and t.dim() == 2 and t.shape[1] > 0
+    if not (t.dtype == torch.int32 and t.dim() == 2 and t.shape[1] > 0
             and (t.stride(1) == 1 or t.shape[1] == 1) and (rows is None or t.shape[0] >= rows)):
-        raise ValueError(f"{name}: an int32 CUDA tensor [rows, width], unit stride over the columns")
+        raise ValueError(f"{name}: an int32 tensor [rows, width], unit stride over the columns")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
@@ -363,7 +373,9 @@ def xp_verify_drafts(head, target, draft, blk, n_draft, temperature, u, noise, t
     import torch
     N, B, V = target.shape
     f32, i64, i32 = torch.float32, torch.int64, torch.int32
-    _want(target.stride(2) == 1 and target.is_cuda, "target: [N, B, V] with unit stride over V")
+    _here(target=target, draft=draft, blk=blk, n_draft=n_draft, temperature=temperature, u=u,
+          noise=noise, tokens=tokens, counts=counts, prob=prob, ws=ws)
+    _want(target.stride(2) == 1, "target: [N, B, V] with unit stride over V")
     _want(draft is None or (draft.dtype == f32 and draft.dim() == 2 and draft.stride(1) == 1
                             and draft.shape[0] >= N * (B - 1) and draft.shape[1] >= V),
           "draft: fp32 [N*(B-1), >= V] with unit stride over V")
@@ -385,9 +397,10 @@ def xp_verify_drafts(head, target, draft, blk, n_draft, temperature, u, noise, t
 def make_cache_desc(k, v, max_seqs: int = 4096) -> xp_cache_desc:
     """Descriptor of K and V pools seen as [layers, pages, page_size, kv_heads, head_dim] (views
     with the heads outside the tokens too)."""
+    _here(k=k, v=v)
     _want(k.dim() == 5 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
-          and k.stride(4) == 1 and k.is_cuda and v.is_cuda,
-          "k, v: bf16 or fp32 CUDA tensors [layers, pages, page_size, kv_heads, head_dim] of the "
+          and k.stride(4) == 1,
+          "k, v: bf16 or fp32 tensors [layers, pages, page_size, kv_heads, head_dim] of the "
           "same strides, unit stride over head_dim")
     layers, pages, ps, heads, dim = k.shape
     return xp_cache_desc(pages, ps, layers, heads, dim, max_seqs, _code("k", k), k.stride(0),
@@ -400,6 +413,7 @@ def xp_cache_prep_bytes(d: xp_cache_desc) -> int:
 
 def xp_cache_create(d: xp_cache_desc, prep, stream=None):
     out = ctypes.c_void_p()
+    _here(prep=prep)
     _check("xp_cache_create", lib().xp_cache_create(ctypes.byref(d), _ptr(prep), _nbytes(prep),
                                                     _stream(stream), ctypes.byref(out)))
     return out.value
@@ -418,6 +432,7 @@ def xp_cache_append(cache, layer, k, v, table, lens, stream=None):
     """Write the K and V rows [N, T, kv_heads, head_dim] of the newest tokens (lens counts them).
     Only the table's own columns are read, those of a wider tensor that it is a part of are not."""
     N, T = k.shape[:2]
+    _here(k=k, v=v, table=table, lens=lens)
     _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
           and k.stride(3) == 1, "k, v: [N, T, kv_heads, head_dim] of the same strides")
     ld = _table("table", table, N)
@@ -430,6 +445,7 @@ def xp_cache_append(cache, layer, k, v, table, lens, stream=None):
 
 def xp_cache_copy(cache, src, dst, stream=None):
     """Copy whole pages src[i] -> dst[i] in every layer."""
+    _here(src=src, dst=dst)
     _ints("src", src, 0)
     _ints("dst", dst, src.numel())
     _check("xp_cache_copy", lib().xp_cache_copy(cache, _ptr(src), _ptr(dst), src.numel(),
@@ -439,6 +455,8 @@ def xp_cache_copy(cache, src, dst, stream=None):
 def xp_cache_resize(cache, table, lens, new_lens, refs, table_out, lens_out, refs_out, stream=None):
     """Lengths lens -> new_lens: give back or take pages (outputs may be the inputs)."""
     N, width = table.shape
+    _here(table=table, lens=lens, new_lens=new_lens, refs=refs, table_out=table_out,
+          lens_out=lens_out, refs_out=refs_out)
     ld, ld_out = _table("table", table), _table("table_out", table_out, N)
     _want(table_out.shape[1] >= width, "table_out: as wide as table")
     for name, t in (("lens", lens), ("new_lens", new_lens), ("lens_out", lens_out)):
@@ -455,6 +473,8 @@ def xp_cache_fork(cache, table, lens, parent, cut, refs, child_table, child_lens
     """Children parent[i] continued at min(lens[parent[i]], cut[i]) (cut may be None)."""
     rows, width = table.shape
     M = parent.numel()
+    _here(table=table, lens=lens, parent=parent, cut=cut, refs=refs, child_table=child_table,
+          child_lens=child_lens, refs_out=refs_out)
     ld, ld_child = _table("table", table), _table("child_table", child_table, M)
     _want(child_table.shape[1] >= width, "child_table: as wide as table")
     for name, t, n in (("lens", lens, rows), ("parent", parent, M), ("cut", cut, M),
@@ -470,6 +490,8 @@ def xp_cache_compact(cache, table, lens, refs, table_out, refs_out, map=None, li
                      stream=None):
     """Pack the pages in use to the pool's front; map[page] is each page's new id."""
     N, width = table.shape
+    _here(table=table, lens=lens, refs=refs, table_out=table_out, refs_out=refs_out, map=map,
+          live=live)
     ld, ld_out = _table("table", table), _table("table_out", table_out, N)
     _want(table_out.shape[1] >= width, "table_out: as wide as table")
     _ints("lens", lens, N)
@@ -500,15 +522,17 @@ def xp_attention_workspace_bytes(cache, attn: xp_attn) -> int:
 def xp_prefix_attention(cache, attn, q, prefix_table, table, lens, out, lse, ws, stream=None):
     """Attention of attn.N sequences of attn.T new tokens over a shared prefix and their tails
     (attn from make_attn for tensors of these shapes and strides)."""
+    import torch
     _want((q.shape, q.stride(), q.dtype) == attn.q_like
           and (out.shape, out.stride(), out.dtype) == attn.out_like,
           "q, out: the shapes, strides and type that make_attn was given")
+    _here(q=q, prefix_table=prefix_table, table=table, lens=lens, out=out, lse=lse, ws=ws)
     ld = width = 0
     if table is not None:
         ld, width = _table("table", table, attn.N), table.shape[1]
     _ints("lens", lens, attn.N)
     _ints("prefix_table", prefix_table, 0)
-    _want(lse is None or (lse.is_contiguous() and lse.element_size() == 4
+    _want(lse is None or (lse.is_contiguous() and lse.dtype == torch.float32
                           and lse.numel() >= attn.N * attn.T * attn.heads),
           "lse: contiguous fp32 [N, T, heads]")
     _check("xp_prefix_attention", lib().xp_prefix_attention(
