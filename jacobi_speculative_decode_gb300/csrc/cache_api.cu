@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <new>
+#include <numeric>
 
 #include "xp_internal.h"
 
@@ -85,6 +86,22 @@ xp_attn_plan attn_plan(const xp_cache* c, const xp_attn* a) {
   p.acc_off = align_up(rows * p.parts * 8);
   p.total = p.acc_off + align_up(rows * p.parts * c->d.head_dim * 4);
   return p;
+}
+
+// Whether rows of two tables (a: na rows lda apart, b likewise) share entries: 0 no, 1 the same
+// columns of the same rows only, -1 an entry of another column too (or strides too unlike to tell).
+int table_overlap(const int32_t* a, int64_t lda, int na, const int32_t* b, int64_t ldb, int nb,
+                  int width) {
+  if (na == 0 || nb == 0) return 0;
+  if (na == 1) lda = nb == 1 ? 2 * (int64_t)width : ldb;   // one row has no stride of its own
+  if (nb == 1) ldb = lda;
+  const intptr_t a0 = (intptr_t)a, b0 = (intptr_t)b, es = sizeof(int32_t);
+  if (a0 + ((na - 1) * lda + width) * es <= b0 || b0 + ((nb - 1) * ldb + width) * es <= a0) return 0;
+  // all rows of both begin at multiples of `unit` from a, or d behind one (told apart only where a
+  // unit holds a row)
+  const int64_t unit = std::gcd(lda, ldb), d = (((b0 - a0) / es) % unit + unit) % unit;
+  if (d == 0 && unit >= width) return 1;
+  return d >= width && d + width <= unit ? 0 : -1;
 }
 
 xp_status append(const xp_cache* c, int layer, const void* k, const void* v, int64_t stride_n,
@@ -211,9 +228,11 @@ xp_status xp_cache_fork(const xp_cache* c, const int32_t* table, int64_t ld_tabl
   if (!parent || !refs || pages != c->d.pages || !child_table || !child_lens || !refs_out ||
       ld_child < width || M < 0)
     return XP_EINVAL;
-  if (M > c->d.max_seqs) return XP_ECAPACITY;
+  const int shared = table_overlap(table, ld_table, rows, child_table, ld_child, M, width);
+  if (shared < 0) return XP_EINVAL;
+  if (M > c->d.max_seqs || (shared && M > xp_fork_rows_in_place)) return XP_ECAPACITY;
   return cuda_status(xp_launch_fork(c, table, ld_table, lens, rows, parent, cut, M, width, refs,
-                                    child_table, ld_child, child_lens, refs_out, stream));
+                                    shared != 0, child_table, ld_child, child_lens, refs_out, stream));
 }
 
 xp_status xp_cache_compact(const xp_cache* c, const int32_t* table, int64_t ld_table,

@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kCtas = 8;
 constexpr int kThreads = 1024;
+constexpr int kForkHeld = xp_fork_rows_in_place / (kCtas * kThreads);   // entries a thread holds
 
 struct Scan {
   int warp[32];
@@ -218,6 +219,7 @@ struct ForkArgs {
   int rows;
   const int32_t *parent, *cut, *refs;
   int M, width, pages, ps;
+  bool in_place;   // children are rows of the parents' table: all are read before any is written
   int32_t* child;
   int64_t ld_child;
   int32_t *child_lens, *refs_out;
@@ -266,23 +268,52 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
   for (int i0 = r0; i0 < r1; i0 += kThreads) {
     const int i = i0 + tid;
     int sum;
-    const int off = base + block_scan(i < r1 && a.row_len[i] % a.ps != 0, s, &sum);
+    const int part = i < r1 ? a.row_len[i] % a.ps : 0;
+    const int off = base + block_scan(part != 0, s, &sum);
     if (i < r1) a.row_off[i] = off;
+    if (part && off < a.pages) {   // there are no more moves than pages
+      a.src[off] = a.table[a.row_parent[i] * a.ld + a.row_len[i] / a.ps];
+      a.cnt[off] = part;
+    }
     base += sum;
   }
 
   // full pages are shared
-  for (int i = r0 + (tid >> 5); i < r1; i += kThreads / 32) {
-    const int full = a.row_len[i] / a.ps;
-    const int32_t* row = a.table + a.row_parent[i] * a.ld;
-    for (int j = tid & 31; j < a.width; j += 32) {
-      int out = -1;
-      if (j < full) {
-        out = row[j];
-        if (out >= 0 && out < a.pages) atomicAdd(&a.refs_out[out], 1);
-        else flag(a.err, XP_ERR_BADPAGE);
+  auto shared_page = [&](const int32_t* row, int full, int j) {
+    int out = -1;
+    if (j < full) {
+      out = row[j];
+      if (out >= 0 && out < a.pages) atomicAdd(&a.refs_out[out], 1);
+      else flag(a.err, XP_ERR_BADPAGE);
+    }
+    return out;
+  };
+  if (!a.in_place) {
+    for (int i = r0 + (tid >> 5); i < r1; i += kThreads / 32) {
+      const int full = a.row_len[i] / a.ps;
+      const int32_t* row = a.table + a.row_parent[i] * a.ld;
+      for (int j = tid & 31; j < a.width; j += 32)
+        a.child[i * a.ld_child + j] = shared_page(row, full, j);
+    }
+  } else {
+    // some columns of all rows at a time: a child's column is made from its parent's alone
+    const int rows = (a.M + kCtas - 1) / kCtas, cols = max(1, kThreads * kForkHeld / rows);
+    for (int c0 = 0; c0 < a.width; c0 += cols) {
+      const int cw = min(cols, a.width - c0), entries = (r1 - r0) * cw;
+      int out[kForkHeld];
+#pragma unroll
+      for (int k = 0; k < kForkHeld; ++k) {
+        const int e = tid + k * kThreads;
+        const int i = r0 + e / cw;
+        if (e < entries)
+          out[k] = shared_page(a.table + a.row_parent[i] * a.ld, a.row_len[i] / a.ps, c0 + e % cw);
       }
-      a.child[i * a.ld_child + j] = out;
+      cl.sync();
+#pragma unroll
+      for (int k = 0; k < kForkHeld; ++k) {
+        const int e = tid + k * kThreads;
+        if (e < entries) a.child[(r0 + e / cw) * a.ld_child + c0 + e % cw] = out[k];
+      }
     }
   }
   cl.sync();
@@ -295,8 +326,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     const int part = len % a.ps, full = len / a.ps, off = a.row_off[i];
     if (part) {
       if (off < n_free) {
-        a.src[off] = a.table[a.row_parent[i] * a.ld + full];
-        a.cnt[off] = part;
         a.child[i * a.ld_child + full] = a.dst[off];
       } else {
         flag(a.err, XP_ERR_NOPAGES);
@@ -566,10 +595,10 @@ cudaError_t xp_launch_resize(const xp_cache* c, const int32_t* table, int64_t ld
 cudaError_t xp_launch_fork(const xp_cache* c, const int32_t* table, int64_t ld,
                            const int32_t* lens, int rows, const int32_t* parent,
                            const int32_t* cut, int M, int width, const int32_t* refs,
-                           int32_t* child, int64_t ld_child, int32_t* child_lens,
+                           bool in_place, int32_t* child, int64_t ld_child, int32_t* child_lens,
                            int32_t* refs_out, cudaStream_t s) {
   ForkArgs a = {table, ld, lens, rows, parent, cut, refs, M, width, c->d.pages, c->d.page_size,
-                child, ld_child, child_lens, refs_out, c->row_a, c->row_b, c->row_c,
+                in_place, child, ld_child, child_lens, refs_out, c->row_a, c->row_b, c->row_c,
                 c->src, c->dst, c->cnt, c->n_moves, c->err};
   fork_kernel<<<kCtas, kThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();

@@ -208,10 +208,12 @@ cudaError_t xp_launch_resize(const xp_cache* c, const int32_t* table, int64_t ld
                              const int32_t* lens, const int32_t* new_lens, const int32_t* refs,
                              int N, int width, int32_t* table_out, int64_t ld_out,
                              int32_t* lens_out, int32_t* refs_out, cudaStream_t s);
+// children that may be rows of their parents' table (in_place): a row's entry each is held meanwhile
+constexpr int xp_fork_rows_in_place = 65536;
 cudaError_t xp_launch_fork(const xp_cache* c, const int32_t* table, int64_t ld,
                            const int32_t* lens, int rows, const int32_t* parent,
                            const int32_t* cut, int M, int width, const int32_t* refs,
-                           int32_t* child, int64_t ld_child, int32_t* child_lens,
+                           bool in_place, int32_t* child, int64_t ld_child, int32_t* child_lens,
                            int32_t* refs_out, cudaStream_t s);
 cudaError_t xp_launch_compact(const xp_cache* c, const int32_t* table, int64_t ld,
                               const int32_t* lens, int N, int width, const int32_t* refs,

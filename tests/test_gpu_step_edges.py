@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from jacobi_speculative_decode_gb300 import xp
+from oracle import step_oracle as S
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,75 @@ def test_append_keeps_to_the_columns_of_its_table(first):
         pool[0, row[0], ps - 1] = new[1, 0]
         pool[0, row[1], 0] = new[1, 1]
     assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
+def beams(g, rows, width, ps):
+    """A table of `rows` filled rows over shuffled pages, lengths, counts and an fp32 pool for it."""
+    lens = g.integers(0, width * ps + 1, rows).astype(np.int32)
+    used = -(-lens // ps)
+    pages = int(used.sum()) + 2 * rows + 3
+    ids, at = g.permutation(pages).astype(np.int32), 0
+    table, refs = np.full((rows, width), -1, np.int32), np.zeros(pages, np.int32)
+    for n, u in enumerate(used):
+        table[n, :u] = ids[at:at + u]
+        at += u
+    refs[ids[:at]] = 1
+    return table, lens, refs, torch.arange(pages * ps * 4, device="cuda").view(1, pages, ps, 1, 4).float()
+
+
+@pytest.mark.parametrize("rows,width,ps", [(2, 1, 3), (4, 3, 4), (33, 20, 5), (40, 400, 2), (1500, 7, 4)])
+@pytest.mark.parametrize("first", [0, 1])
+def test_fork_over_its_own_parents(rows, width, ps, first):
+    # a beam's reorder: children take the places of rows that are parents of others, in a table that
+    # is some columns of a wider one
+    g = np.random.default_rng(rows + width + first)
+    table, lens, refs, k = beams(g, rows, width, ps)
+    M = rows - first
+    parent = g.integers(0, rows, M).astype(np.int32)
+    parent[:M // 2] = (np.arange(M // 2) + 1) % rows
+    cut = g.integers(0, width * ps + 1, M).astype(np.int32)
+    v = k + 0.5
+    want_k, want_v = k.clone(), v.clone()
+    cache = xp.Cache(k, v)
+    wide = torch.full((rows, width + 5), 99, dtype=torch.int32, device="cuda")
+    t = wide[:, 2:2 + width]
+    t.copy_(ints(table))
+    n, r = ints(lens), ints(refs)
+    xp.xp_cache_fork(cache.handle, t, n, ints(parent), ints(cut), r, t[first:], n[first:], r)
+    assert xp.xp_cache_get_error(cache.handle) == xp.XP_OK
+    child, child_lens, want_refs, moves = S.fork(table, lens, parent, cut, refs, ps)
+    assert np.array_equal(t[first:].cpu().numpy(), child)
+    assert np.array_equal(t[:first].cpu().numpy(), table[:first])
+    assert np.array_equal(n[first:].cpu().numpy(), child_lens)
+    assert np.array_equal(r.cpu().numpy(), want_refs)
+    assert (wide[:, :2] == 99).all() and (wide[:, 2 + width:] == 99).all()
+    for s, d, count in moves:
+        want_k[:, d, :count], want_v[:, d, :count] = want_k[:, s, :count], want_v[:, s, :count]
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
+def test_fork_between_tables_that_lie_among_each_other():
+    # columns side by side and rows in turn share no entry; a shift by a column is refused
+    k = torch.zeros(1, 16, 4, 1, 4, device="cuda")
+    cache = xp.Cache(k, k.clone())
+    refs = ints([1, 1, 1] + [0] * 13)
+    both = ints(np.full((4, 6), -1))
+    for parents, children in ((both[:2, :3], both[:2, 3:]), (both[::2, :3], both[1::2, :3])):
+        both.fill_(-1)
+        parents.copy_(ints([[2, 0, -1], [1, -1, -1]]))
+        lens, out_lens, out_refs = ints([8, 4]), ints([0, 0]), refs.clone()
+        xp.xp_cache_fork(cache.handle, parents, lens, ints([1, 0]), None, refs, children, out_lens,
+                         out_refs)
+        assert xp.xp_cache_get_error(cache.handle) == xp.XP_OK
+        assert children.tolist() == [[1, -1, -1], [2, 0, -1]] and out_lens.tolist() == [4, 8]
+        assert parents.tolist() == [[2, 0, -1], [1, -1, -1]]
+        assert out_refs.tolist()[:4] == [2, 2, 2, 0]
+    before = both.clone()
+    for parents, children in ((both[:2, :3], both[:2, 1:4]), (both[:2, :3], both[1:3, 2:5]),
+                              (both[:1, :3], both[:1, 1:4]),
+                              (both.view(-1)[:20].view(5, 4)[:3, :3], both[:2, :3])):
+        with pytest.raises(xp.XPError) as e:
+            xp.xp_cache_fork(cache.handle, parents, ints([4] * len(parents)), ints([0] * len(children)),
+                             None, refs, children, ints([0] * len(children)), refs.clone())
+        assert e.value.code == xp.XP_EINVAL
+    assert torch.equal(both, before)
