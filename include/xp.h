@@ -338,8 +338,8 @@ const char* xp_readout_kernel_name(const xp_head* head);
  * stride over v.  draft: device fp32, row n*(B-1) + b at draft + (n*(B-1) + b)*ld_draft (the
  * layout xp_refine_logits writes), or NULL.  blk: device [N, B] int64.  n_draft: device [N]
  * int32 (clamped to [0, B-1], XP_ELENGTH), or NULL for B-1.  temperature: device [N] fp32, or
- * NULL for 1; a negative or NaN one counts as 0.  u: device [N, B-1] fp32 in [0, 1).  noise:
- * device fp32 > 0, row n at noise + n*ld_noise.
+ * NULL for 1; one below the least normal float (1.1755e-38), negative or NaN counts as 0.
+ * u: device [N, B-1] fp32 in [0, 1).  noise: device fp32 > 0, row n at noise + n*ld_noise.
  * tokens (out): device [N, B] int64: the accepted drafts, then the drawn token, then -1.
  * counts (out): device [N] int32, tokens emitted (accepted + 1).  prob (out): device
  * [N, B-1] fp32 = min(1, p_b(x_b) / q_b(x_b)) for the slots tested, 0 behind them, or NULL.

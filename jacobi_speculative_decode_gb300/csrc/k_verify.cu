@@ -29,6 +29,11 @@ constexpr float kLog2e = 1.44269504088896f;
 __device__ __forceinline__ float read_logit(float l, float inv_t) {
   return fminf(fmaxf(l * inv_t, -INFINITY), FLT_MAX);
 }
+// e^((l - m) / t) for a row's maximum m.  The difference is taken before it is scaled: l / t and m / t
+// apart would be rounded at their own size, and clipped where t is small.
+__device__ __forceinline__ float share(float l, float m, float inv_t) {
+  return expf((read_logit(l, 1.0f) - m) * inv_t);
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -76,7 +81,7 @@ __device__ __forceinline__ Stat warp_join(Stat v, float c) {
 
 __device__ __forceinline__ float heat_of(const xp_verify_args& a, int n) {
   const float t = a.temperature ? a.temperature[n] : 1.0f;
-  return t > 0.0f ? t : 0.0f;
+  return t >= FLT_MIN ? t : 0.0f;   // of a smaller one 1 / t is not finite, or its product with log2 e
 }
 __device__ __forceinline__ int drafts_of(const xp_verify_args& a, int n, bool tell) {
   if (!a.n_draft) return a.B - 1;
@@ -416,12 +421,10 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
           px = x == top ? 1.0f : 0.0f;
         } else {
           const T* t_row = (const T*)a.target + n * a.sn + b * a.sb;
-          px = expf(read_logit(to_f(t_row[x]), inv_t) - read_logit(t.m, inv_t)) / t.s;
+          px = share(to_f(t_row[x]), t.m, inv_t) / t.s;
           if (draft) {
             const float* d_row = a.draft + ((int64_t)n * (a.B - 1) + b) * a.ld_draft;
-            qx = d.m > -INFINITY
-                     ? expf(read_logit(d_row[x], inv_t) - read_logit(d.m, inv_t)) / d.s
-                     : 0.0f;
+            qx = d.m > -INFINITY ? share(d_row[x], d.m, inv_t) / d.s : 0.0f;
           }
         }
       }

@@ -3,15 +3,15 @@ table calls, and shared-prefix attention.  Test infrastructure: shares no code w
 import numpy as np
 
 
-def softmax(z):
-    """Probabilities of one row of logits; NaN reads as -inf, +inf as the largest finite value;
-    all zeros when nothing is above -inf."""
+def softmax(z, heat=1.0):
+    """Probabilities of one row of logits at a temperature; NaN reads as -inf, +inf as the largest
+    finite value; all zeros when nothing is above -inf."""
     z = np.asarray(z, np.float64)
     z = np.where(np.isnan(z), -np.inf, np.minimum(z, np.finfo(np.float32).max))
     top = z.max()
     if top == -np.inf:
         return np.zeros_like(z)
-    e = np.exp(z - top)
+    e = np.where(z > -np.inf, np.exp(np.maximum(z - top, -1e39) / heat), 0)
     return e / e.sum()
 
 
@@ -26,20 +26,20 @@ def verify(target, draft, blk, n_draft, temperature, u, noise):
     margin = np.full(N, np.inf)
     for n in range(N):
         heat = 1.0 if temperature is None else float(temperature[n])
-        heat = heat if heat > 0 else 0.0
+        heat = heat if heat >= np.finfo(np.float32).tiny else 0.0
         D = B - 1 if n_draft is None else int(np.clip(n_draft[n], 0, B - 1))
 
         def p_of(b):
             row = np.asarray(target[n, b], np.float64)
             if heat:
-                return softmax(row / heat)
+                return softmax(row, heat)
             row = np.where(np.isnan(row), -np.inf, row)
             return (np.arange(V) == np.argmax(row)) * float(row.max() > -np.inf)
 
         def q_of(b):
             if draft is None or not heat:
                 return (np.arange(V) == blk[n, 1 + b]).astype(np.float64)
-            return softmax(np.asarray(draft[n * (B - 1) + b], np.float64) / heat)
+            return softmax(draft[n * (B - 1) + b], heat)
 
         a = D
         for b in range(D):

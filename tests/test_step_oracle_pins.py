@@ -71,3 +71,19 @@ def test_attention_by_hand():
     assert np.allclose(out[0, :, 0], [[2, 4], [4, 2]]) and np.allclose(lse[0, :, 0], [0, np.log(2)])
     out, lse, _, _ = S.attention(q, kp[:0], vp[:0], [tail], 1.0)
     assert np.allclose(out[0, :, 0], [[0, 0], [6, 0]]) and lse[0, 0, 0] == -np.inf
+
+
+def test_temperatures_scale_differences():
+    # the difference to the maximum is what is scaled: no clipping, however small the temperature
+    p = S.softmax([20.0, 5.0, 20.0, -np.inf, 1e38], 1e-38)
+    assert p.tolist() == [0, 0, 0, 0, 1]
+    assert S.softmax([20.0, 5.0, 20.0], 1e-38).tolist() == [0.5, 0, 0.5]
+    assert np.allclose(S.softmax([3e38, 3e38, -3e38], 10.0), [0.5, 0.5, 0])
+    assert np.allclose(S.softmax([8.0, 8.0 - 1e-3 * np.log(3), -np.inf], 1e-3), [0.75, 0.25, 0])
+    # the least temperature that is one
+    t = np.array([[[5.0, 20.0, 20.0], [0, 0, 0]]])
+    e = np.array([[1.0, 2.0, 1.0]])
+    for heat, token in ((2e-38, 2), (1e-38, 1), (-1.0, 1), (np.nan, 1)):
+        tok, count, prob, _ = S.verify(t, None, np.array([[0, 0]]), None, np.array([heat]),
+                                       np.array([[0.0]]), e)
+        assert tok.tolist() == [[token, -1]] and count[0] == 1 and prob[0, 0] == 0
