@@ -144,9 +144,12 @@ template <typename T>
 __device__ __forceinline__ float batch_stat(const uint4 (&x)[kLoads], float k, Stat& st) {
   constexpr int VN = Vec<T>::N;
   const float m = fminf(Vec<T>::top(x), FLT_MAX), now = fmaxf(st.m, m), base = base_of(now);
-  // two logits an instruction: 2^(l k - base k)
+  // two logits an instruction: 2^(l k - bk), bk = base k rounded; what that rounding took, at most
+  // 2^-11, is given back to the sum: 2^(bk - base k) = 1 + ln 2 (bk - base k), within 2^-23
   uint64_t sum[2] = {0, 0};
-  const uint64_t k2 = pair(k, k), b2 = pair(-base * k, -base * k);
+  const float bk = __fmul_rn(base, k);
+  float back = fmaf(fmaf(-base, k, bk), 0.693147180559945f, 1.0f);
+  const uint64_t k2 = pair(k, k), b2 = pair(-bk, -bk);
 #pragma unroll
   for (int u = 0; u < kLoads; ++u)
 #pragma unroll
@@ -156,15 +159,16 @@ __device__ __forceinline__ float batch_stat(const uint4 (&x)[kLoads], float k, S
     }
   sum[0] = add2(sum[0], sum[1]);
   float s = low(sum[0]) + high(sum[0]);
-  // NaN or +inf among them, or a base whose rounding would show: logit by logit
-  if (!(s <= (float)(kLoads * VN + 1)) || fabsf(base * k) > 16384.0f) {
+  // NaN or +inf among them, or a base whose rounding is more: logit by logit
+  if (!(s <= (float)(kLoads * VN + 1)) || fabsf(bk) > 16384.0f) {
     s = 0.0f;
+    back = 1.0f;
 #pragma unroll
     for (int u = 0; u < kLoads; ++u)
 #pragma unroll 1
       for (int e = 0; e < VN; ++e) s += weight(element<T>(x[u], e), k, base);
   }
-  st.s = st.s * weight(st.m, k, base) + s;
+  st.s = fmaf(s, back, st.s * weight(st.m, k, base));
   st.m = now;
   return m;
 }

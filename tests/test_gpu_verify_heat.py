@@ -80,3 +80,11 @@ def test_tests_of_slots_at_tiny_temperatures(dtype):
     assert np.array_equal(counts, np.full(c.N, 2)) and (tokens[:, 0] == 100).all()
     assert np.array_equal(prob, np.tile(np.float32([1, 0, 0]), (c.N, 1)))
     assert np.array_equal(counts, c.want()[1]) and np.array_equal(prob, c.want()[2])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heat,offset", [(0.01, 8.0), (1.0, 3000.0), (0.7, -7000.0), (0.6, 40.0)])
+def test_sums_behind_a_large_maximum(heat, offset, dtype):
+    # the maximum's scaled value is large enough for its rounding to show in a sum of its own
+    c = heated(heat, offset, False, V=5000, dtype=dtype, seed=3)
+    held(c, tokens=False)
