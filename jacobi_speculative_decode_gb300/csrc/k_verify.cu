@@ -25,14 +25,14 @@ constexpr int kStages = 4;              // 64 KB in flight a CTA
 constexpr int kResident = 2;            // CTAs an SM
 constexpr float kLog2e = 1.44269504088896f;
 
-// a logit as the softmax reads it: scaled, NaN as -inf, +inf as the largest finite value
-__device__ __forceinline__ float read_logit(float l, float inv_t) {
-  return fminf(fmaxf(l * inv_t, -INFINITY), FLT_MAX);
+// a logit as the softmax reads it: NaN as -inf, +inf as the largest finite value
+__device__ __forceinline__ float read_logit(float l) {
+  return fminf(fmaxf(l, -INFINITY), FLT_MAX);
 }
 // e^((l - m) / t) for a row's maximum m.  The difference is taken before it is scaled: l / t and m / t
 // apart would be rounded at their own size, and clipped where t is small.
 __device__ __forceinline__ float share(float l, float m, float inv_t) {
-  return expf((read_logit(l, 1.0f) - m) * inv_t);
+  return expf((read_logit(l) - m) * inv_t);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -193,7 +193,7 @@ __device__ __forceinline__ int id_of(const T* row, int V, int v1, const Top& t, 
       if (at < v1)
         for (int e = VN - 1; e >= 0; --e) {
           const int v = head + at * VN + e;
-          if (read_logit(to_f(row[v]), 1.0f) == m) id = min(id, v);
+          if (read_logit(to_f(row[v])) == m) id = min(id, v);
         }
     }
   return id;
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
                       : c == chunks - 1 && i >= 32 && i < 32 + rest ? a.V - rest + i - 32
                                                                     : -1;
         if (v < 0) return;
-        const float l = read_logit(to_f(row[v]), 1.0f);
+        const float l = read_logit(to_f(row[v]));
         if (heat == 0.0f) {
           tp.single = l;
           tp.single_id = v;
@@ -555,34 +555,34 @@ __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
 // from quick exponentials and logarithms, and keeps each thread's highest bound and the one
 // after it; the exact form, which alone counts, is computed for the highest, and for the
 // others only where their bound reaches the best exact value of the CTA.
-//  one row (TWO false): log2(p / e) = l k - shift - log2 e, as l k - log2 e
+//  one row (TWO false): log2(p / e) + log2 s = (l - m) k - log2 e
 //  two rows: (p (1 + d) - q (1 - d)) / e
-// `slack` and d = 2^-14 cover the rounding of l k at most 200 below the maximum, of ex2, lg2
-// and of the exact form's own exponent.
+// Both forms take the same rounded difference l - m (of p down to 2^-150) and scale it by factors
+// that differ by 2^-22 at most: 4e-5 in the exponent.  `slack` = 2e-4 and d = 2^-14 cover that, and
+// the errors of ex2, lg2 (2^-22 of |log2 e|) and expf.
 struct Race {
-  float inv_t, inv_s, tz, inv_d, dz;   // dz, inv_d: the draft's, where it has a row
-  float k, slack, shift;
+  static constexpr float slack = 2e-4f;
+  float inv_t, inv_s, m, inv_d, dm;    // dm, inv_d: the draft's, where it has a row
+  float k, shift;
   int64_t x;                           // a one-hot draft's id, -1
 
   __device__ __forceinline__ void start(float heat, float tm, float ts) {
     inv_t = 1.0f / heat;
     inv_s = 1.0f / ts;
-    tz = read_logit(tm, inv_t);
+    m = tm;
     k = inv_t * kLog2e;
-    shift = tz * kLog2e + log2f(ts);
-    slack = 1e-4f + fabsf(tz) * 1e-6f;
+    shift = log2f(ts);
   }
   template <bool TWO>
   __device__ __forceinline__ float bound(float l, float d, float e) const {
     if (TWO) {
       constexpr float kMore = 1.0f + 1.0f / 16384, kLess = 1.0f - 1.0f / 16384;
-      const float p = __saturatef(ex2((l * inv_t - tz) * kLog2e)) * inv_s;
-      const float q = __saturatef(ex2((d * inv_t - dz) * kLog2e)) * inv_d;
+      const float p = weight(l, k, m) * inv_s, q = weight(d, k, dm) * inv_d;
       return __fdividef(p * kMore - q * kLess, e) * kMore;
     }
     float lg;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(e));
-    return fmaf(l, k, -lg);
+    return fmaf(l - m, k, -lg);
   }
   // the bound that an exact value of `best` asks for
   template <bool TWO>
@@ -593,8 +593,8 @@ struct Race {
   }
   template <bool TWO>
   __device__ __forceinline__ unsigned long long exact(float l, float d, float e, int v) const {
-    const float p = expf(read_logit(l, inv_t) - tz) * inv_s;
-    const float q = TWO ? expf(read_logit(d, inv_t) - dz) * inv_d : v == x ? 1.0f : 0.0f;
+    const float p = share(l, m, inv_t) * inv_s;
+    const float q = TWO ? share(d, dm, inv_t) * inv_d : v == x ? 1.0f : 0.0f;
     return p > q && (p - q) / e > 0.0f ? pack_best((p - q) / e, (uint32_t)v) : 0ull;
   }
 };
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 5) verify_draw_kernel(const xp_verif
     unsigned long long best;
     if (two) {
       r.inv_d = 1.0f / a.row[row * 5 + 3];
-      r.dz = read_logit(dm, r.inv_t);
+      r.dm = dm;
       best = race<T, true>(r, t_row, d_row, e_row, lo, hi, &s_best);
     } else {
       best = race<T, false>(r, t_row, nullptr, e_row, lo, hi, &s_best);

@@ -88,3 +88,54 @@ def test_sums_behind_a_large_maximum(heat, offset, dtype):
     # the maximum's scaled value is large enough for its rounding to show in a sum of its own
     c = heated(heat, offset, False, V=5000, dtype=dtype, seed=3)
     held(c, tokens=False)
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("heat,offset", [(0.01, 8.0), (0.01, 100.0), (1e-3, 20.0), (1e-4, -3.0), (1.0, 3e4)])
+def test_draws_at_large_scaled_logits(heat, offset, drafts):
+    for seed in range(3):
+        held(heated(heat, offset, drafts, N=60, seed=seed))
+    c = heated(heat, offset, drafts, N=7, V=9001, dtype="bf16", seed=9)   # steps of z: many equal logits
+    held(c)
+
+
+@pytest.mark.parametrize("heat", [1.2e-38, 1e-36, 1e-30, 1e-10])
+def test_draws_at_tiny_temperatures(heat):
+    # shares are even among a row's equal maxima, and the race decides: the least noise of them
+    c = Case(N=6, B=4, V=500, dtype="f32", drafts=False, seed=2)
+    c.temperature = np.full(6, heat, np.float32)
+    c.target[:] = 5
+    c.target[:, :, 100:110] = 20
+    c.blk[:, 1:] = 7
+    tokens, counts, _ = c.run()
+    assert c.error == xp.XP_OK
+    best = 100 + c.noise[:, 100:110].argmin(1)
+    assert (counts == 1).all() and np.array_equal(tokens[:, 0], best)
+    assert np.array_equal(tokens, c.want()[0])
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+@pytest.mark.parametrize("heat,offset", [(1.0, 10.0), (0.01, 100.0), (1e-3, 30.0), (1.0, 3e4)])
+def test_draws_between_nearly_equal_ratios(heat, offset, drafts):
+    # noise in proportion to the weights: all ratios lie within 2%, the best one 1e-3 above the others.
+    # A bound that is not one, or a share rounded at its scaled logit's size, loses it.  Weights below
+    # half of p, whose difference magnifies its roundings, stay out of the race.
+    N, V = 40, 4000
+    c = heated(heat, offset, drafts, N=N, B=2, V=V, seed=4)
+    g = np.random.default_rng(5)
+    c.u[:] = np.float32(1 - 2 ** -24)
+    target = c.target.float().cpu().numpy().astype(np.float64)
+    best = np.zeros(N, np.int64)
+    for n in range(N):
+        p = S.softmax(target[n, 0], heat)
+        q = S.softmax(c.draft[n], heat) if drafts else np.zeros(V)
+        c.blk[n, 1] = np.argmax(q - p) if drafts else np.argmin(p)       # a draft that is refused
+        q = q if drafts else (np.arange(V) == c.blk[n, 1]).astype(float)
+        w = np.maximum(p - q, 0)
+        best[n] = g.choice(np.nonzero((w > 0.5 * p) & (p > 1e-6))[0])
+        spread = g.uniform(0.0, 0.02, V)
+        spread[best[n]] = -1e-3
+        c.noise[n] = np.where((w > 0.5 * p) & (w > 1e-30), w * np.exp(spread), 1e3).astype(np.float32)
+    tokens, counts, _ = c.run()
+    assert c.error == xp.XP_OK
+    assert (counts == 1).all() and np.array_equal(tokens[:, 0], best)
