@@ -344,8 +344,8 @@ const char* xp_readout_kernel_name(const xp_head* head);
  * counts (out): device [N] int32, tokens emitted (accepted + 1).  prob (out): device
  * [N, B-1] fp32 = min(1, p_b(x_b) / q_b(x_b)) for the slots tested, 0 behind them, or NULL.
  * Logits are read as: NaN like -inf (never drawn), +inf like the largest finite value.  A
- * target row with nothing above -inf accepts nothing, and a block that ends there gets
- * token -1 (XP_EEMPTY).  A drafted id outside [0, V) is rejected (XP_EBADTOKEN).
+ * target row with nothing above -inf accepts nothing, and a block that ends there, or whose
+ * race no id wins (noise that is NaN or infinite), gets token -1 (XP_EEMPTY).  A drafted id outside [0, V) is rejected (XP_EBADTOKEN).
  * Rows behind a block's first rejection cannot change the result and are mostly not read.
  * B, V, dtype: what the buffers were made for; XP_EINVAL unless they are the head's.
  * ws: xp_verify_workspace_bytes, zeroed once with xp_workspace_init; calls that overlap on

@@ -720,7 +720,8 @@ __global__ void __launch_bounds__(kThreads, 5) verify_draw_kernel(const xp_verif
       r.x = -1;
       best = race<T, false>(r, t_row, nullptr, e_row, 0, a.V, &s_best);
     }
-    last = packed_idx(best);
+    if (best) last = packed_idx(best);
+    else if (threadIdx.x == 0) atomicOr(a.err, XP_ERR_EMPTY);   // noise that lets no id win
   }
   __syncthreads();   // read by everyone before thread 0 clears
   for (int b = threadIdx.x; b < a.B; b += kThreads) {

@@ -5,6 +5,7 @@ import torch
 
 from jacobi_speculative_decode_gb300 import xp
 from oracle import step_oracle as S
+from test_gpu_verify import Case
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +105,21 @@ def test_fork_between_tables_that_lie_among_each_other():
                              None, refs, children, ints([0] * len(children)), refs.clone())
         assert e.value.code == xp.XP_EINVAL
     assert torch.equal(both, before)
+
+
+@pytest.mark.parametrize("drafts", [True, False])
+def test_noise_that_lets_no_id_win(drafts):
+    # a row of NaN or infinite noise: no token, not an id outside the vocabulary
+    c = Case(N=6, B=4, V=600, seed=3, dtype="f32", drafts=drafts)
+    c.u[:3] = np.float32(1 - 2 ** -24)
+    c.noise[0], c.noise[1], c.noise[4] = np.nan, np.inf, np.nan
+    tokens, counts, _ = c.run()
+    assert c.error == xp.XP_EEMPTY
+    want, want_counts, _, _ = c.want()
+    for n in range(c.N):
+        accepted = want_counts[n] - 1
+        if n in (0, 1, 4):
+            assert counts[n] == accepted and (tokens[n, accepted:] == -1).all()
+            assert np.array_equal(tokens[n, :accepted], want[n, :accepted])
+        else:
+            assert np.array_equal(tokens[n], want[n]) and counts[n] == want_counts[n]
