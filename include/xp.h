@@ -318,6 +318,8 @@ const char* xp_readout_kernel_name(const xp_head* head);
  * After the refinement: the drafted blocks are scored by the target model over a paged
  * cache, verified, and the cache is cut back to what was accepted.  None of these calls has
  * a counterpart on the pages; they are the target's side of the same draft step.
+ * An empty batch (no rows, sequences or children) is XP_OK, and the pointers that belong to it may
+ * be NULL.
  * ------------------------------------------------------------------------------------- */
 
 /* Verification of drafted blocks against the target's probabilities, from given random

@@ -61,7 +61,7 @@ bool on_device(const xp_cache* c) {
 xp_status check_table(const xp_cache* c, const int32_t* table, int64_t ld, const int32_t* lens,
                       int rows, int width) {
   if (!c) return XP_ENOTPREPARED;
-  if (!table || !lens || rows < 0 || width <= 0 || ld < width || !on_device(c) ||
+  if (rows < 0 || (rows > 0 && (!table || !lens)) || width <= 0 || ld < width || !on_device(c) ||
       (int64_t)width * c->d.page_size > INT_MAX)
     return XP_EINVAL;
   return rows > c->d.max_seqs ? XP_ECAPACITY : XP_OK;
@@ -109,10 +109,12 @@ xp_status append(const xp_cache* c, int layer, const void* k, const void* v, int
                  const int32_t* table, int64_t ld_table, int64_t width, const int32_t* lens, int N,
                  int T, cudaStream_t stream) {
   if (!c) return XP_ENOTPREPARED;
-  if (heads != c->d.kv_heads || head_dim != c->d.head_dim || dtype != c->d.dtype || !k || !v || !table || !lens || layer < 0 || layer >= c->d.layers || N < 0 || T <= 0 ||
-      width <= 0 || ld_table < width || (int64_t)N * T * c->d.kv_heads > INT_MAX || !on_device(c))
+  if (heads != c->d.kv_heads || head_dim != c->d.head_dim || dtype != c->d.dtype || layer < 0 ||
+      layer >= c->d.layers || N < 0 || T <= 0 || width <= 0 || ld_table < width ||
+      (int64_t)N * T * c->d.kv_heads > INT_MAX || !on_device(c))
     return XP_EINVAL;
-  if (N == 0) return XP_OK;
+  if (N == 0) return XP_OK;   // an empty batch needs no pointers, here and in the calls below
+  if (!k || !v || !table || !lens) return XP_EINVAL;
   return cuda_status(xp_launch_append(c, layer, k, v, stride_n, stride_t, stride_h, table, ld_table,
                                       width, lens, N, T, stream));
 }
@@ -211,8 +213,8 @@ xp_status xp_cache_resize(const xp_cache* c, const int32_t* table, int64_t ld_ta
                           int32_t* refs_out, cudaStream_t stream) {
   const xp_status st = check_table(c, table, ld_table, lens, N, width);
   if (st != XP_OK) return st;
-  if (!new_lens || !refs || pages != c->d.pages || !table_out || !lens_out || !refs_out ||
-      ld_out < width)
+  if (!refs || pages != c->d.pages || !refs_out || ld_out < width ||
+      (N > 0 && (!new_lens || !table_out || !lens_out)))
     return XP_EINVAL;
   return cuda_status(xp_launch_resize(c, table, ld_table, lens, new_lens, refs, N, width, table_out,
                                       ld_out, lens_out, refs_out, stream));
@@ -225,8 +227,8 @@ xp_status xp_cache_fork(const xp_cache* c, const int32_t* table, int64_t ld_tabl
                         cudaStream_t stream) {
   const xp_status st = check_table(c, table, ld_table, lens, rows, width);
   if (st != XP_OK) return st;
-  if (!parent || !refs || pages != c->d.pages || !child_table || !child_lens || !refs_out ||
-      ld_child < width || M < 0)
+  if (!refs || pages != c->d.pages || !refs_out || ld_child < width || M < 0 ||
+      (M > 0 && (!parent || !child_table || !child_lens)))
     return XP_EINVAL;
   const int shared = table_overlap(table, ld_table, rows, child_table, ld_child, M, width);
   if (shared < 0) return XP_EINVAL;
@@ -241,7 +243,7 @@ xp_status xp_cache_compact(const xp_cache* c, const int32_t* table, int64_t ld_t
                            int32_t* live, cudaStream_t stream) {
   const xp_status st = check_table(c, table, ld_table, lens, N, width);
   if (st != XP_OK) return st;
-  if (!refs || pages != c->d.pages || !table_out || !refs_out || ld_out < width)
+  if (!refs || pages != c->d.pages || (N > 0 && !table_out) || !refs_out || ld_out < width)
     return XP_EINVAL;
   return cuda_status(xp_launch_compact(c, table, ld_table, lens, N, width, refs, table_out, ld_out,
                                        refs_out, map, live, stream));
@@ -256,9 +258,9 @@ xp_status xp_prefix_attention(const xp_cache* c, const xp_attn* a, const void* q
                               int64_t ld_table, int width, const int32_t* lens, void* out, float* lse,
                               void* ws, size_t ws_bytes, cudaStream_t stream) {
   if (!c) return XP_ENOTPREPARED;
-  if (!valid_attn(c, a) || !q || !out || !ws || (uintptr_t)ws % 256 ||
-      !on_device(c))
-    return XP_EINVAL;
+  if (!valid_attn(c, a) || !on_device(c)) return XP_EINVAL;
+  if (a->N == 0) return XP_OK;
+  if (!q || !out || !ws || (uintptr_t)ws % 256) return XP_EINVAL;
   const int ps = c->d.page_size;
   if (a->prefix_len > 0 && (!prefix_table || prefix_pages < (a->prefix_len - 1) / ps + 1))
     return XP_EINVAL;
@@ -267,7 +269,6 @@ xp_status xp_prefix_attention(const xp_cache* c, const xp_attn* a, const void* q
     return XP_EINVAL;
   const xp_attn_plan plan = attn_plan(c, a);
   if (ws_bytes < plan.total) return XP_ECAPACITY;
-  if (a->N == 0) return XP_OK;
   const size_t es = xp_elem(c->d.dtype);
   xp_attn_args g;
   g.a = *a;
@@ -310,14 +311,15 @@ xp_status xp_verify_drafts(const xp_head* h, const void* target, int64_t stride_
                            int64_t ld_noise, int64_t* tokens, int32_t* counts, float* prob,
                            void* ws, size_t ws_bytes, cudaStream_t stream) {
   if (!h) return XP_ENOTPREPARED;
+  if (N < 0 || B != h->B || V != h->V || dtype != h->dtype || !xp_on_head_device(h))
+    return XP_EINVAL;
+  if (N == 0) return XP_OK;
   if (!target || !blk || !u || !noise || !tokens || !counts || !ws || (uintptr_t)ws % 256 ||
-      stride_n < 0 || stride_b < 0 || (draft && ld_draft < h->V) || ld_noise < h->V || N < 0 ||
-      B != h->B || V != h->V || dtype != h->dtype || !xp_on_head_device(h))
+      stride_n < 0 || stride_b < 0 || (draft && ld_draft < h->V) || ld_noise < h->V)
     return XP_EINVAL;
   if (N > h->max_N || N > 65535) return XP_ECAPACITY;
   const xp_verify_ws L = xp_verify_layout(h, N);
   if (ws_bytes < L.total) return XP_ECAPACITY;
-  if (N == 0) return XP_OK;
   char* w = (char*)ws;
   xp_verify_args a;
   a.target = target;

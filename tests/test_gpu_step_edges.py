@@ -5,7 +5,7 @@ import torch
 
 from jacobi_speculative_decode_gb300 import xp
 from oracle import step_oracle as S
-from test_gpu_verify import Case
+from test_gpu_verify import Case, make_head
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +123,47 @@ def test_noise_that_lets_no_id_win(drafts):
             assert np.array_equal(tokens[n, :accepted], want[n, :accepted])
         else:
             assert np.array_equal(tokens[n], want[n]) and counts[n] == want_counts[n]
+
+
+def test_empty_batches():
+    # no rows, sequences or children: nothing to do, and an empty tensor has no address
+    k = torch.randn(1, 6, 4, 2, 64, device="cuda")
+    cache = xp.Cache(k, k.clone())
+    none = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    no = torch.empty(0, dtype=torch.int32, device="cuda")
+    refs = ints([0, 2, 0, 1, 0, 0])
+    new = torch.empty(0, 5, 2, 64, device="cuda")
+    xp.xp_cache_append(cache.handle, 0, new, new, none, no)
+    out = ints([9] * 6)
+    xp.xp_cache_resize(cache.handle, none, no, no, refs, none, no, out)
+    assert torch.equal(out, refs)
+    table, lens = ints([[1, 3, -1], [1, -1, -1]]), ints([6, 4])
+    out.fill_(9)
+    xp.xp_cache_fork(cache.handle, table, lens, no, None, refs, none, no, out)
+    assert torch.equal(out, refs)
+    child, child_lens = ints([[7, 7, 7]]), ints([7])
+    xp.xp_cache_fork(cache.handle, none, no, ints([0]), None, refs, child, child_lens, out)
+    assert xp.xp_cache_get_error(cache.handle) == xp.XP_ELENGTH         # there is no row 0
+    assert child.tolist() == [[-1, -1, -1]] and child_lens.tolist() == [0] and torch.equal(out, refs)
+    # packing without tables moves what refs hold
+    want = k.clone()
+    want[:, 0] = want[:, 3]
+    new_id = ints([9] * 6)
+    xp.xp_cache_compact(cache.handle, none, no, refs, none, out, new_id)
+    assert xp.xp_cache_get_error(cache.handle) == xp.XP_OK
+    assert out.tolist() == [1, 2, 0, 0, 0, 0] and new_id.tolist() == [-1, 1, -1, 0, -1, -1]
+    assert torch.equal(k, want)
+    q = torch.empty(0, 5, 4, 64, device="cuda")
+    for prefix_len in (0, 8):
+        a = xp.make_attn(q, q, 0, prefix_len, 12, 0.1)
+        xp.xp_prefix_attention(cache.handle, a, q, ints([1, 3]), none, no, q, None,
+                               cache.attention_workspace(a))
+    c = Case(N=2, B=4, V=64, seed=1)
+    head = make_head(64, 4, 2, "bf16")
+    xp.xp_verify_drafts(head.handle, c.target[:0], torch.empty(0, 64, device="cuda"),
+                        torch.empty(0, 4, dtype=torch.int64, device="cuda"), no,
+                        torch.empty(0, device="cuda"), torch.empty(0, 3, device="cuda"),
+                        torch.empty(0, 64, device="cuda"),
+                        torch.empty(0, 4, dtype=torch.int64, device="cuda"), no,
+                        torch.empty(0, 3, device="cuda"), head.verify_workspace(0))
+    assert xp.xp_get_error(head.handle) == xp.XP_OK and xp.xp_cache_get_error(cache.handle) == xp.XP_OK
