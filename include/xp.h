@@ -413,9 +413,9 @@ xp_status xp_cache_append_columns(const xp_cache* cache, int layer, const void* 
 /* The table calls below change page tables, lengths and reference counts (and, where they
  * say so, move pages of K and V in every layer).  Each output may be the matching input
  * itself.  Page ids of a table behind ceil(length / page_size) are not read and are written
- * as -1.  `width`: columns of the tables; `pages`: entries of refs, refs_out and map, XP_EINVAL
- * unless the pool's.  They share the handle's scratch: calls on one
- * cache must not overlap on the GPU. */
+ * as -1.  `width`: columns of the tables (width*page_size, and resize's N*width, below 2^31);
+ * `pages`: entries of refs, refs_out and map, XP_EINVAL unless the pool's.  They share the
+ * handle's scratch: calls on one cache must not overlap on the GPU. */
 
 /* Copy whole pages src[i] -> dst[i] (device int32, `count` of them), K and V, every layer.
  * A negative id skips the pair; no page may be the target of one pair and in another. */

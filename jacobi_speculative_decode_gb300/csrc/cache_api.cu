@@ -14,6 +14,11 @@ namespace {
 inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 inline xp_status cuda_status(cudaError_t e) { return e == cudaSuccess ? XP_OK : XP_ECUDA; }
 
+// a b c < 2^31, whatever they are (none negative)
+bool fits(int a, int b, int c) {
+  return (int64_t)a * b <= INT_MAX && (int64_t)a * b * c <= INT_MAX;
+}
+
 // heads outside the tokens of a page, tokens outside the heads, or neither (-1)
 int page_order(const xp_cache_desc* d) {
   const int64_t D = d->head_dim, H = d->kv_heads, ps = d->page_size;
@@ -27,8 +32,8 @@ bool valid_desc(const xp_cache_desc* d) {
       d->head_dim <= 0 || d->head_dim > 256 || d->max_seqs <= 0)
     return false;
   if (d->dtype != XP_BF16 && d->dtype != XP_F32) return false;
+  if (!fits(d->page_size, d->kv_heads, d->head_dim) || page_order(d) < 0) return false;
   const int64_t block = (int64_t)d->page_size * d->kv_heads * d->head_dim;
-  if (block > INT_MAX || page_order(d) < 0) return false;
   return d->stride_page >= block && d->stride_layer >= 0;
 }
 
@@ -71,7 +76,7 @@ bool valid_attn(const xp_cache* c, const xp_attn* a) {
   return a && a->layer >= 0 && a->layer < c->d.layers && a->N >= 0 && a->T > 0 && a->heads > 0 &&
          a->head_dim == c->d.head_dim && a->dtype == c->d.dtype &&
          a->scale > 0.0f && a->scale <= FLT_MAX && a->heads % c->d.kv_heads == 0 && a->prefix_len >= 0 && a->max_len >= 0 &&
-         (int64_t)a->N * a->T * a->heads <= INT_MAX &&
+         fits(a->N, a->T, a->heads) &&
          (int64_t)a->prefix_len + a->max_len <= INT_MAX - 1024;
 }
 
@@ -111,7 +116,7 @@ xp_status append(const xp_cache* c, int layer, const void* k, const void* v, int
   if (!c) return XP_ENOTPREPARED;
   if (heads != c->d.kv_heads || head_dim != c->d.head_dim || dtype != c->d.dtype || layer < 0 ||
       layer >= c->d.layers || N < 0 || T <= 0 || width <= 0 || ld_table < width ||
-      (int64_t)N * T * c->d.kv_heads > INT_MAX || !on_device(c))
+      !fits(N, T, c->d.kv_heads) || !on_device(c))
     return XP_EINVAL;
   if (N == 0) return XP_OK;   // an empty batch needs no pointers, here and in the calls below
   if (!k || !v || !table || !lens) return XP_EINVAL;
@@ -213,7 +218,7 @@ xp_status xp_cache_resize(const xp_cache* c, const int32_t* table, int64_t ld_ta
                           int32_t* refs_out, cudaStream_t stream) {
   const xp_status st = check_table(c, table, ld_table, lens, N, width);
   if (st != XP_OK) return st;
-  if (!refs || pages != c->d.pages || !refs_out || ld_out < width ||
+  if (!refs || pages != c->d.pages || !refs_out || ld_out < width || !fits(N, width, 1) ||
       (N > 0 && (!new_lens || !table_out || !lens_out)))
     return XP_EINVAL;
   return cuda_status(xp_launch_resize(c, table, ld_table, lens, new_lens, refs, N, width, table_out,

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, RM <= 2 ? 2 : 1) attn_simt_kernel(co
     }
   }
   const int step = prefix ? pl.prefix_keys : pl.tail_keys;
-  const int k0 = split * step, k1 = min(keys, k0 + step);
+  const int k0 = split * step, k1 = k0 + min(step, keys - k0);   // none where keys < k0
 
   for (int i = tid; i < BM; i += kThreads) {
     Row r;
@@ -357,7 +357,7 @@ xp_attn_plan xp_attn_simt_plan(const xp_cache* c, const xp_attn* a) {
   auto splits = [&](int keys, int* range) {
     const int64_t r = std::min<int64_t>(steps * kKeys, ((int64_t)keys + kKeys - 1) / kKeys * kKeys);
     *range = (int)std::max<int64_t>(kKeys, r);
-    return keys > 0 ? (keys + *range - 1) / *range : 0;
+    return keys > 0 ? (keys - 1) / *range + 1 : 0;
   };
   p.prefix_tiles = (int)(((int64_t)a->N * per_seq + p.rows_tile - 1) / p.rows_tile);
   p.tail_tiles = (per_seq + p.rows_tile - 1) / p.rows_tile;

@@ -27,7 +27,7 @@ struct Scan {
 
 __device__ __forceinline__ void flag(uint32_t* err, uint32_t bit) { atomicOr(err, bit); }
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
 // Exclusive prefix of v over the CTA's threads; *sum gets the CTA's total.  Two barriers.
 __device__ __forceinline__ int block_scan(int v, Scan& s, int* sum) {

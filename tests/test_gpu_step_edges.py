@@ -167,3 +167,19 @@ def test_empty_batches():
                         torch.empty(0, 4, dtype=torch.int64, device="cuda"), no,
                         torch.empty(0, 3, device="cuda"), head.verify_workspace(0))
     assert xp.xp_get_error(head.handle) == xp.XP_OK and xp.xp_cache_get_error(cache.handle) == xp.XP_OK
+
+
+def test_sizes_whose_products_pass_32_and_64_bits():
+    # host arithmetic only: what is refused and what a plan asks for
+    k = torch.zeros(1, 2, 4, 1, 4, device="cuda")
+    cache = xp.Cache(k, k.clone())
+
+    def bytes_of(N, T, heads, prefix_len, max_len=0):
+        a = xp.xp_attn(0, N, T, heads, 4, xp.XP_F32, prefix_len, max_len, 1.0, 4, 4, 4, 4, 4, 4)
+        return xp.xp_attention_workspace_bytes(cache.handle, a)
+
+    assert bytes_of(1 << 22, 1 << 22, 1 << 22, 4) == 0             # 2^66 rows
+    assert bytes_of(1 << 30, 4, 1, 4) == 0                         # 2^32
+    # one range over 2^31 - 2000 keys: a partial result a row
+    assert bytes_of(20000, 1, 1, (1 << 31) - 2000) == 20000 * 8 + 20000 * 16
+    assert bytes_of(20000, 1, 1, 0, (1 << 31) - 2000) == 20000 * 8 + 20000 * 16

@@ -76,3 +76,9 @@ def test_page_orders(lib):
 def test_new_status_strings(lib):
     for code in range(9, 14):
         assert xp.status_str(code) != "unknown status" and code in xp.STATUS
+
+
+def test_pages_whose_size_passes_64_bits_are_refused(lib):
+    huge = dict(page_size=1 << 30, kv_heads=1 << 30, head_dim=16, stride_token=1 << 34, stride_head=16)
+    assert xp.xp_cache_prep_bytes(desc(**huge)) == 0          # 2^64 elements
+    assert xp.xp_cache_prep_bytes(desc(page_size=1 << 21, stride_page=1 << 40)) == 0          # 2^31
