@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const xp_attn_args g)
   for (int p0 = 0; p0 < parts; p0 += 32) {   // a lane a range's weight, then all ranges' results
     float2 st = make_float2(0.0f, 0.0f);
     if (p0 + lane < parts) st = *(const float2*)&g.stat[((p0 + lane) * rows + row) * 2];
-    const float mine = st.y != 0.0f ? exp2f(st.x - m) : 0.0f;   // 0: no key of this range
+    // 0: no key of this range.  A weight that underflows is the least number instead, so that an
+    // infinite or NaN result still shows.
+    const float mine = st.y != 0.0f ? fmaxf(exp2f(st.x - m), 1.4e-45f) : 0.0f;
     l += mine * st.y;
     const int n = min(32, parts - p0);
 #pragma unroll 4

@@ -183,3 +183,28 @@ def test_sizes_whose_products_pass_32_and_64_bits():
     # one range over 2^31 - 2000 keys: a partial result a row
     assert bytes_of(20000, 1, 1, (1 << 31) - 2000) == 20000 * 8 + 20000 * 16
     assert bytes_of(20000, 1, 1, 0, (1 << 31) - 2000) == 20000 * 8 + 20000 * 16
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_infinite_value_shows_where_its_weight_underflows(dtype):
+    # the first 128 keys score 400 below the others, a whole range of them: their weights are 0 in 32
+    # bits, but a row that sees an infinite or NaN value does not come out finite there
+    D, n = 64, 600
+    k, v = (torch.randn(1, 40, 16, 1, D, device="cuda").to(xp.torch_dtype(dtype)) for _ in range(2))
+    q = torch.zeros(2, 1, 1, D, device="cuda", dtype=k.dtype)
+    q[..., 0] = 1
+    k[:, :8, :, :, 0], k[:, 8:, :, :, 0] = -200, 200
+    v[0, 0, 3, 0, 5], v[0, 7, 15, 0, 9], v[0, 2, 0, 0, 63] = torch.inf, torch.nan, -torch.inf
+    cache = xp.Cache(k, v)
+    table = torch.arange(40, dtype=torch.int32, device="cuda").repeat(2, 1)
+    out = torch.empty_like(q)
+    for prefix_len, lens in ((0, [n, 0]), (n, [0, 0])):
+        a = xp.make_attn(q, out, 0, prefix_len, max(lens), 1.0)
+        xp.xp_prefix_attention(cache.handle, a, q, table[0], table, ints(lens), out, None,
+                               cache.attention_workspace(a))
+        odd = torch.zeros(D, dtype=torch.bool, device="cuda")
+        odd[[5, 9, 63]] = True
+        assert torch.equal(~out[0, 0, 0].isfinite(), odd)
+        if prefix_len:
+            assert torch.equal(~out[1, 0, 0].isfinite(), odd)
+    assert xp.xp_cache_get_error(cache.handle) == xp.XP_OK
