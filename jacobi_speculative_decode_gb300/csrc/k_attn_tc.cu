@@ -823,8 +823,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // A row's tail from the definition, joined to what its prefix left (maximum *m in base 2, sum *l,
 // weighted values o of this thread's dims).  Hidden keys weigh nothing on the tensor cores, but nothing
-// times an infinite or NaN value is NaN; a row with a NaN in its result comes here, where
-// hidden values are not read.  A thread a row: slow, and for such inputs only.
+// times an infinite or NaN value is NaN; a row with a NaN in its result that its prefix alone does
+// not have comes here, where hidden values are not read.  A thread a row: slow, and for such
+// inputs only.
 template <int D>
 __device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, int t, int h, int warp,
                                         float* m, float* l, float4* o) {
@@ -941,22 +942,35 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
     join(0);
     if (g.a.max_len > 0) {
       join(1);
+      auto nans = [&]() {   // of this thread's dims, a bit each
+        unsigned bits = 0;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c)
+          bits |= (o[c].x != o[c].x ? 1u : 0u) << 4 * c | (o[c].y != o[c].y ? 2u : 0u) << 4 * c |
+                  (o[c].z != o[c].z ? 4u : 0u) << 4 * c | (o[c].w != o[c].w ? 8u : 0u) << 4 * c;
+        return bits;
+      };
       float all = 0.0f;
 #pragma unroll
       for (int c = 0; c < kPer; ++c) all += o[c].x + o[c].y + o[c].z + o[c].w;
       if (all != all && l == l && g.a.T > 1) {
+        const unsigned whole = nans();
         m = -INFINITY, l = 0.0f;
 #pragma unroll
         for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         join(0);
-        float m2 = m, l2 = l;
-        float4 o2[kPer];
+        if (whole & ~nans()) {   // the tail's doing
+          float m2 = m, l2 = l;
+          float4 o2[kPer];
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) o2[c] = o[c];
-        tail_again<D>(g, n, hk, t, h, warp, &m2, &l2, o2);
-        m = m2, l = l2;
+          for (int c = 0; c < kPer; ++c) o2[c] = o[c];
+          tail_again<D>(g, n, hk, t, h, warp, &m2, &l2, o2);
+          m = m2, l = l2;
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) o[c] = o2[c];
+          for (int c = 0; c < kPer; ++c) o[c] = o2[c];
+        } else {   // the prefix has them too, and every row sees that
+          join(1);
+        }
       }
     }
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // NaN where a visible score is

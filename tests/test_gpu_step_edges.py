@@ -5,6 +5,7 @@ import torch
 
 from jacobi_speculative_decode_gb300 import xp
 from oracle import step_oracle as S
+from test_gpu_attention import Case as Attention
 from test_gpu_verify import Case, make_head
 
 pytestmark = pytest.mark.gpu
@@ -208,3 +209,26 @@ def test_an_infinite_value_shows_where_its_weight_underflows(dtype):
         if prefix_len:
             assert torch.equal(~out[1, 0, 0].isfinite(), odd)
     assert xp.xp_cache_get_error(cache.handle) == xp.XP_OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_nan_of_the_prefix_leaves_the_rest_of_a_row_as_it_was(D):
+    # every row sees it: its dim is NaN, and nothing is summed anew for the others (another way of
+    # summing, a thread a row, would show in their last bits, and in a call of many rows take seconds)
+    c = Attention([40, 300, 7, 130, 0], T=5, H=2, G=4, D=D, P=200, seed=6)
+    out, lse = c.run()
+    page, row = int(c.prefix_table[9]), 3
+    c.v[0, page, row, 1, 6] = torch.nan
+    c.v[0, page, row, 1, D - 1] = torch.inf
+    got, got_lse = c.run()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[:, :, 4:, [6, D - 1]] = True
+    assert torch.equal(got.isnan(), hit & (torch.arange(D, device="cuda") == 6))
+    assert (got[:, :, 4:, D - 1] == torch.inf).all()
+    assert torch.equal(got[~hit], out[~hit]) and torch.equal(got_lse, lse)
+    # a hidden value on top of it still reaches only the rows that see it
+    c.v[0, int(c.table[1, 299 // 16]), 299 % 16, 1, 7] = torch.nan
+    again, _ = c.run()
+    hit[1, 4, 4:, 7] = True
+    assert torch.equal(again.isnan(), hit & (torch.arange(D, device="cuda") != D - 1))
+    assert xp.xp_cache_get_error(c.cache.handle) == xp.XP_OK
