@@ -143,6 +143,12 @@ xp_status xp_cache_create(const xp_cache_desc* d, void* prep_dev, size_t prep_by
   if (!c) return XP_ECAPACITY;
   c->d = *d;
   c->heads_outside = page_order(d) == 1;
+  // What one head, token, page or layer has for a stride is never used: set to the dense one, so that
+  // an odd value does not keep the pools from 16-byte accesses and TMA.
+  if (d->kv_heads == 1) c->d.stride_head = d->head_dim;
+  if (d->page_size == 1) c->d.stride_token = (int64_t)d->kv_heads * d->head_dim;
+  if (d->pages == 1) c->d.stride_page = (int64_t)d->page_size * d->kv_heads * d->head_dim;
+  if (d->layers == 1) c->d.stride_layer = c->d.stride_page * d->pages;
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device) !=
           cudaSuccess) {

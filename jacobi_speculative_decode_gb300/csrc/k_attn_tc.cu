@@ -1008,17 +1008,20 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // Queries by TMA where a tile is a whole number of tokens, one stride apart; else by loads.
   CUtensorMap tm_q = {};
-  const int64_t token = g.a.T > 1 ? g.a.q_stride_t : g.a.q_stride_n;
+  // strides that are never used (one sequence, token or head) do not count
+  const int64_t sh = g.a.heads > 1 ? g.a.q_stride_h : D;
+  const int64_t token = g.a.T > 1   ? g.a.q_stride_t
+                        : g.a.N > 1 ? g.a.q_stride_n
+                                    : (int64_t)g.a.heads * D;
   const bool q_wide = (uintptr_t)g.q % 16 == 0 &&
-                      (g.a.q_stride_n | g.a.q_stride_t | g.a.q_stride_h) % 8 == 0;
+                      ((g.a.N > 1 ? g.a.q_stride_n : 0) | (g.a.T > 1 ? g.a.q_stride_t : 0) | sh) % 8 == 0;
   bool q_tma = q_wide && g.group <= kRows &&
-               (g.a.T == 1 || g.a.N == 1 || g.a.q_stride_n == g.a.T * token) && token > 0 &&
-               g.a.q_stride_h > 0;
+               (g.a.T == 1 || g.a.N == 1 || g.a.q_stride_n == g.a.T * token) && token > 0 && sh > 0;
   if (q_tma) {
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)g.group, (cuuint64_t)g.kv_heads,
                                 (cuuint64_t)g.a.N * g.a.T};
-    const cuuint64_t strides[3] = {(cuuint64_t)g.a.q_stride_h * 2,
-                                   (cuuint64_t)g.a.q_stride_h * 2 * g.group, (cuuint64_t)token * 2};
+    const cuuint64_t strides[3] = {(cuuint64_t)sh * 2, (cuuint64_t)sh * 2 * g.group,
+                                   (cuuint64_t)token * 2};
     const cuuint32_t boxes[4] = {64, (cuuint32_t)g.group, 1, (cuuint32_t)(g.plan.rows_tile / g.group)};
     const cuuint32_t es[4] = {1, 1, 1, 1};
     q_tma = xp_get_encode_tiled()(&tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void*)g.q, dims, strides,

@@ -536,6 +536,9 @@ cudaError_t xp_launch_append(const xp_cache* c, int layer, const void* k, const 
   const xp_cache_desc& d = c->d;
   const size_t es = xp_elem(d.dtype);
   char *kp = (char*)d.k + layer * d.stride_layer * es, *vp = (char*)d.v + layer * d.stride_layer * es;
+  if (N == 1) sn = 0;   // strides that are never used
+  if (T == 1) st = 0;
+  if (d.kv_heads == 1) sh = 0;
   const int64_t strides = sn | st | sh | d.stride_page | d.stride_token | d.stride_head | d.head_dim;
   const bool wide = (((uintptr_t)k | (uintptr_t)v | (uintptr_t)kp | (uintptr_t)vp) & 15) == 0 &&
                     strides * (int64_t)es % 16 == 0;

@@ -232,3 +232,36 @@ def test_a_nan_of_the_prefix_leaves_the_rest_of_a_row_as_it_was(D):
     hit[1, 4, 4:, 7] = True
     assert torch.equal(again.isnan(), hit & (torch.arange(D, device="cuda") != D - 1))
     assert xp.xp_cache_get_error(c.cache.handle) == xp.XP_OK
+
+
+@pytest.mark.parametrize("page", [16, 1])
+def test_strides_that_are_never_used_do_not_count(page):
+    # one layer, head, page or token may come with any stride (a view's): the same form of every call
+    # runs, to the bit, as the workspace that it asks for tells
+    D, n, pages = 128, 48, 48 // page
+    k, v = (torch.randn(1, pages, page, 1, D, device="cuda").bfloat16() for _ in range(2))
+    odd = [t.as_strided(t.shape, (0, page * D, 7 if page == 1 else D, 5, 1)) for t in (k, v)]
+    assert odd[0].stride() != k.stride() and torch.equal(odd[0], k)
+    q = torch.randn(1, 1, 1, D, device="cuda").bfloat16()
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    got = []
+    for (a, b), x in (((k, v), q), (odd, q.as_strided(q.shape, (3, 1, 9, 1)))):
+        cache = xp.Cache(a, b)
+        out = torch.empty_like(q)
+        attn = xp.make_attn(x, out, 0, 0, n, 0.1)
+        ws = cache.attention_workspace(attn)
+        xp.xp_prefix_attention(cache.handle, attn, x, None, table, ints([n]), out, None, ws)
+        xp.xp_cache_append(cache.handle, 0, x, x, table, ints([n - 1]))
+        if page == 16:
+            xp.xp_cache_copy(cache.handle, ints([0]), ints([1]))
+        assert xp.xp_cache_get_error(cache.handle) == xp.XP_OK
+        got.append((ws.numel(), out, k.clone(), v.clone()))
+        assert out.isfinite().all() and torch.equal(k[0, (n - 2) // page, (n - 2) % page], q[0, 0])
+        k[0, (n - 2) // page, (n - 2) % page], v[0, (n - 2) // page, (n - 2) % page] = 0.5, 0.25
+    assert got[0][0] == got[1][0]
+    one_page = torch.randn(3, 1, 16, 2, 64, device="cuda").bfloat16()
+    view = one_page.as_strided(one_page.shape, (2048, 2049, 128, 64, 1))
+    a = xp.make_attn(torch.empty(1, 1, 2, 64, device="cuda").bfloat16(),
+                     torch.empty(1, 1, 2, 64, device="cuda").bfloat16(), 2, 0, 16, 0.1)
+    sizes = [xp.Cache(t, t).attention_workspace(a).numel() for t in (one_page, view)]
+    assert sizes[0] == sizes[1]
