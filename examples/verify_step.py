@@ -4,6 +4,8 @@ A small random target model (embedding, one attention layer over the cache, unem
 N requests that share a prompt.  Every step
 
   1. the refinement drafts a block per request            xp_jacobi_refine
+     (or tokens are drawn from its logits, which the
+     verification then needs)                             xp_latent_pass, xp_refine_logits
   2. the cache takes pages for the block                  xp_cache_resize
   3. the block's keys and values go in                    xp_cache_append
   4. the target attends for all B slots at once,
@@ -78,12 +80,31 @@ class Drafter:
         h = torch.zeros(N, B, self.hidden, dtype=self.target.dtype, device="cuda")
         xp.xp_jacobi_refine(self.head.handle, base, (B - 1) * V, V, h, anchor, before, N, passes, 0,
                             self.blk, self.ws)
+        self.base, self.h = base, h
         return self.blk
+
+    def sample(self, anchor, before, heat, generator, passes=2):
+        """Blocks whose drafts are drawn from the refinement's distribution at temperatures `heat` [N]
+        (their argmax at 0), and the logits [N*(B-1), V] of that distribution."""
+        N, B, V, r = anchor.numel(), self.B, self.target.vocab, self.head.r
+        blk = self.draft(anchor, before, passes)
+        xh = torch.empty(N, B, r, device="cuda")
+        xp.xp_hidden_cache(self.head.handle, self.h, N, xh, self.ws)
+        lat = torch.empty(N, B - 1, r, dtype=self.target.dtype, device="cuda")
+        xp.xp_latent_pass(self.head.handle, blk, before, xh, N, lat)
+        logits = torch.empty(N * (B - 1), V, device="cuda")
+        xp.xp_refine_logits(self.head.handle, lat, self.base, (B - 1) * V, V, N, logits, V)
+        race = torch.empty(N, B - 1, V).exponential_(generator=generator).clamp_(min=1e-20).cuda()
+        hot = torch.where(heat > 0, heat, 1.0)[:, None, None]
+        drawn = logits.view(N, B - 1, V) / hot - torch.log(race) * (heat > 0)[:, None, None]
+        blk[:, 1:] = drawn.argmax(-1)
+        return blk, logits
 
 
 def run(requests=5, block=6, steps=6, prompt_len=75, page=16, temperature=0.0, dtype=torch.float32,
-        seed=0):
-    """Decode `requests` continuations of one prompt.  Returns (target, prompt, first tokens, tokens
+        seed=0, sampled=False):
+    """Decode `requests` continuations of one prompt, from greedy drafts or (sampled) from drafts drawn
+    from the refinement's logits.  Returns (target, prompt, first tokens, tokens
     emitted by each request, drafts accepted, drafts made)."""
     target = Target(dtype=dtype, seed=seed)
     drafter = Drafter(target, block, requests)
@@ -116,7 +137,8 @@ def run(requests=5, block=6, steps=6, prompt_len=75, page=16, temperature=0.0, d
     emitted, accepted = [[] for _ in range(N)], 0
     tails, lengths = table[1:], lens[1:]
     for _ in range(steps):
-        blk = drafter.draft(anchor, before)
+        blk, draft = drafter.sample(anchor, before, heat, g) if sampled \
+            else (drafter.draft(anchor, before), None)
         kept = lens.clone()
         want = kept + B
         want[0] = prompt_len
@@ -129,7 +151,7 @@ def run(requests=5, block=6, steps=6, prompt_len=75, page=16, temperature=0.0, d
         logits = target.logits(x, out)
         u = torch.rand(N, B - 1, generator=g).cuda()
         noise = torch.empty(N, V).exponential_(generator=g).clamp_(min=1e-20).cuda()
-        xp.xp_verify_drafts(drafter.head.handle, logits, None, blk, None, heat, u, noise, tokens, counts,
+        xp.xp_verify_drafts(drafter.head.handle, logits, draft, blk, None, heat, u, noise, tokens, counts,
                             None, drafter.verify_ws)
         # the anchor and the accepted drafts stay: as many tokens as were emitted
         keep = kept.clone()
@@ -160,10 +182,11 @@ def run(requests=5, block=6, steps=6, prompt_len=75, page=16, temperature=0.0, d
 
 
 def main():
-    _, _, _, emitted, accepted, made = run(temperature=0.8, dtype=torch.bfloat16)
-    print("drafts accepted: %d of %d" % (accepted, made))
-    for n, row in enumerate(emitted):
-        print("request %d: %s" % (n, row))
+    for sampled in (False, True):
+        _, _, _, emitted, accepted, made = run(temperature=0.8, dtype=torch.bfloat16, sampled=sampled)
+        print("%s drafts accepted: %d of %d" % ("sampled" if sampled else "greedy", accepted, made))
+        for n, row in enumerate(emitted):
+            print("request %d: %s" % (n, row))
 
 
 if __name__ == "__main__":

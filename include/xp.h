@@ -334,7 +334,11 @@ const char* xp_readout_kernel_name(const xp_head* head);
  * exponential; equal ratios go to the lowest id.  (Where rounding leaves no positive
  * residual, p_a itself is drawn from.)  t[n] = 0 makes block n greedy: p_b is one-hot at the
  * lowest argmax, a draft is accepted when it is that id, and no noise is read.
- * The emitted tokens then follow the target's own distribution, whatever the draft's.
+ * The emitted tokens then follow the target's own distribution, whatever the draft's, provided that
+ * each x_b was drawn from q_b.  So the refinement's own blocks, which are argmaxes, go with
+ * draft == NULL; draft logits go with tokens drawn from their softmax at the block's temperature.  An
+ * argmax given with the logits it was taken from, proposed with certainty but tested as if with
+ * probability q, would be refused too often: the tokens emitted would not follow the target.
  *
  * target: device [N, B, V] head dtype, row (n, b) at target + n*stride_n + b*stride_b, unit
  * stride over v.  draft: device fp32, row n*(B-1) + b at draft + (n*(B-1) + b)*ld_draft (the

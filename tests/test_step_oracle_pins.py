@@ -87,3 +87,21 @@ def test_temperatures_scale_differences():
         tok, count, prob, _ = S.verify(t, None, np.array([[0, 0]]), None, np.array([heat]),
                                        np.array([[0.0]]), e)
         assert tok.tolist() == [[token, -1]] and count[0] == 1 and prob[0, 0] == 0
+
+
+def test_an_argmax_offered_with_its_logits_is_biased():
+    # the condition of the law above: x has to be drawn from q.  q's argmax, which is certain, follows
+    # the target when it is taken as one-hot and not when it is given with q
+    rng = np.random.default_rng(4)
+    V, trials = 4, 3000
+    target, draft = np.log([[[0.4, 0.3, 0.2, 0.1], [1, 1, 1, 1]]]), np.log([[0.7, 0.1, 0.1, 0.1]])
+    p = S.softmax(target[0, 0])
+    off = []
+    for given in (None, draft):
+        seen = np.zeros(V)
+        for _ in range(trials):
+            tok, _, _, _ = S.verify(target, given, np.array([[0, 0]]), None, None, rng.random((1, 1)),
+                                    rng.exponential(size=(1, V)))
+            seen[tok[0, 0]] += 1
+        off.append(np.abs(seen / trials - p) / np.sqrt(p * (1 - p) / trials))
+    assert off[0].max() < 5 and off[1].max() > 15
