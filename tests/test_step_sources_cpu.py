@@ -53,3 +53,12 @@ def test_one_lane_reads_what_a_whole_warp_decides_by():
         uses = [m for m in re.finditer(r"\b%s\b(?!\s*=[^=])" % name, b)]
         shuffled = re.findall(r"__shfl_sync\(0xFFFFFFFFu, %s, 0\)" % name, b)
         assert len(uses) == len(shuffled) == 1, name
+
+
+def test_every_device_helper_is_called():
+    text = {name: source(name) for name in sorted(os.listdir(CSRC))}
+    everything = "".join(text.values())
+    idle = [(name, f) for name, t in text.items()
+            for f in re.findall(r"__device__ (?:__forceinline__|__noinline__|inline) [\w:<> *&]+?\b(\w+)\(", t)
+            if len(re.findall(r"\b%s\b" % f, everything)) < 2]
+    assert not idle
