@@ -146,8 +146,10 @@ def _stream(stream):
         import torch
         if not torch.cuda.is_initialized() and not torch.cuda.is_available():
             raise RuntimeError("no CUDA device: libxp has no CPU path")
-        # the current stream's handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the current stream's handle, without a Stream object around it where torch gives it so (not a
+        # public call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -116,3 +116,19 @@ def test_lse_is_fp32(calls):
     with pytest.raises(ValueError, match="lse"):
         xp.xp_prefix_attention(1, stream=0, **{**args, "lse": i32(2, 3, 4)})
     assert not calls
+
+
+@pytest.mark.parametrize("has_raw", [True, False])
+def test_the_current_stream_with_and_without_the_private_call(monkeypatch, has_raw):
+    class Stream:
+        cuda_stream = 1234
+
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    if has_raw:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 77 + device, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert xp._stream(None) == (80 if has_raw else 1234)
+    assert xp._stream(5) == 5 and xp._stream(Stream) == 1234
