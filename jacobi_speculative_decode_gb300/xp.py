@@ -141,15 +141,17 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """The handle of a stream, or of the current one (on `device`, where the caller has looked it up)."""
     if stream is None:
         import torch
-        if not torch.cuda.is_initialized() and not torch.cuda.is_available():
-            raise RuntimeError("no CUDA device: libxp has no CPU path")
-        # the current stream's handle, without a Stream object around it where torch gives it so (not a
-        # public call)
+        if device is None:
+            if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+                raise RuntimeError("no CUDA device: libxp has no CPU path")
+            device = torch.cuda.current_device()
+        # without a Stream object around it where torch gives it so (not a public call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return raw(device) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -327,13 +329,15 @@ def _want(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _here(**tensors):
-    """All of them on the current device (None passes)."""
+def _here(names, *tensors):
+    """All of them on the current device (None passes), which is returned."""
     import torch
     device = torch.cuda.current_device()
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.get_device() != device:
+            name = next(n for n, x in zip(names.split(), tensors) if x is t)
             raise ValueError(f"{name}: not on the current CUDA device")
+    return device
 
 
 def _code(name, t):
@@ -375,9 +379,10 @@ def xp_verify_drafts(head, target, draft, blk, n_draft, temperature, u, noise, t
     import torch
     N, B, V = target.shape
     f32, i64, i32 = torch.float32, torch.int64, torch.int32
-    _here(target=target, draft=draft, blk=blk, n_draft=n_draft, temperature=temperature, u=u,
-          noise=noise, tokens=tokens, counts=counts, prob=prob, ws=ws)
-    _want(target.stride(2) == 1, "target: [N, B, V] with unit stride over V")
+    device = _here("target draft blk n_draft temperature u noise tokens counts prob ws", target, draft, blk,
+                   n_draft, temperature, u, noise, tokens, counts, prob, ws)
+    sn, sb, sv = target.stride()
+    _want(sv == 1, "target: [N, B, V] with unit stride over V")
     _want(draft is None or (draft.dtype == f32 and draft.dim() == 2 and draft.stride(1) == 1
                             and draft.shape[0] >= N * (B - 1) and draft.shape[1] >= V),
           "draft: fp32 [N*(B-1), >= V] with unit stride over V")
@@ -390,16 +395,16 @@ def xp_verify_drafts(head, target, draft, blk, n_draft, temperature, u, noise, t
         if t is not None and not (t.dtype == dt and t.is_contiguous() and t.numel() >= count):
             raise ValueError(f"{name}: contiguous {dt} of at least {count} elements")
     _check("xp_verify_drafts", lib().xp_verify_drafts(
-        head, _ptr(target), target.stride(0), target.stride(1), _ptr(draft),
+        head, _ptr(target), sn, sb, _ptr(draft),
         draft.stride(0) if draft is not None else 0, _ptr(blk), _ptr(n_draft), N, B, V,
         _code("target", target), _ptr(temperature), _ptr(u), _ptr(noise), noise.stride(0) if N > 1 else noise.shape[1], _ptr(tokens),
-        _ptr(counts), _ptr(prob), _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(counts), _ptr(prob), _ptr(ws), _nbytes(ws), _stream(stream, device)))
 
 
 def make_cache_desc(k, v, max_seqs: int = 4096) -> xp_cache_desc:
     """Descriptor of K and V pools seen as [layers, pages, page_size, kv_heads, head_dim] (views
     with the heads outside the tokens too)."""
-    _here(k=k, v=v)
+    _here("k v", k, v)
     _want(k.dim() == 5 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
           and k.stride(4) == 1,
           "k, v: bf16 or fp32 tensors [layers, pages, page_size, kv_heads, head_dim] of the "
@@ -415,9 +420,9 @@ def xp_cache_prep_bytes(d: xp_cache_desc) -> int:
 
 def xp_cache_create(d: xp_cache_desc, prep, stream=None):
     out = ctypes.c_void_p()
-    _here(prep=prep)
+    device = _here("prep", prep)
     _check("xp_cache_create", lib().xp_cache_create(ctypes.byref(d), _ptr(prep), _nbytes(prep),
-                                                    _stream(stream), ctypes.byref(out)))
+                                                    _stream(stream, device), ctypes.byref(out)))
     return out.value
 
 
@@ -434,31 +439,31 @@ def xp_cache_append(cache, layer, k, v, table, lens, stream=None):
     """Write the K and V rows [N, T, kv_heads, head_dim] of the newest tokens (lens counts them).
     Only the table's own columns are read, those of a wider tensor that it is a part of are not."""
     N, T = k.shape[:2]
-    _here(k=k, v=v, table=table, lens=lens)
+    device = _here("k v table lens", k, v, table, lens)
     _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
           and k.stride(3) == 1, "k, v: [N, T, kv_heads, head_dim] of the same strides")
     ld = _table("table", table, N)
     _ints("lens", lens, N)
     _check("xp_cache_append", lib().xp_cache_append_columns(
-        cache, layer, _ptr(k), _ptr(v), k.stride(0), k.stride(1), k.stride(2), k.shape[2],
-        k.shape[3], _code("k", k), _ptr(table), ld, table.shape[1], _ptr(lens), N, T,
-        _stream(stream)))
+        cache, layer, _ptr(k), _ptr(v), *k.stride()[:3], k.shape[2], k.shape[3],
+        _code("k", k), _ptr(table), ld, table.shape[1], _ptr(lens), N, T,
+        _stream(stream, device)))
 
 
 def xp_cache_copy(cache, src, dst, stream=None):
     """Copy whole pages src[i] -> dst[i] in every layer."""
-    _here(src=src, dst=dst)
+    device = _here("src dst", src, dst)
     _ints("src", src, 0)
     _ints("dst", dst, src.numel())
     _check("xp_cache_copy", lib().xp_cache_copy(cache, _ptr(src), _ptr(dst), src.numel(),
-                                                _stream(stream)))
+                                                _stream(stream, device)))
 
 
 def xp_cache_resize(cache, table, lens, new_lens, refs, table_out, lens_out, refs_out, stream=None):
     """Lengths lens -> new_lens: give back or take pages (outputs may be the inputs)."""
     N, width = table.shape
-    _here(table=table, lens=lens, new_lens=new_lens, refs=refs, table_out=table_out,
-          lens_out=lens_out, refs_out=refs_out)
+    device = _here("table lens new_lens refs table_out lens_out refs_out", table, lens, new_lens, refs, table_out,
+                   lens_out, refs_out)
     ld, ld_out = _table("table", table), _table("table_out", table_out, N)
     _want(table_out.shape[1] >= width, "table_out: as wide as table")
     for name, t in (("lens", lens), ("new_lens", new_lens), ("lens_out", lens_out)):
@@ -467,7 +472,7 @@ def xp_cache_resize(cache, table, lens, new_lens, refs, table_out, lens_out, ref
     _ints("refs_out", refs_out, refs.numel())
     _check("xp_cache_resize", lib().xp_cache_resize(
         cache, _ptr(table), ld, _ptr(lens), _ptr(new_lens), _ptr(refs), refs.numel(), N, width,
-        _ptr(table_out), ld_out, _ptr(lens_out), _ptr(refs_out), _stream(stream)))
+        _ptr(table_out), ld_out, _ptr(lens_out), _ptr(refs_out), _stream(stream, device)))
 
 
 def xp_cache_fork(cache, table, lens, parent, cut, refs, child_table, child_lens, refs_out,
@@ -475,8 +480,8 @@ def xp_cache_fork(cache, table, lens, parent, cut, refs, child_table, child_lens
     """Children parent[i] continued at min(lens[parent[i]], cut[i]) (cut may be None)."""
     rows, width = table.shape
     M = parent.numel()
-    _here(table=table, lens=lens, parent=parent, cut=cut, refs=refs, child_table=child_table,
-          child_lens=child_lens, refs_out=refs_out)
+    device = _here("table lens parent cut refs child_table child_lens refs_out", table, lens, parent, cut, refs,
+                   child_table, child_lens, refs_out)
     ld, ld_child = _table("table", table), _table("child_table", child_table, M)
     _want(child_table.shape[1] >= width, "child_table: as wide as table")
     for name, t, n in (("lens", lens, rows), ("parent", parent, M), ("cut", cut, M),
@@ -485,15 +490,15 @@ def xp_cache_fork(cache, table, lens, parent, cut, refs, child_table, child_lens
     _ints("refs_out", refs_out, refs.numel())
     _check("xp_cache_fork", lib().xp_cache_fork(
         cache, _ptr(table), ld, _ptr(lens), rows, _ptr(parent), _ptr(cut), M, width, _ptr(refs),
-        refs.numel(), _ptr(child_table), ld_child, _ptr(child_lens), _ptr(refs_out), _stream(stream)))
+        refs.numel(), _ptr(child_table), ld_child, _ptr(child_lens), _ptr(refs_out), _stream(stream, device)))
 
 
 def xp_cache_compact(cache, table, lens, refs, table_out, refs_out, map=None, live=None,
                      stream=None):
     """Pack the pages in use to the pool's front; map[page] is each page's new id."""
     N, width = table.shape
-    _here(table=table, lens=lens, refs=refs, table_out=table_out, refs_out=refs_out, map=map,
-          live=live)
+    device = _here("table lens refs table_out refs_out map live", table, lens, refs, table_out, refs_out, map,
+                   live)
     ld, ld_out = _table("table", table), _table("table_out", table_out, N)
     _want(table_out.shape[1] >= width, "table_out: as wide as table")
     _ints("lens", lens, N)
@@ -503,7 +508,7 @@ def xp_cache_compact(cache, table, lens, refs, table_out, refs_out, map=None, li
     _ints("live", live, 1)
     _check("xp_cache_compact", lib().xp_cache_compact(
         cache, _ptr(table), ld, _ptr(lens), N, width, _ptr(refs), refs.numel(), _ptr(table_out),
-        ld_out, _ptr(refs_out), _ptr(map), _ptr(live), _stream(stream)))
+        ld_out, _ptr(refs_out), _ptr(map), _ptr(live), _stream(stream, device)))
 
 
 def make_attn(q, out, layer: int, prefix_len: int, max_len: int, scale: float) -> xp_attn:
@@ -528,7 +533,7 @@ def xp_prefix_attention(cache, attn, q, prefix_table, table, lens, out, lse, ws,
     _want((q.shape, q.stride(), q.dtype) == attn.q_like
           and (out.shape, out.stride(), out.dtype) == attn.out_like,
           "q, out: the shapes, strides and type that make_attn was given")
-    _here(q=q, prefix_table=prefix_table, table=table, lens=lens, out=out, lse=lse, ws=ws)
+    device = _here("q prefix_table table lens out lse ws", q, prefix_table, table, lens, out, lse, ws)
     ld = width = 0
     if table is not None:
         ld, width = _table("table", table, attn.N), table.shape[1]
@@ -540,7 +545,7 @@ def xp_prefix_attention(cache, attn, q, prefix_table, table, lens, out, lse, ws,
     _check("xp_prefix_attention", lib().xp_prefix_attention(
         cache, ctypes.byref(attn), _ptr(q), _ptr(prefix_table),
         0 if prefix_table is None else prefix_table.numel(), _ptr(table), ld, width, _ptr(lens),
-        _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream, device)))
 
 
 # ------------------------------------------------------ torch conveniences ---
