@@ -468,17 +468,19 @@ xp_status xp_cache_compact(const xp_cache* cache, const int32_t* table, int64_t 
  * h / (heads / kv_heads):
  *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale * q . k_j).
  * The prefix is read once for the whole batch, not once a sequence.  A query that sees
- * nothing gets out = 0 and lse = -inf.  Tokens behind the lengths may hold anything, and an
- * infinite or NaN key or value reaches the queries that see it and no others.
+ * nothing, or only scores of -inf, gets out = 0 and lse = -inf.  Tokens behind the lengths may
+ * hold anything, and an infinite or NaN key or value reaches the queries that see it and no others.
  * q, out: cache dtype, element (n, t, h, i) at n*stride_n + t*stride_t + h*stride_h + i.
  * prefix_table: device int32, prefix_pages >= ceil(prefix_len / page_size) entries.  table:
  * device int32, row n at table + n*ld_table, width >= ceil(max_len / page_size) columns.
  * lens: device [N] int32; lengths above max_len are clamped (XP_ELENGTH).  lse: device fp32
  * [N, T, heads] or NULL.  scale: positive and finite.  Scores, softmax and sums are fp32 (bf16:
  * each weight is rounded to bf16 before it multiplies v, as the tensor cores take it).
- * bf16 caches of head_dim 64 or 128 and pages of a multiple of 8 tokens run on the tensor cores;
- * there queries on 16-byte boundaries with one stride from token to token (across sequences
- * too) are loaded fastest. */
+ * bf16 caches of head_dim 64 or 128 and pages of a multiple of 8 tokens, with pools on 16-byte
+ * boundaries and strides that are multiples of 8, run on the tensor cores; all others run on CUDA
+ * cores, at a small part of that rate (an fp32 cache keeps the weights in 32 bits).  On tensor cores
+ * queries on 16-byte boundaries with one stride from token to token, across sequences too, are
+ * loaded fastest: a slice of the last T tokens of longer rows costs half the call's time again. */
 typedef struct {
   int layer, N, T, heads;
   int head_dim;      /* head_dim and dtype: those of q and out, which must be the cache's */

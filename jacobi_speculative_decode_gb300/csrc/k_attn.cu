@@ -50,10 +50,14 @@ __device__ __forceinline__ float4 load4(const bf16* p, bool wide, int n) {
 // A CTA holds BM query rows and walks over its keys 64 at a time: scores from shared memory (RM
 // x 4 a thread), one pass of the softmax in base 2 with a running maximum and sum, weights times
 // values.  A warp loads eight keys and values at once, a lane four dims.
-// For large calls the fp32 multiply-adds bound it; for small ones the latency of a step's loads
-// (page ids, then keys and values), so key ranges are as short as one step of 64 keys until two
-// CTAs an SM have work: 7 sequences of 5 tokens, 12 heads of 96 over 3, prefix 1001, tails up to
-// 333: 33.3 us both kernels (84 with loads of single elements and longer ranges).
+// Large calls wait for shared memory: 64 rows a CTA leave 8 warps an SM, which issue in 57% of the
+// cycles with that pipe 59% and the multiply-adds 44% busy.  32 blocks of 16 tokens, 32 heads of 128
+// over 8, prefix 8192, tails up to 1500, fp32: 2,646 us, 28.8 TFLOP/s, 36% of 152 SMs' fp32 rate;
+// bf16 of heads that the tensor cores' form does not take is no faster (heads of 96: 18.4, pages of
+// 20 tokens: 23.9).  Small ones are bound by the latency of a step's loads (page ids, then keys and
+// values), so key ranges are as short as one step of 64 keys until two CTAs an SM have work:
+// 7 sequences of 5 tokens, 12 heads of 96 over 3, prefix 1001, tails up to 333: 33.3 us both kernels
+// (84 with loads of single elements and longer ranges).
 template <typename T, int RM, int NC>
 __global__ void __launch_bounds__(kThreads, RM <= 2 ? 2 : 1) attn_simt_kernel(const xp_attn_args g,
                                                              bool wide) {

@@ -19,12 +19,22 @@
 // 2,800, as each stream's chain is as long: S 512, softmax to the first half of P 990 and to the
 // second 550, the second half of P V 256, and about 100 for each of four hand-overs.  128
 // blocks of 16 tokens, 32 heads of 128 over 8, behind a shared prefix of 8192 and tails up to
-// 2048 (309 GFLOP, 608 MB): 248 us back to back, 1.25 PFLOP/s, 66% of measured.
+// 2048 (309 GFLOP, 608 MB): 244 us with the joining kernel, back to back, 1.27 PFLOP/s, 68% of
+// measured.
 // A tail of few rows is bound by one tile's chain, 2,160 cycles for a tile of 128 keys of two
 // heads, and by what a unit costs at its ends (about 5,000 cycles: a masked tile, the last
 // product, the result's way out, code and constants that must be fetched anew).  256 single tokens,
-// 64 heads of 64 over 8, a prefix of 16384 and tails up to 2000 (588 MB): 165 us, 3.6 TB/s.
-// (Two streams on one head's even and odd tiles took 197: two results and two ends a unit.)
+// 64 heads of 64 over 8, a prefix of 16384 and tails up to 2000 (588 MB): 164 us, 3.6 TB/s.
+// (Two streams on one head's even and odd tiles took 20% more: two results and two ends a unit.)
+// A prompt's tiles are all walked, those above the diagonal too: 2,048 tokens of 32 heads of 128 over
+// 8 take 77 us, 446 TFLOP/s of what the mask leaves; 8,192 take 819, 671.
+//
+// P is rounded to bf16, 2^-9 of each weight, because the tensor core takes both operands of a
+// product in one 16-bit type, and V is bf16; the sum of a row is taken before that rounding, in fp32.
+// Errors against 64 bits are 2.1e-3 to 2.3e-3 of the outputs' norm, of which the outputs' own
+// rounding to bf16 is 1.7e-3.  (The rest of each weight as a second operand would cost a third
+// product for every two.)
+//
 // Tiles of 128 x 128: a product reads 8 KB of shared memory for 64 cycles of work, which is all
 // that can be read; half a tile of rows or keys would be bound by it.  Two streams: 128 columns of
 // scores and D of results each fill tensor memory at D = 128.
@@ -94,9 +104,9 @@ struct Bars {
 // same.  A piece that begins its unit leaves its result in the unit's place, one that does not in
 // the place of its CTA, of which there is at most one.
 // The costs are timed (a unit 2.2 us, two row tiles 1.4 a key tile, two heads 1.6, or 1.4 with one
-// warp's rows).  Many blocks of 16 tokens take 253 us; with 8 or 10 for two heads 259 and 258,
-// with units of 20 254.  256 single tokens take 162; with 9 or 7 for few rows 171 and 163, and 128
-// blocks of 4 tokens (32 rows, not few) 195 to 198 with 9 to 10 and 217 with 7.
+// warp's rows).  With 8 or 10 for two heads many blocks of 16 tokens take 2% more, with units of 20
+// as long.  With 9 or 7 for few rows 256 single tokens take 6% and 1% more; 128 blocks of 4 tokens
+// (32 rows, not few) 11% more with 7 than with 9 or 10.
 struct Line {
   int H, pairs, odd, T;    // kv heads; row tiles as pairs and one over; key tiles
   bool few;                // rows of the one over
@@ -859,11 +869,11 @@ __device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, in
 // A CTA joins 32 rows of (sequence, kv head, token, head) order: a thread is a row, a warp every
 // eighth of its 16-byte pieces; the rows leave through shared memory.  Bound by the partial
 // results' bytes, mostly from L2: 65,536 rows of 128 with two or three each, about 80 MB, in
-// 20 to 25 us; with few rows by the latency of what it asks for.
+// 20 to 29 us; with few rows by the latency of what it asks for.
 // TOGETHER: partial results asked for at once.  Few rows have many (a long prefix is cut by every
-// CTA) and nobody else's work to wait under: four at once take 16.4 us where one takes 17.3 (both
-// kernels, one request of 4 tokens).  Many rows have three or four, and one at a time leaves
-// room for more CTAs: 266 us and 274 (128 blocks of 16 tokens).
+// CTA) and nobody else's work to wait under: four at once take 5% off both kernels' time (one
+// request of 4 tokens).  Many rows have three or four, and one at a time leaves room for more
+// CTAs: 3% off (128 blocks of 16 tokens).
 template <int D, int TOGETHER>
 __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_constant__ xp_attn_args g,
                                                               int ctas) {
@@ -1078,8 +1088,9 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
   xp_attn_plan p = {};
   p.tc = true;
   const int per_seq = a->T * (a->heads / c->d.kv_heads);
-  // Whole tokens, so that a tile's queries are one box: loaded by plain loads instead (tiles of 128
-  // rows for every group), a tile took one warp 20 us, and 80 single tokens of groups of 7 111 us.
+  // Whole tokens, so that a tile's queries are one box.  Loaded by one warp's plain loads instead,
+  // as where tokens are not one stride apart, 80 blocks of 2 tokens of groups of 7 take 45 us and not
+  // 27, 128 blocks of 16 tokens 381 and not 240 (108 and 822 off 16-byte boundaries).
   const int group = a->heads / c->d.kv_heads, RT = group <= kRows ? kRows / group * group : kRows;
   p.rows_tile = RT;
   p.prefix_tiles = (int)(((int64_t)a->N * per_seq + RT - 1) / RT);

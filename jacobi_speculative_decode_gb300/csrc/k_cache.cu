@@ -2,7 +2,7 @@
 // compact).  A table call is one cluster of 8 CTAs: its phases (release, rank the free
 // pages, hand them out) each need the whole of the one before, and a cluster's barrier and
 // shared memory order them within one launch.  Their bound is latency: four or five cluster barriers and the
-// loads between them, 9 to 11 us for tables of up to 256 rows and 16,384 pages, whose bytes
+// loads between them, about 10 us on the GPU (12 a call) for 256 rows and 16,384 pages, whose bytes
 // would take less than one.  (One CTA would order the phases more cheaply, but read 16,384 counts
 // in 16 rounds; a grid-wide barrier costs more than a cluster's.)
 #include <cooperative_groups.h>
@@ -422,10 +422,11 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------------------
-// Page copies: (move, plane, chunk) items, a plane being K or V of one layer.  Bound by HBM: 491
-// pages of 2 MB in 8 layers moved in 300 us, 6.9 TB/s read and written together (101% of measured);
-// 256 partial pages, 520 MB, in 67 us.  32 KB a CTA and eight CTAs an SM are in flight, all loads
-// before the first store.
+// Page copies: (move, plane, chunk) items, a plane being K or V of one layer.  Bound by HBM: the
+// call that moves 491 pages of 2 MB in 8 layers takes 321 us, 6.4 TB/s read and written together
+// (95% of measured); 256 partial pages, 520 MB, take 71 us of their call's 83.  32 KB a CTA are in
+// flight, all loads before the first store; 68 registers a thread leave three CTAs an SM, so that
+// the grid of eight an SM comes in turns.
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
 constexpr int kPerThread = 8;   // vectors of a thread in flight: 32 KB a CTA

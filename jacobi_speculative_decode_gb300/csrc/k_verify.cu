@@ -232,20 +232,19 @@ struct Ring {
 // skipped.  Nothing waits for that: a row read in vain changes no result.
 // Warp 8 claims the items from a counter and streams the rows into a ring by bulk copies, ahead
 // over the items' ends; warps 0-7 sum what it holds; warp 9 writes the items' results, and
-// where an item is its row's last joins them and tests the slot (its round trips to memory
-// hold nobody up).
-// Bound by HBM, and by rows read in vain: two items a CTA are claimed and under way, close to a
-// slot of a large batch, and a rejection is known only when its row is done.  So the streaming
-// warp looks at the block's mark again with every stage and leaves a row in the middle (draft
-// logits below: 75 us without).
-// 256 blocks of 16 slots, 151,936 ids, bf16, one-hot drafts of which 0.7 are accepted: 105 us, 4.6
-// TB/s of what it reads (490 MB, a quarter of it in vain); the wanted rows alone would take 55.  Both kernels take 150 there, 68 for
-// 32 blocks with the drafter's logits.
-// Two CTAs of 64 KB in flight an SM: one of 512 threads and 96 to 192 KB takes 10 to 30 us more.
-// Items of 65536 ids where there are enough of them: 32768, 16384 and 8192 took 23, 70 and 157 us
-// more for the large batch (an item's end costs about 3 us of latency).  Claims of several
-// items at once, for the slots where most are not wanted, leave some CTAs with several rows at the
-// end: 10 to 190 us more.
+// where an item is its row's last joins them and tests the slot.
+// What bounds it: rows read in vain, and the ends of items.  Two items a CTA are claimed and under
+// way, close to a slot of a large batch, and a rejection is known only when its row is done.  So
+// the streaming warp looks at the block's mark again with every stage and leaves a row in the
+// middle (7 us of 75 for the drafter's logits below).  256 blocks of 16 slots, 151,936 ids, bf16,
+// one-hot drafts of which 0.7 are accepted: 111 us for 472 MB, a quarter of it in vain, 4.3 TB/s (63%
+// of measured; instructions issue in 53% of the cycles).  Both kernels take 154 there, 67 for 32
+// blocks with the drafter's logits.
+// Smaller items reach a rejection sooner but end more often, which costs more than it saves (what of
+// it is not hidden is not known): with 32768, 16384 and 8192 ids instead of 65536 the large batch took
+// 23, 70 and 157 us more.  Two CTAs of 64 KB in flight an SM: one of 512 threads and 96 to 192 KB
+// took 10 to 30 us more.  Claims of several items at once, for the slots where most are not wanted,
+// leave some CTAs with several rows at the end: 10 to 190 us more.
 template <typename T>
 __global__ void __launch_bounds__(kThreads + 64, kResident) verify_stats_kernel(
     const xp_verify_args a, int chunk, int chunks) {
@@ -670,9 +669,10 @@ __device__ unsigned long long race(const Race& r, const T* t_row, const float* d
 
 // Work items (block, chunk): the race of every id of the chunk, merged into the block's best;
 // the block's last chunk writes its tokens and clears its counters for the next call.
-// Bound by HBM: 224 blocks' target row and noise, 204 MB, in 45 us (4.5 TB/s) with five CTAs an SM
-// and items of 32768 ids (48 with the four that its registers would leave; 8192, 16384 and 65536
-// ids: 4, 1 and 5 us more).  Where few blocks would leave SMs idle an item is down to 2048 ids.
+// Bound by its loads, at 71% of HBM's rate: 224 blocks' target row and noise, 220 MB read in 46 us
+// (4.8 TB/s) with five CTAs an SM and items of 32768 ids (3 us more with the four that its registers
+// would leave; 8192, 16384 and 65536 ids: 4, 1 and 5 us more).  Where few blocks would leave SMs idle
+// an item is down to 2048 ids.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 5) verify_draw_kernel(const xp_verify_args a, int chunk) {
   __shared__ unsigned long long s_best;
