@@ -354,8 +354,8 @@ const char* xp_readout_kernel_name(const xp_head* head);
  * race no id wins (noise that is NaN or infinite), gets token -1 (XP_EEMPTY).  A drafted id outside [0, V) is rejected (XP_EBADTOKEN).
  * Rows behind a block's first rejection cannot change the result and are mostly not read.
  * B, V, dtype: what the buffers were made for; XP_EINVAL unless they are the head's.
- * ws: xp_verify_workspace_bytes, zeroed once with xp_workspace_init; calls that overlap on
- * the GPU need a workspace each. */
+ * ws: xp_verify_workspace_bytes, zeroed once with xp_workspace_init (again after XP_ETIMEOUT);
+ * calls that overlap on the GPU need a workspace each. */
 size_t xp_verify_workspace_bytes(const xp_head* head, int N);
 xp_status xp_verify_drafts(const xp_head* head, const void* target, int64_t stride_n,
                            int64_t stride_b, const float* draft, int64_t ld_draft,

@@ -179,11 +179,8 @@ void xp_cache_destroy(xp_cache* c) { delete c; }
 xp_status xp_cache_get_error(const xp_cache* c, cudaStream_t stream) {
   if (!c) return XP_ENOTPREPARED;
   if (!on_device(c)) return XP_EINVAL;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return XP_ECUDA;
   uint32_t word = 0;
-  if (cudaMemcpy(&word, c->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(c->err, 0, sizeof(word)) != cudaSuccess)
-    return XP_ECUDA;
+  if (xp_take_error(c->err, stream, &word) != cudaSuccess) return XP_ECUDA;
   if (word & XP_ERR_TIMEOUT) return XP_ETIMEOUT;
   if (word & XP_ERR_LENGTH) return XP_ELENGTH;
   if (word & XP_ERR_SHARED) return XP_ESHARED;

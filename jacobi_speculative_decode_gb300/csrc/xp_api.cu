@@ -444,11 +444,8 @@ xp_status xp_jacobi_passes(const xp_head* h, const void* base, int64_t sn, int64
 xp_status xp_get_error(const xp_head* h, cudaStream_t stream) {
   if (!h) return XP_ENOTPREPARED;
   if (!on_head_device(h)) return XP_EINVAL;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return XP_ECUDA;
   uint32_t word = 0;
-  if (cudaMemcpy(&word, h->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
-    return XP_ECUDA;
-  if (cudaMemset(h->err, 0, sizeof(word)) != cudaSuccess) return XP_ECUDA;
+  if (xp_take_error(h->err, stream, &word) != cudaSuccess) return XP_ECUDA;
   if (word & XP_ERR_TIMEOUT) return XP_ETIMEOUT;
   if (word & XP_ERR_RANGE) return XP_ERANGE;
   if (word & XP_ERR_EMPTY) return XP_EEMPTY;

@@ -256,6 +256,14 @@ cudaError_t xp_launch_attn_tc(const xp_cache* c, const xp_attn_args& g, cudaStre
 cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 cudaError_t xp_launch_attn_combine(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 
+// Read and clear an error word behind what the stream holds, and wait for both.
+inline cudaError_t xp_take_error(uint32_t* err, cudaStream_t s, uint32_t* word) {
+  cudaError_t e = cudaMemcpyAsync(word, err, sizeof(*word), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(err, 0, sizeof(*word), s);
+  const cudaError_t done = cudaStreamSynchronize(s);
+  return e == cudaSuccess ? done : e;
+}
+
 // Let a kernel use `bytes` of dynamic shared memory: asked of the runtime once a device.
 inline cudaError_t xp_allow_smem(const void* kernel, size_t bytes, unsigned long long* devices) {
   int dev = 0;

@@ -62,3 +62,15 @@ def test_every_device_helper_is_called():
             for f in re.findall(r"__device__ (?:__forceinline__|__noinline__|inline) [\w:<> *&]+?\b(\w+)\(", t)
             if len(re.findall(r"\b%s\b" % f, everything)) < 2]
     assert not idle
+
+
+def test_an_error_word_is_cleared_in_the_callers_stream():
+    # a clear in the default stream may run after the call returned, over what a kernel of a
+    # non-blocking stream has recorded since
+    text = "".join(source(name) for name in sorted(os.listdir(CSRC)))
+    assert not re.search(r"\bcudaMem(set|cpy)\s*\(", text)
+    take = body(text, "xp_take_error")
+    order = [take.index(x) for x in ("cudaMemcpyAsync(", "cudaMemsetAsync(", "cudaStreamSynchronize(")]
+    assert order == sorted(order)
+    for f in ("xp_get_error", "xp_cache_get_error"):
+        assert "xp_take_error(" in body(text, f), f
