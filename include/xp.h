@@ -442,10 +442,9 @@ xp_status xp_cache_resize(const xp_cache* cache, const int32_t* table, int64_t l
  * partly filled last page it gets a copy of its own, the tokens it holds only: the lowest
  * free id, in child order.  Without one it ends at its last full page (XP_ENOPAGES).  A
  * parent outside [0, rows) gives an empty child (XP_ELENGTH).  child_table may be rows of the
- * same table, parents among them: all parents are read before any child is written (65,536
- * children at most there; XP_EINVAL where entries of different columns overlap, or the rows lie
- * at strides too unlike to tell).  What a child's row held before is not let go: its pages stay
- * counted. */
+ * same table, parents among them: all parents are read before any child is written (XP_EINVAL
+ * where entries of different columns overlap, or the rows lie at strides too unlike to tell).
+ * What a child's row held before is not let go: its pages stay counted. */
 xp_status xp_cache_fork(const xp_cache* cache, const int32_t* table, int64_t ld_table,
                         const int32_t* lens, int rows, const int32_t* parent, const int32_t* cut,
                         int M, int width, const int32_t* refs, int pages, int32_t* child_table,

@@ -38,7 +38,7 @@ bool valid_desc(const xp_cache_desc* d) {
 }
 
 struct CachePrep {
-  size_t err, src, dst, cnt, n_moves, map, row_a, row_b, row_c, total;
+  size_t err, src, dst, cnt, n_moves, map, row_a, row_b, row_c, row_d, total;
 };
 CachePrep cache_prep(const xp_cache_desc* d) {
   CachePrep L;
@@ -53,6 +53,7 @@ CachePrep cache_prep(const xp_cache_desc* d) {
   L.row_a = take(d->max_seqs);
   L.row_b = take(d->max_seqs);
   L.row_c = take(d->max_seqs);
+  L.row_d = take(d->max_seqs);
   L.total = o;
   return L;
 }
@@ -165,6 +166,7 @@ xp_status xp_cache_create(const xp_cache_desc* d, void* prep_dev, size_t prep_by
   c->row_a = (int32_t*)(p + L.row_a);
   c->row_b = (int32_t*)(p + L.row_b);
   c->row_c = (int32_t*)(p + L.row_c);
+  c->row_d = (int32_t*)(p + L.row_d);
   c->attn_tc = xp_attn_tc_maps(c);
   if (cudaMemsetAsync(prep_dev, 0, L.total, stream) != cudaSuccess) {
     delete c;
@@ -240,7 +242,7 @@ xp_status xp_cache_fork(const xp_cache* c, const int32_t* table, int64_t ld_tabl
     return XP_EINVAL;
   const int shared = table_overlap(table, ld_table, rows, child_table, ld_child, M, width);
   if (shared < 0) return XP_EINVAL;
-  if (M > c->d.max_seqs || (shared && M > xp_fork_rows_in_place)) return XP_ECAPACITY;
+  if (M > c->d.max_seqs) return XP_ECAPACITY;
   return cuda_status(xp_launch_fork(c, table, ld_table, lens, rows, parent, cut, M, width, refs,
                                     shared != 0, child_table, ld_child, child_lens, refs_out, stream));
 }

@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kCtas = 8;
 constexpr int kThreads = 1024;
-constexpr int kForkHeld = xp_fork_rows_in_place / (kCtas * kThreads);   // entries a thread holds
+constexpr int kForkHeld = 8;   // entries that a thread holds of children made in their parents' places
 
 struct Scan {
   int warp[32];
@@ -223,7 +223,7 @@ struct ForkArgs {
   int32_t* child;
   int64_t ld_child;
   int32_t *child_lens, *refs_out;
-  int32_t *row_parent, *row_len, *row_off;
+  int32_t *row_parent, *row_len, *row_off, *row_entry;
   int32_t *src, *dst, *cnt, *n_moves;
   uint32_t* err;
 };
@@ -297,8 +297,14 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     }
   } else {
     // some columns of all rows at a time: a child's column is made from its parent's alone
-    const int rows = (a.M + kCtas - 1) / kCtas, cols = max(1, kThreads * kForkHeld / rows);
-    for (int c0 = 0; c0 < a.width; c0 += cols) {
+    const int rows = (a.M + kCtas - 1) / kCtas, cols = kThreads * kForkHeld / rows;
+    for (int j = 0; cols == 0 && j < a.width; ++j) {   // more rows than entries held: from memory
+      for (int i = r0 + tid; i < r1; i += kThreads)
+        a.row_entry[i] = shared_page(a.table + a.row_parent[i] * a.ld, a.row_len[i] / a.ps, j);
+      cl.sync();
+      for (int i = r0 + tid; i < r1; i += kThreads) a.child[i * a.ld_child + j] = a.row_entry[i];
+    }
+    for (int c0 = 0; cols > 0 && c0 < a.width; c0 += cols) {
       const int cw = min(cols, a.width - c0), entries = (r1 - r0) * cw;
       int out[kForkHeld];
 #pragma unroll
@@ -603,7 +609,7 @@ cudaError_t xp_launch_fork(const xp_cache* c, const int32_t* table, int64_t ld,
                            int32_t* refs_out, cudaStream_t s) {
   ForkArgs a = {table, ld, lens, rows, parent, cut, refs, M, width, c->d.pages, c->d.page_size,
                 in_place, child, ld_child, child_lens, refs_out, c->row_a, c->row_b, c->row_c,
-                c->src, c->dst, c->cnt, c->n_moves, c->err};
+                c->row_d, c->src, c->dst, c->cnt, c->n_moves, c->err};
   fork_kernel<<<kCtas, kThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

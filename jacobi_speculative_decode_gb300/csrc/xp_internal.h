@@ -191,7 +191,7 @@ struct xp_cache {
   int32_t *src, *dst, *cnt;  // page moves: source, target, tokens (scratch, `pages` each)
   int32_t* n_moves;        // their number
   int32_t* map;            // compaction: new id of every page (scratch)
-  int32_t *row_a, *row_b, *row_c;  // per-row scratch of the table calls (max_seqs each)
+  int32_t *row_a, *row_b, *row_c, *row_d;  // per-row scratch of the table calls (max_seqs each)
   int attn_tc;             // tokens of a TMA box of the tensor-core attention, 0: not usable
   CUtensorMap tm_k, tm_v;  // the pools as (dim, token, head, page, layer)
 };
@@ -208,8 +208,7 @@ cudaError_t xp_launch_resize(const xp_cache* c, const int32_t* table, int64_t ld
                              const int32_t* lens, const int32_t* new_lens, const int32_t* refs,
                              int N, int width, int32_t* table_out, int64_t ld_out,
                              int32_t* lens_out, int32_t* refs_out, cudaStream_t s);
-// children that may be rows of their parents' table (in_place): a row's entry each is held meanwhile
-constexpr int xp_fork_rows_in_place = 65536;
+// in_place: children may be rows of their parents' table
 cudaError_t xp_launch_fork(const xp_cache* c, const int32_t* table, int64_t ld,
                            const int32_t* lens, int rows, const int32_t* parent,
                            const int32_t* cut, int M, int width, const int32_t* refs,

@@ -265,3 +265,29 @@ def test_strides_that_are_never_used_do_not_count(page):
                      torch.empty(1, 1, 2, 64, device="cuda").bfloat16(), 2, 0, 16, 0.1)
     sizes = [xp.Cache(t, t).attention_workspace(a).numel() for t in (one_page, view)]
     assert sizes[0] == sizes[1]
+
+
+def test_fork_of_more_rows_than_a_cluster_holds_over_its_own_parents():
+    rows, width, ps = 70001, 2, 3
+    g = np.random.default_rng(8)
+    table, lens, refs, k = beams(g, rows, width, ps)
+    parent = np.concatenate([np.arange(1, rows), [0]]).astype(np.int32)
+    cache = xp.Cache(k, k + 0.5, max_seqs=rows)
+    t, n, r = ints(table), ints(lens), ints(refs)
+    xp.xp_cache_fork(cache.handle, t, n, ints(parent), None, r, t, n, r)
+    assert xp.xp_cache_get_error(cache.handle) == xp.XP_OK
+    # worked out at once: every row's full pages are held twice, partly filled last pages are copied to
+    # the lowest free ids in child order
+    lens = lens[parent]
+    full, part = lens // ps, lens % ps
+    child = np.where(np.arange(width) < full[:, None], table[parent], -1)
+    np.add.at(refs, child[child >= 0], 1)
+    free = np.nonzero(refs == 0)[0][:(part > 0).sum()]
+    child[np.nonzero(part)[0], full[part > 0]] = free
+    refs[free] = 1
+    assert np.array_equal(t.cpu().numpy(), child) and np.array_equal(n.cpu().numpy(), lens)
+    assert np.array_equal(r.cpu().numpy(), refs)
+    some = np.nonzero(part)[0][::997]
+    src, dst = table[parent[some], full[some]], child[some, full[some]]
+    for s, d, count in zip(src.tolist(), dst.tolist(), part[some].tolist()):
+        assert torch.equal(cache.k[:, d, :count], cache.k[:, s, :count])
