@@ -59,7 +59,8 @@ typedef enum {
   XP_ETIMEOUT = 6,      /* device flag: a bounded wait inside a kernel gave up         */
   XP_EUNSUPPORTED = 7,  /* shape not supported by this build                           */
   XP_ERANGE = 8,        /* device flag: a latent-stage value left the fp16 range of the
-                           tensor-core latent's exchanges (saturated; results unreliable) */
+                           tensor-core latent's exchanges (saturated; results unreliable), or a
+                           row written to a quantised cache held NaN or more than it can hold   */
   XP_EBADPAGE = 9,      /* device flag: a page id outside the pool (clamped when read, ignored
                            when freed) or a page freed more often than it was held        */
   XP_ENOPAGES = 10,     /* device flag: the pool ran out of free pages; rows were cut short */
@@ -69,7 +70,8 @@ typedef enum {
   XP_EEMPTY = 13        /* device flag: a target row left no token to draw (token -1)      */
 } xp_status;
 
-typedef enum { XP_BF16 = 0, XP_F32 = 1 } xp_dtype;
+/* XP_Q8 and XP_Q4 are types of paged caches alone (see xp_cache_desc). */
+typedef enum { XP_BF16 = 0, XP_F32 = 1, XP_Q8 = 2, XP_Q4 = 3 } xp_dtype;
 
 /* Head weights, torch layouts ([out, in] row-major for linear maps).  All
  * pointers are device pointers, read only during xp_head_create /
@@ -364,6 +366,32 @@ xp_status xp_verify_drafts(const xp_head* head, const void* target, int64_t stri
                            int64_t ld_noise, int64_t* tokens, int32_t* counts, float* prob,
                            void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* Log probabilities of given tokens under the rows they were drawn from, with the entropy of the
+ * distribution, the token's rank and the best alternatives.  With x = tokens[n, b], l = logits[n, b] and
+ * t = temperature[n], p = softmax(l / t):
+ *   logprob[n, b] = log p(x),  entropy[n, b] = -sum_v p(v) log p(v),
+ *   rank[n, b] = 1 + the number of ids ahead of x in order of l, ties to the lower id,
+ *   top_ids[n, b, 0..top-1], top_logprobs: the first ids in that order (-1 and -inf where there are not
+ *   as many ids above -inf), and their log p.
+ * tokens: the layout that xp_verify_drafts writes (its token of slot b was drawn from target row b).  A row
+ * whose token is -1 is not read: logprob, entropy, rank and top_logprobs 0, top_ids -1; so is one whose
+ * token lies outside [-1, V) (XP_EBADTOKEN).  temperature as for xp_verify_drafts: t = 0 makes p one-hot at
+ * the lowest argmax.  Logits are read as there: NaN like -inf, +inf like the largest finite value; a
+ * row with nothing above -inf has logprob -inf, entropy 0, rank x + 1 and no alternatives (XP_EEMPTY).
+ * logits: device, bf16 or fp32 as `dtype` says (not the head's necessarily), row (n, b) at
+ * n*stride_n + b*stride_b, unit stride over v; V: XP_EINVAL unless the head's.  tokens: device [N, B] int64;
+ * B is any number of rows a block.  Outputs: device [N, B] (logprob, entropy fp32, rank int32) and
+ * [N, B, top] (int64, fp32), each may be NULL; 0 <= top <= 32 (the top pointers are not used at 0).
+ * Sums are fp32 of the differences from the row's maximum.  N*B rows below 2^31 / 64.
+ * ws: xp_logprobs_workspace_bytes, zeroed once with xp_workspace_init; calls that overlap on the GPU need
+ * a workspace each. */
+size_t xp_logprobs_workspace_bytes(const xp_head* head, int rows, int top);
+xp_status xp_token_logprobs(const xp_head* head, const void* logits, int64_t stride_n, int64_t stride_b,
+                            const int64_t* tokens, int N, int B, int V, xp_dtype dtype,
+                            const float* temperature, int top, float* logprob, float* entropy,
+                            int32_t* rank, int64_t* top_ids, float* top_logprobs, void* ws,
+                            size_t ws_bytes, cudaStream_t stream);
+
 /* A paged key/value cache.  K and V are pools of `pages` pages of `page_size` tokens in each
  * of `layers` layers; a sequence is a row of page ids (its table) and a length, and a page
  * that several rows hold is counted in `refs`.  The pools belong to the caller; element
@@ -381,6 +409,27 @@ typedef struct {
   void* v;
 } xp_cache_desc;
 
+/* Quantised caches: dtype XP_Q8 or XP_Q4.  16 consecutive dims of a token's head share a scale s and are
+ * held as whole numbers c of 8 or 4 bits that stand for c*s, |c| <= 127 or 7.  s is an 8-bit float without a
+ * sign, 5 bits of exponent and 3 of mantissa: the 16-bit float whose bits are the byte << 7.  It is the least
+ * one for which 127*s or 7*s reaches the largest magnitude of the 16, at most 512 or 9216; c is the element
+ * over s, rounded to nearest, ties to even.  So every value held is exact in 16-bit floats (and those of 4
+ * bits in bf16), and an element is off by at most s/2.  A NaN is held as 0, and what lies beyond
+ * 127*512 or 7*9216 as the nearest value that can be held; both raise XP_ERANGE.
+ * All strides are in bytes, and heads lie outside the tokens of a page.  A head of a page is
+ * xp_quant_head_bytes: the codes of its tokens, head_dim*8/8 or head_dim*4/8 bytes each, then their scales,
+ * head_dim/16 bytes each, padded to a multiple of 4; the whole is padded to a multiple of 16.  8-bit codes
+ * are c + 128, a byte a dim.  4-bit codes are c + 8; those of 8 dims are a 32-bit word (lowest byte first),
+ * dim 2j + e of the 8 in the bits from 4*(j + 4*e) on.  head_dim: a multiple of 16; stride_token: the bytes
+ * of a token's codes; stride_head: xp_quant_head_bytes; pools on 16-byte boundaries; stride_page and
+ * stride_layer: multiples of 16.  Every call on caches takes them.  The rows of xp_cache_append and
+ * xp_cache_read are bf16 or fp32, queries and results of xp_prefix_attention bf16; where the calls below
+ * copy part of a page, they copy a quantised one whole. */
+
+/* Bytes of one head of a page of a quantised cache (0: not XP_Q8 or XP_Q4, or sizes it cannot have).
+ * Host only. */
+size_t xp_quant_head_bytes(int page_size, int head_dim, xp_dtype dtype);
+
 typedef struct xp_cache xp_cache; /* opaque, host-side */
 
 /* Device bytes of the cache's error word and of the table calls' scratch. */
@@ -392,14 +441,15 @@ xp_status xp_cache_create(const xp_cache_desc* d, void* prep_dev, size_t prep_by
                           cudaStream_t stream, xp_cache** out);
 void xp_cache_destroy(xp_cache* cache);
 
-/* Synchronise `stream`, read and clear the cache's device error word: XP_OK or one of
+/* Synchronise `stream`, read and clear the cache's device error word: XP_OK or one of XP_ERANGE,
  * XP_EBADPAGE, XP_ENOPAGES, XP_ESHARED, XP_ELENGTH, XP_ETIMEOUT (the last named first). */
 xp_status xp_cache_get_error(const xp_cache* cache, cudaStream_t stream);
 
 /* Write the keys and values of the T newest tokens of N sequences: token t of row n goes to
  * position lens[n] - T + t (lens counts them already; positions below 0 are skipped).
  * k, v: device, element (n, t, head, i) at n*stride_n + t*stride_t + head*stride_h + i.
- * heads, head_dim, dtype: theirs; XP_EINVAL unless they are the cache's.  table: device
+ * heads, head_dim, dtype: theirs; XP_EINVAL unless they are the cache's (of a quantised one: dtype
+ * XP_BF16 or XP_F32).  table: device
  * int32, row n at table + n*ld_table; lens: device [N] int32.  Positions behind a row's columns are
  * skipped (XP_ELENGTH): xp_cache_append takes ld_table as their number, xp_cache_append_columns
  * has `width` of them (a table that is some columns of a wider one). */
@@ -413,6 +463,17 @@ xp_status xp_cache_append_columns(const xp_cache* cache, int layer, const void* 
                                   int heads, int head_dim, xp_dtype dtype, const int32_t* table,
                                   int64_t ld_table, int width, const int32_t* lens, int N, int T,
                                   cudaStream_t stream);
+
+/* Read back T positions of N sequences as dense rows: row (n, t) is position first[n] + t, its keys and
+ * values where it lies in [0, lens[n]) and zeros where it does not.  first: device [N] int32, or NULL for
+ * 0 (lens[n] - T gives what xp_cache_append wrote last).  k, v (out): device, element (n, t, head, i) at
+ * n*stride_n + t*stride_t + head*stride_h + i, of type `dtype`, XP_BF16 or XP_F32, whatever the cache's
+ * (rounded to nearest once where it cannot hold the cache's value).  table, ld_table, width, lens as for
+ * xp_cache_append_columns; positions behind a row's columns are zeros (XP_ELENGTH). */
+xp_status xp_cache_read(const xp_cache* cache, int layer, const int32_t* table, int64_t ld_table, int width,
+                        const int32_t* lens, const int32_t* first, int N, int T, void* k, void* v,
+                        int64_t stride_n, int64_t stride_t, int64_t stride_h, int heads, int head_dim,
+                        xp_dtype dtype, cudaStream_t stream);
 
 /* The table calls below change page tables, lengths and reference counts (and, where they
  * say so, move pages of K and V in every layer).  Each output may be the matching input

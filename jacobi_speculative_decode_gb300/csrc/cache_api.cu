@@ -7,6 +7,7 @@
 #include <new>
 #include <numeric>
 
+#include "quant.cuh"
 #include "xp_internal.h"
 
 namespace {
@@ -27,10 +28,24 @@ int page_order(const xp_cache_desc* d) {
   return -1;
 }
 
+bool valid_quant(int page_size, int head_dim, xp_dtype dtype) {
+  return xp_is_quant(dtype) && page_size > 0 && head_dim > 0 && head_dim <= 256 && head_dim % 16 == 0;
+}
+
+bool valid_quant_desc(const xp_cache_desc* d) {
+  if (!valid_quant(d->page_size, d->head_dim, d->dtype) || !fits(d->page_size, d->kv_heads, 2 * d->head_dim))
+    return false;
+  const xp_quant_sizes q = xp_quant_of(d->page_size, d->head_dim, d->dtype);
+  return (d->kv_heads == 1 || d->stride_head == q.head) && (d->page_size == 1 || d->stride_token == q.code) &&
+         d->stride_page >= d->kv_heads * q.head && d->stride_layer >= 0 &&
+         (d->pages == 1 || d->stride_page % 16 == 0) && (d->layers == 1 || d->stride_layer % 16 == 0);
+}
+
 bool valid_desc(const xp_cache_desc* d) {
   if (!d || d->pages <= 0 || d->page_size <= 0 || d->layers <= 0 || d->kv_heads <= 0 ||
       d->head_dim <= 0 || d->head_dim > 256 || d->max_seqs <= 0)
     return false;
+  if (xp_is_quant(d->dtype)) return valid_quant_desc(d);
   if (d->dtype != XP_BF16 && d->dtype != XP_F32) return false;
   if (!fits(d->page_size, d->kv_heads, d->head_dim) || page_order(d) < 0) return false;
   const int64_t block = (int64_t)d->page_size * d->kv_heads * d->head_dim;
@@ -75,7 +90,7 @@ xp_status check_table(const xp_cache* c, const int32_t* table, int64_t ld, const
 
 bool valid_attn(const xp_cache* c, const xp_attn* a) {
   return a && a->layer >= 0 && a->layer < c->d.layers && a->N >= 0 && a->T > 0 && a->heads > 0 &&
-         a->head_dim == c->d.head_dim && a->dtype == c->d.dtype &&
+         a->head_dim == c->d.head_dim && a->dtype == (xp_is_quant(c->d.dtype) ? XP_BF16 : c->d.dtype) &&
          a->scale > 0.0f && a->scale <= FLT_MAX && a->heads % c->d.kv_heads == 0 && a->prefix_len >= 0 && a->max_len >= 0 &&
          fits(a->N, a->T, a->heads) &&
          (int64_t)a->prefix_len + a->max_len <= INT_MAX - 1024;
@@ -86,7 +101,7 @@ xp_attn_plan attn_plan(const xp_cache* c, const xp_attn* a) {
     const xp_attn_plan tc = xp_attn_tc_plan(c, a);
     if (tc.total) return tc;   // 0: more work than its line can count
   }
-  xp_attn_plan p = xp_attn_simt_plan(c, a);
+  xp_attn_plan p = xp_is_quant(c->d.dtype) ? xp_attn_quant_plan(c, a) : xp_attn_simt_plan(c, a);
   const size_t rows = (size_t)a->N * a->T * a->heads;
   p.stat_off = 0;
   p.acc_off = align_up(rows * p.parts * 8);
@@ -115,12 +130,17 @@ xp_status append(const xp_cache* c, int layer, const void* k, const void* v, int
                  const int32_t* table, int64_t ld_table, int64_t width, const int32_t* lens, int N,
                  int T, cudaStream_t stream) {
   if (!c) return XP_ENOTPREPARED;
-  if (heads != c->d.kv_heads || head_dim != c->d.head_dim || dtype != c->d.dtype || layer < 0 ||
+  const bool quant = xp_is_quant(c->d.dtype);
+  if (heads != c->d.kv_heads || head_dim != c->d.head_dim ||
+      (quant ? dtype != XP_BF16 && dtype != XP_F32 : dtype != c->d.dtype) || layer < 0 ||
       layer >= c->d.layers || N < 0 || T <= 0 || width <= 0 || ld_table < width ||
       !fits(N, T, c->d.kv_heads) || !on_device(c))
     return XP_EINVAL;
   if (N == 0) return XP_OK;   // an empty batch needs no pointers, here and in the calls below
   if (!k || !v || !table || !lens) return XP_EINVAL;
+  if (quant)
+    return cuda_status(xp_launch_append_quant(c, layer, k, v, stride_n, stride_t, stride_h, dtype, table,
+                                              ld_table, width, lens, N, T, stream));
   return cuda_status(xp_launch_append(c, layer, k, v, stride_n, stride_t, stride_h, table, ld_table,
                                       width, lens, N, T, stream));
 }
@@ -137,18 +157,27 @@ xp_status xp_cache_create(const xp_cache_desc* d, void* prep_dev, size_t prep_by
   *out = nullptr;
   if (!valid_desc(d) || !d->k || !d->v || !prep_dev || (uintptr_t)prep_dev % 256) return XP_EINVAL;
   const size_t es = xp_elem(d->dtype);
-  if ((uintptr_t)d->k % es || (uintptr_t)d->v % es) return XP_EINVAL;
+  const size_t boundary = xp_is_quant(d->dtype) ? 16 : es;
+  if ((uintptr_t)d->k % boundary || (uintptr_t)d->v % boundary) return XP_EINVAL;
   const CachePrep L = cache_prep(d);
   if (prep_bytes < L.total) return XP_ECAPACITY;
   xp_cache* c = new (std::nothrow) xp_cache();
   if (!c) return XP_ECAPACITY;
   c->d = *d;
-  c->heads_outside = page_order(d) == 1;
+  const bool quant = xp_is_quant(d->dtype);
+  c->heads_outside = quant || page_order(d) == 1;
   // What one head, token, page or layer has for a stride is never used: set to the dense one, so that
   // an odd value does not keep the pools from 16-byte accesses and TMA.
-  if (d->kv_heads == 1) c->d.stride_head = d->head_dim;
-  if (d->page_size == 1) c->d.stride_token = (int64_t)d->kv_heads * d->head_dim;
-  if (d->pages == 1) c->d.stride_page = (int64_t)d->page_size * d->kv_heads * d->head_dim;
+  if (quant) {
+    const xp_quant_sizes q = xp_quant_of(d->page_size, d->head_dim, d->dtype);
+    c->d.stride_head = q.head;
+    c->d.stride_token = q.code;
+    if (d->pages == 1) c->d.stride_page = d->kv_heads * q.head;
+  } else {
+    if (d->kv_heads == 1) c->d.stride_head = d->head_dim;
+    if (d->page_size == 1) c->d.stride_token = (int64_t)d->kv_heads * d->head_dim;
+    if (d->pages == 1) c->d.stride_page = (int64_t)d->page_size * d->kv_heads * d->head_dim;
+  }
   if (d->layers == 1) c->d.stride_layer = c->d.stride_page * d->pages;
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device) !=
@@ -188,6 +217,7 @@ xp_status xp_cache_get_error(const xp_cache* c, cudaStream_t stream) {
   if (word & XP_ERR_SHARED) return XP_ESHARED;
   if (word & XP_ERR_NOPAGES) return XP_ENOPAGES;
   if (word & XP_ERR_BADPAGE) return XP_EBADPAGE;
+  if (word & XP_ERR_RANGE) return XP_ERANGE;
   return XP_OK;
 }
 
@@ -207,6 +237,26 @@ xp_status xp_cache_append_columns(const xp_cache* c, int layer, const void* k, c
                                   cudaStream_t stream) {
   return append(c, layer, k, v, stride_n, stride_t, stride_h, heads, head_dim, dtype, table,
                 ld_table, width, lens, N, T, stream);
+}
+
+size_t xp_quant_head_bytes(int page_size, int head_dim, xp_dtype dtype) {
+  return valid_quant(page_size, head_dim, dtype) ? (size_t)xp_quant_of(page_size, head_dim, dtype).head : 0;
+}
+
+xp_status xp_cache_read(const xp_cache* c, int layer, const int32_t* table, int64_t ld_table, int width,
+                        const int32_t* lens, const int32_t* first, int N, int T, void* k, void* v,
+                        int64_t stride_n, int64_t stride_t, int64_t stride_h, int heads, int head_dim,
+                        xp_dtype dtype, cudaStream_t stream) {
+  if (!c) return XP_ENOTPREPARED;
+  if (heads != c->d.kv_heads || head_dim != c->d.head_dim || (dtype != XP_BF16 && dtype != XP_F32) ||
+      layer < 0 || layer >= c->d.layers || N < 0 || T < 0 || width <= 0 || (N > 1 && ld_table < width) ||
+      !fits(N, T, c->d.kv_heads) || !on_device(c))
+    return XP_EINVAL;
+  if (N == 0 || T == 0) return XP_OK;
+  if (!k || !v || !table || !lens || (uintptr_t)k % xp_elem(dtype) || (uintptr_t)v % xp_elem(dtype))
+    return XP_EINVAL;
+  return cuda_status(xp_launch_cache_read(c, layer, table, ld_table, width, lens, first, N, T, k, v, stride_n,
+                                          stride_t, stride_h, dtype, stream));
 }
 
 xp_status xp_cache_copy(const xp_cache* c, const int32_t* src, const int32_t* dst, int count,
@@ -305,8 +355,10 @@ xp_status xp_prefix_attention(const xp_cache* c, const xp_attn* a, const void* q
   g.err = c->err;
   g.plan = plan;
   if (plan.tc) return cuda_status(xp_launch_attn_tc(c, g, stream));
-  cudaError_t e = xp_launch_attn_simt(c, g, stream);
-  if (e == cudaSuccess) e = xp_launch_attn_combine(c, g, stream);
+  const bool quant = xp_is_quant(c->d.dtype);
+  cudaError_t e = quant ? xp_launch_attn_quant(c, g, stream) : xp_launch_attn_simt(c, g, stream);
+  // one range a row of the quantised form is written out by its kernel
+  if (e == cudaSuccess && !(quant && plan.parts == 1)) e = xp_launch_attn_combine(g, stream);
   return cuda_status(e);
 }
 
@@ -358,6 +410,48 @@ xp_status xp_verify_drafts(const xp_head* h, const void* target, int64_t stride_
   a.part = (float*)(w + L.part);
   a.row = (float*)(w + L.row);
   return cuda_status(xp_launch_verify(h, a, stream));
+}
+
+size_t xp_logprobs_workspace_bytes(const xp_head* h, int rows, int top) {
+  return h && rows >= 0 && rows < INT_MAX / 64 && top >= 0 && top <= 32 ? xp_logprobs_layout(h, rows, top).total
+                                                                        : 0;
+}
+
+xp_status xp_token_logprobs(const xp_head* h, const void* logits, int64_t stride_n, int64_t stride_b,
+                            const int64_t* tokens, int N, int B, int V, xp_dtype dtype,
+                            const float* temperature, int top, float* logprob, float* entropy,
+                            int32_t* rank, int64_t* top_ids, float* top_logprobs, void* ws,
+                            size_t ws_bytes, cudaStream_t stream) {
+  if (!h) return XP_ENOTPREPARED;
+  if (N < 0 || B < 0 || V != h->V || (dtype != XP_BF16 && dtype != XP_F32) || top < 0 || top > 32 ||
+      !xp_on_head_device(h) || (int64_t)N * B >= INT_MAX / 64)
+    return XP_EINVAL;
+  if (N == 0 || B == 0) return XP_OK;
+  if (!logits || (uintptr_t)logits % xp_elem(dtype) || !tokens || !ws || (uintptr_t)ws % 256 || stride_n < 0 ||
+      stride_b < 0)
+    return XP_EINVAL;
+  const xp_logprobs_ws L = xp_logprobs_layout(h, N * B, top);
+  if (ws_bytes < L.total) return XP_ECAPACITY;
+  char* w = (char*)ws;
+  xp_logprobs_args a;
+  a.logits = logits;
+  a.sn = stride_n;
+  a.sb = stride_b;
+  a.tokens = tokens;
+  a.temperature = temperature;
+  a.N = N;
+  a.B = B;
+  a.top = top;
+  a.dtype = dtype;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.rank = rank;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.tickets = (unsigned*)(w + L.tickets);
+  a.stat = w + L.stat;
+  a.best = (unsigned long long*)(w + L.best);
+  return cuda_status(xp_launch_logprobs(h, a, stream));
 }
 
 }  // extern "C"

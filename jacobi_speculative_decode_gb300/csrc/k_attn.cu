@@ -381,9 +381,9 @@ cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaSt
   return rm == 1 ? launch_nc<float, 1>(g, s) : rm == 2 ? launch_nc<float, 2>(g, s) : launch_nc<float, 4>(g, s);
 }
 
-cudaError_t xp_launch_attn_combine(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
+cudaError_t xp_launch_attn_combine(const xp_attn_args& g, cudaStream_t s) {
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
   const dim3 grid((unsigned)((rows + 7) / 8)), block(256);
-  return c->d.dtype == XP_BF16 ? xp_launch_pdl(attn_combine_kernel<bf16>, grid, block, 0, s, g)
+  return g.a.dtype == XP_BF16 ? xp_launch_pdl(attn_combine_kernel<bf16>, grid, block, 0, s, g)
                                : xp_launch_pdl(attn_combine_kernel<float>, grid, block, 0, s, g);
 }

@@ -9,6 +9,7 @@
 
 #include <algorithm>
 
+#include "quant.cuh"
 #include "sm100_ptx.cuh"
 #include "xp_device.cuh"
 
@@ -573,9 +574,15 @@ cudaError_t xp_launch_copy_pages(const xp_cache* c, const int32_t* src, const in
   a.page_bytes = d.stride_page * es;
   a.layers = d.layers;
   a.pages = d.pages;
-  a.block_bytes = (int64_t)d.page_size * d.kv_heads * d.head_dim * es;
-  a.token_bytes = (c->heads_outside ? 1 : d.kv_heads) * d.head_dim * es;
-  a.seg_bytes = a.token_bytes * d.page_size;
+  if (xp_is_quant(d.dtype)) {   // codes and scales of a token lie apart: pages move whole
+    a.block_bytes = d.kv_heads * xp_quant_of(d.page_size, d.head_dim, d.dtype).head;
+    a.token_bytes = a.seg_bytes = a.block_bytes;
+    tokens = nullptr;
+  } else {
+    a.block_bytes = (int64_t)d.page_size * d.kv_heads * d.head_dim * es;
+    a.token_bytes = (c->heads_outside ? 1 : d.kv_heads) * d.head_dim * es;
+    a.seg_bytes = a.token_bytes * d.page_size;
+  }
   a.src = src;
   a.dst = dst;
   a.tokens = tokens;

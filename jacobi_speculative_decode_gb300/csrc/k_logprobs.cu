@@ -1,0 +1,350 @@
+// Log probabilities of given tokens, the entropy, the token's rank and the best alternatives: one pass
+// over the row.
+//
+// A row, or a part of one, is a CTA's.  Every thread keeps a running maximum m, S = sum 2^((l - m) c)
+// and W = sum (l - m) c 2^((l - m) c), c = log2(e) / t; then, all joined at the row's maximum,
+//   log p(x) = (l_x - m) / t - log S,   H = log S - log(2) W / S.
+// Differences are taken before they are scaled, so that neither large logits nor small temperatures lose
+// digits.  The best ids are a list of 32 a warp, a lane an entry, kept sorted; an id is
+// looked at only where it passes the list's last entry and a bound that all warps know.
+#include <float.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "xp_device.cuh"
+
+using namespace xpd;
+typedef __nv_bfloat16 bf16;
+typedef unsigned long long u64;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kLoads = 4;             // 16-byte vectors of a thread in flight
+constexpr int kResident = 4;          // CTAs an SM that a row is cut for
+constexpr int kLeastVectors = kThreads * kLoads;   // of a part of a row
+constexpr float kLog2e = 1.44269504088896f;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+struct Args {
+  const void* logits;
+  int64_t sn, sb;
+  const int64_t* tokens;
+  const float* temperature;
+  int B, V, top, parts;
+  float *logprob, *entropy;
+  int32_t* rank;
+  int64_t* top_ids;
+  float* top_logprobs;
+  uint32_t* err;
+  unsigned* tickets;     // a row's finished parts; zero between calls
+  float4* stat;          // (m, S, W, ids ahead) of a part
+  u64* best;             // its list
+};
+
+struct Stat {
+  float m, s, w;   // m: -FLT_MAX at least
+  int ahead;
+};
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// the sums of a at a maximum m that is not below its own
+__device__ __forceinline__ void rebase(Stat& a, float m, float c) {
+  if (a.s > 0.0f) {
+    const float d = (a.m - m) * c, f = ex2(d);
+    a.w = f > 0.0f ? (a.w + d * a.s) * f : 0.0f;
+    a.s *= f;
+  }
+  a.m = m;
+}
+__device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  rebase(a, m, c);
+  rebase(b, m, c);
+  return {m, a.s + b.s, a.w + b.w, a.ahead + b.ahead};
+}
+
+template <typename T> struct Vec;
+template <> struct Vec<bf16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void get(const uint4& x, float (&f)[8]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void get(const uint4& x, float (&f)[4]) {
+    f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y);
+    f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
+  }
+};
+// as the softmax reads a logit: NaN as -inf, +inf as the largest finite value
+__device__ __forceinline__ float read_logit(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
+
+// A list of the 32 best (value, lowest id first) of a warp, lane i its entry i; 0: none.
+__device__ __forceinline__ void insert(u64& list, u64 key, int lane) {
+  const int at = __popc(__ballot_sync(kAll, list > key));   // entries that stay ahead
+  const u64 up = __shfl_up_sync(kAll, list, 1);
+  if (lane >= at) list = lane == at ? key : up;
+}
+// the 32 best of two lists
+__device__ __forceinline__ u64 merge(u64 a, u64 b, int lane) {
+  const u64 r = __shfl_sync(kAll, b, 31 - lane);
+  u64 v = a > r ? a : r;   // the 32 best, rising and falling
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const u64 w = __shfl_xor_sync(kAll, v, o);
+    v = ((lane & o) == 0) == (v > w) ? v : w;
+  }
+  return v;
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
+  constexpr int E = Vec<T>::N;
+  __shared__ Stat s_stat[kWarps];
+  __shared__ u64 s_best[kWarps][32];
+  __shared__ float s_bound[kWarps];
+  __shared__ int s_last;
+
+  const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  const int n = row / a.B, b = row % a.B;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t x = a.tokens[row];
+  if (x < 0 || x >= a.V) {   // none: nothing is read
+    if (part != 0) return;
+    if (threadIdx.x == 0) {
+      if (x != -1) atomicOr(a.err, XP_ERR_BADTOKEN);
+      if (a.logprob) a.logprob[row] = 0.0f;
+      if (a.entropy) a.entropy[row] = 0.0f;
+      if (a.rank) a.rank[row] = 0;
+    }
+    if (TOP && (int)threadIdx.x < a.top) {
+      if (a.top_ids) a.top_ids[(int64_t)row * a.top + threadIdx.x] = -1;
+      if (a.top_logprobs) a.top_logprobs[(int64_t)row * a.top + threadIdx.x] = 0.0f;
+    }
+    return;
+  }
+  const T* l = (const T*)a.logits + n * a.sn + b * a.sb;
+  const float heat = a.temperature ? a.temperature[n] : 1.0f;
+  const bool greedy = !(heat >= FLT_MIN);   // of a smaller one 1 / t is not finite
+  const float inv_t = greedy ? 1.0f : fmaxf(1.0f / heat, FLT_MIN), c = inv_t * kLog2e;
+  const float mine = read_logit(to_f(l[x]));
+  // an id at -inf has all lower ids ahead of it, and of the higher ones those above -inf
+  const bool low = mine == -INFINITY;
+
+  // vectors from the first 16-byte boundary on; this CTA's are [v0, v1)
+  const int head = min(a.V, (int)((16 - ((uintptr_t)l & 15)) % 16 / sizeof(T)));
+  const int vectors = (a.V - head) / E;
+  const int v0 = (int)((int64_t)vectors * part / a.parts), v1 = (int)((int64_t)vectors * (part + 1) / a.parts);
+  const uint4* body = (const uint4*)(l + head);
+
+  Stat st = {-FLT_MAX, 0.0f, 0.0f, 0};
+  u64 list = 0;
+  float own = -INFINITY;      // an id has to be above it,
+  float bound = -INFINITY;    // and not below this
+  const int share = (a.top + kWarps - 1) / kWarps;   // entries a warp brings to the bound
+  if (TOP) {
+    if (threadIdx.x < kWarps) s_bound[threadIdx.x] = -INFINITY;
+    __syncthreads();
+  }
+  volatile float* bounds = s_bound;
+
+  // E elements of ids from `id` on
+  auto take = [&](float (&f)[E], int id) {
+    float most = f[0];
+#pragma unroll
+    for (int i = 1; i < E; ++i) most = fmaxf(most, f[i]);   // NaN left out
+    if (most > FLT_MAX) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] = fminf(f[i], FLT_MAX);
+      most = FLT_MAX;
+    }
+    if (most > st.m) rebase(st, most, c);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float d = (fmaxf(f[i], -INFINITY) - st.m) * c, e = ex2(d);
+      st.s += e;
+      st.w = fmaf(fmaxf(d, -FLT_MAX), e, st.w);   // nothing of -inf
+    }
+    if (most >= mine) {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        st.ahead += low ? f[i] > mine && id + i > x : f[i] > mine || (f[i] == mine && id + i < x);
+    }
+    return most;
+  };
+  // the ids of a warp's vectors that may be among the best; all lanes call it
+  auto look = [&](const float (&f)[E], float most, int id) {
+    unsigned lanes = __ballot_sync(kAll, most > own && most >= bound);
+    while (lanes) {
+      const int from = __ffs(lanes) - 1;
+      lanes &= lanes - 1;
+      float v = -INFINITY;   // lane i: element i of lane `from`
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float t = __shfl_sync(kAll, f[i], from);
+        if (lane == i) v = t;
+      }
+      const int first = __shfl_sync(kAll, id, from);
+      unsigned good = __ballot_sync(kAll, v > own && v >= bound);
+      const u64 key = pack_best(v, (uint32_t)(first + lane));
+      while (good) {
+        const int i = __ffs(good) - 1;
+        good &= good - 1;
+        insert(list, __shfl_sync(kAll, key, i), lane);
+      }
+      const u64 last = __shfl_sync(kAll, list, a.top - 1);
+      if (last) own = packed_val(last);
+    }
+  };
+
+  // ids before the first boundary and behind the last vector: one element a lane of warp 0
+  auto ends = [&](int from, int to) {
+    const int id = from + lane;
+    float f[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] = -INFINITY;
+    if (id < to) f[0] = to_f(l[id]);
+    const float most = take(f, id);
+    if (TOP) look(f, most, id);
+  };
+  if (warp == 0 && part == 0 && head > 0) ends(0, head);
+
+  for (int v = v0 + warp * 32; v < v1; v += kThreads * kLoads) {
+    uint4 raw[kLoads];
+    const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int at = v + u * kThreads + lane;
+      raw[u] = at < v1 ? __ldcs(body + at) : make_uint4(none, none, none, none);
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      float f[E];
+      Vec<T>::get(raw[u], f);
+      const int id = head + (v + u * kThreads + lane) * E;
+      const float most = take(f, id);
+      if (TOP) look(f, most, id);
+    }
+    if (TOP) {
+      // every warp has `share` ids at or above its own word: `top` of them are above the least
+      const u64 e = __shfl_sync(kAll, list, share - 1);
+      if (lane == 0 && e) bounds[warp] = packed_val(e);
+      float t = lane < kWarps ? bounds[lane] : INFINITY;
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) t = fminf(t, __shfl_xor_sync(kAll, t, o));
+      bound = fmaxf(bound, __shfl_sync(kAll, t, 0));
+    }
+  }
+  if (warp == 0 && part == a.parts - 1 && head + vectors * E < a.V) ends(head + vectors * E, a.V);
+
+  // the CTA's, in warp 0
+  auto gather = [&]() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      st = join(st, {__shfl_xor_sync(kAll, st.m, o), __shfl_xor_sync(kAll, st.s, o),
+                     __shfl_xor_sync(kAll, st.w, o), __shfl_xor_sync(kAll, st.ahead, o)}, c);
+    if (lane == 0) s_stat[warp] = st;
+    if (TOP) s_best[warp][lane] = list;
+    __syncthreads();
+    if (warp == 0) {
+      st = s_stat[0];
+      for (int w = 1; w < kWarps; ++w) {
+        st = join(st, s_stat[w], c);
+        if (TOP) list = merge(list, s_best[w][lane], lane);
+      }
+    }
+  };
+  gather();
+
+  if (a.parts > 1) {
+    const int64_t at = (int64_t)row * a.parts;
+    if (warp == 0) {
+      if (lane == 0) __stcg(a.stat + at + part, make_float4(st.m, st.s, st.w, __int_as_float(st.ahead)));
+      if (TOP && lane < a.top) __stcg(a.best + (at + part) * a.top + lane, list);
+      __threadfence();
+    }
+    if (!arrive_last(a.tickets + row, a.parts, &s_last)) return;
+    if (threadIdx.x == 0) a.tickets[row] = 0;
+    st = {-FLT_MAX, 0.0f, 0.0f, 0};
+    for (int p = threadIdx.x; p < a.parts; p += kThreads) {
+      const float4 v = __ldcg(a.stat + at + p);
+      st = join(st, {v.x, v.y, v.z, __float_as_int(v.w)}, c);
+    }
+    list = 0;
+    if (TOP)
+      for (int p = warp; p < a.parts; p += kWarps)
+        list = merge(list, lane < a.top ? __ldcg(a.best + (at + p) * a.top + lane) : 0ull, lane);
+    gather();
+  }
+  if (warp != 0) return;
+
+  const float log_s = logf(st.s);   // s = 0: nothing above -inf
+  const int ahead = st.ahead + (low ? (int)x : 0);
+  auto log_p = [&](float v) { return greedy ? -INFINITY : (v - st.m) * inv_t - log_s; };
+  if (lane == 0) {
+    if (!(st.s > 0.0f)) atomicOr(a.err, XP_ERR_EMPTY);
+    if (a.logprob) a.logprob[row] = !(st.s > 0.0f) ? -INFINITY : greedy && ahead == 0 ? 0.0f : log_p(mine);
+    if (a.entropy) a.entropy[row] = greedy || !(st.s > 0.0f) ? 0.0f : log_s - st.w / st.s * 0.693147180559945f;
+    if (a.rank) a.rank[row] = ahead + 1;
+  }
+  if (TOP && lane < a.top) {
+    const int64_t at = (int64_t)row * a.top + lane;
+    if (a.top_ids) a.top_ids[at] = list ? (int64_t)packed_idx(list) : -1;
+    if (a.top_logprobs)
+      a.top_logprobs[at] = !list ? -INFINITY : greedy && lane == 0 ? 0.0f : log_p(packed_val(list));
+  }
+}
+
+}  // namespace
+
+// Tickets of the most rows that are cut (at a place of their own, so that it does not move with the
+// call), then what parts leave: a row is cut so that the CTAs fill the GPU once.
+xp_logprobs_ws xp_logprobs_layout(const xp_head* h, int rows, int top) {
+  (void)rows;
+  const size_t cut = (size_t)h->num_sms * kResident;
+  xp_logprobs_ws L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
+  L.tickets = take(cut * 4);
+  L.stat = take(2 * cut * sizeof(float4));
+  L.best = take(2 * cut * 8 * (size_t)top);
+  L.total = o;
+  return L;
+}
+
+cudaError_t xp_launch_logprobs(const xp_head* h, const xp_logprobs_args& g, cudaStream_t s) {
+  const int es = (int)xp_elem(g.dtype), rows = g.N * g.B, cut = h->num_sms * kResident;
+  Args a;
+  a.logits = g.logits;
+  a.sn = g.sn, a.sb = g.sb;
+  a.tokens = g.tokens, a.temperature = g.temperature;
+  a.B = g.B, a.V = h->V, a.top = g.top;
+  // rows * parts < cut + rows <= 2 cut where there are parts
+  const int most = std::max(1, h->V / (16 / es) / kLeastVectors);
+  a.parts = rows >= cut ? 1 : std::min(most, (cut + rows - 1) / rows);
+  a.logprob = g.logprob, a.entropy = g.entropy, a.rank = g.rank;
+  a.top_ids = g.top_ids, a.top_logprobs = g.top_logprobs;
+  a.err = h->err;
+  a.tickets = g.tickets, a.stat = (float4*)g.stat, a.best = g.best;
+  const unsigned grid = (unsigned)(rows * a.parts);
+  if (g.dtype == XP_BF16) {
+    if (a.top) logprobs_kernel<bf16, true><<<grid, kThreads, 0, s>>>(a);
+    else logprobs_kernel<bf16, false><<<grid, kThreads, 0, s>>>(a);
+  } else {
+    if (a.top) logprobs_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
+    else logprobs_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}

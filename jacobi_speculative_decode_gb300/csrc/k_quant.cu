@@ -1,0 +1,280 @@
+// Rows into a quantised cache, and rows of any cache back out.
+//
+// A CTA takes kTokens tokens of one sequence and finds their pages once; a thread is one piece of a token's
+// row (16 dims of K or V written, 16 bytes of them read) and walks over the tokens, so that nothing is divided
+// inside.  Both are bound by the bytes of the wide rows.
+#include <algorithm>
+
+#include "quant.cuh"
+#include "xp_device.cuh"
+
+using namespace xpd;
+typedef __nv_bfloat16 bf16;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = 16;
+
+struct RowArgs {
+  char *kp, *vp;                // this layer's pools
+  int64_t page, token, head;    // strides: bytes of a quantised pool, elements of another
+  int scale_at, scale;          // quantised: where a head's scales begin, and a token's bytes of them
+  void *k, *v;                  // the dense rows
+  int64_t sn, st, sh;
+  const int32_t* table;
+  int64_t ld, width;
+  const int32_t *lens, *first;
+  int N, T, H, D, ps, pages;
+  uint32_t* err;
+};
+
+// Where the CTA's tokens lie: page id (-1: nowhere) and place in the page.  `len`: the sequence's end.
+struct Places {
+  int page[kTokens], at[kTokens];
+};
+__device__ __forceinline__ void find_pages(const RowArgs& a, int n, int t0, int64_t pos0, int64_t len,
+                                           Places* s) {
+  if (threadIdx.x < kTokens) {
+    const int t = t0 + (int)threadIdx.x;
+    const int64_t pos = pos0 + t;
+    int page = -1, at = 0;
+    if (t < a.T && pos >= 0 && pos < len) {
+      const int64_t col = pos / a.ps;
+      at = (int)(pos - col * a.ps);
+      if (col >= a.width) {
+        atomicOr(a.err, XP_ERR_LENGTH);
+      } else {
+        page = a.table[n * a.ld + col];
+        if (page < 0 || page >= a.pages) {
+          atomicOr(a.err, XP_ERR_BADPAGE);
+          page = -1;
+        }
+      }
+    }
+    s->page[threadIdx.x] = page;
+    s->at[threadIdx.x] = at;
+  }
+  __syncthreads();
+}
+
+// 16 consecutive elements as floats; wide: from 16-byte boundaries
+__device__ __forceinline__ void load16(const float* p, bool wide, float (&x)[16]) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = __ldcs((const float4*)p + i);
+      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = p[i];
+  }
+}
+__device__ __forceinline__ void load16(const bf16* p, bool wide, float (&x)[16]) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = __ldcs((const uint4*)p + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = to_f(p[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Quantised append.
+// ---------------------------------------------------------------------------
+template <int BITS, typename T>
+__global__ void __launch_bounds__(kThreads) append_quant_kernel(const RowArgs a, bool wide) {
+  __shared__ Places s;
+  const int chunks = (a.T + kTokens - 1) / kTokens;
+  const int n = blockIdx.x / chunks, t0 = (int)(blockIdx.x % chunks) * kTokens;
+  find_pages(a, n, t0, (int64_t)a.lens[n] - a.T, INT64_MAX, &s);
+
+  const int groups = a.D / 16, units = 2 * a.H * groups;
+  const int lanes = max(1, kThreads / units);   // tokens at once where a row is short
+  const int lane = units < kThreads ? threadIdx.x / units : 0;
+  if (lane >= lanes) return;
+  for (int u = units < kThreads ? threadIdx.x % units : threadIdx.x; u < units; u += kThreads) {
+    const int g = u % groups, h = u / groups % a.H, is_v = u / groups / a.H;
+    const T* from = (const T*)(is_v ? a.v : a.k) + n * a.sn + h * a.sh + g * 16;
+    char* pool = (is_v ? a.vp : a.kp) + h * a.head;
+#pragma unroll 2
+    for (int i = lane; i < kTokens; i += lanes) {
+      if (s.page[i] < 0) continue;
+      float x[16];
+      load16(from + (t0 + i) * a.st, wide, x);
+      float top = 0.0f;
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        bad |= x[j] != x[j];
+        x[j] = x[j] != x[j] ? 0.0f : x[j];
+        top = fmaxf(top, fabsf(x[j]));
+      }
+      bool over;
+      const unsigned b = xpq::scale_byte<BITS>(top, &over);
+      if (bad || over) atomicOr(a.err, XP_ERR_RANGE);
+      const float step = xpq::scale_of(b);
+      char* head = pool + s.page[i] * a.page;
+      head[a.scale_at + s.at[i] * a.scale + g] = (char)b;
+      if (g == groups - 1)   // the padding behind the scales
+        for (int p = groups; p < a.scale; ++p) head[a.scale_at + s.at[i] * a.scale + p] = 0;
+      uint32_t w[BITS / 2] = {};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t c = xpq::code_of<BITS>(x[j], step) + xpq::Codes<BITS>::kZero;
+        if (BITS == 8) w[j / 4] |= c << j % 4 * 8;
+        else w[j / 8] |= c << (j % 8 / 2 + j % 2 * 4) * 4;
+      }
+      char* to = head + s.at[i] * a.token + g * (2 * BITS);
+      if (BITS == 8) *(uint4*)to = make_uint4(w[0], w[1], w[BITS / 2 - 2], w[BITS / 2 - 1]);
+      else *(uint2*)to = make_uint2(w[0], w[1]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Read back: BITS of a code, or 16 / 32 for a cache of bf16 / fp32.
+// ---------------------------------------------------------------------------
+template <typename T> struct Piece {              // elements of 16 bytes
+  static constexpr int N = 16 / sizeof(T);
+};
+__device__ __forceinline__ void store(float* p, bool wide, const float (&x)[4], int n) {
+  if (wide) {
+    __stcs((float4*)p, make_float4(x[0], x[1], x[2], x[3]));
+  } else {
+    for (int i = 0; i < n; ++i) p[i] = x[i];
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *(const uint32_t*)&v;
+}
+__device__ __forceinline__ void store(bf16* p, bool wide, const float (&x)[8], int n) {
+  if (wide) {
+    __stcs((uint4*)p, make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])));
+  } else {
+    for (int i = 0; i < n; ++i) p[i] = from_f<bf16>(x[i]);
+  }
+}
+
+template <int BITS, typename T>
+__global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wide) {
+  constexpr int E = Piece<T>::N;
+  __shared__ Places s;
+  const int chunks = (a.T + kTokens - 1) / kTokens;
+  const int n = blockIdx.x / chunks, t0 = (int)(blockIdx.x % chunks) * kTokens;
+  find_pages(a, n, t0, a.first ? a.first[n] : 0, a.lens[n], &s);
+
+  const int pieces = (a.D + E - 1) / E, units = 2 * a.H * pieces;
+  const int lanes = max(1, kThreads / units);
+  const int lane = units < kThreads ? threadIdx.x / units : 0;
+  if (lane >= lanes) return;
+  const int count = min(kTokens, a.T - t0);
+  for (int u = units < kThreads ? threadIdx.x % units : threadIdx.x; u < units; u += kThreads) {
+    const int e = u % pieces * E, h = u / pieces % a.H, is_v = u / pieces / a.H;
+    T* to = (T*)(is_v ? a.v : a.k) + n * a.sn + h * a.sh + e;
+    const char* pool = is_v ? a.vp : a.kp;
+    const int live = min(E, a.D - e);
+#pragma unroll 4
+    for (int i = lane; i < count; i += lanes) {
+      float x[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = 0.0f;
+      if (s.page[i] >= 0) {
+        if (BITS <= 8) {
+          const char* head = pool + s.page[i] * a.page + h * a.head;
+          const float step = xpq::scale_of((uint8_t)head[a.scale_at + s.at[i] * a.scale + e / 16]);
+          const uint32_t* code = (const uint32_t*)(head + s.at[i] * a.token + e / 8 * BITS);
+          if (BITS == 4) {   // a word of 8 dims, of which fp32 rows take the first or the last four
+            const uint32_t w = *code >> e % 8 * 2;
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+              x[j] = (float)((int)(w >> (j / 2 + j % 2 * 4) * 4 & 15u) - 8) * step;
+          } else {
+            code += e % 8 / 4;
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+              x[j] = (float)((int)(code[j / 4] >> j % 4 * 8 & 255u) - 128) * step;
+          }
+        } else {
+          const int64_t at = s.page[i] * a.page + s.at[i] * a.token + h * a.head + e;
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (j < live) x[j] = BITS == 16 ? to_f(((const bf16*)pool)[at + j]) : ((const float*)pool)[at + j];
+        }
+      }
+      store(to + (t0 + i) * a.st, wide, x, live);
+    }
+  }
+}
+
+template <typename T> bool wide_rows(const RowArgs& a) {
+  const int64_t strides = a.sn | a.st | a.sh | a.D;
+  return (((uintptr_t)a.k | (uintptr_t)a.v) & 15) == 0 && strides * (int64_t)sizeof(T) % 16 == 0;
+}
+
+RowArgs row_args(const xp_cache* c, int layer, void* k, void* v, int64_t sn, int64_t st, int64_t sh,
+                 const int32_t* table, int64_t ld, int64_t width, const int32_t* lens,
+                 const int32_t* first, int N, int T) {
+  const xp_cache_desc& d = c->d;
+  const int64_t es = (int64_t)xp_elem(d.dtype);
+  RowArgs a = {};
+  a.kp = (char*)d.k + layer * d.stride_layer * es;
+  a.vp = (char*)d.v + layer * d.stride_layer * es;
+  a.page = d.stride_page, a.token = d.stride_token, a.head = d.stride_head;
+  if (xp_is_quant(d.dtype)) {
+    const xp_quant_sizes q = xp_quant_of(d.page_size, d.head_dim, d.dtype);
+    a.scale_at = d.page_size * q.code;
+    a.scale = q.scale;
+  }
+  a.k = k, a.v = v;
+  a.sn = N == 1 ? 0 : sn, a.st = T == 1 ? 0 : st, a.sh = d.kv_heads == 1 ? 0 : sh;   // 0: never used
+  a.table = table, a.ld = ld, a.width = width, a.lens = lens, a.first = first;
+  a.N = N, a.T = T, a.H = d.kv_heads, a.D = d.head_dim, a.ps = d.page_size, a.pages = d.pages;
+  a.err = c->err;
+  return a;
+}
+unsigned row_grid(int N, int T) { return (unsigned)((int64_t)N * ((T + kTokens - 1) / kTokens)); }
+
+template <int BITS> cudaError_t append(const RowArgs& a, xp_dtype rows, cudaStream_t s) {
+  if (rows == XP_BF16) append_quant_kernel<BITS, bf16><<<row_grid(a.N, a.T), kThreads, 0, s>>>(a, wide_rows<bf16>(a));
+  else append_quant_kernel<BITS, float><<<row_grid(a.N, a.T), kThreads, 0, s>>>(a, wide_rows<float>(a));
+  return cudaGetLastError();
+}
+template <int BITS> cudaError_t read(const RowArgs& a, xp_dtype rows, cudaStream_t s) {
+  if (rows == XP_BF16) read_kernel<BITS, bf16><<<row_grid(a.N, a.T), kThreads, 0, s>>>(a, wide_rows<bf16>(a));
+  else read_kernel<BITS, float><<<row_grid(a.N, a.T), kThreads, 0, s>>>(a, wide_rows<float>(a));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t xp_launch_append_quant(const xp_cache* c, int layer, const void* k, const void* v, int64_t sn,
+                                   int64_t st, int64_t sh, xp_dtype rows, const int32_t* table, int64_t ld,
+                                   int64_t width, const int32_t* lens, int N, int T, cudaStream_t s) {
+  const RowArgs a = row_args(c, layer, (void*)k, (void*)v, sn, st, sh, table, ld, width, lens, nullptr, N, T);
+  return c->d.dtype == XP_Q8 ? append<8>(a, rows, s) : append<4>(a, rows, s);
+}
+
+cudaError_t xp_launch_cache_read(const xp_cache* c, int layer, const int32_t* table, int64_t ld,
+                                 int64_t width, const int32_t* lens, const int32_t* first, int N, int T,
+                                 void* k, void* v, int64_t sn, int64_t st, int64_t sh, xp_dtype rows,
+                                 cudaStream_t s) {
+  const RowArgs a = row_args(c, layer, k, v, sn, st, sh, table, ld, width, lens, first, N, T);
+  switch (c->d.dtype) {
+    case XP_BF16: return read<16>(a, rows, s);
+    case XP_F32: return read<32>(a, rows, s);
+    case XP_Q8: return read<8>(a, rows, s);
+    default: return read<4>(a, rows, s);
+  }
+}

@@ -57,7 +57,8 @@ struct xp_ws_layout {
 xp_ws_layout xp_layout(int V, int hidden, int r, int H, int B, int max_N, xp_dtype dt, int N,
                        int C);
 
-static inline size_t xp_elem(xp_dtype d) { return d == XP_BF16 ? 2 : 4; }
+// bytes of an element; of a quantised cache, whose sizes and strides are bytes, 1
+static inline size_t xp_elem(xp_dtype d) { return d == XP_BF16 ? 2 : d == XP_F32 ? 4 : 1; }
 
 // true when the current device is the one the head was created on
 bool xp_on_head_device(const xp_head* h);
@@ -182,6 +183,28 @@ struct xp_verify_args {
 };
 cudaError_t xp_launch_verify(const xp_head* h, const xp_verify_args& a, cudaStream_t s);
 
+// Log probabilities of given tokens.  tickets must be zero between calls.
+struct xp_logprobs_ws {
+  size_t tickets, stat, best, total;
+};
+xp_logprobs_ws xp_logprobs_layout(const xp_head* h, int rows, int top);
+struct xp_logprobs_args {
+  const void* logits;
+  int64_t sn, sb;
+  const int64_t* tokens;
+  const float* temperature;
+  int N, B, top;
+  xp_dtype dtype;
+  float *logprob, *entropy;
+  int32_t* rank;
+  int64_t* top_ids;
+  float* top_logprobs;
+  unsigned* tickets;
+  void* stat;
+  unsigned long long* best;
+};
+cudaError_t xp_launch_logprobs(const xp_head* h, const xp_logprobs_args& a, cudaStream_t s);
+
 // Host-side cache: the caller's pools, the prepared scratch, device facts.
 struct xp_cache {
   xp_cache_desc d;
@@ -199,6 +222,14 @@ struct xp_cache {
 cudaError_t xp_launch_append(const xp_cache* c, int layer, const void* k, const void* v, int64_t sn,
                              int64_t st, int64_t sh, const int32_t* table, int64_t ld,
                              int64_t width, const int32_t* lens, int N, int T, cudaStream_t s);
+// rows: their type, XP_BF16 or XP_F32
+cudaError_t xp_launch_append_quant(const xp_cache* c, int layer, const void* k, const void* v, int64_t sn,
+                                   int64_t st, int64_t sh, xp_dtype rows, const int32_t* table, int64_t ld,
+                                   int64_t width, const int32_t* lens, int N, int T, cudaStream_t s);
+cudaError_t xp_launch_cache_read(const xp_cache* c, int layer, const int32_t* table, int64_t ld,
+                                 int64_t width, const int32_t* lens, const int32_t* first, int N, int T,
+                                 void* k, void* v, int64_t sn, int64_t st, int64_t sh, xp_dtype rows,
+                                 cudaStream_t s);
 // moves given by the caller (n on the host) or left by a table kernel (n_moves on the device);
 // tokens == nullptr copies whole pages
 cudaError_t xp_launch_copy_pages(const xp_cache* c, const int32_t* src, const int32_t* dst,
@@ -242,8 +273,8 @@ struct xp_attn_args {
   int64_t ld_table;
   void* out;
   float* lse;
-  float* stat;                   // CUDA-core form: [parts][N*T*heads][2]
-  float* acc;                    //                 [parts][N*T*heads][dim]
+  float* stat;                   // CUDA-core and quantised forms: [parts][N*T*heads][2]
+  float* acc;                    //                                [parts][N*T*heads][dim]
   int* line;
   uint32_t* err;
   xp_attn_plan plan;
@@ -253,7 +284,10 @@ int xp_attn_tc_maps(xp_cache* c);   // tokens of a TMA box, 0 where the kernel c
 xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a);
 cudaError_t xp_launch_attn_tc(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
-cudaError_t xp_launch_attn_combine(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
+// joins the ranges of either form
+cudaError_t xp_launch_attn_combine(const xp_attn_args& g, cudaStream_t s);
+xp_attn_plan xp_attn_quant_plan(const xp_cache* c, const xp_attn* a);
+cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 
 // Read and clear an error word behind what the stream holds, and wait for both.
 inline cudaError_t xp_take_error(uint32_t* err, cudaStream_t s, uint32_t* word) {

@@ -15,7 +15,7 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libxp.so")
 
-XP_BF16, XP_F32 = 0, 1
+XP_BF16, XP_F32, XP_Q8, XP_Q4 = 0, 1, 2, 3
 XP_PASSES_AUTO, XP_PASSES_PERSISTENT, XP_PASSES_PER_STAGE = 0, 1, 2
 STATUS = {0: "XP_OK", 1: "XP_EINVAL", 2: "XP_ECAPACITY", 3: "XP_ENOTPREPARED", 4: "XP_ECUDA",
           5: "XP_EBADTOKEN", 6: "XP_ETIMEOUT", 7: "XP_EUNSUPPORTED", 8: "XP_ERANGE",
@@ -94,6 +94,11 @@ _SIGS = {
     "xp_verify_workspace_bytes": (_S, [_P, _I]),
     "xp_verify_drafts": (_I, [_P, _P, _I64, _I64, _P, _I64, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I64, _P, _P,
                               _P, _P, _S, _P]),
+    "xp_logprobs_workspace_bytes": (_S, [_P, _I, _I]),
+    "xp_token_logprobs": (_I, [_P, _P, _I64, _I64, _P, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _S,
+                               _P]),
+    "xp_quant_head_bytes": (_S, [_I, _I, _I]),
+    "xp_cache_read": (_I, [_P, _I, _P, _I64, _I, _P, _P, _I, _I, _P, _P, _I64, _I64, _I64, _I, _I, _I, _P]),
     "xp_cache_prep_bytes": (_S, [ctypes.POINTER(xp_cache_desc)]),
     "xp_cache_create": (_I, [ctypes.POINTER(xp_cache_desc), _P, _S, _P, ctypes.POINTER(_P)]),
     "xp_cache_destroy": (None, [_P]),
@@ -401,6 +406,38 @@ def xp_verify_drafts(head, target, draft, blk, n_draft, temperature, u, noise, t
         _ptr(counts), _ptr(prob), _ptr(ws), _nbytes(ws), _stream(stream, device)))
 
 
+def xp_logprobs_workspace_bytes(head, rows: int, top: int) -> int:
+    return lib().xp_logprobs_workspace_bytes(head, rows, top)
+
+
+def xp_token_logprobs(head, logits, tokens, temperature, logprob, entropy, rank, top_ids, top_logprobs, ws,
+                      stream=None):
+    """Log probabilities of tokens [N, B] (-1: none) under logits [N, B, V] at temperature [N] (None: 1).
+    Out, each may be None: logprob, entropy [N, B], rank [N, B] int32, top_ids int64 and top_logprobs
+    [N, B, top], top up to 32."""
+    import torch
+    N, B, V = logits.shape
+    f32, i64, i32 = torch.float32, torch.int64, torch.int32
+    device = _here("logits tokens temperature logprob entropy rank top_ids top_logprobs ws", logits, tokens,
+                   temperature, logprob, entropy, rank, top_ids, top_logprobs, ws)
+    sn, sb, sv = logits.stride()
+    _want(sv == 1, "logits: [N, B, V] with unit stride over V")
+    tops = {t.shape[-1] for t in (top_ids, top_logprobs) if t is not None}
+    _want(all(t is None or t.shape[:-1] == (N, B) for t in (top_ids, top_logprobs)) and len(tops) < 2,
+          "top_ids, top_logprobs: [N, B, top]")
+    top = tops.pop() if tops else 0
+    for name, t, dt, count in (("tokens", tokens, i64, N * B), ("temperature", temperature, f32, N),
+                               ("logprob", logprob, f32, N * B), ("entropy", entropy, f32, N * B),
+                               ("rank", rank, i32, N * B), ("top_ids", top_ids, i64, N * B * top),
+                               ("top_logprobs", top_logprobs, f32, N * B * top)):
+        if t is not None and not (t.dtype == dt and t.is_contiguous() and t.numel() >= count):
+            raise ValueError(f"{name}: contiguous {dt} of at least {count} elements")
+    _check("xp_token_logprobs", lib().xp_token_logprobs(
+        head, _ptr(logits), sn, sb, _ptr(tokens), N, B, V, _code("logits", logits), _ptr(temperature), top,
+        _ptr(logprob), _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top_logprobs), _ptr(ws), _nbytes(ws),
+        _stream(stream, device)))
+
+
 def make_cache_desc(k, v, max_seqs: int = 4096) -> xp_cache_desc:
     """Descriptor of K and V pools seen as [layers, pages, page_size, kv_heads, head_dim] (views
     with the heads outside the tokens too)."""
@@ -412,6 +449,31 @@ def make_cache_desc(k, v, max_seqs: int = 4096) -> xp_cache_desc:
     layers, pages, ps, heads, dim = k.shape
     return xp_cache_desc(pages, ps, layers, heads, dim, max_seqs, _code("k", k), k.stride(0),
                          k.stride(1), k.stride(2), k.stride(3), _ptr(k), _ptr(v))
+
+
+def xp_quant_head_bytes(page_size: int, head_dim: int, bits: int) -> int:
+    """Bytes of one head of a page of a cache of 8 or 4 bits (0: sizes it cannot have)."""
+    return lib().xp_quant_head_bytes(page_size, head_dim, _bits(bits))
+
+
+def _bits(bits: int) -> int:
+    _want(bits in (4, 8), "bits: 8 or 4")
+    return XP_Q8 if bits == 8 else XP_Q4
+
+
+def make_quant_cache_desc(k, v, page_size: int, head_dim: int, bits: int, max_seqs: int = 4096) -> xp_cache_desc:
+    """Descriptor of K and V pools of 8 or 4 bits: uint8 [layers, pages, kv_heads, xp_quant_head_bytes]."""
+    import torch
+    _here("k v", k, v)
+    size = xp_quant_head_bytes(page_size, head_dim, bits)
+    _want(size > 0, "page_size: positive; head_dim: a multiple of 16 up to 256")
+    _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride()
+          and k.dtype == v.dtype == torch.uint8 and k.shape[3] == size and k.stride(3) == 1
+          and (k.shape[2] == 1 or k.stride(2) == size),
+          f"k, v: uint8 tensors [layers, pages, kv_heads, {size}] of the same strides, a page's heads dense")
+    layers, pages, heads, _ = k.shape
+    return xp_cache_desc(pages, page_size, layers, heads, head_dim, max_seqs, _bits(bits), k.stride(0),
+                         k.stride(1), head_dim * bits // 8, size, _ptr(k), _ptr(v))
 
 
 def xp_cache_prep_bytes(d: xp_cache_desc) -> int:
@@ -448,6 +510,21 @@ def xp_cache_append(cache, layer, k, v, table, lens, stream=None):
         cache, layer, _ptr(k), _ptr(v), *k.stride()[:3], k.shape[2], k.shape[3],
         _code("k", k), _ptr(table), ld, table.shape[1], _ptr(lens), N, T,
         _stream(stream, device)))
+
+
+def xp_cache_read(cache, layer, table, lens, first, k, v, stream=None):
+    """Read back T positions of every row into k, v [N, T, kv_heads, head_dim] (bf16 or fp32, whatever the
+    cache's type), from position first[n] on (None: 0); zeros where a position is not in [0, lens[n])."""
+    N, T = k.shape[:2]
+    device = _here("table lens first k v", table, lens, first, k, v)
+    _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
+          and k.stride(3) == 1, "k, v: [N, T, kv_heads, head_dim] of the same strides")
+    ld = _table("table", table, N)
+    _ints("lens", lens, N)
+    _ints("first", first, N)
+    _check("xp_cache_read", lib().xp_cache_read(
+        cache, layer, _ptr(table), ld, table.shape[1], _ptr(lens), _ptr(first), N, T, _ptr(k), _ptr(v),
+        *k.stride()[:3], k.shape[2], k.shape[3], _code("k", k), _stream(stream, device)))
 
 
 def xp_cache_copy(cache, src, dst, stream=None):
@@ -597,6 +674,11 @@ class Head:
         w = self.weights_struct()
         return torch.zeros(xp_workspace_bytes(w, N, topc), dtype=torch.uint8, device="cuda")
 
+    def logprobs_workspace(self, rows: int, top: int):
+        import torch
+        return torch.zeros(xp_logprobs_workspace_bytes(self.handle, rows, top), dtype=torch.uint8,
+                           device="cuda")
+
     def verify_workspace(self, N: int):
         import torch
         return torch.zeros(xp_verify_workspace_bytes(self.handle, N), dtype=torch.uint8,
@@ -619,10 +701,12 @@ class Cache:
     head_dim] (kept alive here), with its prepared scratch and handle."""
 
     def __init__(self, k, v, max_seqs: int = 4096, stream=None):
-        import torch
         self.handle = None
+        self._create(k, v, make_cache_desc(k, v, max_seqs), stream)
+
+    def _create(self, k, v, desc, stream):
+        import torch
         self.k, self.v = k, v
-        desc = make_cache_desc(k, v, max_seqs)
         self.prep = torch.empty(max(256, xp_cache_prep_bytes(desc)), dtype=torch.uint8,
                                 device=k.device)
         self.handle = xp_cache_create(desc, self.prep, stream)
@@ -642,6 +726,22 @@ class Cache:
             self.close()
         except Exception:
             pass
+
+
+class QuantCache(Cache):
+    """A paged cache held in 8 or 4 bits over the caller's K and V pools, uint8 [layers, pages, kv_heads,
+    xp_quant_head_bytes] (`pool` makes one).  Every call on caches takes it."""
+
+    def __init__(self, k, v, page_size: int, head_dim: int, bits: int, max_seqs: int = 4096, stream=None):
+        self.handle = None
+        self._create(k, v, make_quant_cache_desc(k, v, page_size, head_dim, bits, max_seqs), stream)
+
+    @staticmethod
+    def pool(layers: int, pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int):
+        import torch
+        size = xp_quant_head_bytes(page_size, head_dim, bits)
+        _want(size > 0, "page_size: positive; head_dim: a multiple of 16 up to 256")
+        return torch.empty(layers, pages, kv_heads, size, dtype=torch.uint8, device="cuda")
 
 
 def head_from_inputs(inp: dict, wl, max_N: int | None = None, stream=None):
