@@ -97,14 +97,16 @@ bool valid_attn(const xp_cache* c, const xp_attn* a) {
 }
 
 xp_attn_plan attn_plan(const xp_cache* c, const xp_attn* a) {
-  if (c->attn_tc) {
+  const bool quant = xp_is_quant(c->d.dtype);
+  if (c->attn_tc && !quant) {
     const xp_attn_plan tc = xp_attn_tc_plan(c, a);
     if (tc.total) return tc;   // 0: more work than its line can count
   }
-  xp_attn_plan p = xp_is_quant(c->d.dtype) ? xp_attn_quant_plan(c, a) : xp_attn_simt_plan(c, a);
+  xp_attn_plan p = quant ? xp_attn_quant_plan(c, a) : xp_attn_simt_plan(c, a);
+  if (p.tc) return p;   // quantised, and widened whole
   const size_t rows = (size_t)a->N * a->T * a->heads;
-  p.stat_off = 0;
-  p.acc_off = align_up(rows * p.parts * 8);
+  p.stat_off = p.total;   // behind what the quantised form has taken
+  p.acc_off = p.stat_off + align_up(rows * p.parts * 8);
   p.total = p.acc_off + align_up(rows * p.parts * c->d.head_dim * 4);
   return p;
 }
@@ -352,13 +354,15 @@ xp_status xp_prefix_attention(const xp_cache* c, const xp_attn* a, const void* q
   g.stat = (float*)((char*)ws + plan.stat_off);
   g.acc = (float*)((char*)ws + plan.acc_off);
   g.line = (int*)((char*)ws + plan.line_off);
+  g.q_factor = nullptr;
+  g.part_stat = g.part_acc = nullptr;
+  g.ws = (char*)ws;
   g.err = c->err;
   g.plan = plan;
+  if (xp_is_quant(c->d.dtype)) return cuda_status(xp_launch_attn_quant(c, g, stream));
   if (plan.tc) return cuda_status(xp_launch_attn_tc(c, g, stream));
-  const bool quant = xp_is_quant(c->d.dtype);
-  cudaError_t e = quant ? xp_launch_attn_quant(c, g, stream) : xp_launch_attn_simt(c, g, stream);
-  // one range a row of the quantised form is written out by its kernel
-  if (e == cudaSuccess && !(quant && plan.parts == 1)) e = xp_launch_attn_combine(g, stream);
+  cudaError_t e = xp_launch_attn_simt(c, g, stream);
+  if (e == cudaSuccess) e = xp_launch_attn_combine(g, stream);
   return cuda_status(e);
 }
 

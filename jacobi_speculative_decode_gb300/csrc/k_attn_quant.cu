@@ -275,9 +275,8 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
     }
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-    // 2^e, 2^-e: e the exponent of the largest (0 for a row of zeros; what is not finite stays so)
-    const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253);
-    const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
+    float up;
+    const float down = xpq::row_scale(top, &up);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {   // of a k step: dims 4 i.. of the lane's
       const uint32_t b0 = pack(x[4 * i] * down, x[4 * i + 1] * down);
@@ -285,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
       if constexpr (QREGS) qr[q][2 * i] = b0, qr[q][2 * i + 1] = b1;
       else if (warp == 0) sq[(q * KS + i) * 32 + lane] = make_uint2(b0, b1);
     }
-    const float c = top > 0.0f ? fminf(g.a.scale * 1.44269504088896f * up, 3.0e38f) : 0.0f;
+    const float c = xpq::row_factor(up, g.a.scale * 1.44269504088896f);
     const int lim = !is_row ? k1 : min(k1, prefix ? keys : keys - g.a.T + rt + 1);
     least = min(least, lim);
 #pragma unroll
@@ -564,34 +563,136 @@ template <int BITS> cudaError_t launch_dims(const xp_attn_args& g, const Quant& 
 
 }  // namespace
 
+// Many queries of each key are the tensor cores' work, not that of widening: from so many of a kv head on,
+// what they see is widened to fp16 in the workspace once (exactly, as here) and attended over on tcgen05.
+constexpr int kWidePrefixRows = 256, kWideTailRows = 64;
+constexpr size_t kWideTailBytes = (size_t)1 << 30;   // of tails that may be widened
+
+// The cache that the widened tokens are: heads outside, one layer.  False where its maps cannot be made.
+static bool wide_cache(const xp_cache* c, const xp_attn_plan& p, int64_t pages, char* ws, xp_cache* w) {
+  const int D = c->d.head_dim;
+  *w = *c;
+  w->d.dtype = XP_BF16;
+  w->d.pages = (int)pages;
+  w->d.page_size = kWidePage;
+  w->d.layers = 1;
+  w->d.stride_token = D;
+  w->d.stride_page = (int64_t)kWidePage * D;
+  w->d.stride_head = p.wide_plane;
+  w->d.stride_layer = w->d.stride_head * c->d.kv_heads;
+  w->d.k = ws + p.wide_k;
+  w->d.v = ws + p.wide_v;
+  w->heads_outside = true;
+  w->attn_tc = xp_attn_tc_maps(w);
+  return w->attn_tc != 0;
+}
+// the call that the tcgen05 form does: all of it, or the prefix alone
+static xp_attn wide_call(const xp_attn& a, const xp_attn_plan& p) {
+  xp_attn w = a;
+  w.layer = 0;
+  if (!p.tc) w.max_len = 0;
+  return w;
+}
+
 // Row tiles of 8, 16 or 32 queries (heads wider than 128: 8 or 16, their results fill the registers): the
 // least that hold a sequence's rows of one kv head, or where there is a prefix the batch's.  Key ranges of
 // whole rounds of the four warps, so that the units fill the GPU about four times over.
 xp_attn_plan xp_attn_quant_plan(const xp_cache* c, const xp_attn* a) {
   xp_attn_plan p = {};
-  const int group = a->heads / c->d.kv_heads, per_seq = a->T * group;
-  const int64_t seen = (int64_t)per_seq * (a->prefix_len > 0 ? a->N : 1);
-  p.rows_tile = seen <= 8 ? 8 : seen <= 16 || a->head_dim > 128 ? 16 : 32;
+  const int group = a->heads / c->d.kv_heads, per_seq = a->T * group, D = c->d.head_dim;
+  auto pages = [](int keys) { return (keys + kWidePage - 1) / kWidePage; };
+  const size_t page_bytes = (size_t)kWidePage * c->d.kv_heads * D * 4;
+  const bool prefix = c->attn_tc && a->prefix_len > 0 && (int64_t)a->N * per_seq >= kWidePrefixRows;
+  const bool tails = c->attn_tc && a->max_len > 0 && per_seq >= kWideTailRows &&
+                     (prefix || a->prefix_len == 0) &&
+                     (size_t)a->N * pages(a->max_len) * page_bytes <= kWideTailBytes;
+  if (prefix || tails) {
+    p.wide_prefix = prefix ? pages(a->prefix_len) : 0;
+    p.wide_tail = tails ? pages(a->max_len) : 0;
+    p.tc = (prefix || a->prefix_len == 0) && (tails || a->max_len == 0);
+    const int64_t count = p.wide_prefix + (int64_t)a->N * p.wide_tail;
+    p.wide_plane = count * kWidePage * D;
+    size_t o = 0;
+    auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
+    p.wide_k = take(count * page_bytes / 2);
+    p.wide_v = take(count * page_bytes / 2);
+    p.wide_table = take(count * 4);
+    p.wide_q = take((size_t)a->N * a->T * a->heads * D * 2);
+    p.wide_factor = take((size_t)a->N * a->T * a->heads * 4);
+    const xp_attn w = wide_call(*a, p);
+    const xp_attn_plan tc = xp_attn_tc_plan(c, &w);
+    if (tc.total && count < INT_MAX / kWidePage) {
+      const size_t at = take(tc.total);
+      p.wide_line = at + tc.line_off;
+      p.wide_stat = at + tc.stat_off;
+      p.wide_acc = at + tc.acc_off;
+      p.total = o;
+      if (p.tc) return p;
+    } else {
+      p = {};   // more work than the tcgen05 form's line can count
+    }
+  }
+
+  // what is not widened
+  const int prefix_len = p.wide_prefix ? 0 : a->prefix_len;
+  const int64_t seen = (int64_t)per_seq * (prefix_len > 0 ? a->N : 1);
+  p.rows_tile = seen <= 8 ? 8 : seen <= 16 || D > 128 ? 16 : 32;
   const int round = kWarps * kStep;
-  p.prefix_tiles = (int)(((int64_t)a->N * per_seq + p.rows_tile - 1) / p.rows_tile);
+  p.prefix_tiles = p.wide_prefix ? 0 : (int)(((int64_t)a->N * per_seq + p.rows_tile - 1) / p.rows_tile);
   p.tail_tiles = (per_seq + p.rows_tile - 1) / p.rows_tile;
   auto rounds = [&](int keys) { return ((int64_t)keys + round - 1) / round; };
-  const int64_t all = (p.prefix_tiles * rounds(a->prefix_len) +
+  const int64_t all = (p.prefix_tiles * rounds(prefix_len) +
                        (int64_t)a->N * p.tail_tiles * rounds(a->max_len)) * c->d.kv_heads;
   const int64_t want = (int64_t)c->num_sms * 16, each = std::max<int64_t>(1, (all + want - 1) / want);
   auto splits = [&](int keys, int* range) {
     *range = (int)(std::min<int64_t>(each, std::max<int64_t>(1, rounds(keys))) * round);
     return keys > 0 ? (keys - 1) / *range + 1 : 0;
   };
-  p.prefix_splits = splits(a->prefix_len, &p.prefix_keys);
+  p.prefix_splits = p.wide_prefix ? 1 : splits(prefix_len, &p.prefix_keys);   // 1: what tcgen05 leaves
   p.tail_splits = splits(a->max_len, &p.tail_keys);
   p.parts = p.prefix_splits + p.tail_splits;
   return p;
 }
 
 cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
-  if (g.plan.parts == 0) return cudaSuccess;
+  const xp_attn_plan& p = g.plan;
+  if (p.wide_prefix || p.wide_tail) {
+    const int64_t count = p.wide_prefix + (int64_t)g.a.N * p.wide_tail;
+    xp_cache wide;
+    if (!wide_cache(c, p, count, g.ws, &wide)) return cudaErrorInvalidValue;
+    int32_t* table = (int32_t*)(g.ws + p.wide_table);
+    cudaError_t e = xp_launch_widen(c, g, p.wide_prefix, p.wide_tail, wide.d.k, wide.d.v, p.wide_plane, table,
+                                    g.ws + p.wide_q, (float*)(g.ws + p.wide_factor), s);
+    if (e != cudaSuccess) return e;
+    xp_attn_args w = g;
+    w.a = wide_call(g.a, p);
+    w.q = g.ws + p.wide_q;
+    w.q_factor = (float*)(g.ws + p.wide_factor);
+    w.a.q_stride_h = g.dim;
+    w.a.q_stride_t = (int64_t)g.a.heads * g.dim;
+    w.a.q_stride_n = g.a.T * w.a.q_stride_t;
+    w.page_size = kWidePage;
+    w.pages = (int)count;
+    w.k = wide.d.k;
+    w.v = wide.d.v;
+    w.kv_page = wide.d.stride_page;
+    w.kv_token = wide.d.stride_token;
+    w.kv_head = wide.d.stride_head;
+    w.prefix_table = table;
+    w.table = table + p.wide_prefix;
+    w.ld_table = p.wide_tail;
+    w.plan = xp_attn_tc_plan(c, &w.a);
+    w.line = (int*)(g.ws + p.wide_line);
+    w.stat = (float*)(g.ws + p.wide_stat);
+    w.acc = (float*)(g.ws + p.wide_acc);
+    if (!p.tc) w.part_stat = g.stat, w.part_acc = g.acc;   // the first range
+    e = xp_launch_attn_tc(&wide, w, s);
+    if (e != cudaSuccess || p.tc) return e;
+  }
   const xp_quant_sizes q = xp_quant_of(c->d.page_size, c->d.head_dim, c->d.dtype);
   const Quant z = {q.code, q.scale, c->d.page_size * q.code};
-  return c->d.dtype == XP_Q8 ? launch_dims<8>(g, z, s) : launch_dims<4>(g, z, s);
+  cudaError_t e = cudaSuccess;
+  if (p.parts > (p.wide_prefix ? 1 : 0)) e = c->d.dtype == XP_Q8 ? launch_dims<8>(g, z, s) : launch_dims<4>(g, z, s);
+  // a row of one range is written out by that kernel
+  return e == cudaSuccess && p.parts != 1 ? xp_launch_attn_combine(g, s) : e;
 }

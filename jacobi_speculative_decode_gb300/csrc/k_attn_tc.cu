@@ -42,6 +42,7 @@
 
 #include <algorithm>
 
+#include "quant.cuh"
 #include "sm100_ptx.cuh"
 #include "xp_device.cuh"
 
@@ -57,6 +58,7 @@ constexpr int kRegsIssue = 64, kRegsSoftmax = 104;
 constexpr int kChunkBytes = kTile * 128;   // 64 elements of 128 rows, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;   // growth of the maximum (base 2) that P may carry
+constexpr float kLift = 6.0f;   // fp16 weights are 2^(z - m + kLift): at most 2^14, and small ones kept longer
 
 template <int D>
 struct Cfg {
@@ -164,6 +166,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -269,7 +276,9 @@ __device__ int plan_line(const xp_attn_args& g, Bars* bars) {
   return x < all ? chunk : 0;
 }
 
-template <int D>
+// F16: queries, keys and values are fp16 (what a quantised cache's call has widened), and every query row
+// has a factor of its own.
+template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ CUtensorMap tm_q, const xp_attn_args g, int box, bool q_tma,
@@ -524,8 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the products of stream t: O += P V of its item j, then S = Q K^T of item j + 1 in
       // its place.  The warp runs the loop converged, so that descriptors stay in uniform
       // registers, and a warp a stream, so that one's waits run under the other's products ----
-      constexpr uint32_t kS = ptx::idesc_bf16_f32(kRows, kTile);
-      constexpr uint32_t kO = ptx::idesc_bf16_f32(kRows, D) | (1u << 16);   // V: head dims contiguous
+      constexpr uint32_t kS = F16 ? ptx::idesc_f16_f32(kRows, kTile) : ptx::idesc_bf16_f32(kRows, kTile);
+      constexpr uint32_t kO =   // V: head dims contiguous
+          (F16 ? ptx::idesc_f16_f32(kRows, D) : ptx::idesc_bf16_f32(kRows, D)) | (1u << 16);
       const int t = warp - 16;
       const uint32_t s_col = uniform(tmem + t * kTile), o_col = uniform(tmem + 2 * kTile + t * D);
       const bool leader = ptx::elect_one();
@@ -647,7 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp / 8, quad = lane % 4;
     const int r0 = warp % 4 * 32 + warp / 4 % 2 * 16 + lane / 4;      // and r0 + 8
     const uint32_t lanes = (uint32_t)(r0 - lane / 4) << 16;
-    const float c = g.a.scale * 1.44269504088896f;
+    float c[2];
+    c[0] = c[1] = g.a.scale * 1.44269504088896f;
     const int all_rows = g.a.N * g.a.T * g.group, RT = g.plan.rows_tile;
     int done = 0, known = -1, token[2] = {0, 0};   // the rows' tokens in a tail's row tile `known`
     Frag w;
@@ -671,6 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool is_row = r0 + 8 * i < RT && (w.kind == 0 ? tile * RT + r0 + 8 * i < all_rows : token[i] < g.a.T);
         limit[i] = is_row && w.kind == 1 ? min(w.len - g.a.T + token[i] + 1, end) : end;
         any_row |= is_row;   // rows behind the end ask for no mask
+        if constexpr (F16) {
+          const int64_t row = (int64_t)hk * all_rows + (w.kind == 0 ? 0 : w.n * g.a.T * g.group) + tile * RT + r0 + 8 * i;
+          c[i] = is_row ? g.q_factor[row] : 0.0f;
+        }
       }
       const bool active = __any_sync(0xFFFFFFFFu, any_row);
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // l: of this thread's columns
@@ -702,18 +717,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // The first half's weights are computed with the maximum as it was: it rarely grows by
         // more than P may carry, and neither has to wait for the other.
-        const uint64_t c2 = pair(c, c);
+        const uint64_t c2[2] = {pair(c[0], c[0]), pair(c[1], c[1])};
         uint64_t sum[2];
         uint32_t pk[16];
         auto weights = [&](int q) {   // row x % 2, columns 8 (x / 2) + 2 quad
-          const float b0 = m[0] == -INFINITY ? 0.0f : m[0] * c, b1 = m[1] == -INFINITY ? 0.0f : m[1] * c;
+          constexpr float lift = F16 ? kLift : 0.0f;
+          const float b0 = (m[0] == -INFINITY ? 0.0f : m[0] * c[0]) - lift;
+          const float b1 = (m[1] == -INFINITY ? 0.0f : m[1] * c[1]) - lift;
           const uint64_t nb[2] = {pair(-b0, -b0), pair(-b1, -b1)};
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2, nb[x % 2]);
+            const uint64_t z = fma2(pair(s[q][2 * x], s[q][2 * x + 1]), c2[x % 2], nb[x % 2]);
             const float a = ex2(low(z)), b = ex2(high(z));
             sum[x % 2] = add2(sum[x % 2], pair(a, b));
-            pk[x] = pack_bf16(a, b);
+            pk[x] = F16 ? pack_f16(a, b) : pack_bf16(a, b);
           }
         };
         sum[0] = sum[1] = 0;
@@ -739,15 +756,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             now[i] = fmaxf(now[i], __shfl_xor_sync(0xFFFFFFFFu, now[i], o));
         now[0] = fmaxf(now[0], m[0]);
         now[1] = fmaxf(now[1], m[1]);
-        const bool grown0 = j == 0 || (now[0] - m[0]) * c > kLazy;   // from -inf too
-        const bool grown1 = j == 0 || (now[1] - m[1]) * c > kLazy;
+        const bool grown0 = j == 0 || (now[0] - m[0]) * c[0] > kLazy;   // from -inf too
+        const bool grown1 = j == 0 || (now[1] - m[1]) * c[1] > kLazy;
         if (__any_sync(0xFFFFFFFFu, grown0 || grown1)) {
           if (j > 0) {
             ok = wait(&bars->o_full[t], done + j - 1);
             if (!ok) break;
             ptx::tc_fence_after();
-            const float f0 = grown0 ? ex2((m[0] - now[0]) * c) : 1.0f;
-            const float f1 = grown1 ? ex2((m[1] - now[1]) * c) : 1.0f;
+            const float f0 = grown0 ? ex2((m[0] - now[0]) * c[0]) : 1.0f;
+            const float f1 = grown1 ? ex2((m[1] - now[1]) * c[1]) : 1.0f;
             const uint32_t ocol = tmem + lanes + 2 * kTile + t * D;
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -802,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           ((float2*)g.stat)[block * 32 + rb + 8 * i] =
-              make_float2(l[i] > 0.0f ? m[i] * c : -INFINITY, l[i]);
+              make_float2(l[i] > 0.0f ? m[i] * c[i] - (F16 ? kLift : 0.0f) : -INFINITY, l[i]);
       __syncwarp();
       float* acc = g.acc + block * D * 32 + (quad / 2 * 32 + rb) * 4 + quad % 2 * 2;
 #pragma unroll
@@ -963,7 +980,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
       float all = 0.0f;
 #pragma unroll
       for (int c = 0; c < kPer; ++c) all += o[c].x + o[c].y + o[c].z + o[c].w;
-      if (all != all && l == l && g.a.T > 1) {
+      if (all != all && l == l && g.a.T > 1 && !g.q_factor) {   // values of fp16 are all finite
         const unsigned whole = nans();
         m = -INFINITY, l = 0.0f;
 #pragma unroll
@@ -983,15 +1000,22 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
         }
       }
     }
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // NaN where a visible score is
+    if (g.part_acc) {   // one range of a larger call: the rows are joined again
+      const int64_t row = ((int64_t)n * g.a.T + t) * g.a.heads + h;
+      if (warp == 0) ((float2*)g.part_stat)[row] = make_float2(m, l);
 #pragma unroll
-    for (int c = 0; c < kPer; ++c)
-      s_out[lane][warp + 8 * c] = make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv),
-                                             pack_bf16(o[c].z * inv, o[c].w * inv));
-    to = (bf16*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h;
-    if (warp == 0 && g.lse)
-      g.lse[((int64_t)n * g.a.T + t) * g.a.heads + h] =
-          l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+      for (int c = 0; c < kPer; ++c) ((float4*)g.part_acc)[row * (D / 4) + warp + 8 * c] = o[c];
+    } else {
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // NaN where a visible score is
+#pragma unroll
+      for (int c = 0; c < kPer; ++c)
+        s_out[lane][warp + 8 * c] = make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv),
+                                               pack_bf16(o[c].z * inv, o[c].w * inv));
+      to = (bf16*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h;
+      if (warp == 0 && g.lse)
+        g.lse[((int64_t)n * g.a.T + t) * g.a.heads + h] =
+            l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+    }
   }
   if (warp == 0) s_to[lane] = to;
   __syncthreads();
@@ -1010,11 +1034,11 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
   }
 }
 
-template <int D>
+template <int D, bool F16>
 cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   const size_t smem = Cfg<D>::SMEM + sizeof(Bars);
   static unsigned long long allowed = 0;
-  cudaError_t e = xp_allow_smem((const void*)attn_tc_kernel<D>, smem, &allowed);
+  cudaError_t e = xp_allow_smem((const void*)attn_tc_kernel<D, F16>, smem, &allowed);
   if (e != cudaSuccess) return e;
   // Queries by TMA where a tile is a whole number of tokens, one stride apart; else by loads.
   CUtensorMap tm_q = {};
@@ -1039,7 +1063,7 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   }
-  attn_tc_kernel<D><<<c->num_sms, kThreads, smem, s>>>(c->tm_k, c->tm_v, tm_q, g, c->attn_tc, q_tma, q_wide);
+  attn_tc_kernel<D, F16><<<c->num_sms, kThreads, smem, s>>>(c->tm_k, c->tm_v, tm_q, g, c->attn_tc, q_tma, q_wide);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
@@ -1055,13 +1079,15 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
 // keys are a whole number of boxes.  0 where the shapes do not allow it.
 int xp_attn_tc_maps(xp_cache* c) {
   const xp_cache_desc& d = c->d;
-  if (d.dtype != XP_BF16 || (d.head_dim != 64 && d.head_dim != 128) || d.page_size % 8 != 0 ||
-      !xp_get_encode_tiled())
+  const bool quant = xp_is_quant(d.dtype);   // the maps are those of what a call widens
+  if ((d.dtype != XP_BF16 && !quant) || (d.head_dim != 64 && d.head_dim != 128) ||
+      (d.page_size % 8 != 0 && !quant) || !xp_get_encode_tiled())
     return 0;
   int major = 0, minor = 0;
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, c->device);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, c->device);
   if (major != 10 || minor != 3) return 0;
+  if (quant) return kWidePage;
   int box = 8;
   while (box < 128 && d.page_size % (box * 2) == 0) box *= 2;
   const cuuint64_t dims[5] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size,
@@ -1124,5 +1150,6 @@ xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a) {
 }
 
 cudaError_t xp_launch_attn_tc(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
-  return g.dim == 128 ? launch<128>(c, g, s) : launch<64>(c, g, s);
+  if (g.q_factor) return g.dim == 128 ? launch<128, true>(c, g, s) : launch<64, true>(c, g, s);
+  return g.dim == 128 ? launch<128, false>(c, g, s) : launch<64, false>(c, g, s);
 }

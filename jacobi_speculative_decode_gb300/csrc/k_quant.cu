@@ -218,6 +218,115 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
   }
 }
 
+// ---------------------------------------------------------------------------
+// A quantised cache's tokens as fp16 (exactly) for attention on tcgen05, which many queries of each key are
+// better done by: pools [head][page of kWidePage tokens][dim] and the table that names their pages in order.
+// Behind a sequence's end its last page is zeros.  A CTA is 64 tokens of a head.  The CTAs behind the pages'
+// make the queries fp16, a warp a row, scaled by the power of two that brings the row's largest into [1, 4).
+// ---------------------------------------------------------------------------
+constexpr int kWideTokens = 64;
+struct WidenArgs {
+  RowArgs r;                      // r.table, r.ld, r.lens: the tails'
+  const int32_t* prefix_table;
+  int prefix, prefix_pages, tail_pages, max_len;   // tokens; pages of it and of a tail; longest tail
+  int64_t plane;                  // elements of a head in either pool
+  int32_t* table;                 // [prefix_pages], then [N][tail_pages]
+  int page_ctas;
+  const bf16* q;
+  int64_t q_n, q_t, q_h;
+  int T, heads, group;
+  float scale;                    // of the scores, to base 2
+  __half* q_out;                  // [N][T][heads][dim]
+  float* q_factor;                // [kv heads][N][T][group]
+};
+
+__device__ __forceinline__ void widen_queries(const WidenArgs& w) {
+  const int64_t rows = (int64_t)w.r.N * w.T * w.heads;
+  const int64_t cta = ((int64_t)blockIdx.x - w.page_ctas) * gridDim.y + blockIdx.y;
+  const int64_t row = cta * (kThreads / 32) + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, D = w.r.D;
+  if (row >= rows) return;
+  const int h = (int)(row % w.heads), t = (int)(row / w.heads % w.T), n = (int)(row / w.heads / w.T);
+  const bf16* q = w.q + n * w.q_n + t * w.q_t + h * w.q_h;
+  float x[4], top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int d = lane * 2 + i % 2 + i / 2 * 64;
+    x[i] = d < D ? to_f(q[d]) : 0.0f;
+    top = fmaxf(top, fabsf(x[i]));
+  }
+  top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
+  float up;
+  const float down = xpq::row_scale(top, &up);
+#pragma unroll
+  for (int i = 0; i < 4; i += 2)
+    if (i * 32 < D)
+      *(__half2*)(w.q_out + row * D + lane * 2 + i * 32) = __floats2half2_rn(x[i] * down, x[i + 1] * down);
+  if (lane == 0) {
+    const int64_t per_head = (int64_t)w.r.N * w.T * w.group;
+    w.q_factor[h / w.group * per_head + ((int64_t)n * w.T + t) * w.group + h % w.group] =
+        xpq::row_factor(up, w.scale);
+  }
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ WidenArgs w) {
+  __shared__ int s_page[kWideTokens], s_at[kWideTokens];
+  const RowArgs& a = w.r;
+  if ((int)blockIdx.x >= w.page_ctas) return widen_queries(w);
+  constexpr int per = kWidePage / kWideTokens;
+  const int page = blockIdx.x / per, t0 = (int)(blockIdx.x % per) * kWideTokens, h = blockIdx.y;
+  const int tail = page - w.prefix_pages, n = tail < 0 ? 0 : tail / w.tail_pages;
+  const int32_t* table = tail < 0 ? w.prefix_table : a.table + n * a.ld;
+  int len = tail < 0 ? w.prefix : a.lens[n];
+  if (tail >= 0 && (len < 0 || len > w.max_len)) len = len < 0 ? 0 : w.max_len;   // told by the attention
+  const int pos0 = (tail < 0 ? page : tail % w.tail_pages) * kWidePage;
+  if (pos0 >= len) return;
+  if (h == 0 && t0 == 0 && threadIdx.x == 0) w.table[page] = page;
+  if (threadIdx.x < kWideTokens) {
+    const int pos = pos0 + t0 + (int)threadIdx.x;
+    int p = -1, at = 0;
+    if (pos < len) {
+      const int col = pos / a.ps;
+      at = pos - col * a.ps;
+      p = table[col];
+      if (p < 0 || p >= a.pages) {
+        atomicOr(a.err, XP_ERR_BADPAGE);
+        p = p < 0 ? 0 : a.pages - 1;
+      }
+    }
+    s_page[threadIdx.x] = p;
+    s_at[threadIdx.x] = at;
+  }
+  __syncthreads();
+  const int pieces = a.D / 8;   // 8 or 16: a piece is 8 dims
+  const int e = threadIdx.x % pieces * 8;
+  __half* to = (__half*)a.k + h * w.plane + ((int64_t)page * kWidePage + t0) * a.D + e;
+  const int64_t to_v = (__half*)a.v - (__half*)a.k;
+#pragma unroll 4
+  for (int i = threadIdx.x / pieces; i < kWideTokens; i += kThreads / pieces) {
+    const int p = s_page[i];
+    const int64_t head = p * a.page + h * a.head;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      float x[8] = {};
+      if (p >= 0) {
+        const char* from = (kv ? a.vp : a.kp) + head;
+        const float step = xpq::scale_of((uint8_t)from[a.scale_at + s_at[i] * a.scale + e / 16]);
+        const uint32_t* code = (const uint32_t*)(from + s_at[i] * a.token + e / 8 * BITS);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x[j] = BITS == 4 ? (float)((int)(code[0] >> (j / 2 + j % 2 * 4) * 4 & 15u) - 8) * step
+                           : (float)((int)(code[j / 4 % (BITS / 4)] >> j % 4 * 8 & 255u) - 128) * step;
+      }
+      __half2 y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+      *(uint4*)(to + (kv ? to_v : 0) + (int64_t)i * a.D) = *(const uint4*)y;
+    }
+  }
+}
+
 template <typename T> bool wide_rows(const RowArgs& a) {
   const int64_t strides = a.sn | a.st | a.sh | a.D;
   return (((uintptr_t)a.k | (uintptr_t)a.v) & 15) == 0 && strides * (int64_t)sizeof(T) % 16 == 0;
@@ -264,6 +373,28 @@ cudaError_t xp_launch_append_quant(const xp_cache* c, int layer, const void* k, 
                                    int64_t width, const int32_t* lens, int N, int T, cudaStream_t s) {
   const RowArgs a = row_args(c, layer, (void*)k, (void*)v, sn, st, sh, table, ld, width, lens, nullptr, N, T);
   return c->d.dtype == XP_Q8 ? append<8>(a, rows, s) : append<4>(a, rows, s);
+}
+
+cudaError_t xp_launch_widen(const xp_cache* c, const xp_attn_args& g, int prefix_pages, int tail_pages,
+                            void* k, void* v, int64_t plane, int32_t* table, void* q, float* q_factor,
+                            cudaStream_t s) {
+  WidenArgs w;
+  w.r = row_args(c, g.a.layer, k, v, 0, 0, 0, g.table, g.ld_table, 0, g.lens, nullptr, g.a.N, 0);
+  w.prefix_table = g.prefix_table;
+  w.prefix = g.a.prefix_len, w.prefix_pages = prefix_pages, w.tail_pages = tail_pages;
+  w.max_len = g.a.max_len;
+  w.plane = plane, w.table = table;
+  w.page_ctas = (int)((prefix_pages + (int64_t)g.a.N * tail_pages) * (kWidePage / kWideTokens));
+  w.q = (const bf16*)g.q;
+  w.q_n = g.a.q_stride_n, w.q_t = g.a.q_stride_t, w.q_h = g.a.q_stride_h;
+  w.T = g.a.T, w.heads = g.a.heads, w.group = g.group;
+  w.scale = g.a.scale * 1.44269504088896f;
+  w.q_out = (__half*)q, w.q_factor = q_factor;
+  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads, each = (int64_t)g.kv_heads * (kThreads / 32);
+  const dim3 grid((unsigned)(w.page_ctas + (rows + each - 1) / each), g.kv_heads);
+  if (c->d.dtype == XP_Q8) widen_kernel<8><<<grid, kThreads, 0, s>>>(w);
+  else widen_kernel<4><<<grid, kThreads, 0, s>>>(w);
+  return cudaGetLastError();
 }
 
 cudaError_t xp_launch_cache_read(const xp_cache* c, int layer, const int32_t* table, int64_t ld,

@@ -7,6 +7,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <float.h>
 #include <math.h>
 
 #include "xp_internal.h"
@@ -25,6 +26,8 @@ inline xp_quant_sizes xp_quant_of(int page_size, int head_dim, xp_dtype t) {
   return q;
 }
 
+constexpr int kWidePage = 128;   // tokens of a page of a cache widened for tcgen05
+
 #ifdef __CUDACC__
 namespace xpq {
 
@@ -37,6 +40,19 @@ template <int BITS> struct Codes {
 
 __device__ __forceinline__ float scale_of(unsigned byte) {
   return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
+}
+
+// A query row of largest magnitude `top` as fp16: times 2^-e, e its exponent (0 for a row of zeros; what is
+// not finite stays so), which is exact but for what lies 2^-14 and more below the largest; *up: 2^e.
+__device__ __forceinline__ float row_scale(float top, float* up) {
+  const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253);
+  *up = __uint_as_float((uint32_t)e << 23);
+  return __uint_as_float((uint32_t)(254 - e) << 23);
+}
+// What a product of that row is multiplied by to be a score in base 2.  Never 0: a hidden key's -inf times it
+// has to stay -inf.
+__device__ __forceinline__ float row_factor(float up, float scale) {
+  return fmaxf(fminf(scale * up, 3.0e38f), FLT_MIN);
 }
 
 // The least scale that reaches `top`, a group's largest magnitude; *over where none does.

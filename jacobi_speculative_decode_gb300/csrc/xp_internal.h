@@ -215,7 +215,8 @@ struct xp_cache {
   int32_t* n_moves;        // their number
   int32_t* map;            // compaction: new id of every page (scratch)
   int32_t *row_a, *row_b, *row_c, *row_d;  // per-row scratch of the table calls (max_seqs each)
-  int attn_tc;             // tokens of a TMA box of the tensor-core attention, 0: not usable
+  int attn_tc;             // tokens of a TMA box of the tensor-core attention, 0: not usable (of a
+                           // quantised cache: of what is widened for it)
   CUtensorMap tm_k, tm_v;  // the pools as (dim, token, head, page, layer)
 };
 
@@ -261,6 +262,12 @@ struct xp_attn_plan {
   int64_t second_blocks;            // and those of the second stream's own results
   int prefix_splits, prefix_keys, tail_splits, tail_keys;
   int parts;
+  // quantised form: what is widened to bf16 first, in pages of kWidePage tokens (0: nothing), where its
+  // pools and its table are, elements of a head there; tc: then all of the call, else the prefix
+  int wide_prefix, wide_tail;
+  int64_t wide_plane;
+  size_t wide_k, wide_v, wide_table, wide_q, wide_factor;
+  size_t wide_stat, wide_acc, wide_line;   // and the tcgen05 form's own workspace
   // workspace: (max, sum) pairs, accumulators; tensor-core form: where each sequence's work begins
   size_t stat_off, acc_off, line_off, total;
 };
@@ -276,6 +283,13 @@ struct xp_attn_args {
   float* stat;                   // CUDA-core and quantised forms: [parts][N*T*heads][2]
   float* acc;                    //                                [parts][N*T*heads][dim]
   int* line;
+  // tcgen05 form: not null where q, k and v are fp16: what a product of query row r (rows of a kv head
+  // together, [kv_heads][N*T*group]) is multiplied by to be a score in base 2
+  const float* q_factor;
+  // tcgen05 form: not null where the joined rows are not the call's results but one range of it, and
+  // left as such: (max, sum) and weighted values, in the layout of stat and acc above
+  float *part_stat, *part_acc;
+  char* ws;
   uint32_t* err;
   xp_attn_plan plan;
 };
@@ -286,6 +300,9 @@ cudaError_t xp_launch_attn_tc(const xp_cache* c, const xp_attn_args& g, cudaStre
 cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 // joins the ranges of either form
 cudaError_t xp_launch_attn_combine(const xp_attn_args& g, cudaStream_t s);
+cudaError_t xp_launch_widen(const xp_cache* c, const xp_attn_args& g, int prefix_pages, int tail_pages,
+                            void* k, void* v, int64_t plane, int32_t* table, void* q, float* q_factor,
+                            cudaStream_t s);
 xp_attn_plan xp_attn_quant_plan(const xp_cache* c, const xp_attn* a);
 cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 

@@ -8,8 +8,7 @@ sum |q||k|, and a quotient of weighted sums within 2 dz A; sums over n keys with
 that otherwise, which is below dz.  A weight is held as 2^(z - m + 6) with m at most the row's largest
 score, so the largest is at least 2^6; where that of a key is below 2^-14, fp16 is a fixed grid of 2^-24 and
 it is off by up to 2^-25, 2^-31 of the largest and so of the sum: together 2^-31 sum_j |v_j|.  lse: dz + n 2^-23 + 2^-21 (1 + |lse|).
-Where many queries see each key the cache is widened to bf16 first, and the weights are rounded to bf16 as
-well: 2^-8 in place of 2^-11, and for 8 bits 2^-8 of every key and value."""
+Where many queries see each key the cache is widened to fp16 first, exactly, and all else is the same."""
 import math
 
 import numpy as np
@@ -58,8 +57,7 @@ def build(bits, ps, H, D, prefix, lens, seed, layer=0, layers=1, fill=None):
     return c, cu(table[0]), cu(table[1:, :width]), held
 
 
-def check(bits, N, T, H, G, D, ps, prefix, lens, seed=0, layer=0, layers=1, scale=None, q=None, fill=None,
-          widened=False):
+def check(bits, N, T, H, G, D, ps, prefix, lens, seed=0, layer=0, layers=1, scale=None, q=None, fill=None):
     c, prefix_table, table, held = build(bits, ps, H, D, prefix, lens, seed, layer, layers, fill)
     g = np.random.default_rng(seed + 1)
     scale = scale or 1 / math.sqrt(D)
@@ -82,14 +80,12 @@ def check(bits, N, T, H, G, D, ps, prefix, lens, seed=0, layer=0, layers=1, scal
     assert torch.equal(out, again) and torch.equal(lse, lse2)      # and results repeat bit for bit
     assert (wide[:, :, G * H:] == 7.0).all()
     got, got_lse, qs = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().cpu().numpy()
-    p = 2.0 ** -8 if widened else 2.0 ** -11
-    kv = 2.0 ** -8 if widened and bits == 8 else 0.0
     for n in range(N):
         k, v = (np.concatenate([h[0], h[n + 1]]) for h in held)
         sees = [prefix + max(0, lens[n] - T + 1 + t) for t in range(T)]
         want, want_lse, mean, size = Q.attention(qs[n], k, v, sees, scale)
-        dz = ((D + 8) * 2.0 ** -22 + kv) * size
-        tol = 2.0 ** -8 * np.abs(want) + mean * (p + kv + 2 * dz + len(k) * 2.0 ** -23 + 2.0 ** -20)[..., None] \
+        dz = (D + 8) * 2.0 ** -22 * size
+        tol = 2.0 ** -8 * np.abs(want) + mean * (2.0 ** -11 + 2 * dz + len(k) * 2.0 ** -23 + 2.0 ** -20)[..., None] \
             + 2.0 ** -31 * np.abs(v).sum(0).repeat(G, 0) + 1e-30
         assert (np.abs(got[n] - want) <= tol).all(), (n, np.max(np.abs(got[n] - want) / tol))
         seen = np.isfinite(want_lse)
@@ -115,6 +111,15 @@ CASES = [  # N, T, kv heads, group, dim, page, prefix, lens
     (6, 1, 2, 4, 128, 16, 700, [0] * 6),
     (1, 40, 2, 4, 64, 16, 0, [40]),
     (2, 1, 1, 4, 128, 64, 0, [5000, 4000]),
+    # many queries a key: the prefix, the tails or both are widened first
+    (70, 1, 2, 4, 128, 16, 700, [1 + 5 * i % 90 for i in range(70)]),
+    (40, 1, 1, 8, 64, 20, 129, [7 * i % 150 for i in range(40)]),
+    (20, 5, 2, 3, 128, 64, 1000, [3 * i for i in range(20)]),
+    (33, 1, 3, 8, 128, 8, 128, [0] * 33),
+    (3, 40, 2, 4, 64, 16, 0, [300, 40, 7]),
+    (2, 150, 2, 2, 128, 20, 130, [150, 400]),
+    (5, 16, 1, 4, 128, 64, 40, [0, 16, 128, 129, 500]),
+    (1, 300, 1, 1, 64, 16, 5, [300]),
 ]
 
 
@@ -122,6 +127,16 @@ CASES = [  # N, T, kv heads, group, dim, page, prefix, lens
 @pytest.mark.parametrize("bits", [4, 8])
 def test_against_the_definition(case, bits):
     check(bits, *case, seed=sum(case[:7]))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_widened_layers_and_values_of_any_size(bits):
+    def fill(rows):
+        rows[0][:, :, 0] *= 1e-4
+        rows[1][:, :, 1] *= 8000.0 if bits == 8 else 100.0
+        rows[1][:, 3] *= 1e-5
+    check(bits, 20, 4, 2, 4, 128, 16, 200, [70 + i for i in range(20)], layer=1, layers=3, fill=fill)
+    check(bits, 4, 20, 2, 4, 64, 16, 200, [70 + i for i in range(4)], layer=2, layers=3, fill=fill, scale=0.4)
 
 
 @pytest.mark.parametrize("bits", [4, 8])
@@ -138,6 +153,7 @@ def test_queries_of_any_size(bits, size):
     q[0, 0, 0] = 0
     q[1, 1, 2, ::3] *= 1e-3
     check(bits, 2, 2, 2, 2, 128, 16, 20, [70, 40], q=q, scale=min(1.0, 1 / size) * 0.1)
+    check(bits, 2, 70, 2, 2, 128, 16, 20, [170, 40], q=q.repeat(1, 35, 1, 1), scale=min(1.0, 1 / size) * 0.1)
 
 
 def test_large_and_small_values():
@@ -149,25 +165,26 @@ def test_large_and_small_values():
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-def test_a_query_that_is_not_finite_spoils_its_row_alone(bits):
+@pytest.mark.parametrize("T", [2, 140])
+def test_a_query_that_is_not_finite_spoils_its_row_alone(bits, T):
     c, prefix_table, table, _ = build(bits, 16, 2, 64, 40, [30, 70], 3)
     g = torch.Generator(device="cuda").manual_seed(1)
-    q = torch.randn(2, 2, 4, 64, generator=g, device="cuda", dtype=torch.bfloat16)
+    q = torch.randn(2, T, 4, 64, generator=g, device="cuda", dtype=torch.bfloat16)
     outs = []
     for bad in (None, math.nan, math.inf):
         x = q.clone()
         if bad is not None:
-            x[1, 0, 2, 5] = bad
+            x[1, T - 2, 2, 5] = bad
         out = torch.empty_like(x)
         a = xp.make_attn(x, out, 0, 40, 70, 0.1)
         xp.xp_prefix_attention(c.handle, a, x, prefix_table, table, cu([30, 70]), out, None,
                                c.attention_workspace(a))
         outs.append(out)
     for out, bad in zip(outs[1:], (math.nan, math.inf)):
-        mask = torch.ones(2, 2, 4, dtype=torch.bool, device="cuda")
-        mask[1, 0, 2] = False
+        mask = torch.ones(2, T, 4, dtype=torch.bool, device="cuda")
+        mask[1, T - 2, 2] = False
         assert torch.equal(out[mask], outs[0][mask])
-        assert torch.isnan(out[1, 0, 2]).any()
+        assert torch.isnan(out[1, T - 2, 2]).any()
 
 
 def test_lengths_beyond_the_limit_and_bad_pages_are_told():
