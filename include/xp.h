@@ -412,10 +412,10 @@ typedef struct {
 /* Quantised caches: dtype XP_Q8 or XP_Q4.  16 consecutive dims of a token's head share a scale s and are
  * held as whole numbers c of 8 or 4 bits that stand for c*s, |c| <= 127 or 7.  s is an 8-bit float without a
  * sign, 5 bits of exponent and 3 of mantissa: the 16-bit float whose bits are the byte << 7.  It is the least
- * one for which 127*s or 7*s reaches the largest magnitude of the 16, at most 512 or 9216; c is the element
+ * one for which 127*s or 7*s reaches the largest magnitude of the 16, at most 512 or 7680; c is the element
  * over s, rounded to nearest, ties to even.  So every value held is exact in 16-bit floats (and those of 4
  * bits in bf16), and an element is off by at most s/2.  A NaN is held as 0, and what lies beyond
- * 127*512 or 7*9216 as the nearest value that can be held; both raise XP_ERANGE.
+ * 127*512 or 7*7680 as the nearest value that can be held; both raise XP_ERANGE.
  * All strides are in bytes, and heads lie outside the tokens of a page.  A head of a page is
  * xp_quant_head_bytes: the codes of its tokens, head_dim*8/8 or head_dim*4/8 bytes each, then their scales,
  * head_dim/16 bytes each, padded to a multiple of 4; the whole is padded to a multiple of 16.  8-bit codes

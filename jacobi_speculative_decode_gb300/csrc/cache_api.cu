@@ -102,11 +102,11 @@ xp_attn_plan attn_plan(const xp_cache* c, const xp_attn* a) {
     const xp_attn_plan tc = xp_attn_tc_plan(c, a);
     if (tc.total) return tc;   // 0: more work than its line can count
   }
-  xp_attn_plan p = quant ? xp_attn_quant_plan(c, a) : xp_attn_simt_plan(c, a);
-  if (p.tc) return p;   // quantised, and widened whole
+  if (quant) return xp_attn_quant_plan(c, a);
+  xp_attn_plan p = xp_attn_simt_plan(c, a);
   const size_t rows = (size_t)a->N * a->T * a->heads;
-  p.stat_off = p.total;   // behind what the quantised form has taken
-  p.acc_off = p.stat_off + align_up(rows * p.parts * 8);
+  p.stat_off = 0;
+  p.acc_off = align_up(rows * p.parts * 8);
   p.total = p.acc_off + align_up(rows * p.parts * c->d.head_dim * 4);
   return p;
 }

@@ -40,9 +40,83 @@ constexpr float kLazy = 8.0f;         // growth of the maximum (base 2) that wei
 constexpr float kLift = 6.0f;         // weights are 2^(z - m + kLift): at most 2^14
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
+constexpr int kRound = kWarps * kStep;   // keys of a round of the four warps
+constexpr int kUnitCost = 1;          // what a unit costs besides its keys, in rounds
+constexpr int kMostResident = 5;      // CTAs an SM
+constexpr int kMinChunk = 2;          // least work of a CTA, in rounds
+
 struct Quant {
   int code, scale, scale_at;   // bytes of a token's codes and scales; where a head's scales begin
+  bool q_wide;                 // queries by 16 bytes
 };
+
+// The work is one line of cost: the prefix's units (kv head by kv head, row tile by row tile), then those
+// of each sequence's tail.  A unit costs its rounds of keys and kUnitCost; CTA i does [i*chunk, (i+1)*chunk) of
+// the line, so that every CTA gets the same whatever the lengths are.  A piece that begins its unit leaves
+// its result in the unit's place, one that does not in its CTA's, of which there is at most one.
+__host__ __device__ inline int rounds_of(int keys) { return (keys + kRound - 1) / kRound; }
+__host__ __device__ inline int cost_of(int keys) { return keys > 0 ? rounds_of(keys) + kUnitCost : 0; }
+// first round of a unit of T that lies behind a cost of x from its beginning
+__device__ __forceinline__ int round_at(int64_t x, int T) {
+  const int64_t y = x - kUnitCost;
+  return y <= 0 ? 0 : y > T ? T : (int)y;
+}
+__device__ __forceinline__ int tail_len(const xp_attn_args& g, int n, bool tell) {
+  int len = g.lens[n];
+  if (len < 0 || len > g.a.max_len) {
+    if (tell) atomicOr(g.err, XP_ERR_LENGTH);
+    len = len < 0 ? 0 : g.a.max_len;
+  }
+  return len;
+}
+// what the prefix costs that is attended over here
+__device__ __forceinline__ int64_t prefix_cost(const xp_attn_args& g) {
+  return (int64_t)g.kv_heads * g.plan.prefix_tiles * cost_of(g.a.prefix_len);
+}
+
+struct Start {
+  int64_t total[kWarps], base;   // where the sequence in which this CTA begins has its beginning
+  int n;
+};
+// Sums the tails' costs over the CTA: the chunk (0 where the line ends before this CTA's share), and where
+// the share begins.  CTA 0 leaves the chunk and every sequence's beginning for the kernel that joins.
+__device__ __forceinline__ int64_t plan_line(const xp_attn_args& g, Start* s) {
+  const int64_t before = prefix_cost(g);
+  const int N = g.a.max_len > 0 ? g.a.N : 0, units = g.kv_heads * g.plan.tail_tiles;
+  const int per = (N + kThreads - 1) / kThreads, n0 = min(N, (int)threadIdx.x * per), n1 = min(N, n0 + per);
+  auto cost = [&](int n) { return (int64_t)units * cost_of(tail_len(g, n, blockIdx.x == 0)); };
+  int64_t mine = 0;
+  for (int n = n0; n < n1; ++n) mine += cost(n);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(kAll, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) s->total[warp] = inc;
+  __syncthreads();
+  int64_t base = before + inc - mine, all = before;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    base += w < warp ? s->total[w] : 0;
+    all += s->total[w];
+  }
+  const int64_t chunk = max((int64_t)kMinChunk, (all + gridDim.x - 1) / gridDim.x), x = blockIdx.x * chunk;
+  int64_t* line = (int64_t*)g.line;
+  for (int n = n0; n < n1; ++n) {
+    const int64_t c = per == 1 ? mine : cost(n);
+    if (blockIdx.x == 0) line[1 + n] = base;
+    if (x >= base && x < base + c) {
+      s->n = n;
+      s->base = base;
+    }
+    base += c;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) line[0] = chunk;
+  __syncthreads();
+  return x < all ? chunk : 0;
+}
 
 template <int BITS, int DP, int NQ> struct Cfg {
   static constexpr int CODE = DP * BITS / 8;              // bytes a token of the ring
@@ -54,6 +128,11 @@ template <int BITS, int DP, int NQ> struct Cfg {
   static constexpr int JOIN = kWarps * 8 * PITCH * 4;
   static constexpr int QUERIES = NQ == 4 ? NQ * (DP / 16) * 32 * 8 : 0;   // held in shared memory
   static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + QUERIES;
+  // CTAs an SM, as registers (results: 4 NQ KS a thread) and shared memory allow
+  static constexpr int RESIDENT = DP == 64 ? (NQ == 1 ? 5 : NQ == 2 ? 4 : 2) : DP == 128 && NQ == 1 && BITS == 4 ? 4 : 2;
+  // 4 bits: values are widened 2^-7 times as large (see widen4), queries are 16 times (so that 1/16 of
+  // them keeps as much)
+  static constexpr float UNIT = BITS == 4 ? 128.0f : 1.0f, QUERY = BITS == 4 ? 16.0f : 1.0f;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -91,15 +170,24 @@ __device__ __forceinline__ uint32_t u32(__half2 v) { return *(const uint32_t*)&v
 // two scales as fp16: the bytes lo and hi
 __device__ __forceinline__ __half2 scales(uint32_t lo, uint32_t hi) { return h2(lo << 7 | hi << 23); }
 
-// Four pairs of codes of 4 bits: bits 4j.. of either half of w, times s.  1024 + c and 1024 + 16 c are fp16
-// numbers with c in their last bits.
-__device__ __forceinline__ void widen4(uint32_t w, __half2 s, uint32_t (&out)[4]) {
-  const __half2 sixteenth = h2(0x2C002C00u), low = h2(0xE408E408u), high = h2(0xD480D480u);   // 1/16, -1032, -72
+// Codes of 4 bits as they are held, c + 8 = 0..15, times a scale: pairs j = 0..3 of either half of w.
+// 1024 + c and 1024 + 16 c are fp16 numbers with c in their last bits, so one multiply-add gives
+// (1024 + c) s - 1024 s, exactly.  Two factors stay: odd pairs come 16 times too large (the queries' dims
+// there are 1/16, and the results' are divided at the end), and scales are s 2^-7, so that 1024 s is finite
+// and c s down to the least scale is whole 2^-24.  What the 8 too much brings is one product more for
+// every 16 keys: 8 sum_d s q_d for scores, 8 sum_j s p_j for results.
+struct Scale4 {
+  __half2 s, base;
+};
+__device__ __forceinline__ Scale4 scale4(__half2 s) {
+  const __half2 t = __hmul2(s, h2(0x20002000u));          // 2^-7
+  return {t, __hmul2(t, h2(0xE400E400u))};                // -1024
+}
+__device__ __forceinline__ void widen4(uint32_t w, Scale4 f, uint32_t (&out)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const __half2 a = h2((w & 0x000F000Fu) | 0x64006400u), b = h2((w & 0x00F000F0u) | 0x64006400u);
-    out[2 * i] = u32(__hmul2(__hadd2(a, low), s));
-    out[2 * i + 1] = u32(__hmul2(__hfma2(b, sixteenth, high), s));
+    out[2 * i] = u32(__hfma2(h2((w & 0x000F000Fu) | 0x64006400u), f.s, f.base));
+    out[2 * i + 1] = u32(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), f.s, f.base));
     w >>= 8;
   }
 }
@@ -125,46 +213,55 @@ template <int NW> __device__ __forceinline__ void load_words(const char* p, uint
 }
 
 template <int BITS, int DP, int NQ>
-__global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_constant__ xp_attn_args g,
-                                                              const Quant z) {
+__global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
+    attn_quant_kernel(const __grid_constant__ xp_attn_args g, const Quant z) {
   using C = Cfg<BITS, DP, NQ>;
   constexpr int KS = DP / 16;             // k steps of the first product, row tiles of the second
   constexpr int KW = DP / 4 * BITS / 32;  // words of a lane's 1/4 of a key
   constexpr int VW = DP / 8 * BITS / 32;  // and of its 1/8 of a value
   constexpr int WPG = 16 * BITS / 32;     // words of 16 dims
+  constexpr int KG = KS / 4;              // groups of 16 dims of a lane's 1/4 of a key
+  constexpr int VG = DP <= 128 ? 1 : 2;   // and of its 1/8 of a value
+  constexpr int KB = BITS == 4 ? (KG + 1) / 2 : 0;   // products for the 8 too much: of scores,
+  constexpr bool VB = BITS == 4;                     // of results
   constexpr bool QREGS = NQ < 4;
   extern __shared__ __align__(16) char smem[];
   __shared__ float s_m[kWarps][8 * NQ], s_l[kWarps][8 * NQ];
+  __shared__ Start s_start;
 
   const xp_attn_plan& pl = g.plan;
-  const int hk = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gr = lane >> 2, t4 = lane & 3;   // row group and place in it of a product's fragments
   const int per_seq = g.a.T * g.group, RT = 8 * NQ;
-  int unit = blockIdx.x;
-  const bool prefix = unit < pl.prefix_tiles * pl.prefix_splits;
-  int tile, split, n = 0, part, keys;
-  const int32_t* table = g.prefix_table;
-  if (prefix) {
-    tile = unit / pl.prefix_splits;
-    split = unit % pl.prefix_splits;
-    part = split;
-    keys = g.a.prefix_len;
-  } else {
-    unit -= pl.prefix_tiles * pl.prefix_splits;
-    split = unit % pl.tail_splits;
-    tile = unit / pl.tail_splits % pl.tail_tiles;
-    n = unit / pl.tail_splits / pl.tail_tiles;
-    part = pl.prefix_splits + split;
-    table = g.table + n * g.ld_table;
-    keys = g.lens[n];
-    if (keys < 0 || keys > g.a.max_len) {
-      if (threadIdx.x == 0) atomicOr(g.err, XP_ERR_LENGTH);
-      keys = keys < 0 ? 0 : g.a.max_len;
-    }
-  }
-  const int range = prefix ? pl.prefix_keys : pl.tail_keys;
-  const int k0 = split * range, k1 = k0 + min(range, keys - k0);   // none where keys < k0
+  const int64_t chunk = plan_line(g, &s_start);
+  if (chunk == 0) return;
+  const int64_t x0 = blockIdx.x * chunk, x1 = x0 + chunk, prefix_units = (int64_t)g.kv_heads * pl.prefix_tiles;
 
+  // the unit in which this CTA's share begins: unit u of the prefix (n < 0) or of sequence n
+  int n, keys, u;
+  int64_t at;
+  if (x0 < prefix_cost(g)) {
+    n = -1, keys = g.a.prefix_len;
+    u = (int)(x0 / cost_of(keys));
+    at = (int64_t)u * cost_of(keys);
+  } else {
+    n = s_start.n, keys = tail_len(g, n, false);
+    u = (int)((x0 - s_start.base) / cost_of(keys));
+    at = s_start.base + (int64_t)u * cost_of(keys);
+  }
+  const int more = kRound / g.page_size, rest = kRound % g.page_size;   // a round further in a table
+
+  while (true) {   // unit by unit; the same in every thread
+  const bool prefix = n < 0;
+  const int tiles = prefix ? pl.prefix_tiles : pl.tail_tiles, T = rounds_of(keys);
+  const int r0 = round_at(x0 - at, T), r1 = round_at(min(x1 - at, (int64_t)cost_of(keys)), T);
+  if (r0 < r1) {
+  const int hk = u / tiles, tile = u % tiles;
+  const int32_t* table = prefix ? g.prefix_table : g.table + n * g.ld_table;
+  const int64_t slot = r0 > 0 ? pl.units + blockIdx.x
+                       : prefix ? u
+                                : prefix_units + (int64_t)n * g.kv_heads * pl.tail_tiles + u;
+  const int k0 = r0 * kRound, k1 = min(keys, r1 * kRound);
   const int D = g.dim;
   auto row_at = [&](int r, int* rn, int* rt, int* rj) {   // false behind the end
     const int i = tile * RT + r;
@@ -181,11 +278,10 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
   int64_t key_at = 0;   // of this lane's key in the step to be loaded: its codes,
   int scale_at = 0;     // and its scales from there
   bool key_in = false;
-  auto find = [&](int kb) {
-    const int key = kb + lane;
+  int key = k0 + warp * kStep + lane, col = key / g.page_size, at = key - col * g.page_size;
+  auto find = [&]() {   // the next step's
     key_in = key < k1;
     if (!key_in) return;
-    const int col = key / g.page_size, at = key - col * g.page_size;
     int p = table[col];
     if (p < 0 || p >= g.pages) {
       atomicOr(g.err, XP_ERR_BADPAGE);
@@ -193,6 +289,10 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
     }
     key_at = p * g.kv_page + hk * g.kv_head + (int64_t)at * z.code;
     scale_at = z.scale_at + at * (z.scale - z.code);
+    key += kRound;
+    col += more;
+    at += rest;
+    if (at >= g.page_size) at -= g.page_size, ++col;
   };
   auto load = [&](int stage) {
     const uint32_t to = ring_at + stage * C::STAGE;
@@ -201,10 +301,10 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
       constexpr int PB = decltype(piece_bytes)::value, PIECES = C::CODE / PB;   // of a token
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        const int at = i * 32 + lane, key = at / PIECES, p = at % PIECES;
-        const int64_t from = __shfl_sync(kAll, key_at, key) + p * PB;
-        if ((in >> key & 1) && p * PB < z.code) {
-          const uint32_t d = to + key * C::CODE + p * PB;
+        const int piece = i * 32 + lane, of = piece / PIECES, p = piece % PIECES;
+        const int64_t from = __shfl_sync(kAll, key_at, of) + p * PB;
+        if ((in >> of & 1) && p * PB < z.code) {
+          const uint32_t d = to + of * C::CODE + p * PB;
           copy_async(d, (const char*)g.k + from, PB);
           copy_async(d + kStep * C::CODE, (const char*)g.v + from, PB);
         }
@@ -243,12 +343,12 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
   const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;   // this warp's
   auto base_of = [&](int i) { return k0 + (warp + i * kWarps) * kStep; };
   int found = 0;
-  if (mine > 0) find(base_of(0));
+  if (mine > 0) find();
 #pragma unroll
   for (int i = 0; i < C::STAGES - 1; ++i) {
     if (i < mine) {
       load(i);
-      if (++found < mine) find(base_of(found));
+      if (++found < mine) find();
     }
     commit();
   }
@@ -256,6 +356,7 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
   // Queries: lane (gr, t4) holds dims t4 DP/4.. of query gr of every column tile, as fp16 pairs
   uint32_t qr[QREGS ? NQ : 1][QREGS ? 2 * KS : 1];
   uint2* sq = (uint2*)(smem + (C::SMEM - C::QUERIES));
+  uint32_t qb[NQ][KB > 0 ? 2 * KB : 1];   // -8 times the sums of groups of 16 dims, as two fp16 each
   float cz[NQ][2];       // of queries 2 t4 and 2 t4 + 1: score to base 2,
   int limit[NQ][2];      // keys it sees
   int least = k1;        // and the least of them
@@ -268,23 +369,45 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
                              : nullptr;
     float x[DP / 4], top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < DP / 4; ++i) {
+    for (int i = 0; i < DP / 4; i += 8) {
       const int d = t4 * (DP / 4) + i;
-      x[i] = is_row && d < D ? __bfloat162float(src[d]) : 0.0f;
-      top = fmaxf(top, fabsf(x[i]));
+      if (is_row && d < D && z.q_wide) {
+        const uint4 v = *(const uint4*)(src + d);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i + j] = __uint_as_float(j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i + j] = is_row && d < D ? __bfloat162float(src[d + j]) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[i + j]));
     }
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
     float up;
-    const float down = xpq::row_scale(top, &up);
+    const float down = C::QUERY * xpq::row_scale(top, &up);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {   // of a k step: dims 4 i.. of the lane's
       const uint32_t b0 = pack(x[4 * i] * down, x[4 * i + 1] * down);
-      const uint32_t b1 = pack(x[4 * i + 2] * down, x[4 * i + 3] * down);
+      const float odd = BITS == 4 ? down * 0.0625f : down;
+      const uint32_t b1 = pack(x[4 * i + 2] * odd, x[4 * i + 3] * odd);
       if constexpr (QREGS) qr[q][2 * i] = b0, qr[q][2 * i + 1] = b1;
       else if (warp == 0) sq[(q * KS + i) * 32 + lane] = make_uint2(b0, b1);
     }
-    const float c = xpq::row_factor(up, g.a.scale * 1.44269504088896f);
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {   // k of the product: (group, group + 1) as fp16, then what that leaves
+      float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int e = 0; e < (KG > 1 ? 2 : 1); ++e)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[e] += x[(2 * i + e) * 16 + j] * down;
+      const float h0 = -8.0f * sum[0], h1 = -8.0f * sum[1];
+      const uint32_t hi = pack(h0, h1);
+      qb[q][2 * i] = hi;
+      qb[q][2 * i + 1] = pack(h0 - __low2float(h2(hi)), h1 - __high2float(h2(hi)));
+    }
+    const float c = C::UNIT / C::QUERY * xpq::row_factor(up, g.a.scale * 1.44269504088896f);
     const int lim = !is_row ? k1 : min(k1, prefix ? keys : keys - g.a.T + rt + 1);
     least = min(least, lim);
 #pragma unroll
@@ -296,13 +419,13 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
   least = __reduce_min_sync(kAll, least);
   if constexpr (!QREGS) __syncthreads();
 
-  float o[NQ][KS][4], m[NQ][2], l[NQ][2];
+  float o[NQ][KS][4], ob[NQ][4], m[NQ][2], l[NQ][2];   // ob: sum_j s p_j of the lane's groups
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[q][i][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) o[q][i][e] = ob[q][e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) m[q][i] = -INFINITY, l[q][i] = 0.0f;
   }
@@ -313,7 +436,7 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
     __syncwarp();   // every lane's copies are in, and every lane is done with the stage to be refilled
     if (it + C::STAGES - 1 < mine) {
       load((it + C::STAGES - 1) % C::STAGES);
-      if (++found < mine) find(base_of(found));
+      if (++found < mine) find();
     }
     commit();
     const char* st = ring + it % C::STAGES * C::STAGE;
@@ -330,18 +453,32 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[kt][q][e] = 0.0f;
-      uint32_t w[2][KW];
-      __half2 sc[2][KS / 4];   // scales of the lane's KS/4 groups
+      uint32_t w[2][KW], byte[2][KG];   // scales of the lane's groups
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int key = kt * 16 + r * 8 + gr;
         load_words<KW>(sk + key * C::CODE + t4 * (C::CODE / 4), w[r]);
 #pragma unroll
-        for (int i = 0; i < KS / 4; ++i) {
-          const int group = t4 * (KS / 4) + i;
-          const uint32_t b = group < groups ? ks[key * C::SCALE + group] : 0;
-          sc[r][i] = scales(b, b);
+        for (int i = 0; i < KG; ++i)
+          byte[r][i] = t4 * KG + i < groups ? ks[key * C::SCALE + t4 * KG + i] : 0;
+      }
+      Scale4 sc4[2][KG];
+      __half2 sc8[2][KG];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < KG; ++i) {
+          sc8[r][i] = scales(byte[r][i], byte[r][i]);
+          if constexpr (BITS == 4) sc4[r][i] = scale4(sc8[r][i]);
         }
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        uint32_t f[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          f[r] = f[2 + r] = __byte_perm(u32(sc4[r][2 * i].s), KG > 1 ? u32(sc4[r][KG > 1 ? 2 * i + 1 : 0].s) : 0, 0x5410);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) mma(s[kt][q], f, qb[q][2 * i], qb[q][2 * i + 1]);
       }
 #pragma unroll
       for (int i = 0; i < KS; i += 2) {   // two k steps: 8 dims of the lane
@@ -349,11 +486,11 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if constexpr (BITS == 4) {
-            widen4(w[r][i / 2], sc[r][i / 4], a[r]);
+            widen4(w[r][i / 2], sc4[r][i / 4], a[r]);
           } else {
 #pragma unroll
             for (int p = 0; p < 4; ++p)   // bytes 0, 1 or 2, 3 of a word, one in each half
-              a[r][p] = widen8(__byte_perm(w[r][i + p / 2], 0, p % 2 ? 0x4342 : 0x4140), sc[r][i / 4]);
+              a[r][p] = widen8(__byte_perm(w[r][i + p / 2], 0, p % 2 ? 0x4342 : 0x4140), sc8[r][i / 4]);
           }
         }
 #pragma unroll
@@ -404,6 +541,7 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
           l[q][i] *= f;
 #pragma unroll
           for (int j = 0; j < KS; ++j) o[q][j][i] *= f, o[q][j][2 + i] *= f;
+          if (VB) ob[q][i] *= f, ob[q][2 + i] *= f;
         }
     }
     uint32_t p[2][NQ][2];
@@ -429,35 +567,43 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
       uint32_t w[4][VW];
-      __half2 sc[2][DP <= 128 ? 1 : 2];   // scales of a pair of keys
+      Scale4 sc4[2][VG];   // of a pair of keys
+      __half2 sc8[2][VG];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         load_words<VW>(sv + (kt * 16 + 2 * t4 + r / 2 * 8 + r % 2) * C::CODE + gr * (C::CODE / 8), w[r]);
 #pragma unroll
-      for (int i = 0; i < (DP <= 128 ? 1 : 2); ++i) {
+      for (int i = 0; i < VG; ++i) {
         const int group = DP == 64 ? gr / 2 : DP == 128 ? gr : 2 * gr + i;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint8_t* at = vs + (kt * 16 + 2 * t4 + r * 8) * C::SCALE + group;
-          sc[r][i] = scales(group < groups ? at[0] : 0, group < groups ? at[C::SCALE] : 0);
+          const uint8_t* from = vs + (kt * 16 + 2 * t4 + r * 8) * C::SCALE + group;
+          sc8[r][i] = scales(group < groups ? from[0] : 0, group < groups ? from[C::SCALE] : 0);
+          if constexpr (BITS == 4) sc4[r][i] = scale4(sc8[r][i]);
         }
+      }
+      if constexpr (VB) {   // rows: the lane's groups
+        const uint32_t f[4] = {u32(sc4[0][0].s), VG > 1 ? u32(sc4[0][VG - 1].s) : 0, u32(sc4[1][0].s),
+                               VG > 1 ? u32(sc4[1][VG - 1].s) : 0};
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) mma(ob[q], f, p[kt][q][0], p[kt][q][1]);
       }
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
-        const int gi = DP <= 128 ? 0 : i / WPG;
+        const int gi = VG == 1 ? 0 : i / WPG;
         uint32_t a[2][8];   // [keys 2 t4.. or those 8 on][dim of the word]
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if constexpr (BITS == 4) {
             uint32_t even[4], odd[4];
-            widen4(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x5410), sc[r][gi], even);
-            widen4(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x7632), sc[r][gi], odd);
+            widen4(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x5410), sc4[r][gi], even);
+            widen4(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x7632), sc4[r][gi], odd);
 #pragma unroll
             for (int j = 0; j < 4; ++j) a[r][2 * j] = even[j], a[r][2 * j + 1] = odd[j];
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              a[r][j] = widen8(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x0400 + 0x0101 * j), sc[r][gi]);
+              a[r][j] = widen8(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x0400 + 0x0101 * j), sc8[r][gi]);
           }
         }
 #pragma unroll
@@ -486,7 +632,6 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
     }
   __syncthreads();   // the rings are read no more either
   float* join = (float*)smem;
-  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
 #pragma unroll
@@ -495,10 +640,15 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
       const float all = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
       const float f = m[q][i] == all ? 1.0f : ex2(m[q][i] - all);
       float* to = join + (warp * 8 + 2 * t4 + i) * C::PITCH + gr * (DP / 8);
+      // 4 bits: row tiles in pairs, of which the second came 16 times too large; a lane's first and second
+      // half have a group each where it has two
+      const float even = C::UNIT * f, odd = BITS == 4 ? even * 0.0625f : even;
 #pragma unroll
-      for (int j = 0; j < KS; j += 2)
-        *(float4*)(to + 2 * j) = make_float4(o[q][j][i] * f, o[q][j][2 + i] * f, o[q][j + 1][i] * f,
-                                             o[q][j + 1][2 + i] * f);
+      for (int j = 0; j < KS; j += 2) {
+        const float over = VB ? 8.0f * even * ob[q][VG > 1 && j >= KS / 2 ? 2 + i : i] : 0.0f;
+        *(float4*)(to + 2 * j) = make_float4(o[q][j][i] * even - over, o[q][j][2 + i] * even - over,
+                                             o[q][j + 1][i] * odd - over, o[q][j + 1][2 + i] * odd - over);
+      }
     }
     __syncthreads();
     for (int u = threadIdx.x; u < 8 * (DP / 4); u += kThreads) {
@@ -516,49 +666,120 @@ __global__ void __launch_bounds__(kThreads) attn_quant_kernel(const __grid_const
         const float4 x = *(const float4*)(join + (w * 8 + r) * C::PITCH + d);
         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
       }
-      const int h = hk * g.group + rj;
-      const int64_t row = ((int64_t)rn * g.a.T + rt) * g.a.heads + h;
-      if (pl.parts == 1) {
-        const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;   // NaN where a visible score is
-        bf16* out = (bf16*)g.out + rn * g.a.o_stride_n + rt * g.a.o_stride_t + h * g.a.o_stride_h + d;
-        out[0] = __float2bfloat16_rn(v.x * inv), out[1] = __float2bfloat16_rn(v.y * inv);
-        out[2] = __float2bfloat16_rn(v.z * inv), out[3] = __float2bfloat16_rn(v.w * inv);
-        if (d == 0 && g.lse)
-          g.lse[row] = sum != 0.0f ? (all - kLift + log2f(sum)) * 0.693147180559945f : -INFINITY;
-      } else {
-        if (d == 0) *(float2*)&g.stat[(part * rows + row) * 2] = make_float2(all - kLift, sum);
-        if (sum != 0.0f) *(float4*)&g.acc[(part * rows + row) * D + d] = v;
-      }
+      const int64_t row = slot * RT + q * 8 + r;
+      if (d == 0) *(float2*)&g.stat[row * 2] = make_float2(all - kLift, sum);
+      if (sum != 0.0f) *(float4*)&g.acc[row * D + d] = v;
     }
     __syncthreads();
   }
+  }
+
+  at += cost_of(keys);
+  if (++u == g.kv_heads * tiles) {
+    u = 0;
+    const int N = g.a.max_len > 0 ? g.a.N : 0;
+    do ++n;
+    while (n < N && (keys = tail_len(g, n, false)) == 0);
+    if (n >= N) return;
+  }
+  if (at >= x1) return;
+  }
+}
+
+// One warp a query row: what tcgen05 left of its prefix, and the pieces of its prefix and of its tail (the
+// unit's own and those of the CTAs at whose beginning it was cut), brought to a common maximum:
+//   out = sum_p a_p O_p / sum_p a_p l_p,  a_p = 2^(m_p - m).
+__global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_constant__ xp_attn_args g) {
+  ptx::pdl_wait();
+  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 31, D = g.dim, RT = g.plan.rows_tile, per_seq = g.a.T * g.group;
+  const int h = (int)(row % g.a.heads), t = (int)(row / g.a.heads % g.a.T);
+  const int n = (int)(row / g.a.heads / g.a.T), hk = h / g.group, i = t * g.group + h % g.group;
+  const int64_t* line = (const int64_t*)g.line;
+  const int64_t chunk = line[0];
+
+  float o[8], m = -INFINITY, l = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) o[c] = 0.0f;
+  auto add = [&](float2 st, const float* acc) {   // a piece, the same in all lanes
+    if (st.y == 0.0f) return;                     // no visible key: acc may hold anything
+    float x[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x[c] = c * 32 + lane < D ? __ldcg(acc + c * 32 + lane) : 0.0f;
+    const float now = fmaxf(m, st.x), a = exp2f(m - now), b = exp2f(st.x - now);
+    m = now;
+    l = l * a + st.y * b;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = o[c] * a + x[c] * b;
+  };
+  auto pieces = [&](int keys, int64_t at, int64_t unit, int r) {
+    const int T = rounds_of(keys), cost = cost_of(keys);
+    const int64_t c0 = at / chunk, c1 = (at + cost - 1) / chunk;
+    for (int64_t first = c0; first <= c1; first += 32) {   // a lane a CTA
+      const int64_t c = first + lane;
+      int64_t from = -1;
+      float2 st = make_float2(0.0f, 0.0f);
+      if (c <= c1) {
+        const int r0 = round_at(c * chunk - at, T), r1 = round_at(min((c + 1) * chunk - at, (int64_t)cost), T);
+        if (r0 < r1) {
+          from = (r0 > 0 ? g.plan.units + c : unit) * RT + r;
+          st = __ldcg((const float2*)g.stat + from);
+        }
+      }
+      const int count = (int)min((int64_t)32, c1 - first + 1);
+#pragma unroll 2
+      for (int k = 0; k < count; ++k) {
+        const float2 s = make_float2(__shfl_sync(kAll, st.x, k), __shfl_sync(kAll, st.y, k));
+        add(s, g.acc + __shfl_sync(kAll, from, k) * D);
+      }
+    }
+  };
+  if (g.part_stat) add(__ldcg((const float2*)g.part_stat + row), g.part_acc + row * D);
+  const int units = g.kv_heads * g.plan.prefix_tiles;
+  if (units > 0 && g.a.prefix_len > 0) {
+    const int at_row = n * per_seq + i, u = hk * g.plan.prefix_tiles + at_row / RT;
+    pieces(g.a.prefix_len, (int64_t)u * cost_of(g.a.prefix_len), u, at_row % RT);
+  }
+  if (g.a.max_len > 0) {
+    const int keys = tail_len(g, n, false), u = hk * g.plan.tail_tiles + i / RT;
+    if (keys > 0)
+      pieces(keys, line[1 + n] + (int64_t)u * cost_of(keys), units + (int64_t)n * g.kv_heads * g.plan.tail_tiles + u,
+             i % RT);
+  }
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // NaN where a visible score is
+  bf16* out = (bf16*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (c * 32 + lane < D) out[c * 32 + lane] = __float2bfloat16_rn(o[c] * inv);
+  if (lane == 0 && g.lse) g.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
 }
 
 template <int BITS, int DP, int NQ>
-cudaError_t launch(const xp_attn_args& g, const Quant& z, cudaStream_t s) {
+cudaError_t launch(const xp_attn_args& g, const Quant& z, int sms, cudaStream_t s) {
   using C = Cfg<BITS, DP, NQ>;
   static unsigned long long allowed = 0;
   const cudaError_t e = xp_allow_smem((const void*)attn_quant_kernel<BITS, DP, NQ>, C::SMEM, &allowed);
   if (e != cudaSuccess) return e;
-  const xp_attn_plan& p = g.plan;
-  const dim3 grid(p.prefix_tiles * p.prefix_splits + g.a.N * p.tail_tiles * p.tail_splits, g.kv_heads);
-  attn_quant_kernel<BITS, DP, NQ><<<grid, kThreads, C::SMEM, s>>>(g, z);
+  static_assert(C::RESIDENT <= kMostResident, "places for pieces");
+  attn_quant_kernel<BITS, DP, NQ><<<sms * C::RESIDENT, kThreads, C::SMEM, s>>>(g, z);
   return cudaGetLastError();
 }
 template <int BITS, int DP>
-cudaError_t launch_rows(const xp_attn_args& g, const Quant& z, cudaStream_t s) {
+cudaError_t launch_rows(const xp_attn_args& g, const Quant& z, int sms, cudaStream_t s) {
   switch (g.plan.rows_tile) {
-    case 8: return launch<BITS, DP, 1>(g, z, s);
-    case 16: return launch<BITS, DP, 2>(g, z, s);
+    case 8: return launch<BITS, DP, 1>(g, z, sms, s);
+    case 16: return launch<BITS, DP, 2>(g, z, sms, s);
     default:
-      if constexpr (DP <= 128) return launch<BITS, DP, 4>(g, z, s);
+      if constexpr (DP <= 128) return launch<BITS, DP, 4>(g, z, sms, s);
       else return cudaErrorInvalidValue;
   }
 }
-template <int BITS> cudaError_t launch_dims(const xp_attn_args& g, const Quant& z, cudaStream_t s) {
-  return g.dim <= 64 ? launch_rows<BITS, 64>(g, z, s)
-         : g.dim <= 128 ? launch_rows<BITS, 128>(g, z, s)
-                        : launch_rows<BITS, 256>(g, z, s);
+template <int BITS> cudaError_t launch_dims(const xp_attn_args& g, const Quant& z, int sms, cudaStream_t s) {
+  return g.dim <= 64 ? launch_rows<BITS, 64>(g, z, sms, s)
+         : g.dim <= 128 ? launch_rows<BITS, 128>(g, z, sms, s)
+                        : launch_rows<BITS, 256>(g, z, sms, s);
 }
 
 }  // namespace
@@ -595,8 +816,8 @@ static xp_attn wide_call(const xp_attn& a, const xp_attn_plan& p) {
 }
 
 // Row tiles of 8, 16 or 32 queries (heads wider than 128: 8 or 16, their results fill the registers): the
-// least that hold a sequence's rows of one kv head, or where there is a prefix the batch's.  Key ranges of
-// whole rounds of the four warps, so that the units fill the GPU about four times over.
+// least that hold a sequence's rows of one kv head, or where there is a prefix the batch's.  Where the work is
+// cut is found on the device, from the lengths.
 xp_attn_plan xp_attn_quant_plan(const xp_cache* c, const xp_attn* a) {
   xp_attn_plan p = {};
   const int group = a->heads / c->d.kv_heads, per_seq = a->T * group, D = c->d.head_dim;
@@ -637,20 +858,21 @@ xp_attn_plan xp_attn_quant_plan(const xp_cache* c, const xp_attn* a) {
   const int prefix_len = p.wide_prefix ? 0 : a->prefix_len;
   const int64_t seen = (int64_t)per_seq * (prefix_len > 0 ? a->N : 1);
   p.rows_tile = seen <= 8 ? 8 : seen <= 16 || D > 128 ? 16 : 32;
-  const int round = kWarps * kStep;
-  p.prefix_tiles = p.wide_prefix ? 0 : (int)(((int64_t)a->N * per_seq + p.rows_tile - 1) / p.rows_tile);
+  p.prefix_tiles = prefix_len > 0 ? (int)(((int64_t)a->N * per_seq + p.rows_tile - 1) / p.rows_tile) : 0;
   p.tail_tiles = (per_seq + p.rows_tile - 1) / p.rows_tile;
-  auto rounds = [&](int keys) { return ((int64_t)keys + round - 1) / round; };
-  const int64_t all = (p.prefix_tiles * rounds(prefix_len) +
-                       (int64_t)a->N * p.tail_tiles * rounds(a->max_len)) * c->d.kv_heads;
-  const int64_t want = (int64_t)c->num_sms * 16, each = std::max<int64_t>(1, (all + want - 1) / want);
-  auto splits = [&](int keys, int* range) {
-    *range = (int)(std::min<int64_t>(each, std::max<int64_t>(1, rounds(keys))) * round);
-    return keys > 0 ? (keys - 1) / *range + 1 : 0;
-  };
-  p.prefix_splits = p.wide_prefix ? 1 : splits(prefix_len, &p.prefix_keys);   // 1: what tcgen05 leaves
-  p.tail_splits = splits(a->max_len, &p.tail_keys);
-  p.parts = p.prefix_splits + p.tail_splits;
+  const size_t H = c->d.kv_heads;
+  p.units = H * p.prefix_tiles + (a->max_len > 0 ? (size_t)a->N * H * p.tail_tiles : 0);
+  const size_t places = ((size_t)p.units + (size_t)c->num_sms * kMostResident) * p.rows_tile;
+  size_t o = p.total;
+  auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
+  p.line_off = take(((size_t)a->N + 1) * 8);
+  p.stat_off = take(places * 8);
+  p.acc_off = take(places * D * 4);
+  if (p.wide_prefix) {
+    p.part_stat = take((size_t)a->N * a->T * a->heads * 8);
+    p.part_acc = take((size_t)a->N * a->T * a->heads * D * 4);
+  }
+  p.total = o;
   return p;
 }
 
@@ -685,14 +907,25 @@ cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaS
     w.line = (int*)(g.ws + p.wide_line);
     w.stat = (float*)(g.ws + p.wide_stat);
     w.acc = (float*)(g.ws + p.wide_acc);
-    if (!p.tc) w.part_stat = g.stat, w.part_acc = g.acc;   // the first range
+    if (!p.tc) {
+      w.part_stat = (float*)(g.ws + p.part_stat);
+      w.part_acc = (float*)(g.ws + p.part_acc);
+    }
     e = xp_launch_attn_tc(&wide, w, s);
     if (e != cudaSuccess || p.tc) return e;
   }
-  const xp_quant_sizes q = xp_quant_of(c->d.page_size, c->d.head_dim, c->d.dtype);
-  const Quant z = {q.code, q.scale, c->d.page_size * q.code};
-  cudaError_t e = cudaSuccess;
-  if (p.parts > (p.wide_prefix ? 1 : 0)) e = c->d.dtype == XP_Q8 ? launch_dims<8>(g, z, s) : launch_dims<4>(g, z, s);
-  // a row of one range is written out by that kernel
-  return e == cudaSuccess && p.parts != 1 ? xp_launch_attn_combine(g, s) : e;
+  xp_attn_args q = g;
+  if (p.wide_prefix) {
+    q.part_stat = (float*)(g.ws + p.part_stat);
+    q.part_acc = (float*)(g.ws + p.part_acc);
+  }
+  const xp_quant_sizes size = xp_quant_of(c->d.page_size, c->d.head_dim, c->d.dtype);
+  const int64_t strides = (g.a.N > 1 ? g.a.q_stride_n : 0) | (g.a.T > 1 ? g.a.q_stride_t : 0) |
+                          (g.a.heads > 1 ? g.a.q_stride_h : 0);
+  const Quant z = {size.code, size.scale, c->d.page_size * size.code,
+                   (uintptr_t)g.q % 16 == 0 && strides % 8 == 0};
+  const cudaError_t e = c->d.dtype == XP_Q8 ? launch_dims<8>(q, z, c->num_sms, s) : launch_dims<4>(q, z, c->num_sms, s);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
+  return xp_launch_pdl(attn_quant_combine_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, q);
 }

@@ -34,18 +34,19 @@ namespace xpq {
 template <int BITS> struct Codes {
   static constexpr int kMost = (1 << (BITS - 1)) - 1;   // greatest code
   static constexpr int kZero = 1 << (BITS - 1);         // how code 0 is held
-  // greatest scale: the last for which kMost * s is a finite 16-bit float (9216, 512)
-  static constexpr unsigned kTop = BITS == 4 ? 0xE1u : 0xC0u;
+  // greatest scale: the last for which kMost * s is a finite 16-bit float (512); of 4 bits 7680, for which
+  // 1024 * s * 2^-7 is
+  static constexpr unsigned kTop = BITS == 4 ? 0xDFu : 0xC0u;
 };
 
 __device__ __forceinline__ float scale_of(unsigned byte) {
   return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
 
-// A query row of largest magnitude `top` as fp16: times 2^-e, e its exponent (0 for a row of zeros; what is
+// A query row of largest magnitude `top` as fp16: times 2^-e, e its exponent, 2^-119 at least (what is
 // not finite stays so), which is exact but for what lies 2^-14 and more below the largest; *up: 2^e.
 __device__ __forceinline__ float row_scale(float top, float* up) {
-  const int e = min(max((int)(__float_as_uint(top) >> 23), 1), 253);
+  const int e = min(max((int)(__float_as_uint(top) >> 23), 8), 253);   // so that 2^-e times 16 is finite too
   *up = __uint_as_float((uint32_t)e << 23);
   return __uint_as_float((uint32_t)(254 - e) << 23);
 }

@@ -267,7 +267,9 @@ struct xp_attn_plan {
   int wide_prefix, wide_tail;
   int64_t wide_plane;
   size_t wide_k, wide_v, wide_table, wide_q, wide_factor;
-  size_t wide_stat, wide_acc, wide_line;   // and the tcgen05 form's own workspace
+  size_t wide_stat, wide_acc, wide_line;   // the tcgen05 form's own workspace
+  size_t part_stat, part_acc;              // and what it leaves of the prefix
+  int64_t units;                           // row tiles of kv heads, of the prefix and of all tails
   // workspace: (max, sum) pairs, accumulators; tensor-core form: where each sequence's work begins
   size_t stat_off, acc_off, line_off, total;
 };
@@ -280,8 +282,8 @@ struct xp_attn_args {
   int64_t ld_table;
   void* out;
   float* lse;
-  float* stat;                   // CUDA-core and quantised forms: [parts][N*T*heads][2]
-  float* acc;                    //                                [parts][N*T*heads][dim]
+  float* stat;                   // CUDA-core form: [parts][N*T*heads][2]
+  float* acc;                    //                 [parts][N*T*heads][dim]
   int* line;
   // tcgen05 form: not null where q, k and v are fp16: what a product of query row r (rows of a kv head
   // together, [kv_heads][N*T*group]) is multiplied by to be a score in base 2
@@ -298,7 +300,6 @@ int xp_attn_tc_maps(xp_cache* c);   // tokens of a TMA box, 0 where the kernel c
 xp_attn_plan xp_attn_tc_plan(const xp_cache* c, const xp_attn* a);
 cudaError_t xp_launch_attn_tc(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
 cudaError_t xp_launch_attn_simt(const xp_cache* c, const xp_attn_args& g, cudaStream_t s);
-// joins the ranges of either form
 cudaError_t xp_launch_attn_combine(const xp_attn_args& g, cudaStream_t s);
 cudaError_t xp_launch_widen(const xp_cache* c, const xp_attn_args& g, int prefix_pages, int tail_pages,
                             void* k, void* v, int64_t plane, int32_t* table, void* q, float* q_factor,

@@ -14,9 +14,8 @@ def most_of(bits):
 
 
 def top_byte(bits):
-    """The greatest scale for which the greatest code still is a finite 16-bit float."""
-    s = scale_values()
-    return max(b for b in range(0xF8) if s[b] * most_of(bits) <= 65504)
+    """The greatest scale: 512 of 8 bits, 7680 of 4."""
+    return int(np.nonzero(scale_values()[:0xF8] == (512 if bits == 8 else 7680))[0][0])
 
 
 def quantise(x, bits):

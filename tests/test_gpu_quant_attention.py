@@ -7,7 +7,11 @@ sum |q||k|, and a quotient of weighted sums within 2 dz A; sums over n keys with
 2^-21.  Queries are exact in fp16 where they lie within 2^14 of their row's largest, and lose less than 2^-25 of
 that otherwise, which is below dz.  A weight is held as 2^(z - m + 6) with m at most the row's largest
 score, so the largest is at least 2^6; where that of a key is below 2^-14, fp16 is a fixed grid of 2^-24 and
-it is off by up to 2^-25, 2^-31 of the largest and so of the sum: together 2^-31 sum_j |v_j|.  lse: dz + n 2^-23 + 2^-21 (1 + |lse|).
+it is off by up to 2^-25, 2^-31 of the largest and so of the sum: together 2^-31 sum_j |v_j|.  Codes of 4 bits
+are summed as they are held, c + 8 <= 15, and 8 times the weighted mean B of their scales is taken off:
+sums of up to 15 B and 8 B, each within (n + 8) 2^-23, (n + 8) 2^-23 23 B together (the least scale that reaches a
+group's largest leaves it a code of 3 or more, so a scale is at most a third of what is held there).
+lse: dz + n 2^-23 + 2^-21 (1 + |lse|).
 Where many queries see each key the cache is widened to fp16 first, exactly, and all else is the same."""
 import math
 
@@ -84,9 +88,13 @@ def check(bits, N, T, H, G, D, ps, prefix, lens, seed=0, layer=0, layers=1, scal
         k, v = (np.concatenate([h[0], h[n + 1]]) for h in held)
         sees = [prefix + max(0, lens[n] - T + 1 + t) for t in range(T)]
         want, want_lse, mean, size = Q.attention(qs[n], k, v, sees, scale)
+        held_as = 0.0
+        if bits == 4:
+            step = np.abs(v).reshape(len(v), H, D // 16, 16).max(-1).repeat(16, -1) / 3
+            held_as = Q.attention(qs[n], k, step, sees, scale)[0] * 23 * (len(k) + 8) * 2.0 ** -23
         dz = (D + 8) * 2.0 ** -22 * size
         tol = 2.0 ** -8 * np.abs(want) + mean * (2.0 ** -11 + 2 * dz + len(k) * 2.0 ** -23 + 2.0 ** -20)[..., None] \
-            + 2.0 ** -31 * np.abs(v).sum(0).repeat(G, 0) + 1e-30
+            + 2.0 ** -31 * np.abs(v).sum(0).repeat(G, 0) + held_as + 1e-30
         assert (np.abs(got[n] - want) <= tol).all(), (n, np.max(np.abs(got[n] - want) / tol))
         seen = np.isfinite(want_lse)
         assert (got_lse[n][~seen] == -np.inf).all() and (got[n][~seen] == 0).all()

@@ -12,7 +12,7 @@ def test_scales_are_floats_of_five_and_three_bits():
     assert s[0] == 0 and s[1] == 2.0 ** -17 and s[7] == 7 * 2.0 ** -17 and s[8] == 2.0 ** -14
     assert s[120] == 1.0 and s[121] == 1.125 and s[127] == 1.875 and s[128] == 2.0
     assert all(np.diff(s[:0xF8]) > 0)
-    assert Q.top_byte(4) == 0xE1 and s[0xE1] == 9216 and Q.top_byte(8) == 0xC0 and s[0xC0] == 512
+    assert Q.top_byte(4) == 0xDF and s[0xDF] == 7680 and Q.top_byte(8) == 0xC0 and s[0xC0] == 512
 
 
 @pytest.mark.parametrize("bits", [4, 8])
@@ -38,7 +38,7 @@ def test_what_does_not_fit():
     x = np.zeros((2, 16))
     x[0, 0], x[1, 3] = np.nan, -np.inf
     codes, byte, bad = Q.quantise(x, 4)
-    assert bad and codes[0, 0] == 0 and codes[1, 3] == -7 and byte[1, 0] == 0xE1
+    assert bad and codes[0, 0] == 0 and codes[1, 3] == -7 and byte[1, 0] == 0xDF
 
 
 @pytest.mark.parametrize("bits,dim,ps", [(4, 128, 16), (4, 80, 5), (8, 64, 3), (8, 256, 20)])
