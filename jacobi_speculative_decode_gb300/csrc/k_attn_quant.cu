@@ -48,6 +48,7 @@ constexpr int kMinChunk = 2;          // least work of a CTA, in rounds
 struct Quant {
   int code, scale, scale_at;   // bytes of a token's codes and scales; where a head's scales begin
   bool q_wide;                 // queries by 16 bytes
+  bool runs;                   // 16 tokens from a multiple of 16 on lie side by side, as in the ring
 };
 
 // The work is one line of cost: the prefix's units (kv head by kv head, row tile by row tile), then those
@@ -167,27 +168,24 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 __device__ __forceinline__ __half2 h2(uint32_t v) { return *(const __half2*)&v; }
 __device__ __forceinline__ uint32_t u32(__half2 v) { return *(const uint32_t*)&v; }
-// two scales as fp16: the bytes lo and hi
-__device__ __forceinline__ __half2 scales(uint32_t lo, uint32_t hi) { return h2(lo << 7 | hi << 23); }
+// two scales as fp16: the bytes lo and hi (by multiplies: what widens codes fills the logic pipe)
+__device__ __forceinline__ __half2 scales(uint32_t lo, uint32_t hi) { return h2((hi * 65536u + lo) * 128u); }
 
 // Codes of 4 bits as they are held, c + 8 = 0..15, times a scale: pairs j = 0..3 of either half of w.
-// 1024 + c and 1024 + 16 c are fp16 numbers with c in their last bits, so one multiply-add gives
-// (1024 + c) s - 1024 s, exactly.  Two factors stay: odd pairs come 16 times too large (the queries' dims
-// there are 1/16, and the results' are divided at the end), and scales are s 2^-7, so that 1024 s is finite
-// and c s down to the least scale is whole 2^-24.  What the 8 too much brings is one product more for
-// every 16 keys: 8 sum_d s q_d for scores, 8 sum_j s p_j for results.
+// 8 + c/128 and 8 + 16 c/128 are fp16 numbers with c in their last bits, so one multiply-add gives
+// (8 + c/128) s - 8 s = c s / 128, exactly (8 s is finite, and c s down to the least scale is whole 2^-17).
+// Odd pairs come 16 times too large: the queries' dims there are 1/16 of the others', and the results' are
+// divided at the end.  What the 8 too much brings is one product more for every 16 keys: 8 sum_d s q_d for
+// scores, 8 sum_j s p_j for results.
 struct Scale4 {
   __half2 s, base;
 };
-__device__ __forceinline__ Scale4 scale4(__half2 s) {
-  const __half2 t = __hmul2(s, h2(0x20002000u));          // 2^-7
-  return {t, __hmul2(t, h2(0xE400E400u))};                // -1024
-}
+__device__ __forceinline__ Scale4 scale4(__half2 s) { return {s, __hmul2(s, h2(0xC800C800u))}; }   // -8
 __device__ __forceinline__ void widen4(uint32_t w, Scale4 f, uint32_t (&out)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    out[2 * i] = u32(__hfma2(h2((w & 0x000F000Fu) | 0x64006400u), f.s, f.base));
-    out[2 * i + 1] = u32(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), f.s, f.base));
+    out[2 * i] = u32(__hfma2(h2((w & 0x000F000Fu) | 0x48004800u), f.s, f.base));
+    out[2 * i + 1] = u32(__hfma2(h2((w & 0x00F000F0u) | 0x48004800u), f.s, f.base));
     w >>= 8;
   }
 }
@@ -310,7 +308,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
         }
       }
     };
-    if (z.code % 16 == 0) codes(std::integral_constant<int, 16>());
+    if (z.runs) {   // half a step at a time, a lane 16 bytes
+      constexpr int PIECES = C::CODE / 32;
+      const uint32_t d = to + lane * 16;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int64_t from = __shfl_sync(kAll, key_at, half * 16) + lane * 16;
+        if (in >> half * 16 & 1) {
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i) {
+            const int at = half * 16 * C::CODE + i * 512;
+            copy_async(d + at, (const char*)g.k + from + i * 512, 16);
+            copy_async(d + at + kStep * C::CODE, (const char*)g.v + from + i * 512, 16);
+          }
+        }
+      }
+    } else if (z.code % 16 == 0) codes(std::integral_constant<int, 16>());
     else codes(std::integral_constant<int, 8>());
     // a key behind the end: scales of 0, so that whatever codes the ring holds there are worth nothing
     const uint32_t d = to + 2 * kStep * C::CODE + lane * C::SCALE, dv = d + kStep * C::SCALE;
@@ -402,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
       for (int e = 0; e < (KG > 1 ? 2 : 1); ++e)
 #pragma unroll
         for (int j = 0; j < 16; ++j) sum[e] += x[(2 * i + e) * 16 + j] * down;
-      const float h0 = -8.0f * sum[0], h1 = -8.0f * sum[1];
+      const float h0 = -8.0f / C::UNIT * sum[0], h1 = -8.0f / C::UNIT * sum[1];
       const uint32_t hi = pack(h0, h1);
       qb[q][2 * i] = hi;
       qb[q][2 * i + 1] = pack(h0 - __low2float(h2(hi)), h1 - __high2float(h2(hi)));
@@ -430,6 +443,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     for (int i = 0; i < 2; ++i) m[q][i] = -INFINITY, l[q][i] = 0.0f;
   }
   const int groups = D / 16;
+  // the groups of a lane's key that there are, as bytes
+  const int k_count = min(max(groups - t4 * KG, 0), KG);
+  const uint32_t k_groups = k_count >= 4 ? 0xFFFFFFFFu : (1u << k_count * 8) - 1;
 
   for (int it = 0; it < mine; ++it) {
     wait_groups<C::STAGES - 2>();
@@ -453,14 +469,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[kt][q][e] = 0.0f;
-      uint32_t w[2][KW], byte[2][KG];   // scales of the lane's groups
+      uint32_t w[2][KW], bytes[2];   // scales of the lane's groups
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int key = kt * 16 + r * 8 + gr;
         load_words<KW>(sk + key * C::CODE + t4 * (C::CODE / 4), w[r]);
-#pragma unroll
-        for (int i = 0; i < KG; ++i)
-          byte[r][i] = t4 * KG + i < groups ? ks[key * C::SCALE + t4 * KG + i] : 0;
+        const uint8_t* from = ks + key * C::SCALE + t4 * KG;
+        bytes[r] = (KG == 1 ? *from : KG == 2 ? *(const uint16_t*)from : *(const uint32_t*)from) & k_groups;
       }
       Scale4 sc4[2][KG];
       __half2 sc8[2][KG];
@@ -468,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int i = 0; i < KG; ++i) {
-          sc8[r][i] = scales(byte[r][i], byte[r][i]);
+          sc8[r][i] = KG == 1 ? h2(bytes[r] * 0x00800080u)
+                              : h2(__byte_perm(bytes[r], 0, 0x4040 + 0x0101 * i) * 128u);
           if constexpr (BITS == 4) sc4[r][i] = scale4(sc8[r][i]);
         }
 #pragma unroll
@@ -645,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
       const float even = C::UNIT * f, odd = BITS == 4 ? even * 0.0625f : even;
 #pragma unroll
       for (int j = 0; j < KS; j += 2) {
-        const float over = VB ? 8.0f * even * ob[q][VG > 1 && j >= KS / 2 ? 2 + i : i] : 0.0f;
+        const float over = VB ? 8.0f * f * ob[q][VG > 1 && j >= KS / 2 ? 2 + i : i] : 0.0f;
         *(float4*)(to + 2 * j) = make_float4(o[q][j][i] * even - over, o[q][j][2 + i] * even - over,
                                              o[q][j + 1][i] * odd - over, o[q][j + 1][2 + i] * odd - over);
       }
@@ -922,8 +938,9 @@ cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaS
   const xp_quant_sizes size = xp_quant_of(c->d.page_size, c->d.head_dim, c->d.dtype);
   const int64_t strides = (g.a.N > 1 ? g.a.q_stride_n : 0) | (g.a.T > 1 ? g.a.q_stride_t : 0) |
                           (g.a.heads > 1 ? g.a.q_stride_h : 0);
-  const Quant z = {size.code, size.scale, c->d.page_size * size.code,
-                   (uintptr_t)g.q % 16 == 0 && strides % 8 == 0};
+  const int D = c->d.head_dim;
+  const Quant z = {size.code, size.scale, c->d.page_size * size.code, (uintptr_t)g.q % 16 == 0 && strides % 8 == 0,
+                   c->d.page_size % 16 == 0 && (D == 64 || D == 128 || D == 256)};
   const cudaError_t e = c->d.dtype == XP_Q8 ? launch_dims<8>(q, z, c->num_sms, s) : launch_dims<4>(q, z, c->num_sms, s);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
