@@ -171,6 +171,18 @@ __device__ __forceinline__ uint32_t u32(__half2 v) { return *(const uint32_t*)&v
 // two scales as fp16: the bytes lo and hi (by multiplies: what widens codes fills the logic pipe)
 __device__ __forceinline__ __half2 scales(uint32_t lo, uint32_t hi) { return h2((hi * 65536u + lo) * 128u); }
 
+// w & mask | magic in one instruction: of two constants one has to be in a register, and the compiler, where it
+// sees both, takes two instructions (which cost long contexts 10% of their time)
+__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+
 // Codes of 4 bits as they are held, c + 8 = 0..15, times a scale: pairs j = 0..3 of either half of w.
 // 8 + c/128 and 8 + 16 c/128 are fp16 numbers with c in their last bits, so one multiply-add gives
 // (8 + c/128) s - 8 s = c s / 128, exactly (8 s is finite, and c s down to the least scale is whole 2^-17).
@@ -181,17 +193,17 @@ struct Scale4 {
   __half2 s, base;
 };
 __device__ __forceinline__ Scale4 scale4(__half2 s) { return {s, __hmul2(s, h2(0xC800C800u))}; }   // -8
-__device__ __forceinline__ void widen4(uint32_t w, Scale4 f, uint32_t (&out)[4]) {
+__device__ __forceinline__ void widen4(uint32_t w, Scale4 f, uint32_t magic, uint32_t (&out)[4]) {   // 0x48004800
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    out[2 * i] = u32(__hfma2(h2((w & 0x000F000Fu) | 0x48004800u), f.s, f.base));
-    out[2 * i + 1] = u32(__hfma2(h2((w & 0x00F000F0u) | 0x48004800u), f.s, f.base));
+    out[2 * i] = u32(__hfma2(h2(pick(w, 0x000F000Fu, magic)), f.s, f.base));
+    out[2 * i + 1] = u32(__hfma2(h2(pick(w, 0x00F000F0u, magic)), f.s, f.base));
     w >>= 8;
   }
 }
 // one pair of codes of 8 bits: the low byte of either half of w
-__device__ __forceinline__ uint32_t widen8(uint32_t w, __half2 s) {
-  return u32(__hmul2(__hadd2(h2((w & 0x00FF00FFu) | 0x64006400u), h2(0xE480E480u)), s));   // -1152
+__device__ __forceinline__ uint32_t widen8(uint32_t w, __half2 s, uint32_t magic) {   // 0x64006400: 1024 + c + 128
+  return u32(__hmul2(__hadd2(h2(pick(w, 0x00FF00FFu, magic)), h2(0xE480E480u)), s));   // -1152
 }
 
 // NW 32-bit words of shared memory, from a boundary of their size
@@ -247,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     u = (int)((x0 - s_start.base) / cost_of(keys));
     at = s_start.base + (int64_t)u * cost_of(keys);
   }
+  const uint32_t magic = in_register(BITS == 4 ? 0x48004800u : 0x64006400u);
   const int more = kRound / g.page_size, rest = kRound % g.page_size;   // a round further in a table
 
   while (true) {   // unit by unit; the same in every thread
@@ -502,11 +515,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if constexpr (BITS == 4) {
-            widen4(w[r][i / 2], sc4[r][i / 4], a[r]);
+            widen4(w[r][i / 2], sc4[r][i / 4], magic, a[r]);
           } else {
 #pragma unroll
             for (int p = 0; p < 4; ++p)   // bytes 0, 1 or 2, 3 of a word, one in each half
-              a[r][p] = widen8(__byte_perm(w[r][i + p / 2], 0, p % 2 ? 0x4342 : 0x4140), sc8[r][i / 4]);
+              a[r][p] = widen8(__byte_perm(w[r][i + p / 2], 0, p % 2 ? 0x4342 : 0x4140), sc8[r][i / 4], magic);
           }
         }
 #pragma unroll
@@ -612,14 +625,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
         for (int r = 0; r < 2; ++r) {
           if constexpr (BITS == 4) {
             uint32_t even[4], odd[4];
-            widen4(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x5410), sc4[r][gi], even);
-            widen4(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x7632), sc4[r][gi], odd);
+            widen4(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x5410), sc4[r][gi], magic, even);
+            widen4(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x7632), sc4[r][gi], magic, odd);
 #pragma unroll
             for (int j = 0; j < 4; ++j) a[r][2 * j] = even[j], a[r][2 * j + 1] = odd[j];
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              a[r][j] = widen8(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x0400 + 0x0101 * j), sc8[r][gi]);
+              a[r][j] = widen8(__byte_perm(w[2 * r][i], w[2 * r + 1][i], 0x0400 + 0x0101 * j), sc8[r][gi], magic);
           }
         }
 #pragma unroll
