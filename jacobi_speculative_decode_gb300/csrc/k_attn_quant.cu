@@ -283,31 +283,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     return true;
   };
 
-  // The loads of a step.  A lane finds the place of the key that it is for, a step ahead.
+  // The loads of a step.  A lane asks for the page of the key that it is for a step ahead, and looks at the
+  // answer when the loads are made.
   char* ring = smem + warp * (C::STAGES * C::STAGE);
   const uint32_t ring_at = ptx::smem_u32(ring);
-  int64_t key_at = 0;   // of this lane's key in the step to be loaded: its codes,
-  int scale_at = 0;     // and its scales from there
+  int key = k0 + warp * kStep + lane, col = key / g.page_size, at_page = key - col * g.page_size;
+  int page = 0, in_page = 0;
   bool key_in = false;
-  int key = k0 + warp * kStep + lane, col = key / g.page_size, at = key - col * g.page_size;
   auto find = [&]() {   // the next step's
     key_in = key < k1;
-    if (!key_in) return;
-    int p = table[col];
-    if (p < 0 || p >= g.pages) {
-      atomicOr(g.err, XP_ERR_BADPAGE);
-      p = p < 0 ? 0 : g.pages - 1;
-    }
-    key_at = p * g.kv_page + hk * g.kv_head + (int64_t)at * z.code;
-    scale_at = z.scale_at + at * (z.scale - z.code);
+    if (key_in) page = table[col];
+    in_page = at_page;
     key += kRound;
     col += more;
-    at += rest;
-    if (at >= g.page_size) at -= g.page_size, ++col;
+    at_page += rest;
+    if (at_page >= g.page_size) at_page -= g.page_size, ++col;
   };
   auto load = [&](int stage) {
     const uint32_t to = ring_at + stage * C::STAGE;
     const uint32_t in = __ballot_sync(kAll, key_in);
+    if (key_in && (page < 0 || page >= g.pages)) {
+      atomicOr(g.err, XP_ERR_BADPAGE);
+      page = page < 0 ? 0 : g.pages - 1;
+    }
+    const int64_t key_at = page * g.kv_page + hk * g.kv_head + (int64_t)in_page * z.code;   // its codes,
+    const int scale_at = z.scale_at + in_page * (z.scale - z.code);                        // its scales from there
     auto codes = [&](auto piece_bytes) {
       constexpr int PB = decltype(piece_bytes)::value, PIECES = C::CODE / PB;   // of a token
 #pragma unroll
@@ -718,6 +718,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
 // One warp a query row: what tcgen05 left of its prefix, and the pieces of its prefix and of its tail (the
 // unit's own and those of the CTAs at whose beginning it was cut), brought to a common maximum:
 //   out = sum_p a_p O_p / sum_p a_p l_p,  a_p = 2^(m_p - m).
+// A lane holds E dims.  Bound by the latency of what it asks for, so four pieces are asked for at once.
+template <int E>
 __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_constant__ xp_attn_args g) {
   ptx::pdl_wait();
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
@@ -727,29 +729,38 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
   const int h = (int)(row % g.a.heads), t = (int)(row / g.a.heads % g.a.T);
   const int n = (int)(row / g.a.heads / g.a.T), hk = h / g.group, i = t * g.group + h % g.group;
   const int64_t* line = (const int64_t*)g.line;
-  const int64_t chunk = line[0];
+  const int64_t chunk = line[0], begin = g.a.max_len > 0 ? line[1 + n] : 0;
+  const bool dims = lane * E < D;
 
-  float o[8], m = -INFINITY, l = 0.0f;
+  float o[E], m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) o[c] = 0.0f;
-  auto add = [&](float2 st, const float* acc) {   // a piece, the same in all lanes
-    if (st.y == 0.0f) return;                     // no visible key: acc may hold anything
-    float x[8];
+  for (int c = 0; c < E; ++c) o[c] = 0.0f;
+  auto load = [&](const float* acc, float (&x)[E]) {
+    if constexpr (E == 2) {
+      const float2 v = __ldcg((const float2*)(acc + lane * 2));
+      x[0] = v.x, x[1] = v.y;
+    } else {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) x[c] = c * 32 + lane < D ? __ldcg(acc + c * 32 + lane) : 0.0f;
+      for (int c = 0; c < E; c += 4) {
+        const float4 v = __ldcg((const float4*)(acc + lane * E + c));
+        x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
+      }
+    }
+  };
+  auto add = [&](float2 st, const float (&x)[E]) {   // a piece that has a visible key
     const float now = fmaxf(m, st.x), a = exp2f(m - now), b = exp2f(st.x - now);
     m = now;
     l = l * a + st.y * b;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) o[c] = o[c] * a + x[c] * b;
+    for (int c = 0; c < E; ++c) o[c] = o[c] * a + x[c] * b;
   };
   auto pieces = [&](int keys, int64_t at, int64_t unit, int r) {
     const int T = rounds_of(keys), cost = cost_of(keys);
     const int64_t c0 = at / chunk, c1 = (at + cost - 1) / chunk;
     for (int64_t first = c0; first <= c1; first += 32) {   // a lane a CTA
       const int64_t c = first + lane;
-      int64_t from = -1;
-      float2 st = make_float2(0.0f, 0.0f);
+      int64_t from = 0;
+      float2 st = make_float2(0.0f, 0.0f);   // of no piece, and where no key was visible: acc may hold anything
       if (c <= c1) {
         const int r0 = round_at(c * chunk - at, T), r1 = round_at(min((c + 1) * chunk - at, (int64_t)cost), T);
         if (r0 < r1) {
@@ -758,14 +769,28 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
         }
       }
       const int count = (int)min((int64_t)32, c1 - first + 1);
-#pragma unroll 2
-      for (int k = 0; k < count; ++k) {
-        const float2 s = make_float2(__shfl_sync(kAll, st.x, k), __shfl_sync(kAll, st.y, k));
-        add(s, g.acc + __shfl_sync(kAll, from, k) * D);
+      for (int k = 0; k < count; k += 4) {
+        float2 s[4];
+        float x[4][E];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t f = __shfl_sync(kAll, from, min(k + j, 31));
+          s[j] = make_float2(__shfl_sync(kAll, st.x, min(k + j, 31)), __shfl_sync(kAll, st.y, min(k + j, 31)));
+          if (k + j >= count) s[j].y = 0.0f;
+          if (dims && s[j].y != 0.0f) load(g.acc + f * D, x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (s[j].y != 0.0f) add(s[j], x[j]);
       }
     }
   };
-  if (g.part_stat) add(__ldcg((const float2*)g.part_stat + row), g.part_acc + row * D);
+  if (g.part_stat) {
+    const float2 st = __ldcg((const float2*)g.part_stat + row);
+    float x[E];
+    if (dims) load(g.part_acc + row * D, x);
+    if (st.y != 0.0f) add(st, x);
+  }
   const int units = g.kv_heads * g.plan.prefix_tiles;
   if (units > 0 && g.a.prefix_len > 0) {
     const int at_row = n * per_seq + i, u = hk * g.plan.prefix_tiles + at_row / RT;
@@ -774,14 +799,26 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
   if (g.a.max_len > 0) {
     const int keys = tail_len(g, n, false), u = hk * g.plan.tail_tiles + i / RT;
     if (keys > 0)
-      pieces(keys, line[1 + n] + (int64_t)u * cost_of(keys), units + (int64_t)n * g.kv_heads * g.plan.tail_tiles + u,
-             i % RT);
+      pieces(keys, begin + (int64_t)u * cost_of(keys), units + (int64_t)n * g.kv_heads * g.plan.tail_tiles + u, i % RT);
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // NaN where a visible score is
-  bf16* out = (bf16*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h;
+  bf16* out = (bf16*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h + lane * E;
+  if (dims) {
+    if ((uintptr_t)out % (2 * E) == 0) {
+      uint32_t v[E / 2];
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    if (c * 32 + lane < D) out[c * 32 + lane] = __float2bfloat16_rn(o[c] * inv);
+      for (int c = 0; c < E; c += 2) {
+        const __nv_bfloat162 w = __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
+        v[c / 2] = *(const uint32_t*)&w;
+      }
+      if constexpr (E == 2) *(uint32_t*)out = v[0];
+      else if constexpr (E == 4) *(uint2*)out = make_uint2(v[0], v[1]);
+      else *(uint4*)out = make_uint4(v[0], v[1], v[E / 2 - 2], v[E / 2 - 1]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < E; ++c) out[c] = __float2bfloat16_rn(o[c] * inv);
+    }
+  }
   if (lane == 0 && g.lse) g.lse[row] = l != 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
 }
 
@@ -957,5 +994,8 @@ cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaS
   const cudaError_t e = c->d.dtype == XP_Q8 ? launch_dims<8>(q, z, c->num_sms, s) : launch_dims<4>(q, z, c->num_sms, s);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
-  return xp_launch_pdl(attn_quant_combine_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, q);
+  return xp_launch_pdl(D <= 64    ? attn_quant_combine_kernel<2>
+                       : D <= 128 ? attn_quant_combine_kernel<4>
+                                  : attn_quant_combine_kernel<8>,
+                       dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, q);
 }
