@@ -53,6 +53,27 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// two fp32 operations an instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 // the sums of a at a maximum m that is not below its own
 __device__ __forceinline__ void rebase(Stat& a, float m, float c) {
   if (a.s > 0.0f) {
@@ -69,23 +90,27 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
   return {m, a.s + b.s, a.w + b.w, a.ahead + b.ahead};
 }
 
+// 16 bytes of logits as floats, NaN as -inf
 template <typename T> struct Vec;
 template <> struct Vec<bf16> {
   static constexpr int N = 8;
   static __device__ __forceinline__ void get(const uint4& x, float (&f)[8]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const __nv_bfloat162 least = __float2bfloat162_rn(-INFINITY);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      const __nv_bfloat162 v = __hmax2(*(const __nv_bfloat162*)&w[i], least);
+      const uint32_t u = *(const uint32_t*)&v;
+      f[2 * i] = __uint_as_float(u * 65536u);   // a multiply: the logic pipe has enough to do
+      f[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
     }
   }
 };
 template <> struct Vec<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ void get(const uint4& x, float (&f)[4]) {
-    f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y);
-    f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
+    f[0] = fmaxf(__uint_as_float(x.x), -INFINITY), f[1] = fmaxf(__uint_as_float(x.y), -INFINITY);
+    f[2] = fmaxf(__uint_as_float(x.z), -INFINITY), f[3] = fmaxf(__uint_as_float(x.w), -INFINITY);
   }
 };
 // as the softmax reads a logit: NaN as -inf, +inf as the largest finite value
@@ -107,6 +132,19 @@ __device__ __forceinline__ u64 merge(u64 a, u64 b, int lane) {
     v = ((lane & o) == 0) == (v > w) ? v : w;
   }
   return v;
+}
+
+// The k-th largest of the lanes' values.
+__device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int o = size / 2; o > 0; o >>= 1) {
+      const float w = __shfl_xor_sync(kAll, v, o);
+      const bool falling = (lane & size) == 0 || size == 32;
+      v = ((lane & o) == 0) == falling ? fmaxf(v, w) : fminf(v, w);
+    }
+  return __shfl_sync(kAll, v, k - 1);
 }
 
 template <typename T, bool TOP>
@@ -141,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   const float inv_t = greedy ? 1.0f : fmaxf(1.0f / heat, FLT_MIN), c = inv_t * kLog2e;
   const float mine = read_logit(to_f(l[x]));
   // an id at -inf has all lower ids ahead of it, and of the higher ones those above -inf
-  const bool low = mine == -INFINITY;
+  const bool low_id = mine == -INFINITY;
 
   // vectors from the first 16-byte boundary on; this CTA's are [v0, v1)
   const int head = min(a.V, (int)((16 - ((uintptr_t)l & 15)) % 16 / sizeof(T)));
@@ -150,37 +188,50 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   const uint4* body = (const uint4*)(l + head);
 
   Stat st = {-FLT_MAX, 0.0f, 0.0f, 0};
+  uint64_t s2 = 0, w2 = 0;   // its sums while the row is read, of even and odd elements
+  const uint64_t c2 = pair(c, c);
+  const float below = low_id ? INFINITY : nextafterf(mine, -INFINITY);   // what an id before x has to be above
   u64 list = 0;
   float own = -INFINITY;      // an id has to be above it,
   float bound = -INFINITY;    // and not below this
   const int share = (a.top + kWarps - 1) / kWarps;   // entries a warp brings to the bound
-  if (TOP) {
-    if (threadIdx.x < kWarps) s_bound[threadIdx.x] = -INFINITY;
-    __syncthreads();
-  }
   volatile float* bounds = s_bound;
 
   // E elements of ids from `id` on
   auto take = [&](float (&f)[E], int id) {
     float most = f[0];
 #pragma unroll
-    for (int i = 1; i < E; ++i) most = fmaxf(most, f[i]);   // NaN left out
+    for (int i = 1; i < E; ++i) most = fmaxf(most, f[i]);
     if (most > FLT_MAX) {
 #pragma unroll
       for (int i = 0; i < E; ++i) f[i] = fminf(f[i], FLT_MAX);
       most = FLT_MAX;
     }
-    if (most > st.m) rebase(st, most, c);
+    if (most > st.m) {   // sums to the new maximum
+      const float d = (st.m - most) * c, by = ex2(d);
+      const uint64_t by2 = pair(by, by);
+      w2 = by > 0.0f ? mul2(fma2(pair(d, d), s2, w2), by2) : 0ull;
+      s2 = mul2(s2, by2);
+      st.m = most;
+    }
+    const uint64_t off = pair(-st.m, -st.m);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float d = (fmaxf(f[i], -INFINITY) - st.m) * c, e = ex2(d);
-      st.s += e;
-      st.w = fmaf(fmaxf(d, -FLT_MAX), e, st.w);   // nothing of -inf
+    for (int i = 0; i < E; i += 2) {
+      const uint64_t d = mul2(add2(pair(f[i], f[i + 1]), off), c2);
+      const uint64_t e = pair(ex2(low(d)), ex2(high(d)));
+      s2 = add2(s2, e);
+      w2 = fma2(pair(fmaxf(low(d), -FLT_MAX), fmaxf(high(d), -FLT_MAX)), e, w2);   // nothing of -inf
     }
     if (most >= mine) {
+      if (id <= x && x < id + E) {
 #pragma unroll
-      for (int i = 0; i < E; ++i)
-        st.ahead += low ? f[i] > mine && id + i > x : f[i] > mine || (f[i] == mine && id + i < x);
+        for (int i = 0; i < E; ++i)
+          st.ahead += low_id ? f[i] > mine && id + i > x : f[i] > mine || (f[i] == mine && id + i < x);
+      } else {
+        const float t = id < x ? below : mine;
+#pragma unroll
+        for (int i = 0; i < E; ++i) st.ahead += f[i] > t;
+      }
     }
     return most;
   };
@@ -215,24 +266,49 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
     float f[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) f[i] = -INFINITY;
-    if (id < to) f[0] = to_f(l[id]);
+    if (id < to) f[0] = fmaxf(to_f(l[id]), -INFINITY);
     const float most = take(f, id);
     if (TOP) look(f, most, id);
   };
-  if (warp == 0 && part == 0 && head > 0) ends(0, head);
-
-  for (int v = v0 + warp * 32; v < v1; v += kThreads * kLoads) {
-    uint4 raw[kLoads];
+  uint4 raw[kLoads];
+  auto load = [&](int v) {
     const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       const int at = v + u * kThreads + lane;
       raw[u] = at < v1 ? __ldcs(body + at) : make_uint4(none, none, none, none);
     }
+  };
+  load(v0 + warp * 32);
+  if (TOP) {
+    // A first bound, so that the lists begin with ids that are likely to stay: each warp's share-th largest of
+    // its lanes' largest.
+    float most = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       float f[E];
       Vec<T>::get(raw[u], f);
+#pragma unroll
+      for (int i = 0; i < E; ++i) most = fmaxf(most, f[i]);
+    }
+    most = kth_of_lanes(fminf(most, FLT_MAX), share, lane);
+    if (lane == 0) s_bound[warp] = most;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) most = fminf(most, s_bound[w]);
+    bound = most;
+  }
+  if (warp == 0 && part == 0 && head > 0) ends(0, head);
+
+  for (int v = v0 + warp * 32; v < v1; v += kThreads * kLoads) {
+    uint4 now[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) now[u] = raw[u];
+    load(v + kThreads * kLoads);   // the next ones are on their way meanwhile
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      float f[E];
+      Vec<T>::get(now[u], f);
       const int id = head + (v + u * kThreads + lane) * E;
       const float most = take(f, id);
       if (TOP) look(f, most, id);
@@ -240,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
     if (TOP) {
       // every warp has `share` ids at or above its own word: `top` of them are above the least
       const u64 e = __shfl_sync(kAll, list, share - 1);
-      if (lane == 0 && e) bounds[warp] = packed_val(e);
+      if (lane == 0 && e) bounds[warp] = fmaxf(bounds[warp], packed_val(e));
       float t = lane < kWarps ? bounds[lane] : INFINITY;
 #pragma unroll
       for (int o = kWarps / 2; o > 0; o >>= 1) t = fminf(t, __shfl_xor_sync(kAll, t, o));
@@ -249,6 +325,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   }
   if (warp == 0 && part == a.parts - 1 && head + vectors * E < a.V) ends(head + vectors * E, a.V);
 
+  st.s = low(s2) + high(s2);
+  st.w = low(w2) + high(w2);
   // the CTA's, in warp 0
   auto gather = [&]() {
 #pragma unroll
@@ -291,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   if (warp != 0) return;
 
   const float log_s = logf(st.s);   // s = 0: nothing above -inf
-  const int ahead = st.ahead + (low ? (int)x : 0);
+  const int ahead = st.ahead + (low_id ? (int)x : 0);
   auto log_p = [&](float v) { return greedy ? -INFINITY : (v - st.m) * inv_t - log_s; };
   if (lane == 0) {
     if (!(st.s > 0.0f)) atomicOr(a.err, XP_ERR_EMPTY);
