@@ -1,12 +1,16 @@
 // Log probabilities of given tokens, the entropy, the token's rank and the best alternatives: one pass
 // over the row.
 //
-// A row, or a part of one, is a CTA's.  Every thread keeps a running maximum m, S = sum 2^((l - m) c)
+// A row, or a part of one, is a CTA's.  Every thread keeps a base m, near its running maximum, S = sum 2^((l - m) c)
 // and W = sum (l - m) c 2^((l - m) c), c = log2(e) / t; then, all joined at the row's maximum,
 //   log p(x) = (l_x - m) / t - log S,   H = log S - log(2) W / S.
 // Differences are taken before they are scaled, so that neither large logits nor small temperatures lose
-// digits.  The best ids are a list of 32 a warp, a lane an entry, kept sorted; an id is
-// looked at only where it passes the list's last entry and a bound that all warps know.
+// digits.
+// The best ids.  Of the 256 threads' greatest elements so far, each warp's ceil(top / 8)-th is a bound: there are
+// `top` elements that are not below the least of the eight.  What reaches it goes to a buffer in shared
+// memory (some 40 elements whenever as many more have been read as before), and the buffer is sorted at
+// the end.  Where it overflows, as it does for a row that rises from end to end, the row is read again and
+// every element above the last of a sorted list put in its place there.
 #include <float.h>
 #include <math.h>
 
@@ -23,8 +27,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLoads = 4;             // 16-byte vectors of a thread in flight
-constexpr int kResident = 4;          // CTAs an SM that a row is cut for
+constexpr int kResident = 4;          // CTAs an SM
+constexpr int kMostParts = 4;         // parts of cut rows, all together, per CTA that runs at once
+constexpr float kPartCost = 0.03f;    // what a part costs besides its elements, in rows of a usual vocabulary
+constexpr int kCand = 2048;           // places of the buffer: elements of fewer than 227 vectors all fit,
+                                      // and from there on every warp has its share of them
 constexpr int kLeastVectors = kThreads * kLoads;   // of a part of a row
+constexpr float kLazy = 8.0f;         // how far (base 2) a logit may lie above the base of its thread's sums
 constexpr float kLog2e = 1.44269504088896f;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
@@ -134,6 +143,17 @@ __device__ __forceinline__ u64 merge(u64 a, u64 b, int lane) {
   return v;
 }
 
+// 32 entries sorted, the best first
+__device__ __forceinline__ u64 sorted(u64 v, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int o = size / 2; o > 0; o >>= 1) {
+      const u64 w = __shfl_xor_sync(kAll, v, o);
+      v = (((lane & o) == 0) == ((lane & size) == 0)) == (v > w) ? v : w;
+    }
+  return v;
+}
 // The k-th largest of the lanes' values.
 __device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
 #pragma unroll
@@ -141,18 +161,19 @@ __device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
 #pragma unroll
     for (int o = size / 2; o > 0; o >>= 1) {
       const float w = __shfl_xor_sync(kAll, v, o);
-      const bool falling = (lane & size) == 0 || size == 32;
-      v = ((lane & o) == 0) == falling ? fmaxf(v, w) : fminf(v, w);
+      v = ((lane & o) == 0) == ((lane & size) == 0) ? fmaxf(v, w) : fminf(v, w);
     }
   return __shfl_sync(kAll, v, k - 1);
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Args a) {
   constexpr int E = Vec<T>::N;
   __shared__ Stat s_stat[kWarps];
   __shared__ u64 s_best[kWarps][32];
   __shared__ float s_bound[kWarps];
+  __shared__ u64 s_cand[TOP ? kCand : 1];
+  __shared__ int s_count;
   __shared__ int s_last;
 
   const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
@@ -188,17 +209,17 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
   const uint4* body = (const uint4*)(l + head);
 
   Stat st = {-FLT_MAX, 0.0f, 0.0f, 0};
+  float peak = -FLT_MAX, limit = -FLT_MAX;   // running maximum; where the base has to follow it
   uint64_t s2 = 0, w2 = 0;   // its sums while the row is read, of even and odd elements
   const uint64_t c2 = pair(c, c);
   const float below = low_id ? INFINITY : nextafterf(mine, -INFINITY);   // what an id before x has to be above
   u64 list = 0;
-  float own = -INFINITY;      // an id has to be above it,
-  float bound = -INFINITY;    // and not below this
+  float bound = -INFINITY;    // what the best are not below
   const int share = (a.top + kWarps - 1) / kWarps;   // entries a warp brings to the bound
   volatile float* bounds = s_bound;
 
-  // E elements of ids from `id` on
-  auto take = [&](float (&f)[E], int id) {
+  // E elements of ids from `id` on; before: x is behind them
+  auto take = [&](float (&f)[E], int id, bool before) {
     float most = f[0];
 #pragma unroll
     for (int i = 1; i < E; ++i) most = fmaxf(most, f[i]);
@@ -207,12 +228,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
       for (int i = 0; i < E; ++i) f[i] = fminf(f[i], FLT_MAX);
       most = FLT_MAX;
     }
-    if (most > st.m) {   // sums to the new maximum
+    peak = fmaxf(peak, most);
+    if (most > limit) {   // sums to the new base
       const float d = (st.m - most) * c, by = ex2(d);
       const uint64_t by2 = pair(by, by);
       w2 = by > 0.0f ? mul2(fma2(pair(d, d), s2, w2), by2) : 0ull;
       s2 = mul2(s2, by2);
       st.m = most;
+      limit = most + kLazy / c;
     }
     const uint64_t off = pair(-st.m, -st.m);
 #pragma unroll
@@ -223,43 +246,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
       w2 = fma2(pair(fmaxf(low(d), -FLT_MAX), fmaxf(high(d), -FLT_MAX)), e, w2);   // nothing of -inf
     }
     if (most >= mine) {
-      if (id <= x && x < id + E) {
+      const float t = before ? below : mine;   // the vector with x in it is put right at the end
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          st.ahead += low_id ? f[i] > mine && id + i > x : f[i] > mine || (f[i] == mine && id + i < x);
-      } else {
-        const float t = id < x ? below : mine;
-#pragma unroll
-        for (int i = 0; i < E; ++i) st.ahead += f[i] > t;
-      }
+      for (int i = 0; i < E; ++i) st.ahead += f[i] > t;
     }
-    return most;
-  };
-  // the ids of a warp's vectors that may be among the best; all lanes call it
-  auto look = [&](const float (&f)[E], float most, int id) {
-    unsigned lanes = __ballot_sync(kAll, most > own && most >= bound);
-    while (lanes) {
-      const int from = __ffs(lanes) - 1;
-      lanes &= lanes - 1;
-      float v = -INFINITY;   // lane i: element i of lane `from`
+    if (TOP && most >= bound) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float t = __shfl_sync(kAll, f[i], from);
-        if (lane == i) v = t;
-      }
-      const int first = __shfl_sync(kAll, id, from);
-      unsigned good = __ballot_sync(kAll, v > own && v >= bound);
-      const u64 key = pack_best(v, (uint32_t)(first + lane));
-      while (good) {
-        const int i = __ffs(good) - 1;
-        good &= good - 1;
-        insert(list, __shfl_sync(kAll, key, i), lane);
-      }
-      const u64 last = __shfl_sync(kAll, list, a.top - 1);
-      if (last) own = packed_val(last);
+      for (int i = 0; i < E; ++i)
+        if (f[i] >= bound && f[i] > -INFINITY) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kCand) s_cand[at] = pack_best(f[i], (uint32_t)(id + i));
+        }
     }
   };
-
   // ids before the first boundary and behind the last vector: one element a lane of warp 0
   auto ends = [&](int from, int to) {
     const int id = from + lane;
@@ -267,9 +266,22 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
 #pragma unroll
     for (int i = 0; i < E; ++i) f[i] = -INFINITY;
     if (id < to) f[0] = fmaxf(to_f(l[id]), -INFINITY);
-    const float most = take(f, id);
-    if (TOP) look(f, most, id);
+    take(f, id, id < x);
   };
+  // one id a lane into the warp's sorted list; *own: its last entry of `top`
+  auto put = [&](float v, int id, float* own) {
+    const u64 key = pack_best(v, (uint32_t)id);
+    unsigned good = __ballot_sync(kAll, v >= bound && v > *own);
+    while (good) {
+      const int i = __ffs(good) - 1;
+      good &= good - 1;
+      insert(list, __shfl_sync(kAll, key, i), lane);
+      const u64 last = __shfl_sync(kAll, list, a.top - 1);
+      if (last) *own = packed_val(last);
+      good &= __ballot_sync(kAll, v > *own);
+    }
+  };
+
   uint4 raw[kLoads];
   auto load = [&](int v) {
     const uint32_t none = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
@@ -280,9 +292,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
     }
   };
   load(v0 + warp * 32);
+  auto tighten = [&](float most) {   // this lane's greatest so far
+    const float mine = kth_of_lanes(most, share, lane);
+    if (lane == 0) bounds[warp] = mine;
+  };
+  auto read_bound = [&]() {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) bound = w == 0 ? bounds[0] : fminf(bound, bounds[w]);
+  };
   if (TOP) {
-    // A first bound, so that the lists begin with ids that are likely to stay: each warp's share-th largest of
-    // its lanes' largest.
     float most = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
@@ -291,15 +309,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
 #pragma unroll
       for (int i = 0; i < E; ++i) most = fmaxf(most, f[i]);
     }
-    most = kth_of_lanes(fminf(most, FLT_MAX), share, lane);
-    if (lane == 0) s_bound[warp] = most;
+    tighten(fminf(most, FLT_MAX));
+    if (threadIdx.x == 0) s_count = 0;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) most = fminf(most, s_bound[w]);
-    bound = most;
+    read_bound();
   }
   if (warp == 0 && part == 0 && head > 0) ends(0, head);
 
+  int batch = 0;
   for (int v = v0 + warp * 32; v < v1; v += kThreads * kLoads) {
     uint4 now[kLoads];
 #pragma unroll
@@ -310,21 +327,45 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
       float f[E];
       Vec<T>::get(now[u], f);
       const int id = head + (v + u * kThreads + lane) * E;
-      const float most = take(f, id);
-      if (TOP) look(f, most, id);
+      take(f, id, id + E <= x);
     }
-    if (TOP) {
-      // every warp has `share` ids at or above its own word: `top` of them are above the least
-      const u64 e = __shfl_sync(kAll, list, share - 1);
-      if (lane == 0 && e) bounds[warp] = fmaxf(bounds[warp], packed_val(e));
-      float t = lane < kWarps ? bounds[lane] : INFINITY;
-#pragma unroll
-      for (int o = kWarps / 2; o > 0; o >>= 1) t = fminf(t, __shfl_xor_sync(kAll, t, o));
-      bound = fmaxf(bound, __shfl_sync(kAll, t, 0));
+    if (TOP && (++batch & (batch - 1)) == 0) {   // after 1, 2, 4, ... of them; another warp's word may be its last one
+      tighten(peak);
+      __syncwarp();
+      read_bound();
     }
   }
   if (warp == 0 && part == a.parts - 1 && head + vectors * E < a.V) ends(head + vectors * E, a.V);
 
+  if (TOP) {
+    __syncthreads();
+    const int count = s_count;
+    if (count <= kCand) {
+      for (int i = warp * 32; i < count; i += kThreads) {
+        const u64 more = sorted(i + lane < count ? s_cand[i + lane] : 0, lane);
+        list = i == warp * 32 ? more : merge(list, more, lane);
+      }
+    } else {
+      // a list a warp, in ascending order of ids, so that what only equals its last entry is passed over
+      read_bound();
+      float own = -INFINITY;
+      if (warp == 0 && part == 0) put(lane < head ? read_logit(to_f(l[lane])) : -INFINITY, lane, &own);
+      for (int id0 = head + v0 * E + warp * 32; id0 < a.V; id0 += kThreads) {
+        const int id = id0 + lane, end = part == a.parts - 1 ? a.V : head + v1 * E;
+        if (id0 >= end) break;
+        put(id < end ? read_logit(to_f(l[id])) : -INFINITY, id, &own);
+      }
+    }
+  }
+  // x's own vector was counted by what is above it: of the ids before x, equal ones are ahead too
+  const int own_vector = x < head || x >= head + vectors * E ? -1 : (int)(x - head) / E;
+  if (own_vector >= v0 && own_vector < v1) {
+    const int from = head + own_vector * E;
+    if (warp == 0 && from + lane < x) {
+      const float v = read_logit(to_f(l[from + lane]));
+      st.ahead += low_id ? -(v > mine) : v == mine;
+    }
+  }
   st.s = low(s2) + high(s2);
   st.w = low(w2) + high(w2);
   // the CTA's, in warp 0
@@ -336,12 +377,16 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
     if (lane == 0) s_stat[warp] = st;
     if (TOP) s_best[warp][lane] = list;
     __syncthreads();
+    if (TOP) {
+#pragma unroll
+      for (int o = kWarps / 2; o > 0; o >>= 1) {
+        if (warp < o) s_best[warp][lane] = list = merge(list, s_best[warp + o][lane], lane);
+        __syncthreads();
+      }
+    }
     if (warp == 0) {
       st = s_stat[0];
-      for (int w = 1; w < kWarps; ++w) {
-        st = join(st, s_stat[w], c);
-        if (TOP) list = merge(list, s_best[w][lane], lane);
-      }
+      for (int w = 1; w < kWarps; ++w) st = join(st, s_stat[w], c);
     }
   };
   gather();
@@ -388,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Args a) {
 }  // namespace
 
 // Tickets of the most rows that are cut (at a place of their own, so that it does not move with the
-// call), then what parts leave: a row is cut so that the CTAs fill the GPU once.
+// call), then what parts leave.
 xp_logprobs_ws xp_logprobs_layout(const xp_head* h, int rows, int top) {
   (void)rows;
   const size_t cut = (size_t)h->num_sms * kResident;
@@ -396,8 +441,8 @@ xp_logprobs_ws xp_logprobs_layout(const xp_head* h, int rows, int top) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
   L.tickets = take(cut * 4);
-  L.stat = take(2 * cut * sizeof(float4));
-  L.best = take(2 * cut * 8 * (size_t)top);
+  L.stat = take(kMostParts * cut * sizeof(float4));
+  L.best = take(kMostParts * cut * 8 * (size_t)top);
   L.total = o;
   return L;
 }
@@ -409,9 +454,15 @@ cudaError_t xp_launch_logprobs(const xp_head* h, const xp_logprobs_args& g, cuda
   a.sn = g.sn, a.sb = g.sb;
   a.tokens = g.tokens, a.temperature = g.temperature;
   a.B = g.B, a.V = h->V, a.top = g.top;
-  // rows * parts < cut + rows <= 2 cut where there are parts
-  const int most = std::max(1, h->V / (16 / es) / kLeastVectors);
-  a.parts = rows >= cut ? 1 : std::min(most, (cut + rows - 1) / rows);
+  // Parts so that the CTAs come in whole turns: the least turns * (1 / parts + kPartCost).  Rows that fill the
+  // GPU by themselves are not cut.
+  const int most = std::min(std::max(1, h->V / (16 / es) / kLeastVectors), kMostParts * cut / std::max(1, rows));
+  a.parts = 1;
+  float best = FLT_MAX;
+  for (int parts = 1; rows < cut && parts <= most; ++parts) {
+    const float time = (float)((rows * parts + cut - 1) / cut) * (1.0f / parts + kPartCost);
+    if (time < best) best = time, a.parts = parts;
+  }
   a.logprob = g.logprob, a.entropy = g.entropy, a.rank = g.rank;
   a.top_ids = g.top_ids, a.top_logprobs = g.top_logprobs;
   a.err = h->err;

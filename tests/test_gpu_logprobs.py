@@ -117,6 +117,21 @@ def test_ties_and_values_that_are_not_finite():
             check(head, rows.to(dtype), torch.full((8, 1), token, device="cuda"), None, 32)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [1700, 1830, 2049, 9001, 70001, 300007])
+def test_rows_that_rise_fall_and_stay(dtype, V):
+    """Rows whose best come last, first, or all alike; masked ones with few ids left, and none in some warps."""
+    at = torch.arange(V, device="cuda")
+    rows = torch.stack([at * (20.0 / V), -at * (20.0 / V), torch.full((V,), 3.0, device="cuda"),
+                        torch.where(at % 97 == 5, at % 7 * 1.0, -math.inf),
+                        torch.where(at >= V - 3, 1.0, -math.inf), torch.where(at < 40, at * 0.5, -math.inf),
+                        torch.full((V,), torch.finfo(dtype).min, device="cuda"),
+                        torch.where(at % 256 < 8, -math.inf, (at // 2048 % 5) * 1.0)])[:, None].to(dtype)
+    assert torch.isfinite(rows[6].float()).all()
+    for top in (32, 3):
+        check(make_head(V), rows, torch.full((8, 1), V // 3, device="cuda"), None, top)
+
+
 def test_large_logits_and_small_temperatures():
     V = 3001
     g = torch.Generator(device="cuda").manual_seed(0)
