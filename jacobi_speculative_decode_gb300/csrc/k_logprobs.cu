@@ -99,31 +99,81 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
   return {m, a.s + b.s, a.w + b.w, a.ahead + b.ahead};
 }
 
-// 16 bytes of logits as floats, NaN as -inf
+// 16 bytes of logits.  W: what greatest values and counts are kept in, two halves of bf16 or one float.
 template <typename T> struct Vec;
 template <> struct Vec<bf16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void get(const uint4& x, float (&f)[8]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    const __nv_bfloat162 least = __float2bfloat162_rn(-INFINITY);
+  static constexpr float kLeast = -3.38953139e38f;   // the least finite value
+  typedef __nv_bfloat162 W;
+  static __device__ __forceinline__ W word(const uint4& x, int i) {
+    const uint32_t w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+    return *(const W*)&w;
+  }
+  static __device__ __forceinline__ W all(float v) { return __float2bfloat162_rn(v); }
+  static __device__ __forceinline__ W join(W a, W b) { return __hmax2(a, b); }   // NaN left out
+  static __device__ __forceinline__ W top(const uint4& x) {
+    return join(join(word(x, 0), word(x, 1)), join(word(x, 2), word(x, 3)));
+  }
+  static __device__ __forceinline__ float most(W a) { return fmaxf(__low2float(a), __high2float(a)); }
+  // a value of the type that is not above v
+  static __device__ __forceinline__ float round_down(float v) {
+    return __bfloat162float(__float2bfloat16_rd(fmaxf(v, kLeast)));
+  }
+  // elements, those below `least` (and NaN) as that
+  static __device__ __forceinline__ void get(const uint4& x, float least, float (&f)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __hmax2(*(const __nv_bfloat162*)&w[i], least);
+      const W v = join(word(x, i), all(least));
       const uint32_t u = *(const uint32_t*)&v;
       f[2 * i] = __uint_as_float(u * 65536u);   // a multiply: the logic pipe has enough to do
       f[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
     }
   }
+  // elements above v, or not below it
+  static __device__ __forceinline__ W count(const uint4& x, float v, bool equal) {
+    W n = all(0.0f);
+    if (equal) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n = __hadd2(n, __hge2(word(x, i), all(v)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n = __hadd2(n, __hgt2(word(x, i), all(v)));
+    }
+    return n;
+  }
+  static __device__ __forceinline__ W add(W a, W b) { return __hadd2(a, b); }   // counts to 256 are exact
+  static __device__ __forceinline__ float sum(W a) { return __low2float(a) + __high2float(a); }
 };
 template <> struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void get(const uint4& x, float (&f)[4]) {
-    f[0] = fmaxf(__uint_as_float(x.x), -INFINITY), f[1] = fmaxf(__uint_as_float(x.y), -INFINITY);
-    f[2] = fmaxf(__uint_as_float(x.z), -INFINITY), f[3] = fmaxf(__uint_as_float(x.w), -INFINITY);
+  static constexpr float kLeast = -FLT_MAX;
+  typedef float W;
+  static __device__ __forceinline__ float word(const uint4& x, int i) {
+    return __uint_as_float(i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w);
   }
+  static __device__ __forceinline__ W join(W a, W b) { return fmaxf(a, b); }
+  static __device__ __forceinline__ W top(const uint4& x) {
+    return fmaxf(fmaxf(word(x, 0), word(x, 1)), fmaxf(word(x, 2), word(x, 3)));
+  }
+  static __device__ __forceinline__ float most(W a) { return a; }
+  static __device__ __forceinline__ float round_down(float v) { return fmaxf(v, kLeast); }
+  static __device__ __forceinline__ void get(const uint4& x, float least, float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = fmaxf(word(x, i), least);
+  }
+  static __device__ __forceinline__ W count(const uint4& x, float v, bool equal) {
+    W n = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += (equal ? word(x, i) >= v : word(x, i) > v) ? 1.0f : 0.0f;
+    return n;
+  }
+  static __device__ __forceinline__ W add(W a, W b) { return a + b; }
+  static __device__ __forceinline__ float sum(W a) { return a; }
 };
 // as the softmax reads a logit: NaN as -inf, +inf as the largest finite value
-__device__ __forceinline__ float read_logit(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
+template <typename T> __device__ __forceinline__ float read_logit(T l) {
+  return fminf(fmaxf(to_f(l), -INFINITY), FLT_MAX);
+}
 
 // A list of the 32 best (value, lowest id first) of a warp, lane i its entry i; 0: none.
 __device__ __forceinline__ void insert(u64& list, u64 key, int lane) {
@@ -198,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   const float heat = a.temperature ? a.temperature[n] : 1.0f;
   const bool greedy = !(heat >= FLT_MIN);   // of a smaller one 1 / t is not finite
   const float inv_t = greedy ? 1.0f : fmaxf(1.0f / heat, FLT_MIN), c = inv_t * kLog2e;
-  const float mine = read_logit(to_f(l[x]));
+  const float mine = read_logit(l[x]), raw_mine = fmaxf(to_f(l[x]), -INFINITY);
   // an id at -inf has all lower ids ahead of it, and of the higher ones those above -inf
   const bool low_id = mine == -INFINITY;
 
@@ -208,65 +258,53 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   const int v0 = (int)((int64_t)vectors * part / a.parts), v1 = (int)((int64_t)vectors * (part + 1) / a.parts);
   const uint4* body = (const uint4*)(l + head);
 
+  typedef Vec<T> Vt;
   Stat st = {-FLT_MAX, 0.0f, 0.0f, 0};
-  float peak = -FLT_MAX, limit = -FLT_MAX;   // running maximum; where the base has to follow it
-  uint64_t s2 = 0, w2 = 0;   // its sums while the row is read, of even and odd elements
+  // Of this thread's sums: above `limit` the base has to follow, what is not above `least` adds nothing.
+  float peak = -FLT_MAX, limit = -INFINITY, least = -INFINITY, ahead_of = 0.0f;
+  uint64_t s2 = 0, w2 = 0;   // the sums while the row is read, of even and odd elements
   const uint64_t c2 = pair(c, c);
-  const float below = low_id ? INFINITY : nextafterf(mine, -INFINITY);   // what an id before x has to be above
   u64 list = 0;
   float bound = -INFINITY;    // what the best are not below
   const int share = (a.top + kWarps - 1) / kWarps;   // entries a warp brings to the bound
   volatile float* bounds = s_bound;
 
-  // E elements of ids from `id` on; before: x is behind them
-  auto take = [&](float (&f)[E], int id, bool before) {
-    float most = f[0];
-#pragma unroll
-    for (int i = 1; i < E; ++i) most = fmaxf(most, f[i]);
-    if (most > FLT_MAX) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) f[i] = fminf(f[i], FLT_MAX);
-      most = FLT_MAX;
-    }
-    peak = fmaxf(peak, most);
-    if (most > limit) {   // sums to the new base
-      const float d = (st.m - most) * c, by = ex2(d);
-      const uint64_t by2 = pair(by, by);
-      w2 = by > 0.0f ? mul2(fma2(pair(d, d), s2, w2), by2) : 0ull;
-      s2 = mul2(s2, by2);
-      st.m = most;
-      limit = most + kLazy / c;
-    }
-    const uint64_t off = pair(-st.m, -st.m);
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const uint64_t d = mul2(add2(pair(f[i], f[i + 1]), off), c2);
-      const uint64_t e = pair(ex2(low(d)), ex2(high(d)));
-      s2 = add2(s2, e);
-      w2 = fma2(pair(fmaxf(low(d), -FLT_MAX), fmaxf(high(d), -FLT_MAX)), e, w2);   // nothing of -inf
-    }
-    if (most >= mine) {
-      const float t = before ? below : mine;   // the vector with x in it is put right at the end
-#pragma unroll
-      for (int i = 0; i < E; ++i) st.ahead += f[i] > t;
-    }
-    if (TOP && most >= bound) {
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (f[i] >= bound && f[i] > -INFINITY) {
-          const int at = atomicAdd(&s_count, 1);
-          if (at < kCand) s_cand[at] = pack_best(f[i], (uint32_t)(id + i));
-        }
-    }
+  auto follow = [&](float most) {   // the base
+    const float d = (st.m - most) * c, by = ex2(d);
+    const uint64_t by2 = pair(by, by);
+    w2 = by > 0.0f ? mul2(fma2(pair(d, d), s2, w2), by2) : 0ull;
+    s2 = mul2(s2, by2);
+    st.m = most;
+    limit = most + kLazy / c;
+    least = Vt::round_down(__fsub_rd(most, 200.0f / c));   // 2^-200 is nothing
+    if (least == Vt::kLeast) least = -INFINITY;
   };
-  // ids before the first boundary and behind the last vector: one element a lane of warp 0
+  auto add = [&](float lo, float hi) {   // neither infinite
+    const uint64_t d = mul2(add2(pair(lo, hi), pair(-st.m, -st.m)), c2);
+    const uint64_t e = pair(ex2(low(d)), ex2(high(d)));
+    s2 = add2(s2, e);
+    w2 = fma2(d, e, w2);
+  };
+  auto add_one = [&](float v) {
+    if (!(v > -INFINITY)) return;
+    const float d = (v - st.m) * c, e = ex2(d);
+    s2 = add2(s2, pair(e, 0.0f));
+    if (e > 0.0f) w2 = fma2(pair(d, 0.0f), pair(e, 0.0f), w2);
+  };
+  auto push = [&](float v, int id) {   // one that may be among the best
+    const int at = atomicAdd(&s_count, 1);
+    if (at < kCand) s_cand[at] = pack_best(v, (uint32_t)id);
+  };
+  // ids before the first boundary and behind the last vector: one a lane of warp 0
   auto ends = [&](int from, int to) {
     const int id = from + lane;
-    float f[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = -INFINITY;
-    if (id < to) f[0] = fmaxf(to_f(l[id]), -INFINITY);
-    take(f, id, id < x);
+    if (id >= to) return;
+    const float raw = fmaxf(to_f(l[id]), -INFINITY), v = fminf(raw, FLT_MAX);
+    peak = fmaxf(peak, v);
+    if (v > limit) follow(v);
+    add_one(v);
+    ahead_of += (low_id ? raw > raw_mine && id > x : raw > raw_mine || (raw == raw_mine && id < x)) ? 1.0f : 0.0f;
+    if (TOP && v >= bound && v > -INFINITY) push(v, id);
   };
   // one id a lane into the warp's sorted list; *own: its last entry of `top`
   auto put = [&](float v, int id, float* own) {
@@ -301,15 +339,10 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     for (int w = 0; w < kWarps; ++w) bound = w == 0 ? bounds[0] : fminf(bound, bounds[w]);
   };
   if (TOP) {
-    float most = -INFINITY;
+    typename Vt::W most = Vt::top(raw[0]);
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      float f[E];
-      Vec<T>::get(raw[u], f);
-#pragma unroll
-      for (int i = 0; i < E; ++i) most = fmaxf(most, f[i]);
-    }
-    tighten(fminf(most, FLT_MAX));
+    for (int u = 1; u < kLoads; ++u) most = Vt::join(most, Vt::top(raw[u]));
+    tighten(fminf(fmaxf(Vt::most(most), -INFINITY), FLT_MAX));
     if (threadIdx.x == 0) s_count = 0;
     __syncthreads();
     read_bound();
@@ -322,12 +355,57 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) now[u] = raw[u];
     load(v + kThreads * kLoads);   // the next ones are on their way meanwhile
+    typename Vt::W top[kLoads], of_all;
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
-      float f[E];
-      Vec<T>::get(now[u], f);
-      const int id = head + (v + u * kThreads + lane) * E;
-      take(f, id, id + E <= x);
+      top[u] = Vt::top(now[u]);
+      of_all = u == 0 ? top[0] : Vt::join(of_all, top[u]);
+    }
+    const float raw_most = fmaxf(Vt::most(of_all), -INFINITY), most = fminf(raw_most, FLT_MAX);
+    auto id_of = [&](int u) { return head + (v + u * kThreads + lane) * E; };
+    peak = fmaxf(peak, most);
+    // Where all are NaN or -inf, or too small to add anything, nothing is added.
+    if (most > least) {
+      if (most > limit) follow(most);
+      if (least > -INFINITY && raw_most <= FLT_MAX) {
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          float f[E];
+          Vt::get(now[u], least, f);
+#pragma unroll
+          for (int i = 0; i < E; i += 2) add(f[i], f[i + 1]);
+        }
+      } else {   // an infinity, or one that would not be told from the least value: one by one
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          float f[E];
+          Vt::get(now[u], -INFINITY, f);
+#pragma unroll
+          for (int i = 0; i < E; ++i) add_one(fminf(f[i], FLT_MAX));
+        }
+      }
+    }
+    // ids ahead of x; x's own vector is put right at the end
+    if (sizeof(T) == 2 || most >= mine) {
+      typename Vt::W n;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const bool before = id_of(u) + E <= x;
+        const typename Vt::W k = Vt::count(now[u], before && low_id ? INFINITY : raw_mine, before && !low_id);
+        n = u == 0 ? k : Vt::add(n, k);
+      }
+      ahead_of += Vt::sum(n);
+    }
+    if (TOP && most >= bound) {
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        if (Vt::most(top[u]) >= bound) {
+          float f[E];
+          Vt::get(now[u], -INFINITY, f);
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (f[i] >= bound && f[i] > -INFINITY) push(fminf(f[i], FLT_MAX), id_of(u) + i);
+        }
     }
     if (TOP && (++batch & (batch - 1)) == 0) {   // after 1, 2, 4, ... of them; another warp's word may be its last one
       tighten(peak);
@@ -349,11 +427,11 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
       // a list a warp, in ascending order of ids, so that what only equals its last entry is passed over
       read_bound();
       float own = -INFINITY;
-      if (warp == 0 && part == 0) put(lane < head ? read_logit(to_f(l[lane])) : -INFINITY, lane, &own);
+      if (warp == 0 && part == 0) put(lane < head ? read_logit(l[lane]) : -INFINITY, lane, &own);
       for (int id0 = head + v0 * E + warp * 32; id0 < a.V; id0 += kThreads) {
         const int id = id0 + lane, end = part == a.parts - 1 ? a.V : head + v1 * E;
         if (id0 >= end) break;
-        put(id < end ? read_logit(to_f(l[id])) : -INFINITY, id, &own);
+        put(id < end ? read_logit(l[id]) : -INFINITY, id, &own);
       }
     }
   }
@@ -362,10 +440,11 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   if (own_vector >= v0 && own_vector < v1) {
     const int from = head + own_vector * E;
     if (warp == 0 && from + lane < x) {
-      const float v = read_logit(to_f(l[from + lane]));
-      st.ahead += low_id ? -(v > mine) : v == mine;
+      const float v = fmaxf(to_f(l[from + lane]), -INFINITY);
+      ahead_of += low_id ? (v > mine ? -1.0f : 0.0f) : v == raw_mine ? 1.0f : 0.0f;
     }
   }
+  st.ahead = (int)ahead_of;
   st.s = low(s2) + high(s2);
   st.w = low(w2) + high(w2);
   // the CTA's, in warp 0
