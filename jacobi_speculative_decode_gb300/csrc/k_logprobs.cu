@@ -6,10 +6,9 @@
 //   log p(x) = (l_x - m) / t - log S,   H = log S - log(2) W / S.
 // Differences are taken before they are scaled, so that neither large logits nor small temperatures lose
 // digits.
-// The best ids.  Of the 256 threads' greatest elements so far, each warp's ceil(top / 8)-th is a bound: there are
-// `top` elements that are not below the least of the eight.  What reaches it goes to a buffer in shared
-// memory (some 40 elements whenever as many more have been read as before), and the buffer is sorted at
-// the end.  Where it overflows, as it does for a row that rises from end to end, the row is read again and
+// The best ids.  The `top`-th of the 256 threads' greatest elements so far is a bound: there are `top`
+// elements that are not below it.  What reaches it goes to a buffer in shared memory (about `top` elements
+// whenever as many more have been read as before), and the buffer is sorted at the end.  Where it overflows, as it does for a row that rises from end to end, the row is read again and
 // every element above the last of a sorted list put in its place there.
 #include <float.h>
 #include <math.h>
@@ -30,8 +29,7 @@ constexpr int kLoads = 4;             // 16-byte vectors of a thread in flight
 constexpr int kResident = 4;          // CTAs an SM
 constexpr int kMostParts = 4;         // parts of cut rows, all together, per CTA that runs at once
 constexpr float kPartCost = 0.03f;    // what a part costs besides its elements, in rows of a usual vocabulary
-constexpr int kCand = 2048;           // places of the buffer: elements of fewer than 227 vectors all fit,
-                                      // and from there on every warp has its share of them
+constexpr int kCand = 1024;           // places of the buffer
 constexpr int kLeastVectors = kThreads * kLoads;   // of a part of a row
 constexpr float kLazy = 8.0f;         // how far (base 2) a logit may lie above the base of its thread's sums
 constexpr float kLog2e = 1.44269504088896f;
@@ -204,16 +202,19 @@ __device__ __forceinline__ u64 sorted(u64 v, int lane) {
     }
   return v;
 }
-// The k-th largest of the lanes' values.
-__device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
+// A value that k of the 256 are not below, at most 2^-7 under the k-th largest: by halving, the same in all
+// lanes of a warp.
+__device__ __forceinline__ float kth_of(const volatile float* v, int k, int lane) {
+  uint32_t key[kThreads / 32], low = 0;
 #pragma unroll
-  for (int size = 2; size <= 32; size *= 2)
+  for (int i = 0; i < kThreads / 32; ++i) key[i] = f2key(v[i * 32 + lane]);
+  for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+    int n = 0;
 #pragma unroll
-    for (int o = size / 2; o > 0; o >>= 1) {
-      const float w = __shfl_xor_sync(kAll, v, o);
-      v = ((lane & o) == 0) == ((lane & size) == 0) ? fmaxf(v, w) : fminf(v, w);
-    }
-  return __shfl_sync(kAll, v, k - 1);
+    for (int i = 0; i < kThreads / 32; ++i) n += key[i] >= (low | bit);
+    if (__reduce_add_sync(kAll, n) >= k) low |= bit;
+  }
+  return fmaxf(key2f(low), -FLT_MAX);
 }
 
 template <typename T, bool TOP>
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   constexpr int E = Vec<T>::N;
   __shared__ Stat s_stat[kWarps];
   __shared__ u64 s_best[kWarps][32];
-  __shared__ float s_bound[kWarps];
+  __shared__ float s_peak[TOP ? kThreads : 1], s_bound;   // the threads' greatest; what the best are not below
   __shared__ u64 s_cand[TOP ? kCand : 1];
   __shared__ int s_count;
   __shared__ int s_last;
@@ -265,9 +266,8 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   uint64_t s2 = 0, w2 = 0;   // the sums while the row is read, of even and odd elements
   const uint64_t c2 = pair(c, c);
   u64 list = 0;
-  float bound = -INFINITY;    // what the best are not below
-  const int share = (a.top + kWarps - 1) / kWarps;   // entries a warp brings to the bound
-  volatile float* bounds = s_bound;
+  float bound = -FLT_MAX;    // s_bound as last read
+  volatile float *peaks = s_peak, *best_bound = &s_bound;
 
   auto follow = [&](float most) {   // the base
     const float d = (st.m - most) * c, by = ex2(d);
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     if (v > limit) follow(v);
     add_one(v);
     ahead_of += (low_id ? raw > raw_mine && id > x : raw > raw_mine || (raw == raw_mine && id < x)) ? 1.0f : 0.0f;
-    if (TOP && v >= bound && v > -INFINITY) push(v, id);
+    if (TOP && v >= bound) push(v, id);
   };
   // one id a lane into the warp's sorted list; *own: its last entry of `top`
   auto put = [&](float v, int id, float* own) {
@@ -330,26 +330,23 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     }
   };
   load(v0 + warp * 32);
-  auto tighten = [&](float most) {   // this lane's greatest so far
-    const float mine = kth_of_lanes(most, share, lane);
-    if (lane == 0) bounds[warp] = mine;
-  };
-  auto read_bound = [&]() {
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) bound = w == 0 ? bounds[0] : fminf(bound, bounds[w]);
-  };
   if (TOP) {
     typename Vt::W most = Vt::top(raw[0]);
 #pragma unroll
     for (int u = 1; u < kLoads; ++u) most = Vt::join(most, Vt::top(raw[u]));
-    tighten(fminf(fmaxf(Vt::most(most), -INFINITY), FLT_MAX));
+    peaks[threadIdx.x] = fminf(fmaxf(Vt::most(most), -FLT_MAX), FLT_MAX);
     if (threadIdx.x == 0) s_count = 0;
     __syncthreads();
-    read_bound();
+    if (warp == 0) {
+      bound = kth_of(peaks, a.top, lane);
+      if (lane == 0) *best_bound = bound;
+    }
+    __syncthreads();
+    bound = *best_bound;
   }
   if (warp == 0 && part == 0 && head > 0) ends(0, head);
 
-  int batch = 0;
+  int batch = 0, turn = 1;
   for (int v = v0 + warp * 32; v < v1; v += kThreads * kLoads) {
     uint4 now[kLoads];
 #pragma unroll
@@ -404,13 +401,23 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
           Vt::get(now[u], -INFINITY, f);
 #pragma unroll
           for (int i = 0; i < E; ++i)
-            if (f[i] >= bound && f[i] > -INFINITY) push(fminf(f[i], FLT_MAX), id_of(u) + i);
+            if (f[i] >= bound) push(fminf(f[i], FLT_MAX), id_of(u) + i);
         }
     }
-    if (TOP && (++batch & (batch - 1)) == 0) {   // after 1, 2, 4, ... of them; another warp's word may be its last one
-      tighten(peak);
-      __syncwarp();
-      read_bound();
+    if (TOP) {
+      // After 2, 3, 4, 6, 8, 12, ... of them, one warp in turn looks at all threads' peaks, some of which may
+      // be those of a batch before.
+      ++batch;
+      const int even = batch & (batch - 1);
+      if (batch > 1 && (even == 0 || (even & (even - 1)) == 0 && batch == even + even / 2)) {
+        peaks[threadIdx.x] = peak;
+        __syncwarp();
+        if (warp == (turn++ & (kWarps - 1))) {
+          const float now = kth_of(peaks, a.top, lane);
+          if (lane == 0 && now > *best_bound) *best_bound = now;
+        }
+      }
+      bound = *best_bound;
     }
   }
   if (warp == 0 && part == a.parts - 1 && head + vectors * E < a.V) ends(head + vectors * E, a.V);
@@ -425,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
       }
     } else {
       // a list a warp, in ascending order of ids, so that what only equals its last entry is passed over
-      read_bound();
+      bound = *best_bound;
       float own = -INFINITY;
       if (warp == 0 && part == 0) put(lane < head ? read_logit(l[lane]) : -INFINITY, lane, &own);
       for (int id0 = head + v0 * E + warp * 32; id0 < a.V; id0 += kThreads) {
