@@ -6,10 +6,12 @@
 //   log p(x) = (l_x - m) / t - log S,   H = log S - log(2) W / S.
 // Differences are taken before they are scaled, so that neither large logits nor small temperatures lose
 // digits.
-// The best ids.  The `top`-th of the 256 threads' greatest elements so far is a bound: there are `top`
-// elements that are not below it.  What reaches it goes to a buffer in shared memory (about `top` elements
-// whenever as many more have been read as before), and the buffer is sorted at the end.  Where it overflows, as it does for a row that rises from end to end, the row is read again and
-// every element above the last of a sorted list put in its place there.
+// The best ids.  On the way a thread only writes down the greatest of every 16 bytes' batch.  The `top`-th of the
+// 256 threads' greatest is a bound: there are `top` elements that are not below it, and few that are above.
+// The batches that reach it are read again (from L2, some 25 of a row's), their elements that do go to a buffer,
+// and an element of the buffer counts those before it and so knows its place.  Where the buffer overflows, as
+// for a row of equal logits, every warp reads its part of the row again into a sorted list.
+// (Looked at on the way, under a bound that follows, the same rows took 62 us where 44 are taken without.)
 #include <float.h>
 #include <math.h>
 
@@ -30,6 +32,7 @@ constexpr int kResident = 4;          // CTAs an SM
 constexpr int kMostParts = 4;         // parts of cut rows, all together, per CTA that runs at once
 constexpr float kPartCost = 0.03f;    // what a part costs besides its elements, in rows of a usual vocabulary
 constexpr int kCand = 1024;           // places of the buffer
+constexpr int kBatches = 64;          // of which the greatest is held; all behind them share the last place
 constexpr int kLeastVectors = kThreads * kLoads;   // of a part of a row
 constexpr float kLazy = 8.0f;         // how far (base 2) a logit may lie above the base of its thread's sums
 constexpr float kLog2e = 1.44269504088896f;
@@ -179,32 +182,9 @@ __device__ __forceinline__ void insert(u64& list, u64 key, int lane) {
   const u64 up = __shfl_up_sync(kAll, list, 1);
   if (lane >= at) list = lane == at ? key : up;
 }
-// the 32 best of two lists
-__device__ __forceinline__ u64 merge(u64 a, u64 b, int lane) {
-  const u64 r = __shfl_sync(kAll, b, 31 - lane);
-  u64 v = a > r ? a : r;   // the 32 best, rising and falling
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const u64 w = __shfl_xor_sync(kAll, v, o);
-    v = ((lane & o) == 0) == (v > w) ? v : w;
-  }
-  return v;
-}
-
-// 32 entries sorted, the best first
-__device__ __forceinline__ u64 sorted(u64 v, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-    for (int o = size / 2; o > 0; o >>= 1) {
-      const u64 w = __shfl_xor_sync(kAll, v, o);
-      v = (((lane & o) == 0) == ((lane & size) == 0)) == (v > w) ? v : w;
-    }
-  return v;
-}
 // A value that k of the 256 are not below, at most 2^-7 under the k-th largest: by halving, the same in all
 // lanes of a warp.
-__device__ __forceinline__ float kth_of(const volatile float* v, int k, int lane) {
+__device__ __forceinline__ float kth_of(const float* v, int k, int lane) {
   uint32_t key[kThreads / 32], low = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) key[i] = f2key(v[i * 32 + lane]);
@@ -221,9 +201,10 @@ template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Args a) {
   constexpr int E = Vec<T>::N;
   __shared__ Stat s_stat[kWarps];
-  __shared__ u64 s_best[kWarps][32];
-  __shared__ float s_peak[TOP ? kThreads : 1], s_bound;   // the threads' greatest; what the best are not below
+  __shared__ u64 s_best[32];
+  __shared__ float s_peak[TOP ? kThreads : 1], s_bound;   // the threads' greatest; a bound of the best
   __shared__ u64 s_cand[TOP ? kCand : 1];
+  __shared__ bf16 s_most[TOP ? kBatches : 1][TOP ? kThreads : 1];   // rounded up
   __shared__ int s_count;
   __shared__ int s_last;
 
@@ -266,8 +247,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   uint64_t s2 = 0, w2 = 0;   // the sums while the row is read, of even and odd elements
   const uint64_t c2 = pair(c, c);
   u64 list = 0;
-  float bound = -FLT_MAX;    // s_bound as last read
-  volatile float *peaks = s_peak, *best_bound = &s_bound;
+  float bound = -FLT_MAX;   // what the best are not below
 
   auto follow = [&](float most) {   // the base
     const float d = (st.m - most) * c, by = ex2(d);
@@ -292,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     if (e > 0.0f) w2 = fma2(pair(d, 0.0f), pair(e, 0.0f), w2);
   };
   auto push = [&](float v, int id) {   // one that may be among the best
+    if (!(v >= bound)) return;
     const int at = atomicAdd(&s_count, 1);
     if (at < kCand) s_cand[at] = pack_best(v, (uint32_t)id);
   };
@@ -304,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     if (v > limit) follow(v);
     add_one(v);
     ahead_of += (low_id ? raw > raw_mine && id > x : raw > raw_mine || (raw == raw_mine && id < x)) ? 1.0f : 0.0f;
-    if (TOP && v >= bound) push(v, id);
+    if (TOP) push(v, id);
   };
   // one id a lane into the warp's sorted list; *own: its last entry of `top`
   auto put = [&](float v, int id, float* own) {
@@ -329,25 +310,17 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
       raw[u] = at < v1 ? __ldcs(body + at) : make_uint4(none, none, none, none);
     }
   };
-  load(v0 + warp * 32);
+  const int first = v0 + warp * 32;
+  load(first);
   if (TOP) {
-    typename Vt::W most = Vt::top(raw[0]);
-#pragma unroll
-    for (int u = 1; u < kLoads; ++u) most = Vt::join(most, Vt::top(raw[u]));
-    peaks[threadIdx.x] = fminf(fmaxf(Vt::most(most), -FLT_MAX), FLT_MAX);
     if (threadIdx.x == 0) s_count = 0;
+    if (threadIdx.x < 32) s_best[threadIdx.x] = 0;
     __syncthreads();
-    if (warp == 0) {
-      bound = kth_of(peaks, a.top, lane);
-      if (lane == 0) *best_bound = bound;
-    }
-    __syncthreads();
-    bound = *best_bound;
   }
   if (warp == 0 && part == 0 && head > 0) ends(0, head);
 
-  int batch = 0, turn = 1;
-  for (int v = v0 + warp * 32; v < v1; v += kThreads * kLoads) {
+  int batch = 0;
+  for (int v = first; v < v1; v += kThreads * kLoads) {
     uint4 now[kLoads];
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) now[u] = raw[u];
@@ -393,46 +366,51 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
       }
       ahead_of += Vt::sum(n);
     }
-    if (TOP && most >= bound) {
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u)
-        if (Vt::most(top[u]) >= bound) {
-          float f[E];
-          Vt::get(now[u], -INFINITY, f);
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (f[i] >= bound) push(fminf(f[i], FLT_MAX), id_of(u) + i);
-        }
-    }
     if (TOP) {
-      // After 2, 3, 4, 6, 8, 12, ... of them, one warp in turn looks at all threads' peaks, some of which may
-      // be those of a batch before.
+      bf16* to = &s_most[min(batch, kBatches - 1)][threadIdx.x];
+      *to = __float2bfloat16_ru(batch < kBatches ? most : fmaxf(most, to_f(*to)));
       ++batch;
-      const int even = batch & (batch - 1);
-      if (batch > 1 && (even == 0 || (even & (even - 1)) == 0 && batch == even + even / 2)) {
-        peaks[threadIdx.x] = peak;
-        __syncwarp();
-        if (warp == (turn++ & (kWarps - 1))) {
-          const float now = kth_of(peaks, a.top, lane);
-          if (lane == 0 && now > *best_bound) *best_bound = now;
-        }
-      }
-      bound = *best_bound;
     }
   }
   if (warp == 0 && part == a.parts - 1 && head + vectors * E < a.V) ends(head + vectors * E, a.V);
 
-  if (TOP) {
+  // the keys in the buffer to their places
+  auto place = [&](int count) {
+    for (int i = threadIdx.x; i < count; i += kThreads) {
+      const u64 key = s_cand[i];
+      int ahead = 0;
+#pragma unroll 8
+      for (int j = 0; j < count; ++j) ahead += s_cand[j] > key;
+      if (key && ahead < a.top) s_best[ahead] = key;
+    }
     __syncthreads();
-    const int count = s_count;
-    if (count <= kCand) {
-      for (int i = warp * 32; i < count; i += kThreads) {
-        const u64 more = sorted(i + lane < count ? s_cand[i + lane] : 0, lane);
-        list = i == warp * 32 ? more : merge(list, more, lane);
+  };
+  if (TOP) {
+    s_peak[threadIdx.x] = peak;
+    __syncthreads();
+    if (warp == 0) {
+      bound = kth_of(s_peak, a.top, lane);
+      if (lane == 0) s_bound = bound;
+    }
+    __syncthreads();
+    bound = s_bound;
+    batch = 0;
+    for (int v = first; v < v1; v += kThreads * kLoads, ++batch) {
+      if (!__any_sync(kAll, to_f(s_most[min(batch, kBatches - 1)][threadIdx.x]) >= bound)) continue;
+      load(v);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        if (!(Vt::most(Vt::top(raw[u])) >= bound)) continue;
+        float f[E];
+        Vt::get(raw[u], -INFINITY, f);
+#pragma unroll
+        for (int i = 0; i < E; ++i) push(fminf(f[i], FLT_MAX), head + (v + u * kThreads + lane) * E + i);
       }
-    } else {
+    }
+    __syncthreads();
+    int count = s_count;
+    if (count > kCand) {
       // a list a warp, in ascending order of ids, so that what only equals its last entry is passed over
-      bound = *best_bound;
       float own = -INFINITY;
       if (warp == 0 && part == 0) put(lane < head ? read_logit(l[lane]) : -INFINITY, lane, &own);
       for (int id0 = head + v0 * E + warp * 32; id0 < a.V; id0 += kThreads) {
@@ -440,7 +418,12 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
         if (id0 >= end) break;
         put(id < end ? read_logit(l[id]) : -INFINITY, id, &own);
       }
+      __syncthreads();   // count has been read by all
+      s_cand[threadIdx.x] = list;
+      __syncthreads();
+      count = kThreads;
     }
+    place(count);
   }
   // x's own vector was counted by what is above it: of the ids before x, equal ones are ahead too
   const int own_vector = x < head || x >= head + vectors * E ? -1 : (int)(x - head) / E;
@@ -461,15 +444,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
       st = join(st, {__shfl_xor_sync(kAll, st.m, o), __shfl_xor_sync(kAll, st.s, o),
                      __shfl_xor_sync(kAll, st.w, o), __shfl_xor_sync(kAll, st.ahead, o)}, c);
     if (lane == 0) s_stat[warp] = st;
-    if (TOP) s_best[warp][lane] = list;
     __syncthreads();
-    if (TOP) {
-#pragma unroll
-      for (int o = kWarps / 2; o > 0; o >>= 1) {
-        if (warp < o) s_best[warp][lane] = list = merge(list, s_best[warp + o][lane], lane);
-        __syncthreads();
-      }
-    }
     if (warp == 0) {
       st = s_stat[0];
       for (int w = 1; w < kWarps; ++w) st = join(st, s_stat[w], c);
@@ -481,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     const int64_t at = (int64_t)row * a.parts;
     if (warp == 0) {
       if (lane == 0) __stcg(a.stat + at + part, make_float4(st.m, st.s, st.w, __int_as_float(st.ahead)));
-      if (TOP && lane < a.top) __stcg(a.best + (at + part) * a.top + lane, list);
+      if (TOP && lane < a.top) __stcg(a.best + (at + part) * a.top + lane, s_best[lane]);
       __threadfence();
     }
     if (!arrive_last(a.tickets + row, a.parts, &s_last)) return;
@@ -491,14 +466,18 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
       const float4 v = __ldcg(a.stat + at + p);
       st = join(st, {v.x, v.y, v.z, __float_as_int(v.w)}, c);
     }
-    list = 0;
-    if (TOP)
-      for (int p = warp; p < a.parts; p += kWarps)
-        list = merge(list, lane < a.top ? __ldcg(a.best + (at + p) * a.top + lane) : 0ull, lane);
+    if (TOP) {
+      if (threadIdx.x < 32) s_best[threadIdx.x] = 0;
+      const int count = a.parts * a.top;   // at most the buffer's places
+      for (int i = threadIdx.x; i < count; i += kThreads) s_cand[i] = __ldcg(a.best + at * a.top + i);
+      __syncthreads();
+      place(count);
+    }
     gather();
   }
   if (warp != 0) return;
 
+  if (TOP) list = s_best[lane];
   const float log_s = logf(st.s);   // s = 0: nothing above -inf
   const int ahead = st.ahead + (low_id ? (int)x : 0);
   auto log_p = [&](float v) { return greedy ? -INFINITY : (v - st.m) * inv_t - log_s; };
@@ -542,7 +521,8 @@ cudaError_t xp_launch_logprobs(const xp_head* h, const xp_logprobs_args& g, cuda
   a.B = g.B, a.V = h->V, a.top = g.top;
   // Parts so that the CTAs come in whole turns: the least turns * (1 / parts + kPartCost).  Rows that fill the
   // GPU by themselves are not cut.
-  const int most = std::min(std::max(1, h->V / (16 / es) / kLeastVectors), kMostParts * cut / std::max(1, rows));
+  int most = std::min(std::max(1, h->V / (16 / es) / kLeastVectors), kMostParts * cut / std::max(1, rows));
+  if (g.top > 0) most = std::min(most, kCand / g.top);   // what they leave has to fit the buffer
   a.parts = 1;
   float best = FLT_MAX;
   for (int parts = 1; rows < cut && parts <= most; ++parts) {
