@@ -269,9 +269,24 @@ __device__ __forceinline__ void widen_queries(const WidenArgs& w) {
   }
 }
 
+// 8 codes times a scale, two dims an operation: 1024 + c is an fp16 number with c in its last bits
 template <int BITS>
+__device__ __forceinline__ uint4 widen8(uint2 w, unsigned scale) {
+  uint32_t out[4];
+  const uint32_t s = scale * 0x00800080u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t pair = BITS == 4 ? (w.x >> 4 * j & 0x000F000Fu) | 0x64006400u
+                                    : __byte_perm(j < 2 ? w.x : w.y, 0x64646464u, j % 2 ? 0x4342 : 0x4140);
+    const uint32_t zero = BITS == 4 ? 0xE408E408u : 0xE480E480u;   // -1024 - 8, -1024 - 128
+    const __half2 v = __hmul2(__hadd2(*(const __half2*)&pair, *(const __half2*)&zero), *(const __half2*)&s);
+    out[j] = *(const uint32_t*)&v;
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <int BITS, int D>
 __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__ WidenArgs w) {
-  __shared__ int s_page[kWideTokens], s_at[kWideTokens];
   const RowArgs& a = w.r;
   if ((int)blockIdx.x >= w.page_ctas) return widen_queries(w);
   constexpr int per = kWidePage / kWideTokens;
@@ -283,48 +298,47 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
   const int pos0 = (tail < 0 ? page : tail % w.tail_pages) * kWidePage;
   if (pos0 >= len) return;
   if (h == 0 && t0 == 0 && threadIdx.x == 0) w.table[page] = page;
-  if (threadIdx.x < kWideTokens) {
-    const int pos = pos0 + t0 + (int)threadIdx.x;
-    int p = -1, at = 0;
-    if (pos < len) {
-      const int col = pos / a.ps;
-      at = pos - col * a.ps;
-      p = table[col];
-      if (p < 0 || p >= a.pages) {
-        atomicOr(a.err, XP_ERR_BADPAGE);
-        p = p < 0 ? 0 : a.pages - 1;
-      }
-    }
-    s_page[threadIdx.x] = p;
-    s_at[threadIdx.x] = at;
+
+  // A thread takes a piece of 8 dims of every 256 / (D/8)-th token: all pages, then all codes, then all stores.
+  constexpr int kPieces = D / 8, kStep = kThreads / kPieces, kEach = kWideTokens / kStep;
+  const int e = threadIdx.x % kPieces * 8, i0 = threadIdx.x / kPieces;
+  int p[kEach], at[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int pos = pos0 + t0 + i0 + k * kStep, col = pos / a.ps;
+    at[k] = pos - col * a.ps;
+    p[k] = pos < len ? table[col] : -1;
   }
-  __syncthreads();
-  const int pieces = a.D / 8;   // 8 or 16: a piece is 8 dims
-  const int e = threadIdx.x % pieces * 8;
-  __half* to = (__half*)a.k + h * w.plane + ((int64_t)page * kWidePage + t0) * a.D + e;
-  const int64_t to_v = (__half*)a.v - (__half*)a.k;
-#pragma unroll 4
-  for (int i = threadIdx.x / pieces; i < kWideTokens; i += kThreads / pieces) {
-    const int p = s_page[i];
-    const int64_t head = p * a.page + h * a.head;
+  uint2 code[kEach][2];
+  unsigned scale[kEach][2];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const bool live = pos0 + t0 + i0 + k * kStep < len;
+    if (live && (p[k] < 0 || p[k] >= a.pages)) {
+      atomicOr(a.err, XP_ERR_BADPAGE);
+      p[k] = p[k] < 0 ? 0 : a.pages - 1;
+    }
+    const int64_t head = p[k] * a.page + h * a.head;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      float x[8] = {};
-      if (p >= 0) {
-        const char* from = (kv ? a.vp : a.kp) + head;
-        const float step = xpq::scale_of((uint8_t)from[a.scale_at + s_at[i] * a.scale + e / 16]);
-        const uint32_t* code = (const uint32_t*)(from + s_at[i] * a.token + e / 8 * BITS);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[j] = BITS == 4 ? (float)((int)(code[0] >> (j / 2 + j % 2 * 4) * 4 & 15u) - 8) * step
-                           : (float)((int)(code[j / 4 % (BITS / 4)] >> j % 4 * 8 & 255u) - 128) * step;
+      const char* from = (kv ? a.vp : a.kp) + head;
+      code[k][kv] = make_uint2(0, 0);
+      scale[k][kv] = 0;
+      if (live) {
+        scale[k][kv] = (uint8_t)from[a.scale_at + at[k] * a.scale + e / 16];
+        const char* c = from + at[k] * a.token + e / 8 * BITS;
+        if (BITS == 4) code[k][kv].x = __ldcs((const unsigned*)c);
+        else code[k][kv] = __ldcs((const uint2*)c);
       }
-      __half2 y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
-      *(uint4*)(to + (kv ? to_v : 0) + (int64_t)i * a.D) = *(const uint4*)y;
     }
   }
+  __half* to = (__half*)a.k + h * w.plane + ((int64_t)page * kWidePage + t0 + i0) * D + e;
+  const int64_t to_v = (__half*)a.v - (__half*)a.k;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+      *(uint4*)(to + (kv ? to_v : 0) + k * kStep * D) = widen8<BITS>(code[k][kv], scale[k][kv]);
 }
 
 template <typename T> bool wide_rows(const RowArgs& a) {
@@ -392,8 +406,14 @@ cudaError_t xp_launch_widen(const xp_cache* c, const xp_attn_args& g, int prefix
   w.q_out = (__half*)q, w.q_factor = q_factor;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads, each = (int64_t)g.kv_heads * (kThreads / 32);
   const dim3 grid((unsigned)(w.page_ctas + (rows + each - 1) / each), g.kv_heads);
-  if (c->d.dtype == XP_Q8) widen_kernel<8><<<grid, kThreads, 0, s>>>(w);
-  else widen_kernel<4><<<grid, kThreads, 0, s>>>(w);
+  const bool narrow = c->d.head_dim == 64;   // or 128
+  if (c->d.dtype == XP_Q8) {
+    if (narrow) widen_kernel<8, 64><<<grid, kThreads, 0, s>>>(w);
+    else widen_kernel<8, 128><<<grid, kThreads, 0, s>>>(w);
+  } else {
+    if (narrow) widen_kernel<4, 64><<<grid, kThreads, 0, s>>>(w);
+    else widen_kernel<4, 128><<<grid, kThreads, 0, s>>>(w);
+  }
   return cudaGetLastError();
 }
 
