@@ -58,96 +58,146 @@ __device__ __forceinline__ void find_pages(const RowArgs& a, int n, int t0, int6
   __syncthreads();
 }
 
-// 16 consecutive elements as floats; wide: from 16-byte boundaries
-__device__ __forceinline__ void load16(const float* p, bool wide, float (&x)[16]) {
-  if (wide) {
+template <typename T> struct Piece {              // elements of 16 bytes
+  static constexpr int N = 16 / sizeof(T);
+};
+// a piece; wide: from a 16-byte boundary
+template <typename T> __device__ __forceinline__ uint4 load_piece(const T* p, bool wide) {
+  if (wide) return __ldcs((const uint4*)p);
+  uint4 v;
+  T* e = (T*)&v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldcs((const float4*)p + i);
-      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = p[i];
-  }
+  for (int i = 0; i < Piece<T>::N; ++i) e[i] = p[i];
+  return v;
 }
-__device__ __forceinline__ void load16(const bf16* p, bool wide, float (&x)[16]) {
-  if (wide) {
+__device__ __forceinline__ void floats_of(const uint4& v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void floats_of(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = __ldcs((const uint4*)p + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = to_f(p[i]);
+  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN where either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float reciprocal(float x) {   // nearly
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr int kBatch = 4;   // tokens of a thread whose loads are on their way together
+
+// What a thread does of a row: piece `e` of head `h` of K or V, for every lanes-th token from `lane` on.
+struct Part {
+  int e, h, is_v, lane, lanes;
+};
+template <typename F> __device__ __forceinline__ void for_parts(const RowArgs& a, int elements, F f) {
+  const int pieces = (a.D + elements - 1) / elements, units = 2 * a.H * pieces;
+  Part p;
+  p.lanes = max(1, kThreads / units);   // tokens at once where a row is short
+  p.lane = units < kThreads ? threadIdx.x / units : 0;
+  if (p.lane >= p.lanes) return;
+  for (int u = units < kThreads ? threadIdx.x % units : threadIdx.x; u < units; u += kThreads) {
+    p.e = u % pieces * elements;
+    p.h = u / pieces % a.H;
+    p.is_v = u / pieces / a.H;
+    f(p);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Quantised append.
+// Quantised append.  The 4 (fp32) or 2 (bf16) threads of 16 dims find their largest together.
 // ---------------------------------------------------------------------------
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kThreads) append_quant_kernel(const RowArgs a, bool wide) {
+  constexpr int E = Piece<T>::N;
   __shared__ Places s;
   const int chunks = (a.T + kTokens - 1) / kTokens;
   const int n = blockIdx.x / chunks, t0 = (int)(blockIdx.x % chunks) * kTokens;
   find_pages(a, n, t0, (int64_t)a.lens[n] - a.T, INT64_MAX, &s);
 
-  const int groups = a.D / 16, units = 2 * a.H * groups;
-  const int lanes = max(1, kThreads / units);   // tokens at once where a row is short
-  const int lane = units < kThreads ? threadIdx.x / units : 0;
-  if (lane >= lanes) return;
-  for (int u = units < kThreads ? threadIdx.x % units : threadIdx.x; u < units; u += kThreads) {
-    const int g = u % groups, h = u / groups % a.H, is_v = u / groups / a.H;
-    const T* from = (const T*)(is_v ? a.v : a.k) + n * a.sn + h * a.sh + g * 16;
-    char* pool = (is_v ? a.vp : a.kp) + h * a.head;
-#pragma unroll 2
-    for (int i = lane; i < kTokens; i += lanes) {
-      if (s.page[i] < 0) continue;
-      float x[16];
-      load16(from + (t0 + i) * a.st, wide, x);
-      float top = 0.0f;
-      bool bad = false;
+  // threads of one group: neighbours, as a row's pieces are a whole number of groups
+  const unsigned group = (E == 4 ? 0xFu : 0x3u) << (threadIdx.x & 31 & -(16 / E));
+  for_parts(a, E, [&](const Part& part) {
+    const T* from = (const T*)(part.is_v ? a.v : a.k) + n * a.sn + t0 * a.st + part.h * a.sh + part.e;
+    char* pool = (part.is_v ? a.vp : a.kp) + part.h * a.head;
+    const int g = part.e / 16, in = part.e % 16;
+    for (int i0 = part.lane; i0 < kTokens; i0 += kBatch * part.lanes) {
+      uint4 raw[kBatch];
+      int page[kBatch];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        bad |= x[j] != x[j];
-        x[j] = x[j] != x[j] ? 0.0f : x[j];
-        top = fmaxf(top, fabsf(x[j]));
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * part.lanes;
+        page[k] = i < kTokens ? s.page[i] : -1;
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (page[k] >= 0) raw[k] = load_piece(from + i * a.st, wide);
       }
-      bool over;
-      const unsigned b = xpq::scale_byte<BITS>(top, &over);
-      if (bad || over) atomicOr(a.err, XP_ERR_RANGE);
-      const float step = xpq::scale_of(b);
-      char* head = pool + s.page[i] * a.page;
-      head[a.scale_at + s.at[i] * a.scale + g] = (char)b;
-      if (g == groups - 1)   // the padding behind the scales
-        for (int p = groups; p < a.scale; ++p) head[a.scale_at + s.at[i] * a.scale + p] = 0;
-      uint32_t w[BITS / 2] = {};
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const uint32_t c = xpq::code_of<BITS>(x[j], step) + xpq::Codes<BITS>::kZero;
-        if (BITS == 8) w[j / 4] |= c << j % 4 * 8;
-        else w[j / 8] |= c << (j % 8 / 2 + j % 2 * 4) * 4;
+      for (int k = 0; k < kBatch; ++k) {
+        if (page[k] < 0) continue;   // the same in the whole group
+        const int at = s.at[i0 + k * part.lanes];
+        float x[E], top = 0.0f;
+        floats_of(raw[k], x);
+#pragma unroll
+        for (int j = 0; j < E; ++j) top = max_nan(top, fabsf(x[j]));
+#pragma unroll
+        for (int o = 1; o < 16 / E; o *= 2) top = max_nan(top, __shfl_xor_sync(group, top, o));
+        bool over = false;
+        if (top != top) {   // a NaN is held as 0
+          top = 0.0f;
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            x[j] = x[j] != x[j] ? 0.0f : x[j];
+            top = fmaxf(top, fabsf(x[j]));
+          }
+#pragma unroll
+          for (int o = 1; o < 16 / E; o *= 2) top = fmaxf(top, __shfl_xor_sync(group, top, o));
+          atomicOr(a.err, XP_ERR_RANGE);
+        }
+        const unsigned b = xpq::scale_byte<BITS>(top, &over);
+        const float step = xpq::scale_of(b), r = b ? reciprocal(step) : 0.0f;   // b = 0: all are 0
+        if (over) {
+          const float most = xpq::Codes<BITS>::kMost * step;
+#pragma unroll
+          for (int j = 0; j < E; ++j) x[j] = fminf(fmaxf(x[j], -most), most);
+          atomicOr(a.err, XP_ERR_RANGE);
+        }
+        char* head = pool + page[k] * a.page;
+        char* scale = head + a.scale_at + at * a.scale;
+        if (in == 0) scale[g] = (char)b;
+        if (part.e + E == a.D)   // the padding behind the scales
+          for (int p = g + 1; p < a.scale; ++p) scale[p] = 0;
+        uint32_t c[E], w[BITS == 8 ? E / 4 : 1] = {};
+        xpq::codes_of<BITS>(x, step, r, c);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          if (BITS == 8) w[j / 4] |= c[j] << j % 4 * 8;
+          else w[0] |= c[j] << (j / 2 + j % 2 * 4) * 4;
+        }
+        char* to = head + at * a.token;
+        if (BITS == 8) {
+          if constexpr (E == 4) *(uint32_t*)(to + part.e) = w[0];
+          else *(uint2*)(to + part.e) = make_uint2(w[0], w[E / 4 - 1]);
+        } else if constexpr (E == 4) {   // dims 4 to 7 of a word are 8 bits on; the first half's thread writes it
+          w[0] <<= part.e % 8 * 2;
+          w[0] |= __shfl_xor_sync(group, w[0], 1);
+          if (part.e % 8 == 0) *(uint32_t*)(to + part.e / 2) = w[0];
+        } else {
+          *(uint32_t*)(to + part.e / 2) = w[0];
+        }
       }
-      char* to = head + s.at[i] * a.token + g * (2 * BITS);
-      if (BITS == 8) *(uint4*)to = make_uint4(w[0], w[1], w[BITS / 2 - 2], w[BITS / 2 - 1]);
-      else *(uint2*)to = make_uint2(w[0], w[1]);
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
 // Read back: BITS of a code, or 16 / 32 for a cache of bf16 / fp32.
 // ---------------------------------------------------------------------------
-template <typename T> struct Piece {              // elements of 16 bytes
-  static constexpr int N = 16 / sizeof(T);
-};
 __device__ __forceinline__ void store(float* p, bool wide, const float (&x)[4], int n) {
   if (wide) {
     __stcs((float4*)p, make_float4(x[0], x[1], x[2], x[3]));
@@ -166,6 +216,18 @@ __device__ __forceinline__ void store(bf16* p, bool wide, const float (&x)[8], i
     for (int i = 0; i < n; ++i) p[i] = from_f<bf16>(x[i]);
   }
 }
+// N pairs of codes times a scale, two dims an operation and exactly: 1024 + c is an fp16 number with c in its
+// last bits.  4 bits: pair j is nibbles j and j + 4 of w.x; 8 bits: bytes 2j and 2j + 1 of w.
+template <int BITS, int N>
+__device__ __forceinline__ void widen(uint2 w, unsigned scale, __half2 (&out)[N]) {
+  const uint32_t s = scale * 0x00800080u, zero = BITS == 4 ? 0xE408E408u : 0xE480E480u;   // -1024 - 8, -1024 - 128
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t pair = BITS == 4 ? (w.x >> 4 * j & 0x000F000Fu) | 0x64006400u
+                                    : __byte_perm(j < 2 ? w.x : w.y, 0x64646464u, j % 2 ? 0x4342 : 0x4140);
+    out[j] = __hmul2(__hadd2(*(const __half2*)&pair, *(const __half2*)&zero), *(const __half2*)&s);
+  }
+}
 
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wide) {
@@ -175,47 +237,59 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
   const int n = blockIdx.x / chunks, t0 = (int)(blockIdx.x % chunks) * kTokens;
   find_pages(a, n, t0, a.first ? a.first[n] : 0, a.lens[n], &s);
 
-  const int pieces = (a.D + E - 1) / E, units = 2 * a.H * pieces;
-  const int lanes = max(1, kThreads / units);
-  const int lane = units < kThreads ? threadIdx.x / units : 0;
-  if (lane >= lanes) return;
   const int count = min(kTokens, a.T - t0);
-  for (int u = units < kThreads ? threadIdx.x % units : threadIdx.x; u < units; u += kThreads) {
-    const int e = u % pieces * E, h = u / pieces % a.H, is_v = u / pieces / a.H;
-    T* to = (T*)(is_v ? a.v : a.k) + n * a.sn + h * a.sh + e;
-    const char* pool = is_v ? a.vp : a.kp;
-    const int live = min(E, a.D - e);
-#pragma unroll 4
-    for (int i = lane; i < count; i += lanes) {
-      float x[E];
+  for_parts(a, E, [&](const Part& part) {
+    const int e = part.e, live = min(E, a.D - e);
+    T* to = (T*)(part.is_v ? a.v : a.k) + n * a.sn + t0 * a.st + part.h * a.sh + e;
+    const char* pool = part.is_v ? a.vp : a.kp;
+    for (int i0 = part.lane; i0 < count; i0 += kBatch * part.lanes) {
+      if constexpr (BITS <= 8) {
+        uint2 code[kBatch];
+        unsigned scale[kBatch];
 #pragma unroll
-      for (int j = 0; j < E; ++j) x[j] = 0.0f;
-      if (s.page[i] >= 0) {
-        if (BITS <= 8) {
-          const char* head = pool + s.page[i] * a.page + h * a.head;
-          const float step = xpq::scale_of((uint8_t)head[a.scale_at + s.at[i] * a.scale + e / 16]);
-          const uint32_t* code = (const uint32_t*)(head + s.at[i] * a.token + e / 8 * BITS);
-          if (BITS == 4) {   // a word of 8 dims, of which fp32 rows take the first or the last four
-            const uint32_t w = *code >> e % 8 * 2;
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-              x[j] = (float)((int)(w >> (j / 2 + j % 2 * 4) * 4 & 15u) - 8) * step;
-          } else {
-            code += e % 8 / 4;
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-              x[j] = (float)((int)(code[j / 4] >> j % 4 * 8 & 255u) - 128) * step;
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * part.lanes, page = i < count ? s.page[i] : -1;
+          code[k] = make_uint2(0, 0);
+          scale[k] = 0;   // what lies nowhere reads as 0
+          if (page >= 0) {
+            const char* head = pool + page * a.page + part.h * a.head;
+            scale[k] = (uint8_t)head[a.scale_at + s.at[i] * a.scale + e / 16];
+            const char* from = head + s.at[i] * a.token + e / 8 * BITS;
+            if constexpr (BITS == 4) code[k].x = *(const uint32_t*)from >> e % 8 * 2;   // fp32: the first four or the last
+            else if constexpr (E == 4) code[k].x = *(const uint32_t*)(from + e % 8);
+            else code[k] = *(const uint2*)from;
           }
-        } else {
-          const int64_t at = s.page[i] * a.page + s.at[i] * a.token + h * a.head + e;
+        }
 #pragma unroll
-          for (int j = 0; j < E; ++j)
-            if (j < live) x[j] = BITS == 16 ? to_f(((const bf16*)pool)[at + j]) : ((const float*)pool)[at + j];
+        for (int k = 0; k < kBatch; ++k) {
+          if (i0 + k * part.lanes >= count) break;
+          __half2 v[E / 2];
+          widen<BITS>(code[k], scale[k], v);
+          float x[E];
+#pragma unroll
+          for (int j = 0; j < E / 2; ++j) {
+            const float2 f = __half22float2(v[j]);
+            x[2 * j] = f.x, x[2 * j + 1] = f.y;
+          }
+          store(to + (i0 + k * part.lanes) * a.st, wide, x, live);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * part.lanes;
+          if (i >= count) break;
+          float x[E] = {};
+          if (s.page[i] >= 0) {
+            const int64_t at = s.page[i] * a.page + s.at[i] * a.token + part.h * a.head + e;
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+              if (j < live) x[j] = BITS == 16 ? to_f(((const bf16*)pool)[at + j]) : ((const float*)pool)[at + j];
+          }
+          store(to + i * a.st, wide, x, live);
         }
       }
-      store(to + (t0 + i) * a.st, wide, x, live);
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -267,22 +341,6 @@ __device__ __forceinline__ void widen_queries(const WidenArgs& w) {
     w.q_factor[h / w.group * per_head + ((int64_t)n * w.T + t) * w.group + h % w.group] =
         xpq::row_factor(up, w.scale);
   }
-}
-
-// 8 codes times a scale, two dims an operation: 1024 + c is an fp16 number with c in its last bits
-template <int BITS>
-__device__ __forceinline__ uint4 widen8(uint2 w, unsigned scale) {
-  uint32_t out[4];
-  const uint32_t s = scale * 0x00800080u;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t pair = BITS == 4 ? (w.x >> 4 * j & 0x000F000Fu) | 0x64006400u
-                                    : __byte_perm(j < 2 ? w.x : w.y, 0x64646464u, j % 2 ? 0x4342 : 0x4140);
-    const uint32_t zero = BITS == 4 ? 0xE408E408u : 0xE480E480u;   // -1024 - 8, -1024 - 128
-    const __half2 v = __hmul2(__hadd2(*(const __half2*)&pair, *(const __half2*)&zero), *(const __half2*)&s);
-    out[j] = *(const uint32_t*)&v;
-  }
-  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 template <int BITS, int D>
@@ -337,8 +395,11 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
 #pragma unroll
   for (int k = 0; k < kEach; ++k)
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-      *(uint4*)(to + (kv ? to_v : 0) + k * kStep * D) = widen8<BITS>(code[k][kv], scale[k][kv]);
+    for (int kv = 0; kv < 2; ++kv) {
+      __half2 v[4];
+      widen<BITS>(code[k][kv], scale[k][kv], v);
+      *(uint4*)(to + (kv ? to_v : 0) + k * kStep * D) = *(const uint4*)v;
+    }
 }
 
 template <typename T> bool wide_rows(const RowArgs& a) {

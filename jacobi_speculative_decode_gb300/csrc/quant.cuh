@@ -58,24 +58,41 @@ __device__ __forceinline__ float row_factor(float up, float scale) {
 
 // The least scale that reaches `top`, a group's largest magnitude; *over where none does.
 template <int BITS> __device__ __forceinline__ unsigned scale_byte(float top, bool* over) {
-  constexpr float most = Codes<BITS>::kMost;
-  const unsigned h = __half_as_ushort(__float2half_ru(top / most));
-  unsigned b = min((h + 127u) >> 7, Codes<BITS>::kTop);
-  // the quotient may have been rounded down onto a scale just short of it; products are exact
-  if (b < Codes<BITS>::kTop && scale_of(b) * most < top) ++b;
+  constexpr float most = Codes<BITS>::kMost, least = 6.103515625e-05f;   // 2^-14, the least that is not subnormal
+  // A quotient that is not above the true one; in the scales' bits, rounded up.  A subnormal one, whole 2^-17,
+  // is taken 2^-14 higher, where the spacing is the same, and 8 places back.
+  const float q = __fmul_rd(fminf(top, 65536.0f), BITS == 4 ? 0x1.249248p-3f : 0x1.020408p-7f);
+  const bool low = q < least;
+  const unsigned bits = __float_as_uint(low ? __fadd_rd(q, least) : q) - (112u << 23);
+  unsigned b = ((bits + 0xFFFFFu) >> 20) - (low ? 8u : 0u);
+  b = min(b, Codes<BITS>::kTop);
+  if (b < Codes<BITS>::kTop && scale_of(b) * most < top) ++b;   // products are exact
   *over = scale_of(b) * most < top;
   return b;
 }
 
-// x over s to the nearest whole number, ties to even, at most +-kMost (s = 0: every x of its group is 0)
-template <int BITS> __device__ __forceinline__ int code_of(float x, float s) {
-  constexpr float most = Codes<BITS>::kMost;
-  if (s == 0.0f) return 0;
-  float n = fminf(fmaxf(rintf(x / s), -most), most);
-  // The quotient may have been rounded onto a tie that is none.  What is left is exact.
-  const float rest = fmaf(-n, s, x);
-  n += rest > 0.5f * s ? 1.0f : rest < -0.5f * s ? -1.0f : 0.0f;
-  return (int)fminf(fmaxf(n, -most), most);
+// E elements x over s (|x| at most kMost * s) to the nearest whole numbers, ties to even, as they are held; r: about
+// 1/s.  A product with r may lie across a half, or on one; what a code leaves of x is exact, and where it is
+// half of s or more the code is looked at again.
+template <int BITS, int E>
+__device__ __forceinline__ void codes_of(const float (&x)[E], float s, float r, uint32_t (&code)[E]) {
+  constexpr float magic = 12582912.0f + Codes<BITS>::kZero;   // 1.5 * 2^23: a sum's last bits are the whole number
+  const float half = 0.5f * s;
+  bool look = false;
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    const float t = fmaf(x[j], r, magic);
+    look |= fabsf(fmaf(magic - t, s, x[j])) >= half;
+    code[j] = __float_as_uint(t) & 0xFFu;
+  }
+  if (look && s > 0.0f) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int whole = (int)code[j] - Codes<BITS>::kZero;
+      const float rest = fmaf(-(float)whole, s, x[j]);
+      if (fabsf(rest) > half || (fabsf(rest) == half && (whole & 1))) code[j] += rest > 0.0f ? 1 : -1;
+    }
+  }
 }
 
 }  // namespace xpq
