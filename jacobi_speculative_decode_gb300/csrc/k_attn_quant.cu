@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
   constexpr int KB = BITS == 4 ? (KG + 1) / 2 : 0;   // products for the 8 too much: of scores,
   constexpr bool VB = BITS == 4;                     // of results
   constexpr bool QREGS = NQ < 4;
+  constexpr int KT = NQ * KS >= 32 ? 1 : 2;          // tiles of 16 keys at a time
   extern __shared__ __align__(16) char smem[];
   __shared__ float s_m[kWarps][8 * NQ], s_l[kWarps][8 * NQ];
   __shared__ Start s_start;
@@ -474,10 +475,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     const uint8_t* vs = ks + kStep * C::SCALE;
     const int kb = base_of(it);
 
-    // S^T: 32 keys by 8 NQ queries
-    float s[2][NQ][4];
+    // 16 KT keys at a time: where the results of 32 queries fill the registers, half a step's scores fit beside them
+#pragma unroll(KT == 2 ? 2 : 1)
+    for (int kh = 0; kh < 2; kh += KT) {
+    // S^T: 16 KT keys by 8 NQ queries
+    float s[KT][NQ][4];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
+    for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
       uint32_t w[2][KW], bytes[2];   // scales of the lane's groups
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int key = kt * 16 + r * 8 + gr;
+        const int key = (kh + kt) * 16 + r * 8 + gr;
         load_words<KW>(sk + key * C::CODE + t4 * (C::CODE / 4), w[r]);
         const uint8_t* from = ks + key * C::SCALE + t4 * KG;
         bytes[r] = (KG == 1 ? *from : KG == 2 ? *(const uint16_t*)from : *(const uint32_t*)from) & k_groups;
@@ -545,11 +549,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     for (int q = 0; q < NQ; ++q) {
       top[q][0] = top[q][1] = -INFINITY;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float v = s[kt][q][e] * cz[q][e % 2];
-          if (kb + kStep > least && kb + kt * 16 + e / 2 * 8 + gr >= limit[q][e % 2]) v = -INFINITY;
+          if (kb + kStep > least && kb + (kh + kt) * 16 + e / 2 * 8 + gr >= limit[q][e % 2]) v = -INFINITY;
           s[kt][q][e] = v;
           top[q][e % 2] = fmaxf(top[q][e % 2], v);
         }
@@ -573,14 +577,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
           if (VB) ob[q][i] *= f, ob[q][2 + i] *= f;
         }
     }
-    uint32_t p[2][NQ][2];
+    uint32_t p[KT][NQ][2];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       float base[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) base[i] = (m[q][i] == -INFINITY ? 0.0f : m[q][i]) - kLift;
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
+      for (int kt = 0; kt < KT; ++kt) {
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -594,19 +598,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
 
     // O^T: a lane's rows are dims 2 i and 2 i + 1 of its DP / 8, its keys 2 t4, 2 t4 + 1 and those 8 on
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
+    for (int kt = 0; kt < KT; ++kt) {
       uint32_t w[4][VW];
       Scale4 sc4[2][VG];   // of a pair of keys
       __half2 sc8[2][VG];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        load_words<VW>(sv + (kt * 16 + 2 * t4 + r / 2 * 8 + r % 2) * C::CODE + gr * (C::CODE / 8), w[r]);
+        load_words<VW>(sv + ((kh + kt) * 16 + 2 * t4 + r / 2 * 8 + r % 2) * C::CODE + gr * (C::CODE / 8), w[r]);
 #pragma unroll
       for (int i = 0; i < VG; ++i) {
         const int group = DP == 64 ? gr / 2 : DP == 128 ? gr : 2 * gr + i;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint8_t* from = vs + (kt * 16 + 2 * t4 + r * 8) * C::SCALE + group;
+          const uint8_t* from = vs + ((kh + kt) * 16 + 2 * t4 + r * 8) * C::SCALE + group;
           sc8[r][i] = scales(group < groups ? from[0] : 0, group < groups ? from[C::SCALE] : 0);
           if constexpr (BITS == 4) sc4[r][i] = scale4(sc8[r][i]);
         }
@@ -643,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
             mma(o[q][i * (BITS == 4 ? 4 : 2) + j], f, p[kt][q][0], p[kt][q][1]);
         }
       }
+    }
     }
   }
   wait_groups<0>();
@@ -715,36 +720,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
   }
 }
 
-// One warp a query row: what tcgen05 left of its prefix, and the pieces of its prefix and of its tail (the
+// L lanes a query row (32, or 16 for heads to 64): what tcgen05 left of its prefix, and the pieces of its prefix and of its tail (the
 // unit's own and those of the CTAs at whose beginning it was cut), brought to a common maximum:
 //   out = sum_p a_p O_p / sum_p a_p l_p,  a_p = 2^(m_p - m).
 // A lane holds E dims.  Bound by the latency of what it asks for, so four pieces are asked for at once.
-template <int E>
+template <int E, int L>
 __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_constant__ xp_attn_args g) {
   ptx::pdl_wait();
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
   if (row >= rows) return;
-  const int lane = threadIdx.x & 31, D = g.dim, RT = g.plan.rows_tile, per_seq = g.a.T * g.group;
+  const int lane = threadIdx.x % L, D = g.dim, RT = g.plan.rows_tile, per_seq = g.a.T * g.group;
   const int h = (int)(row % g.a.heads), t = (int)(row / g.a.heads % g.a.T);
   const int n = (int)(row / g.a.heads / g.a.T), hk = h / g.group, i = t * g.group + h % g.group;
   const int64_t* line = (const int64_t*)g.line;
   const int64_t chunk = line[0], begin = g.a.max_len > 0 ? line[1 + n] : 0;
   const bool dims = lane * E < D;
+  const unsigned row_lanes = L == 32 ? kAll : 0xFFFFu << (threadIdx.x & 16);
 
   float o[E], m = -INFINITY, l = 0.0f;
 #pragma unroll
   for (int c = 0; c < E; ++c) o[c] = 0.0f;
   auto load = [&](const float* acc, float (&x)[E]) {
-    if constexpr (E == 2) {
-      const float2 v = __ldcg((const float2*)(acc + lane * 2));
-      x[0] = v.x, x[1] = v.y;
-    } else {
 #pragma unroll
-      for (int c = 0; c < E; c += 4) {
-        const float4 v = __ldcg((const float4*)(acc + lane * E + c));
-        x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
-      }
+    for (int c = 0; c < E; c += 4) {
+      const float4 v = __ldcg((const float4*)(acc + lane * E + c));
+      x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
     }
   };
   auto add = [&](float2 st, const float (&x)[E]) {   // a piece that has a visible key
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
   auto pieces = [&](int keys, int64_t at, int64_t unit, int r) {
     const int T = rounds_of(keys), cost = cost_of(keys);
     const int64_t c0 = at / chunk, c1 = (at + cost - 1) / chunk;
-    for (int64_t first = c0; first <= c1; first += 32) {   // a lane a CTA
+    for (int64_t first = c0; first <= c1; first += L) {   // a lane a CTA
       const int64_t c = first + lane;
       int64_t from = 0;
       float2 st = make_float2(0.0f, 0.0f);   // of no piece, and where no key was visible: acc may hold anything
@@ -768,14 +769,14 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
           st = __ldcg((const float2*)g.stat + from);
         }
       }
-      const int count = (int)min((int64_t)32, c1 - first + 1);
+      const int count = (int)min((int64_t)L, c1 - first + 1);
       for (int k = 0; k < count; k += 4) {
         float2 s[4];
         float x[4][E];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int64_t f = __shfl_sync(kAll, from, min(k + j, 31));
-          s[j] = make_float2(__shfl_sync(kAll, st.x, min(k + j, 31)), __shfl_sync(kAll, st.y, min(k + j, 31)));
+          const int64_t f = __shfl_sync(row_lanes, from, min(k + j, L - 1), L);
+          s[j] = make_float2(__shfl_sync(row_lanes, st.x, min(k + j, L - 1), L), __shfl_sync(row_lanes, st.y, min(k + j, L - 1), L));
           if (k + j >= count) s[j].y = 0.0f;
           if (dims && s[j].y != 0.0f) load(g.acc + f * D, x[j]);
         }
@@ -811,8 +812,7 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
         const __nv_bfloat162 w = __floats2bfloat162_rn(o[c] * inv, o[c + 1] * inv);
         v[c / 2] = *(const uint32_t*)&w;
       }
-      if constexpr (E == 2) *(uint32_t*)out = v[0];
-      else if constexpr (E == 4) *(uint2*)out = make_uint2(v[0], v[1]);
+      if constexpr (E == 4) *(uint2*)out = make_uint2(v[0], v[1]);
       else *(uint4*)out = make_uint4(v[0], v[1], v[E / 2 - 2], v[E / 2 - 1]);
     } else {
 #pragma unroll
@@ -852,6 +852,9 @@ template <int BITS> cudaError_t launch_dims(const xp_attn_args& g, const Quant& 
 
 // Many queries of each key are the tensor cores' work, not that of widening: from so many of a kv head on,
 // what they see is widened to fp16 in the workspace once (exactly, as here) and attended over on tcgen05.
+// 32 sequences of 1, 2, 4 tokens behind 8192, 8 kv heads of 4 x 128 in 4 bits: 64 rows 65 us widened and 46 not,
+// 128 rows 66 and 61, 256 rows 62 and 93.  32 tails of 17 to 1500 tokens, rows of one: 16 take 65 and 41, 32 take
+// 69 and 69, 64 take 73 and 108.
 constexpr int kWidePrefixRows = 256, kWideTailRows = 64;
 constexpr size_t kWideTailBytes = (size_t)1 << 30;   // of tails that may be widened
 
@@ -890,9 +893,12 @@ xp_attn_plan xp_attn_quant_plan(const xp_cache* c, const xp_attn* a) {
   auto pages = [](int keys) { return (keys + kWidePage - 1) / kWidePage; };
   const size_t page_bytes = (size_t)kWidePage * c->d.kv_heads * D * 4;
   const bool prefix = c->attn_tc && a->prefix_len > 0 && (int64_t)a->N * per_seq >= kWidePrefixRows;
-  const bool tails = c->attn_tc && a->max_len > 0 && per_seq >= kWideTailRows &&
-                     (prefix || a->prefix_len == 0) &&
-                     (size_t)a->N * pages(a->max_len) * page_bytes <= kWideTailBytes;
+  // Tails beside a widened prefix are widened too where they are no longer than it all together: a kernel of
+  // their own and a second joining take 20 us.
+  const size_t tail_pages = (size_t)a->N * pages(a->max_len);
+  const bool tails = c->attn_tc && a->max_len > 0 && tail_pages * page_bytes <= kWideTailBytes &&
+                     ((per_seq >= kWideTailRows && (prefix || a->prefix_len == 0)) ||
+                      (prefix && tail_pages <= 2 * (size_t)pages(a->prefix_len)));
   if (prefix || tails) {
     p.wide_prefix = prefix ? pages(a->prefix_len) : 0;
     p.wide_tail = tails ? pages(a->max_len) : 0;
@@ -994,8 +1000,8 @@ cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaS
   const cudaError_t e = c->d.dtype == XP_Q8 ? launch_dims<8>(q, z, c->num_sms, s) : launch_dims<4>(q, z, c->num_sms, s);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
-  return xp_launch_pdl(D <= 64    ? attn_quant_combine_kernel<2>
-                       : D <= 128 ? attn_quant_combine_kernel<4>
-                                  : attn_quant_combine_kernel<8>,
-                       dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, q);
+  return xp_launch_pdl(D <= 64    ? attn_quant_combine_kernel<4, 16>
+                       : D <= 128 ? attn_quant_combine_kernel<4, 32>
+                                  : attn_quant_combine_kernel<8, 32>,
+                       dim3((unsigned)((rows * (D <= 64 ? 16 : 32) + 255) / 256)), dim3(256), 0, s, q);
 }

@@ -61,20 +61,28 @@ __device__ __forceinline__ void find_pages(const RowArgs& a, int n, int t0, int6
 template <typename T> struct Piece {              // elements of 16 bytes
   static constexpr int N = 16 / sizeof(T);
 };
-// a piece; wide: from a 16-byte boundary
-template <typename T> __device__ __forceinline__ uint4 load_piece(const T* p, bool wide) {
-  if (wide) return __ldcs((const uint4*)p);
-  uint4 v;
-  T* e = (T*)&v;
+// 8 consecutive elements; wide: from a 16-byte boundary
+template <typename T> struct Eight {
+  uint4 v[8 / Piece<T>::N];
+  __device__ __forceinline__ void load(const T* p, bool wide) {
+    if (wide) {
 #pragma unroll
-  for (int i = 0; i < Piece<T>::N; ++i) e[i] = p[i];
-  return v;
+      for (int i = 0; i < 8 / Piece<T>::N; ++i) v[i] = __ldcs((const uint4*)p + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ((T*)v)[i] = p[i];
+    }
+  }
+};
+__device__ __forceinline__ void floats_of(const Eight<float>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[4 * i] = __uint_as_float(r.v[i].x), x[4 * i + 1] = __uint_as_float(r.v[i].y);
+    x[4 * i + 2] = __uint_as_float(r.v[i].z), x[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
 }
-__device__ __forceinline__ void floats_of(const uint4& v, float (&x)[4]) {
-  x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
-}
-__device__ __forceinline__ void floats_of(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void floats_of(const Eight<bf16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
 }
@@ -90,7 +98,8 @@ __device__ __forceinline__ float reciprocal(float x) {   // nearly
   return r;
 }
 
-constexpr int kBatch = 4;   // tokens of a thread whose loads are on their way together
+// tokens of a thread whose loads are on their way together (four to append leave two CTAs an SM: 140 us, not 133)
+constexpr int kAppendBatch = 2, kReadBatch = 4;
 
 // What a thread does of a row: piece `e` of head `h` of K or V, for every lanes-th token from `lane` on.
 struct Part {
@@ -111,84 +120,73 @@ template <typename F> __device__ __forceinline__ void for_parts(const RowArgs& a
 }
 
 // ---------------------------------------------------------------------------
-// Quantised append.  The 4 (fp32) or 2 (bf16) threads of 16 dims find their largest together.
+// Quantised append.  A thread has 8 dims, and its neighbour the other 8 of their scale: with 4, as 16-byte loads
+// would have it of fp32, what a scale costs is too much (write prompts' append 102 us and not 80).
 // ---------------------------------------------------------------------------
 template <int BITS, typename T>
-__global__ void __launch_bounds__(kThreads) append_quant_kernel(const RowArgs a, bool wide) {
-  constexpr int E = Piece<T>::N;
+__global__ void __launch_bounds__(kThreads, 4) append_quant_kernel(const RowArgs a, bool wide) {
   __shared__ Places s;
   const int chunks = (a.T + kTokens - 1) / kTokens;
   const int n = blockIdx.x / chunks, t0 = (int)(blockIdx.x % chunks) * kTokens;
   find_pages(a, n, t0, (int64_t)a.lens[n] - a.T, INT64_MAX, &s);
 
-  // threads of one group: neighbours, as a row's pieces are a whole number of groups
-  const unsigned group = (E == 4 ? 0xFu : 0x3u) << (threadIdx.x & 31 & -(16 / E));
-  for_parts(a, E, [&](const Part& part) {
+  const unsigned both = 3u << (threadIdx.x & 30);   // the two of a group: rows are a whole number of groups
+  for_parts(a, 8, [&](const Part& part) {
     const T* from = (const T*)(part.is_v ? a.v : a.k) + n * a.sn + t0 * a.st + part.h * a.sh + part.e;
     char* pool = (part.is_v ? a.vp : a.kp) + part.h * a.head;
-    const int g = part.e / 16, in = part.e % 16;
-    for (int i0 = part.lane; i0 < kTokens; i0 += kBatch * part.lanes) {
-      uint4 raw[kBatch];
-      int page[kBatch];
+    const int g = part.e / 16;
+    for (int i0 = part.lane; i0 < kTokens; i0 += kAppendBatch * part.lanes) {
+      Eight<T> raw[kAppendBatch];
+      int page[kAppendBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
+      for (int k = 0; k < kAppendBatch; ++k) {
         const int i = i0 + k * part.lanes;
         page[k] = i < kTokens ? s.page[i] : -1;
-        raw[k] = make_uint4(0, 0, 0, 0);
-        if (page[k] >= 0) raw[k] = load_piece(from + i * a.st, wide);
+        if (page[k] >= 0) raw[k].load(from + i * a.st, wide);
       }
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (page[k] < 0) continue;   // the same in the whole group
+      for (int k = 0; k < kAppendBatch; ++k) {
+        if (page[k] < 0) continue;   // the same in both
         const int at = s.at[i0 + k * part.lanes];
-        float x[E], top = 0.0f;
+        float x[8], top = 0.0f;
         floats_of(raw[k], x);
 #pragma unroll
-        for (int j = 0; j < E; ++j) top = max_nan(top, fabsf(x[j]));
-#pragma unroll
-        for (int o = 1; o < 16 / E; o *= 2) top = max_nan(top, __shfl_xor_sync(group, top, o));
-        bool over = false;
+        for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(x[j]));
+        top = max_nan(top, __shfl_xor_sync(both, top, 1));
         if (top != top) {   // a NaN is held as 0
           top = 0.0f;
 #pragma unroll
-          for (int j = 0; j < E; ++j) {
+          for (int j = 0; j < 8; ++j) {
             x[j] = x[j] != x[j] ? 0.0f : x[j];
             top = fmaxf(top, fabsf(x[j]));
           }
-#pragma unroll
-          for (int o = 1; o < 16 / E; o *= 2) top = fmaxf(top, __shfl_xor_sync(group, top, o));
+          top = fmaxf(top, __shfl_xor_sync(both, top, 1));
           atomicOr(a.err, XP_ERR_RANGE);
         }
+        bool over;
         const unsigned b = xpq::scale_byte<BITS>(top, &over);
         const float step = xpq::scale_of(b), r = b ? reciprocal(step) : 0.0f;   // b = 0: all are 0
         if (over) {
           const float most = xpq::Codes<BITS>::kMost * step;
 #pragma unroll
-          for (int j = 0; j < E; ++j) x[j] = fminf(fmaxf(x[j], -most), most);
+          for (int j = 0; j < 8; ++j) x[j] = fminf(fmaxf(x[j], -most), most);
           atomicOr(a.err, XP_ERR_RANGE);
         }
         char* head = pool + page[k] * a.page;
         char* scale = head + a.scale_at + at * a.scale;
-        if (in == 0) scale[g] = (char)b;
-        if (part.e + E == a.D)   // the padding behind the scales
+        if (part.e % 16 == 0) scale[g] = (char)b;
+        if (part.e + 8 == a.D)   // the padding behind the scales
           for (int p = g + 1; p < a.scale; ++p) scale[p] = 0;
-        uint32_t c[E], w[BITS == 8 ? E / 4 : 1] = {};
+        uint32_t c[8];
         xpq::codes_of<BITS>(x, step, r, c);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          if (BITS == 8) w[j / 4] |= c[j] << j % 4 * 8;
-          else w[0] |= c[j] << (j / 2 + j % 2 * 4) * 4;
-        }
-        char* to = head + at * a.token;
-        if (BITS == 8) {
-          if constexpr (E == 4) *(uint32_t*)(to + part.e) = w[0];
-          else *(uint2*)(to + part.e) = make_uint2(w[0], w[E / 4 - 1]);
-        } else if constexpr (E == 4) {   // dims 4 to 7 of a word are 8 bits on; the first half's thread writes it
-          w[0] <<= part.e % 8 * 2;
-          w[0] |= __shfl_xor_sync(group, w[0], 1);
-          if (part.e % 8 == 0) *(uint32_t*)(to + part.e / 2) = w[0];
+        char* to = head + at * a.token + part.e / 8 * BITS;
+        if constexpr (BITS == 8) {
+          *(uint2*)to = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24, c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
         } else {
-          *(uint32_t*)(to + part.e / 2) = w[0];
+          uint32_t w = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w |= c[j] << (j / 2 + j % 2 * 4) * 4;
+          *(uint32_t*)to = w;
         }
       }
     }
@@ -242,12 +240,12 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
     const int e = part.e, live = min(E, a.D - e);
     T* to = (T*)(part.is_v ? a.v : a.k) + n * a.sn + t0 * a.st + part.h * a.sh + e;
     const char* pool = part.is_v ? a.vp : a.kp;
-    for (int i0 = part.lane; i0 < count; i0 += kBatch * part.lanes) {
+    for (int i0 = part.lane; i0 < count; i0 += kReadBatch * part.lanes) {
       if constexpr (BITS <= 8) {
-        uint2 code[kBatch];
-        unsigned scale[kBatch];
+        uint2 code[kReadBatch];
+        unsigned scale[kReadBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < kReadBatch; ++k) {
           const int i = i0 + k * part.lanes, page = i < count ? s.page[i] : -1;
           code[k] = make_uint2(0, 0);
           scale[k] = 0;   // what lies nowhere reads as 0
@@ -261,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
           }
         }
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < kReadBatch; ++k) {
           if (i0 + k * part.lanes >= count) break;
           __half2 v[E / 2];
           widen<BITS>(code[k], scale[k], v);
@@ -275,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < kReadBatch; ++k) {
           const int i = i0 + k * part.lanes;
           if (i >= count) break;
           float x[E] = {};
