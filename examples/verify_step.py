@@ -11,9 +11,10 @@ N requests that share a prompt.  Every step
   4. the target attends for all B slots at once,
      the shared prompt read once for the batch            xp_prefix_attention
   5. the drafts are verified, one token is drawn          xp_verify_drafts
+     and what was emitted is scored, if asked for         xp_token_logprobs
   6. what was not accepted leaves the cache               xp_cache_resize
 
-and at the end one request is continued twice (xp_cache_fork), another dropped, and the pool
+(the cache may be one of 8 or 4 bits: the calls are the same) and at the end one request is continued twice (xp_cache_fork), another dropped, and the pool
 packed (xp_cache_compact).
 
     python -m examples.verify_step
@@ -102,10 +103,12 @@ class Drafter:
 
 
 def run(requests=5, block=6, steps=6, prompt_len=75, page=16, temperature=0.0, dtype=torch.float32,
-        seed=0, sampled=False):
+        seed=0, sampled=False, bits=0, scores=None, top=3):
     """Decode `requests` continuations of one prompt, from greedy drafts or (sampled) from drafts drawn
-    from the refinement's logits.  Returns (target, prompt, first tokens, tokens
-    emitted by each request, drafts accepted, drafts made)."""
+    from the refinement's logits, over a cache of the target's type or (bits, 8 or 4; bf16 targets) a quantised
+    one.  Returns (target, prompt, first tokens, tokens emitted by each request, drafts accepted, drafts made).
+    scores: a list that receives, for every step, the logits, the tokens emitted and their logprob, entropy,
+    rank and `top` alternatives."""
     target = Target(dtype=dtype, seed=seed)
     drafter = Drafter(target, block, requests)
     g = torch.Generator().manual_seed(seed + 7)
@@ -115,8 +118,12 @@ def run(requests=5, block=6, steps=6, prompt_len=75, page=16, temperature=0.0, d
     width = -(-(steps + 1) * B // page)
     prompt_pages = -(-prompt_len // page)
     pages = prompt_pages + (N + 2) * width
-    k, v = (torch.empty(1, pages, page, H, D, dtype=dtype, device="cuda") for _ in range(2))
-    cache = xp.Cache(k, v)
+    if bits:
+        k, v = (xp.QuantCache.pool(1, pages, page, H, D, bits) for _ in range(2))
+        cache = xp.QuantCache(k, v, page, D, bits)
+    else:
+        k, v = (torch.empty(1, pages, page, H, D, dtype=dtype, device="cuda") for _ in range(2))
+        cache = xp.Cache(k, v)
 
     # row 0 of the table is the shared prompt, the requests' tails follow
     table = torch.full((N + 1, max(width, prompt_pages)), -1, **int32)
@@ -153,6 +160,14 @@ def run(requests=5, block=6, steps=6, prompt_len=75, page=16, temperature=0.0, d
         noise = torch.empty(N, V).exponential_(generator=g).clamp_(min=1e-20).cuda()
         xp.xp_verify_drafts(drafter.head.handle, logits, draft, blk, None, heat, u, noise, tokens, counts,
                             None, drafter.verify_ws)
+        if scores is not None:
+            score = dict(logprob=torch.empty(N, B, device="cuda"), entropy=torch.empty(N, B, device="cuda"),
+                         rank=torch.empty(N, B, **int32),
+                         top_ids=torch.empty(N, B, top, dtype=torch.int64, device="cuda"),
+                         top_logprobs=torch.empty(N, B, top, device="cuda"))
+            xp.xp_token_logprobs(drafter.head.handle, logits, tokens, heat, *score.values(),
+                                 drafter.head.logprobs_workspace(N * B, top))
+            scores.append(dict(score, logits=logits, tokens=tokens.clone(), heat=heat))
         # the anchor and the accepted drafts stay: as many tokens as were emitted
         keep = kept.clone()
         keep[1:] += counts
@@ -187,6 +202,13 @@ def main():
         print("%s drafts accepted: %d of %d" % ("sampled" if sampled else "greedy", accepted, made))
         for n, row in enumerate(emitted):
             print("request %d: %s" % (n, row))
+    for bits in (8, 4):
+        scores = []
+        _, _, _, emitted, accepted, made = run(temperature=0.8, dtype=torch.bfloat16, bits=bits, scores=scores)
+        print("a cache of %d bits: accepted %d of %d" % (bits, accepted, made))
+        for n in range(len(emitted)):
+            print("request %d: %s" % (n, ["%.2f" % x for s in scores for t, x in zip(s["tokens"][n], s["logprob"][n])
+                                          if t >= 0]))
 
 
 if __name__ == "__main__":

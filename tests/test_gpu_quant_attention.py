@@ -119,6 +119,11 @@ CASES = [  # N, T, kv heads, group, dim, page, prefix, lens
     (6, 1, 2, 4, 128, 16, 700, [0] * 6),
     (1, 40, 2, 4, 64, 16, 0, [40]),
     (2, 1, 1, 4, 128, 64, 0, [5000, 4000]),
+    # more sequences than a CTA has threads; one that every CTA has a piece of
+    (300, 1, 1, 2, 64, 8, 0, [i % 41 for i in range(300)]),
+    (1, 1, 1, 4, 64, 64, 0, [30000]),
+    (1, 2, 1, 4, 128, 32, 0, [20011]),
+    (2, 1, 1, 1, 256, 48, 9001, [0, 700]),
     # many queries a key: the prefix, the tails or both are widened first
     (70, 1, 2, 4, 128, 16, 700, [1 + 5 * i % 90 for i in range(70)]),
     (40, 1, 1, 8, 64, 20, 129, [7 * i % 150 for i in range(40)]),
@@ -237,3 +242,73 @@ def test_streams_and_graphs_with_a_workspace_each():
                 graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_pages_past_two_to_the_31_bytes(T):
+    ps, H, D, bits = 64, 2, 128, 4
+    size = xp.xp_quant_head_bytes(ps, D, bits)
+    pages = 2 ** 31 // (H * size) + 5
+    g = np.random.default_rng(8)
+    rows = [torch.from_numpy(g.normal(size=(1, 200, H, D)).astype(np.float32)).cuda() for _ in range(2)]
+    q = torch.from_numpy(g.normal(size=(1, T, 4, D))).to(torch.bfloat16).cuda()
+    outs = []
+    for count, ids in ((pages, [pages - 1, pages - 3, 0, pages - 2]), (4, [2, 1, 0, 3])):
+        k, v = (xp.QuantCache.pool(1, count, ps, H, D, bits) for _ in range(2))
+        c = xp.QuantCache(k, v, ps, D, bits)
+        xp.xp_cache_append(c.handle, 0, *rows, cu([ids]), cu([200]))
+        out = torch.empty_like(q)
+        a = xp.make_attn(q, out, 0, 0, 200, 0.1)
+        xp.xp_prefix_attention(c.handle, a, q, None, cu([ids]), cu([200]), out, None, c.attention_workspace(a))
+        assert xp.xp_cache_get_error(c.handle) == xp.XP_OK
+        outs.append(out)
+    assert torch.equal(*outs) and torch.isfinite(outs[0].float()).all()
+
+
+def test_queries_and_results_off_sixteen_byte_boundaries():
+    for T in (1, 80):
+        c, prefix_table, table, _ = build(4, 16, 2, 64, 40, [130, 170], 6)
+        g = torch.Generator(device="cuda").manual_seed(T)
+        q = torch.randn(2, T, 8, 64, generator=g, device="cuda", dtype=torch.bfloat16)
+        outs = []
+        for shift in (0, 3):
+            wide_q = torch.zeros(2, T, 8, 69, device="cuda", dtype=torch.bfloat16)
+            wide_o = torch.full_like(wide_q, 7.0)
+            x, out = wide_q[..., shift:shift + 64], wide_o[..., shift:shift + 64]
+            x.copy_(q)
+            a = xp.make_attn(x, out, 0, 40, 170, 0.1)
+            xp.xp_prefix_attention(c.handle, a, x, prefix_table, table, cu([130, 170]), out, None,
+                                   c.attention_workspace(a))
+            assert (wide_o[..., :shift] == 7).all() and (wide_o[..., shift + 64:] == 7).all()
+            outs.append(out.clone())
+        assert torch.equal(*outs)
+
+
+def test_refusals():
+    c, prefix_table, table, _ = build(4, 16, 1, 64, 20, [64], 4)
+    q = torch.randn(1, 1, 2, 64, device="cuda", dtype=torch.bfloat16)
+    out, lens = torch.empty_like(q), cu([64])
+    a = xp.make_attn(q, out, 0, 20, 64, 0.1)
+    ws = c.attention_workspace(a)
+
+    def call(code, cache=c, attn=a, q=q, prefix=prefix_table, table=table, out=out, ws=ws):
+        with pytest.raises(xp.XPError) as e:
+            xp.xp_prefix_attention(cache.handle, attn, q, prefix, table, lens, out, None, ws)
+        assert e.value.code == code
+
+    f = q.float()
+    call(xp.XP_EINVAL, attn=xp.make_attn(f, torch.empty_like(f), 0, 20, 64, 0.1), q=f, out=torch.empty_like(f))
+    narrow = q[..., :48].contiguous()
+    call(xp.XP_EINVAL, attn=xp.make_attn(narrow, torch.empty_like(narrow), 0, 20, 64, 0.1), q=narrow,
+         out=torch.empty_like(narrow))
+    call(xp.XP_EINVAL, attn=xp.make_attn(q, out, 1, 20, 64, 0.1))
+    call(xp.XP_EINVAL, prefix=prefix_table[:1])
+    call(xp.XP_EINVAL, table=table[:, :1].contiguous())
+    call(xp.XP_ECAPACITY, ws=ws[:256])
+    rows = torch.zeros(1, 1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    for bad in (rows.expand(1, 1, 2, 64), rows[..., :32]):
+        with pytest.raises(xp.XPError):
+            xp.xp_cache_append(c.handle, 0, bad, bad, table, lens)
+        with pytest.raises(xp.XPError):
+            xp.xp_cache_read(c.handle, 0, table, lens, None, bad, bad)
+    assert xp.xp_cache_get_error(c.handle) == xp.XP_OK
