@@ -293,10 +293,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
 // ---------------------------------------------------------------------------
 // A quantised cache's tokens as fp16 (exactly) for attention on tcgen05, which many queries of each key are
 // better done by: pools [head][page of kWidePage tokens][dim] and the table that names their pages in order.
-// Behind a sequence's end its last page is zeros.  A CTA is 64 tokens of a head.  The CTAs behind the pages'
-// make the queries fp16, a warp a row, scaled by the power of two that brings the row's largest into [1, 4).
+// Behind a sequence's end its last page is zeros.  A CTA is 32 tokens of a head (with 64 draft blocks take 6 us
+// more, with 128 24).  The CTAs behind the pages' make the queries fp16, a warp a row, scaled by the power of two that brings the row's largest into [1, 4).
 // ---------------------------------------------------------------------------
-constexpr int kWideTokens = 64;
+constexpr int kWideTokens = 32;
 struct WidenArgs {
   RowArgs r;                      // r.table, r.ld, r.lens: the tails'
   const int32_t* prefix_table;
