@@ -130,17 +130,17 @@ template <> struct Vec<bf16> {
       f[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
     }
   }
-  // elements above v, or not below it
-  static __device__ __forceinline__ W count(const uint4& x, float v, bool equal) {
-    W n = all(0.0f);
-    if (equal) {
+  // elements above v
+  static __device__ __forceinline__ W count(const uint4& x, float v) {
+    W n = __hgt2(word(x, 0), all(v));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n = __hadd2(n, __hge2(word(x, i), all(v)));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) n = __hadd2(n, __hgt2(word(x, i), all(v)));
-    }
+    for (int i = 1; i < 4; ++i) n = __hadd2(n, __hgt2(word(x, i), all(v)));
     return n;
+  }
+  // the next value of the type below a value v of it
+  static __device__ __forceinline__ float before(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return v == 0.0f ? __uint_as_float(0x80010000u) : __uint_as_float(v > 0.0f ? u - 0x10000u : u + 0x10000u);
   }
   static __device__ __forceinline__ W add(W a, W b) { return __hadd2(a, b); }   // counts to 256 are exact
   static __device__ __forceinline__ float sum(W a) { return __low2float(a) + __high2float(a); }
@@ -162,12 +162,13 @@ template <> struct Vec<float> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = fmaxf(word(x, i), least);
   }
-  static __device__ __forceinline__ W count(const uint4& x, float v, bool equal) {
+  static __device__ __forceinline__ W count(const uint4& x, float v) {
     W n = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n += (equal ? word(x, i) >= v : word(x, i) > v) ? 1.0f : 0.0f;
+    for (int i = 0; i < 4; ++i) n += word(x, i) > v ? 1.0f : 0.0f;
     return n;
   }
+  static __device__ __forceinline__ float before(float v) { return nextafterf(v, -INFINITY); }
   static __device__ __forceinline__ W add(W a, W b) { return a + b; }
   static __device__ __forceinline__ float sum(W a) { return a; }
 };
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   const uint4* body = (const uint4*)(l + head);
 
   typedef Vec<T> Vt;
+  const float below = low_id ? INFINITY : Vt::before(raw_mine);   // what an id before x is above if it is ahead
   Stat st = {-FLT_MAX, 0.0f, 0.0f, 0};
   // Of this thread's sums: above `limit` the base has to follow, what is not above `least` adds nothing.
   float peak = -FLT_MAX, limit = -INFINITY, least = -INFINITY, ahead_of = 0.0f;
@@ -360,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
       typename Vt::W n;
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
-        const bool before = id_of(u) + E <= x;
-        const typename Vt::W k = Vt::count(now[u], before && low_id ? INFINITY : raw_mine, before && !low_id);
+        const typename Vt::W k = Vt::count(now[u], id_of(u) + E <= x ? below : raw_mine);
         n = u == 0 ? k : Vt::add(n, k);
       }
       ahead_of += Vt::sum(n);
