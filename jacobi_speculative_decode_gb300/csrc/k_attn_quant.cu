@@ -284,16 +284,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     return true;
   };
 
-  // The loads of a step.  A lane asks for the page of the key that it is for a step ahead, and looks at the
-  // answer when the loads are made.
+  // The loads of a step.  A lane asks for the page of its key (where 16 tokens lie side by side: of the first key
+  // of its half of the step) a step ahead, and looks at the answer when the loads are made.
   char* ring = smem + warp * (C::STAGES * C::STAGE);
   const uint32_t ring_at = ptx::smem_u32(ring);
-  int key = k0 + warp * kStep + lane, col = key / g.page_size, at_page = key - col * g.page_size;
-  int page = 0, in_page = 0;
-  bool key_in = false;
+  const int64_t head_at = hk * g.kv_head;
+  const int in_run = z.runs ? lane & 15 : 0;
+  int key = k0 + warp * kStep + lane - in_run, col = key / g.page_size, at_page = key - col * g.page_size;
+  int page = 0, in_page = 0, left = 0;   // left: keys of the range from there on
   auto find = [&]() {   // the next step's
-    key_in = key < k1;
-    if (key_in) page = table[col];
+    left = k1 - key;
+    if (left > 0) page = table[col];
     in_page = at_page;
     key += kRound;
     col += more;
@@ -302,19 +303,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
   };
   auto load = [&](int stage) {
     const uint32_t to = ring_at + stage * C::STAGE;
-    const uint32_t in = __ballot_sync(kAll, key_in);
-    if (key_in && (page < 0 || page >= g.pages)) {
+    if (left > 0 && (page < 0 || page >= g.pages)) {
       atomicOr(g.err, XP_ERR_BADPAGE);
       page = page < 0 ? 0 : g.pages - 1;
     }
-    const int64_t key_at = page * g.kv_page + hk * g.kv_head + (int64_t)in_page * z.code;   // its codes,
-    const int scale_at = z.scale_at + in_page * (z.scale - z.code);                        // its scales from there
+    const int64_t page_at = page * g.kv_page + head_at, code_at = page_at + (int64_t)in_page * z.code;
     auto codes = [&](auto piece_bytes) {
       constexpr int PB = decltype(piece_bytes)::value, PIECES = C::CODE / PB;   // of a token
+      const uint32_t in = __ballot_sync(kAll, left > 0);
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         const int piece = i * 32 + lane, of = piece / PIECES, p = piece % PIECES;
-        const int64_t from = __shfl_sync(kAll, key_at, of) + p * PB;
+        const int64_t from = __shfl_sync(kAll, code_at, of) + p * PB;
         if ((in >> of & 1) && p * PB < z.code) {
           const uint32_t d = to + of * C::CODE + p * PB;
           copy_async(d, (const char*)g.k + from, PB);
@@ -322,27 +322,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
         }
       }
     };
-    if (z.runs) {   // half a step at a time, a lane 16 bytes
-      constexpr int PIECES = C::CODE / 32;
-      const uint32_t d = to + lane * 16;
+    if (z.runs) {   // half a warp copies its half's 16 tokens, a lane 16 bytes
+      const uint32_t d = to + (lane & 16) * C::CODE + in_run * 16;
+      const char *k = (const char*)g.k + code_at + in_run * 16, *v = (const char*)g.v + code_at + in_run * 16;
+      if (left > 0) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int64_t from = __shfl_sync(kAll, key_at, half * 16) + lane * 16;
-        if (in >> half * 16 & 1) {
-#pragma unroll
-          for (int i = 0; i < PIECES; ++i) {
-            const int at = half * 16 * C::CODE + i * 512;
-            copy_async(d + at, (const char*)g.k + from + i * 512, 16);
-            copy_async(d + at + kStep * C::CODE, (const char*)g.v + from + i * 512, 16);
-          }
+        for (int i = 0; i < C::CODE / 16; ++i) {
+          copy_async(d + i * 256, k + i * 256, 16);
+          copy_async(d + kStep * C::CODE + i * 256, v + i * 256, 16);
         }
       }
     } else if (z.code % 16 == 0) codes(std::integral_constant<int, 16>());
     else codes(std::integral_constant<int, 8>());
     // a key behind the end: scales of 0, so that whatever codes the ring holds there are worth nothing
     const uint32_t d = to + 2 * kStep * C::CODE + lane * C::SCALE, dv = d + kStep * C::SCALE;
-    if (key_in) {
-      const char *k = (const char*)g.k + key_at + scale_at, *v = (const char*)g.v + key_at + scale_at;
+    if (left > in_run) {
+      const int64_t scale_at = page_at + z.scale_at + (in_page + in_run) * z.scale;
+      const char *k = (const char*)g.k + scale_at, *v = (const char*)g.v + scale_at;
       if (C::SCALE >= 8 && z.scale % 8 == 0) {
 #pragma unroll
         for (int p = 0; p < C::SCALE; p += 8)
