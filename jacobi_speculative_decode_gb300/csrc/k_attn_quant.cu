@@ -48,7 +48,8 @@ constexpr int kMinChunk = 2;          // least work of a CTA, in rounds
 struct Quant {
   int code, scale, scale_at;   // bytes of a token's codes and scales; where a head's scales begin
   bool q_wide;                 // queries by 16 bytes
-  bool runs;                   // 16 tokens from a multiple of 16 on lie side by side, as in the ring
+  // 16 tokens from a multiple of 16 on lie side by side, as in the ring, and pages less than 2^32 bytes apart
+  bool runs;
 };
 
 // The work is one line of cost: the prefix's units (kv head by kv head, row tile by row tile), then those
@@ -301,65 +302,70 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     at_page += rest;
     if (at_page >= g.page_size) at_page -= g.page_size, ++col;
   };
+  const char *k_head = (const char*)g.k + head_at, *v_head = (const char*)g.v + head_at;
   auto load = [&](int stage) {
     const uint32_t to = ring_at + stage * C::STAGE;
-    if (left > 0 && (page < 0 || page >= g.pages)) {
+    if (left > 0 && (unsigned)page >= (unsigned)g.pages) {
       atomicOr(g.err, XP_ERR_BADPAGE);
       page = page < 0 ? 0 : g.pages - 1;
     }
-    const int64_t page_at = page * g.kv_page + head_at, code_at = page_at + (int64_t)in_page * z.code;
+    // a key behind the end: scales of 0, so that whatever codes the ring holds there are worth nothing
+    const uint32_t ds = to + 2 * kStep * C::CODE + lane * C::SCALE;
+    auto no_scale = [&]() {
+#pragma unroll
+      for (int p = 0; p < C::SCALE; p += 4) {
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ds + p), "r"(0) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ds + kStep * C::SCALE + p), "r"(0) : "memory");
+      }
+    };
+    if (z.runs) {   // half a warp copies its half's 16 tokens, a lane 16 bytes
+      const uint64_t page_at = (uint64_t)(unsigned)page * (unsigned)g.kv_page;
+      const unsigned code_at = in_page * C::CODE + in_run * 16;
+      const unsigned scale_at = z.scale_at + (in_page + in_run) * C::SCALE;
+      const char *k = k_head + page_at, *v = v_head + page_at;
+      if (left > 0) {
+        const uint32_t d = to + (lane & 16) * C::CODE + in_run * 16;
+#pragma unroll
+        for (int i = 0; i < C::CODE / 16; ++i) {
+          copy_async(d + i * 256, k + code_at + i * 256, 16);
+          copy_async(d + kStep * C::CODE + i * 256, v + code_at + i * 256, 16);
+        }
+      }
+      if (left > in_run) {
+        copy_async(ds, k + scale_at, C::SCALE);
+        copy_async(ds + kStep * C::SCALE, v + scale_at, C::SCALE);
+      } else {
+        no_scale();
+      }
+      return;
+    }
+    const int64_t page_at = page * g.kv_page, code_at = page_at + (int64_t)in_page * z.code;
+    const uint32_t in = __ballot_sync(kAll, left > 0);
     auto codes = [&](auto piece_bytes) {
       constexpr int PB = decltype(piece_bytes)::value, PIECES = C::CODE / PB;   // of a token
-      const uint32_t in = __ballot_sync(kAll, left > 0);
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         const int piece = i * 32 + lane, of = piece / PIECES, p = piece % PIECES;
         const int64_t from = __shfl_sync(kAll, code_at, of) + p * PB;
         if ((in >> of & 1) && p * PB < z.code) {
           const uint32_t d = to + of * C::CODE + p * PB;
-          copy_async(d, (const char*)g.k + from, PB);
-          copy_async(d + kStep * C::CODE, (const char*)g.v + from, PB);
+          copy_async(d, k_head + from, PB);
+          copy_async(d + kStep * C::CODE, v_head + from, PB);
         }
       }
     };
-    if (z.runs) {   // half a warp copies its half's 16 tokens, a lane 16 bytes
-      const uint32_t d = to + (lane & 16) * C::CODE + in_run * 16;
-      const char *k = (const char*)g.k + code_at + in_run * 16, *v = (const char*)g.v + code_at + in_run * 16;
-      if (left > 0) {
-#pragma unroll
-        for (int i = 0; i < C::CODE / 16; ++i) {
-          copy_async(d + i * 256, k + i * 256, 16);
-          copy_async(d + kStep * C::CODE + i * 256, v + i * 256, 16);
-        }
-      }
-    } else if (z.code % 16 == 0) codes(std::integral_constant<int, 16>());
+    if (z.code % 16 == 0) codes(std::integral_constant<int, 16>());
     else codes(std::integral_constant<int, 8>());
-    // a key behind the end: scales of 0, so that whatever codes the ring holds there are worth nothing
-    const uint32_t d = to + 2 * kStep * C::CODE + lane * C::SCALE, dv = d + kStep * C::SCALE;
-    if (left > in_run) {
-      const int64_t scale_at = page_at + z.scale_at + (in_page + in_run) * z.scale;
-      const char *k = (const char*)g.k + scale_at, *v = (const char*)g.v + scale_at;
-      if (C::SCALE >= 8 && z.scale % 8 == 0) {
+    if (left > 0) {
+      const int64_t scale_at = page_at + z.scale_at + (int64_t)in_page * z.scale;
 #pragma unroll
-        for (int p = 0; p < C::SCALE; p += 8)
-          if (p < z.scale) {
-            copy_async(d + p, k + p, 8);
-            copy_async(dv + p, v + p, 8);
-          }
-      } else {
-#pragma unroll
-        for (int p = 0; p < C::SCALE; p += 4)
-          if (p < z.scale) {
-            copy_async(d + p, k + p, 4);
-            copy_async(dv + p, v + p, 4);
-          }
-      }
+      for (int p = 0; p < C::SCALE; p += 4)
+        if (p < z.scale) {
+          copy_async(ds + p, k_head + scale_at + p, 4);
+          copy_async(ds + kStep * C::SCALE + p, v_head + scale_at + p, 4);
+        }
     } else {
-#pragma unroll
-      for (int p = 0; p < C::SCALE; p += 4) {
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(d + p), "r"(0) : "memory");
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dv + p), "r"(0) : "memory");
-      }
+      no_scale();
     }
   };
   const int steps = k1 > k0 ? (k1 - k0 + kStep - 1) / kStep : 0;
@@ -992,7 +998,8 @@ cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaS
                           (g.a.heads > 1 ? g.a.q_stride_h : 0);
   const int D = c->d.head_dim;
   const Quant z = {size.code, size.scale, c->d.page_size * size.code, (uintptr_t)g.q % 16 == 0 && strides % 8 == 0,
-                   c->d.page_size % 16 == 0 && (D == 64 || D == 128 || D == 256)};
+                   c->d.page_size % 16 == 0 && (D == 64 || D == 128 || D == 256) &&
+                       c->d.stride_page <= UINT_MAX};
   const cudaError_t e = c->d.dtype == XP_Q8 ? launch_dims<8>(q, z, c->num_sms, s) : launch_dims<4>(q, z, c->num_sms, s);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
