@@ -725,14 +725,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
 // L lanes a query row (32, or 16 for heads to 64): what tcgen05 left of its prefix, and the pieces of its prefix and of its tail (the
 // unit's own and those of the CTAs at whose beginning it was cut), brought to a common maximum:
 //   out = sum_p a_p O_p / sum_p a_p l_p,  a_p = 2^(m_p - m).
-// A lane holds E dims.  Bound by the latency of what it asks for, so four pieces are asked for at once.
-template <int E, int L>
+// A lane holds E dims.  Bound by the latency of what it asks for, so four pieces are asked for at once, and where
+// there are few rows, which have many pieces, W warps share a row's.
+template <int E, int L, int W>
 __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_constant__ xp_attn_args g) {
   ptx::pdl_wait();
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / (L * W);
   if (row >= rows) return;
-  const int lane = threadIdx.x % L, D = g.dim, RT = g.plan.rows_tile, per_seq = g.a.T * g.group;
+  const int lane = threadIdx.x % L, warp = W == 1 ? 0 : threadIdx.x / L, D = g.dim, RT = g.plan.rows_tile, per_seq = g.a.T * g.group;
   const int h = (int)(row % g.a.heads), t = (int)(row / g.a.heads % g.a.T);
   const int n = (int)(row / g.a.heads / g.a.T), hk = h / g.group, i = t * g.group + h % g.group;
   const int64_t* line = (const int64_t*)g.line;
@@ -760,8 +761,8 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
   auto pieces = [&](int keys, int64_t at, int64_t unit, int r) {
     const int T = rounds_of(keys), cost = cost_of(keys);
     const int64_t c0 = at / chunk, c1 = (at + cost - 1) / chunk;
-    for (int64_t first = c0; first <= c1; first += L) {   // a lane a CTA
-      const int64_t c = first + lane;
+    for (int64_t first = c0 + warp; first <= c1; first += L * W) {   // a lane a CTA
+      const int64_t c = first + lane * W;
       int64_t from = 0;
       float2 st = make_float2(0.0f, 0.0f);   // of no piece, and where no key was visible: acc may hold anything
       if (c <= c1) {
@@ -771,7 +772,7 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
           st = __ldcg((const float2*)g.stat + from);
         }
       }
-      const int count = (int)min((int64_t)L, c1 - first + 1);
+      const int count = (int)min((int64_t)L, (c1 - first) / W + 1);
       for (int k = 0; k < count; k += 4) {
         float2 s[4];
         float x[4][E];
@@ -788,7 +789,7 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
       }
     }
   };
-  if (g.part_stat) {
+  if (g.part_stat && warp == 0) {
     const float2 st = __ldcg((const float2*)g.part_stat + row);
     float x[E];
     if (dims) load(g.part_acc + row * D, x);
@@ -803,6 +804,21 @@ __global__ void __launch_bounds__(256) attn_quant_combine_kernel(const __grid_co
     const int keys = tail_len(g, n, false), u = hk * g.plan.tail_tiles + i / RT;
     if (keys > 0)
       pieces(keys, begin + (int64_t)u * cost_of(keys), units + (int64_t)n * g.kv_heads * g.plan.tail_tiles + u, i % RT);
+  }
+  if constexpr (W > 1) {   // the warps', in the first
+    __shared__ float2 s_st[W];
+    __shared__ float s_o[W][E][L];
+    if (lane == 0) s_st[warp] = make_float2(m, l);
+#pragma unroll
+    for (int c = 0; c < E; ++c) s_o[warp][c][lane] = o[c];
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < W; ++w) {
+      float x[E];
+#pragma unroll
+      for (int c = 0; c < E; ++c) x[c] = s_o[w][c][lane];
+      if (s_st[w].y != 0.0f) add(s_st[w], x);
+    }
   }
   const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // NaN where a visible score is
   bf16* out = (bf16*)g.out + n * g.a.o_stride_n + t * g.a.o_stride_t + h * g.a.o_stride_h + lane * E;
@@ -856,7 +872,8 @@ template <int BITS> cudaError_t launch_dims(const xp_attn_args& g, const Quant& 
 // what they see is widened to fp16 in the workspace once (exactly, as here) and attended over on tcgen05.
 // 32 sequences of 1, 2, 4 tokens behind 8192, 8 kv heads of 4 x 128 in 4 bits: 64 rows 65 us widened and 46 not,
 // 128 rows 66 and 61, 256 rows 62 and 93.  32 tails of 17 to 1500 tokens, rows of one: 16 take 65 and 41, 32 take
-// 69 and 69, 64 take 73 and 108.
+// 69 and 69, 64 take 73 and 108.  Tails beside a widened prefix, which spare a kernel and a second joining: 32
+// rows 89 and 119 us, 16 rows 80 and 81 (128 sequences: 223 and 173), 8 rows 117 and 79.
 constexpr int kWidePrefixRows = 256, kWideTailRows = 64;
 constexpr size_t kWideTailBytes = (size_t)1 << 30;   // of tails that may be widened
 
@@ -899,7 +916,7 @@ xp_attn_plan xp_attn_quant_plan(const xp_cache* c, const xp_attn* a) {
   // their own and a second joining take 20 us.
   const size_t tail_pages = (size_t)a->N * pages(a->max_len);
   const bool tails = c->attn_tc && a->max_len > 0 && tail_pages * page_bytes <= kWideTailBytes &&
-                     ((per_seq >= kWideTailRows && (prefix || a->prefix_len == 0)) ||
+                     ((per_seq >= (prefix ? kWideTailRows / 2 : kWideTailRows) && (prefix || a->prefix_len == 0)) ||
                       (prefix && tail_pages <= 2 * (size_t)pages(a->prefix_len)));
   if (prefix || tails) {
     p.wide_prefix = prefix ? pages(a->prefix_len) : 0;
@@ -1003,8 +1020,11 @@ cudaError_t xp_launch_attn_quant(const xp_cache* c, const xp_attn_args& g, cudaS
   const cudaError_t e = c->d.dtype == XP_Q8 ? launch_dims<8>(q, z, c->num_sms, s) : launch_dims<4>(q, z, c->num_sms, s);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
-  return xp_launch_pdl(D <= 64    ? attn_quant_combine_kernel<4, 16>
-                       : D <= 128 ? attn_quant_combine_kernel<4, 32>
-                                  : attn_quant_combine_kernel<8, 32>,
+  if (rows <= c->num_sms * 4)
+    return xp_launch_pdl(D <= 128 ? attn_quant_combine_kernel<4, 32, 8> : attn_quant_combine_kernel<8, 32, 8>,
+                         dim3((unsigned)rows), dim3(256), 0, s, q);
+  return xp_launch_pdl(D <= 64    ? attn_quant_combine_kernel<4, 16, 1>
+                       : D <= 128 ? attn_quant_combine_kernel<4, 32, 1>
+                                  : attn_quant_combine_kernel<8, 32, 1>,
                        dim3((unsigned)((rows * (D <= 64 ? 16 : 32) + 255) / 256)), dim3(256), 0, s, q);
 }
