@@ -119,6 +119,14 @@ CASES = [  # N, T, kv heads, group, dim, page, prefix, lens
     (6, 1, 2, 4, 128, 16, 700, [0] * 6),
     (1, 40, 2, 4, 64, 16, 0, [40]),
     (2, 1, 1, 4, 128, 64, 0, [5000, 4000]),
+    # work enough for tiles of 16 and of 32 queries
+    (64, 4, 4, 4, 128, 16, 0, [130 + i for i in range(64)]),
+    (64, 4, 4, 4, 64, 20, 0, [130 + 2 * i for i in range(64)]),
+    (64, 3, 4, 3, 256, 16, 0, [130 + i for i in range(64)]),
+    (40, 6, 4, 4, 128, 16, 0, [260 + 2 * i for i in range(40)]),
+    (40, 6, 4, 4, 96, 7, 0, [260 + 2 * i for i in range(40)]),
+    (40, 6, 4, 4, 64, 32, 0, [260 + 2 * i for i in range(40)]),
+    (8, 6, 4, 4, 128, 16, 3000, [20 + 9 * i for i in range(8)]),
     # more sequences than a CTA has threads; one that every CTA has a piece of
     (300, 1, 1, 2, 64, 8, 0, [i % 41 for i in range(300)]),
     (1, 1, 1, 4, 64, 64, 0, [30000]),
