@@ -29,9 +29,11 @@ struct RowArgs {
   uint32_t* err;
 };
 
-// Where the CTA's tokens lie: page id (-1: nowhere) and place in the page.  `len`: the sequence's end.
+// Where the CTA's tokens lie: their page's beginning (-1: nowhere) and place in the page.  `len`: the
+// sequence's end.
 struct Places {
-  int page[kTokens], at[kTokens];
+  int64_t page[kTokens];
+  int at[kTokens];
 };
 __device__ __forceinline__ void find_pages(const RowArgs& a, int n, int t0, int64_t pos0, int64_t len,
                                            Places* s) {
@@ -52,7 +54,7 @@ __device__ __forceinline__ void find_pages(const RowArgs& a, int n, int t0, int6
         }
       }
     }
-    s->page[threadIdx.x] = page;
+    s->page[threadIdx.x] = page < 0 ? -1 : page * a.page;
     s->at[threadIdx.x] = at;
   }
   __syncthreads();
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_quant_kernel(const RowArgs
     const int g = part.e / 16;
     for (int i0 = part.lane; i0 < kTokens; i0 += kAppendBatch * part.lanes) {
       Eight<T> raw[kAppendBatch];
-      int page[kAppendBatch];
+      int64_t page[kAppendBatch];
 #pragma unroll
       for (int k = 0; k < kAppendBatch; ++k) {
         const int i = i0 + k * part.lanes;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_quant_kernel(const RowArgs
           for (int j = 0; j < 8; ++j) x[j] = fminf(fmaxf(x[j], -most), most);
           atomicOr(a.err, XP_ERR_RANGE);
         }
-        char* head = pool + page[k] * a.page;
+        char* head = pool + page[k];
         char* scale = head + a.scale_at + at * a.scale;
         if (part.e % 16 == 0) scale[g] = (char)b;
         if (part.e + 8 == a.D)   // the padding behind the scales
@@ -227,6 +229,19 @@ __device__ __forceinline__ void widen(uint2 w, unsigned scale, __half2 (&out)[N]
   }
 }
 
+// 8 codes of 4 bits as bf16: 128 + c is a bf16 number with c in its last bits
+__device__ __forceinline__ uint4 widen_bf16(uint32_t w, unsigned scale) {
+  const __nv_bfloat162 s = __float2bfloat162_rn(xpq::scale_of(scale)), zero = __float2bfloat162_rn(-136.0f);
+  uint32_t out[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t pair = (w >> 4 * j & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hmul2(__hadd2(*(const __nv_bfloat162*)&pair, zero), s);
+    out[j] = *(const uint32_t*)&v;
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wide) {
   constexpr int E = Piece<T>::N;
@@ -240,17 +255,19 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
     const int e = part.e, live = min(E, a.D - e);
     T* to = (T*)(part.is_v ? a.v : a.k) + n * a.sn + t0 * a.st + part.h * a.sh + e;
     const char* pool = part.is_v ? a.vp : a.kp;
+    if (BITS <= 8) pool += part.h * a.head;
     for (int i0 = part.lane; i0 < count; i0 += kReadBatch * part.lanes) {
       if constexpr (BITS <= 8) {
         uint2 code[kReadBatch];
         unsigned scale[kReadBatch];
 #pragma unroll
         for (int k = 0; k < kReadBatch; ++k) {
-          const int i = i0 + k * part.lanes, page = i < count ? s.page[i] : -1;
+          const int i = i0 + k * part.lanes;
+          const int64_t page = i < count ? s.page[i] : -1;
           code[k] = make_uint2(0, 0);
           scale[k] = 0;   // what lies nowhere reads as 0
           if (page >= 0) {
-            const char* head = pool + page * a.page + part.h * a.head;
+            const char* head = pool + page;
             scale[k] = (uint8_t)head[a.scale_at + s.at[i] * a.scale + e / 16];
             const char* from = head + s.at[i] * a.token + e / 8 * BITS;
             if constexpr (BITS == 4) code[k].x = *(const uint32_t*)from >> e % 8 * 2;   // fp32: the first four or the last
@@ -261,6 +278,12 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
 #pragma unroll
         for (int k = 0; k < kReadBatch; ++k) {
           if (i0 + k * part.lanes >= count) break;
+          if constexpr (BITS == 4 && E == 8) {   // c s is exact in bf16 too: no way by fp32
+            if (wide) {
+              __stcs((uint4*)(to + (i0 + k * part.lanes) * a.st), widen_bf16(code[k].x, scale[k]));
+              continue;
+            }
+          }
           __half2 v[E / 2];
           widen<BITS>(code[k], scale[k], v);
           float x[E];
@@ -278,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
           if (i >= count) break;
           float x[E] = {};
           if (s.page[i] >= 0) {
-            const int64_t at = s.page[i] * a.page + s.at[i] * a.token + part.h * a.head + e;
+            const int64_t at = s.page[i] + s.at[i] * a.token + part.h * a.head + e;
 #pragma unroll
             for (int j = 0; j < E; ++j)
               if (j < live) x[j] = BITS == 16 ? to_f(((const bf16*)pool)[at + j]) : ((const float*)pool)[at + j];
