@@ -6,6 +6,9 @@
 //   log p(x) = (l_x - m) / t - log S,   H = log S - log(2) W / S.
 // Differences are taken before they are scaled, so that neither large logits nor small temperatures lose
 // digits.
+// Bound by the row's bytes in fp32: 2048 rows of 151647, 1.24 GB, 196 us, 6.3 TB/s, 93% of measured.  In bf16 by
+// instructions: 2048 rows of 151647, 621 MB, 116 us, 79%.  One CTA
+// a row leaves few rows to as many CTAs: 410 rows (125 MB) with 20 alternatives 49 us, with none 39.
 // The best ids.  On the way a thread only writes down the greatest of every 16 bytes' batch.  The `top`-th of the
 // 256 threads' greatest is a bound: there are `top` elements that are not below it, and few that are above.
 // The batches that reach it are read again (from L2, some 25 of a row's), their elements that do go to a buffer,
@@ -137,7 +140,7 @@ template <> struct Vec<bf16> {
     for (int i = 1; i < 4; ++i) n = __hadd2(n, __hgt2(word(x, i), all(v)));
     return n;
   }
-  // the next value of the type below a value v of it
+  // the greatest value of the type that reads less than v does
   static __device__ __forceinline__ float before(float v) {
     const uint32_t u = __float_as_uint(v);
     return v == 0.0f ? __uint_as_float(0x80010000u) : __uint_as_float(v > 0.0f ? u - 0x10000u : u + 0x10000u);
@@ -168,7 +171,7 @@ template <> struct Vec<float> {
     for (int i = 0; i < 4; ++i) n += word(x, i) > v ? 1.0f : 0.0f;
     return n;
   }
-  static __device__ __forceinline__ float before(float v) { return nextafterf(v, -INFINITY); }
+  static __device__ __forceinline__ float before(float v) { return nextafterf(fminf(v, FLT_MAX), -INFINITY); }
   static __device__ __forceinline__ W add(W a, W b) { return a + b; }
   static __device__ __forceinline__ float sum(W a) { return a; }
 };
@@ -242,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   const uint4* body = (const uint4*)(l + head);
 
   typedef Vec<T> Vt;
-  const float below = low_id ? INFINITY : Vt::before(raw_mine);   // what an id before x is above if it is ahead
+  // what an id before x is above if it is ahead, and one behind
+  const float below = low_id ? INFINITY : Vt::before(raw_mine), above = mine < FLT_MAX ? raw_mine : INFINITY;
   Stat st = {-FLT_MAX, 0.0f, 0.0f, 0};
   // Of this thread's sums: above `limit` the base has to follow, what is not above `least` adds nothing.
   float peak = -FLT_MAX, limit = -INFINITY, least = -INFINITY, ahead_of = 0.0f;
@@ -282,11 +286,11 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   auto ends = [&](int from, int to) {
     const int id = from + lane;
     if (id >= to) return;
-    const float raw = fmaxf(to_f(l[id]), -INFINITY), v = fminf(raw, FLT_MAX);
+    const float v = read_logit(l[id]);
     peak = fmaxf(peak, v);
     if (v > limit) follow(v);
     add_one(v);
-    ahead_of += (low_id ? raw > raw_mine && id > x : raw > raw_mine || (raw == raw_mine && id < x)) ? 1.0f : 0.0f;
+    ahead_of += (low_id ? v > mine && id > x : v > mine || (v == mine && id < x)) ? 1.0f : 0.0f;
     if (TOP) push(v, id);
   };
   // one id a lane into the warp's sorted list; *own: its last entry of `top`
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
       typename Vt::W n;
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
-        const typename Vt::W k = Vt::count(now[u], id_of(u) + E <= x ? below : raw_mine);
+        const typename Vt::W k = Vt::count(now[u], id_of(u) + E <= x ? below : above);
         n = u == 0 ? k : Vt::add(n, k);
       }
       ahead_of += Vt::sum(n);
@@ -431,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   if (own_vector >= v0 && own_vector < v1) {
     const int from = head + own_vector * E;
     if (warp == 0 && from + lane < x) {
-      const float v = fmaxf(to_f(l[from + lane]), -INFINITY);
-      ahead_of += low_id ? (v > mine ? -1.0f : 0.0f) : v == raw_mine ? 1.0f : 0.0f;
+      const float v = read_logit(l[from + lane]);
+      ahead_of += low_id ? (v > mine ? -1.0f : 0.0f) : v == mine ? 1.0f : 0.0f;
     }
   }
   st.ahead = (int)ahead_of;

@@ -214,3 +214,18 @@ def test_a_stream_and_a_graph():
         torch.cuda.synchronize()
         want = call(head, rows, tokens, None, 5)
         assert all(torch.equal(a, b) for a, b in zip(out, want.values()))
+
+
+@pytest.mark.parametrize("shift", [0, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_infinity_beside_the_largest_finite_value(dtype, shift):
+    """+inf reads as fp32's largest value: in fp32 rows the two are a tie, whichever comes first."""
+    V = 4100
+    wide = torch.zeros(4, 1, V + 3, device="cuda", dtype=dtype)
+    rows, most = wide[:, :, shift:shift + V], torch.finfo(dtype).max
+    rows[0, 0, [1, 40, 2050, 4099]] = torch.tensor([most, math.inf, most, math.inf], device="cuda", dtype=dtype)
+    rows[1, 0, [0, 41, 2051, 4098]] = torch.tensor([math.inf, most, math.inf, most], device="cuda", dtype=dtype)
+    rows[2, 0, 2048:2056] = torch.tensor([most, math.inf] * 4, device="cuda", dtype=dtype)
+    rows[3, 0, 2048:2056] = torch.tensor([math.inf, most] * 4, device="cuda", dtype=dtype)
+    for token in (0, 1, 40, 41, 2050, 2051, 2053, 2054, 4098, 4099):
+        check(make_head(V), rows, torch.full((4, 1), token, device="cuda"), None, 9)
