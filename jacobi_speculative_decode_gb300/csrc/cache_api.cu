@@ -140,6 +140,7 @@ xp_status append(const xp_cache* c, int layer, const void* k, const void* v, int
     return XP_EINVAL;
   if (N == 0) return XP_OK;   // an empty batch needs no pointers, here and in the calls below
   if (!k || !v || !table || !lens) return XP_EINVAL;
+  if (quant && ((uintptr_t)k | (uintptr_t)v) % xp_elem(dtype)) return XP_EINVAL;
   if (quant)
     return cuda_status(xp_launch_append_quant(c, layer, k, v, stride_n, stride_t, stride_h, dtype, table,
                                               ld_table, width, lens, N, T, stream));
@@ -323,6 +324,7 @@ xp_status xp_prefix_attention(const xp_cache* c, const xp_attn* a, const void* q
   if (!valid_attn(c, a) || !on_device(c)) return XP_EINVAL;
   if (a->N == 0) return XP_OK;
   if (!q || !out || !ws || (uintptr_t)ws % 256) return XP_EINVAL;
+  if (xp_is_quant(c->d.dtype) && (((uintptr_t)q | (uintptr_t)out) % 2 || (uintptr_t)lse % 4)) return XP_EINVAL;
   const int ps = c->d.page_size;
   if (a->prefix_len > 0 && (!prefix_table || prefix_pages < (a->prefix_len - 1) / ps + 1))
     return XP_EINVAL;

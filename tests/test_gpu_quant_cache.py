@@ -256,3 +256,28 @@ def test_a_stream_and_a_graph():
         torch.cuda.synchronize()
         codes, byte, _ = Q.quantise(y.double().cpu().numpy(), 4)
         assert (ko.double().cpu().numpy() == Q.values(codes, byte)).all() and (ko == vo).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_off_their_types_boundary_are_refused(dtype):
+    c = make(8, 1, 2, 16, 1, 64, fill=0)
+    x = torch.ones(1, 3, 1, 64, device="cuda", dtype=dtype)
+    table, lens = cu([[0, 1]]), cu([3])
+    code = xp.XP_BF16 if dtype == torch.bfloat16 else xp.XP_F32
+    for dk, dv in ((1, 0), (0, 1)):
+        k, v = x.data_ptr() + dk, x.data_ptr() + dv
+        assert xp.lib().xp_cache_append(c.handle, 0, k, v, 192, 64, 64, 1, 64, code, table.data_ptr(), 2,
+                                        lens.data_ptr(), 1, 2, None) == xp.XP_EINVAL
+        assert xp.lib().xp_cache_read(c.handle, 0, table.data_ptr(), 2, 2, lens.data_ptr(), None, 1, 2, k, v, 192, 64,
+                                      64, 1, 64, code, None) == xp.XP_EINVAL
+    if dtype == torch.bfloat16:
+        q = torch.ones(1, 1, 1, 64, device="cuda", dtype=dtype)
+        a = xp.make_attn(q, q, 0, 0, 16, 0.1)
+        ws = c.attention_workspace(a)
+        for dq, do in ((1, 0), (0, 1)):
+            with pytest.raises(xp.XPError) as e:
+                xp._check("attention", xp.lib().xp_prefix_attention(
+                    c.handle, a, q.data_ptr() + dq, None, 0, table.data_ptr(), 2, 2, lens.data_ptr(),
+                    q.data_ptr() + do, None, ws.data_ptr(), ws.numel() * ws.element_size(), None))
+            assert e.value.code == xp.XP_EINVAL
+    assert int(c.k.max()) == 0
