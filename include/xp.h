@@ -500,7 +500,7 @@ xp_status xp_cache_resize(const xp_cache* cache, const int32_t* table, int64_t l
 
 /* M children: child i continues row parent[i] of a table of `rows` rows at length
  * min(lens[parent[i]], cut[i]) (cut may be NULL).  Its full pages are shared (refs + 1); of a
- * partly filled last page it gets a copy of its own, the tokens it holds only: the lowest
+ * partly filled last page it gets a copy of its own, the tokens it holds only (a quantised one whole): the lowest
  * free id, in child order.  Without one it ends at its last full page (XP_ENOPAGES).  A
  * parent outside [0, rows) gives an empty child (XP_ELENGTH).  child_table may be rows of the
  * same table, parents among them: all parents are read before any child is written (XP_EINVAL
@@ -540,7 +540,12 @@ xp_status xp_cache_compact(const xp_cache* cache, const int32_t* table, int64_t 
  * boundaries and strides that are multiples of 8, run on the tensor cores; all others run on CUDA
  * cores, at a small part of that rate (an fp32 cache keeps the weights in 32 bits).  On tensor cores
  * queries on 16-byte boundaries with one stride from token to token, across sequences too, are
- * loaded fastest: a slice of the last T tokens of longer rows costs half the call's time again. */
+ * loaded fastest: a slice of the last T tokens of longer rows costs half the call's time again.
+ * Quantised caches: q and out are bf16, any head_dim and page size, on tensor cores; values are those held,
+ * in 16-bit floats, and each weight is rounded to one of those.  Where many queries share a key (256 rows
+ * of N T heads/kv_heads for the prefix, 32 or 64 of T heads/kv_heads for tails; head_dim 64 or 128) keys and
+ * values are written out in 16 bits to the workspace, which is as much larger: 4 kv_heads head_dim bytes a
+ * token, for tails 1 GiB at most. */
 typedef struct {
   int layer, N, T, heads;
   int head_dim;      /* head_dim and dtype: those of q and out, which must be the cache's */

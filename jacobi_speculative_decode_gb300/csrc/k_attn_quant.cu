@@ -11,16 +11,25 @@
 // a lane takes the dims and keys whose codes lie side by side: 32 dims of a key for K^, 16 dims
 // of four keys for V^, each one or two vector loads from shared memory.
 //
+// What bounds it.  A warp's step of 32 keys of 128 dims in 4 bits is 4.6 KB, 206 cycles of an SM's share of HBM,
+// and 700 instructions, 175 cycles of its four issue slots; 290 of them, mostly what picks codes out of
+// words, are the logic pipe's, which takes one every other cycle.  16 single tokens, 32 heads of 128 over 8,
+// contexts of 1000 to 32768 (311 MB): 75 us, 4.1 TB/s, 61% of measured, and 9 for the joining; issue slots
+// are busy in 58% of the cycles, the logic pipe in 48%, the tensor pipe in 24%, with 14 of 16 warps an SM.
+// In 8 bits (589 MB) 125 us for both kernels, 69% of measured.  (Other numbers of CTAs an SM and of stages
+// gave nothing.)
+//
 // A value held is exact in fp16 (quant.cuh).  Queries are bf16, scaled by a power of two a row so that
-// their largest is in [1, 4): exact but for what lies 2^-14 and more below it, which loses less than 2^-25 of the
-// largest.  Weights are 2^(z - m + 6), rounded to fp16 (2^-12 of each, and 2^-31 of the largest where that
-// is more): as the second product's operand they have to be 16 bits, and fp16 leaves an eighth of
+// their largest is in [1, 4) (4 bits: 16 times that, and 1/16 in odd pairs): exact but for what lies 2^-14 and more
+// below it, which loses less than 2^-25 of the largest.  Weights are 2^(z - m + 6), rounded to fp16 (2^-12 of
+// each, and 2^-31 of the largest where that is more): as the second product's operand they have to be 16 bits, and fp16 leaves an eighth of
 // bf16's error.  Sums are taken before that rounding, in fp32, as are all statistics.
 //
-// A CTA is four warps on one unit: a row tile of 8 NQ queries of a kv head and a range of keys.  Every warp
+// Work is one line, cut into equal shares of as many CTAs as the GPU holds (plan_line).  A CTA is four warps on
+// one unit at a time: a row tile of 8 NQ queries of a kv head and a range of keys.  Every warp
 // takes every fourth step of 32 keys, through a ring of its own in shared memory (cp.async, no barrier
-// between warps), and the four results are joined at the end.  A unit's result goes to the workspace, and
-// attn_combine_kernel joins the units of a row; where a row has one unit it is written out at once.
+// between warps), and the four results are joined at the end.  Results go to the workspace, and
+// attn_quant_combine_kernel joins those of a row.
 #include <limits.h>
 
 #include <algorithm>

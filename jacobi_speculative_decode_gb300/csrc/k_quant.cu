@@ -1,8 +1,10 @@
 // Rows into a quantised cache, and rows of any cache back out.
 //
 // A CTA takes kTokens tokens of one sequence and finds their pages once; a thread is one piece of a token's
-// row (16 dims of K or V written, 16 bytes of them read) and walks over the tokens, so that nothing is divided
-// inside.  Both are bound by the bytes of the wide rows.
+// row (8 dims of K or V written, 16 bytes of them read) and walks over the tokens, so that nothing is divided
+// inside.  8 prompts of 4096 tokens, 8 heads of 128, fp32 in 8 bits: written in 68 us (340 MB, 4.9 TB/s, issue slots
+// busy in 64% of the cycles), read back in 61 (5.5 TB/s, 82% of measured); 32 sequences to 3000 tokens out of 4
+// bits as bf16 75 us, 6.0 TB/s, 88%.
 #include <algorithm>
 
 #include "quant.cuh"
@@ -100,7 +102,8 @@ __device__ __forceinline__ float reciprocal(float x) {   // nearly
   return r;
 }
 
-// tokens of a thread whose loads are on their way together (four to append leave two CTAs an SM: 140 us, not 133)
+// tokens of a thread whose loads are on their way together (four to append leave two CTAs an SM: 141 us for
+// both calls of the prompts, not 133)
 constexpr int kAppendBatch = 2, kReadBatch = 4;
 
 // What a thread does of a row: piece `e` of head `h` of K or V, for every lanes-th token from `lane` on.
@@ -123,7 +126,7 @@ template <typename F> __device__ __forceinline__ void for_parts(const RowArgs& a
 
 // ---------------------------------------------------------------------------
 // Quantised append.  A thread has 8 dims, and its neighbour the other 8 of their scale: with 4, as 16-byte loads
-// would have it of fp32, what a scale costs is too much (write prompts' append 102 us and not 80).
+// would have it of fp32, what a scale costs is too much (the prompts above took 102 us and not 80).
 // ---------------------------------------------------------------------------
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kThreads, 4) append_quant_kernel(const RowArgs a, bool wide) {
