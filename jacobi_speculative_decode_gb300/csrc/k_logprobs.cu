@@ -8,7 +8,7 @@
 // digits.
 // Bound by the row's bytes in fp32: 2048 rows of 151647, 1.24 GB, 196 us, 6.3 TB/s, 93% of measured.  In bf16 by
 // instructions: 2048 rows of 151647, 621 MB, 116 us, 79%.  One CTA
-// a row leaves few rows to as many CTAs: 410 rows (125 MB) with 20 alternatives 49 us, with none 39.
+// a row leaves few rows to as many CTAs: 410 rows (125 MB) with 20 alternatives 42 us, with none 31.
 // The best ids.  On the way a thread only writes down the greatest of every 16 bytes' batch.  The `top`-th of the
 // 256 threads' greatest is a bound: there are `top` elements that are not below it, and few that are above.
 // The batches that reach it are read again (from L2, some 25 of a row's), their elements that do go to a buffer,
@@ -32,9 +32,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLoads = 4;             // 16-byte vectors of a thread in flight
 constexpr int kResident = 4;          // CTAs an SM
-constexpr int kMostParts = 4;         // parts of cut rows, all together, per CTA that runs at once
-constexpr float kPartCost = 0.03f;    // what a part costs besides its elements, in rows of a usual vocabulary
+constexpr int kMostParts = 10;        // of a row
 constexpr int kCand = 1024;           // places of the buffer
+static_assert(kMostParts * 32 <= kCand, "the parts of a row leave what the buffer holds");
 constexpr int kBatches = 64;          // of which the greatest is held; all behind them share the last place
 constexpr int kLeastVectors = kThreads * kLoads;   // of a part of a row
 constexpr float kLazy = 8.0f;         // how far (base 2) a logit may lie above the base of its thread's sums
@@ -46,7 +46,7 @@ struct Args {
   int64_t sn, sb;
   const int64_t* tokens;
   const float* temperature;
-  int B, V, top, parts;
+  int B, V, top, parts, rows;   // rows: 0 where there are more than CTAs at once
   float *logprob, *entropy;
   int32_t* rank;
   int64_t* top_ids;
@@ -201,6 +201,33 @@ __device__ __forceinline__ float kth_of(const float* v, int k, int lane) {
   return fmaxf(key2f(low), -FLT_MAX);
 }
 
+// The i-th row in an order that has those with a token first: where all CTAs run at once, SMs get as many of them
+// each, but for one.
+__device__ __forceinline__ void in_order(const Args& a, int i, int lane, int warp, int* row) {
+  __shared__ int s_live[kWarps];
+  const int per = (a.rows + kThreads - 1) / kThreads, r0 = min(a.rows, (int)threadIdx.x * per), r1 = min(a.rows, r0 + per);
+  auto has = [&](int r) { return a.tokens[r] >= 0 && a.tokens[r] < a.V; };
+  int mine = 0;
+  for (int r = r0; r < r1; ++r) mine += has(r);
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(kAll, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) s_live[warp] = inc;
+  __syncthreads();
+  int live = inc - mine, all = 0;   // before this thread's, and all
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    live += w < warp ? s_live[w] : 0;
+    all += s_live[w];
+  }
+  int none = all + r0 - live;
+  for (int r = r0; r < r1; ++r)
+    if ((has(r) ? live++ : none++) == i) *row = r;
+}
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Args a) {
   constexpr int E = Vec<T>::N;
@@ -209,12 +236,15 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   __shared__ float s_peak[TOP ? kThreads : 1], s_bound;   // the threads' greatest; a bound of the best
   __shared__ u64 s_cand[TOP ? kCand : 1];
   __shared__ bf16 s_most[TOP ? kBatches : 1][TOP ? kThreads : 1];   // rounded up
-  __shared__ int s_count;
+  __shared__ int s_count, s_row;
   __shared__ int s_last;
 
-  const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-  const int n = row / a.B, b = row % a.B;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = blockIdx.x % a.parts;
+  if (a.rows) in_order(a, blockIdx.x / a.parts, lane, warp, &s_row);
+  else if (threadIdx.x == 0) s_row = blockIdx.x / a.parts;
+  __syncthreads();
+  const int row = s_row, n = row / a.B, b = row % a.B;
   const int64_t x = a.tokens[row];
   if (x < 0 || x >= a.V) {   // none: nothing is read
     if (part != 0) return;
@@ -458,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   gather();
 
   if (a.parts > 1) {
+    const int row = s_row;   // again, so that no register holds it all the way
     const int64_t at = (int64_t)row * a.parts;
     if (warp == 0) {
       if (lane == 0) __stcg(a.stat + at + part, make_float4(st.m, st.s, st.w, __int_as_float(st.ahead)));
@@ -473,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     }
     if (TOP) {
       if (threadIdx.x < 32) s_best[threadIdx.x] = 0;
-      const int count = a.parts * a.top;   // at most the buffer's places
+      const int count = a.parts * a.top;   // at most the places of the buffer
       for (int i = threadIdx.x; i < count; i += kThreads) s_cand[i] = __ldcg(a.best + at * a.top + i);
       __syncthreads();
       place(count);
@@ -483,17 +514,18 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
   if (warp != 0) return;
 
   if (TOP) list = s_best[lane];
+  const int out = s_row;
   const float log_s = logf(st.s);   // s = 0: nothing above -inf
   const int ahead = st.ahead + (low_id ? (int)x : 0);
   auto log_p = [&](float v) { return greedy ? -INFINITY : (v - st.m) * inv_t - log_s; };
   if (lane == 0) {
     if (!(st.s > 0.0f)) atomicOr(a.err, XP_ERR_EMPTY);
-    if (a.logprob) a.logprob[row] = !(st.s > 0.0f) ? -INFINITY : greedy && ahead == 0 ? 0.0f : log_p(mine);
-    if (a.entropy) a.entropy[row] = greedy || !(st.s > 0.0f) ? 0.0f : log_s - st.w / st.s * 0.693147180559945f;
-    if (a.rank) a.rank[row] = ahead + 1;
+    if (a.logprob) a.logprob[out] = !(st.s > 0.0f) ? -INFINITY : greedy && ahead == 0 ? 0.0f : log_p(mine);
+    if (a.entropy) a.entropy[out] = greedy || !(st.s > 0.0f) ? 0.0f : log_s - st.w / st.s * 0.693147180559945f;
+    if (a.rank) a.rank[out] = ahead + 1;
   }
   if (TOP && lane < a.top) {
-    const int64_t at = (int64_t)row * a.top + lane;
+    const int64_t at = (int64_t)out * a.top + lane;
     if (a.top_ids) a.top_ids[at] = list ? (int64_t)packed_idx(list) : -1;
     if (a.top_logprobs)
       a.top_logprobs[at] = !list ? -INFINITY : greedy && lane == 0 ? 0.0f : log_p(packed_val(list));
@@ -511,8 +543,8 @@ xp_logprobs_ws xp_logprobs_layout(const xp_head* h, int rows, int top) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = (o + bytes + 255) / 256 * 256; return at; };
   L.tickets = take(cut * 4);
-  L.stat = take(kMostParts * cut * sizeof(float4));
-  L.best = take(kMostParts * cut * 8 * (size_t)top);
+  L.stat = take(cut * sizeof(float4));
+  L.best = take(cut * 8 * (size_t)top);
   L.total = o;
   return L;
 }
@@ -524,16 +556,10 @@ cudaError_t xp_launch_logprobs(const xp_head* h, const xp_logprobs_args& g, cuda
   a.sn = g.sn, a.sb = g.sb;
   a.tokens = g.tokens, a.temperature = g.temperature;
   a.B = g.B, a.V = h->V, a.top = g.top;
-  // Parts so that the CTAs come in whole turns: the least turns * (1 / parts + kPartCost).  Rows that fill the
-  // GPU by themselves are not cut.
-  int most = std::min(std::max(1, h->V / (16 / es) / kLeastVectors), kMostParts * cut / std::max(1, rows));
-  if (g.top > 0) most = std::min(most, kCand / g.top);   // what they leave has to fit the buffer
-  a.parts = 1;
-  float best = FLT_MAX;
-  for (int parts = 1; rows < cut && parts <= most; ++parts) {
-    const float time = (float)((rows * parts + cut - 1) / cut) * (1.0f / parts + kPartCost);
-    if (time < best) best = time, a.parts = parts;
-  }
+  // As many parts as run at once: 32 rows of 151936 in fp32 45 us whole, 25 in 10 parts, 31 in 18; 200 rows 50 whole,
+  // 42 in 3, 56 in 4; 456 rows 65 whole, 85 in 2.
+  a.parts = std::max(1, std::min({h->V / (16 / es) / kLeastVectors, cut / rows, kMostParts}));
+  a.rows = rows <= cut ? rows : 0;
   a.logprob = g.logprob, a.entropy = g.entropy, a.rank = g.rank;
   a.top_ids = g.top_ids, a.top_logprobs = g.top_logprobs;
   a.err = h->err;

@@ -229,3 +229,16 @@ def test_infinity_beside_the_largest_finite_value(dtype, shift):
     rows[3, 0, 2048:2056] = torch.tensor([math.inf, most] * 4, device="cuda", dtype=dtype)
     for token in (0, 1, 40, 41, 2050, 2051, 2053, 2054, 4098, 4099):
         check(make_head(V), rows, torch.full((4, 1), token, device="cuda"), None, 9)
+
+
+@pytest.mark.parametrize("size", [(300, 1, 700), (75, 8, 700), (76, 8, 33), (3, 50, 20011), (1, 2, 40000)], ids=str)
+def test_rows_without_a_token_among_others(size):
+    """Up to as many rows as run at once, cut and whole: half of them without a token."""
+    N, B, V = size
+    g = torch.Generator(device="cuda").manual_seed(N)
+    logits = torch.randn(N, B, V, generator=g, device="cuda", dtype=torch.bfloat16)
+    tokens = torch.randint(0, V, (N, B), generator=g, device="cuda")
+    tokens[torch.rand(N, B, generator=g, device="cuda") < 0.5] = -1
+    tokens[-1, -1] = V - 1
+    check(make_head(V), logits, tokens, None, 3)
+    check(make_head(V), logits, torch.full_like(tokens, -1), None, 3)
