@@ -116,6 +116,13 @@ _SIGS = {
 }
 
 _lib = None
+torch = None   # once something has needed it
+
+
+def _need_torch():
+    global torch
+    import torch as module
+    torch = module
 
 
 def lib() -> ctypes.CDLL:
@@ -336,7 +343,8 @@ def _want(ok: bool, what: str):
 
 def _here(names, *tensors):
     """All of them on the current device (None passes), which is returned."""
-    import torch
+    if torch is None:
+        _need_torch()
     device = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != device:
@@ -347,29 +355,57 @@ def _here(names, *tensors):
 
 def _code(name, t):
     """The library's type code of a tensor's dtype."""
-    import torch
-    if t.dtype == torch.bfloat16:
+    if torch is None:
+        _need_torch()
+    dtype = t.dtype
+    if dtype == torch.bfloat16:
         return XP_BF16
-    if t.dtype != torch.float32:
+    if dtype != torch.float32:
         raise ValueError(f"{name}: bf16 or fp32")
     return XP_F32
 
 
 def _ints(name, t, n):
     """A contiguous int32 vector of at least n elements on the GPU (None passes)."""
-    import torch
+    if torch is None:
+        _need_torch()
     if t is not None and not (t.dtype == torch.int32 and t.is_cuda and t.is_contiguous()
                               and t.numel() >= n):
         raise ValueError(f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
 
 
 def _table(name, t, rows=None):
-    """An int32 page table [rows, width], unit stride over the columns."""
-    import torch
-    if not (t.dtype == torch.int32 and t.dim() == 2 and t.shape[1] > 0
-            and (t.stride(1) == 1 or t.shape[1] == 1) and (rows is None or t.shape[0] >= rows)):
-        raise ValueError(f"{name}: an int32 tensor [rows, width], unit stride over the columns")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    """An int32 page table [rows, width], unit stride over the columns: its rows' stride."""
+    return _columns(name, t, rows)[0]
+
+
+def _columns(name, t, rows=None):
+    """The same: its rows' stride and its columns."""
+    if torch is None:
+        _need_torch()
+    shape = t.shape
+    if t.dtype == torch.int32 and len(shape) == 2:
+        (have, width), (ld, step) = shape, t.stride()
+        if width > 0 and (step == 1 or width == 1) and (rows is None or have >= rows):
+            return (ld if have > 1 else width), width
+    raise ValueError(f"{name}: an int32 tensor [rows, width], unit stride over the columns")
+
+
+def _flat(name, t, dtype, n):
+    """A contiguous tensor of a type and at least n elements (None passes): its pointer."""
+    if t is None:
+        return None
+    if not (t.dtype == dtype and t.is_contiguous() and t.numel() >= n):
+        raise ValueError(f"{name}: contiguous {dtype} of at least {n} elements")
+    return t.data_ptr()
+
+
+def _rows(k, v):
+    """K and V rows of the same strides: their sizes and strides."""
+    shape, strides = k.shape, k.stride()
+    _want(len(shape) == 4 and strides[3] == 1 and shape == v.shape and strides == v.stride() and k.dtype == v.dtype,
+          "k, v: [N, T, kv_heads, head_dim] of the same strides")
+    return *shape, *strides[:3]
 
 
 def xp_verify_workspace_bytes(head, N: int) -> int:
@@ -415,27 +451,24 @@ def xp_token_logprobs(head, logits, tokens, temperature, logprob, entropy, rank,
     """Log probabilities of tokens [N, B] (-1: none) under logits [N, B, V] at temperature [N] (None: 1).
     Out, each may be None: logprob, entropy [N, B], rank [N, B] int32, top_ids int64 and top_logprobs
     [N, B, top], top up to 32."""
-    import torch
-    N, B, V = logits.shape
-    f32, i64, i32 = torch.float32, torch.int64, torch.int32
     device = _here("logits tokens temperature logprob entropy rank top_ids top_logprobs ws", logits, tokens,
                    temperature, logprob, entropy, rank, top_ids, top_logprobs, ws)
+    N, B, V = logits.shape
     sn, sb, sv = logits.stride()
     _want(sv == 1, "logits: [N, B, V] with unit stride over V")
-    tops = {t.shape[-1] for t in (top_ids, top_logprobs) if t is not None}
-    _want(all(t is None or t.shape[:-1] == (N, B) for t in (top_ids, top_logprobs)) and len(tops) < 2,
-          "top_ids, top_logprobs: [N, B, top]")
-    top = tops.pop() if tops else 0
-    for name, t, dt, count in (("tokens", tokens, i64, N * B), ("temperature", temperature, f32, N),
-                               ("logprob", logprob, f32, N * B), ("entropy", entropy, f32, N * B),
-                               ("rank", rank, i32, N * B), ("top_ids", top_ids, i64, N * B * top),
-                               ("top_logprobs", top_logprobs, f32, N * B * top)):
-        if t is not None and not (t.dtype == dt and t.is_contiguous() and t.numel() >= count):
-            raise ValueError(f"{name}: contiguous {dt} of at least {count} elements")
+    top = 0
+    some = top_ids if top_ids is not None else top_logprobs
+    if some is not None:
+        top = some.shape[-1]
+        for t in (top_ids, top_logprobs):
+            _want(t is None or t.shape == (N, B, top), "top_ids, top_logprobs: [N, B, top]")
+    f32, i64 = torch.float32, torch.int64
     _check("xp_token_logprobs", lib().xp_token_logprobs(
-        head, _ptr(logits), sn, sb, _ptr(tokens), N, B, V, _code("logits", logits), _ptr(temperature), top,
-        _ptr(logprob), _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top_logprobs), _ptr(ws), _nbytes(ws),
-        _stream(stream, device)))
+        head, logits.data_ptr(), sn, sb, _flat("tokens", tokens, i64, N * B), N, B, V, _code("logits", logits),
+        _flat("temperature", temperature, f32, N), top, _flat("logprob", logprob, f32, N * B),
+        _flat("entropy", entropy, f32, N * B), _flat("rank", rank, torch.int32, N * B),
+        _flat("top_ids", top_ids, i64, N * B * top), _flat("top_logprobs", top_logprobs, f32, N * B * top),
+        _ptr(ws), _nbytes(ws), _stream(stream, device)))
 
 
 def make_cache_desc(k, v, max_seqs: int = 4096) -> xp_cache_desc:
@@ -500,31 +533,26 @@ def xp_cache_get_error(cache, stream=None) -> int:
 def xp_cache_append(cache, layer, k, v, table, lens, stream=None):
     """Write the K and V rows [N, T, kv_heads, head_dim] of the newest tokens (lens counts them).
     Only the table's own columns are read, those of a wider tensor that it is a part of are not."""
-    N, T = k.shape[:2]
     device = _here("k v table lens", k, v, table, lens)
-    _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
-          and k.stride(3) == 1, "k, v: [N, T, kv_heads, head_dim] of the same strides")
-    ld = _table("table", table, N)
+    N, T, heads, dim, sn, st, sh = _rows(k, v)
+    ld, width = _columns("table", table, N)
     _ints("lens", lens, N)
     _check("xp_cache_append", lib().xp_cache_append_columns(
-        cache, layer, _ptr(k), _ptr(v), *k.stride()[:3], k.shape[2], k.shape[3],
-        _code("k", k), _ptr(table), ld, table.shape[1], _ptr(lens), N, T,
-        _stream(stream, device)))
+        cache, layer, k.data_ptr(), v.data_ptr(), sn, st, sh, heads, dim, _code("k", k), table.data_ptr(), ld,
+        width, _ptr(lens), N, T, _stream(stream, device)))
 
 
 def xp_cache_read(cache, layer, table, lens, first, k, v, stream=None):
     """Read back T positions of every row into k, v [N, T, kv_heads, head_dim] (bf16 or fp32, whatever the
     cache's type), from position first[n] on (None: 0); zeros where a position is not in [0, lens[n])."""
-    N, T = k.shape[:2]
     device = _here("table lens first k v", table, lens, first, k, v)
-    _want(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
-          and k.stride(3) == 1, "k, v: [N, T, kv_heads, head_dim] of the same strides")
-    ld = _table("table", table, N)
+    N, T, heads, dim, sn, st, sh = _rows(k, v)
+    ld, width = _columns("table", table, N)
     _ints("lens", lens, N)
     _ints("first", first, N)
     _check("xp_cache_read", lib().xp_cache_read(
-        cache, layer, _ptr(table), ld, table.shape[1], _ptr(lens), _ptr(first), N, T, _ptr(k), _ptr(v),
-        *k.stride()[:3], k.shape[2], k.shape[3], _code("k", k), _stream(stream, device)))
+        cache, layer, table.data_ptr(), ld, width, _ptr(lens), _ptr(first), N, T, k.data_ptr(), v.data_ptr(),
+        sn, st, sh, heads, dim, _code("k", k), _stream(stream, device)))
 
 
 def xp_cache_copy(cache, src, dst, stream=None):
@@ -606,23 +634,22 @@ def xp_attention_workspace_bytes(cache, attn: xp_attn) -> int:
 def xp_prefix_attention(cache, attn, q, prefix_table, table, lens, out, lse, ws, stream=None):
     """Attention of attn.N sequences of attn.T new tokens over a shared prefix and their tails
     (attn from make_attn for tensors of these shapes and strides)."""
-    import torch
     _want((q.shape, q.stride(), q.dtype) == attn.q_like
           and (out.shape, out.stride(), out.dtype) == attn.out_like,
           "q, out: the shapes, strides and type that make_attn was given")
     device = _here("q prefix_table table lens out lse ws", q, prefix_table, table, lens, out, lse, ws)
-    ld = width = 0
+    N, ld, width = attn.N, 0, 0
     if table is not None:
-        ld, width = _table("table", table, attn.N), table.shape[1]
-    _ints("lens", lens, attn.N)
+        ld, width = _columns("table", table, N)
+    _ints("lens", lens, N)
     _ints("prefix_table", prefix_table, 0)
     _want(lse is None or (lse.is_contiguous() and lse.dtype == torch.float32
-                          and lse.numel() >= attn.N * attn.T * attn.heads),
+                          and lse.numel() >= N * attn.T * attn.heads),
           "lse: contiguous fp32 [N, T, heads]")
     _check("xp_prefix_attention", lib().xp_prefix_attention(
-        cache, ctypes.byref(attn), _ptr(q), _ptr(prefix_table),
+        cache, ctypes.byref(attn), q.data_ptr(), _ptr(prefix_table),
         0 if prefix_table is None else prefix_table.numel(), _ptr(table), ld, width, _ptr(lens),
-        _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream, device)))
+        out.data_ptr(), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream, device)))
 
 
 # ------------------------------------------------------ torch conveniences ---
