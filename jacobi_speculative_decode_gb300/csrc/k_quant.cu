@@ -319,8 +319,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const RowArgs a, bool wi
 // ---------------------------------------------------------------------------
 // A quantised cache's tokens as fp16 (exactly) for attention on tcgen05, which many queries of each key are
 // better done by: pools [head][page of kWidePage tokens][dim] and the table that names their pages in order.
-// Behind a sequence's end its last page is zeros.  A CTA is 32 tokens of a head (with 64 draft blocks take 6 us
-// more, with 128 24).  The CTAs behind the pages' make the queries fp16, a warp a row, scaled by the power of two that brings the row's largest into [1, 4).
+// Behind a sequence's end its last page is zeros.  A CTA is 32 tokens of a head.  Bound by what it writes: 8192 and 32
+// times 17 to 1500 tokens, 8 heads of 128 in 8 bits, 70 MB in, 135 out to L2 and past it, 33 us (64 tokens a CTA 1 us
+// more, 128 5 us).  The CTAs behind the pages' make the queries fp16, a warp a row, scaled by the power of two that
+// brings the row's largest into [1, 4).
 // ---------------------------------------------------------------------------
 constexpr int kWideTokens = 32;
 struct WidenArgs {
@@ -381,34 +383,43 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
   if (pos0 >= len) return;
   if (h == 0 && t0 == 0 && threadIdx.x == 0) w.table[page] = page;
 
-  // A thread takes a piece of 8 dims of every 256 / (D/8)-th token: all pages, then all codes, then all stores.
+  // where the CTA's tokens begin in either pool, and their scales; behind the end -1
+  __shared__ int64_t s_code[kWideTokens], s_scale[kWideTokens];
+  if (threadIdx.x < kWideTokens) {
+    const int pos = pos0 + t0 + (int)threadIdx.x;
+    int64_t code = -1, scale = 0;
+    if (pos < len) {
+      const int col = pos / a.ps, at = pos - col * a.ps;
+      int p = table[col];
+      if (p < 0 || p >= a.pages) {
+        atomicOr(a.err, XP_ERR_BADPAGE);
+        p = p < 0 ? 0 : a.pages - 1;
+      }
+      const int64_t from = p * a.page + h * a.head;
+      code = from + at * a.token;
+      scale = from + a.scale_at + at * a.scale;
+    }
+    s_code[threadIdx.x] = code;
+    s_scale[threadIdx.x] = scale;
+  }
+  __syncthreads();
+
+  // A thread takes a piece of 8 dims of every 256 / (D/8)-th token: all codes, then all stores.
   constexpr int kPieces = D / 8, kStep = kThreads / kPieces, kEach = kWideTokens / kStep;
   const int e = threadIdx.x % kPieces * 8, i0 = threadIdx.x / kPieces;
-  int p[kEach], at[kEach];
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int pos = pos0 + t0 + i0 + k * kStep, col = pos / a.ps;
-    at[k] = pos - col * a.ps;
-    p[k] = pos < len ? table[col] : -1;
-  }
+  const char *k_code = a.kp + e / 8 * BITS, *v_code = a.vp + e / 8 * BITS, *k_scale = a.kp + e / 16, *v_scale = a.vp + e / 16;
   uint2 code[kEach][2];
   unsigned scale[kEach][2];
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    const bool live = pos0 + t0 + i0 + k * kStep < len;
-    if (live && (p[k] < 0 || p[k] >= a.pages)) {
-      atomicOr(a.err, XP_ERR_BADPAGE);
-      p[k] = p[k] < 0 ? 0 : a.pages - 1;
-    }
-    const int64_t head = p[k] * a.page + h * a.head;
+    const int64_t at = s_code[i0 + k * kStep], of_scale = s_scale[i0 + k * kStep];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const char* from = (kv ? a.vp : a.kp) + head;
       code[k][kv] = make_uint2(0, 0);
       scale[k][kv] = 0;
-      if (live) {
-        scale[k][kv] = (uint8_t)from[a.scale_at + at[k] * a.scale + e / 16];
-        const char* c = from + at[k] * a.token + e / 8 * BITS;
+      if (at >= 0) {
+        scale[k][kv] = (uint8_t)(kv ? v_scale : k_scale)[of_scale];
+        const char* c = (kv ? v_code : k_code) + at;
         if (BITS == 4) code[k][kv].x = __ldcs((const unsigned*)c);
         else code[k][kv] = __ldcs((const uint2*)c);
       }
