@@ -2,8 +2,8 @@
 //
 // A CTA takes kTokens tokens of one sequence and finds their pages once; a thread is one piece of a token's
 // row (8 dims of K or V written, 16 bytes of them read) and walks over the tokens, so that nothing is divided
-// inside.  8 prompts of 4096 tokens, 8 heads of 128, fp32 in 8 bits: written in 68 us (340 MB, 4.9 TB/s, issue slots
-// busy in 64% of the cycles), read back in 61 (5.5 TB/s, 82% of measured); 32 sequences to 3000 tokens out of 4
+// inside.  8 prompts of 4096 tokens, 8 heads of 128, fp32 in 8 bits: written in 65 us (340 MB, 5.2 TB/s, between
+// HBM and what quantising costs), read back in 61 (5.5 TB/s, 82% of measured); 32 sequences to 3000 tokens out of 4
 // bits as bf16 75 us, 6.0 TB/s, 88%.
 #include <algorithm>
 
@@ -102,8 +102,8 @@ __device__ __forceinline__ float reciprocal(float x) {   // nearly
   return r;
 }
 
-// tokens of a thread whose loads are on their way together (four to append leave two CTAs an SM: 141 us for
-// both calls of the prompts, not 133)
+// tokens of a thread whose loads are on their way together; to append, the next while one is quantised (both calls
+// of the prompts 126 us, 128 with two and two together; with four, which leave two CTAs an SM, 8 us more)
 constexpr int kAppendBatch = 2, kReadBatch = 4;
 
 // What a thread does of a row: piece `e` of head `h` of K or V, for every lanes-th token from `lane` on.
@@ -135,26 +135,29 @@ __global__ void __launch_bounds__(kThreads, 4) append_quant_kernel(const RowArgs
   const int n = blockIdx.x / chunks, t0 = (int)(blockIdx.x % chunks) * kTokens;
   find_pages(a, n, t0, (int64_t)a.lens[n] - a.T, INT64_MAX, &s);
 
+  const int count = min(kTokens, a.T - t0);
   const unsigned both = 3u << (threadIdx.x & 30);   // the two of a group: rows are a whole number of groups
   for_parts(a, 8, [&](const Part& part) {
     const T* from = (const T*)(part.is_v ? a.v : a.k) + n * a.sn + t0 * a.st + part.h * a.sh + part.e;
     char* pool = (part.is_v ? a.vp : a.kp) + part.h * a.head;
     const int g = part.e / 16;
-    for (int i0 = part.lane; i0 < kTokens; i0 += kAppendBatch * part.lanes) {
-      Eight<T> raw[kAppendBatch];
-      int64_t page[kAppendBatch];
+    Eight<T> raw[kAppendBatch];
+    int64_t page[kAppendBatch];
+    auto load = [&](int k, int i) {
+      page[k] = i < count ? s.page[i] : -1;
+      if (page[k] >= 0) raw[k].load(from + i * a.st, wide);
+    };
+#pragma unroll
+    for (int k = 0; k < kAppendBatch; ++k) load(k, part.lane + k * part.lanes);
+    for (int i0 = part.lane; i0 < count; i0 += kAppendBatch * part.lanes) {
 #pragma unroll
       for (int k = 0; k < kAppendBatch; ++k) {
-        const int i = i0 + k * part.lanes;
-        page[k] = i < kTokens ? s.page[i] : -1;
-        if (page[k] >= 0) raw[k].load(from + i * a.st, wide);
-      }
-#pragma unroll
-      for (int k = 0; k < kAppendBatch; ++k) {
-        if (page[k] < 0) continue;   // the same in both
-        const int at = s.at[i0 + k * part.lanes];
+        const int64_t to_page = page[k];
         float x[8], top = 0.0f;
         floats_of(raw[k], x);
+        load(k, i0 + (k + kAppendBatch) * part.lanes);
+        if (to_page < 0) continue;   // the same in both
+        const int at = s.at[i0 + k * part.lanes];
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(x[j]));
         top = max_nan(top, __shfl_xor_sync(both, top, 1));
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_quant_kernel(const RowArgs
           for (int j = 0; j < 8; ++j) x[j] = fminf(fmaxf(x[j], -most), most);
           atomicOr(a.err, XP_ERR_RANGE);
         }
-        char* head = pool + page[k];
+        char* head = pool + to_page;
         char* scale = head + a.scale_at + at * a.scale;
         if (part.e % 16 == 0) scale[g] = (char)b;
         if (part.e + 8 == a.D)   // the padding behind the scales
