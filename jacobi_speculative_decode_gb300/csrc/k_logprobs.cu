@@ -8,10 +8,11 @@
 // digits.
 // Bound by the row's bytes in fp32: 2048 rows of 151647, 1.24 GB, 196 us, 6.3 TB/s, 93% of measured.  In bf16 by
 // instructions: 2048 rows of 151647, 621 MB, 116 us, 79%.  One CTA
-// a row leaves few rows to as many CTAs: 410 rows (125 MB) with 20 alternatives 42 us, with none 31.
+// a row leaves few rows to as many CTAs: 410 rows (125 MB) with 20 alternatives 39 us, with none 31.
 // The best ids.  On the way a thread only writes down the greatest of every 16 bytes' batch.  The `top`-th of the
 // 256 threads' greatest is a bound: there are `top` elements that are not below it, and few that are above.
-// The batches that reach it are read again (from L2, some 25 of a row's), their elements that do go to a buffer,
+// The batches that reach it are read again (from L2, some 25 of a row's, by the threads they are of, all at once:
+// warp by warp 42 us, not 39), their elements that do go to a buffer,
 // and an element of the buffer counts those before it and so knows its place.  Where the buffer overflows, as
 // for a row of equal logits, every warp reads its part of the row again into a sorted list.
 // (Looked at on the way, under a bound that follows, the same rows took 62 us where 44 are taken without.)
@@ -429,9 +430,14 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     }
     __syncthreads();
     bound = s_bound;
-    batch = 0;
-    for (int v = first; v < v1; v += kThreads * kLoads, ++batch) {
-      if (!__any_sync(kAll, to_f(s_most[min(batch, kBatches - 1)][threadIdx.x]) >= bound)) continue;
+    // every lane its own batches, all lanes' first ones together
+    u64 reach = 0;
+    for (int i = 0; i < min(batch, kBatches); ++i) reach |= (u64)(to_f(s_most[i][threadIdx.x]) >= bound) << i;
+    int behind = 0;   // of the batches that share the last place
+    while (__any_sync(kAll, reach != 0)) {
+      const int i = __ffsll(reach) - 1;
+      const int v = i < 0 ? v1 : first + (i + behind) * (kThreads * kLoads);
+      if (i < kBatches - 1 || ++behind == batch - i) reach &= reach - 1;
       load(v);
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {

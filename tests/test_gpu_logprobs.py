@@ -242,3 +242,24 @@ def test_rows_without_a_token_among_others(size):
     tokens[-1, -1] = V - 1
     check(make_head(V), logits, tokens, None, 3)
     check(make_head(V), logits, torch.full_like(tokens, -1), None, 3)
+
+
+@pytest.mark.parametrize("rise", [-1, 0, 1])
+def test_more_batches_than_places(rise):
+    """Whole rows of 300000: 74 batches a thread, of which the greatest of 64 are held."""
+    V, N = 300000, 620
+    g = torch.Generator(device="cuda").manual_seed(5)
+    row = torch.randn(1, 1, V, generator=g, device="cuda") + rise * torch.linspace(0, 40, V, device="cuda")
+    logits, tokens = row.expand(N, 1, V), torch.full((N, 1), -1, device="cuda")
+    at = {3: 0, 300: V - 1, 619: int(row.argmax())}
+    for n, token in at.items():
+        tokens[n] = token
+    out = call(make_head(V), logits, tokens, None, 32)
+    got = {k: t.cpu().numpy() for k, t in out.items()}
+    for n, token in at.items():
+        lp, h, rank, ids, tops = Q.logprobs(row[0, 0].double().cpu().numpy(), token, 1.0, 32)
+        assert got["rank"][n, 0] == rank and got["top_ids"][n, 0].tolist() == ids
+        # V/256 + 64 additions of 2^-24, and 2^-22 of x below 2^6 and of the differences' mean
+        assert abs(got["logprob"][n, 0] - lp) <= 1300 * 2.0 ** -24 + 2.0 ** -15
+        assert np.abs(got["top_logprobs"][n, 0] - np.array(tops)).max() <= 1300 * 2.0 ** -24 + 2.0 ** -15
+    assert (got["rank"][[0, 2, 618]] == 0).all()
