@@ -16,7 +16,7 @@
 // words, are the logic pipe's, which takes one every other cycle.  16 single tokens, 32 heads of 128 over 8,
 // contexts of 1000 to 32768 (311 MB): 75 us, 4.1 TB/s, 61% of measured, and 9 for the joining; issue slots
 // are busy in 58% of the cycles, the logic pipe in 48%, the tensor pipe in 24%, with 14 of 16 warps an SM.
-// In 8 bits (589 MB) 125 us for both kernels, 69% of measured.  (Other numbers of CTAs an SM and of stages
+// In 8 bits (589 MB) 116 us for both kernels, 75% of measured.  (Other numbers of CTAs an SM and of stages
 // gave nothing.)
 //
 // A value held is exact in fp16 (quant.cuh).  Queries are bf16, scaled by a power of two a row so that
@@ -133,14 +133,18 @@ template <int BITS, int DP, int NQ> struct Cfg {
   static constexpr int CODE = DP * BITS / 8;              // bytes a token of the ring
   static constexpr int SCALE = DP / 16;
   static constexpr int STAGE = kStep * 2 * (CODE + SCALE);
-  static constexpr int STAGES = STAGE > 9000 ? 2 : 3;
+  static constexpr int STAGES = STAGE > 8000 ? 2 : 3;
   static constexpr int RING = kWarps * STAGES * STAGE;
   static constexpr int PITCH = DP + 4;                    // floats of a row of the joined results
   static constexpr int JOIN = kWarps * 8 * PITCH * 4;
   static constexpr int QUERIES = NQ == 4 ? NQ * (DP / 16) * 32 * 8 : 0;   // held in shared memory
   static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + QUERIES;
-  // CTAs an SM, as registers (results: 4 NQ KS a thread) and shared memory allow
-  static constexpr int RESIDENT = DP == 64 ? (NQ == 1 ? 5 : NQ == 2 ? 4 : 2) : DP == 128 && NQ == 1 && BITS == 4 ? 4 : 2;
+  // CTAs an SM, as registers (results: 4 NQ KS a thread) and shared memory allow.  Heads of 128 in 8 bits: three with
+  // two stages and two with three, contexts of 1000 to 32768 behind 1 token 116 and 123 us, behind 4 134 and 147 (in
+  // 4 bits, behind 4: three and two 115 both).
+  static constexpr int RESIDENT = DP == 64    ? (NQ == 1 ? 5 : NQ == 2 ? 4 : 2)
+                                  : DP == 128 ? (BITS == 4 ? (NQ == 1 ? 4 : 2) : NQ < 4 ? 3 : 2)
+                                              : 2;
   // 4 bits: values are widened 2^-7 times as large (see widen4), queries are 16 times (so that 1/16 of
   // them keeps as much)
   static constexpr float UNIT = BITS == 4 ? 128.0f : 1.0f, QUERY = BITS == 4 ? 16.0f : 1.0f;
