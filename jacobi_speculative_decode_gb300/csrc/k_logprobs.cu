@@ -217,6 +217,7 @@ __device__ __forceinline__ void in_order(const Args& a, int i, int lane, int war
     if (lane >= o) inc += t;
   }
   if (lane == 31) s_live[warp] = inc;
+  if (threadIdx.x == 0) *row = i;   // a row at any rate, were the tokens written to meanwhile
   __syncthreads();
   int live = inc - mine, all = 0;   // before this thread's, and all
 #pragma unroll
