@@ -560,6 +560,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     // scores in base 2; element e of a tile: key gr + 8 (e / 2), query 2 t4 + e % 2
     bool grew = false;
     float top[NQ][2];
+    if (kb + kStep > least) {   // some are hidden (never so but in the last steps)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (kb + (kh + kt) * 16 + e / 2 * 8 + gr >= limit[q][e % 2]) s[kt][q][e] = -INFINITY;
+    }
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       top[q][0] = top[q][1] = -INFINITY;
@@ -567,10 +576,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float v = s[kt][q][e] * cz[q][e % 2];
-          if (kb + kStep > least && kb + (kh + kt) * 16 + e / 2 * 8 + gr >= limit[q][e % 2]) v = -INFINITY;
-          s[kt][q][e] = v;
-          top[q][e % 2] = fmaxf(top[q][e % 2], v);
+          s[kt][q][e] *= cz[q][e % 2];   // positive, so -inf stays
+          top[q][e % 2] = fmaxf(top[q][e % 2], s[kt][q][e]);
         }
 #pragma unroll
       for (int i = 0; i < 2; ++i) grew |= top[q][i] > m[q][i] + kLazy;
