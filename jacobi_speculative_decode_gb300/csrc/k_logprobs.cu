@@ -47,7 +47,7 @@ struct Args {
   int64_t sn, sb;
   const int64_t* tokens;
   const float* temperature;
-  int B, V, top, parts, rows;   // rows: 0 where there are more than CTAs at once
+  int B, V, top, parts, rows;   // rows: 0 where they are taken as they come
   float *logprob, *entropy;
   int32_t* rank;
   int64_t* top_ids;
@@ -566,7 +566,8 @@ cudaError_t xp_launch_logprobs(const xp_head* h, const xp_logprobs_args& g, cuda
   // As many parts as run at once: 32 rows of 151936 in fp32 45 us whole, 25 in 10 parts, 31 in 18; 200 rows 50 whole,
   // 42 in 3, 56 in 4; 456 rows 65 whole, 85 in 2.
   a.parts = std::max(1, std::min({h->V / (16 / es) / kLeastVectors, cut / rows, kMostParts}));
-  a.rows = rows <= cut ? rows : 0;
+  // An order, which takes a microsecond, where SMs have more than one CTA and all run at once
+  a.rows = rows <= cut && rows * a.parts > h->num_sms ? rows : 0;
   a.logprob = g.logprob, a.entropy = g.entropy, a.rank = g.rank;
   a.top_ids = g.top_ids, a.top_logprobs = g.top_logprobs;
   a.err = h->err;
