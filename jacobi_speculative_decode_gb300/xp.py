@@ -366,12 +366,14 @@ def _code(name, t):
 
 
 def _ints(name, t, n):
-    """A contiguous int32 vector of at least n elements on the GPU (None passes)."""
+    """A contiguous int32 vector of at least n elements on the GPU (None passes): its pointer."""
     if torch is None:
         _need_torch()
-    if t is not None and not (t.dtype == torch.int32 and t.is_cuda and t.is_contiguous()
-                              and t.numel() >= n):
-        raise ValueError(f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
+    if t is None:
+        return None
+    if t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    raise ValueError(f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
 
 
 def _table(name, t, rows=None):
@@ -536,10 +538,9 @@ def xp_cache_append(cache, layer, k, v, table, lens, stream=None):
     device = _here("k v table lens", k, v, table, lens)
     N, T, heads, dim, sn, st, sh = _rows(k, v)
     ld, width = _columns("table", table, N)
-    _ints("lens", lens, N)
     _check("xp_cache_append", lib().xp_cache_append_columns(
         cache, layer, k.data_ptr(), v.data_ptr(), sn, st, sh, heads, dim, _code("k", k), table.data_ptr(), ld,
-        width, _ptr(lens), N, T, _stream(stream, device)))
+        width, _ints("lens", lens, N), N, T, _stream(stream, device)))
 
 
 def xp_cache_read(cache, layer, table, lens, first, k, v, stream=None):
@@ -548,10 +549,8 @@ def xp_cache_read(cache, layer, table, lens, first, k, v, stream=None):
     device = _here("table lens first k v", table, lens, first, k, v)
     N, T, heads, dim, sn, st, sh = _rows(k, v)
     ld, width = _columns("table", table, N)
-    _ints("lens", lens, N)
-    _ints("first", first, N)
     _check("xp_cache_read", lib().xp_cache_read(
-        cache, layer, table.data_ptr(), ld, width, _ptr(lens), _ptr(first), N, T, k.data_ptr(), v.data_ptr(),
+        cache, layer, table.data_ptr(), ld, width, _ints("lens", lens, N), _ints("first", first, N), N, T, k.data_ptr(), v.data_ptr(),
         sn, st, sh, heads, dim, _code("k", k), _stream(stream, device)))
 
 
@@ -638,18 +637,16 @@ def xp_prefix_attention(cache, attn, q, prefix_table, table, lens, out, lse, ws,
           and (out.shape, out.stride(), out.dtype) == attn.out_like,
           "q, out: the shapes, strides and type that make_attn was given")
     device = _here("q prefix_table table lens out lse ws", q, prefix_table, table, lens, out, lse, ws)
-    N, ld, width = attn.N, 0, 0
+    N, columns, ld, width = attn.N, None, 0, 0
     if table is not None:
-        ld, width = _columns("table", table, N)
-    _ints("lens", lens, N)
-    _ints("prefix_table", prefix_table, 0)
+        columns, (ld, width) = table.data_ptr(), _columns("table", table, N)
     _want(lse is None or (lse.is_contiguous() and lse.dtype == torch.float32
                           and lse.numel() >= N * attn.T * attn.heads),
           "lse: contiguous fp32 [N, T, heads]")
     _check("xp_prefix_attention", lib().xp_prefix_attention(
-        cache, ctypes.byref(attn), q.data_ptr(), _ptr(prefix_table),
-        0 if prefix_table is None else prefix_table.numel(), _ptr(table), ld, width, _ptr(lens),
-        out.data_ptr(), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream, device)))
+        cache, ctypes.byref(attn), q.data_ptr(), _ints("prefix_table", prefix_table, 0),
+        0 if prefix_table is None else prefix_table.numel(), columns, ld, width, _ints("lens", lens, N),
+        out.data_ptr(), None if lse is None else lse.data_ptr(), _ptr(ws), _nbytes(ws), _stream(stream, device)))
 
 
 # ------------------------------------------------------ torch conveniences ---
