@@ -22,8 +22,8 @@
 // A value held is exact in fp16 (quant.cuh).  Queries are bf16, scaled by a power of two a row so that
 // their largest is in [1, 4) (4 bits: 16 times that, and 1/16 in odd pairs): exact but for what lies 2^-14 and more
 // below it, which loses less than 2^-25 of the largest.  Weights are 2^(z - m + 6), rounded to fp16 (2^-12 of
-// each, and 2^-31 of the largest where that is more): as the second product's operand they have to be 16 bits, and fp16 leaves an eighth of
-// bf16's error.  Sums are taken before that rounding, in fp32, as are all statistics.
+// each, and 2^-31 of the largest where that is more): as the second product's operand they have to be 16 bits,
+// and fp16 leaves an eighth of bf16's error.  Sums are taken before that rounding, in fp32, as are all statistics.
 //
 // Work is one line, cut into equal shares of as many CTAs as the GPU holds (plan_line).  A CTA is four warps on
 // one unit at a time: a row tile of 8 NQ queries of a kv head and a range of keys.  Every warp
@@ -742,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
   }
 }
 
-// L lanes a query row (32, or 16 for heads to 64): what tcgen05 left of its prefix, and the pieces of its prefix and of its tail (the
-// unit's own and those of the CTAs at whose beginning it was cut), brought to a common maximum:
+// L lanes a query row (32, or 16 for heads to 64): what tcgen05 left of its prefix, and the pieces of its prefix
+// and of its tail (the unit's own and those of the CTAs at whose beginning it was cut), brought to a common maximum:
 //   out = sum_p a_p O_p / sum_p a_p l_p,  a_p = 2^(m_p - m).
 // A lane holds E dims.  Bound by the latency of what it asks for, so four pieces are asked for at once, and where
 // there are few rows, which have many pieces, W warps share a row's.

@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(kThreads) widen_kernel(const __grid_constant__
   // A thread takes a piece of 8 dims of every 256 / (D/8)-th token: all codes, then all stores.
   constexpr int kPieces = D / 8, kStep = kThreads / kPieces, kEach = kWideTokens / kStep;
   const int e = threadIdx.x % kPieces * 8, i0 = threadIdx.x / kPieces;
-  const char *k_code = a.kp + e / 8 * BITS, *v_code = a.vp + e / 8 * BITS, *k_scale = a.kp + e / 16, *v_scale = a.vp + e / 16;
+  const char *k_code = a.kp + e / 8 * BITS, *v_code = a.vp + e / 8 * BITS;
+  const char *k_scale = a.kp + e / 16, *v_scale = a.vp + e / 16;
   uint2 code[kEach][2];
   unsigned scale[kEach][2];
 #pragma unroll
