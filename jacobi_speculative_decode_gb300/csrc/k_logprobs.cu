@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Arg
     st.m = most;
     limit = most + kLazy / c;
     least = Vt::round_down(__fsub_rd(most, 200.0f / c));   // 2^-200 is nothing
-    if (least == Vt::kLeast) least = -INFINITY;
+    // one by one where there is no such value, or the next one below is so far away that its difference is infinite
+    if (least == Vt::kLeast || (least - most) * c == -INFINITY) least = -INFINITY;
   };
   auto add = [&](float lo, float hi) {   // neither infinite
     const uint64_t d = mul2(add2(pair(lo, hi), pair(-st.m, -st.m)), c2);
