@@ -20,7 +20,7 @@
 // gave nothing.)
 //
 // A value held is exact in fp16 (quant.cuh).  Queries are bf16, scaled by a power of two a row so that
-// their largest is in [1, 4) (4 bits: 16 times that, and 1/16 in odd pairs): exact but for what lies 2^-14 and more
+// their largest is in [1, 4) (4 bits: 128 times that, and 1/16 in odd pairs): exact but for what lies 2^-14 and more
 // below it, which loses less than 2^-25 of the largest.  Weights are 2^(z - m + 6), rounded to fp16 (2^-12 of
 // each, and 2^-31 of the largest where that is more): as the second product's operand they have to be 16 bits,
 // and fp16 leaves an eighth of bf16's error.  Sums are taken before that rounding, in fp32, as are all statistics.
@@ -145,9 +145,9 @@ template <int BITS, int DP, int NQ> struct Cfg {
   static constexpr int RESIDENT = DP == 64    ? (NQ == 1 ? 5 : NQ == 2 ? 4 : 2)
                                   : DP == 128 ? (BITS == 4 ? (NQ == 1 ? 4 : 2) : NQ < 4 ? 3 : 2)
                                               : 2;
-  // 4 bits: values are widened 2^-7 times as large (see widen4), queries are 16 times (so that 1/16 of
-  // them keeps as much)
-  static constexpr float UNIT = BITS == 4 ? 128.0f : 1.0f, QUERY = BITS == 4 ? 16.0f : 1.0f;
+  // 4 bits: values are widened 2^-7 times as large (see widen4), queries are 2^7 times, to 512 (1/16 of them keeps
+  // more than in 8 bits), so that a product is as large and its factor as far from fp32's ends
+  static constexpr float UNIT = BITS == 4 ? 128.0f : 1.0f;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
     float up;
-    const float down = C::QUERY * xpq::row_scale(top, &up);
+    const float down = C::UNIT * xpq::row_scale(top, &up);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {   // of a k step: dims 4 i.. of the lane's
       const uint32_t b0 = pack(x[4 * i] * down, x[4 * i + 1] * down);
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BITS, DP, NQ>::RESIDENT)
       qb[q][2 * i] = hi;
       qb[q][2 * i + 1] = pack(h0 - __low2float(h2(hi)), h1 - __high2float(h2(hi)));
     }
-    const float c = C::UNIT / C::QUERY * xpq::row_factor(up, g.a.scale * 1.44269504088896f);
+    const float c = xpq::row_factor(up, g.a.scale * 1.44269504088896f);
     const int lim = !is_row ? k1 : min(k1, prefix ? keys : keys - g.a.T + rt + 1);
     least = min(least, lim);
 #pragma unroll

@@ -46,7 +46,7 @@ __device__ __forceinline__ float scale_of(unsigned byte) {
 // A query row of largest magnitude `top` as fp16: times 2^-e, e its exponent, 2^-119 at least (what is
 // not finite stays so), which is exact but for what lies 2^-14 and more below the largest; *up: 2^e.
 __device__ __forceinline__ float row_scale(float top, float* up) {
-  const int e = min(max((int)(__float_as_uint(top) >> 23), 8), 253);   // so that 2^-e times 16 is finite too
+  const int e = min(max((int)(__float_as_uint(top) >> 23), 8), 253);   // so that 2^-e times 128 is finite too
   *up = __uint_as_float((uint32_t)e << 23);
   return __uint_as_float((uint32_t)(254 - e) << 23);
 }
