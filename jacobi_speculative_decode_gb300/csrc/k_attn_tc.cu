@@ -59,6 +59,9 @@ constexpr int kChunkBytes = kTile * 128;   // 64 elements of 128 rows, 128-byte 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;   // growth of the maximum (base 2) that P may carry
 constexpr float kLift = 6.0f;   // fp16 weights are 2^(z - m + kLift): at most 2^14, and small ones kept longer
+// Weights come from one multiply-add with the maximum's rounded product, whose rounding stays in the exponent: from
+// scores (base 2) of 2^25 on that is more than fp16 has room for.  F16: rows whose maximum passes this are summed again.
+constexpr float kFar = 262144.0f;
 
 template <int D>
 struct Cfg {
@@ -817,9 +820,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rb = r0 % 32;   // in the block, and rb + 8
       if (quad == 0)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          const bool some = l[i] > 0.0f || (F16 && fabsf(m[i] * c[i]) > kFar);
           ((float2*)g.stat)[block * 32 + rb + 8 * i] =
-              make_float2(l[i] > 0.0f ? m[i] * c[i] - (F16 ? kLift : 0.0f) : -INFINITY, l[i]);
+              make_float2(some ? m[i] * c[i] - (F16 ? kLift : 0.0f) : -INFINITY, l[i]);
+        }
       __syncwarp();
       float* acc = g.acc + block * D * 32 + (quad / 2 * 32 + rb) * 4 + quad % 2 * 2;
 #pragma unroll
@@ -880,6 +885,37 @@ __device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, in
   }
 }
 
+// A row of the fp16 form from the definition, its prefix and its tail (kFar): maximum *m in base 2, sum *l, weighted
+// values o of this thread's dims.  A thread a row too.
+template <int D>
+__device__ __noinline__ void row_again(const xp_attn_args& g, int n, int hk, int t, int h, int warp,
+                                       float* m, float* l, float4* o) {
+  const int end = g.a.max_len > 0 ? max(tail_len(g, n, false) - g.a.T + t + 1, 0) : 0;
+  const float c = g.q_factor[((int64_t)hk * g.a.N + n) * g.a.T * g.group + t * g.group + h % g.group];
+  const __half* q = (const __half*)g.q + n * g.a.q_stride_n + t * g.a.q_stride_t + h * g.a.q_stride_h;
+  *m = -INFINITY, *l = 0.0f;
+  for (int i = 0; i < D / 32; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j = -g.a.prefix_len; j < end; ++j) {   // below 0: the prefix
+    const int pos = j < 0 ? j + g.a.prefix_len : j;
+    const int32_t* table = j < 0 ? g.prefix_table : g.table + n * g.ld_table;
+    const int64_t at = table[pos / g.page_size] * g.kv_page + pos % g.page_size * g.kv_token + hk * g.kv_head;
+    const __half *k = (const __half*)g.k + at, *v = (const __half*)g.v + at;
+    float z = 0.0f;
+#pragma unroll 8
+    for (int d = 0; d < D; ++d) z = fmaf(__half2float(q[d]), __half2float(k[d]), z);
+    z *= c;
+    if (z == -INFINITY) continue;
+    const float now = fmaxf(*m, z), a = exp2f(*m - now), p = exp2f(z - now);
+    *m = now;
+    *l = *l * a + p;
+    for (int i = 0; i < D / 32; ++i) {
+      const __half* x = v + (warp + 8 * i) * 4;
+      o[i] = make_float4(o[i].x * a + p * __half2float(x[0]), o[i].y * a + p * __half2float(x[1]),
+                         o[i].z * a + p * __half2float(x[2]), o[i].w * a + p * __half2float(x[3]));
+    }
+  }
+}
+
 // A query row's partial results: of the prefix and of its tail, each the unit's own and those of
 // the CTAs at whose beginning it was cut, brought to a common maximum:
 //   out = sum a_p O_p / sum a_p l_p,  a_p = 2^(m_p - m).
@@ -891,7 +927,8 @@ __device__ __noinline__ void tail_again(const xp_attn_args& g, int n, int hk, in
 // CTA) and nobody else's work to wait under: four at once take 5% off both kernels' time (one
 // request of 4 tokens).  Many rows have three or four, and one at a time leaves room for more
 // CTAs: 3% off (128 blocks of 16 tokens).
-template <int D, int TOGETHER>
+// F16: the fp16 form, whose rows may be one range of a larger call.
+template <int D, int TOGETHER, bool F16>
 __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_constant__ xp_attn_args g,
                                                               int ctas) {
   constexpr int kPer = D / 32;   // 16-byte pieces a thread
@@ -905,7 +942,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
     const int i = (int)(e % per_seq), hk = (int)(e / per_seq % g.kv_heads);
     const int n = (int)(e / per_seq / g.kv_heads), t = i / g.group, h = hk * g.group + i % g.group;
     const int chunk = g.line[0], RT = g.plan.rows_tile;
-    float m = -INFINITY, l = 0.0f;
+    float m = -INFINITY, l = 0.0f, far = -INFINITY;   // far: the largest maximum of a piece that is not to be used
     float4 o[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c) o[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -955,6 +992,10 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
         }
 #pragma unroll
         for (int u = 0; u < TOGETHER; ++u) {
+          if (F16 && fabsf(st[u].x) > kFar && st[u].x != -INFINITY) {
+            far = fmaxf(far, st[u].x);
+            continue;
+          }
           if (st[u].y == 0.0f) continue;   // no visible key in this piece: x may be anything
           const float now = fmaxf(m, st[u].x), a = exp2f(m - now), b = exp2f(st[u].x - now);
           m = now;
@@ -967,8 +1008,17 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
       }
     };
     join(0);
-    if (g.a.max_len > 0) {
-      join(1);
+    if (g.a.max_len > 0) join(1);
+    if constexpr (F16) {
+      if (far > m - 400.0f) {   // of less there is nothing left
+        float m2, l2;
+        float4 o2[kPer];
+        row_again<D>(g, n, hk, t, h, warp, &m2, &l2, o2);
+        m = m2, l = l2;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) o[c] = o2[c];
+      }
+    } else if (g.a.max_len > 0) {
       auto nans = [&]() {   // of this thread's dims, a bit each
         unsigned bits = 0;
 #pragma unroll
@@ -980,7 +1030,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
       float all = 0.0f;
 #pragma unroll
       for (int c = 0; c < kPer; ++c) all += o[c].x + o[c].y + o[c].z + o[c].w;
-      if (all != all && l == l && g.a.T > 1 && !g.q_factor) {   // values of fp16 are all finite
+      if (all != all && l == l && g.a.T > 1) {
         const unsigned whole = nans();
         m = -INFINITY, l = 0.0f;
 #pragma unroll
@@ -1000,7 +1050,7 @@ __global__ void __launch_bounds__(256) attn_tc_combine_kernel(const __grid_const
         }
       }
     }
-    if (g.part_acc) {   // one range of a larger call: the rows are joined again
+    if (F16 && g.part_acc) {   // one range of a larger call: the rows are joined again
       const int64_t row = ((int64_t)n * g.a.T + t) * g.a.heads + h;
       if (warp == 0) ((float2*)g.part_stat)[row] = make_float2(m, l);
 #pragma unroll
@@ -1068,7 +1118,7 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
   const unsigned grid = (unsigned)((rows + 31) / 32);
-  return xp_launch_pdl(grid <= (unsigned)c->num_sms ? attn_tc_combine_kernel<D, 4> : attn_tc_combine_kernel<D, 1>,
+  return xp_launch_pdl(grid <= (unsigned)c->num_sms ? attn_tc_combine_kernel<D, 4, F16> : attn_tc_combine_kernel<D, 1, F16>,
                        dim3(grid), dim3(256), 0, s, g, c->num_sms);
 }
 

@@ -32,20 +32,19 @@ def test_scores_of_order_one(bits, size):
         check(bits, 2, T, 2, 2, D, 16, 20, [170, 40], q=x, scale=min(0.1 / size, 3e38))
 
 
-def huge(bits, size, scale, T, D):
-    H, G, lens = 2, 2, [130, 37]
-    prefix = 20
+def huge(bits, size, scale, T, D, lens=(130, 37), G=2, prefix=20):
+    H, N = 2, len(lens)
 
     def fill(rows):   # scores below half of what fp32 holds
         rows[0].mul_(0.05)
     c, prefix_table, table, held = build(bits, 16, H, D, prefix, lens, T + D, fill=fill)
     g = np.random.default_rng(T)
-    q = torch.zeros(2, T, H * G, D)
-    dims = g.integers(0, D, (2, T, H * G))
+    q = torch.zeros(N, T, H * G, D)
+    dims = g.integers(0, D, (N, T, H * G))
     for at in np.ndindex(dims.shape):
         q[at][dims[at]] = size * (1 if g.random() < 0.5 else -1)
     q = q.to(torch.bfloat16).cuda()
-    out, lse = torch.empty_like(q), torch.empty(2, T, H * G, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(N, T, H * G, device="cuda")
     a = xp.make_attn(q, out, 0, prefix, max(lens), scale)
     xp.xp_prefix_attention(c.handle, a, q, prefix_table, table, cu(lens), out, lse, c.attention_workspace(a))
     assert xp.xp_cache_get_error(c.handle) == xp.XP_OK
@@ -53,6 +52,9 @@ def huge(bits, size, scale, T, D):
     for n, t, h in np.ndindex(dims.shape):
         k, v = (np.concatenate([x[0], x[n + 1]])[:, h // G] for x in held)
         sees = prefix + max(0, lens[n] - T + 1 + t)
+        if sees == 0:
+            assert (got[n, t, h] == 0).all() and got_lse[n, t, h] == -np.inf
+            continue
         z, v = k[:sees] @ qs[n, t, h] * scale, v[:sees]
         best = v[z == z.max()]
         assert len(best) < 8 and z.max() < 3e38
@@ -75,3 +77,45 @@ HUGE = [(5e37, 1.0), (1.6e38, 1.0), (1e38, 0.25), (3.0, 2e37), (1e10, 1e28), (6e
 @pytest.mark.parametrize("T,D", [(1, 128), (2, 64), (5, 96), (3, 256)])
 def test_products_that_are_huge(bits, size, scale, T, D):
     huge(bits, size, scale, T, D)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("size,scale", HUGE + [(1e9, 1.0), (1e11, 0.7), (3e7, 3.0)])
+@pytest.mark.parametrize("T,D,lens,G,prefix", [
+    (70, 64, (130, 37), 2, 20), (70, 128, (130, 37), 2, 0),             # all of it widened
+    (1, 128, tuple(1 + 3 * i % 200 for i in range(70)), 4, 130),        # the prefix alone
+    (3, 64, (300, 0, 2) * 15, 2, 700)], ids=lambda x: str(x)[:16])      # tails beside it
+def test_products_that_are_huge_over_widened_keys(bits, size, scale, T, D, lens, G, prefix):
+    huge(bits, size, scale, T, D, lens, G, prefix)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T,lens,prefix", [(70, (130, 37), 20), (1, tuple(range(1, 200, 2)), 130)],
+                         ids=lambda x: str(x)[:16])
+@pytest.mark.parametrize("size", [1e6, 1e9, 1e20, 3e37])
+def test_a_large_query_beside_others(bits, T, lens, prefix, size):
+    """Rows of one tile have nothing to do with one another, and queries turned round get the least score's key."""
+    H, G, D, N = 2, 4, 128, len(lens)
+    c, prefix_table, table, held = build(bits, 16, H, D, prefix, lens, 3)
+    q = torch.randn(N, T, H * G, D, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    at = (N - 1, T // 2, 5)
+    outs = []
+    for sign in (0, 1, -1):
+        x = q.clone()
+        if sign:
+            x[at] = 0
+            x[at][17] = sign * size
+        out = torch.empty_like(x)
+        a = xp.make_attn(x, out, 0, prefix, max(lens), 0.1)
+        xp.xp_prefix_attention(c.handle, a, x, prefix_table, table, cu(lens), out, None, c.attention_workspace(a))
+        outs.append(out)
+    k, v = (np.concatenate([h[0], h[N]])[:, at[2] // G] for h in held)
+    sees = prefix + max(0, lens[-1] - T + 1 + at[1])
+    for out, sign in zip(outs[1:], (1, -1)):
+        z = sign * k[:sees, 17]
+        best = v[:sees][z == z.max()]
+        want, got = best.mean(0), out[at].double().cpu().numpy()
+        near = 2.0 ** -8 * np.abs(want) + 2.0 ** -16 * np.abs(best).max()
+        assert len(best) < 8 and (np.abs(got - want) <= near).all()
+        out[at] = outs[0][at]
+        assert torch.equal(out, outs[0])
