@@ -139,12 +139,16 @@ template <int BITS, int DP, int NQ> struct Cfg {
   static constexpr int JOIN = kWarps * 8 * PITCH * 4;
   static constexpr int QUERIES = NQ == 4 ? NQ * (DP / 16) * 32 * 8 : 0;   // held in shared memory
   static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + QUERIES;
-  // CTAs an SM, as registers (results: 4 NQ KS a thread) and shared memory allow.  Heads of 128 in 8 bits: three with
-  // two stages and two with three, contexts of 1000 to 32768 behind 1 token 116 and 123 us, behind 4 134 and 147 (in
-  // 4 bits, behind 4: three and two 115 both).
-  static constexpr int RESIDENT = DP == 64    ? (NQ == 1 ? 5 : NQ == 2 ? 4 : 2)
+  // CTAs an SM, which registers (results: 4 NQ KS a thread) and shared memory have room for: the line is cut into as
+  // many pieces, which all run at once.  Heads of 128 in 8 bits: three with two stages and two with three,
+  // contexts of 1000 to 32768 behind 1 token 116 and 123 us, behind 4 134 and 147 (in 4 bits, behind 4: three and two
+  // 115 both).  Heads of 64 in 8 bits, 64 over 8: three 64 us, four 67, five with two stages 66; of 256, where one
+  // fits, 150.
+  static constexpr int RESIDENT = DP == 64    ? (NQ == 1 ? (BITS == 4 ? 5 : 3) : NQ == 2 ? 4 : 2)
                                   : DP == 128 ? (BITS == 4 ? (NQ == 1 ? 4 : 2) : NQ < 4 ? 3 : 2)
-                                              : 2;
+                                              : (BITS == 4 ? 2 : 1);
+  // an SM's shared memory, of which every CTA takes 1 KB besides its own
+  static_assert(RESIDENT * (SMEM + (int)sizeof(Start) + kWarps * 8 * NQ * 8 + 1024) <= 228 * 1024, "CTAs that do not fit");
   // 4 bits: values are widened 2^-7 times as large (see widen4), queries are 2^7 times, to 512 (1/16 of them keeps
   // more than in 8 bits), so that a product is as large and its factor as far from fp32's ends
   static constexpr float UNIT = BITS == 4 ? 128.0f : 1.0f;
