@@ -83,6 +83,7 @@ def test_products_that_are_huge(bits, size, scale, T, D):
 @pytest.mark.parametrize("size,scale", HUGE + [(1e9, 1.0), (1e11, 0.7), (3e7, 3.0)])
 @pytest.mark.parametrize("T,D,lens,G,prefix", [
     (70, 64, (130, 37), 2, 20), (70, 128, (130, 37), 2, 0),             # all of it widened
+    (70, 128, (1, 3), 2, 0),                                            # one key: a score may be far below 0
     (1, 128, tuple(1 + 3 * i % 200 for i in range(70)), 4, 130),        # the prefix alone
     (3, 64, (300, 0, 2) * 15, 2, 700)], ids=lambda x: str(x)[:16])      # tails beside it
 def test_products_that_are_huge_over_widened_keys(bits, size, scale, T, D, lens, G, prefix):
@@ -119,3 +120,43 @@ def test_a_large_query_beside_others(bits, T, lens, prefix, size):
         assert len(best) < 8 and (np.abs(got - want) <= near).all()
         out[at] = outs[0][at]
         assert torch.equal(out, outs[0])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("size", [1e5, 3e5, 1e6, 3e6])
+@pytest.mark.parametrize("T,lens,prefix", [(2, (130, 37), 20), (70, (130, 37), 20), (1, tuple(range(1, 200, 2)), 5000),
+                                           (16, (300, 16, 700), 3000)], ids=lambda x: str(x)[:16])
+def test_scores_on_both_sides_of_what_is_summed_again(bits, size, T, lens, prefix):
+    """A row's score is one product, exact, and rounded where it is multiplied by its factor, where the maximum is
+    and where pieces are joined, within 2^-24 each: dz = 2^-22 of it together, and a weighted mean within 2 dz of
+    that of |v|."""
+    H, G, D, N = 2, 4, 128, len(lens)
+
+    def fill(rows):
+        rows[0].mul_(0.05)
+    c, prefix_table, table, held = build(bits, 16, H, D, prefix, lens, 9, fill=fill)
+    g = np.random.default_rng(T)
+    q = torch.zeros(N, T, H * G, D)
+    dims = g.integers(0, D, (N, T, H * G))
+    for at in np.ndindex(dims.shape):
+        q[at][dims[at]] = size * g.uniform(0.5, 1.0) * (1 if g.random() < 0.5 else -1)
+    q = q.to(torch.bfloat16).cuda()
+    out, lse = torch.empty_like(q), torch.empty(N, T, H * G, device="cuda")
+    a = xp.make_attn(q, out, 0, prefix, max(lens), 1.0)
+    xp.xp_prefix_attention(c.handle, a, q, prefix_table, table, cu(lens), out, lse, c.attention_workspace(a))
+    assert xp.xp_cache_get_error(c.handle) == xp.XP_OK
+    got, got_lse, qs = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().cpu().numpy()
+    for n, t, h in np.ndindex(dims.shape):
+        k, v = (np.concatenate([x[0], x[n + 1]])[:, h // G] for x in held)
+        sees = prefix + max(0, lens[n] - T + 1 + t)
+        z, v = k[:sees] @ qs[n, t, h], v[:sees]
+        p = np.exp(z - z.max())
+        dz = 2.0 ** -22 * np.abs(z[p > 1e-8]).max()
+        want, mean = p @ v / p.sum(), p @ np.abs(v) / p.sum()
+        # fp16 weights: 2^-11 of each; codes of 4 bits: as in the attention's other tests, a scale is at most |v| / 3
+        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * dz) * mean + 2.0 ** -31 * np.abs(v).sum(0)
+        step = p @ np.abs(v).reshape(sees, D // 16, 16).max(2).repeat(16, 1) / p.sum() / 3
+        tol = tol + step * 23 * (sees + 8) * 2.0 ** -23
+        assert (np.abs(got[n, t, h] - want) <= tol).all(), (n, t, h)
+        top = z.max() + math.log(p.sum())
+        assert abs(got_lse[n, t, h] - top) <= 2 * dz + 2.0 ** -22 * abs(top) + 2.0 ** -18, (n, t, h)
