@@ -542,10 +542,13 @@ xp_status xp_cache_compact(const xp_cache* cache, const int32_t* table, int64_t 
  * queries on 16-byte boundaries with one stride from token to token, across sequences too, are
  * loaded fastest: a slice of the last T tokens of longer rows costs half the call's time again.
  * Quantised caches: q and out are bf16, any head_dim and page size, on tensor cores; values are those held,
- * in 16-bit floats, and each weight is rounded to one of those.  Where many queries share a key (256 rows
- * of N T heads/kv_heads for the prefix, 32 or 64 of T heads/kv_heads for tails; head_dim 64 or 128) keys and
- * values are written out in 16 bits to the workspace, which is as much larger: 4 kv_heads head_dim bytes a
- * token, for tails 1 GiB at most. */
+ * in 16-bit floats, and each weight is rounded to one of those.  Where many queries share a key (head_dim 64
+ * or 128) keys and values are written out in 16 bits to the workspace, which is as much larger: 4 kv_heads
+ * head_dim bytes a token.  A prefix is from 256 rows of N T heads/kv_heads on, whatever its length (a million
+ * tokens of 8 heads of 128: 4.3 GB).  Tails are, to 1 GiB together: without a prefix from 64 rows of T
+ * heads/kv_heads on; beside a prefix that is, from 32, and at any number where they have at most twice its pages
+ * of 128 tokens.  Rows there with scores past 2^17 are right but slow.  scale times a query's largest
+ * magnitude: below 2e38. */
 typedef struct {
   int layer, N, T, heads;
   int head_dim;      /* head_dim and dtype: those of q and out, which must be the cache's */

@@ -11,13 +11,14 @@
 // a lane takes the dims and keys whose codes lie side by side: 32 dims of a key for K^, 16 dims
 // of four keys for V^, each one or two vector loads from shared memory.
 //
-// What bounds it.  A warp's step of 32 keys of 128 dims in 4 bits is 4.6 KB, 206 cycles of an SM's share of HBM,
-// and 700 instructions, 175 cycles of its four issue slots; 290 of them, mostly what picks codes out of
-// words, are the logic pipe's, which takes one every other cycle.  16 single tokens, 32 heads of 128 over 8,
-// contexts of 1000 to 32768 (311 MB): 75 us, 4.1 TB/s, 61% of measured, and 9 for the joining; issue slots
-// are busy in 58% of the cycles, the logic pipe in 48%, the tensor pipe in 24%, with 14 of 16 warps an SM.
-// In 8 bits (589 MB) 116 us for both kernels, 75% of measured.  (Other numbers of CTAs an SM and of stages
-// gave nothing.)
+// What bounds it: no one thing, but a warp's own chain of instructions.  A warp's step of 32 keys of 128 dims in 4
+// bits is 4.6 KB, 206 cycles of an SM's share of HBM, and 700 instructions, 175 cycles of its four issue slots;
+// 290 of them, mostly what picks codes out of words, are the logic pipe's, which takes one every other cycle.  16
+// single tokens, 32 heads of 128 over 8, contexts of 1000 to 32768 (311 MB): 75 us, 4.1 TB/s, 61% of measured,
+// and 4 more with the joining; issue slots are busy in 57% of the cycles, the logic pipe in 48%, the tensor pipe in 24%.
+// An SM's 14 warps, 3.5 a scheduler, issue every 6 cycles each: 1.2 of them wait for the instruction before,
+// 1.6 for a pipe's turn, 0.9 for memory, 1.1 for another warp.  Without its loads it takes 62 us.  In 8 bits (589 MB)
+// 118 us for both kernels, 73% of measured.
 //
 // A value held is exact in fp16 (quant.cuh).  Queries are bf16, scaled by a power of two a row so that
 // their largest is in [1, 4) (4 bits: 128 times that, and 1/16 in odd pairs): exact but for what lies 2^-14 and more
@@ -894,9 +895,11 @@ template <int BITS> cudaError_t launch_dims(const xp_attn_args& g, const Quant& 
 
 // Many queries of each key are the tensor cores' work, not that of widening: from so many of a kv head on,
 // what they see is widened to fp16 in the workspace once (exactly, as here) and attended over on tcgen05.
-// 32 sequences of 1, 2, 4 tokens behind 8192, 8 kv heads of 4 x 128 in 4 bits: 64 rows 65 us widened and 46 not,
-// 128 rows 66 and 61, 256 rows 62 and 93.  32 tails of 17 to 1500 tokens, rows of one: 16 take 65 and 41, 32 take
-// 69 and 69, 64 take 73 and 108.  Tails beside a widened prefix, which spare a kernel and a second joining: 32
+// 32 sequences of 1, 2, 4 tokens behind 8192, 8 kv heads of 4 x 128, widened and not: in 4 bits 128 rows 40 and 39
+// us, 256 rows 36 and 55, 512 rows 41 and 92; in 8 bits 40 and 41, 38 and 61, 42 and 104; heads of 64 in 4 bits 33 and 27,
+// 29 and 35, 30 and 52, in 8 bits 33 and 28, 29 and 37, 30 and 56.  32 tails of 17 to 1500 tokens, rows of one: in 4
+// bits 16 take 52 and 33, 32 take 54 and 57, 64 take 59 and 95; in 8 bits 54 and 35, 56 and 58, 60 and 96; heads of 64
+// in 4 bits 38 and 18, 41 and 33, 44 and 54, in 8 bits 38 and 20, 41 and 37, 44 and 61.  Tails beside a widened prefix, which spare a kernel and a second joining: 32
 // rows 89 and 119 us, 16 rows 80 and 81 (128 sequences: 223 and 173), 8 rows 117 and 79.
 constexpr int kWidePrefixRows = 256, kWideTailRows = 64;
 constexpr size_t kWideTailBytes = (size_t)1 << 30;   // of tails that may be widened

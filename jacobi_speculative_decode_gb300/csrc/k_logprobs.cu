@@ -6,10 +6,10 @@
 //   log p(x) = (l_x - m) / t - log S,   H = log S - log(2) W / S.
 // Differences are taken before they are scaled, so that neither large logits nor small temperatures lose
 // digits.
-// Bound by the row's bytes in fp32: 2048 rows of 151647, 1.24 GB, 196 us, 6.3 TB/s, 93% of measured.  In bf16 by
-// instructions: 2048 rows of 151647, 621 MB, 116 us, 79%.  One CTA
+// Bound by the row's bytes in fp32: 2048 rows of 151647, 1.24 GB, 199 to 202 us, 6.2 TB/s, 91% of measured.  In bf16 by
+// instructions: 2048 rows of 151647, 621 MB, 117 us, 78%.  One CTA
 // a row leaves few rows to as many CTAs: 410 rows (125 MB) with 20 alternatives 39 us, with none 31.
-// The best ids.  On the way a thread only writes down the greatest of every 16 bytes' batch.  The `top`-th of the
+// The best ids.  On the way a thread only writes down the greatest of every batch of four 16-byte vectors.  The `top`-th of the
 // 256 threads' greatest is a bound: there are `top` elements that are not below it, and few that are above.
 // The batches that reach it are read again (from L2, some 25 of a row's, by the threads they are of, all at once:
 // warp by warp 42 us, not 39), their elements that do go to a buffer,

@@ -2,9 +2,10 @@
 //
 // A CTA takes kTokens tokens of one sequence and finds their pages once; a thread is one piece of a token's
 // row (8 dims of K or V written, 16 bytes of them read) and walks over the tokens, so that nothing is divided
-// inside.  8 prompts of 4096 tokens, 8 heads of 128, fp32 in 8 bits: written in 65 us (340 MB, 5.2 TB/s, between
-// HBM and what quantising costs), read back in 61 (5.5 TB/s, 82% of measured); 32 sequences to 3000 tokens out of 4
-// bits as bf16 75 us, 6.0 TB/s, 88%.
+// inside.  8 prompts of 4096 tokens, 8 heads of 128, fp32 in 8 bits: written in 64 us (340 MB, 5.3 TB/s, between
+// HBM and what quantising costs), read back in 62 (5.5 TB/s, 81% of measured); 32 sequences to 3000 tokens out of 4
+// bits as bf16 75 us, 6.0 TB/s, 88%.  Rows of bf16 are half the bytes and more instructions, 79 us of 30 that their
+// bytes take: they are widened to fp32 and quantised element by element as those are.
 #include <algorithm>
 
 #include "quant.cuh"
@@ -202,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_quant_kernel(const RowArgs
 }
 
 // ---------------------------------------------------------------------------
-// Read back: BITS of a code, or 16 / 32 for a cache of bf16 / fp32.
+// Read back: BITS of a code, or 16 / 32 for a cache of bf16 / fp32.  Those are read one element a load, as their
+// strides may be any: the prompts above out of bf16 as bf16 55 us of 40, out of fp32 as fp32 99 of 79.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void store(float* p, bool wide, const float (&x)[4], int n) {
   if (wide) {

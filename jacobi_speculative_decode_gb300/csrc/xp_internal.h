@@ -262,7 +262,7 @@ struct xp_attn_plan {
   int64_t second_blocks;            // and those of the second stream's own results
   int prefix_splits, prefix_keys, tail_splits, tail_keys;
   int parts;
-  // quantised form: what is widened to bf16 first, in pages of kWidePage tokens (0: nothing), where its
+  // quantised form: what is widened to fp16 first, in pages of kWidePage tokens (0: nothing), where its
   // pools and its table are, elements of a head there; tc: then all of the call, else the prefix
   int wide_prefix, wide_tail;
   int64_t wide_plane;
