@@ -281,3 +281,25 @@ def test_rows_off_their_types_boundary_are_refused(dtype):
                     q.data_ptr() + do, None, ws.data_ptr(), ws.numel() * ws.element_size(), None))
             assert e.value.code == xp.XP_EINVAL
     assert int(c.k.max()) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_magnitudes_around_the_greatest_that_is_held(bits, dtype):
+    """The range ends at 127*512 and 7*7680, though larger scales would have finite values too: above it a group is
+    held at the end and told, up to it nothing is."""
+    end = Q.most_of(bits) * Q.scale_values()[Q.top_byte(bits)]
+    g = np.random.default_rng(3)
+    c = make(bits, 1, 1, 1, 1, 16, fill=0)
+    got = torch.empty(1, 1, 1, 16, device="cuda", dtype=dtype)
+    for top in (0.9 * end, end * (1 - 2.0 ** -7), end, end * (1 + 2.0 ** -6), 1.1 * end, 1.2 * end, 65504.0, 3e38):
+        x = g.uniform(-0.5, 0.5, 16) * end
+        x[5] = -top
+        x = torch.from_numpy(x).reshape(1, 1, 1, 16).to(dtype).cuda()
+        codes, byte, over = Q.quantise(x.double().cpu().numpy(), bits)
+        assert over == (abs(x[0, 0, 0, 5].item()) > end)
+        xp.xp_cache_append(c.handle, 0, x, x, cu([[0]]), cu([1]))
+        assert xp.xp_cache_get_error(c.handle) == (xp.XP_ERANGE if over else xp.XP_OK)
+        xp.xp_cache_read(c.handle, 0, cu([[0]]), cu([1]), None, got, torch.empty_like(got))
+        want = torch.from_numpy(Q.values(codes, byte)).to(dtype)      # both round to nearest
+        assert torch.equal(got.cpu(), want)
