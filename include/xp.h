@@ -537,7 +537,8 @@ xp_status xp_cache_compact(const xp_cache* cache, const int32_t* table, int64_t 
  * [N, T, heads] or NULL.  scale: positive and finite.  Scores, softmax and sums are fp32 (bf16:
  * each weight is rounded to bf16 before it multiplies v, as the tensor cores take it).
  * bf16 caches of head_dim 64 or 128 and pages of a multiple of 8 tokens, with pools on 16-byte
- * boundaries and strides that are multiples of 8, run on the tensor cores; all others run on CUDA
+ * boundaries and strides that are multiples of 8, run on the tensor cores (scores there: below 2^29; the
+ * rounding of larger ones leaves what a weight can be); all others run on CUDA
  * cores, at a small part of that rate (an fp32 cache keeps the weights in 32 bits).  On tensor cores
  * queries on 16-byte boundaries with one stride from token to token, across sequences too, are
  * loaded fastest: a slice of the last T tokens of longer rows costs half the call's time again.
