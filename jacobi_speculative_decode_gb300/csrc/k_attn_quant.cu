@@ -149,7 +149,8 @@ template <int BITS, int DP, int NQ> struct Cfg {
                                   : DP == 128 ? (BITS == 4 ? (NQ == 1 ? 4 : 2) : NQ < 4 ? 3 : 2)
                                               : (BITS == 4 ? 2 : 1);
   // an SM's shared memory, of which every CTA takes 1 KB besides its own
-  static_assert(RESIDENT * (SMEM + (int)sizeof(Start) + kWarps * 8 * NQ * 8 + 1024) <= 228 * 1024, "CTAs that do not fit");
+  static constexpr int STATIC = sizeof(Start) + kWarps * 8 * NQ * 8;
+  static_assert(RESIDENT * (SMEM + STATIC + 1024) <= 228 * 1024, "more CTAs than fit");
   // 4 bits: values are widened 2^-7 times as large (see widen4), queries are 2^7 times, to 512 (1/16 of them keeps
   // more than in 8 bits), so that a product is as large and its factor as far from fp32's ends
   static constexpr float UNIT = BITS == 4 ? 128.0f : 1.0f;
@@ -895,12 +896,13 @@ template <int BITS> cudaError_t launch_dims(const xp_attn_args& g, const Quant& 
 
 // Many queries of each key are the tensor cores' work, not that of widening: from so many of a kv head on,
 // what they see is widened to fp16 in the workspace once (exactly, as here) and attended over on tcgen05.
-// 32 sequences of 1, 2, 4 tokens behind 8192, 8 kv heads of 4 x 128, widened and not: in 4 bits 128 rows 40 and 39
-// us, 256 rows 36 and 55, 512 rows 41 and 92; in 8 bits 40 and 41, 38 and 61, 42 and 104; heads of 64 in 4 bits 33 and 27,
-// 29 and 35, 30 and 52, in 8 bits 33 and 28, 29 and 37, 30 and 56.  32 tails of 17 to 1500 tokens, rows of one: in 4
-// bits 16 take 52 and 33, 32 take 54 and 57, 64 take 59 and 95; in 8 bits 54 and 35, 56 and 58, 60 and 96; heads of 64
-// in 4 bits 38 and 18, 41 and 33, 44 and 54, in 8 bits 38 and 20, 41 and 37, 44 and 61.  Tails beside a widened prefix, which spare a kernel and a second joining: 32
-// rows 89 and 119 us, 16 rows 80 and 81 (128 sequences: 223 and 173), 8 rows 117 and 79.
+// 32 sequences of 1, 2, 4 tokens behind 8192, 8 kv heads of 4 x 128, widened and not: in 4 bits 128 rows 40 and
+// 39 us, 256 rows 36 and 55, 512 rows 41 and 92; in 8 bits 40 and 41, 38 and 61, 42 and 104; heads of 64 in 4 bits
+// 33 and 27, 29 and 35, 30 and 52, in 8 bits 33 and 28, 29 and 37, 30 and 56.  32 tails of 17 to 1500 tokens, rows
+// of one: in 4 bits 16 take 52 and 33, 32 take 54 and 57, 64 take 59 and 95; in 8 bits 54 and 35, 56 and 58, 60 and
+// 96; heads of 64 in 4 bits 38 and 18, 41 and 33, 44 and 54, in 8 bits 38 and 20, 41 and 37, 44 and 61.  Tails
+// beside a widened prefix, which spare a kernel and a second joining: 32 rows 89 and 119 us, 16 rows 80 and 81 (128
+// sequences: 223 and 173), 8 rows 117 and 79.
 constexpr int kWidePrefixRows = 256, kWideTailRows = 64;
 constexpr size_t kWideTailBytes = (size_t)1 << 30;   // of tails that may be widened
 

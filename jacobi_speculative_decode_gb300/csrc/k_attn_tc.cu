@@ -60,7 +60,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kLazy = 8.0f;   // growth of the maximum (base 2) that P may carry
 constexpr float kLift = 6.0f;   // fp16 weights are 2^(z - m + kLift): at most 2^14, and small ones kept longer
 // Weights come from one multiply-add with the maximum's rounded product, whose rounding stays in the exponent: from
-// scores (base 2) of 2^25 on that is more than fp16 has room for.  F16: rows whose maximum passes this are summed again.
+// scores (base 2) of 2^25 on that is more than fp16 has room for.  F16: rows whose maximum passes this are summed
+// again.
 constexpr float kFar = 262144.0f;
 
 template <int D>
@@ -1127,7 +1128,8 @@ cudaError_t launch(const xp_cache* c, const xp_attn_args& g, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)g.a.N * g.a.T * g.a.heads;
   const unsigned grid = (unsigned)((rows + 31) / 32);
-  return xp_launch_pdl(grid <= (unsigned)c->num_sms ? attn_tc_combine_kernel<D, 4, F16> : attn_tc_combine_kernel<D, 1, F16>,
+  return xp_launch_pdl(grid <= (unsigned)c->num_sms ? attn_tc_combine_kernel<D, 4, F16>
+                                                    : attn_tc_combine_kernel<D, 1, F16>,
                        dim3(grid), dim3(256), 0, s, g, c->num_sms);
 }
 
